@@ -216,6 +216,103 @@ int norm_bwd_ex(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t 
                 float *dbeta, void *workspace, size_t workspace_bytes, gbnorm_stream_t stream);
 
 /*
+ * Norms with 8-bit rows.
+ *
+ * Two places of a norm hold rows that may be stored in 8 bits: its output,
+ * when the next product reads 8-bit operands, and the input it keeps for its
+ * backward pass (the activation checkpoint).  h, mean, rstd and y are those of
+ * the general form above (strided rows, a storage type per tensor, optional
+ * residual, gamma and beta).
+ *
+ * 8-bit output rows: a scale for every group of q_group consecutive columns
+ * (32, 64, 128 or 256; the last group of a row may be shorter), or one per row
+ * (q_group 0), with Q = 448 (GBNORM_E4M3) or 127 (GBNORM_INT8):
+ *       scale = max |y_j| / Q,    code_j = y_j / scale rounded to nearest even
+ * (saturating; int8 codes lie in [-127, 127]).  A group whose values all lie
+ * below 2^-100 (for RMSNorm: whose |h_j gamma_j| do) has scale 0 and codes 0,
+ * so code * scale is the value in every case.  A NaN in a row makes every
+ * scale of the row NaN.  For RMSNorm the codes are taken of h_j gamma_j, rstd
+ * cancelling in y_j / max |y_j|.
+ *
+ * 8-bit checkpoint of h: int8 codes about the middle of each group's range,
+ * with a pair (scale, mid) for every group of c_group columns (32, 64, 128 or
+ * 256), by these fp32 steps:
+ *       mid = max h / 2 + min h / 2,   half = max(max h - mid, mid - min h),
+ *       scale = half / 127,            code_j = rint((h_j - mid) * (1 / scale))
+ * (half < 2^-100: scale 0, codes 0).  The codes depend on the stored rows
+ * alone.  What they stand for is v_j = mid + scale * code_j, with
+ * |v_j - h_j| <= scale / 2 up to fp32 rounding.
+ *
+ * norm_fwd_q8   writes the 8-bit output (and, if `codes` is given, the
+ *               checkpoint); norm_fwd_ck8 writes y in y_dtype and the
+ *               checkpoint.
+ * norm_bwd_ck8  the backward of either from the checkpoint: the formulas at
+ *               the top of this file with xhat_j = (v_j - mean) * rstd and the
+ *               saved statistics (of h itself), dres added into dx.  For the
+ *               8-bit output this is the straight-through gradient.
+ * q8_read       reads 8-bit rows of either kind back:
+ *       y_j = (((mid + scale * code_j) - mean) * rstd) * gamma_j + beta_j
+ *               with mid and mean 0, rstd and gamma 1, beta 0 where they are
+ *               NULL: the values alone, or the norm's output computed again
+ *               from its checkpoint (e.g. for the gradient of the weights that
+ *               read it).  A checkpoint is read with scale = c_scale,
+ *               mid = c_scale + 1, s_row = ldcs, s_group = 2.
+ *
+ * Arguments (those not listed are as for norm_fwd_ex / norm_bwd_ex):
+ *   q, ldq, q_format, q_group   [M] rows of N codes, one byte each.
+ *   q_scale, qs_row, qs_group   float32, 4-byte aligned: the scale of row i,
+ *                               group g at q_scale[i * qs_row + g * qs_group]
+ *                               (either order of the two; no two of them in
+ *                               one place).  q_group 0: g = 0 alone.
+ *   codes, ldc, c_group         [M] rows of N int8 codes; NULL in norm_fwd_q8:
+ *                               no checkpoint.
+ *   c_scale, ldcs               [M] rows of ceil(N / c_group) pairs (scale,
+ *                               mid), 8-byte aligned, ldcs floats apart
+ *                               (even, at least 2 ceil(N / c_group)).
+ *   workspace                   at least norm_bwd_ck8_workspace_size bytes
+ *                               (never 0 for valid arguments on a usable
+ *                               device), 16-byte aligned, not shared with a
+ *                               concurrent call.
+ *
+ * Aliasing: h and y may each be exactly x or residual, dx exactly dy or dres
+ * (same address, row stride and element size); 8-bit rows, scales and
+ * statistics overlap nothing, and q8_read's y overlaps no input.  With
+ * 16-byte-aligned rows of x, residual, h, y, dy, dres, dx and parameters
+ * (base and stride), 8-byte-aligned 8-bit rows and N a multiple of 8, rows
+ * move as vectors; anything else takes a correct element-wise path.  Status
+ * codes, ownership, streams and threading as above.
+ */
+typedef enum {
+    GBNORM_E4M3 = 0, /* 4 exponent bits, 3 mantissa bits, largest value 448 */
+    GBNORM_INT8 = 1
+} gbnorm_q8_t;
+
+int norm_fwd_q8(int is_layernorm, int64_t M, int64_t N, float eps, const void *x, int64_t ldx, int x_dtype,
+                const void *residual, int64_t ldr, void *h, int64_t ldh, const void *gamma, const void *beta,
+                int param_dtype, void *q, int64_t ldq, int q_format, int q_group, float *q_scale, int64_t qs_row,
+                int64_t qs_group, int8_t *codes, int64_t ldc, int c_group, float *c_scale, int64_t ldcs, float *mean,
+                float *rstd, gbnorm_stream_t stream);
+int norm_fwd_ck8(int is_layernorm, int64_t M, int64_t N, float eps, const void *x, int64_t ldx, int x_dtype,
+                 const void *residual, int64_t ldr, void *h, int64_t ldh, const void *gamma, const void *beta,
+                 int param_dtype, void *y, int64_t ldy, int y_dtype, int8_t *codes, int64_t ldc, int c_group,
+                 float *c_scale, int64_t ldcs, float *mean, float *rstd, gbnorm_stream_t stream);
+size_t norm_bwd_ck8_workspace_size(int is_layernorm, int64_t M, int64_t N);
+int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t lddy, int y_dtype,
+                 const int8_t *codes, int64_t ldc, int c_group, const float *c_scale, int64_t ldcs, const void *dres,
+                 int64_t lddres, const void *gamma, int param_dtype, const float *mean, const float *rstd, void *dx,
+                 int64_t lddx, int x_dtype, float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                 gbnorm_stream_t stream);
+int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int q_group, const float *scale,
+            const float *mid, int64_t s_row, int64_t s_group, const float *mean, const float *rstd, const void *gamma,
+            const void *beta, int param_dtype, void *y, int64_t ldy, int y_dtype, gbnorm_stream_t stream);
+
+/*
+ * The kernel that the calling thread's last 8-bit forward (what 0), backward
+ * (1) or q8_read (2) launched, as gbnorm_ex_last_variant.  For tests.
+ */
+int gbnorm_q8_last_variant(int what, char *buf, size_t len);
+
+/*
  * RMSNorm backward without a caller-provided workspace.
  *
  * No counterpart on the pages: this entry point exists for callers that cannot

@@ -1174,6 +1174,32 @@ int launch_colreduce(int is_ln, const float *wsc, int64_t P, int64_t N, float *d
 }  // namespace
 }  // namespace gbn
 
+// ------------------------------------------------------------------ for the other host units
+#include "host_shared.h"
+
+namespace gbn {
+
+static_assert(kMaxDev == kHostMaxDev, "device caches of the other units");
+
+int host_device(HostDevice *d) {
+    const int s = current_device(&d->dev);
+    if (s != GBNORM_OK) return s;
+    const DevInfo &i = g_dev[d->dev];
+    d->sms = i.sms;
+    d->smem_optin = i.smem_optin;
+    d->fault = i.fault;
+    return GBNORM_OK;
+}
+
+int64_t host_grid_limit() { return g_grid_limit.load(std::memory_order_relaxed); }
+
+int host_colreduce(int is_ln, const float *ws, int64_t P, int64_t N, float *dgamma, float *dbeta, bool after_rows,
+                   cudaStream_t stream) {
+    return launch_colreduce(is_ln, ws, P, N, dgamma, dbeta, after_rows, stream);
+}
+
+}  // namespace gbn
+
 using namespace gbn;
 
 extern "C" {

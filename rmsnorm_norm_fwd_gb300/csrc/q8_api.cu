@@ -1,0 +1,291 @@
+// q8_api.cu -- the C ABI of the 8-bit operators (include/gbnorm.h): argument
+// checks, the choice of a kernel, launches.  As in api.cu nothing here
+// allocates device memory or synchronises.
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+
+#include <cuda_runtime.h>
+
+#include "../../include/gbnorm.h"
+#include "host_shared.h"
+#include "q8_params.h"
+
+namespace gbn {
+namespace {
+
+int elem_size(int dtype) { return dtype == GBNORM_F32 ? 4 : 2; }
+bool valid_dtype(int d) { return d == GBNORM_F32 || d == GBNORM_F16 || d == GBNORM_BF16; }
+bool aligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+bool valid_shape(int64_t M, int64_t N) {
+    if (M < 0 || N < 1 || N > GBNORM_MAX_N) return false;
+    return M == 0 || M <= (INT64_MAX / 16) / N;  // byte offsets fit comfortably in int64
+}
+bool valid_ld(int64_t ld, int64_t N, int64_t M) { return ld >= N && (M == 0 || ld <= (INT64_MAX / 16) / M); }
+
+// log2 of a group size, -1 for one scale per row, -2 if not supported.
+int group_log2(int group) {
+    switch (group) {
+        case 0: return -1;
+        case 32: return 5;
+        case 64: return 6;
+        case 128: return 7;
+        case 256: return 8;
+        default: return -2;
+    }
+}
+int64_t groups_of(int64_t N, int lg) { return lg < 0 ? 1 : (N + ((int64_t)1 << lg) - 1) >> lg; }
+
+// A tensor as the aliasing check sees it: the bytes [p, p + bytes), and what
+// has to agree for an output to be exactly an input (in place).
+struct Span {
+    const void *p;
+    size_t bytes;
+    int64_t ld;   // row stride in elements; 0: not a row tensor
+    int es;       // element size
+    bool inplace; // outputs: may be exactly a row tensor among the inputs (inputs: may be overwritten so)
+};
+Span rows(const void *p, int64_t M, int64_t N, int64_t ld, int es, bool inplace) {
+    return {p, p && M > 0 ? ((size_t)(M - 1) * (size_t)ld + (size_t)N) * (size_t)es : 0, ld, es, inplace};
+}
+Span flat(const void *p, int64_t n, int es) { return {p, p ? (size_t)n * (size_t)es : 0, 0, es, false}; }
+
+bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
+}
+bool bad_aliasing(const Span *outs, int no, const Span *ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < ni; ++j) {
+            const Span &o = outs[i], &s = ins[j];
+            if (o.inplace && s.inplace && o.p == s.p && o.ld == s.ld && o.es == s.es && o.bytes == s.bytes) continue;
+            if (overlap(o, s)) return true;
+        }
+        for (int j = i + 1; j < no; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+// Scales of [M, G] groups at i * row + g * grp: positive strides that put no
+// two of them in one place.  The floats they span, 0 if invalid.
+int64_t scale_span(int64_t M, int64_t G, int64_t row, int64_t grp) {
+    if (M == 0) return 1;
+    const int64_t most = INT64_MAX / 64;
+    if ((M > 1 && (row < 1 || row > most / M)) || (G > 1 && (grp < 1 || grp > most / G))) return 0;
+    const int64_t rs = M > 1 ? (M - 1) * row : 0, gs = G > 1 ? (G - 1) * grp : 0;
+    if (M > 1 && G > 1 && row <= gs && grp <= rs) return 0;
+    return rs + gs + 1;
+}
+
+// Name of the kernel the calling thread's last call launched: forward,
+// backward, read.
+thread_local const char *t_last[3] = {"", "", ""};
+
+int launch(const void *kernel, int64_t grid, int cta, size_t dyn, void *params, cudaStream_t s) {
+    void *args[1] = {params};
+    if (cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)cta), args, dyn, s) != cudaSuccess)
+        return GBNORM_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
+}
+
+// Persistent grid of `units` pieces of work at `per_sm` CTAs an SM.
+int64_t grid_of(int64_t units, int64_t per_sm, const HostDevice &d) {
+    int64_t cap = per_sm * d.sms;
+    const int64_t limit = host_grid_limit();
+    if (limit > 0 && limit < cap) cap = limit;
+    return units < cap ? units : cap;
+}
+
+// Checks shared by the two forwards; fills the spans of what every forward has.
+struct FwdArgs {
+    int is_ln;
+    Q8FwdParams p;
+    int qgroup, cgroup;
+};
+
+int do_fwd(FwdArgs &a, cudaStream_t stream) {
+    Q8FwdParams &p = a.p;
+    if ((a.is_ln != 0 && a.is_ln != 1) || !valid_dtype(p.xdt) || !valid_dtype(p.pdt) || !valid_dtype(p.ydt))
+        return GBNORM_ERR_INVALID_ARG;
+    if (!valid_shape(p.M, p.N) || !std::isfinite(p.eps) || p.eps < 0.f) return GBNORM_ERR_INVALID_ARG;
+    if (p.qfmt != GBNORM_E4M3 && p.qfmt != GBNORM_INT8) return GBNORM_ERR_INVALID_ARG;
+    p.qg = group_log2(a.qgroup);
+    p.cg = group_log2(a.cgroup);
+    const int64_t M = p.M, N = p.N;
+    if (!a.is_ln) {
+        p.beta = nullptr;
+        p.mean = nullptr;
+    }
+    if (!p.res && p.h) return GBNORM_ERR_INVALID_ARG;
+    if (!p.res) p.ldr = N;
+    if (!p.h) p.ldh = N;
+    if (!p.y) p.ldy = N;
+    if (!p.q) p.ldq = N;
+    if (!p.c) p.ldc = N;
+    const int xs = elem_size(p.xdt), ps = elem_size(p.pdt);
+    int64_t qspan = 0, cspan = 0;
+    for (int64_t ld : {p.ldx, p.ldr, p.ldh, p.ldy, p.ldq, p.ldc})
+        if (M > 0 && !valid_ld(ld, N, M)) return GBNORM_ERR_INVALID_ARG;
+    if (p.q) {
+        if (p.qg == -2 || !p.qs || !aligned(p.qs, 4)) return GBNORM_ERR_INVALID_ARG;
+        qspan = scale_span(M, groups_of(N, p.qg), p.qs_row, p.qs_grp);
+        if (qspan == 0) return GBNORM_ERR_INVALID_ARG;
+    }
+    if (p.c) {
+        const int64_t pairs = 2 * groups_of(N, p.cg);
+        if (p.cg < 0 || !p.cs || !aligned(p.cs, 8) || (M > 0 && !valid_ld(p.ldcs, pairs, M)) || p.ldcs % 2 != 0)
+            return GBNORM_ERR_INVALID_ARG;
+        cspan = M > 0 ? (M - 1) * p.ldcs + pairs : 0;
+    }
+    if (M > 0 && (!p.x || (!p.y && !p.q))) return GBNORM_ERR_INVALID_ARG;
+    const Span outs[8] = {rows(p.y, M, N, p.ldy, elem_size(p.ydt), true), rows(p.h, M, N, p.ldh, xs, true),
+                          rows(p.q, M, N, p.ldq, 1, false), rows(p.c, M, N, p.ldc, 1, false),
+                          flat(p.qs, p.q && M > 0 ? qspan : 0, 4), flat(p.cs, p.c ? cspan : 0, 4),
+                          flat(p.rstd, M, 4), flat(p.mean, M, 4)};
+    const Span ins[4] = {rows(p.x, M, N, p.ldx, xs, true), rows(p.res, M, N, p.ldr, xs, true),
+                         flat(p.gamma, N, ps), flat(p.beta, N, ps)};
+    if (bad_aliasing(outs, 8, ins, 4)) return GBNORM_ERR_INVALID_ARG;
+    HostDevice d;
+    const int s = host_device(&d);
+    if (s != GBNORM_OK) return s;
+    t_last[0] = "";
+    if (M == 0) return GBNORM_OK;
+    t_last[0] = "elem";
+    return launch(kQ8FwdElem[a.is_ln], grid_of(M, 8, d), kElemCTA, 0, &p, stream);
+}
+
+// Partial rows of the backward: at most one per SM.
+size_t bwd_ws_bytes(int is_ln, int64_t M, int64_t N, const HostDevice &d) {
+    const int64_t P = grid_of(M, 1, d);
+    const size_t need = (size_t)P * (size_t)N * 4u * (is_ln ? 2u : 1u);
+    return (need + 255u) & ~(size_t)255u;
+}
+
+}  // namespace
+}  // namespace gbn
+
+using namespace gbn;
+
+extern "C" {
+
+int norm_fwd_q8(int is_layernorm, int64_t M, int64_t N, float eps, const void *x, int64_t ldx, int x_dtype,
+                const void *residual, int64_t ldr, void *h, int64_t ldh, const void *gamma, const void *beta,
+                int param_dtype, void *q, int64_t ldq, int q_format, int q_group, float *q_scale, int64_t qs_row,
+                int64_t qs_group, int8_t *codes, int64_t ldc, int c_group, float *c_scale, int64_t ldcs, float *mean,
+                float *rstd, gbnorm_stream_t stream) {
+    if (M > 0 && !q) return GBNORM_ERR_INVALID_ARG;
+    FwdArgs a{is_layernorm, {}, q_group, codes ? c_group : 128};
+    a.p = Q8FwdParams{x, residual, h, gamma, beta, nullptr, static_cast<uint8_t *>(q), q_scale,
+                      reinterpret_cast<uint8_t *>(codes), c_scale, mean, rstd, ldx, ldr, ldh, N, ldq, qs_row, qs_group,
+                      ldc, ldcs, M, N, eps, x_dtype, param_dtype, x_dtype, q_format, 0, 0};
+    return do_fwd(a, stream);
+}
+
+int norm_fwd_ck8(int is_layernorm, int64_t M, int64_t N, float eps, const void *x, int64_t ldx, int x_dtype,
+                 const void *residual, int64_t ldr, void *h, int64_t ldh, const void *gamma, const void *beta,
+                 int param_dtype, void *y, int64_t ldy, int y_dtype, int8_t *codes, int64_t ldc, int c_group,
+                 float *c_scale, int64_t ldcs, float *mean, float *rstd, gbnorm_stream_t stream) {
+    if (M > 0 && (!y || !codes)) return GBNORM_ERR_INVALID_ARG;
+    FwdArgs a{is_layernorm, {}, 0, c_group};
+    a.p = Q8FwdParams{x, residual, h, gamma, beta, y, nullptr, nullptr, reinterpret_cast<uint8_t *>(codes), c_scale,
+                      mean, rstd, ldx, ldr, ldh, ldy, N, 1, 1, ldc, ldcs, M, N, eps, x_dtype, param_dtype, y_dtype,
+                      GBNORM_E4M3, 0, 0};
+    return do_fwd(a, stream);
+}
+
+size_t norm_bwd_ck8_workspace_size(int is_layernorm, int64_t M, int64_t N) {
+    if ((is_layernorm != 0 && is_layernorm != 1) || !valid_shape(M, N)) return 0;
+    HostDevice d;
+    if (host_device(&d) != GBNORM_OK) return 0;
+    const size_t need = bwd_ws_bytes(is_layernorm, M, N, d);
+    return need > 0 ? need : 256;  // M = 0: nothing is used; 0 means an error
+}
+
+int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t lddy, int y_dtype,
+                 const int8_t *codes, int64_t ldc, int c_group, const float *c_scale, int64_t ldcs, const void *dres,
+                 int64_t lddres, const void *gamma, int param_dtype, const float *mean, const float *rstd, void *dx,
+                 int64_t lddx, int x_dtype, float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                 gbnorm_stream_t stream) {
+    const int cg = group_log2(c_group);
+    if ((is_layernorm != 0 && is_layernorm != 1) || !valid_dtype(x_dtype) || !valid_dtype(param_dtype) ||
+        !valid_dtype(y_dtype) || !valid_shape(M, N) || cg < 0)
+        return GBNORM_ERR_INVALID_ARG;
+    if (!is_layernorm) {
+        dbeta = nullptr;
+        mean = nullptr;
+    }
+    if (!dres) lddres = N;
+    const int64_t pairs = 2 * groups_of(N, cg);
+    if (M > 0) {
+        if (!dy || !codes || !c_scale || !rstd || !dx || (is_layernorm && !mean)) return GBNORM_ERR_INVALID_ARG;
+        for (int64_t ld : {lddy, ldc, lddres, lddx})
+            if (!valid_ld(ld, N, M)) return GBNORM_ERR_INVALID_ARG;
+        if (!valid_ld(ldcs, pairs, M) || ldcs % 2 != 0 || !aligned(c_scale, 8)) return GBNORM_ERR_INVALID_ARG;
+    }
+    const int xs = elem_size(x_dtype);
+    HostDevice d;
+    const int s = host_device(&d);
+    const size_t need = s == GBNORM_OK ? bwd_ws_bytes(is_layernorm, M, N, d) : 0;
+    const Span outs[4] = {rows(dx, M, N, lddx, xs, true), flat(dgamma, N, 4), flat(dbeta, N, 4),
+                          flat(M > 0 ? workspace : nullptr, (int64_t)need, 1)};
+    const Span ins[7] = {rows(dy, M, N, lddy, elem_size(y_dtype), true), rows(dres, M, N, lddres, xs, true),
+                         rows(codes, M, N, ldc, 1, false), flat(c_scale, M > 0 ? (M - 1) * ldcs + pairs : 0, 4),
+                         flat(gamma, N, elem_size(param_dtype)), flat(rstd, M, 4), flat(mean, M, 4)};
+    if (bad_aliasing(outs, 4, ins, 7)) return GBNORM_ERR_INVALID_ARG;
+    if (s != GBNORM_OK) return s;
+    t_last[1] = "";
+    int64_t P = 0;
+    if (M > 0) {
+        if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return GBNORM_ERR_WORKSPACE;
+        Q8BwdParams p{dy, reinterpret_cast<const uint8_t *>(codes), c_scale, dres, gamma, mean, rstd, dx,
+                      static_cast<float *>(workspace), lddy, ldc, ldcs, lddres, lddx, M, N, x_dtype, param_dtype,
+                      y_dtype, cg};
+        P = grid_of(M, 1, d);
+        t_last[1] = "elem";
+        const int st = launch(kQ8BwdElem[is_layernorm], P, kElemCTA, 0, &p, stream);
+        if (st != GBNORM_OK) return st;
+    }
+    return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, M > 0, stream);
+}
+
+int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int q_group, const float *scale,
+            const float *mid, int64_t s_row, int64_t s_group, const float *mean, const float *rstd, const void *gamma,
+            const void *beta, int param_dtype, void *y, int64_t ldy, int y_dtype, gbnorm_stream_t stream) {
+    const int qg = group_log2(q_group);
+    if (!valid_shape(M, N) || qg == -2 || !valid_dtype(param_dtype) || !valid_dtype(y_dtype) ||
+        (q_format != GBNORM_E4M3 && q_format != GBNORM_INT8))
+        return GBNORM_ERR_INVALID_ARG;
+    int64_t sspan = 0;
+    if (M > 0) {
+        if (!q || !scale || !y || !aligned(scale, 4) || !aligned(mid, 4) || !valid_ld(ldq, N, M) ||
+            !valid_ld(ldy, N, M))
+            return GBNORM_ERR_INVALID_ARG;
+        sspan = scale_span(M, groups_of(N, qg), s_row, s_group);
+        if (sspan == 0) return GBNORM_ERR_INVALID_ARG;
+    }
+    const int ps = elem_size(param_dtype);
+    const Span outs[1] = {rows(y, M, N, ldy, elem_size(y_dtype), false)};
+    const Span ins[7] = {rows(q, M, N, ldq, 1, false), flat(scale, sspan, 4), flat(mid, sspan, 4), flat(mean, M, 4),
+                         flat(rstd, M, 4), flat(gamma, N, ps), flat(beta, N, ps)};
+    if (bad_aliasing(outs, 1, ins, 7)) return GBNORM_ERR_INVALID_ARG;
+    HostDevice d;
+    const int s = host_device(&d);
+    if (s != GBNORM_OK) return s;
+    t_last[2] = "";
+    if (M == 0) return GBNORM_OK;
+    Q8ReadParams p{static_cast<const uint8_t *>(q), scale, mid, mean, rstd, gamma, beta, y, ldq, s_row, s_group, ldy,
+                   M, N, param_dtype, y_dtype, q_format, qg};
+    t_last[2] = "elem";
+    return launch(kQ8ReadElem, grid_of(M, 8, d), kElemCTA, 0, &p, stream);
+}
+
+int gbnorm_q8_last_variant(int what, char *buf, size_t len) {
+    if (what < 0 || what > 2 || !buf || len == 0) return GBNORM_ERR_INVALID_ARG;
+    std::snprintf(buf, len, "%s", t_last[what]);
+    return GBNORM_OK;
+}
+
+}  // extern "C"
