@@ -51,6 +51,9 @@ Span rows(const void *p, int64_t M, int64_t N, int64_t ld, int es, bool inplace)
 }
 Span flat(const void *p, int64_t n, int es) { return {p, p ? (size_t)n * (size_t)es : 0, 0, es, false}; }
 
+// 16-byte vectors for a row tensor: aligned base and row stride.
+bool vec_rows(const void *p, int64_t ld, int es) { return !p || (aligned(p, 16) && (ld * es) % 16 == 0); }
+
 bool overlap(const Span &a, const Span &b) {
     if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
@@ -89,6 +92,21 @@ int launch(const void *kernel, int64_t grid, int cta, size_t dyn, void *params, 
     if (cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)cta), args, dyn, s) != cudaSuccess)
         return GBNORM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
+}
+
+// Occupancy of a kernel (CTAs per SM), measured once per device and slot.
+constexpr int kSlots = 3 * 2 * 3 * kQ8MaxVariants;
+std::atomic<int> g_occ[kHostMaxDev][kSlots];
+int occupancy(int dev, int slot, const void *k, int cta, size_t dyn, int *occ) {
+    std::atomic<int> &c = g_occ[dev][slot];
+    int o = c.load(std::memory_order_relaxed);
+    if (o == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k, cta, dyn) != cudaSuccess) return GBNORM_ERR_CUDA;
+        if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
+        c.store(o, std::memory_order_relaxed);
+    }
+    *occ = o;
+    return GBNORM_OK;
 }
 
 // Persistent grid of `units` pieces of work at `per_sm` CTAs an SM.
@@ -153,6 +171,26 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
     if (s != GBNORM_OK) return s;
     t_last[0] = "";
     if (M == 0) return GBNORM_OK;
+    const bool vec = N % 8 == 0 && vec_rows(p.x, p.ldx, xs) && vec_rows(p.res, p.ldr, xs) && vec_rows(p.h, p.ldh, xs) &&
+                     vec_rows(p.y, p.ldy, elem_size(p.ydt)) && aligned(p.gamma, 16) && aligned(p.beta, 16) &&
+                     aligned(p.q, 8) && p.ldq % 8 == 0 && aligned(p.c, 8) && p.ldc % 8 == 0;
+    if (vec) {
+        const int kind = p.y ? 0 : p.c ? 2 : 1;
+        const Q8Table *const byt[3] = {&kQ8Fwd_f32[a.is_ln][kind], &kQ8Fwd_f16[a.is_ln][kind],
+                                       &kQ8Fwd_bf16[a.is_ln][kind]};
+        const Q8Table &t = *byt[p.xdt];
+        for (int i = 0; i < t.count; ++i) {
+            const Q8Variant &v = t.v[i];
+            if ((int64_t)v.tpr * v.vpt * 8 < N) continue;
+            int occ;
+            const int st = occupancy(d.dev, ((p.xdt * 2 + a.is_ln) * 3 + kind) * kQ8MaxVariants + i, v.kernel, v.cta, 0,
+                                     &occ);
+            if (st != GBNORM_OK) return st;
+            const int64_t rpc = v.cta / v.tpr;
+            t_last[0] = v.name;
+            return launch(v.kernel, grid_of((M + rpc - 1) / rpc, occ, d), v.cta, 0, &p, stream);
+        }
+    }
     t_last[0] = "elem";
     return launch(kQ8FwdElem[a.is_ln], grid_of(M, 8, d), kElemCTA, 0, &p, stream);
 }
@@ -180,7 +218,7 @@ int norm_fwd_q8(int is_layernorm, int64_t M, int64_t N, float eps, const void *x
     FwdArgs a{is_layernorm, {}, q_group, codes ? c_group : 128};
     a.p = Q8FwdParams{x, residual, h, gamma, beta, nullptr, static_cast<uint8_t *>(q), q_scale,
                       reinterpret_cast<uint8_t *>(codes), c_scale, mean, rstd, ldx, ldr, ldh, N, ldq, qs_row, qs_group,
-                      ldc, ldcs, M, N, eps, x_dtype, param_dtype, x_dtype, q_format, 0, 0};
+                      ldc, ldcs, M, N, eps, x_dtype, param_dtype, x_dtype, q_format, 0, 0, 1.f};
     return do_fwd(a, stream);
 }
 
@@ -192,7 +230,7 @@ int norm_fwd_ck8(int is_layernorm, int64_t M, int64_t N, float eps, const void *
     FwdArgs a{is_layernorm, {}, 0, c_group};
     a.p = Q8FwdParams{x, residual, h, gamma, beta, y, nullptr, nullptr, reinterpret_cast<uint8_t *>(codes), c_scale,
                       mean, rstd, ldx, ldr, ldh, ldy, N, 1, 1, ldc, ldcs, M, N, eps, x_dtype, param_dtype, y_dtype,
-                      GBNORM_E4M3, 0, 0};
+                      GBNORM_E4M3, 0, 0, 1.f};
     return do_fwd(a, stream);
 }
 

@@ -34,6 +34,7 @@ struct Q8FwdParams {
     float eps;
     int xdt, pdt, ydt;
     int qfmt, qg, cg;
+    float one;          // 1, not known at compile time (codes8_i8)
 };
 
 struct Q8BwdParams {
@@ -66,6 +67,20 @@ struct Q8ReadParams {
     int pdt, ydt;
     int qfmt, qg;
 };
+
+// A compiled kernel with rows in registers: capacity tpr * vpt * 8 elements.
+struct Q8Variant {
+    const char *name;
+    const void *kernel;
+    int tpr, vpt, cta;
+};
+struct Q8Table {
+    const Q8Variant *v;  // by capacity
+    int count;
+};
+constexpr int kQ8MaxVariants = 24;  // entries per table
+// Forward, [is_ln][y and checkpoint, 8-bit output, 8-bit output and checkpoint].
+extern const Q8Table kQ8Fwd_f32[2][3], kQ8Fwd_f16[2][3], kQ8Fwd_bf16[2][3];
 
 // Element-wise kernels, [is_ln].
 extern const void *const kQ8FwdElem[2];
