@@ -10,13 +10,13 @@ namespace gbn {
 #define GBN_Q8F_GEOMS(X) \
     X(32, 1, 256, 4)     \
     X(32, 2, 256, 4)     \
-    X(32, 4, 256, 2)     \
-    X(64, 4, 256, 2)     \
-    X(128, 4, 256, 2)    \
-    X(256, 3, 256, 2)    \
-    X(256, 4, 256, 2)    \
-    X(512, 3, 512, 1)    \
-    X(512, 4, 512, 1)
+    X(32, 4, 256, 4)     \
+    X(64, 4, 256, 4)     \
+    X(128, 4, 256, 4)    \
+    X(256, 3, 256, 4)    \
+    X(256, 4, 256, 4)    \
+    X(512, 3, 512, 2)    \
+    X(512, 4, 512, 2)
 
 #define GBN_STR2(x) #x
 #define GBN_STR(x) GBN_STR2(x)

@@ -16,6 +16,8 @@
 //     statistics too.
 #pragma once
 
+#include <type_traits>
+
 #include "q8_common.cuh"
 
 namespace gbn {
@@ -50,10 +52,6 @@ template <int XT> __device__ __forceinline__ void unpack8(const Raw8<XT> &r, flo
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = vpair<T>(r.v[i / PW], i % PW);
 }
-template <int XT> __device__ __forceinline__ float2 round2(float2 v) {
-    if constexpr (XT == kF32) return v;
-    return make_float2(round_to(v.x, XT), round_to(v.y, XT));
-}
 // Chunk c of a parameter row (read-only, kept in L1), or the constant an
 // absent one stands for.
 __device__ __forceinline__ void par8g(const void *row, int64_t c, int dt, float absent, float2 (&f)[4]) {
@@ -74,6 +72,19 @@ __device__ __forceinline__ void par8g(const void *row, int64_t c, int dt, float 
             for (int i = 0; i < 4; ++i) f[i] = vpair<__half>(a, i);
         }
     }
+}
+
+template <int XT> __device__ __forceinline__ Raw8<XT> pack8(const float2 (&f)[4]) {
+    using T = typename TypeOf<XT>::T;
+    Raw8<XT> r;
+    r.v[0] = vpack2<T>(f);
+    if constexpr (XT == kF32) r.v[1] = vpack2<T>(f + 2);
+    return r;
+}
+template <int XT> __device__ __forceinline__ void st_raw8(void *row, int64_t c, const Raw8<XT> &r) {
+    constexpr int W = XT == kF32 ? 2 : 1;
+#pragma unroll
+    for (int w = 0; w < W; ++w) st_vec(row, c * W + w, r.v[w]);
 }
 
 __device__ __forceinline__ float amax8(const float2 (&f)[4]) {
@@ -146,7 +157,54 @@ __device__ __forceinline__ void group_sum_max(float &s, float &m, float *scratch
     }
 }
 
+// Maximum and minimum of the chunks of a group, one chunk a lane, over its
+// 2^lg lanes; `ok` false: no chunk here.
+template <int XT>
+__device__ __forceinline__ void lanes_range(const Raw8<XT> &r, bool ok, int lg, float &top, float &low) {
+    if constexpr (XT == kF32) {
+        float2 f[4];
+        unpack8<XT>(r, f);
+        top = -INFINITY, low = INFINITY;
+        if (ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                top = fmax_nan(top, fmax_nan(f[i].x, f[i].y));
+                low = fmin_nan(low, fmin_nan(f[i].x, f[i].y));
+            }
+        }
+        top = lanes_max(top, lg);
+        low = lanes_min(low, lg);
+    } else {
+        // on pairs of the stored type, then (max, -min) as one pair, so that a
+        // butterfly step is one shuffle and one maximum
+        using T2 = typename std::conditional<XT == kBF16, __nv_bfloat162, __half2>::type;
+        const T2 *p = reinterpret_cast<const T2 *>(&r.v[0]);
+        const T2 hi = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+        const T2 lo = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
+        T2 m;
+        m.x = __hmax_nan(hi.x, hi.y);
+        m.y = __hneg(__hmin_nan(lo.x, lo.y));
+        uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
+        constexpr uint32_t kLowest = XT == kBF16 ? 0xff80ff80u : 0xfc00fc00u;  // (-inf, -inf)
+        if (!ok) w = kLowest;
+#pragma unroll
+        for (int o = 0; o < 5; ++o)
+            if (o < lg) {
+                const uint32_t v = __shfl_xor_sync(0xffffffffu, w, 1 << o);
+                const T2 n = __hmax2_nan(*reinterpret_cast<const T2 *>(&w), *reinterpret_cast<const T2 *>(&v));
+                w = *reinterpret_cast<const uint32_t *>(&n);
+            }
+        const T2 n = *reinterpret_cast<const T2 *>(&w);
+        top = to_f(n.x);
+        low = -to_f(n.y);
+    }
+}
+
 // OUT 0: y in ydt; 1: 8-bit rows.  CK: the checkpoint too.
+//
+// A row stays in its storage type between the passes (half the registers of
+// fp32 for 16-bit types, so that more rows are in flight) and is widened, and
+// RMSNorm's product with gamma formed, again in each.
 template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int OUT, bool CK>
 __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
     static_assert(NT % TPR == 0 && TPR % 32 == 0 && NT / TPR < 16, "row groups");
@@ -154,48 +212,44 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
     __shared__ __align__(16) float scratch_all[RPC * 4 * WPR];
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     float *scratch = scratch_all + grp * 4 * WPR;
-    const int64_t nc = p.N / 8;
+    const int nc = (int)(p.N / 8);
     const float n = (float)p.N;
-    const bool full = nc == (int64_t)TPR * VPT;  // every thread holds VPT chunks (uniform)
-    const int xes = XT == kF32 ? 4 : 2;
+    const bool full = nc == TPR * VPT;  // every thread holds VPT chunks (uniform)
+    constexpr int xes = XT == kF32 ? 4 : 2;
     const float qmax = q8_max(p.qfmt);
     const int qlg = p.qg - 3, clg = p.cg - 3;  // log2 of the lanes of a group
     int parity = 0;
     for (int64_t row = (int64_t)blockIdx.x * RPC + grp; row < p.M; row += (int64_t)gridDim.x * RPC) {
+        Raw8<XT> h[VPT];
         const unsigned char *xr = static_cast<const unsigned char *>(p.x) + row * p.ldx * xes;
-        float2 v[VPT][4];  // h; RMSNorm's 8-bit output: h * gamma
-        {
-            Raw8<XT> xw[VPT], rw[VPT];
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (k * TPR + t < nc) xw[k] = ld_raw8<XT>(xr, k * TPR + t);
-            if (p.res) {
-                const unsigned char *rr = static_cast<const unsigned char *>(p.res) + row * p.ldr * xes;
+        for (int k = 0; k < VPT; ++k) {
+            h[k] = Raw8<XT>{};
+            if (k * TPR + t < nc) h[k] = ld_raw8<XT>(xr, k * TPR + t);
+        }
+        if (p.res) {
+            const unsigned char *rr = static_cast<const unsigned char *>(p.res) + row * p.ldr * xes;
+            Raw8<XT> r[VPT];
 #pragma unroll
-                for (int k = 0; k < VPT; ++k)
-                    if (k * TPR + t < nc) rw[k] = ld_raw8<XT>(rr, k * TPR + t);
+            for (int k = 0; k < VPT; ++k) {
+                r[k] = Raw8<XT>{};
+                if (k * TPR + t < nc) r[k] = ld_raw8<XT>(rr, k * TPR + t);
             }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                if (k * TPR + t < nc) {
-                    unpack8<XT>(xw[k], v[k]);
-                    if (p.res) {
-                        float2 r8[4];
-                        unpack8<XT>(rw[k], r8);
+                float2 a[4], b[4];
+                unpack8<XT>(h[k], a);
+                unpack8<XT>(r[k], b);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[k][i] = round2<XT>(f2add(v[k][i], r8[i]));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[k][i] = f2s(0.f);
-                }
+                for (int i = 0; i < 4; ++i) a[i] = f2add(a[i], b[i]);
+                h[k] = pack8<XT>(a);  // the sum rounded once to the storage type
             }
-        }
-        if (p.h) {
-            unsigned char *hr = static_cast<unsigned char *>(p.h) + row * p.ldh * xes;
+            if (p.h) {
+                unsigned char *hr = static_cast<unsigned char *>(p.h) + row * p.ldh * xes;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (k * TPR + t < nc) st8p(hr, 8 * (int64_t)(k * TPR + t), XT, v[k]);
+                for (int k = 0; k < VPT; ++k)
+                    if (k * TPR + t < nc) st_raw8<XT>(hr, k * TPR + t, h[k]);
+            }
         }
         if constexpr (CK) {
             uint8_t *cr = p.c + row * p.ldc;
@@ -203,183 +257,161 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int c = k * TPR + t;
-                float top = -INFINITY, low = INFINITY;
-                if (c < nc) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        top = fmax_nan(top, fmax_nan(v[k][i].x, v[k][i].y));
-                        low = fmin_nan(low, fmin_nan(v[k][i].x, v[k][i].y));
-                    }
-                }
-                const CkGroup g = ck_group(lanes_max(top, clg), lanes_min(low, clg));
+                float top, low;
+                lanes_range<XT>(h[k], c < nc, clg, top, low);
+                const CkGroup g = ck_group(top, low);
                 if (c < nc) {
                     const float2 nm = f2s(-g.mid), inv = f2s(g.inv);
                     float2 u[4];
+                    unpack8<XT>(h[k], u);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f2mul(f2add(v[k][i], nm), inv);
+                    for (int i = 0; i < 4; ++i) u[i] = f2mul(f2add(u[i], nm), inv);
                     *reinterpret_cast<uint2 *>(cr + 8 * c) = codes8_i8(u, p.one);
                     if ((c & ((1 << clg) - 1)) == 0)
                         *reinterpret_cast<float2 *>(cs + 2 * (c >> clg)) = make_float2(g.scale, g.mid);
                 }
             }
         }
-        float2 a2 = f2s(0.f);
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a2 = LN ? f2add(a2, v[k][i]) : f2fma(v[k][i], v[k][i], a2);
-        float acc = a2.x + a2.y, unused = 0.f;
 
-        if constexpr (!LN && OUT == 1) {
-            // t = h * gamma
+        // ---------------------------------------------------------------- sums of the row
+        uint8_t *qr = p.q + row * p.ldq;
+        float *qs = p.qs + row * p.qs_row;
+        float2 a2 = f2s(0.f);
+        float m = 0.f, unused = 0.f;
+        constexpr bool RQ = !LN && OUT == 1;  // codes of h * gamma
+        float amax[VPT];
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (k * TPR + t < nc) {
+        for (int k = 0; k < VPT; ++k) {
+            const int c = k * TPR + t;
+            float2 v[4];
+            unpack8<XT>(h[k], v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a2 = LN ? f2add(a2, v[i]) : f2fma(v[i], v[i], a2);
+            if constexpr (RQ) {
+                if (c < nc && p.gamma) {
                     float2 g8[4];
-                    par8g(p.gamma, k * TPR + t, p.pdt, 1.f, g8);
+                    par8g(p.gamma, c, p.pdt, 1.f, g8);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[k][i] = f2mul(v[k][i], g8[i]);
+                    for (int i = 0; i < 4; ++i) v[i] = f2mul(v[i], g8[i]);
                 }
-            uint8_t *qr = p.q + row * p.ldq;
-            float amax[VPT];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) amax[k] = amax8(v[k]);
-            if (p.qg >= 0) {
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) {
+                amax[k] = amax8(v);
+                if (p.qg >= 0) {
                     amax[k] = lanes_max(amax[k], qlg);
                     const float2 inv = f2s(q8_inv(amax[k], qmax));
-                    float2 u[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f2mul(v[k][i], inv);
-                    if (k * TPR + t < nc) *reinterpret_cast<uint2 *>(qr + 8 * (k * TPR + t)) = codes8(u, p.qfmt, p.one);
-                }
-                group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
-                const float rstd = rsqrtf(acc / n + p.eps);
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int c = k * TPR + t;
-                    if (c < nc && (c & ((1 << qlg) - 1)) == 0)
-                        p.qs[row * p.qs_row + (c >> qlg) * p.qs_grp] = q8_scale(amax[k], rstd, qmax);
-                }
-                if (t == 0 && p.rstd) p.rstd[row] = rstd;
-            } else {
-                float m = amax[0];
-#pragma unroll
-                for (int k = 1; k < VPT; ++k) m = fmax_nan(m, amax[k]);
-                group_sum_max<TPR, true>(acc, m, scratch, parity, 1 + grp);
-                const float rstd = rsqrtf(acc / n + p.eps);
-                const float2 inv = f2s(q8_inv(m, qmax));
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    float2 u[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f2mul(v[k][i], inv);
-                    if (k * TPR + t < nc) *reinterpret_cast<uint2 *>(qr + 8 * (k * TPR + t)) = codes8(u, p.qfmt, p.one);
-                }
-                if (t == 0) {
-                    p.qs[row * p.qs_row] = q8_scale(m, rstd, qmax);
-                    if (p.rstd) p.rstd[row] = rstd;
+                    for (int i = 0; i < 4; ++i) v[i] = f2mul(v[i], inv);
+                    if (c < nc) *reinterpret_cast<uint2 *>(qr + 8 * c) = codes8(v, p.qfmt, p.one);
+                } else {
+                    m = fmax_nan(m, amax[k]);
                 }
             }
-            continue;
         }
-
-        float mean = 0.f;
+        float acc = a2.x + a2.y, mean = 0.f;
         if constexpr (LN) {
+            float2 q2 = f2s(0.f);
             if (full) {
                 constexpr float kC = (float)(VPT * 8);
                 mean = acc * (1.f / kC);
-                const float2 nm = f2s(-mean);
-                float2 q2 = f2s(0.f);
-#pragma unroll
-                for (int k = 0; k < VPT; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 d = f2add(v[k][i], nm);
-                        q2 = f2fma(d, d, q2);
-                    }
-                acc = q2.x + q2.y;
-                group_meanvar_equal<TPR>(mean, acc, kC, scratch, parity, 1 + grp);
             } else {
                 group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
                 mean = acc / n;
-                const float2 nm = f2s(-mean);
-                float2 q2 = f2s(0.f);
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    if (k * TPR + t >= nc) continue;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 d = f2add(v[k][i], nm);
-                        q2 = f2fma(d, d, q2);
-                    }
-                }
-                acc = q2.x + q2.y;
-                group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
             }
+            const float2 nm = f2s(-mean);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                if (k * TPR + t >= nc) continue;
+                float2 v[4];
+                unpack8<XT>(h[k], v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 d = f2add(v[i], nm);
+                    q2 = f2fma(d, d, q2);
+                }
+            }
+            acc = q2.x + q2.y;
+            if (full) group_meanvar_equal<TPR>(mean, acc, (float)(VPT * 8), scratch, parity, 1 + grp);
+            else group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
         } else {
-            group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
+            group_sum_max<TPR, RQ>(acc, m, scratch, parity, 1 + grp);
         }
         const float rstd = rsqrtf(acc / n + p.eps);
         if (t == 0) {
             if (p.rstd) p.rstd[row] = rstd;
             if (LN && p.mean) p.mean[row] = mean;
         }
+
+        // ---------------------------------------------------------------- output
         const float2 nm = f2s(-mean), rs = f2s(rstd);
-        float m = 0.f;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
+        // chunk k of y (RQ: of h * gamma); zeros past the row's end
+        auto out8 = [&](int k, float2 (&o)[4]) {
             const int c = k * TPR + t;
-            float2 o[4];
+            unpack8<XT>(h[k], o);
             if (c < nc) {
-                float2 g8[4];
-                par8g(p.gamma, c, p.pdt, 1.f, g8);
+                if constexpr (LN) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = f2mul(f2mul(LN ? f2add(v[k][i], nm) : v[k][i], rs), g8[i]);
+                    for (int i = 0; i < 4; ++i) o[i] = f2mul(f2add(o[i], nm), rs);
+                } else if constexpr (!RQ) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], rs);
+                }
+                if (p.gamma) {
+                    float2 g8[4];
+                    par8g(p.gamma, c, p.pdt, 1.f, g8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], g8[i]);
+                }
                 if (LN && p.beta) {
                     float2 b8[4];
                     par8g(p.beta, c, p.pdt, 0.f, b8);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = f2add(o[i], b8[i]);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = f2s(0.f);
             }
-            if constexpr (OUT == 0) {
-                if (c < nc) st8p(row_ptr(p.y, row, p.ldy, p.ydt), 8 * (int64_t)c, p.ydt, o);
-            } else if (p.qg >= 0) {
-                const float amax = lanes_max(amax8(o), qlg);
-                const float2 inv = f2s(q8_inv(amax, qmax));
-                if (c < nc) {
-                    float2 u[4];
+        };
+        if constexpr (OUT == 0) {
+            void *yr = row_ptr(p.y, row, p.ldy, p.ydt);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f2mul(o[i], inv);
-                    *reinterpret_cast<uint2 *>(p.q + row * p.ldq + 8 * c) = codes8(u, p.qfmt, p.one);
-                    if ((c & ((1 << qlg) - 1)) == 0)
-                        p.qs[row * p.qs_row + (c >> qlg) * p.qs_grp] = q8_scale(amax, 1.f, qmax);
+            for (int k = 0; k < VPT; ++k) {
+                float2 o[4];
+                out8(k, o);
+                if (k * TPR + t < nc) st8p(yr, 8 * (int64_t)(k * TPR + t), p.ydt, o);
+            }
+        } else if (p.qg >= 0) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = k * TPR + t;
+                if constexpr (!RQ) {
+                    float2 o[4];
+                    out8(k, o);
+                    amax[k] = lanes_max(amax8(o), qlg);
+                    const float2 inv = f2s(q8_inv(amax[k], qmax));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], inv);
+                    if (c < nc) *reinterpret_cast<uint2 *>(qr + 8 * c) = codes8(o, p.qfmt, p.one);
                 }
-            } else {
-                m = fmax_nan(m, amax8(o));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[k][i] = o[i];
+                if (c < nc && (c & ((1 << qlg) - 1)) == 0)
+                    qs[(c >> qlg) * p.qs_grp] = q8_scale(amax[k], RQ ? rstd : 1.f, qmax);
             }
-        }
-        if constexpr (OUT == 1) {
-            if (p.qg < 0) {
-                group_sum_max<TPR, true>(unused, m, scratch, parity, 1 + grp);
-                const float2 inv = f2s(q8_inv(m, qmax));
+        } else {
+            if constexpr (!RQ) {
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
-                    float2 u[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f2mul(v[k][i], inv);
-                    if (k * TPR + t < nc)
-                        *reinterpret_cast<uint2 *>(p.q + row * p.ldq + 8 * (k * TPR + t)) = codes8(u, p.qfmt, p.one);
+                    float2 o[4];
+                    out8(k, o);
+                    m = fmax_nan(m, amax8(o));
                 }
-                if (t == 0) p.qs[row * p.qs_row] = q8_scale(m, 1.f, qmax);
+                group_sum_max<TPR, true>(unused, m, scratch, parity, 1 + grp);
             }
+            const float2 inv = f2s(q8_inv(m, qmax));
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                float2 o[4];
+                out8(k, o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], inv);
+                if (k * TPR + t < nc) *reinterpret_cast<uint2 *>(qr + 8 * (k * TPR + t)) = codes8(o, p.qfmt, p.one);
+            }
+            if (t == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax);
         }
     }
 }
