@@ -95,12 +95,14 @@ int launch(const void *kernel, int64_t grid, int cta, size_t dyn, void *params, 
 }
 
 // Occupancy of a kernel (CTAs per SM), measured once per device and slot.
-constexpr int kSlots = 3 * 2 * 3 * kQ8MaxVariants;
+constexpr int kSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants;
 std::atomic<int> g_occ[kHostMaxDev][kSlots];
 int occupancy(int dev, int slot, const void *k, int cta, size_t dyn, int *occ) {
     std::atomic<int> &c = g_occ[dev][slot];
     int o = c.load(std::memory_order_relaxed);
     if (o == 0) {
+        if (dyn > 0 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn) != cudaSuccess)
+            return GBNORM_ERR_CUDA;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k, cta, dyn) != cudaSuccess) return GBNORM_ERR_CUDA;
         if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
         c.store(o, std::memory_order_relaxed);
@@ -175,20 +177,20 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
                      vec_rows(p.y, p.ldy, elem_size(p.ydt)) && aligned(p.gamma, 16) && aligned(p.beta, 16) &&
                      aligned(p.q, 8) && p.ldq % 8 == 0 && aligned(p.c, 8) && p.ldc % 8 == 0;
     if (vec) {
-        const int kind = p.y ? 0 : p.c ? 2 : 1;
-        const Q8Table *const byt[3] = {&kQ8Fwd_f32[a.is_ln][kind], &kQ8Fwd_f16[a.is_ln][kind],
-                                       &kQ8Fwd_bf16[a.is_ln][kind]};
-        const Q8Table &t = *byt[p.xdt];
+        static const Q8Table *const tables[2][3] = {{kQ8Fwd_rms_f32, kQ8Fwd_rms_f16, kQ8Fwd_rms_bf16},
+                                                    {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16, kQ8Fwd_ln_bf16}};
+        const int kind = p.y ? 0 : (p.qg < 0 ? 1 : 2) + (p.c ? 2 : 0);
+        const Q8Table &t = tables[a.is_ln][p.xdt][kind];
         for (int i = 0; i < t.count; ++i) {
             const Q8Variant &v = t.v[i];
             if ((int64_t)v.tpr * v.vpt * 8 < N) continue;
             int occ;
-            const int st = occupancy(d.dev, ((p.xdt * 2 + a.is_ln) * 3 + kind) * kQ8MaxVariants + i, v.kernel, v.cta, 0,
-                                     &occ);
+            const int st = occupancy(d.dev, ((p.xdt * 2 + a.is_ln) * kQ8FwdKinds + kind) * kQ8MaxVariants + i, v.kernel,
+                                     v.cta, (size_t)v.smem, &occ);
             if (st != GBNORM_OK) return st;
             const int64_t rpc = v.cta / v.tpr;
             t_last[0] = v.name;
-            return launch(v.kernel, grid_of((M + rpc - 1) / rpc, occ, d), v.cta, 0, &p, stream);
+            return launch(v.kernel, grid_of((M + rpc - 1) / rpc, occ, d), v.cta, (size_t)v.smem, &p, stream);
         }
     }
     t_last[0] = "elem";

@@ -73,14 +73,18 @@ struct Q8Variant {
     const char *name;
     const void *kernel;
     int tpr, vpt, cta;
+    int smem;  // dynamic shared memory
 };
 struct Q8Table {
     const Q8Variant *v;  // by capacity
     int count;
 };
 constexpr int kQ8MaxVariants = 24;  // entries per table
-// Forward, [is_ln][y and checkpoint, 8-bit output, 8-bit output and checkpoint].
-extern const Q8Table kQ8Fwd_f32[2][3], kQ8Fwd_f16[2][3], kQ8Fwd_bf16[2][3];
+// Forward: y and checkpoint; 8-bit rows with a scale per row, with group
+// scales; the same two with the checkpoint.
+constexpr int kQ8FwdKinds = 5;
+extern const Q8Table kQ8Fwd_rms_f32[kQ8FwdKinds], kQ8Fwd_rms_f16[kQ8FwdKinds], kQ8Fwd_rms_bf16[kQ8FwdKinds];
+extern const Q8Table kQ8Fwd_ln_f32[kQ8FwdKinds], kQ8Fwd_ln_f16[kQ8FwdKinds], kQ8Fwd_ln_bf16[kQ8FwdKinds];
 
 // Element-wise kernels, [is_ln].
 extern const void *const kQ8FwdElem[2];

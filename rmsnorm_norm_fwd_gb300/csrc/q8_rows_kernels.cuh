@@ -14,6 +14,12 @@
 //     and the maximum are one reduction with one barrier.
 //   - The checkpoint's codes need h alone and are written before the
 //     statistics too.
+//   - A row stays in its storage type between the passes (half the registers
+//     of fp32 for 16-bit types): four 256-thread CTAs share an SM (LayerNorm
+//     three), and their phases overlap.
+//   - Every thread keeps gamma (beta) of its own columns as fp32 in its own
+//     slots of shared memory: no conversion, no branch on the parameter type
+//     and no barrier in the loop.
 #pragma once
 
 #include <type_traits>
@@ -87,11 +93,14 @@ template <int XT> __device__ __forceinline__ void st_raw8(void *row, int64_t c, 
     for (int w = 0; w < W; ++w) st_vec(row, c * W + w, r.v[w]);
 }
 
+// max(|a|, |b|, m) and max / min of three, NaN kept.
+__device__ __forceinline__ float amax3(float m, float2 f) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(f.x), "f"(f.y));
+    return r;
+}
 __device__ __forceinline__ float amax8(const float2 (&f)[4]) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmax_nan(m, fmax_nan(fabsf(f[i].x), fabsf(f[i].y)));
-    return m;
+    return fmax_nan(amax3(amax3(0.f, f[0]), f[1]), amax3(amax3(0.f, f[2]), f[3]));
 }
 // Maximum over the aligned 2^lg lanes of a group (lg <= 5, uniform).
 __device__ __forceinline__ float lanes_max(float v, int lg) {
@@ -124,36 +133,108 @@ __device__ __forceinline__ uint2 codes8_i8(const float2 (&u)[4], float one) {
     }
     return make_uint2(w[0], w[1]);
 }
+__device__ __forceinline__ uint32_t e4m3_quad(float2 a, float2 b) {
+    uint32_t w;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(w)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return w;
+}
 __device__ __forceinline__ uint2 codes8(const float2 (&u)[4], int fmt, float one) {
     if (fmt == kI8) return codes8_i8(u, one);
-    return make_uint2(e4m3_pair(u[0].x, u[0].y) | e4m3_pair(u[1].x, u[1].y) << 16,
-                      e4m3_pair(u[2].x, u[2].y) | e4m3_pair(u[3].x, u[3].y) << 16);
+    return make_uint2(e4m3_quad(u[0], u[1]), e4m3_quad(u[2], u[3]));
 }
 
+// Lanes that combine WPR warps' partials in a butterfly (a power of two; the
+// same on every warp and, each step being commutative, the same bits on every
+// lane).
+__host__ __device__ constexpr int pow2_at_least(int v) { return v <= 1 ? 1 : 2 * pow2_at_least((v + 1) / 2); }
+
 // Sum over a row group of `s` and maximum (NaN kept) of `m`, through this
-// group's scratch of [2][2][WPR] floats under its named barrier; the same bits
+// group's scratch of [2][WPR] float4 under its named barrier; the same bits
 // on every thread.
 template <int TPR, bool MAX>
-__device__ __forceinline__ void group_sum_max(float &s, float &m, float *scratch, int &parity, int bar_id) {
+__device__ __forceinline__ void group_sum_max(float &s, float &m, float4 *scratch, int &parity, int bar_id) {
+    auto step = [&](int o) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if constexpr (MAX) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    };
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) step(o);
+    if constexpr (TPR > 32) {
+        constexpr int WPR = TPR / 32, L = pow2_at_least(WPR);
+        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+        float4 *buf = scratch + parity * WPR;
+        if (lane == 0) buf[wig] = make_float4(s, MAX ? m : 0.f, 0.f, 0.f);
+        named_sync(bar_id, TPR);
+        const int w = lane & (L - 1);
+        const float4 b = w < WPR ? buf[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+        s = b.x;
+        if constexpr (MAX) m = b.y;  // maxima here are of magnitudes
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) step(o);
+        parity ^= 1;
+    }
+}
+
+// Mean and sum of squared deviations of a row group from its threads' own, of
+// `cnt` elements each (the update of Chan, Golub and LeVeque in its group
+// form, once over a warp's lanes, once over the warps).  EQUAL: every thread
+// has cnt, known at compile time.
+template <int TPR, bool EQUAL>
+__device__ __forceinline__ void group_meanvar(float &mean, float &m2, float cnt, float inv_n, float4 *scratch,
+                                              int &parity, int bar_id) {
+    float s = EQUAL ? mean : mean * cnt, c = cnt;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
-        if constexpr (MAX) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if constexpr (!EQUAL) c += __shfl_xor_sync(0xffffffffu, c, o);
     }
-    if constexpr (TPR > 32) {
-        constexpr int WPR = TPR / 32;
-        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
-        float2 *buf = reinterpret_cast<float2 *>(scratch) + parity * WPR;
-        if (lane == 0) buf[wig] = make_float2(s, MAX ? m : 0.f);
-        named_sync(bar_id, TPR);
-        s = 0.f;
+    const float mw = EQUAL ? s * (1.f / 32) : c > 0.f ? s / c : 0.f;
+    const float d = mean - mw;
+    float q = EQUAL || cnt > 0.f ? m2 + cnt * (d * d) : 0.f;
 #pragma unroll
-        for (int w = 0; w < WPR; ++w) {
-            const float2 b = buf[w];
-            s += b.x;
-            if constexpr (MAX) m = fmax_nan(m, b.y);
-        }
+    for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+    mean = mw;
+    m2 = q;
+    if constexpr (TPR > 32) {
+        constexpr int WPR = TPR / 32, L = pow2_at_least(WPR);
+        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+        float4 *buf = scratch + parity * WPR;
+        if (lane == 0) buf[wig] = make_float4(mw, q, EQUAL ? cnt * 32.f : c, 0.f);
+        named_sync(bar_id, TPR);
+        const int w = lane & (L - 1);
+        const float4 b = w < WPR ? buf[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+        s = b.x * b.z;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        mean = s * inv_n;
+        const float dd = b.x - mean;
+        m2 = b.z > 0.f ? b.y + b.z * (dd * dd) : 0.f;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
         parity ^= 1;
+    }
+}
+
+// h = x + r rounded once to the storage type.
+template <int XT> __device__ __forceinline__ void add8(Raw8<XT> &h, const Raw8<XT> &r) {
+    if constexpr (XT == kF32) {
+        float2 a[4], b[4];
+        unpack8<XT>(h, a);
+        unpack8<XT>(r, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = f2add(a[i], b[i]);
+        h = pack8<XT>(a);
+    } else {
+        using T2 = typename std::conditional<XT == kBF16, __nv_bfloat162, __half2>::type;
+        T2 *a = reinterpret_cast<T2 *>(&h.v[0]);
+        const T2 *b = reinterpret_cast<const T2 *>(&r.v[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = __hadd2_rn(a[i], b[i]);
     }
 }
 
@@ -200,24 +281,48 @@ __device__ __forceinline__ void lanes_range(const Raw8<XT> &r, bool ok, int lg, 
     }
 }
 
-// OUT 0: y in ydt; 1: 8-bit rows.  CK: the checkpoint too.
-//
-// A row stays in its storage type between the passes (half the registers of
-// fp32 for 16-bit types, so that more rows are in flight) and is widened, and
-// RMSNorm's product with gamma formed, again in each.
-template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int OUT, bool CK>
-__global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
-    static_assert(NT % TPR == 0 && TPR % 32 == 0 && NT / TPR < 16, "row groups");
+// The VPT groups that a lane's chunks belong to cost one division each; lane l
+// takes that of chunk l mod 4 alone, and the lanes of a group (at least four)
+// fetch the results from one another.
+template <int VPT> __device__ __forceinline__ int own_chunk(int lane) {
+    return VPT <= 1 ? 0 : (VPT == 2 ? lane & 1 : (lane & 3) < VPT ? lane & 3 : VPT - 1);
+}
+template <int VPT> __device__ __forceinline__ float pick(const float (&a)[VPT], int k) {
+    float r = a[0];
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) r = k == i ? a[i] : r;
+    return r;
+}
+template <int VPT> __device__ __forceinline__ float fetch(float own, int lane, int k) {
+    return VPT == 1 ? own : __shfl_sync(0xffffffffu, own, (lane & ~3) | k);
+}
+
+constexpr int kOutY = 0, kOutRow = 1, kOutGroup = 2;  // y in ydt; 8-bit rows with a scale per row; per group
+
+// Bytes of shared memory for the threads' own parameters.
+__host__ __device__ constexpr int q8_fwd_smem(bool ln, int vpt, int nt) { return nt * vpt * 32 * (ln ? 2 : 1); }
+
+// FULL: every thread holds VPT chunks.
+template <bool LN, int XT, int TPR, int VPT, int NT, int OUT, bool CK, bool FULL>
+__device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, float4 *scratch_all) {
     constexpr int RPC = NT / TPR, WPR = TPR / 32;
-    __shared__ __align__(16) float scratch_all[RPC * 4 * WPR];
-    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    float *scratch = scratch_all + grp * 4 * WPR;
-    const int nc = (int)(p.N / 8);
-    const float n = (float)p.N;
-    const bool full = nc == TPR * VPT;  // every thread holds VPT chunks (uniform)
     constexpr int xes = XT == kF32 ? 4 : 2;
-    const float qmax = q8_max(p.qfmt);
+    constexpr bool RQ = !LN && OUT != kOutY;  // codes of h * gamma
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31;
+    float4 *scratch = scratch_all + grp * 2 * WPR;
+    const int nc = (int)(p.N / 8);
+    const float inv_n = 1.f / (float)p.N;
+    const float qmax = q8_max(p.qfmt), inv_qmax = 1.f / qmax;
     const int qlg = p.qg - 3, clg = p.cg - 3;  // log2 of the lanes of a group
+    const int own = own_chunk<VPT>(lane);
+    auto has = [&](int k) { return FULL || k * TPR + t < nc; };
+    float4 *gp = par + threadIdx.x, *bp = par + 2 * VPT * NT + threadIdx.x;
+    auto param = [&](const float4 *q, int k, float2 (&f)[4]) {
+        const float4 a = q[2 * k * NT], b = q[(2 * k + 1) * NT];
+        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+    };
+    bool first = true;
     int parity = 0;
     for (int64_t row = (int64_t)blockIdx.x * RPC + grp; row < p.M; row += (int64_t)gridDim.x * RPC) {
         Raw8<XT> h[VPT];
@@ -225,7 +330,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             h[k] = Raw8<XT>{};
-            if (k * TPR + t < nc) h[k] = ld_raw8<XT>(xr, k * TPR + t);
+            if (has(k)) h[k] = ld_raw8<XT>(xr, k * TPR + t);
         }
         if (p.res) {
             const unsigned char *rr = static_cast<const unsigned char *>(p.res) + row * p.ldr * xes;
@@ -233,108 +338,138 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 r[k] = Raw8<XT>{};
-                if (k * TPR + t < nc) r[k] = ld_raw8<XT>(rr, k * TPR + t);
+                if (has(k)) r[k] = ld_raw8<XT>(rr, k * TPR + t);
             }
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float2 a[4], b[4];
-                unpack8<XT>(h[k], a);
-                unpack8<XT>(r[k], b);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = f2add(a[i], b[i]);
-                h[k] = pack8<XT>(a);  // the sum rounded once to the storage type
-            }
+            for (int k = 0; k < VPT; ++k) add8<XT>(h[k], r[k]);
             if (p.h) {
                 unsigned char *hr = static_cast<unsigned char *>(p.h) + row * p.ldh * xes;
 #pragma unroll
                 for (int k = 0; k < VPT; ++k)
-                    if (k * TPR + t < nc) st_raw8<XT>(hr, k * TPR + t, h[k]);
+                    if (has(k)) st_raw8<XT>(hr, k * TPR + t, h[k]);
+            }
+        }
+        if (first) {  // behind the first row's loads
+            first = false;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                float2 f[4];
+                par8g(has(k) ? p.gamma : nullptr, k * TPR + t, p.pdt, 1.f, f);
+                gp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+                gp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+                if constexpr (LN) {
+                    par8g(has(k) ? p.beta : nullptr, k * TPR + t, p.pdt, 0.f, f);
+                    bp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+                    bp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+                }
             }
         }
         if constexpr (CK) {
             uint8_t *cr = p.c + row * p.ldc;
-            float *cs = p.cs + row * p.ldcs;
+            float top[VPT], low[VPT];
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) lanes_range<XT>(h[k], has(k), clg, top[k], low[k]);
+            const CkGroup g = ck_group(pick<VPT>(top, own), pick<VPT>(low, own));
+            // the first lanes of a group write its pairs, lane k of it chunk k's
+            const int at = own * TPR + (t & ~((1 << clg) - 1));
+            if ((lane & ((1 << clg) - 1)) < VPT && (FULL || at < nc))
+                *reinterpret_cast<float2 *>(p.cs + row * p.ldcs + 2 * (at >> clg)) = make_float2(g.scale, g.mid);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int c = k * TPR + t;
-                float top, low;
-                lanes_range<XT>(h[k], c < nc, clg, top, low);
-                const CkGroup g = ck_group(top, low);
-                if (c < nc) {
-                    const float2 nm = f2s(-g.mid), inv = f2s(g.inv);
-                    float2 u[4];
-                    unpack8<XT>(h[k], u);
+                const float2 nm = f2s(-fetch<VPT>(g.mid, lane, k)), inv = f2s(fetch<VPT>(g.inv, lane, k));
+                float2 u[4];
+                unpack8<XT>(h[k], u);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f2mul(f2add(u[i], nm), inv);
-                    *reinterpret_cast<uint2 *>(cr + 8 * c) = codes8_i8(u, p.one);
-                    if ((c & ((1 << clg) - 1)) == 0)
-                        *reinterpret_cast<float2 *>(cs + 2 * (c >> clg)) = make_float2(g.scale, g.mid);
-                }
+                for (int i = 0; i < 4; ++i) u[i] = f2mul(f2add(u[i], nm), inv);
+                if (has(k)) *reinterpret_cast<uint2 *>(cr + 8 * (k * TPR + t)) = codes8_i8(u, p.one);
             }
         }
 
         // ---------------------------------------------------------------- sums of the row
         uint8_t *qr = p.q + row * p.ldq;
         float *qs = p.qs + row * p.qs_row;
-        float2 a2 = f2s(0.f);
-        float m = 0.f, unused = 0.f;
-        constexpr bool RQ = !LN && OUT == 1;  // codes of h * gamma
-        float amax[VPT];
+        float acc, mean = 0.f, m = 0.f, unused = 0.f;
+        // codes of o (chunk k), scaled by inv
+        auto put = [&](int k, float2 (&o)[4], float inv) {
+            const float2 i2 = f2s(inv);
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int c = k * TPR + t;
-            float2 v[4];
-            unpack8<XT>(h[k], v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a2 = LN ? f2add(a2, v[i]) : f2fma(v[i], v[i], a2);
-            if constexpr (RQ) {
-                if (c < nc && p.gamma) {
-                    float2 g8[4];
-                    par8g(p.gamma, c, p.pdt, 1.f, g8);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = f2mul(v[i], g8[i]);
-                }
-                amax[k] = amax8(v);
-                if (p.qg >= 0) {
-                    amax[k] = lanes_max(amax[k], qlg);
-                    const float2 inv = f2s(q8_inv(amax[k], qmax));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = f2mul(v[i], inv);
-                    if (c < nc) *reinterpret_cast<uint2 *>(qr + 8 * c) = codes8(v, p.qfmt, p.one);
-                } else {
-                    m = fmax_nan(m, amax[k]);
-                }
-            }
-        }
-        float acc = a2.x + a2.y, mean = 0.f;
-        if constexpr (LN) {
-            float2 q2 = f2s(0.f);
-            if (full) {
-                constexpr float kC = (float)(VPT * 8);
-                mean = acc * (1.f / kC);
-            } else {
-                group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
-                mean = acc / n;
-            }
-            const float2 nm = f2s(-mean);
+            for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], i2);
+            if (has(k)) *reinterpret_cast<uint2 *>(qr + 8 * (k * TPR + t)) = codes8(o, p.qfmt, p.one);
+        };
+        float gscale = 0.f;  // the scale of this lane's own group; RQ: its maximum until rstd is known
+        // group scales: codes of the VPT chunks made by `chunk`
+        auto put_groups = [&](auto &&chunk) {
+            float am[VPT];
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                if (k * TPR + t >= nc) continue;
-                float2 v[4];
+                float2 o[4];
+                chunk(k, o);
+                am[k] = lanes_max(amax8(o), qlg);
+            }
+            gscale = pick<VPT>(am, own);
+            const float inv = q8_inv(gscale, qmax);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                float2 o[4];
+                chunk(k, o);
+                put(k, o, fetch<VPT>(inv, lane, k));
+            }
+        };
+        auto scaled = [&](int k, float2 (&o)[4]) {  // h * gamma
+            float2 g8[4];
+            unpack8<XT>(h[k], o);
+            param(gp, k, g8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], g8[i]);
+        };
+        if constexpr (LN) {
+            // One pass: deviations from the thread's first element.  With it
+            // among the n elements, sum d^2 <= (n + 1) M2, so what the
+            // subtraction below cancels is bounded by n + 1 roundings.
+            float2 v[4];
+            unpack8<XT>(h[0], v);
+            const float ref = v[0].x;
+            const float2 nr = f2s(-ref);
+            float2 s2 = f2s(0.f), q2 = f2s(0.f);
+            float cnt = (float)(VPT * 8);
+            if constexpr (!FULL) cnt = 0.f;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                if (!has(k)) continue;
+                if constexpr (!FULL) cnt += 8.f;
                 unpack8<XT>(h[k], v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 d = f2add(v[i], nm);
+                    const float2 d = f2add(v[i], nr);
+                    s2 = f2add(s2, d);
                     q2 = f2fma(d, d, q2);
                 }
             }
-            acc = q2.x + q2.y;
-            if (full) group_meanvar_equal<TPR>(mean, acc, (float)(VPT * 8), scratch, parity, 1 + grp);
-            else group_sum_max<TPR, false>(acc, unused, scratch, parity, 1 + grp);
+            const float s = s2.x + s2.y;
+            const float dm = FULL ? s * (1.f / (VPT * 8)) : cnt > 0.f ? s / cnt : 0.f;
+            mean = ref + dm;
+            acc = fmax_nan(q2.x + q2.y - s * dm, 0.f);
+            group_meanvar<TPR, FULL>(mean, acc, cnt, inv_n, scratch, parity, 1 + grp);
         } else {
-            group_sum_max<TPR, RQ>(acc, m, scratch, parity, 1 + grp);
+            float2 a2 = f2s(0.f);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                float2 v[4];
+                unpack8<XT>(h[k], v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a2 = f2fma(v[i], v[i], a2);
+                if constexpr (OUT == kOutRow) {
+                    float2 g8[4];
+                    param(gp, k, g8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m = amax3(m, f2mul(v[i], g8[i]));
+                }
+            }
+            acc = a2.x + a2.y;
+            if constexpr (OUT == kOutGroup) put_groups(scaled);
+            group_sum_max<TPR, OUT == kOutRow>(acc, m, scratch, parity, 1 + grp);
         }
-        const float rstd = rsqrtf(acc / n + p.eps);
+        const float rstd = rsqrtf(acc * inv_n + p.eps);
         if (t == 0) {
             if (p.rstd) p.rstd[row] = rstd;
             if (LN && p.mean) p.mean[row] = mean;
@@ -342,78 +477,63 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
 
         // ---------------------------------------------------------------- output
         const float2 nm = f2s(-mean), rs = f2s(rstd);
-        // chunk k of y (RQ: of h * gamma); zeros past the row's end
-        auto out8 = [&](int k, float2 (&o)[4]) {
-            const int c = k * TPR + t;
+        auto normed = [&](int k, float2 (&o)[4]) {  // y; zeros past the row's end
+            float2 g8[4];
             unpack8<XT>(h[k], o);
-            if (c < nc) {
-                if constexpr (LN) {
+            param(gp, k, g8);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = f2mul(f2add(o[i], nm), rs);
-                } else if constexpr (!RQ) {
+            for (int i = 0; i < 4; ++i) o[i] = f2mul(f2mul(LN ? f2add(o[i], nm) : o[i], rs), g8[i]);
+            if constexpr (LN) {
+                param(bp, k, g8);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], rs);
-                }
-                if (p.gamma) {
-                    float2 g8[4];
-                    par8g(p.gamma, c, p.pdt, 1.f, g8);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], g8[i]);
-                }
-                if (LN && p.beta) {
-                    float2 b8[4];
-                    par8g(p.beta, c, p.pdt, 0.f, b8);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = f2add(o[i], b8[i]);
-                }
+                for (int i = 0; i < 4; ++i) o[i] = has(k) ? f2add(o[i], g8[i]) : f2s(0.f);
             }
         };
-        if constexpr (OUT == 0) {
+        if constexpr (OUT == kOutY) {
             void *yr = row_ptr(p.y, row, p.ldy, p.ydt);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float2 o[4];
-                out8(k, o);
-                if (k * TPR + t < nc) st8p(yr, 8 * (int64_t)(k * TPR + t), p.ydt, o);
+                normed(k, o);
+                if (has(k)) st8p(yr, 8 * (int64_t)(k * TPR + t), p.ydt, o);
             }
-        } else if (p.qg >= 0) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = k * TPR + t;
-                if constexpr (!RQ) {
-                    float2 o[4];
-                    out8(k, o);
-                    amax[k] = lanes_max(amax8(o), qlg);
-                    const float2 inv = f2s(q8_inv(amax[k], qmax));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], inv);
-                    if (c < nc) *reinterpret_cast<uint2 *>(qr + 8 * c) = codes8(o, p.qfmt, p.one);
-                }
-                if (c < nc && (c & ((1 << qlg) - 1)) == 0)
-                    qs[(c >> qlg) * p.qs_grp] = q8_scale(amax[k], RQ ? rstd : 1.f, qmax);
-            }
+        } else if constexpr (OUT == kOutGroup) {
+            if constexpr (!RQ) put_groups(normed);
+            const int at = own * TPR + (t & ~((1 << qlg) - 1));
+            if ((lane & ((1 << qlg) - 1)) < VPT && (FULL || at < nc))
+                qs[(at >> qlg) * p.qs_grp] = gscale < kQ8Tiny ? 0.f : RQ ? gscale * rstd * inv_qmax : gscale * inv_qmax;
         } else {
             if constexpr (!RQ) {
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
                     float2 o[4];
-                    out8(k, o);
-                    m = fmax_nan(m, amax8(o));
+                    normed(k, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m = amax3(m, o[i]);
                 }
                 group_sum_max<TPR, true>(unused, m, scratch, parity, 1 + grp);
             }
-            const float2 inv = f2s(q8_inv(m, qmax));
+            const float inv = q8_inv(m, qmax);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float2 o[4];
-                out8(k, o);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], inv);
-                if (k * TPR + t < nc) *reinterpret_cast<uint2 *>(qr + 8 * (k * TPR + t)) = codes8(o, p.qfmt, p.one);
+                if constexpr (RQ) scaled(k, o);
+                else normed(k, o);
+                put(k, o, inv);
             }
             if (t == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax);
         }
     }
+}
+
+template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int OUT, bool CK>
+__global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
+    static_assert(NT % TPR == 0 && TPR % 32 == 0 && VPT <= 4, "row groups");
+    static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
+    extern __shared__ __align__(16) float4 q8_par[];
+    __shared__ float4 scratch[NT / 32 * 2];
+    if (p.N == (int64_t)TPR * VPT * 8) q8_fwd_body<LN, XT, TPR, VPT, NT, OUT, CK, true>(p, q8_par, scratch);
+    else q8_fwd_body<LN, XT, TPR, VPT, NT, OUT, CK, false>(p, q8_par, scratch);
 }
 
 }  // namespace gbn
