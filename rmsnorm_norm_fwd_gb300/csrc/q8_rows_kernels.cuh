@@ -14,9 +14,8 @@
 //     and the maximum are one reduction with one barrier.
 //   - The checkpoint's codes need h alone and are written before the
 //     statistics too.
-//   - A row stays in its storage type between the passes (half the registers
-//     of fp32 for 16-bit types): four 256-thread CTAs share an SM (LayerNorm
-//     three), and their phases overlap.
+//   - A thread holds 8 to 32 elements, so that four 256-thread CTAs share an SM
+//     (LayerNorm three) and their phases overlap.
 //   - Every thread keeps gamma (beta) of its own columns as fp32 in its own
 //     slots of shared memory: no conversion, no branch on the parameter type
 //     and no barrier in the loop.
@@ -57,6 +56,10 @@ template <int XT> __device__ __forceinline__ void unpack8(const Raw8<XT> &r, flo
     constexpr int PW = XT == kF32 ? 2 : 4;  // pairs per 16 bytes
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = vpair<T>(r.v[i / PW], i % PW);
+}
+// Bytes (a multiple of 16, 16-byte aligned) brought to L2; nothing waits for them.
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 // Chunk c of a parameter row (read-only, kept in L1), or the constant an
 // absent one stands for.
@@ -102,20 +105,6 @@ __device__ __forceinline__ float amax3(float m, float2 f) {
 __device__ __forceinline__ float amax8(const float2 (&f)[4]) {
     return fmax_nan(amax3(amax3(0.f, f[0]), f[1]), amax3(amax3(0.f, f[2]), f[3]));
 }
-// Maximum over the aligned 2^lg lanes of a group (lg <= 5, uniform).
-__device__ __forceinline__ float lanes_max(float v, int lg) {
-#pragma unroll
-    for (int o = 0; o < 5; ++o)
-        if (o < lg) v = fmax_nan(v, __shfl_xor_sync(0xffffffffu, v, 1 << o));
-    return v;
-}
-__device__ __forceinline__ float lanes_min(float v, int lg) {
-#pragma unroll
-    for (int o = 0; o < 5; ++o)
-        if (o < lg) v = fmin_nan(v, __shfl_xor_sync(0xffffffffu, v, 1 << o));
-    return v;
-}
-
 // Eight int8 codes of u as two words: rint(u) is the low byte of u + 1.5 *
 // 2^23.  The sum is written as u * one + magic with `one` = 1 from the kernel's
 // arguments: a plain addition was seen fused with the product that made u, and
@@ -238,63 +227,93 @@ template <int XT> __device__ __forceinline__ void add8(Raw8<XT> &h, const Raw8<X
     }
 }
 
-// Maximum and minimum of the chunks of a group, one chunk a lane, over its
-// 2^lg lanes; `ok` false: no chunk here.
-template <int XT>
-__device__ __forceinline__ void lanes_range(const Raw8<XT> &r, bool ok, int lg, float &top, float &low) {
-    if constexpr (XT == kF32) {
-        float2 f[4];
-        unpack8<XT>(r, f);
-        top = -INFINITY, low = INFINITY;
-        if (ok) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                top = fmax_nan(top, fmax_nan(f[i].x, f[i].y));
-                low = fmin_nan(low, fmin_nan(f[i].x, f[i].y));
-            }
+// Each lane has a value for its chunk of VPT groups side by side (chunk k of
+// the 2^lg lanes of a group forms one).  max_of_own reduces all VPT at once: in
+// the first two steps partner lanes trade halves, so that lane l goes on with
+// chunk l mod 4 alone (own_chunk), 5 shuffles for 4 groups of 16 lanes instead
+// of 16.  What follows from a maximum (a division) is then done once a lane, and
+// the lanes of a group (at least four) fetch the results from one another.
+template <int VPT> __device__ __forceinline__ int own_chunk(int lane) {
+    return VPT == 1 ? 0 : VPT == 2 ? lane & 1 : lane & 3;
+}
+template <int VPT, typename V, typename Max>
+__device__ __forceinline__ V max_of_own(const V (&a)[VPT], V none, int lane, int lg, Max &&mx) {
+    V r;
+    int done = 0;  // steps taken
+    if constexpr (VPT == 1) {
+        r = a[0];
+    } else {
+        const bool b0 = lane & 1, b1 = lane & 2;
+        auto trade = [&](V even, V odd, bool bit, int o) {
+            return mx(bit ? odd : even, __shfl_xor_sync(0xffffffffu, bit ? even : odd, o));
+        };
+        r = trade(a[0], a[1], b0, 1);
+        done = 1;
+        if constexpr (VPT > 2) {
+            V hi;
+            if constexpr (VPT == 4) hi = trade(a[2], a[3], b0, 1);
+            else hi = trade(a[2], none, b0, 1);
+            r = trade(r, hi, b1, 2);
+            done = 2;
         }
-        top = lanes_max(top, lg);
-        low = lanes_min(low, lg);
+    }
+#pragma unroll
+    for (int o = 0; o < 5; ++o)
+        if (o >= done && o < lg) r = mx(r, __shfl_xor_sync(0xffffffffu, r, 1 << o));
+    return r;
+}
+template <int VPT> __device__ __forceinline__ float fetch(float own, int lane, int k) {
+    return VPT == 1 ? own : __shfl_sync(0xffffffffu, own, (lane & ~(VPT == 2 ? 1 : 3)) | k);
+}
+
+// Maximum and minimum over the groups of a lane's own chunk (max_of_own) of
+// stored values; has(k) false: no chunk k here.
+template <int XT, int VPT, typename Has>
+__device__ __forceinline__ void range_of_own(const Raw8<XT> (&h)[VPT], Has &&has, int lane, int lg, float &top,
+                                             float &low) {
+    if constexpr (XT == kF32) {
+        float hi[VPT], lo[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            float2 f[4];
+            unpack8<XT>(h[k], f);
+            float a = -INFINITY, b = -INFINITY;  // max, -min
+            if (has(k)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a = fmax_nan(a, fmax_nan(f[i].x, f[i].y));
+                    b = fmax_nan(b, fmax_nan(-f[i].x, -f[i].y));
+                }
+            }
+            hi[k] = a;
+            lo[k] = b;
+        }
+        top = max_of_own<VPT>(hi, -INFINITY, lane, lg, fmax_nan);
+        low = -max_of_own<VPT>(lo, -INFINITY, lane, lg, fmax_nan);
     } else {
         // on pairs of the stored type, then (max, -min) as one pair, so that a
         // butterfly step is one shuffle and one maximum
         using T2 = typename std::conditional<XT == kBF16, __nv_bfloat162, __half2>::type;
-        const T2 *p = reinterpret_cast<const T2 *>(&r.v[0]);
-        const T2 hi = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
-        const T2 lo = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
-        T2 m;
-        m.x = __hmax_nan(hi.x, hi.y);
-        m.y = __hneg(__hmin_nan(lo.x, lo.y));
-        uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
         constexpr uint32_t kLowest = XT == kBF16 ? 0xff80ff80u : 0xfc00fc00u;  // (-inf, -inf)
-        if (!ok) w = kLowest;
+        uint32_t w[VPT];
 #pragma unroll
-        for (int o = 0; o < 5; ++o)
-            if (o < lg) {
-                const uint32_t v = __shfl_xor_sync(0xffffffffu, w, 1 << o);
-                const T2 n = __hmax2_nan(*reinterpret_cast<const T2 *>(&w), *reinterpret_cast<const T2 *>(&v));
-                w = *reinterpret_cast<const uint32_t *>(&n);
-            }
-        const T2 n = *reinterpret_cast<const T2 *>(&w);
+        for (int k = 0; k < VPT; ++k) {
+            const T2 *p = reinterpret_cast<const T2 *>(&h[k].v[0]);
+            const T2 hi = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+            const T2 lo = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
+            T2 m;
+            m.x = __hmax_nan(hi.x, hi.y);
+            m.y = __hneg(__hmin_nan(lo.x, lo.y));
+            w[k] = has(k) ? *reinterpret_cast<const uint32_t *>(&m) : kLowest;
+        }
+        const uint32_t r = max_of_own<VPT>(w, kLowest, lane, lg, [](uint32_t a, uint32_t b) {
+            const T2 n = __hmax2_nan(*reinterpret_cast<const T2 *>(&a), *reinterpret_cast<const T2 *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&n);
+        });
+        const T2 n = *reinterpret_cast<const T2 *>(&r);
         top = to_f(n.x);
         low = -to_f(n.y);
     }
-}
-
-// The VPT groups that a lane's chunks belong to cost one division each; lane l
-// takes that of chunk l mod 4 alone, and the lanes of a group (at least four)
-// fetch the results from one another.
-template <int VPT> __device__ __forceinline__ int own_chunk(int lane) {
-    return VPT <= 1 ? 0 : (VPT == 2 ? lane & 1 : (lane & 3) < VPT ? lane & 3 : VPT - 1);
-}
-template <int VPT> __device__ __forceinline__ float pick(const float (&a)[VPT], int k) {
-    float r = a[0];
-#pragma unroll
-    for (int i = 1; i < VPT; ++i) r = k == i ? a[i] : r;
-    return r;
-}
-template <int VPT> __device__ __forceinline__ float fetch(float own, int lane, int k) {
-    return VPT == 1 ? own : __shfl_sync(0xffffffffu, own, (lane & ~3) | k);
 }
 
 constexpr int kOutY = 0, kOutRow = 1, kOutGroup = 2;  // y in ydt; 8-bit rows with a scale per row; per group
@@ -349,6 +368,13 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
                     if (has(k)) st_raw8<XT>(hr, k * TPR + t, h[k]);
             }
         }
+        // The next row on its way to L2 while this one is worked on; with a
+        // residual the loads of a row alone keep DRAM busy (16384 x 8192:
+        // 149 us without, 158 us with the prefetch).
+        if (t == 0 && p.res == nullptr) {
+            const int64_t next = row + (int64_t)gridDim.x * RPC;
+            if (next < p.M) prefetch_l2(static_cast<const unsigned char *>(p.x) + next * p.ldx * xes, nc * 8 * xes);
+        }
         if (first) {  // behind the first row's loads
             first = false;
 #pragma unroll
@@ -366,10 +392,9 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
         }
         if constexpr (CK) {
             uint8_t *cr = p.c + row * p.ldc;
-            float top[VPT], low[VPT];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) lanes_range<XT>(h[k], has(k), clg, top[k], low[k]);
-            const CkGroup g = ck_group(pick<VPT>(top, own), pick<VPT>(low, own));
+            float top, low;
+            range_of_own<XT, VPT>(h, has, lane, clg, top, low);
+            const CkGroup g = ck_group(top, low);
             // the first lanes of a group write its pairs, lane k of it chunk k's
             const int at = own * TPR + (t & ~((1 << clg) - 1));
             if ((lane & ((1 << clg) - 1)) < VPT && (FULL || at < nc))
@@ -396,39 +421,24 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], i2);
             if (has(k)) *reinterpret_cast<uint2 *>(qr + 8 * (k * TPR + t)) = codes8(o, p.qfmt, p.one);
         };
-        float gscale = 0.f;  // the scale of this lane's own group; RQ: its maximum until rstd is known
-        // group scales: codes of the VPT chunks made by `chunk`
-        auto put_groups = [&](auto &&chunk) {
+        float2 o[VPT][4];    // h, then what is stored of it: h * gamma or y
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) unpack8<XT>(h[k], o[k]);
+        float gscale = 0.f;  // the maximum of this lane's own group
+        auto put_groups = [&]() {
             float am[VPT];
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float2 o[4];
-                chunk(k, o);
-                am[k] = lanes_max(amax8(o), qlg);
-            }
-            gscale = pick<VPT>(am, own);
+            for (int k = 0; k < VPT; ++k) am[k] = amax8(o[k]);
+            gscale = max_of_own<VPT>(am, 0.f, lane, qlg, fmax_nan);
             const float inv = q8_inv(gscale, qmax);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float2 o[4];
-                chunk(k, o);
-                put(k, o, fetch<VPT>(inv, lane, k));
-            }
-        };
-        auto scaled = [&](int k, float2 (&o)[4]) {  // h * gamma
-            float2 g8[4];
-            unpack8<XT>(h[k], o);
-            param(gp, k, g8);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = f2mul(o[i], g8[i]);
+            for (int k = 0; k < VPT; ++k) put(k, o[k], fetch<VPT>(inv, lane, k));
         };
         if constexpr (LN) {
             // One pass: deviations from the thread's first element.  With it
             // among the n elements, sum d^2 <= (n + 1) M2, so what the
             // subtraction below cancels is bounded by n + 1 roundings.
-            float2 v[4];
-            unpack8<XT>(h[0], v);
-            const float ref = v[0].x;
+            const float ref = o[0][0].x;
             const float2 nr = f2s(-ref);
             float2 s2 = f2s(0.f), q2 = f2s(0.f);
             float cnt = (float)(VPT * 8);
@@ -437,10 +447,9 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             for (int k = 0; k < VPT; ++k) {
                 if (!has(k)) continue;
                 if constexpr (!FULL) cnt += 8.f;
-                unpack8<XT>(h[k], v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 d = f2add(v[i], nr);
+                    const float2 d = f2add(o[k][i], nr);
                     s2 = f2add(s2, d);
                     q2 = f2fma(d, d, q2);
                 }
@@ -454,19 +463,18 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             float2 a2 = f2s(0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                float2 v[4];
-                unpack8<XT>(h[k], v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a2 = f2fma(v[i], v[i], a2);
-                if constexpr (OUT == kOutRow) {
+                for (int i = 0; i < 4; ++i) a2 = f2fma(o[k][i], o[k][i], a2);
+                if constexpr (RQ) {
                     float2 g8[4];
                     param(gp, k, g8);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m = amax3(m, f2mul(v[i], g8[i]));
+                    for (int i = 0; i < 4; ++i) o[k][i] = f2mul(o[k][i], g8[i]);
+                    if constexpr (OUT == kOutRow) m = fmax_nan(m, amax8(o[k]));
                 }
             }
             acc = a2.x + a2.y;
-            if constexpr (OUT == kOutGroup) put_groups(scaled);
+            if constexpr (OUT == kOutGroup) put_groups();
             group_sum_max<TPR, OUT == kOutRow>(acc, m, scratch, parity, 1 + grp);
         }
         const float rstd = rsqrtf(acc * inv_n + p.eps);
@@ -477,50 +485,35 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
 
         // ---------------------------------------------------------------- output
         const float2 nm = f2s(-mean), rs = f2s(rstd);
-        auto normed = [&](int k, float2 (&o)[4]) {  // y; zeros past the row's end
-            float2 g8[4];
-            unpack8<XT>(h[k], o);
-            param(gp, k, g8);
+        if constexpr (!RQ) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = f2mul(f2mul(LN ? f2add(o[i], nm) : o[i], rs), g8[i]);
-            if constexpr (LN) {
-                param(bp, k, g8);
+            for (int k = 0; k < VPT; ++k) {  // y; zeros past the row's end
+                float2 g8[4];
+                param(gp, k, g8);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = has(k) ? f2add(o[i], g8[i]) : f2s(0.f);
+                for (int i = 0; i < 4; ++i) o[k][i] = f2mul(f2mul(LN ? f2add(o[k][i], nm) : o[k][i], rs), g8[i]);
+                if constexpr (LN) {
+                    param(bp, k, g8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[k][i] = has(k) ? f2add(o[k][i], g8[i]) : f2s(0.f);
+                }
+                if constexpr (OUT == kOutY) {
+                    if (has(k)) st8p(row_ptr(p.y, row, p.ldy, p.ydt), 8 * (int64_t)(k * TPR + t), p.ydt, o[k]);
+                } else if constexpr (OUT == kOutRow) {
+                    m = fmax_nan(m, amax8(o[k]));
+                }
             }
-        };
-        if constexpr (OUT == kOutY) {
-            void *yr = row_ptr(p.y, row, p.ldy, p.ydt);
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float2 o[4];
-                normed(k, o);
-                if (has(k)) st8p(yr, 8 * (int64_t)(k * TPR + t), p.ydt, o);
-            }
-        } else if constexpr (OUT == kOutGroup) {
-            if constexpr (!RQ) put_groups(normed);
+        }
+        if constexpr (OUT == kOutGroup) {
+            if constexpr (!RQ) put_groups();
             const int at = own * TPR + (t & ~((1 << qlg) - 1));
             if ((lane & ((1 << qlg) - 1)) < VPT && (FULL || at < nc))
                 qs[(at >> qlg) * p.qs_grp] = gscale < kQ8Tiny ? 0.f : RQ ? gscale * rstd * inv_qmax : gscale * inv_qmax;
-        } else {
-            if constexpr (!RQ) {
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    float2 o[4];
-                    normed(k, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) m = amax3(m, o[i]);
-                }
-                group_sum_max<TPR, true>(unused, m, scratch, parity, 1 + grp);
-            }
+        } else if constexpr (OUT == kOutRow) {
+            if constexpr (!RQ) group_sum_max<TPR, true>(unused, m, scratch, parity, 1 + grp);
             const float inv = q8_inv(m, qmax);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float2 o[4];
-                if constexpr (RQ) scaled(k, o);
-                else normed(k, o);
-                put(k, o, inv);
-            }
+            for (int k = 0; k < VPT; ++k) put(k, o[k], inv);
             if (t == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax);
         }
     }
