@@ -1,0 +1,45 @@
+// inst_q8_bwd_body.cuh -- row-resident backward kernels from the 8-bit
+// checkpoint for one norm (the including unit defines GBN_Q8_LN and
+// GBN_Q8_NAME): dy, dres and dx of one type (fp32, fp16, bf16), or of any.
+#include "q8_bwd_kernels.cuh"
+
+namespace gbn {
+
+// (TPR, VPT, NT, MINB) by row capacity TPR * VPT * 8.  LayerNorm holds two
+// column sums per element: fewer elements a thread.
+#if GBN_Q8_LN
+#define GBN_Q8B_GEOMS(X, XT) \
+    X(32, 1, 256, 3, XT)     \
+    X(32, 2, 256, 2, XT)     \
+    X(64, 2, 256, 2, XT)     \
+    X(128, 2, 256, 2, XT)    \
+    X(256, 2, 256, 2, XT)    \
+    X(320, 2, 320, 2, XT)    \
+    X(512, 2, 512, 1, XT)    \
+    X(512, 4, 512, 1, XT)
+#else
+#define GBN_Q8B_GEOMS(X, XT) \
+    X(32, 1, 256, 4, XT)     \
+    X(32, 2, 256, 3, XT)     \
+    X(32, 4, 256, 2, XT)     \
+    X(64, 4, 256, 2, XT)     \
+    X(128, 4, 256, 2, XT)    \
+    X(256, 3, 256, 2, XT)    \
+    X(256, 4, 256, 2, XT)    \
+    X(512, 4, 512, 1, XT)
+#endif
+#define GBN_STR2(x) #x
+#define GBN_STR(x) GBN_STR2(x)
+#define GBN_Q8B_ENTRY(TPR, VPT, NT, MINB, XT)                                                                       \
+    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT), (const void *)&q8_bwd_rows<GBN_Q8_LN, XT, TPR, VPT, NT, MINB>, TPR, VPT, NT, \
+     NT * VPT * 32},
+
+static const Q8Variant kB0[] = {GBN_Q8B_GEOMS(GBN_Q8B_ENTRY, kF32)};
+static const Q8Variant kB1[] = {GBN_Q8B_GEOMS(GBN_Q8B_ENTRY, kF16)};
+static const Q8Variant kB2[] = {GBN_Q8B_GEOMS(GBN_Q8B_ENTRY, kBF16)};
+static const Q8Variant kB3[] = {GBN_Q8B_GEOMS(GBN_Q8B_ENTRY, -1)};
+constexpr int kGeoms = (int)(sizeof(kB0) / sizeof(kB0[0]));
+static_assert(kGeoms <= kQ8MaxVariants, "occupancy slots");
+const Q8Table GBN_Q8_NAME[4] = {{kB0, kGeoms}, {kB1, kGeoms}, {kB2, kGeoms}, {kB3, kGeoms}};
+
+}  // namespace gbn

@@ -95,7 +95,7 @@ int launch(const void *kernel, int64_t grid, int cta, size_t dyn, void *params, 
 }
 
 // Occupancy of a kernel (CTAs per SM), measured once per device and slot.
-constexpr int kSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants;
+constexpr int kBwdSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants, kSlots = kBwdSlots + 2 * 4 * kQ8MaxVariants;
 std::atomic<int> g_occ[kHostMaxDev][kSlots];
 int occupancy(int dev, int slot, const void *k, int cta, size_t dyn, int *occ) {
     std::atomic<int> &c = g_occ[dev][slot];
@@ -197,9 +197,10 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
     return launch(kQ8FwdElem[a.is_ln], grid_of(M, 8, d), kElemCTA, 0, &p, stream);
 }
 
-// Partial rows of the backward: at most one per SM.
+// Partial rows of the backward: an upper bound over its kernels, so that the
+// workspace depends on the shape alone.
 size_t bwd_ws_bytes(int is_ln, int64_t M, int64_t N, const HostDevice &d) {
-    const int64_t P = grid_of(M, 1, d);
+    const int64_t P = grid_of(M, kQ8BwdPerSm, d);
     const size_t need = (size_t)P * (size_t)N * 4u * (is_ln ? 2u : 1u);
     return (need + 255u) & ~(size_t)255u;
 }
@@ -283,9 +284,28 @@ int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t
         Q8BwdParams p{dy, reinterpret_cast<const uint8_t *>(codes), c_scale, dres, gamma, mean, rstd, dx,
                       static_cast<float *>(workspace), lddy, ldc, ldcs, lddres, lddx, M, N, x_dtype, param_dtype,
                       y_dtype, cg};
-        P = grid_of(M, 1, d);
-        t_last[1] = "elem";
-        const int st = launch(kQ8BwdElem[is_layernorm], P, kElemCTA, 0, &p, stream);
+        const int ys = elem_size(y_dtype);
+        const bool vec = N % 8 == 0 && vec_rows(dy, lddy, ys) && vec_rows(dres, lddres, xs) && vec_rows(dx, lddx, xs) &&
+                         aligned(gamma, 16) && aligned(codes, 8) && ldc % 8 == 0;
+        const Q8Table &t = (is_layernorm ? kQ8Bwd_ln : kQ8Bwd_rms)[x_dtype == y_dtype ? x_dtype : 3];
+        int i = 0;
+        while (i < t.count && (int64_t)t.v[i].tpr * t.v[i].vpt * 8 < N) ++i;
+        int st;
+        if (vec && i < t.count) {
+            const Q8Variant &v = t.v[i];
+            int occ;
+            st = occupancy(d.dev, kBwdSlots + (is_layernorm * 4 + (x_dtype == y_dtype ? x_dtype : 3)) * kQ8MaxVariants + i,
+                           v.kernel, v.cta, (size_t)v.smem, &occ);
+            if (st != GBNORM_OK) return st;
+            const int64_t rpc = v.cta / v.tpr;
+            P = grid_of((M + rpc - 1) / rpc, occ < kQ8BwdPerSm ? occ : kQ8BwdPerSm, d);
+            t_last[1] = v.name;
+            st = launch(v.kernel, P, v.cta, (size_t)v.smem, &p, stream);
+        } else {
+            P = grid_of(M, 1, d);
+            t_last[1] = "elem";
+            st = launch(kQ8BwdElem[is_layernorm], P, kElemCTA, 0, &p, stream);
+        }
         if (st != GBNORM_OK) return st;
     }
     return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, M > 0, stream);
@@ -318,6 +338,23 @@ int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int 
     if (M == 0) return GBNORM_OK;
     Q8ReadParams p{static_cast<const uint8_t *>(q), scale, mid, mean, rstd, gamma, beta, y, ldq, s_row, s_group, ldy,
                    M, N, param_dtype, y_dtype, q_format, qg};
+    if (N % 8 == 0 && aligned(q, 8) && ldq % 8 == 0 && vec_rows(y, ldy, elem_size(y_dtype)) && aligned(gamma, 16) &&
+        aligned(beta, 16)) {
+        // column blocks of equal width, as many rows side by side as fit
+        const int64_t nc = N / 8, gx = (nc + kQ8ReadCTA - 1) / kQ8ReadCTA;
+        int tx = (int)((nc + gx - 1) / gx);
+        const int64_t ry = kQ8ReadCTA / tx;
+        const int64_t units = (M + ry * kQ8ReadRows - 1) / (ry * kQ8ReadRows);
+        int64_t gy = grid_of(units * gx, 8, d) / gx;
+        gy = gy < 1 ? 1 : gy > 65535 ? 65535 : gy;
+        const bool norm = mean || rstd || gamma || beta;
+        void *args[2] = {&p, &tx};
+        t_last[2] = "vec";
+        if (cudaLaunchKernel(kQ8Read[q_format][norm][y_dtype], dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)(tx * ry)),
+                             args, 0, stream) != cudaSuccess)
+            return GBNORM_ERR_CUDA;
+        return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
+    }
     t_last[2] = "elem";
     return launch(kQ8ReadElem, grid_of(M, 8, d), kElemCTA, 0, &p, stream);
 }

@@ -1,0 +1,248 @@
+// q8_bwd_kernels.cuh -- backward of the norms from the 8-bit checkpoint, rows
+// in registers: a row group of TPR threads holds one row of codes and dy, each
+// thread VPT chunks of 8 consecutive elements, chunk k * TPR + t, always the
+// same columns, so that its dgamma (dbeta) sums stay in registers.
+//
+// With the group's (scale, mid) and the row's statistics xhat is one
+// multiply-add of the code: xhat = code * (scale * rstd) + (mid - mean) * rstd.
+// Two passes over the registers: sum g xhat (and sum g), one barrier, then dx
+// and the column sums; codes and dy are widened again in the second pass.
+//
+// What bounds it: DRAM, 5 bytes an element (bf16 dy and dx, 1.06 bytes of
+// checkpoint), 7 with a residual's gradient.  The next row is prefetched to L2
+// while one is worked on.
+#pragma once
+
+#include "q8_rows_kernels.cuh"
+
+namespace gbn {
+
+// Eight int8 codes as fp32 (exact): the code with its sign bit flipped as the
+// low byte of 2^23 is 2^23 + 128 + code.
+__device__ __forceinline__ void i8_pairs(uint2 w, float2 (&f)[4]) {
+    const uint32_t a = w.x ^ 0x80808080u, b = w.y ^ 0x80808080u;
+    const float2 off = f2s(-8388736.f);
+    auto at = [](uint32_t v, int i) { return __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7650 | i)); };
+    f[0] = f2add(make_float2(at(a, 0), at(a, 1)), off);
+    f[1] = f2add(make_float2(at(a, 2), at(a, 3)), off);
+    f[2] = f2add(make_float2(at(b, 0), at(b, 1)), off);
+    f[3] = f2add(make_float2(at(b, 2), at(b, 3)), off);
+}
+__device__ __forceinline__ uint2 ld_codes8(const uint8_t *row, int c) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(row + 8 * c));
+    return v;
+}
+
+// NS sums over a row group through scratch [2][WPR] float2; the same bits on
+// every thread.
+template <int TPR, int NS>
+__device__ __forceinline__ void group_sums(float (&v)[2], float2 *scratch, int &parity, int bar_id) {
+    auto step = [&](int o) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    };
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) step(o);
+    if constexpr (TPR > 32) {
+        constexpr int WPR = TPR / 32, L = pow2_at_least(WPR);
+        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+        float2 *buf = scratch + parity * WPR;
+        if (lane == 0) buf[wig] = make_float2(v[0], NS > 1 ? v[1] : 0.f);
+        named_sync(bar_id, TPR);
+        const int w = lane & (L - 1);
+        const float2 b = w < WPR ? buf[w] : make_float2(0.f, 0.f);
+        v[0] = b.x;
+        if constexpr (NS > 1) v[1] = b.y;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) step(o);
+        parity ^= 1;
+    }
+}
+
+// Eight elements as read: a type fixed at compile time stays as stored, an
+// unknown one (XT -1) is widened at once.
+template <int XT> struct Row8 {
+    Raw8<XT> r;
+    __device__ __forceinline__ void load(const void *row, int c, int) { r = ld_raw8<XT>(row, c); }
+    __device__ __forceinline__ void zero() { r = Raw8<XT>{}; }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const { unpack8<XT>(r, f); }
+};
+template <> struct Row8<-1> {
+    float2 v[4];
+    __device__ __forceinline__ void load(const void *row, int c, int dt) {
+        if (dt == kF32) unpack8<kF32>(ld_raw8<kF32>(row, c), v);
+        else if (dt == kBF16) unpack8<kBF16>(ld_raw8<kBF16>(row, c), v);
+        else unpack8<kF16>(ld_raw8<kF16>(row, c), v);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f2s(0.f);
+    }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = v[i];
+    }
+};
+
+// The 16-byte-aligned part of [p, p + bytes) brought to L2.
+__device__ __forceinline__ void prefetch_l2_inner(const void *p, int bytes) {
+    const uintptr_t a = (reinterpret_cast<uintptr_t>(p) + 15) & ~(uintptr_t)15;
+    const uintptr_t e = (reinterpret_cast<uintptr_t>(p) + bytes) & ~(uintptr_t)15;
+    if (e > a) prefetch_l2(reinterpret_cast<const void *>(a), (int)(e - a));
+}
+
+// XT: storage type of dy, dres and dx, or -1 for any combination.
+template <bool LN, int XT, int TPR, int VPT, int NT, int MINB>
+__global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
+    static_assert(NT % TPR == 0 && TPR % 32 == 0, "row groups");
+    static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
+    pdl_launch_dependents();  // the column reduce waits for this grid's completion
+    constexpr int RPC = NT / TPR, WPR = TPR / 32;
+    extern __shared__ __align__(16) float4 q8_par[];  // own gamma, then the row groups' column sums
+    __shared__ float2 scratch_all[RPC * 2 * WPR];
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    float2 *scratch = scratch_all + grp * 2 * WPR;
+    const int nc = (int)(p.N / 8), clg = p.cg - 3;
+    const int xdt = XT >= 0 ? XT : p.xdt, ydt = XT >= 0 ? XT : p.ydt;
+    const float inv_n = 1.f / (float)p.N;
+    auto has = [&](int k) { return k * TPR + t < nc; };
+    float4 *gp = q8_par + threadIdx.x;
+    float2 accg[VPT][4], accb[LN ? VPT : 1][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            accg[k][i] = f2s(0.f);
+            if constexpr (LN) accb[k][i] = f2s(0.f);
+        }
+    bool first = true;
+    int parity = 0;
+    for (int64_t row = (int64_t)blockIdx.x * RPC + grp; row < p.M; row += (int64_t)gridDim.x * RPC) {
+        const void *dyr = row_ptr(p.dy, row, p.lddy, ydt);
+        const uint8_t *cr = p.c + row * p.ldc;
+        const float *cs = p.cs + row * p.ldcs;
+        Row8<XT> dy[VPT];
+        uint2 code[VPT];
+        float2 ab[VPT];  // (scale, mid), then xhat = code * a + b
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            dy[k].zero();
+            code[k] = make_uint2(0, 0);
+            ab[k] = make_float2(0.f, 0.f);
+            if (has(k)) {
+                dy[k].load(dyr, k * TPR + t, ydt);
+                code[k] = ld_codes8(cr, k * TPR + t);
+                ab[k] = __ldg(reinterpret_cast<const float2 *>(cs) + ((k * TPR + t) >> clg));
+            }
+        }
+        const float rstd = __ldg(p.rstd + row);
+        const float mean = LN ? __ldg(p.mean + row) : 0.f;
+        if (t == 0) {
+            const int64_t next = row + (int64_t)gridDim.x * RPC;
+            if (next < p.M) {
+                prefetch_l2(row_ptr(p.dy, next, p.lddy, ydt), nc * 8 * esize(ydt));
+                prefetch_l2_inner(p.c + next * p.ldc, nc * 8);
+                prefetch_l2_inner(p.cs + next * p.ldcs, (((nc - 1) >> clg) + 1) * 8);
+                if (p.dres) prefetch_l2(row_ptr(p.dres, next, p.lddres, xdt), nc * 8 * esize(xdt));
+            }
+        }
+        if (first) {  // behind the first row's loads
+            first = false;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                float2 f[4];
+                par8g(has(k) ? p.gamma : nullptr, k * TPR + t, p.pdt, 1.f, f);
+                gp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+                gp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+            }
+        }
+        // g and xhat of chunk k
+        auto values = [&](int k, float2 (&d)[4], float2 (&g)[4], float2 (&xh)[4]) {
+            const float4 a = gp[2 * k * NT], b = gp[(2 * k + 1) * NT];
+            dy[k].get(d);
+            i8_pairs(code[k], xh);
+            g[0] = f2mul(d[0], make_float2(a.x, a.y)), g[1] = f2mul(d[1], make_float2(a.z, a.w));
+            g[2] = f2mul(d[2], make_float2(b.x, b.y)), g[3] = f2mul(d[3], make_float2(b.z, b.w));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xh[i] = f2fma(xh[i], f2s(ab[k].x), f2s(ab[k].y));
+        };
+        float2 s2 = f2s(0.f), s1 = f2s(0.f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            ab[k] = make_float2(ab[k].x * rstd, (ab[k].y - mean) * rstd);
+            float2 d[4], g[4], xh[4];
+            values(k, d, g, xh);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s2 = f2fma(g[i], xh[i], s2);
+                if constexpr (LN) s1 = f2add(s1, g[i]);
+            }
+        }
+        float sum[2] = {s2.x + s2.y, s1.x + s1.y};
+        group_sums<TPR, LN ? 2 : 1>(sum, scratch, parity, 1 + grp);
+        // dx = rstd (g - c1 - xhat c2) + dres
+        const float2 r2 = f2s(rstd), nrc2 = f2s(-rstd * (sum[0] * inv_n)), nrc1 = f2s(LN ? -rstd * (sum[1] * inv_n) : 0.f);
+        void *dxr = row_ptr(p.dx, row, p.lddx, xdt);
+        const void *drr = p.dres ? row_ptr(p.dres, row, p.lddres, xdt) : nullptr;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (!has(k)) continue;
+            Row8<XT> dr;
+            if (drr) dr.load(drr, k * TPR + t, xdt);
+            float2 d[4], g[4], xh[4], o[4];
+            values(k, d, g, xh);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = f2fma(nrc2, xh[i], LN ? f2fma(r2, g[i], nrc1) : f2mul(r2, g[i]));
+                accg[k][i] = f2fma(d[i], xh[i], accg[k][i]);
+                if constexpr (LN) accb[k][i] = f2add(accb[k][i], d[i]);
+            }
+            if (drr) {
+                float2 r[4];
+                dr.get(r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = f2add(o[i], r[i]);
+            }
+            st8p(dxr, 8 * (int64_t)(k * TPR + t), xdt, o);
+        }
+    }
+
+    // This CTA's partial row: the row groups' sums of the same columns are
+    // added in group order through shared memory.
+    auto store = [&](float2 (&acc)[VPT][4], float *ws) {
+        if constexpr (RPC > 1) {
+            __syncthreads();  // gp, or the other sum, is no longer needed
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                gp[2 * k * NT] = make_float4(acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y);
+                gp[(2 * k + 1) * NT] = make_float4(acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y);
+            }
+            __syncthreads();
+            for (int s = threadIdx.x; s < 2 * VPT * TPR; s += NT) {
+                const int kh = s / TPR, tt = s % TPR;  // half chunk kh of thread tt
+                const int64_t col = 8 * (int64_t)((kh >> 1) * TPR + tt) + 4 * (kh & 1);
+                if (col >= p.N) continue;
+                float4 a = q8_par[kh * NT + tt];
+#pragma unroll
+                for (int g = 1; g < RPC; ++g) {
+                    const float4 b = q8_par[kh * NT + g * TPR + tt];
+                    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+                }
+                *reinterpret_cast<float4 *>(ws + col) = a;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                if (!has(k)) continue;
+                float4 *o = reinterpret_cast<float4 *>(ws + 8 * (int64_t)(k * TPR + t));
+                o[0] = make_float4(acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y);
+                o[1] = make_float4(acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y);
+            }
+        }
+    };
+    store(accg, p.ws + (int64_t)blockIdx.x * p.N);
+    if constexpr (LN) store(accb, p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.N);
+}
+
+}  // namespace gbn

@@ -86,6 +86,15 @@ constexpr int kQ8FwdKinds = 5;
 extern const Q8Table kQ8Fwd_rms_f32[kQ8FwdKinds], kQ8Fwd_rms_f16[kQ8FwdKinds], kQ8Fwd_rms_bf16[kQ8FwdKinds];
 extern const Q8Table kQ8Fwd_ln_f32[kQ8FwdKinds], kQ8Fwd_ln_f16[kQ8FwdKinds], kQ8Fwd_ln_bf16[kQ8FwdKinds];
 
+// Backward: dy, dres and dx all fp32, fp16, bf16; any combination.
+extern const Q8Table kQ8Bwd_rms[4], kQ8Bwd_ln[4];
+// Partial rows of the backward are at most this many CTAs per SM.
+constexpr int kQ8BwdPerSm = 4;
+// Reading back: [format][with the norm on top][type of y]; a second kernel
+// argument (int) is the chunks of a row side by side in a CTA.
+extern const void *const kQ8Read[2][2][3];
+extern const int kQ8ReadCTA, kQ8ReadRows;
+
 // Element-wise kernels, [is_ln].
 extern const void *const kQ8FwdElem[2];
 extern const void *const kQ8BwdElem[2];
