@@ -5,34 +5,40 @@
 
 namespace gbn {
 
-// (TPR, VPT, NT, MINB) by row capacity TPR * VPT * 8.  LayerNorm holds two
+// (TPR, VPT, NT, MINB, CL) by row capacity TPR * VPT * CL * 8.  LayerNorm holds two
 // column sums per element: fewer elements a thread.
 #if GBN_Q8_LN
 #define GBN_Q8B_GEOMS(X, XT) \
-    X(32, 1, 256, 3, XT)     \
-    X(32, 2, 256, 2, XT)     \
-    X(64, 2, 256, 2, XT)     \
-    X(128, 2, 256, 2, XT)    \
-    X(256, 2, 256, 2, XT)    \
-    X(320, 2, 320, 2, XT)    \
-    X(512, 2, 512, 1, XT)    \
-    X(512, 4, 512, 1, XT)
+    X(32, 1, 256, 3, 1, XT)     \
+    X(32, 2, 256, 2, 1, XT)     \
+    X(64, 2, 256, 2, 1, XT)     \
+    X(128, 2, 256, 2, 1, XT)    \
+    X(256, 2, 256, 2, 1, XT)    \
+    X(320, 2, 320, 2, 1, XT)    \
+    X(512, 2, 512, 1, 1, XT)    \
+    X(512, 2, 512, 1, 2, XT)    \
+    X(512, 2, 512, 1, 4, XT)    \
+    X(512, 2, 512, 1, 8, XT)    \
+    X(512, 4, 512, 1, 8, XT)
 #else
 #define GBN_Q8B_GEOMS(X, XT) \
-    X(32, 1, 256, 4, XT)     \
-    X(32, 2, 256, 3, XT)     \
-    X(32, 4, 256, 2, XT)     \
-    X(64, 4, 256, 2, XT)     \
-    X(128, 4, 256, 2, XT)    \
-    X(256, 3, 256, 2, XT)    \
-    X(256, 4, 256, 2, XT)    \
-    X(512, 4, 512, 1, XT)
+    X(32, 1, 256, 4, 1, XT)     \
+    X(32, 2, 256, 3, 1, XT)     \
+    X(32, 4, 256, 2, 1, XT)     \
+    X(64, 4, 256, 2, 1, XT)     \
+    X(128, 4, 256, 2, 1, XT)    \
+    X(256, 3, 256, 2, 1, XT)    \
+    X(256, 4, 256, 2, 1, XT)    \
+    X(512, 4, 512, 1, 1, XT)    \
+    X(512, 4, 512, 1, 2, XT)    \
+    X(512, 4, 512, 1, 4, XT)    \
+    X(512, 4, 512, 1, 8, XT)
 #endif
 #define GBN_STR2(x) #x
 #define GBN_STR(x) GBN_STR2(x)
-#define GBN_Q8B_ENTRY(TPR, VPT, NT, MINB, XT)                                                                       \
-    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT), (const void *)&q8_bwd_rows<GBN_Q8_LN, XT, TPR, VPT, NT, MINB>, TPR, VPT, NT, \
-     NT * VPT * 32},
+#define GBN_Q8B_ENTRY(TPR, VPT, NT, MINB, CL, XT)                                                                       \
+    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT) "c" GBN_STR(CL), (const void *)&q8_bwd_rows<GBN_Q8_LN, XT, TPR, VPT, NT, MINB, CL>, TPR, VPT, \
+     NT, CL, NT * VPT * 32},
 
 static const Q8Variant kB0[] = {GBN_Q8B_GEOMS(GBN_Q8B_ENTRY, kF32)};
 static const Q8Variant kB1[] = {GBN_Q8B_GEOMS(GBN_Q8B_ENTRY, kF16)};

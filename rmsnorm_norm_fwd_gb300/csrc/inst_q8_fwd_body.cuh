@@ -5,43 +5,49 @@
 
 namespace gbn {
 
-// (TPR, VPT, NT, MINB) by row capacity TPR * VPT * 8; MINB CTAs per SM of the
-// launch bound (as many as registers and the parameters in shared memory
+// (TPR, VPT, NT, MINB, CL) by row capacity TPR * VPT * CL * 8; MINB CTAs per SM
+// of the launch bound (as many as registers and the parameters in shared memory
 // allow).
 #if GBN_Q8_LN
 #define GBN_Q8F_GEOMS(X) \
-    X(32, 1, 256, 4)     \
-    X(32, 2, 256, 4)     \
-    X(32, 4, 256, 3)     \
-    X(64, 4, 256, 3)     \
-    X(128, 4, 256, 3)    \
-    X(256, 3, 256, 3)    \
-    X(256, 4, 256, 3)    \
-    X(768, 2, 768, 1)    \
-    X(1024, 2, 1024, 1)
+    X(32, 1, 256, 4, 1)     \
+    X(32, 2, 256, 4, 1)     \
+    X(32, 4, 256, 3, 1)     \
+    X(64, 4, 256, 3, 1)     \
+    X(128, 4, 256, 3, 1)    \
+    X(256, 3, 256, 3, 1)    \
+    X(256, 4, 256, 3, 1)    \
+    X(768, 2, 768, 1, 1)    \
+    X(1024, 2, 1024, 1, 1) \
+    X(1024, 2, 1024, 1, 2) \
+    X(1024, 2, 1024, 1, 4) \
+    X(1024, 2, 1024, 1, 8)
 #else
 #define GBN_Q8F_GEOMS(X) \
-    X(32, 1, 256, 4)     \
-    X(32, 2, 256, 4)     \
-    X(32, 4, 256, 4)     \
-    X(64, 4, 256, 4)     \
-    X(128, 4, 256, 4)    \
-    X(256, 3, 256, 4)    \
-    X(256, 4, 256, 4)    \
-    X(512, 3, 512, 2)    \
-    X(512, 4, 512, 2)
+    X(32, 1, 256, 4, 1)     \
+    X(32, 2, 256, 4, 1)     \
+    X(32, 4, 256, 4, 1)     \
+    X(64, 4, 256, 4, 1)     \
+    X(128, 4, 256, 4, 1)    \
+    X(256, 3, 256, 4, 1)    \
+    X(256, 4, 256, 4, 1)    \
+    X(512, 3, 512, 2, 1)    \
+    X(512, 4, 512, 2, 1) \
+    X(512, 4, 512, 2, 2) \
+    X(512, 4, 512, 2, 4) \
+    X(512, 4, 512, 2, 8)
 #endif
 
 #define GBN_STR2(x) #x
 #define GBN_STR(x) GBN_STR2(x)
-#define GBN_Q8F_ENTRY(TPR, VPT, NT, MINB, OUT, CK)                                                                \
-    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT), (const void *)&q8_fwd_rows<GBN_Q8_LN, GBN_Q8_XT, TPR, VPT, NT, MINB, OUT, CK>, \
-     TPR, VPT, NT, q8_fwd_smem(GBN_Q8_LN, VPT, NT)},
-#define GBN_Q8F_Y(T, V, N, B) GBN_Q8F_ENTRY(T, V, N, B, kOutY, true)
-#define GBN_Q8F_R(T, V, N, B) GBN_Q8F_ENTRY(T, V, N, B, kOutRow, false)
-#define GBN_Q8F_G(T, V, N, B) GBN_Q8F_ENTRY(T, V, N, B, kOutGroup, false)
-#define GBN_Q8F_RC(T, V, N, B) GBN_Q8F_ENTRY(T, V, N, B, kOutRow, true)
-#define GBN_Q8F_GC(T, V, N, B) GBN_Q8F_ENTRY(T, V, N, B, kOutGroup, true)
+#define GBN_Q8F_ENTRY(TPR, VPT, NT, MINB, CL, OUT, CK)                                                                \
+    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT) "c" GBN_STR(CL), (const void *)&q8_fwd_rows<GBN_Q8_LN, GBN_Q8_XT, TPR, VPT, NT, MINB, CL, OUT, CK>, \
+     TPR, VPT, NT, CL, q8_fwd_smem(GBN_Q8_LN, VPT, NT)},
+#define GBN_Q8F_Y(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutY, true)
+#define GBN_Q8F_R(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutRow, false)
+#define GBN_Q8F_G(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutGroup, false)
+#define GBN_Q8F_RC(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutRow, true)
+#define GBN_Q8F_GC(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutGroup, true)
 
 static const Q8Variant kY[] = {GBN_Q8F_GEOMS(GBN_Q8F_Y)};
 static const Q8Variant kR[] = {GBN_Q8F_GEOMS(GBN_Q8F_R)};

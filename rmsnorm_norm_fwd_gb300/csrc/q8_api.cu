@@ -94,29 +94,82 @@ int launch(const void *kernel, int64_t grid, int cta, size_t dyn, void *params, 
     return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
 }
 
-// Occupancy of a kernel (CTAs per SM), measured once per device and slot.
-constexpr int kBwdSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants, kSlots = kBwdSlots + 2 * 4 * kQ8MaxVariants;
-std::atomic<int> g_occ[kHostMaxDev][kSlots];
-int occupancy(int dev, int slot, const void *k, int cta, size_t dyn, int *occ) {
-    std::atomic<int> &c = g_occ[dev][slot];
-    int o = c.load(std::memory_order_relaxed);
-    if (o == 0) {
-        if (dyn > 0 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn) != cudaSuccess)
-            return GBNORM_ERR_CUDA;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k, cta, dyn) != cudaSuccess) return GBNORM_ERR_CUDA;
-        if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
-        c.store(o, std::memory_order_relaxed);
-    }
-    *occ = o;
-    return GBNORM_OK;
-}
-
 // Persistent grid of `units` pieces of work at `per_sm` CTAs an SM.
 int64_t grid_of(int64_t units, int64_t per_sm, const HostDevice &d) {
     int64_t cap = per_sm * d.sms;
     const int64_t limit = host_grid_limit();
     if (limit > 0 && limit < cap) cap = limit;
     return units < cap ? units : cap;
+}
+
+// Kernels with rows in registers: how many row groups (CTAs, or clusters) run
+// at once on the device, measured once per device and slot.
+constexpr int kBwdSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants, kSlots = kBwdSlots + 2 * 4 * kQ8MaxVariants;
+std::atomic<int> g_resident[kHostMaxDev][kSlots];
+
+int cluster_launch(const Q8Variant &v, int64_t units, void *params, cudaStream_t s, cudaLaunchConfig_t *cfg,
+                   cudaLaunchAttribute *attr) {
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)v.cl;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    *cfg = {};
+    cfg->gridDim = dim3((unsigned)(units * v.cl));
+    cfg->blockDim = dim3((unsigned)v.cta);
+    cfg->dynamicSmemBytes = (size_t)v.smem;
+    cfg->stream = s;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    if (!params) return GBNORM_OK;
+    void *args[1] = {params};
+    if (cudaLaunchKernelExC(cfg, v.kernel, args) != cudaSuccess) return GBNORM_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
+}
+
+int resident(const Q8Variant &v, int slot, const HostDevice &d, int *out) {
+    std::atomic<int> &c = g_resident[d.dev][slot];
+    int o = c.load(std::memory_order_relaxed);
+    if (o == 0) {
+        if (cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess)
+            return GBNORM_ERR_CUDA;
+        if (v.cl == 1) {
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, v.kernel, v.cta, (size_t)v.smem) != cudaSuccess)
+                return GBNORM_ERR_CUDA;
+            o *= d.sms;
+        } else {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute attr;
+            cluster_launch(v, 1, nullptr, nullptr, &cfg, &attr);
+            if (cudaOccupancyMaxActiveClusters(&o, v.kernel, &cfg) != cudaSuccess) return GBNORM_ERR_CUDA;
+        }
+        if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
+        c.store(o, std::memory_order_relaxed);
+    }
+    *out = o;
+    return GBNORM_OK;
+}
+
+// Launches variant v over M rows; *units: its CTAs (clusters).
+int launch_rows(const Q8Variant &v, int slot, int64_t M, int64_t most, const HostDevice &d, void *params,
+                cudaStream_t s, int64_t *units) {
+    int o;
+    const int st = resident(v, slot, d, &o);
+    if (st != GBNORM_OK) return st;
+    const int64_t rpc = v.cta / v.tpr, want = (M + rpc - 1) / rpc;
+    int64_t cap = o < most ? o : most;
+    const int64_t limit = host_grid_limit() / v.cl;
+    if (host_grid_limit() > 0 && limit < cap) cap = limit > 0 ? limit : 1;
+    *units = want < cap ? want : cap;
+    if (v.cl == 1) return launch(v.kernel, *units, v.cta, (size_t)v.smem, params, s);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    return cluster_launch(v, *units, params, s, &cfg, &attr);
+}
+
+// The first variant of the table that holds N elements, -1 if none does.
+int find_rows(const Q8Table &t, int64_t N) {
+    for (int i = 0; i < t.count; ++i)
+        if ((int64_t)t.v[i].tpr * t.v[i].vpt * t.v[i].cl * 8 >= N) return i;
+    return -1;
 }
 
 // Checks shared by the two forwards; fills the spans of what every forward has.
@@ -181,16 +234,12 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
                                                     {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16, kQ8Fwd_ln_bf16}};
         const int kind = p.y ? 0 : (p.qg < 0 ? 1 : 2) + (p.c ? 2 : 0);
         const Q8Table &t = tables[a.is_ln][p.xdt][kind];
-        for (int i = 0; i < t.count; ++i) {
-            const Q8Variant &v = t.v[i];
-            if ((int64_t)v.tpr * v.vpt * 8 < N) continue;
-            int occ;
-            const int st = occupancy(d.dev, ((p.xdt * 2 + a.is_ln) * kQ8FwdKinds + kind) * kQ8MaxVariants + i, v.kernel,
-                                     v.cta, (size_t)v.smem, &occ);
-            if (st != GBNORM_OK) return st;
-            const int64_t rpc = v.cta / v.tpr;
-            t_last[0] = v.name;
-            return launch(v.kernel, grid_of((M + rpc - 1) / rpc, occ, d), v.cta, (size_t)v.smem, &p, stream);
+        const int i = find_rows(t, N);
+        if (i >= 0) {
+            int64_t units;
+            t_last[0] = t.v[i].name;
+            return launch_rows(t.v[i], ((p.xdt * 2 + a.is_ln) * kQ8FwdKinds + kind) * kQ8MaxVariants + i, M, INT64_MAX, d,
+                               &p, stream, &units);
         }
     }
     t_last[0] = "elem";
@@ -287,20 +336,14 @@ int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t
         const int ys = elem_size(y_dtype);
         const bool vec = N % 8 == 0 && vec_rows(dy, lddy, ys) && vec_rows(dres, lddres, xs) && vec_rows(dx, lddx, xs) &&
                          aligned(gamma, 16) && aligned(codes, 8) && ldc % 8 == 0;
-        const Q8Table &t = (is_layernorm ? kQ8Bwd_ln : kQ8Bwd_rms)[x_dtype == y_dtype ? x_dtype : 3];
-        int i = 0;
-        while (i < t.count && (int64_t)t.v[i].tpr * t.v[i].vpt * 8 < N) ++i;
+        const int types = x_dtype == y_dtype ? x_dtype : 3;
+        const Q8Table &t = (is_layernorm ? kQ8Bwd_ln : kQ8Bwd_rms)[types];
+        const int i = vec ? find_rows(t, N) : -1;
         int st;
-        if (vec && i < t.count) {
-            const Q8Variant &v = t.v[i];
-            int occ;
-            st = occupancy(d.dev, kBwdSlots + (is_layernorm * 4 + (x_dtype == y_dtype ? x_dtype : 3)) * kQ8MaxVariants + i,
-                           v.kernel, v.cta, (size_t)v.smem, &occ);
-            if (st != GBNORM_OK) return st;
-            const int64_t rpc = v.cta / v.tpr;
-            P = grid_of((M + rpc - 1) / rpc, occ < kQ8BwdPerSm ? occ : kQ8BwdPerSm, d);
-            t_last[1] = v.name;
-            st = launch(v.kernel, P, v.cta, (size_t)v.smem, &p, stream);
+        if (i >= 0) {
+            t_last[1] = t.v[i].name;
+            st = launch_rows(t.v[i], kBwdSlots + (is_layernorm * 4 + types) * kQ8MaxVariants + i, M, kQ8BwdPerSm * d.sms, d,
+                             &p, stream, &P);
         } else {
             P = grid_of(M, 1, d);
             t_last[1] = "elem";

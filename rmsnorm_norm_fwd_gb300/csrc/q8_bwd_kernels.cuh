@@ -8,6 +8,8 @@
 // Two passes over the registers: sum g xhat (and sum g), one barrier, then dx
 // and the column sums; codes and dy are widened again in the second pass.
 //
+// Rows longer than one CTA holds are split over a cluster, as in the forward.
+//
 // What bounds it: DRAM, 5 bytes an element (bf16 dy and dx, 1.06 bytes of
 // checkpoint), 7 with a residual's gradient.  The next row is prefetched to L2
 // while one is worked on.
@@ -34,29 +36,28 @@ __device__ __forceinline__ uint2 ld_codes8(const uint8_t *row, int c) {
     return v;
 }
 
-// NS sums over a row group through scratch [2][WPR] float2; the same bits on
-// every thread.
-template <int TPR, int NS>
-__device__ __forceinline__ void group_sums(float (&v)[2], float2 *scratch, int &parity, int bar_id) {
-    auto step = [&](int o) {
+// NS sums over a row group; the same bits on every thread.
+template <int TPR, int CL, int NS>
+__device__ __forceinline__ void group_sums(float (&v)[2], RowReduce<TPR, CL> &rr) {
+    auto steps = [&](int from) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int o = 16; o > 0; o >>= 1)
+            if (o <= from)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     };
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) step(o);
-    if constexpr (TPR > 32) {
-        constexpr int WPR = TPR / 32, L = pow2_at_least(WPR);
-        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
-        float2 *buf = scratch + parity * WPR;
-        if (lane == 0) buf[wig] = make_float2(v[0], NS > 1 ? v[1] : 0.f);
-        named_sync(bar_id, TPR);
-        const int w = lane & (L - 1);
-        const float2 b = w < WPR ? buf[w] : make_float2(0.f, 0.f);
+    auto take = [&](float4 b) {
         v[0] = b.x;
         if constexpr (NS > 1) v[1] = b.y;
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) step(o);
-        parity ^= 1;
+    };
+    steps(16);
+    if constexpr (TPR > 32) {
+        take(rr.warps(make_float4(v[0], NS > 1 ? v[1] : 0.f, 0.f, 0.f)));
+        steps(pow2_at_least(TPR / 32) / 2);
+    }
+    if constexpr (CL > 1) {
+        take(rr.ctas(make_float4(v[0], NS > 1 ? v[1] : 0.f, 0.f, 0.f)));
+        steps(CL / 2);
     }
 }
 
@@ -92,18 +93,27 @@ __device__ __forceinline__ void prefetch_l2_inner(const void *p, int bytes) {
     if (e > a) prefetch_l2(reinterpret_cast<const void *>(a), (int)(e - a));
 }
 
+__device__ __forceinline__ const void *at_chunk(const void *row, int c, int dt) {
+    return static_cast<const unsigned char *>(row) + (int64_t)c * 8 * esize(dt);
+}
+
 // XT: storage type of dy, dres and dx, or -1 for any combination.
-template <bool LN, int XT, int TPR, int VPT, int NT, int MINB>
+template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int CL>
 __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
     static_assert(NT % TPR == 0 && TPR % 32 == 0, "row groups");
     static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
-    constexpr int RPC = NT / TPR, WPR = TPR / 32;
+    constexpr int RPC = NT / TPR;
+    static_assert(CL == 1 || RPC == 1, "a cluster shares one row");
     extern __shared__ __align__(16) float4 q8_par[];  // own gamma, then the row groups' column sums
-    __shared__ float2 scratch_all[RPC * 2 * WPR];
+    __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
+    if constexpr (CL > 1) cluster_sync_all();  // every CTA runs before another writes to its shared memory
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    float2 *scratch = scratch_all + grp * 2 * WPR;
-    const int nc = (int)(p.N / 8), clg = p.cg - 3;
+    RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
+    // this CTA's part of a row: chunks [c0, c0 + nc)
+    const int slice = cta_slice<CL>((int)(p.N / 8)), c0 = CL == 1 ? 0 : (int)cluster_ctarank() * slice;
+    const int nc = CL == 1 ? slice : max(0, min(slice, (int)(p.N / 8) - c0));
+    const int clg = p.cg - 3;
     const int xdt = XT >= 0 ? XT : p.xdt, ydt = XT >= 0 ? XT : p.ydt;
     const float inv_n = 1.f / (float)p.N;
     auto has = [&](int k) { return k * TPR + t < nc; };
@@ -117,10 +127,10 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
             if constexpr (LN) accb[k][i] = f2s(0.f);
         }
     bool first = true;
-    int parity = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPC + grp; row < p.M; row += (int64_t)gridDim.x * RPC) {
-        const void *dyr = row_ptr(p.dy, row, p.lddy, ydt);
-        const uint8_t *cr = p.c + row * p.ldc;
+    const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
+    for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
+        const void *dyr = at_chunk(row_ptr(p.dy, row, p.lddy, ydt), c0, ydt);
+        const uint8_t *cr = p.c + row * p.ldc + 8 * c0;
         const float *cs = p.cs + row * p.ldcs;
         Row8<XT> dy[VPT];
         uint2 code[VPT];
@@ -133,18 +143,19 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
             if (has(k)) {
                 dy[k].load(dyr, k * TPR + t, ydt);
                 code[k] = ld_codes8(cr, k * TPR + t);
-                ab[k] = __ldg(reinterpret_cast<const float2 *>(cs) + ((k * TPR + t) >> clg));
+                ab[k] = __ldg(reinterpret_cast<const float2 *>(cs) + ((c0 + k * TPR + t) >> clg));
             }
         }
         const float rstd = __ldg(p.rstd + row);
         const float mean = LN ? __ldg(p.mean + row) : 0.f;
         if (t == 0) {
-            const int64_t next = row + (int64_t)gridDim.x * RPC;
-            if (next < p.M) {
-                prefetch_l2(row_ptr(p.dy, next, p.lddy, ydt), nc * 8 * esize(ydt));
-                prefetch_l2_inner(p.c + next * p.ldc, nc * 8);
-                prefetch_l2_inner(p.cs + next * p.ldcs, (((nc - 1) >> clg) + 1) * 8);
-                if (p.dres) prefetch_l2(row_ptr(p.dres, next, p.lddres, xdt), nc * 8 * esize(xdt));
+            const int64_t next = row + stride;
+            if (next < p.M && nc > 0) {
+                prefetch_l2(at_chunk(row_ptr(p.dy, next, p.lddy, ydt), c0, ydt), nc * 8 * esize(ydt));
+                prefetch_l2_inner(p.c + next * p.ldc + 8 * c0, nc * 8);
+                prefetch_l2_inner(p.cs + next * p.ldcs + 2 * (c0 >> clg), (((nc - 1) >> clg) + 1) * 8);
+                if (p.dres)
+                    prefetch_l2(at_chunk(row_ptr(p.dres, next, p.lddres, xdt), c0, xdt), nc * 8 * esize(xdt));
             }
         }
         if (first) {  // behind the first row's loads
@@ -152,7 +163,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float2 f[4];
-                par8g(has(k) ? p.gamma : nullptr, k * TPR + t, p.pdt, 1.f, f);
+                par8g(has(k) ? p.gamma : nullptr, c0 + k * TPR + t, p.pdt, 1.f, f);
                 gp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
                 gp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
             }
@@ -180,11 +191,11 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
             }
         }
         float sum[2] = {s2.x + s2.y, s1.x + s1.y};
-        group_sums<TPR, LN ? 2 : 1>(sum, scratch, parity, 1 + grp);
+        group_sums<TPR, CL, LN ? 2 : 1>(sum, rr);
         // dx = rstd (g - c1 - xhat c2) + dres
         const float2 r2 = f2s(rstd), nrc2 = f2s(-rstd * (sum[0] * inv_n)), nrc1 = f2s(LN ? -rstd * (sum[1] * inv_n) : 0.f);
         void *dxr = row_ptr(p.dx, row, p.lddx, xdt);
-        const void *drr = p.dres ? row_ptr(p.dres, row, p.lddres, xdt) : nullptr;
+        const void *drr = p.dres ? at_chunk(row_ptr(p.dres, row, p.lddres, xdt), c0, xdt) : nullptr;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             if (!has(k)) continue;
@@ -204,11 +215,11 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] = f2add(o[i], r[i]);
             }
-            st8p(dxr, 8 * (int64_t)(k * TPR + t), xdt, o);
+            st8p(dxr, 8 * (int64_t)(c0 + k * TPR + t), xdt, o);
         }
     }
 
-    // This CTA's partial row: the row groups' sums of the same columns are
+    // This CTA's (cluster's) partial row: the row groups' sums of the same columns are
     // added in group order through shared memory.
     auto store = [&](float2 (&acc)[VPT][4], float *ws) {
         if constexpr (RPC > 1) {
@@ -235,14 +246,15 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 if (!has(k)) continue;
-                float4 *o = reinterpret_cast<float4 *>(ws + 8 * (int64_t)(k * TPR + t));
+                float4 *o = reinterpret_cast<float4 *>(ws + 8 * (int64_t)(c0 + k * TPR + t));
                 o[0] = make_float4(acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y);
                 o[1] = make_float4(acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y);
             }
         }
     };
-    store(accg, p.ws + (int64_t)blockIdx.x * p.N);
-    if constexpr (LN) store(accb, p.ws + ((int64_t)gridDim.x + blockIdx.x) * p.N);
+    const int64_t P = gridDim.x / CL, part = blockIdx.x / CL;
+    store(accg, p.ws + part * p.N);
+    if constexpr (LN) store(accb, p.ws + (P + part) * p.N);
 }
 
 }  // namespace gbn

@@ -68,11 +68,12 @@ struct Q8ReadParams {
     int qfmt, qg;
 };
 
-// A compiled kernel with rows in registers: capacity tpr * vpt * 8 elements.
+// A compiled kernel with rows in registers: capacity tpr * vpt * cl * 8 elements.
 struct Q8Variant {
     const char *name;
     const void *kernel;
     int tpr, vpt, cta;
+    int cl;    // CTAs of the cluster that shares a row
     int smem;  // dynamic shared memory
 };
 struct Q8Table {

@@ -16,6 +16,8 @@
 //     statistics too.
 //   - A thread holds 8 to 32 elements, so that four 256-thread CTAs share an SM
 //     (LayerNorm three) and their phases overlap.
+//   - Rows longer than one CTA holds are split over a cluster of 2 to 8 CTAs,
+//     which exchange the row's sums through distributed shared memory.
 //   - Every thread keeps gamma (beta) of its own columns as fp32 in its own
 //     slots of shared memory: no conversion, no branch on the parameter type
 //     and no barrier in the loop.
@@ -142,11 +144,47 @@ __device__ __forceinline__ uint2 codes8(const float2 (&u)[4], int fmt, float one
 // lane).
 __host__ __device__ constexpr int pow2_at_least(int v) { return v <= 1 ? 1 : 2 * pow2_at_least((v + 1) / 2); }
 
-// Sum over a row group of `s` and maximum (NaN kept) of `m`, through this
-// group's scratch of [2][WPR] float4 under its named barrier; the same bits
-// on every thread.
-template <int TPR, bool MAX>
-__device__ __forceinline__ void group_sum_max(float &s, float &m, float4 *scratch, int &parity, int bar_id) {
+// What a row group of TPR threads (CL > 1: in each of the CL CTAs of a cluster)
+// reduces through: its scratch of [2][WPR] float4 and, for a cluster, a buffer
+// of [2][CL] in every CTA.  Two copies, so that one barrier a reduction
+// suffices: it proves that every reader of the copy before last is done.
+template <int TPR, int CL> struct RowReduce {
+    static constexpr int WPR = TPR / 32, SCRATCH = 2 * WPR + (CL > 1 ? 2 * CL : 0);
+    float4 *scratch;
+    int parity, bar_id;
+
+    // The partial v of this thread's warp; every thread gets that of warp
+    // `lane` modulo the next power of two (zeros past the last warp).
+    __device__ __forceinline__ float4 warps(float4 v) {
+        constexpr int L = pow2_at_least(WPR);
+        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+        float4 *buf = scratch + parity * WPR;
+        if (lane == 0) buf[wig] = v;
+        named_sync(bar_id, TPR);
+        const int w = lane & (L - 1);
+        const float4 b = w < WPR ? buf[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (CL == 1) parity ^= 1;
+        return b;
+    }
+    // The same over the CTAs of the cluster (CL a power of two): each CTA
+    // stores its value into every CTA's buffer; that of CTA lane mod CL.
+    __device__ __forceinline__ float4 ctas(float4 v) {
+        float4 *buf = scratch + 2 * WPR + parity * CL;
+        if (threadIdx.x < CL)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             map_to_rank(smem_u32(buf + cluster_ctarank()), threadIdx.x)),
+                         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                         : "memory");
+        cluster_sync_all();
+        parity ^= 1;
+        return buf[threadIdx.x & (CL - 1)];
+    }
+};
+
+// Sum over a row group of `s` and maximum (NaN kept) of `m`; the same bits on
+// every thread.  Maxima are of magnitudes.
+template <int TPR, int CL, bool MAX>
+__device__ __forceinline__ void group_sum_max(float &s, float &m, RowReduce<TPR, CL> &rr) {
     auto step = [&](int o) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
         if constexpr (MAX) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -154,28 +192,28 @@ __device__ __forceinline__ void group_sum_max(float &s, float &m, float4 *scratc
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) step(o);
     if constexpr (TPR > 32) {
-        constexpr int WPR = TPR / 32, L = pow2_at_least(WPR);
-        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
-        float4 *buf = scratch + parity * WPR;
-        if (lane == 0) buf[wig] = make_float4(s, MAX ? m : 0.f, 0.f, 0.f);
-        named_sync(bar_id, TPR);
-        const int w = lane & (L - 1);
-        const float4 b = w < WPR ? buf[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 b = rr.warps(make_float4(s, MAX ? m : 0.f, 0.f, 0.f));
         s = b.x;
-        if constexpr (MAX) m = b.y;  // maxima here are of magnitudes
+        if constexpr (MAX) m = b.y;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) step(o);
-        parity ^= 1;
+        for (int o = pow2_at_least(TPR / 32) / 2; o > 0; o >>= 1) step(o);
+    }
+    if constexpr (CL > 1) {
+        const float4 b = rr.ctas(make_float4(s, MAX ? m : 0.f, 0.f, 0.f));
+        s = b.x;
+        if constexpr (MAX) m = b.y;
+#pragma unroll
+        for (int o = CL / 2; o > 0; o >>= 1) step(o);
     }
 }
 
-// Mean and sum of squared deviations of a row group from its threads' own, of
-// `cnt` elements each (the update of Chan, Golub and LeVeque in its group
-// form, once over a warp's lanes, once over the warps).  EQUAL: every thread
-// has cnt, known at compile time.
-template <int TPR, bool EQUAL>
-__device__ __forceinline__ void group_meanvar(float &mean, float &m2, float cnt, float inv_n, float4 *scratch,
-                                              int &parity, int bar_id) {
+// Mean and sum of squared deviations of a row from its threads' own, of `cnt`
+// elements each (the update of Chan, Golub and LeVeque in its group form: over
+// a warp's lanes, the warps, the CTAs).  EQUAL: every thread has cnt, known at
+// compile time.  cta_cnt: elements of this CTA's part of the row; inv_n: 1 / N.
+template <int TPR, int CL, bool EQUAL>
+__device__ __forceinline__ void group_meanvar(float &mean, float &m2, float cnt, float cta_cnt, float inv_n,
+                                              RowReduce<TPR, CL> &rr) {
     float s = EQUAL ? mean : mean * cnt, c = cnt;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -189,24 +227,23 @@ __device__ __forceinline__ void group_meanvar(float &mean, float &m2, float cnt,
     for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
     mean = mw;
     m2 = q;
-    if constexpr (TPR > 32) {
-        constexpr int WPR = TPR / 32, L = pow2_at_least(WPR);
-        const int wig = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
-        float4 *buf = scratch + parity * WPR;
-        if (lane == 0) buf[wig] = make_float4(mw, q, EQUAL ? cnt * 32.f : c, 0.f);
-        named_sync(bar_id, TPR);
-        const int w = lane & (L - 1);
-        const float4 b = w < WPR ? buf[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+    // the parts' (mean, m2, count), one a lane, over L lanes
+    auto join = [&](float4 b, int L, float inv) {
         s = b.x * b.z;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        mean = s * inv_n;
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < L) s += __shfl_xor_sync(0xffffffffu, s, o);
+        mean = s * inv;
         const float dd = b.x - mean;
         m2 = b.z > 0.f ? b.y + b.z * (dd * dd) : 0.f;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-        parity ^= 1;
-    }
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < L) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+    };
+    if constexpr (TPR > 32)
+        join(rr.warps(make_float4(mean, m2, EQUAL ? cnt * 32.f : c, 0.f)), pow2_at_least(TPR / 32),
+             CL == 1 ? inv_n : cta_cnt > 0.f ? 1.f / cta_cnt : 0.f);
+    if constexpr (CL > 1) join(rr.ctas(make_float4(mean, m2, cta_cnt, 0.f)), CL, inv_n);
 }
 
 // h = x + r rounded once to the storage type.
@@ -321,15 +358,25 @@ constexpr int kOutY = 0, kOutRow = 1, kOutGroup = 2;  // y in ydt; 8-bit rows wi
 // Bytes of shared memory for the threads' own parameters.
 __host__ __device__ constexpr int q8_fwd_smem(bool ln, int vpt, int nt) { return nt * vpt * 32 * (ln ? 2 : 1); }
 
-// FULL: every thread holds VPT chunks.
-template <bool LN, int XT, int TPR, int VPT, int NT, int OUT, bool CK, bool FULL>
+// Chunks of a row of nc that each of CL CTAs holds: a multiple of a warp's
+// lanes, so that groups stay inside a warp.
+template <int CL> __device__ __forceinline__ int cta_slice(int nc) {
+    return CL == 1 ? nc : ((nc + CL - 1) / CL + 31) & ~31;
+}
+
+// FULL: every thread holds VPT chunks.  CL > 1: a row is split over the CTAs
+// of a cluster.
+template <bool LN, int XT, int TPR, int VPT, int NT, int CL, int OUT, bool CK, bool FULL>
 __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, float4 *scratch_all) {
-    constexpr int RPC = NT / TPR, WPR = TPR / 32;
+    constexpr int RPC = NT / TPR;
+    static_assert(CL == 1 || RPC == 1, "a cluster shares one row");
     constexpr int xes = XT == kF32 ? 4 : 2;
     constexpr bool RQ = !LN && OUT != kOutY;  // codes of h * gamma
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31;
-    float4 *scratch = scratch_all + grp * 2 * WPR;
-    const int nc = (int)(p.N / 8);
+    RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
+    // this CTA's part of a row: chunks [c0, c0 + nc)
+    const int slice = cta_slice<CL>((int)(p.N / 8)), c0 = CL == 1 ? 0 : (int)cluster_ctarank() * slice;
+    const int nc = CL == 1 ? slice : max(0, min(slice, (int)(p.N / 8) - c0));
     const float inv_n = 1.f / (float)p.N;
     const float qmax = q8_max(p.qfmt), inv_qmax = 1.f / qmax;
     const int qlg = p.qg - 3, clg = p.cg - 3;  // log2 of the lanes of a group
@@ -342,17 +389,17 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
         f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
     };
     bool first = true;
-    int parity = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPC + grp; row < p.M; row += (int64_t)gridDim.x * RPC) {
+    const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
+    for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
         Raw8<XT> h[VPT];
-        const unsigned char *xr = static_cast<const unsigned char *>(p.x) + row * p.ldx * xes;
+        const unsigned char *xr = static_cast<const unsigned char *>(p.x) + (row * p.ldx + 8 * c0) * xes;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             h[k] = Raw8<XT>{};
             if (has(k)) h[k] = ld_raw8<XT>(xr, k * TPR + t);
         }
         if (p.res) {
-            const unsigned char *rr = static_cast<const unsigned char *>(p.res) + row * p.ldr * xes;
+            const unsigned char *rr = static_cast<const unsigned char *>(p.res) + (row * p.ldr + 8 * c0) * xes;
             Raw8<XT> r[VPT];
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
@@ -362,7 +409,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
 #pragma unroll
             for (int k = 0; k < VPT; ++k) add8<XT>(h[k], r[k]);
             if (p.h) {
-                unsigned char *hr = static_cast<unsigned char *>(p.h) + row * p.ldh * xes;
+                unsigned char *hr = static_cast<unsigned char *>(p.h) + (row * p.ldh + 8 * c0) * xes;
 #pragma unroll
                 for (int k = 0; k < VPT; ++k)
                     if (has(k)) st_raw8<XT>(hr, k * TPR + t, h[k]);
@@ -372,33 +419,34 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
         // residual the loads of a row alone keep DRAM busy (16384 x 8192:
         // 149 us without, 158 us with the prefetch).
         if (t == 0 && p.res == nullptr) {
-            const int64_t next = row + (int64_t)gridDim.x * RPC;
-            if (next < p.M) prefetch_l2(static_cast<const unsigned char *>(p.x) + next * p.ldx * xes, nc * 8 * xes);
+            const int64_t next = row + stride;
+            if (next < p.M && nc > 0)
+                prefetch_l2(static_cast<const unsigned char *>(p.x) + (next * p.ldx + 8 * c0) * xes, nc * 8 * xes);
         }
         if (first) {  // behind the first row's loads
             first = false;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 float2 f[4];
-                par8g(has(k) ? p.gamma : nullptr, k * TPR + t, p.pdt, 1.f, f);
+                par8g(has(k) ? p.gamma : nullptr, c0 + k * TPR + t, p.pdt, 1.f, f);
                 gp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
                 gp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
                 if constexpr (LN) {
-                    par8g(has(k) ? p.beta : nullptr, k * TPR + t, p.pdt, 0.f, f);
+                    par8g(has(k) ? p.beta : nullptr, c0 + k * TPR + t, p.pdt, 0.f, f);
                     bp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
                     bp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
                 }
             }
         }
         if constexpr (CK) {
-            uint8_t *cr = p.c + row * p.ldc;
+            uint8_t *cr = p.c + row * p.ldc + 8 * c0;
             float top, low;
             range_of_own<XT, VPT>(h, has, lane, clg, top, low);
             const CkGroup g = ck_group(top, low);
             // the first lanes of a group write its pairs, lane k of it chunk k's
             const int at = own * TPR + (t & ~((1 << clg) - 1));
             if ((lane & ((1 << clg) - 1)) < VPT && (FULL || at < nc))
-                *reinterpret_cast<float2 *>(p.cs + row * p.ldcs + 2 * (at >> clg)) = make_float2(g.scale, g.mid);
+                *reinterpret_cast<float2 *>(p.cs + row * p.ldcs + 2 * ((c0 + at) >> clg)) = make_float2(g.scale, g.mid);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const float2 nm = f2s(-fetch<VPT>(g.mid, lane, k)), inv = f2s(fetch<VPT>(g.inv, lane, k));
@@ -411,7 +459,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
         }
 
         // ---------------------------------------------------------------- sums of the row
-        uint8_t *qr = p.q + row * p.ldq;
+        uint8_t *qr = p.q + row * p.ldq + 8 * c0;
         float *qs = p.qs + row * p.qs_row;
         float acc, mean = 0.f, m = 0.f, unused = 0.f;
         // codes of o (chunk k), scaled by inv
@@ -458,7 +506,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             const float dm = FULL ? s * (1.f / (VPT * 8)) : cnt > 0.f ? s / cnt : 0.f;
             mean = ref + dm;
             acc = fmax_nan(q2.x + q2.y - s * dm, 0.f);
-            group_meanvar<TPR, FULL>(mean, acc, cnt, inv_n, scratch, parity, 1 + grp);
+            group_meanvar<TPR, CL, FULL>(mean, acc, cnt, (float)(8 * nc), inv_n, rr);
         } else {
             float2 a2 = f2s(0.f);
 #pragma unroll
@@ -475,10 +523,10 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             }
             acc = a2.x + a2.y;
             if constexpr (OUT == kOutGroup) put_groups();
-            group_sum_max<TPR, OUT == kOutRow>(acc, m, scratch, parity, 1 + grp);
+            group_sum_max<TPR, CL, OUT == kOutRow>(acc, m, rr);
         }
         const float rstd = rsqrtf(acc * inv_n + p.eps);
-        if (t == 0) {
+        if (t == 0 && c0 == 0) {
             if (p.rstd) p.rstd[row] = rstd;
             if (LN && p.mean) p.mean[row] = mean;
         }
@@ -498,7 +546,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
                     for (int i = 0; i < 4; ++i) o[k][i] = has(k) ? f2add(o[k][i], g8[i]) : f2s(0.f);
                 }
                 if constexpr (OUT == kOutY) {
-                    if (has(k)) st8p(row_ptr(p.y, row, p.ldy, p.ydt), 8 * (int64_t)(k * TPR + t), p.ydt, o[k]);
+                    if (has(k)) st8p(row_ptr(p.y, row, p.ldy, p.ydt), 8 * (int64_t)(c0 + k * TPR + t), p.ydt, o[k]);
                 } else if constexpr (OUT == kOutRow) {
                     m = fmax_nan(m, amax8(o[k]));
                 }
@@ -508,25 +556,28 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             if constexpr (!RQ) put_groups();
             const int at = own * TPR + (t & ~((1 << qlg) - 1));
             if ((lane & ((1 << qlg) - 1)) < VPT && (FULL || at < nc))
-                qs[(at >> qlg) * p.qs_grp] = gscale < kQ8Tiny ? 0.f : RQ ? gscale * rstd * inv_qmax : gscale * inv_qmax;
+                qs[((c0 + at) >> qlg) * p.qs_grp] = gscale < kQ8Tiny ? 0.f : RQ ? gscale * rstd * inv_qmax : gscale * inv_qmax;
         } else if constexpr (OUT == kOutRow) {
-            if constexpr (!RQ) group_sum_max<TPR, true>(unused, m, scratch, parity, 1 + grp);
+            if constexpr (!RQ) group_sum_max<TPR, CL, true>(unused, m, rr);
             const float inv = q8_inv(m, qmax);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) put(k, o[k], inv);
-            if (t == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax);
+            if (t == 0 && c0 == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax);
         }
     }
 }
 
-template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int OUT, bool CK>
+template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int CL, int OUT, bool CK>
 __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
     static_assert(NT % TPR == 0 && TPR % 32 == 0 && VPT <= 4, "row groups");
     static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
     extern __shared__ __align__(16) float4 q8_par[];
-    __shared__ float4 scratch[NT / 32 * 2];
-    if (p.N == (int64_t)TPR * VPT * 8) q8_fwd_body<LN, XT, TPR, VPT, NT, OUT, CK, true>(p, q8_par, scratch);
-    else q8_fwd_body<LN, XT, TPR, VPT, NT, OUT, CK, false>(p, q8_par, scratch);
+    __shared__ float4 scratch[NT / TPR * RowReduce<TPR, CL>::SCRATCH];
+    if constexpr (CL > 1) cluster_sync_all();  // every CTA runs before another writes to its shared memory
+    if (p.N == (int64_t)CL * TPR * VPT * 8)
+        q8_fwd_body<LN, XT, TPR, VPT, NT, CL, OUT, CK, true>(p, q8_par, scratch);
+    else
+        q8_fwd_body<LN, XT, TPR, VPT, NT, CL, OUT, CK, false>(p, q8_par, scratch);
 }
 
 }  // namespace gbn
