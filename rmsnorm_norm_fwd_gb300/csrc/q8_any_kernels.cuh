@@ -1,0 +1,370 @@
+// q8_any_kernels.cuh -- forward and backward of the 8-bit operators for rows
+// without 16-byte vectors (any length, stride, alignment and types), rows in
+// registers.
+//
+// A warp holds VB blocks of 256 consecutive elements, each lane 8 of a block, 32
+// apart, so that every access of a warp is 32 consecutive elements whatever
+// their alignment, and a group of 32..256 columns is 1..8 of a lane's elements
+// across the warp.  Apart from that the steps are those of the vector kernels.
+// What bounds it: the load and store instructions, one an element.
+#pragma once
+
+#include "q8_bwd_kernels.cuh"
+
+namespace gbn {
+
+// Elements base + 32 i + lane of a row, zero past its end at n.
+__device__ __forceinline__ void ld_block(const void *row, int64_t base, int64_t n, int dt, float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    const int64_t j0 = base + lane;
+    auto all = [&](auto *p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = j0 + 32 * i < n ? to_f(p[j0 + 32 * i]) : 0.f;
+    };
+    if (dt == kF32) all(static_cast<const float *>(row));
+    else if (dt == kBF16) all(static_cast<const __nv_bfloat16 *>(row));
+    else all(static_cast<const __half *>(row));
+}
+__device__ __forceinline__ void st_block(void *row, int64_t base, int64_t n, int dt, const float (&v)[8]) {
+    const int64_t j0 = base + (threadIdx.x & 31);
+    auto all = [&](auto *p) {
+        using T = typename std::remove_pointer<decltype(p)>::type;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j0 + 32 * i < n) p[j0 + 32 * i] = from_f<T>(v[i]);
+    };
+    if (dt == kF32) all(static_cast<float *>(row));
+    else if (dt == kBF16) all(static_cast<__nv_bfloat16 *>(row));
+    else all(static_cast<__half *>(row));
+}
+__device__ __forceinline__ void st_bytes(uint8_t *row, int64_t base, int64_t n, const uint32_t (&v)[8]) {
+    const int64_t j0 = base + (threadIdx.x & 31);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (j0 + 32 * i < n) row[j0 + 32 * i] = (uint8_t)v[i];
+}
+
+// Maxima over the groups of a block: m[i] joined with its 2^lg - 1 neighbours
+// of the same group, then over the warp's lanes, all 8 side by side (partner
+// lanes trade halves in the first three steps): lane l gets that of i = l mod 8.
+__device__ __forceinline__ float block_max(float (&m)[8], int lg) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+        if (o < (1 << lg)) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = fmax_nan(m[i], m[i ^ o]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = t[i];
+        }
+    auto trade = [&](float even, float odd, int o) {
+        const bool b = lane & o;
+        return fmax_nan(b ? odd : even, __shfl_xor_sync(0xffffffffu, b ? even : odd, o));
+    };
+    const float a0 = trade(m[0], m[1], 1), a1 = trade(m[2], m[3], 1), a2 = trade(m[4], m[5], 1), a3 = trade(m[6], m[7], 1);
+    float r = trade(trade(a0, a1, 2), trade(a2, a3, 2), 4);
+    r = fmax_nan(r, __shfl_xor_sync(0xffffffffu, r, 8));
+    return fmax_nan(r, __shfl_xor_sync(0xffffffffu, r, 16));
+}
+__device__ __forceinline__ float from_lane(float v, int i) { return __shfl_sync(0xffffffffu, v, i); }
+
+// Elements of a row that each of CL CTAs holds: whole blocks.
+template <int CL> __device__ __forceinline__ int64_t cta_columns(int64_t n) {
+    return CL == 1 ? n : ((n + CL - 1) / CL + 255) & ~(int64_t)255;
+}
+
+template <bool LN, int TPR, int VB, int NT, int MINB, int CL, int OUT, bool CK>
+__global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
+    static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
+    constexpr int RPC = NT / TPR, WPR = TPR / 32;
+    constexpr bool RQ = !LN && OUT != kOutY;  // codes of h * gamma
+    __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
+    if constexpr (CL > 1) cluster_sync_all();
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = t >> 5;
+    RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
+    // this CTA's part of a row: elements [j0, n)
+    const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
+    const int64_t n = CL == 1 ? p.N : (j0 + cols < p.N ? j0 + cols : p.N);
+    const float mine = n > j0 ? (float)(n - j0) : 0.f, inv_n = 1.f / (float)p.N;
+    const float qmax = q8_max(p.qfmt), inv_qmax = 1.f / qmax;
+    const int qlg = p.qg - 5, clg = p.cg - 5;  // log2 of a lane's elements of a group in a block
+    auto base = [&](int k) { return j0 + 256 * (int64_t)(k * WPR + warp); };
+    auto has = [&](int k, int i) { return base(k) + 32 * i + lane < n; };
+    const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
+    for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
+        float v[VB][8];  // h, then what is stored of it: h * gamma or y
+        const void *xr = row_ptr(p.x, row, p.ldx, p.xdt);
+#pragma unroll
+        for (int k = 0; k < VB; ++k) ld_block(xr, base(k), n, p.xdt, v[k]);
+        if (t == 0 && n > j0) {
+            const int64_t next = row + stride;
+            if (next < p.M)
+                prefetch_l2_inner(static_cast<const unsigned char *>(row_ptr(p.x, next, p.ldx, p.xdt)) + j0 * esize(p.xdt),
+                                  (int)(n - j0) * esize(p.xdt));
+        }
+        if (p.res) {
+            const void *rrow = row_ptr(p.res, row, p.ldr, p.xdt);
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {
+                float r[8];
+                ld_block(rrow, base(k), n, p.xdt, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = round_to(v[k][i] + r[i], p.xdt);
+            }
+            if (p.h) {
+                void *hr = row_ptr(p.h, row, p.ldh, p.xdt);
+#pragma unroll
+                for (int k = 0; k < VB; ++k) st_block(hr, base(k), n, p.xdt, v[k]);
+            }
+        }
+        if constexpr (CK) {
+            uint8_t *cr = p.c + row * p.ldc;
+            float *cs = p.cs + row * p.ldcs;
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {
+                float hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    hi[i] = has(k, i) ? v[k][i] : -INFINITY;
+                    lo[i] = has(k, i) ? -v[k][i] : -INFINITY;
+                }
+                const CkGroup g = ck_group(block_max(hi, clg), -block_max(lo, clg));
+                const int64_t first = base(k) + 32 * lane;  // lane i < 8: first element of i
+                if (lane < 8 && (lane & ((1 << clg) - 1)) == 0 && first < n) {
+                    cs[2 * (first >> p.cg)] = g.scale;
+                    cs[2 * (first >> p.cg) + 1] = g.mid;
+                }
+                uint32_t code[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    code[i] = i8_code(__fmul_rn(__fsub_rn(v[k][i], from_lane(g.mid, i)), from_lane(g.inv, i)));
+                st_bytes(cr, base(k), n, code);
+            }
+        }
+
+        // ---------------------------------------------------------------- sums of the row
+        uint8_t *qr = p.q + row * p.ldq;
+        float *qs = p.qs + row * p.qs_row;
+        float acc = 0.f, mean = 0.f, m = 0.f, unused = 0.f;
+        float gmax[VB];  // lane i < 8: the maximum of i's group
+        auto put = [&](int k, auto &&inv) {
+            uint32_t code[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) code[i] = q8_code(__fmul_rn(v[k][i], inv(i)), p.qfmt);
+            st_bytes(qr, base(k), n, code);
+        };
+        auto put_groups = [&]() {
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {
+                float a[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] = fabsf(v[k][i]);
+                gmax[k] = block_max(a, qlg);
+                const float inv = q8_inv(gmax[k], qmax);
+                put(k, [&](int i) { return from_lane(inv, i); });
+            }
+        };
+        if constexpr (LN) {
+            // one pass about the thread's first element, as the vector kernels
+            const float ref = v[0][0];
+            float s = 0.f, q = 0.f, cnt = 0.f;
+#pragma unroll
+            for (int k = 0; k < VB; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (has(k, i)) {
+                        const float d = v[k][i] - ref;
+                        cnt += 1.f;
+                        s += d;
+                        q = fmaf(d, d, q);
+                    }
+            const float dm = cnt > 0.f ? s / cnt : 0.f;
+            mean = ref + dm;
+            acc = fmax_nan(q - s * dm, 0.f);
+            group_meanvar<TPR, CL, false>(mean, acc, cnt, mine, inv_n, rr);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc = fmaf(v[k][i], v[k][i], acc);
+                if constexpr (RQ) {
+                    if (p.gamma) {
+                        float g[8];
+                        ld_block(p.gamma, base(k), n, p.pdt, g);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[k][i] *= g[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(v[k][i]));
+                }
+            }
+            if constexpr (OUT == kOutGroup) put_groups();
+            group_sum_max<TPR, CL, OUT == kOutRow>(acc, m, rr);
+        }
+        const float rstd = rsqrtf(acc * inv_n + p.eps);
+        if (t == 0 && j0 == 0) {
+            if (p.rstd) p.rstd[row] = rstd;
+            if (LN && p.mean) p.mean[row] = mean;
+        }
+
+        // ---------------------------------------------------------------- output
+        if constexpr (!RQ) {
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {  // y; zeros past the row's end
+                float g[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = has(k, i) ? (v[k][i] - mean) * rstd : 0.f;
+                if (p.gamma) {
+                    ld_block(p.gamma, base(k), n, p.pdt, g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] *= g[i];
+                }
+                if (LN && p.beta) {
+                    ld_block(p.beta, base(k), n, p.pdt, g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] += g[i];
+                }
+                if constexpr (OUT == kOutY) {
+                    st_block(row_ptr(p.y, row, p.ldy, p.ydt), base(k), n, p.ydt, v[k]);
+                } else if constexpr (OUT == kOutRow) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(v[k][i]));
+                }
+            }
+        }
+        if constexpr (OUT == kOutGroup) {
+            if constexpr (!RQ) put_groups();
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {
+                const int64_t first = base(k) + 32 * lane;
+                if (lane < 8 && (lane & ((1 << qlg) - 1)) == 0 && first < n)
+                    qs[(first >> p.qg) * p.qs_grp] =
+                        gmax[k] < kQ8Tiny ? 0.f : RQ ? gmax[k] * rstd * inv_qmax : gmax[k] * inv_qmax;
+            }
+        } else if constexpr (OUT == kOutRow) {
+            if constexpr (!RQ) group_sum_max<TPR, CL, true>(unused, m, rr);
+            const float inv = q8_inv(m, qmax);
+#pragma unroll
+            for (int k = 0; k < VB; ++k) put(k, [&](int) { return inv; });
+            if (t == 0 && j0 == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax);
+        }
+    }
+}
+
+template <bool LN, int TPR, int VB, int NT, int MINB, int CL>
+__global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
+    static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
+    pdl_launch_dependents();  // the column reduce waits for this grid's completion
+    constexpr int RPC = NT / TPR, WPR = TPR / 32;
+    extern __shared__ __align__(16) float q8_sums[];  // RPC > 1: the row groups' column sums, [VB][8][NT]
+    __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
+    if constexpr (CL > 1) cluster_sync_all();
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = t >> 5;
+    RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
+    const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
+    const int64_t n = CL == 1 ? p.N : (j0 + cols < p.N ? j0 + cols : p.N);
+    const float inv_n = 1.f / (float)p.N;
+    auto base = [&](int k) { return j0 + 256 * (int64_t)(k * WPR + warp); };
+    float accg[VB][8], accb[LN ? VB : 1][8];
+#pragma unroll
+    for (int k = 0; k < VB; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            accg[k][i] = 0.f;
+            if constexpr (LN) accb[k][i] = 0.f;
+        }
+    const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
+    for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
+        const void *dyr = row_ptr(p.dy, row, p.lddy, p.ydt);
+        const uint8_t *cr = p.c + row * p.ldc;
+        const float *cs = p.cs + row * p.ldcs;
+        const float rstd = __ldg(p.rstd + row);
+        const float mean = LN ? __ldg(p.mean + row) : 0.f;
+        float d[VB][8], xh[VB][8];
+#pragma unroll
+        for (int k = 0; k < VB; ++k) {
+            ld_block(dyr, base(k), n, p.ydt, d[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t j = base(k) + 32 * i + lane;
+                xh[k][i] = 0.f;
+                if (j < n) {
+                    const float *g = cs + 2 * (j >> p.cg);
+                    xh[k][i] = fmaf((float)(int8_t)cr[j], __ldg(g) * rstd, (__ldg(g + 1) - mean) * rstd);
+                }
+            }
+        }
+        if (t == 0 && n > j0) {
+            const int64_t next = row + stride;
+            if (next < p.M) {
+                prefetch_l2_inner(static_cast<const unsigned char *>(row_ptr(p.dy, next, p.lddy, p.ydt)) + j0 * esize(p.ydt),
+                                  (int)(n - j0) * esize(p.ydt));
+                prefetch_l2_inner(p.c + next * p.ldc + j0, (int)(n - j0));
+            }
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < VB; ++k) {
+            float g[8];
+            if (p.gamma) ld_block(p.gamma, base(k), n, p.pdt, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
+                sum[0] = fmaf(dg, xh[k][i], sum[0]);
+                if constexpr (LN) sum[1] += dg;
+            }
+        }
+        group_sums<TPR, CL, LN ? 2 : 1>(sum, rr);
+        const float nrc2 = -rstd * (sum[0] * inv_n), nrc1 = LN ? -rstd * (sum[1] * inv_n) : 0.f;
+        void *dxr = row_ptr(p.dx, row, p.lddx, p.xdt);
+        const void *drr = p.dres ? row_ptr(p.dres, row, p.lddres, p.xdt) : nullptr;
+#pragma unroll
+        for (int k = 0; k < VB; ++k) {
+            float g[8], o[8];
+            if (p.gamma) ld_block(p.gamma, base(k), n, p.pdt, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
+                o[i] = fmaf(nrc2, xh[k][i], fmaf(rstd, dg, nrc1));
+                accg[k][i] = fmaf(d[k][i], xh[k][i], accg[k][i]);
+                if constexpr (LN) accb[k][i] += d[k][i];
+            }
+            if (drr) {
+                float r[8];
+                ld_block(drr, base(k), n, p.xdt, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += r[i];
+            }
+            st_block(dxr, base(k), n, p.xdt, o);
+        }
+    }
+    // this CTA's (cluster's) partial row; several row groups are added in group order
+    auto store = [&](float (&acc)[VB][8], float *ws) {
+        if constexpr (RPC > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < VB; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q8_sums[(8 * k + i) * NT + threadIdx.x] = acc[k][i];
+            __syncthreads();
+            for (int s = threadIdx.x; s < 8 * VB * TPR; s += NT) {
+                const int ki = s / TPR, tt = s % TPR;
+                const int64_t j = 256 * (int64_t)((ki >> 3) * WPR + (tt >> 5)) + 32 * (ki & 7) + (tt & 31);
+                if (j >= p.N) continue;
+                float a = q8_sums[ki * NT + tt];
+#pragma unroll
+                for (int g = 1; g < RPC; ++g) a += q8_sums[ki * NT + g * TPR + tt];
+                ws[j] = a;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VB; ++k) st_block(ws, base(k), n, kF32, acc[k]);
+        }
+    };
+    const int64_t P = gridDim.x / CL, part = blockIdx.x / CL;
+    store(accg, p.ws + part * p.N);
+    if constexpr (LN) store(accb, p.ws + (P + part) * p.N);
+}
+
+}  // namespace gbn

@@ -104,7 +104,8 @@ int64_t grid_of(int64_t units, int64_t per_sm, const HostDevice &d) {
 
 // Kernels with rows in registers: how many row groups (CTAs, or clusters) run
 // at once on the device, measured once per device and slot.
-constexpr int kBwdSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants, kSlots = kBwdSlots + 2 * 4 * kQ8MaxVariants;
+constexpr int kBwdSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants, kAnySlots = kBwdSlots + 2 * 4 * kQ8MaxVariants,
+              kSlots = kAnySlots + 2 * (kQ8FwdKinds + 1) * kQ8MaxVariants;
 std::atomic<int> g_resident[kHostMaxDev][kSlots];
 
 int cluster_launch(const Q8Variant &v, int64_t units, void *params, cudaStream_t s, cudaLaunchConfig_t *cfg,
@@ -229,18 +230,17 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
     const bool vec = N % 8 == 0 && vec_rows(p.x, p.ldx, xs) && vec_rows(p.res, p.ldr, xs) && vec_rows(p.h, p.ldh, xs) &&
                      vec_rows(p.y, p.ldy, elem_size(p.ydt)) && aligned(p.gamma, 16) && aligned(p.beta, 16) &&
                      aligned(p.q, 8) && p.ldq % 8 == 0 && aligned(p.c, 8) && p.ldc % 8 == 0;
-    if (vec) {
-        static const Q8Table *const tables[2][3] = {{kQ8Fwd_rms_f32, kQ8Fwd_rms_f16, kQ8Fwd_rms_bf16},
-                                                    {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16, kQ8Fwd_ln_bf16}};
-        const int kind = p.y ? 0 : (p.qg < 0 ? 1 : 2) + (p.c ? 2 : 0);
-        const Q8Table &t = tables[a.is_ln][p.xdt][kind];
-        const int i = find_rows(t, N);
-        if (i >= 0) {
-            int64_t units;
-            t_last[0] = t.v[i].name;
-            return launch_rows(t.v[i], ((p.xdt * 2 + a.is_ln) * kQ8FwdKinds + kind) * kQ8MaxVariants + i, M, INT64_MAX, d,
-                               &p, stream, &units);
-        }
+    static const Q8Table *const tables[2][3] = {{kQ8Fwd_rms_f32, kQ8Fwd_rms_f16, kQ8Fwd_rms_bf16},
+                                                {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16, kQ8Fwd_ln_bf16}};
+    const int kind = p.y ? 0 : (p.qg < 0 ? 1 : 2) + (p.c ? 2 : 0);
+    const Q8Table &t = vec ? tables[a.is_ln][p.xdt][kind] : (a.is_ln ? kQ8Any_ln : kQ8Any_rms)[kind];
+    const int i = find_rows(t, N);
+    if (i >= 0) {
+        const int slot = (vec ? ((p.xdt * 2 + a.is_ln) * kQ8FwdKinds + kind) * kQ8MaxVariants
+                              : kAnySlots + (a.is_ln * (kQ8FwdKinds + 1) + kind) * kQ8MaxVariants) + i;
+        int64_t units;
+        t_last[0] = t.v[i].name;
+        return launch_rows(t.v[i], slot, M, INT64_MAX, d, &p, stream, &units);
     }
     t_last[0] = "elem";
     return launch(kQ8FwdElem[a.is_ln], grid_of(M, 8, d), kElemCTA, 0, &p, stream);
@@ -337,12 +337,15 @@ int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t
         const bool vec = N % 8 == 0 && vec_rows(dy, lddy, ys) && vec_rows(dres, lddres, xs) && vec_rows(dx, lddx, xs) &&
                          aligned(gamma, 16) && aligned(codes, 8) && ldc % 8 == 0;
         const int types = x_dtype == y_dtype ? x_dtype : 3;
-        const Q8Table &t = (is_layernorm ? kQ8Bwd_ln : kQ8Bwd_rms)[types];
-        const int i = vec ? find_rows(t, N) : -1;
+        const Q8Table &t = vec ? (is_layernorm ? kQ8Bwd_ln : kQ8Bwd_rms)[types]
+                               : (is_layernorm ? kQ8Any_ln : kQ8Any_rms)[kQ8FwdKinds];
+        const int i = find_rows(t, N);
         int st;
         if (i >= 0) {
+            const int slot = (vec ? kBwdSlots + (is_layernorm * 4 + types) * kQ8MaxVariants
+                                  : kAnySlots + (is_layernorm * (kQ8FwdKinds + 1) + kQ8FwdKinds) * kQ8MaxVariants) + i;
             t_last[1] = t.v[i].name;
-            st = launch_rows(t.v[i], kBwdSlots + (is_layernorm * 4 + types) * kQ8MaxVariants + i, M, kQ8BwdPerSm * d.sms, d,
+            st = launch_rows(t.v[i], slot, M, kQ8BwdPerSm * d.sms, d,
                              &p, stream, &P);
         } else {
             P = grid_of(M, 1, d);

@@ -89,6 +89,8 @@ extern const Q8Table kQ8Fwd_ln_f32[kQ8FwdKinds], kQ8Fwd_ln_f16[kQ8FwdKinds], kQ8
 
 // Backward: dy, dres and dx all fp32, fp16, bf16; any combination.
 extern const Q8Table kQ8Bwd_rms[4], kQ8Bwd_ln[4];
+// Rows without 16-byte vectors, any types: the forward's kinds, then the backward.
+extern const Q8Table kQ8Any_rms[kQ8FwdKinds + 1], kQ8Any_ln[kQ8FwdKinds + 1];
 // Partial rows of the backward are at most this many CTAs per SM.
 constexpr int kQ8BwdPerSm = 4;
 // Reading back: [format][with the norm on top][type of y]; a second kernel

@@ -270,6 +270,54 @@ def test_extreme_values():
         ref.check_q8(False, x[2:], None, q[2:], s[2:], 64, y, tol)
 
 
+ODD = [(300, 32), (500, 64), (1003, 128), (1999, 256), (3001, 128), (6001, 64), (12001, 32), (30001, 128), (60001, 256),
+       (100001, 128)]
+
+
+@pytest.mark.parametrize("N,group", ODD)
+@pytest.mark.parametrize("ln", [False, True])
+def test_odd_lengths(N, group, ln):
+    """Rows without 16-byte vectors, from one warp to a cluster."""
+    M = 33 if N < 10000 else 5
+    run_forward(ln, M, N, "bf16", group=group, ck=group)
+    run_forward(ln, M, N, "fp16", pdt="fp32", group=0, ck=group, residual=False, fmt=I8)
+    run_forward(ln, M, N, "fp32", group=group)
+    run_forward(ln, M, N, "fp32", group=0)
+    run_forward(ln, M, N, "bf16", out="ck8", ck=group)
+    run_backward(ln, M, N, "bf16", group=group)
+    run_backward(ln, M, N, "fp32", ydt="bf16", group=group, dres=False)
+
+
+@pytest.mark.parametrize("N", [131080, 200001])
+@pytest.mark.parametrize("ln", [False, True])
+def test_longer_than_a_cluster_holds(N, ln):
+    g = lib()
+    run_forward(ln, 3, N, "bf16", group=128, ck=128)
+    assert g.q8_last_variant(0) == "elem"
+    run_forward(ln, 3, N, "bf16", group=0)
+    run_forward(ln, 3, N, "bf16", out="ck8", ck=64)
+    run_backward(ln, 3, N, "bf16")
+    assert g.q8_last_variant(1) == "elem"
+
+
+def test_every_kernel_is_reached():
+    """One call for each row capacity, aligned and not: the kernel named for it runs."""
+    g = lib()
+    names = [set(), set(), set()]
+    for ln in (False, True):
+        for N in (8, 256, 512, 1024, 2048, 4096, 5120, 6144, 8192, 12288, 16384, 32768, 65536, 131072, 131080, 7, 301, 1001,
+                  2001, 4001, 8001, 16001, 32001, 65001, 131071):
+            run_forward(ln, 2, N, "bf16", group=32, ck=32)
+            names[0].add((ln, g.q8_last_variant(0)))
+            run_backward(ln, 2, N, "bf16")
+            names[1].add((ln, g.q8_last_variant(1)))
+    for what, want in ((0, ("rows32x1c1", "rows256x4c1", "any32x1c1", "any512x2c8", "any1024x2c8", "elem")),
+                       (1, ("rows32x1c1", "any32x1c1", "any512x2c4", "any1024x2c8", "elem"))):
+        for ln in (False, True):
+            have = {v for l, v in names[what] if l == ln}
+            assert have >= set(want) - ({"rows256x4c1"} if ln and what else set()), (what, ln, have)
+
+
 # ------------------------------------------------------------------ checkpointed forward
 @pytest.mark.parametrize("N", LENGTHS + [16392, 40000])
 @pytest.mark.parametrize("ln", [False, True])
