@@ -52,22 +52,30 @@ def checkpoint8_empty(M: int, N: int, group: int = 128, device="cuda") -> Checkp
                        torch.empty(M, _groups(N, group), 2, device=device, dtype=torch.float32), group)
 
 
+# The current stream's handle without a Stream object around it (a call of a
+# few microseconds would spend a fifth of its time on that), where this torch
+# has the function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class _Call:
     """Checks of one call's tensors against its first one, and its launch on that one's device."""
 
-    __slots__ = ("dev", "M", "N")
+    __slots__ = ("dev", "shape", "M", "N")
 
     def __init__(self, name, t):
-        if not t.is_cuda or t.dim() != 2:
-            raise ValueError(f"{name} must be a 2-D CUDA tensor")
         self.dev = t.get_device()
-        self.M, self.N = t.shape
+        if self.dev < 0 or not t.is_cuda or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-D CUDA tensor")
+        self.shape = t.shape
+        self.M, self.N = self.shape
 
     def rows(self, name, t, dtype=None):
         """(ptr, ld) of [M, N] rows with any row stride."""
         if t is None:
             return None, self.N
-        if t.dim() != 2 or t.get_device() != self.dev or t.shape[0] != self.M or t.shape[1] != self.N:
+        if t.shape != self.shape or t.get_device() != self.dev:
             raise ValueError(f"{name} must be a [{self.M}, {self.N}] CUDA tensor on device {self.dev}")
         ld, col = t.stride()
         if col != 1 and self.N > 1:
@@ -79,24 +87,24 @@ class _Call:
     def vec(self, name, t, n, dtype):
         if t is None:
             return None
-        if t.dim() != 1 or t.get_device() != self.dev or t.shape[0] != n or t.dtype != dtype or not t.is_contiguous():
+        if t.shape != (n,) or t.get_device() != self.dev or t.dtype != dtype or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous 1-D CUDA {dtype} tensor of {n} elements on device {self.dev}")
         return t.data_ptr()
 
     def params(self, gamma, beta, default):
         """(gamma ptr, beta ptr, dtype code)."""
         pdt = gamma.dtype if gamma is not None else beta.dtype if beta is not None else default
-        if pdt not in DTYPE_CODE:
+        code = DTYPE_CODE.get(pdt)
+        if code is None:
             raise ValueError(f"gamma and beta cannot have dtype {pdt}")
-        return self.vec("gamma", gamma, self.N, pdt), self.vec("beta", beta, self.N, pdt), DTYPE_CODE[pdt]
+        return self.vec("gamma", gamma, self.N, pdt), self.vec("beta", beta, self.N, pdt), code
 
     def scales(self, name, t, group):
         """(ptr, row stride, group stride) of [M, G] scales in either order."""
         G = _groups(self.N, group)
-        if t.dim() != 2 or t.get_device() != self.dev or t.shape[0] != self.M or t.shape[1] != G \
-                or t.dtype != torch.float32:
+        if t.shape != (self.M, G) or t.get_device() != self.dev or t.dtype != torch.float32:
             raise ValueError(f"{name} must be a [{self.M}, {G}] float32 CUDA tensor on device {self.dev}")
-        return t.data_ptr(), t.stride(0), t.stride(1)
+        return t.data_ptr(), *t.stride()
 
     def checkpoint(self, ck):
         """The five checkpoint arguments."""
@@ -107,7 +115,7 @@ class _Call:
             raise ValueError(f"checkpoint group must be one of {GROUPS}")
         pc, ldc = self.rows("checkpoint codes", codes, torch.int8)
         G = _groups(self.N, group)
-        if tuple(scales.shape) != (self.M, G, 2) or scales.dtype != torch.float32 or scales.get_device() != self.dev \
+        if scales.shape != (self.M, G, 2) or scales.dtype != torch.float32 or scales.get_device() != self.dev \
                 or (self.M > 0 and (scales.stride(2) != 1 or (G > 1 and scales.stride(1) != 2))):
             raise ValueError(f"checkpoint scales must be [{self.M}, {G}, 2] float32 on device {self.dev}, "
                              "each row contiguous")
@@ -121,15 +129,16 @@ class _Call:
                 mean = torch.empty(self.M, device=self.dev, dtype=torch.float32)
         return mean, rstd, self.vec("mean", mean, self.M, torch.float32), self.vec("rstd", rstd, self.M, torch.float32)
 
+    def on_device(self, fn, *args):
+        """fn(*args) with the tensors' device current."""
+        if self.dev == torch.cuda.current_device():
+            return fn(*args)
+        with torch.cuda.device(self.dev):
+            return fn(*args)
+
     def go(self, name, fn, args, stream):
         """fn(*args, stream) with the tensors' device current."""
-        if self.dev == torch.cuda.current_device():
-            s = torch.cuda.current_stream() if stream is None else stream
-            _check(name, fn(*args, s.cuda_stream))
-        else:
-            with torch.cuda.device(self.dev):
-                s = torch.cuda.current_stream() if stream is None else stream
-                _check(name, fn(*args, s.cuda_stream))
+        _check(name, self.on_device(fn, *args, _raw_stream(self.dev) if stream is None else stream.cuda_stream))
 
 
 def _float_code(name, dtype):
@@ -224,8 +233,7 @@ def norm_bwd_ck8(is_layernorm: bool, dy, checkpoint: Checkpoint8, gamma, mean, r
         raise ValueError("rstd (and mean for LayerNorm) of the forward are needed")
     pg, _, pdt = c.params(gamma, None, dy.dtype)
     if workspace is None:
-        with torch.cuda.device(c.dev):
-            need = lib.norm_bwd_ck8_workspace_size(int(bool(is_layernorm)), c.M, c.N)
+        need = c.on_device(lib.norm_bwd_ck8_workspace_size, int(bool(is_layernorm)), c.M, c.N)
         if need == 0:
             raise GbnormError("norm_bwd_ck8_workspace_size", 2)
         workspace = torch.empty(need, device=dy.device, dtype=torch.uint8)
