@@ -1,10 +1,13 @@
-// Vector kernels that read 8-bit rows back: [format][norm][type of y].
+// Vector kernels that read 8-bit rows back: [format][norm][scale and mid as
+// pairs][type of y].
 #include "q8_read_kernels.cuh"
 
 namespace gbn {
-#define GBN_READ(F, NRM) \
-    {(const void *)&q8_read_vec<F, NRM, kF32>, (const void *)&q8_read_vec<F, NRM, kF16>, (const void *)&q8_read_vec<F, NRM, kBF16>}
-const void *const kQ8Read[2][2][3] = {{GBN_READ(kE4M3, false), GBN_READ(kE4M3, true)},
-                                      {GBN_READ(kI8, false), GBN_READ(kI8, true)}};
+#define GBN_READ(F, NRM, PR)                                                                             \
+    {(const void *)&q8_read_vec<F, NRM, PR, kF32>, (const void *)&q8_read_vec<F, NRM, PR, kF16>, \
+     (const void *)&q8_read_vec<F, NRM, PR, kBF16>}
+#define GBN_READ2(F) \
+    {{GBN_READ(F, false, false), GBN_READ(F, false, true)}, {GBN_READ(F, true, false), GBN_READ(F, true, true)}}
+const void *const kQ8Read[2][2][2][3] = {GBN_READ2(kE4M3), GBN_READ2(kI8)};
 const int kQ8ReadCTA = kReadCTA, kQ8ReadRows = kReadRows;
 }  // namespace gbn

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
                 prefetch_l2_inner(p.c + next * p.ldc + j0, (int)(n - j0));
             }
         }
-        float sum[2] = {0.f, 0.f};
+        float sum[LN ? 2 : 1] = {};
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
             float g[8];
@@ -312,11 +312,11 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
             for (int i = 0; i < 8; ++i) {
                 const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
                 sum[0] = fmaf(dg, xh[k][i], sum[0]);
-                if constexpr (LN) sum[1] += dg;
+                if constexpr (LN) sum[LN ? 1 : 0] += dg;
             }
         }
         group_sums<TPR, CL, LN ? 2 : 1>(sum, rr);
-        const float nrc2 = -rstd * (sum[0] * inv_n), nrc1 = LN ? -rstd * (sum[1] * inv_n) : 0.f;
+        const float nrc2 = -rstd * (sum[0] * inv_n), nrc1 = LN ? -rstd * (sum[LN ? 1 : 0] * inv_n) : 0.f;
         void *dxr = row_ptr(p.dx, row, p.lddx, p.xdt);
         const void *drr = p.dres ? row_ptr(p.dres, row, p.lddres, p.xdt) : nullptr;
 #pragma unroll

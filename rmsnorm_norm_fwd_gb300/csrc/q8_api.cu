@@ -394,9 +394,10 @@ int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int 
         int64_t gy = grid_of(units * gx, 8, d) / gx;
         gy = gy < 1 ? 1 : gy > 65535 ? 65535 : gy;
         const bool norm = mean || rstd || gamma || beta;
+        const bool pair = mid == scale + 1 && s_row % 2 == 0 && s_group % 2 == 0 && aligned(scale, 8);
         void *args[2] = {&p, &tx};
         t_last[2] = "vec";
-        if (cudaLaunchKernel(kQ8Read[q_format][norm][y_dtype], dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)(tx * ry)),
+        if (cudaLaunchKernel(kQ8Read[q_format][norm][pair][y_dtype], dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)(tx * ry)),
                              args, 0, stream) != cudaSuccess)
             return GBNORM_ERR_CUDA;
         return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;

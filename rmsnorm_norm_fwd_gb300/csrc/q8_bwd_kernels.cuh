@@ -36,28 +36,48 @@ __device__ __forceinline__ uint2 ld_codes8(const uint8_t *row, int c) {
     return v;
 }
 
-// NS sums over a row group; the same bits on every thread.
-template <int TPR, int CL, int NS>
-__device__ __forceinline__ void group_sums(float (&v)[2], RowReduce<TPR, CL> &rr) {
-    auto steps = [&](int from) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            if (o <= from)
-#pragma unroll
-                for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+// NV (1, 2, 4) sums over a row group; the same bits on every thread.  Partner
+// lanes trade values first, so that each lane goes on with one of them (value
+// lane mod NV): 6 shuffles for four sums over a warp instead of 20.
+template <int TPR, int CL, int NV>
+__device__ __forceinline__ void group_sums(float (&v)[NV], RowReduce<TPR, CL> &rr) {
+    static_assert(NV == 1 || NV == 2 || NV == 4, "values");
+    const int lane = threadIdx.x & 31;
+    auto trade = [&](float even, float odd, int o) {
+        const bool b = lane & o;
+        return (b ? odd : even) + __shfl_xor_sync(0xffffffffu, b ? even : odd, o);
     };
-    auto take = [&](float4 b) {
-        v[0] = b.x;
-        if constexpr (NS > 1) v[1] = b.y;
-    };
-    steps(16);
+    float r = v[0];
+    if constexpr (NV == 2) r = trade(v[0], v[1], 1);
+    if constexpr (NV == 4) r = trade(trade(v[0], v[1], 1), trade(v[2], v[3], 1), 2);
+#pragma unroll
+    for (int o = NV; o < 32; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if constexpr (TPR > 32) {
-        take(rr.warps(make_float4(v[0], NS > 1 ? v[1] : 0.f, 0.f, 0.f)));
-        steps(pow2_at_least(TPR / 32) / 2);
+        constexpr int WPR = TPR / 32, MOST = 32 / NV, L = pow2_at_least(WPR), AT_ONCE = L < MOST ? L : MOST;
+        float *buf = reinterpret_cast<float *>(rr.scratch + rr.parity * WPR);
+        if (lane < NV) buf[((threadIdx.x % TPR) >> 5) * NV + lane] = r;
+        named_sync(rr.bar_id, TPR);
+        r = 0.f;
+#pragma unroll
+        for (int w0 = 0; w0 < WPR; w0 += AT_ONCE) {
+            const int w = w0 + ((lane / NV) & (AT_ONCE - 1));
+            if (w < WPR) r += buf[w * NV + (lane & (NV - 1))];
+        }
+#pragma unroll
+        for (int o = NV; o < NV * AT_ONCE; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        if constexpr (CL == 1) rr.parity ^= 1;
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = NV == 1 ? r : __shfl_sync(0xffffffffu, r, i);
     if constexpr (CL > 1) {
-        take(rr.ctas(make_float4(v[0], NS > 1 ? v[1] : 0.f, 0.f, 0.f)));
-        steps(CL / 2);
+        float4 b = rr.ctas(make_float4(v[0], NV > 1 ? v[1] : 0.f, NV > 2 ? v[2] : 0.f, NV > 2 ? v[3] : 0.f));
+        float *f = &b.x;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int o = CL / 2; o > 0; o >>= 1) f[i] += __shfl_xor_sync(0xffffffffu, f[i], o);
+            v[i] = f[i];
+        }
     }
 }
 
@@ -97,13 +117,14 @@ __device__ __forceinline__ const void *at_chunk(const void *row, int c, int dt) 
     return static_cast<const unsigned char *>(row) + (int64_t)c * 8 * esize(dt);
 }
 
-// XT: storage type of dy, dres and dx, or -1 for any combination.
-template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int CL>
+// XT: storage type of dy, dres and dx, or -1 for any combination.  R: rows a
+// row group works on at a time (their sums share one barrier).
+template <bool LN, int XT, int TPR, int VPT, int R, int NT, int MINB, int CL>
 __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
     static_assert(NT % TPR == 0 && TPR % 32 == 0, "row groups");
     static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
-    constexpr int RPC = NT / TPR;
+    constexpr int RPC = NT / TPR, NS = LN ? 2 : 1;
     static_assert(CL == 1 || RPC == 1, "a cluster shares one row");
     extern __shared__ __align__(16) float4 q8_par[];  // own gamma, then the row groups' column sums
     __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
@@ -128,28 +149,37 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
         }
     bool first = true;
     const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
-    for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
-        const void *dyr = at_chunk(row_ptr(p.dy, row, p.lddy, ydt), c0, ydt);
-        const uint8_t *cr = p.c + row * p.ldc + 8 * c0;
-        const float *cs = p.cs + row * p.ldcs;
-        Row8<XT> dy[VPT];
-        uint2 code[VPT];
-        float2 ab[VPT];  // (scale, mid), then xhat = code * a + b
+    for (int64_t row0 = (int64_t)(blockIdx.x / CL) * RPC + grp; row0 < p.M; row0 += R * stride) {
+        Row8<XT> dy[R][VPT];
+        uint2 code[R][VPT];
+        float2 ab[R][VPT];  // (scale, mid), then xhat = code * a + b
+        float rstd[R], mean[R];
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            dy[k].zero();
-            code[k] = make_uint2(0, 0);
-            ab[k] = make_float2(0.f, 0.f);
-            if (has(k)) {
-                dy[k].load(dyr, k * TPR + t, ydt);
-                code[k] = ld_codes8(cr, k * TPR + t);
-                ab[k] = __ldg(reinterpret_cast<const float2 *>(cs) + ((c0 + k * TPR + t) >> clg));
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = row0 + r * stride;
+            const bool ok = R == 1 || row < p.M;
+            rstd[r] = mean[r] = 0.f;
+            if (ok) {
+                rstd[r] = __ldg(p.rstd + row);
+                if constexpr (LN) mean[r] = __ldg(p.mean + row);
+            }
+            const void *dyr = at_chunk(row_ptr(p.dy, row, p.lddy, ydt), c0, ydt);
+            const uint8_t *cr = p.c + row * p.ldc + 8 * c0;
+            const float2 *cs = reinterpret_cast<const float2 *>(p.cs + row * p.ldcs);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                dy[r][k].zero();
+                code[r][k] = make_uint2(0, 0);
+                ab[r][k] = make_float2(0.f, 0.f);
+                if (ok && has(k)) {
+                    dy[r][k].load(dyr, k * TPR + t, ydt);
+                    code[r][k] = ld_codes8(cr, k * TPR + t);
+                    ab[r][k] = __ldg(cs + ((c0 + k * TPR + t) >> clg));
+                }
             }
         }
-        const float rstd = __ldg(p.rstd + row);
-        const float mean = LN ? __ldg(p.mean + row) : 0.f;
-        if (t == 0) {
-            const int64_t next = row + stride;
+        if (t < R) {
+            const int64_t next = row0 + (R + t) * stride;
             if (next < p.M && nc > 0) {
                 prefetch_l2(at_chunk(row_ptr(p.dy, next, p.lddy, ydt), c0, ydt), nc * 8 * esize(ydt));
                 prefetch_l2_inner(p.c + next * p.ldc + 8 * c0, nc * 8);
@@ -158,7 +188,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
                     prefetch_l2(at_chunk(row_ptr(p.dres, next, p.lddres, xdt), c0, xdt), nc * 8 * esize(xdt));
             }
         }
-        if (first) {  // behind the first row's loads
+        if (first) {  // behind the first rows' loads
             first = false;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
@@ -169,53 +199,68 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_rows(const Q8BwdParams p) {
             }
         }
         // g and xhat of chunk k
-        auto values = [&](int k, float2 (&d)[4], float2 (&g)[4], float2 (&xh)[4]) {
-            const float4 a = gp[2 * k * NT], b = gp[(2 * k + 1) * NT];
-            dy[k].get(d);
-            i8_pairs(code[k], xh);
+        auto values = [&](int r, int k, const float4 &a, const float4 &b, float2 (&d)[4], float2 (&g)[4], float2 (&xh)[4]) {
+            dy[r][k].get(d);
+            i8_pairs(code[r][k], xh);
             g[0] = f2mul(d[0], make_float2(a.x, a.y)), g[1] = f2mul(d[1], make_float2(a.z, a.w));
             g[2] = f2mul(d[2], make_float2(b.x, b.y)), g[3] = f2mul(d[3], make_float2(b.z, b.w));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xh[i] = f2fma(xh[i], f2s(ab[k].x), f2s(ab[k].y));
+            for (int i = 0; i < 4; ++i) xh[i] = f2fma(xh[i], f2s(ab[r][k].x), f2s(ab[r][k].y));
         };
-        float2 s2 = f2s(0.f), s1 = f2s(0.f);
+        float2 s2[R], s1[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s2[r] = s1[r] = f2s(0.f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            ab[k] = make_float2(ab[k].x * rstd, (ab[k].y - mean) * rstd);
-            float2 d[4], g[4], xh[4];
-            values(k, d, g, xh);
+            const float4 ga = gp[2 * k * NT], gb = gp[(2 * k + 1) * NT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s2 = f2fma(g[i], xh[i], s2);
-                if constexpr (LN) s1 = f2add(s1, g[i]);
+            for (int r = 0; r < R; ++r) {
+                ab[r][k] = make_float2(ab[r][k].x * rstd[r], (ab[r][k].y - mean[r]) * rstd[r]);
+                float2 d[4], g[4], xh[4];
+                values(r, k, ga, gb, d, g, xh);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s2[r] = f2fma(g[i], xh[i], s2[r]);
+                    if constexpr (LN) s1[r] = f2add(s1[r], g[i]);
+                }
             }
         }
-        float sum[2] = {s2.x + s2.y, s1.x + s1.y};
-        group_sums<TPR, CL, LN ? 2 : 1>(sum, rr);
+        float sum[R * NS];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            sum[r * NS] = s2[r].x + s2[r].y;
+            if constexpr (LN) sum[r * NS + 1] = s1[r].x + s1[r].y;
+        }
+        group_sums<TPR, CL, R * NS>(sum, rr);
         // dx = rstd (g - c1 - xhat c2) + dres
-        const float2 r2 = f2s(rstd), nrc2 = f2s(-rstd * (sum[0] * inv_n)), nrc1 = f2s(LN ? -rstd * (sum[1] * inv_n) : 0.f);
-        void *dxr = row_ptr(p.dx, row, p.lddx, xdt);
-        const void *drr = p.dres ? at_chunk(row_ptr(p.dres, row, p.lddres, xdt), c0, xdt) : nullptr;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             if (!has(k)) continue;
-            Row8<XT> dr;
-            if (drr) dr.load(drr, k * TPR + t, xdt);
-            float2 d[4], g[4], xh[4], o[4];
-            values(k, d, g, xh);
+            const float4 ga = gp[2 * k * NT], gb = gp[(2 * k + 1) * NT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[i] = f2fma(nrc2, xh[i], LN ? f2fma(r2, g[i], nrc1) : f2mul(r2, g[i]));
-                accg[k][i] = f2fma(d[i], xh[i], accg[k][i]);
-                if constexpr (LN) accb[k][i] = f2add(accb[k][i], d[i]);
-            }
-            if (drr) {
-                float2 r[4];
-                dr.get(r);
+            for (int r = 0; r < R; ++r) {
+                const int64_t row = row0 + r * stride;
+                if (R > 1 && row >= p.M) continue;
+                const float2 r2 = f2s(rstd[r]), nrc2 = f2s(-rstd[r] * (sum[r * NS] * inv_n)),
+                             nrc1 = f2s(LN ? -rstd[r] * (sum[r * NS + NS - 1] * inv_n) : 0.f);
+                Row8<XT> dr;
+                if (p.dres) dr.load(at_chunk(row_ptr(p.dres, row, p.lddres, xdt), c0, xdt), k * TPR + t, xdt);
+                float2 d[4], g[4], xh[4], o[4];
+                values(r, k, ga, gb, d, g, xh);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = f2add(o[i], r[i]);
+                for (int i = 0; i < 4; ++i) {
+                    o[i] = f2fma(nrc2, xh[i], LN ? f2fma(r2, g[i], nrc1) : f2mul(r2, g[i]));
+                    accg[k][i] = f2fma(d[i], xh[i], accg[k][i]);
+                    if constexpr (LN) accb[k][i] = f2add(accb[k][i], d[i]);
+                }
+                if (p.dres) {
+                    float2 q[4];
+                    dr.get(q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = f2add(o[i], q[i]);
+                }
+                st8p(row_ptr(p.dx, row, p.lddx, xdt), 8 * (int64_t)(c0 + k * TPR + t), xdt, o);
             }
-            st8p(dxr, 8 * (int64_t)(c0 + k * TPR + t), xdt, o);
         }
     }
 

@@ -93,9 +93,9 @@ extern const Q8Table kQ8Bwd_rms[4], kQ8Bwd_ln[4];
 extern const Q8Table kQ8Any_rms[kQ8FwdKinds + 1], kQ8Any_ln[kQ8FwdKinds + 1];
 // Partial rows of the backward are at most this many CTAs per SM.
 constexpr int kQ8BwdPerSm = 4;
-// Reading back: [format][with the norm on top][type of y]; a second kernel
+// Reading back: [format][with the norm on top][scale and mid as pairs][type of y]; a second kernel
 // argument (int) is the chunks of a row side by side in a CTA.
-extern const void *const kQ8Read[2][2][3];
+extern const void *const kQ8Read[2][2][2][3];
 extern const int kQ8ReadCTA, kQ8ReadRows;
 
 // Element-wise kernels, [is_ln].

@@ -1,9 +1,10 @@
 // q8_read_kernels.cuh -- 8-bit rows read back.
 //
 // Nothing is reduced: a thread keeps one chunk of 8 columns, with gamma and
-// beta of it in registers, and walks down the rows, four at a time so that
-// enough loads are in flight.  What bounds it: DRAM, 1 byte in and 2 (4) out an
-// element.
+// beta of it in registers, and walks down the rows, kReadRows at a time so that
+// enough loads are in flight.  With the statistics folded into the group's
+// (scale, mid) a value is one multiply-add of its code, a second one with the
+// norm on top.  What bounds it: DRAM, 1 byte in and 2 (4) out an element.
 #pragma once
 
 #include "q8_bwd_kernels.cuh"
@@ -13,9 +14,10 @@ namespace gbn {
 constexpr int kReadCTA = 256, kReadRows = 4;
 
 // blockDim.x = tx * ry threads: tx chunks of a column block (blockIdx.x), ry
-// rows side by side.  NORM: statistics, gamma or beta are given.
-template <int FMT, bool NORM, int YT>
-__global__ void __launch_bounds__(kReadCTA) q8_read_vec(const Q8ReadParams p, int tx) {
+// rows side by side.  NORM: statistics, gamma or beta are given.  PAIR: scale
+// and mid side by side, 8-byte aligned (a checkpoint).
+template <int FMT, bool NORM, bool PAIR, int YT>
+__global__ void __launch_bounds__(kReadCTA, 4) q8_read_vec(const Q8ReadParams p, int tx) {
     constexpr int yes = YT == kF32 ? 4 : 2;
     const int ry = blockDim.x / tx, r = threadIdx.x / tx;
     const int c = blockIdx.x * tx + threadIdx.x % tx;
@@ -26,21 +28,35 @@ __global__ void __launch_bounds__(kReadCTA) q8_read_vec(const Q8ReadParams p, in
         par8g(p.beta, c, p.pdt, 0.f, b8);
     }
     const int64_t group = p.qg >= 0 ? c >> (p.qg - 3) : 0;
-    const int64_t step = (int64_t)gridDim.y * ry;
-    for (int64_t row0 = (int64_t)blockIdx.y * ry + r; row0 < p.M; row0 += kReadRows * step) {
+    const int64_t rq = ry * p.ldq, rs = ry * p.s_row, ryb = ry * p.ldy * yes;  // from one of a thread's rows to the next
+    const int64_t step = (int64_t)gridDim.y * ry * kReadRows;
+    const int width = min(tx, (int)(p.N / 8) - (int)blockIdx.x * tx) * 8;
+    // kReadRows * ry consecutive rows at a time
+    for (int64_t row0 = (int64_t)blockIdx.y * ry * kReadRows + r; row0 < p.M; row0 += step) {
+        if (threadIdx.x % tx < kReadRows) {  // the next rows' codes on their way to L2
+            const int64_t next = row0 + step + (threadIdx.x % tx) * ry;
+            if (next < p.M) prefetch_l2_inner(p.q + next * p.ldq + 8 * (int64_t)blockIdx.x * tx, width);
+        }
+        const uint8_t *q = p.q + row0 * p.ldq;
+        const int64_t at0 = row0 * p.s_row + group * p.s_grp;
+        unsigned char *y = static_cast<unsigned char *>(p.y) + row0 * p.ldy * yes;
         uint2 w[kReadRows];
-        float scale[kReadRows], mid[kReadRows], mean[kReadRows], rstd[kReadRows];
+        float a[kReadRows], b[kReadRows], mean[kReadRows], rstd[kReadRows];  // a, b: scale, mid
 #pragma unroll
         for (int i = 0; i < kReadRows; ++i) {
-            const int64_t row = row0 + i * step;
+            const int64_t row = row0 + i * ry, at = at0 + i * rs;
             w[i] = make_uint2(0, 0);
-            scale[i] = mid[i] = mean[i] = 0.f;
+            a[i] = b[i] = mean[i] = 0.f;
             rstd[i] = 1.f;
             if (row < p.M) {
-                w[i] = ld_codes8(p.q + row * p.ldq, c);
-                const int64_t at = row * p.s_row + group * p.s_grp;
-                scale[i] = __ldg(p.scale + at);
-                if (p.mid) mid[i] = __ldg(p.mid + at);
+                w[i] = ld_codes8(q + i * rq, c);
+                if constexpr (PAIR) {
+                    const float2 sm = __ldg(reinterpret_cast<const float2 *>(p.scale + at));
+                    a[i] = sm.x, b[i] = sm.y;
+                } else {
+                    a[i] = __ldg(p.scale + at);
+                    if (p.mid) b[i] = __ldg(p.mid + at);
+                }
                 if constexpr (NORM) {
                     if (p.mean) mean[i] = __ldg(p.mean + row);
                     if (p.rstd) rstd[i] = __ldg(p.rstd + row);
@@ -49,9 +65,11 @@ __global__ void __launch_bounds__(kReadCTA) q8_read_vec(const Q8ReadParams p, in
         }
 #pragma unroll
         for (int i = 0; i < kReadRows; ++i) {
-            const int64_t row = row0 + i * step;
-            if (row >= p.M) break;
             float2 v[4];
+            if constexpr (NORM) {  // value = code * a + b
+                a[i] *= rstd[i];
+                b[i] = (b[i] - mean[i]) * rstd[i];
+            }
             if constexpr (FMT == kI8) {
                 i8_pairs(w[i], v);
             } else {
@@ -60,11 +78,10 @@ __global__ void __launch_bounds__(kReadCTA) q8_read_vec(const Q8ReadParams p, in
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[j] = f2fma(v[j], f2s(scale[i]), f2s(mid[i]));
-                if constexpr (NORM)
-                    v[j] = f2add(f2mul(f2mul(f2add(v[j], f2s(-mean[i])), f2s(rstd[i])), g8[j]), b8[j]);
+                v[j] = f2fma(v[j], f2s(a[i]), f2s(b[i]));
+                if constexpr (NORM) v[j] = f2fma(v[j], g8[j], b8[j]);
             }
-            st_raw8<YT>(static_cast<unsigned char *>(p.y) + row * p.ldy * yes, c, pack8<YT>(v));
+            if (row0 + i * ry < p.M) st_raw8<YT>(y + i * ryb, c, pack8<YT>(v));
         }
     }
 }

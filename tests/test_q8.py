@@ -312,7 +312,7 @@ def test_every_kernel_is_reached():
             run_backward(ln, 2, N, "bf16")
             names[1].add((ln, g.q8_last_variant(1)))
     for what, want in ((0, ("rows32x1c1", "rows256x4c1", "any32x1c1", "any512x2c8", "any1024x2c8", "elem")),
-                       (1, ("rows32x1c1", "any32x1c1", "any512x2c4", "any1024x2c8", "elem"))):
+                       (1, ("rows32x1c1r2", "rows512x4c8r1", "any32x1c1", "any512x2c4", "any1024x2c8", "elem"))):
         for ln in (False, True):
             have = {v for l, v in names[what] if l == ln}
             assert have >= set(want) - ({"rows256x4c1"} if ln and what else set()), (what, ln, have)
