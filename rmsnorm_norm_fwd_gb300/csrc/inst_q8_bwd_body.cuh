@@ -19,8 +19,8 @@ namespace gbn {
     X(256, 2, 2, 256, 2, 1, XT)    \
     X(320, 2, 1, 320, 2, 1, XT)    \
     X(512, 2, 2, 512, 1, 1, XT)    \
-    X(512, 2, 2, 512, 1, 2, XT)    \
-    X(512, 2, 2, 512, 1, 4, XT)    \
+    X(256, 2, 2, 256, 2, 4, XT)    \
+    X(256, 2, 2, 256, 2, 8, XT)    \
     X(512, 2, 2, 512, 1, 8, XT)    \
     X(512, 4, 1, 512, 1, 8, XT)
 #else
@@ -35,8 +35,10 @@ namespace gbn {
     X(256, 4, 1, 256, 2, 1, XT)    \
     X(512, 3, 1, 512, 1, 1, XT)    \
     X(512, 4, 1, 512, 1, 1, XT)    \
-    X(512, 4, 1, 512, 1, 2, XT)    \
-    X(512, 4, 1, 512, 1, 4, XT)    \
+    X(256, 3, 1, 256, 2, 4, XT)    \
+    X(256, 4, 1, 256, 2, 4, XT)    \
+    X(256, 3, 1, 256, 2, 8, XT)    \
+    X(256, 4, 1, 256, 2, 8, XT)    \
     X(512, 4, 1, 512, 1, 8, XT)
 #endif
 #define GBN_STR2(x) #x

@@ -1,6 +1,6 @@
 // inst_q8_fwd_body.cuh -- row-resident forward kernels of the 8-bit operators
 // for one storage type of the rows and one norm (the including unit defines
-// GBN_Q8_XT, GBN_Q8_LN and GBN_Q8_NAME).
+// GBN_Q8_XT, GBN_Q8_LN, GBN_Q8_PRAW and GBN_Q8_NAME).
 #include "q8_rows_kernels.cuh"
 
 namespace gbn {
@@ -9,19 +9,31 @@ namespace gbn {
 // of the launch bound (as many as registers and the parameters in shared memory
 // allow).
 #if GBN_Q8_LN
+// raw 16-bit gamma and beta leave room for a fourth CTA
+#if GBN_Q8_PRAW
+#define GBN_Q8_B4 4
+#define GBN_Q8_B2 2
+#else
+#define GBN_Q8_B4 3
+#define GBN_Q8_B2 1
+#endif
 #define GBN_Q8F_GEOMS(X) \
     X(32, 1, 256, 4, 1)     \
     X(32, 2, 256, 4, 1)     \
-    X(32, 4, 256, 3, 1)     \
-    X(64, 4, 256, 3, 1)     \
-    X(128, 4, 256, 3, 1)    \
-    X(256, 3, 256, 3, 1)    \
-    X(256, 4, 256, 3, 1)    \
-    X(768, 2, 768, 1, 1)    \
-    X(1024, 2, 1024, 1, 1) \
-    X(1024, 2, 1024, 1, 2) \
-    X(1024, 2, 1024, 1, 4) \
-    X(1024, 2, 1024, 1, 8)
+    X(32, 4, 256, GBN_Q8_B4, 1)     \
+    X(64, 4, 256, GBN_Q8_B4, 1)     \
+    X(128, 4, 256, GBN_Q8_B4, 1)    \
+    X(160, 4, 160, 5, 1)    \
+    X(256, 3, 256, GBN_Q8_B4, 1)    \
+    X(256, 4, 256, GBN_Q8_B4, 1)    \
+    X(512, 3, 512, GBN_Q8_B2, 1)    \
+    X(512, 4, 512, GBN_Q8_B2, 1)    \
+    X(256, 3, 256, GBN_Q8_B4, 4)    \
+    X(256, 4, 256, GBN_Q8_B4, 4)    \
+    X(256, 3, 256, GBN_Q8_B4, 8)    \
+    X(256, 4, 256, GBN_Q8_B4, 8)    \
+    X(512, 3, 512, GBN_Q8_B2, 8)    \
+    X(512, 4, 512, GBN_Q8_B2, 8)
 #else
 #define GBN_Q8F_GEOMS(X) \
     X(32, 1, 256, 4, 1)     \
@@ -33,16 +45,19 @@ namespace gbn {
     X(256, 4, 256, 4, 1)    \
     X(512, 3, 512, 2, 1)    \
     X(512, 4, 512, 2, 1) \
-    X(512, 4, 512, 2, 2) \
-    X(512, 4, 512, 2, 4) \
+    X(512, 3, 512, 2, 2)    \
+    X(512, 4, 512, 2, 2)    \
+    X(512, 3, 512, 2, 4)    \
+    X(512, 4, 512, 2, 4)    \
+    X(512, 3, 512, 2, 8)    \
     X(512, 4, 512, 2, 8)
 #endif
 
 #define GBN_STR2(x) #x
 #define GBN_STR(x) GBN_STR2(x)
 #define GBN_Q8F_ENTRY(TPR, VPT, NT, MINB, CL, OUT, CK)                                                                \
-    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT) "c" GBN_STR(CL), (const void *)&q8_fwd_rows<GBN_Q8_LN, GBN_Q8_XT, TPR, VPT, NT, MINB, CL, OUT, CK>, \
-     TPR, VPT, NT, CL, q8_fwd_smem(GBN_Q8_LN, VPT, NT)},
+    {"rows" GBN_STR(TPR) "x" GBN_STR(VPT) "c" GBN_STR(CL) , (const void *)&q8_fwd_rows<GBN_Q8_LN, GBN_Q8_XT, GBN_Q8_PRAW, TPR, VPT, NT, MINB, CL, OUT, CK>, \
+     TPR, VPT, NT, CL, q8_fwd_smem(GBN_Q8_LN, GBN_Q8_PRAW, VPT, NT)},
 #define GBN_Q8F_Y(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutY, true)
 #define GBN_Q8F_R(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutRow, false)
 #define GBN_Q8F_G(T, V, N, B, C) GBN_Q8F_ENTRY(T, V, N, B, C, kOutGroup, false)

@@ -13,35 +13,50 @@
 
 namespace gbn {
 
-// Elements base + 32 i + lane of a row, zero past its end at n.
-__device__ __forceinline__ void ld_block(const void *row, int64_t base, int64_t n, int dt, float (&v)[8]) {
+// Where a lane's 8 elements of a block are in every row: from element `at`, 32
+// apart, those below `rem` of 32 i there.
+struct Block {
+    int64_t at;
+    int rem;
+    bool full;  // all 256 elements there (uniform over the warp)
+    __device__ __forceinline__ bool has(int i) const { return 32 * i < rem; }
+};
+__device__ __forceinline__ Block block_at(int64_t base, int64_t n) {
     const int lane = threadIdx.x & 31;
-    const int64_t j0 = base + lane;
-    auto all = [&](auto *p) {
+    const int64_t rem = n - base - lane;
+    return Block{base + lane, (int)(rem < 0 ? 0 : rem > 256 ? 256 : rem), base + 256 <= n};
+}
+// Calls f(i) for the elements that are there.
+template <typename F> __device__ __forceinline__ void each(const Block &b, F &&f) {
+    if (b.full) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = j0 + 32 * i < n ? to_f(p[j0 + 32 * i]) : 0.f;
-    };
+        for (int i = 0; i < 8; ++i) f(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (b.has(i)) f(i);
+    }
+}
+// The block's elements of a row, zero past its end.
+__device__ __forceinline__ void ld_block(const void *row, const Block &b, int dt, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    auto all = [&](auto *p) { each(b, [&](int i) { v[i] = to_f(p[b.at + 32 * i]); }); };
     if (dt == kF32) all(static_cast<const float *>(row));
     else if (dt == kBF16) all(static_cast<const __nv_bfloat16 *>(row));
     else all(static_cast<const __half *>(row));
 }
-__device__ __forceinline__ void st_block(void *row, int64_t base, int64_t n, int dt, const float (&v)[8]) {
-    const int64_t j0 = base + (threadIdx.x & 31);
+__device__ __forceinline__ void st_block(void *row, const Block &b, int dt, const float (&v)[8]) {
     auto all = [&](auto *p) {
         using T = typename std::remove_pointer<decltype(p)>::type;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j0 + 32 * i < n) p[j0 + 32 * i] = from_f<T>(v[i]);
+        each(b, [&](int i) { p[b.at + 32 * i] = from_f<T>(v[i]); });
     };
     if (dt == kF32) all(static_cast<float *>(row));
     else if (dt == kBF16) all(static_cast<__nv_bfloat16 *>(row));
     else all(static_cast<__half *>(row));
 }
-__device__ __forceinline__ void st_bytes(uint8_t *row, int64_t base, int64_t n, const uint32_t (&v)[8]) {
-    const int64_t j0 = base + (threadIdx.x & 31);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (j0 + 32 * i < n) row[j0 + 32 * i] = (uint8_t)v[i];
+__device__ __forceinline__ void st_bytes(uint8_t *row, const Block &b, const uint32_t (&v)[8]) {
+    each(b, [&](int i) { row[b.at + 32 * i] = (uint8_t)v[i]; });
 }
 
 // Maxima over the groups of a block: m[i] joined with its 2^lg - 1 neighbours
@@ -86,17 +101,29 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
     // this CTA's part of a row: elements [j0, n)
     const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
     const int64_t n = CL == 1 ? p.N : (j0 + cols < p.N ? j0 + cols : p.N);
-    const float mine = n > j0 ? (float)(n - j0) : 0.f, inv_n = 1.f / (float)p.N;
+    const float inv_n = 1.f / (float)p.N;
     const float qmax = q8_max(p.qfmt), inv_qmax = 1.f / qmax;
     const int qlg = p.qg - 5, clg = p.cg - 5;  // log2 of a lane's elements of a group in a block
-    auto base = [&](int k) { return j0 + 256 * (int64_t)(k * WPR + warp); };
-    auto has = [&](int k, int i) { return base(k) + 32 * i + lane < n; };
+    Block blk[VB];
+#pragma unroll
+    for (int k = 0; k < VB; ++k) blk[k] = block_at(j0 + 256 * (int64_t)(k * WPR + warp), n);
+    auto base = [&](int k) { return blk[k].at - lane; };
+    auto has = [&](int k, int i) { return blk[k].has(i); };
+    RowCounts cnt;
+    if constexpr (LN) {
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < VB; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine += has(k, i) ? 1 : 0;
+        cnt = row_counts(mine, n > j0 ? (float)(n - j0) : 0.f);
+    }
     const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
     for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
         float v[VB][8];  // h, then what is stored of it: h * gamma or y
         const void *xr = row_ptr(p.x, row, p.ldx, p.xdt);
 #pragma unroll
-        for (int k = 0; k < VB; ++k) ld_block(xr, base(k), n, p.xdt, v[k]);
+        for (int k = 0; k < VB; ++k) ld_block(xr, blk[k], p.xdt, v[k]);
         if (t == 0 && n > j0) {
             const int64_t next = row + stride;
             if (next < p.M)
@@ -108,14 +135,14 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
 #pragma unroll
             for (int k = 0; k < VB; ++k) {
                 float r[8];
-                ld_block(rrow, base(k), n, p.xdt, r);
+                ld_block(rrow, blk[k], p.xdt, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] = round_to(v[k][i] + r[i], p.xdt);
             }
             if (p.h) {
                 void *hr = row_ptr(p.h, row, p.ldh, p.xdt);
 #pragma unroll
-                for (int k = 0; k < VB; ++k) st_block(hr, base(k), n, p.xdt, v[k]);
+                for (int k = 0; k < VB; ++k) st_block(hr, blk[k], p.xdt, v[k]);
             }
         }
         if constexpr (CK) {
@@ -139,7 +166,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     code[i] = i8_code(__fmul_rn(__fsub_rn(v[k][i], from_lane(g.mid, i)), from_lane(g.inv, i)));
-                st_bytes(cr, base(k), n, code);
+                st_bytes(cr, blk[k], code);
             }
         }
 
@@ -152,7 +179,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
             uint32_t code[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) code[i] = q8_code(__fmul_rn(v[k][i], inv(i)), p.qfmt);
-            st_bytes(qr, base(k), n, code);
+            st_bytes(qr, blk[k], code);
         };
         auto put_groups = [&]() {
 #pragma unroll
@@ -168,21 +195,20 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
         if constexpr (LN) {
             // one pass about the thread's first element, as the vector kernels
             const float ref = v[0][0];
-            float s = 0.f, q = 0.f, cnt = 0.f;
+            float s = 0.f, q = 0.f;
 #pragma unroll
             for (int k = 0; k < VB; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (has(k, i)) {
                         const float d = v[k][i] - ref;
-                        cnt += 1.f;
                         s += d;
                         q = fmaf(d, d, q);
                     }
-            const float dm = cnt > 0.f ? s / cnt : 0.f;
+            const float dm = s * cnt.inv_thread;
             mean = ref + dm;
             acc = fmax_nan(q - s * dm, 0.f);
-            group_meanvar<TPR, CL, false>(mean, acc, cnt, mine, inv_n, rr);
+            group_meanvar<TPR, CL>(mean, acc, cnt, inv_n, rr);
         } else {
 #pragma unroll
             for (int k = 0; k < VB; ++k) {
@@ -191,7 +217,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
                 if constexpr (RQ) {
                     if (p.gamma) {
                         float g[8];
-                        ld_block(p.gamma, base(k), n, p.pdt, g);
+                        ld_block(p.gamma, blk[k], p.pdt, g);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[k][i] *= g[i];
                     }
@@ -216,17 +242,17 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] = has(k, i) ? (v[k][i] - mean) * rstd : 0.f;
                 if (p.gamma) {
-                    ld_block(p.gamma, base(k), n, p.pdt, g);
+                    ld_block(p.gamma, blk[k], p.pdt, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[k][i] *= g[i];
                 }
                 if (LN && p.beta) {
-                    ld_block(p.beta, base(k), n, p.pdt, g);
+                    ld_block(p.beta, blk[k], p.pdt, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[k][i] += g[i];
                 }
                 if constexpr (OUT == kOutY) {
-                    st_block(row_ptr(p.y, row, p.ldy, p.ydt), base(k), n, p.ydt, v[k]);
+                    st_block(row_ptr(p.y, row, p.ldy, p.ydt), blk[k], p.ydt, v[k]);
                 } else if constexpr (OUT == kOutRow) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(v[k][i]));
@@ -260,12 +286,14 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
     extern __shared__ __align__(16) float q8_sums[];  // RPC > 1: the row groups' column sums, [VB][8][NT]
     __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
     if constexpr (CL > 1) cluster_sync_all();
-    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = t >> 5;
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, warp = t >> 5;
     RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
     const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
     const int64_t n = CL == 1 ? p.N : (j0 + cols < p.N ? j0 + cols : p.N);
     const float inv_n = 1.f / (float)p.N;
-    auto base = [&](int k) { return j0 + 256 * (int64_t)(k * WPR + warp); };
+    Block blk[VB];
+#pragma unroll
+    for (int k = 0; k < VB; ++k) blk[k] = block_at(j0 + 256 * (int64_t)(k * WPR + warp), n);
     float accg[VB][8], accb[LN ? VB : 1][8];
 #pragma unroll
     for (int k = 0; k < VB; ++k)
@@ -284,16 +312,21 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
         float d[VB][8], xh[VB][8];
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
-            ld_block(dyr, base(k), n, p.ydt, d[k]);
+            ld_block(dyr, blk[k], p.ydt, d[k]);
+            int code[8];
+            float2 sm[8];  // (scale, mid)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int64_t j = base(k) + 32 * i + lane;
-                xh[k][i] = 0.f;
-                if (j < n) {
-                    const float *g = cs + 2 * (j >> p.cg);
-                    xh[k][i] = fmaf((float)(int8_t)cr[j], __ldg(g) * rstd, (__ldg(g + 1) - mean) * rstd);
-                }
+                code[i] = 0;
+                sm[i] = make_float2(0.f, mean);
             }
+            each(blk[k], [&](int i) {
+                const int64_t j = blk[k].at + 32 * i;
+                code[i] = (int8_t)cr[j];
+                sm[i] = __ldg(reinterpret_cast<const float2 *>(cs) + (j >> p.cg));
+            });
+#pragma unroll
+            for (int i = 0; i < 8; ++i) xh[k][i] = fmaf((float)code[i], sm[i].x * rstd, (sm[i].y - mean) * rstd);
         }
         if (t == 0 && n > j0) {
             const int64_t next = row + stride;
@@ -307,7 +340,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
             float g[8];
-            if (p.gamma) ld_block(p.gamma, base(k), n, p.pdt, g);
+            if (p.gamma) ld_block(p.gamma, blk[k], p.pdt, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
@@ -322,7 +355,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
             float g[8], o[8];
-            if (p.gamma) ld_block(p.gamma, base(k), n, p.pdt, g);
+            if (p.gamma) ld_block(p.gamma, blk[k], p.pdt, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
@@ -332,11 +365,11 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
             }
             if (drr) {
                 float r[8];
-                ld_block(drr, base(k), n, p.xdt, r);
+                ld_block(drr, blk[k], p.xdt, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] += r[i];
             }
-            st_block(dxr, base(k), n, p.xdt, o);
+            st_block(dxr, blk[k], p.xdt, o);
         }
     }
     // this CTA's (cluster's) partial row; several row groups are added in group order
@@ -359,7 +392,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < VB; ++k) st_block(ws, base(k), n, kF32, acc[k]);
+            for (int k = 0; k < VB; ++k) st_block(ws, blk[k], kF32, acc[k]);
         }
     };
     const int64_t P = gridDim.x / CL, part = blockIdx.x / CL;

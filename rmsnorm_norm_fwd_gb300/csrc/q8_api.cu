@@ -104,7 +104,7 @@ int64_t grid_of(int64_t units, int64_t per_sm, const HostDevice &d) {
 
 // Kernels with rows in registers: how many row groups (CTAs, or clusters) run
 // at once on the device, measured once per device and slot.
-constexpr int kBwdSlots = 2 * 3 * kQ8FwdKinds * kQ8MaxVariants, kAnySlots = kBwdSlots + 2 * 4 * kQ8MaxVariants,
+constexpr int kBwdSlots = 3 * 3 * kQ8FwdKinds * kQ8MaxVariants, kAnySlots = kBwdSlots + 2 * 4 * kQ8MaxVariants,
               kSlots = kAnySlots + 2 * (kQ8FwdKinds + 1) * kQ8MaxVariants;
 std::atomic<int> g_resident[kHostMaxDev][kSlots];
 
@@ -230,13 +230,16 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
     const bool vec = N % 8 == 0 && vec_rows(p.x, p.ldx, xs) && vec_rows(p.res, p.ldr, xs) && vec_rows(p.h, p.ldh, xs) &&
                      vec_rows(p.y, p.ldy, elem_size(p.ydt)) && aligned(p.gamma, 16) && aligned(p.beta, 16) &&
                      aligned(p.q, 8) && p.ldq % 8 == 0 && aligned(p.c, 8) && p.ldc % 8 == 0;
-    static const Q8Table *const tables[2][3] = {{kQ8Fwd_rms_f32, kQ8Fwd_rms_f16, kQ8Fwd_rms_bf16},
-                                                {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16, kQ8Fwd_ln_bf16}};
+    // rows: RMSNorm, LayerNorm, LayerNorm with gamma and beta of the rows' type
+    static const Q8Table *const tables[3][3] = {{kQ8Fwd_rms_f32, kQ8Fwd_rms_f16, kQ8Fwd_rms_bf16},
+                                                {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16, kQ8Fwd_ln_bf16},
+                                                {kQ8Fwd_ln_f32, kQ8Fwd_ln_f16_raw, kQ8Fwd_ln_bf16_raw}};
+    const int op = a.is_ln && p.pdt == p.xdt ? 2 : a.is_ln;
     const int kind = p.y ? 0 : (p.qg < 0 ? 1 : 2) + (p.c ? 2 : 0);
-    const Q8Table &t = vec ? tables[a.is_ln][p.xdt][kind] : (a.is_ln ? kQ8Any_ln : kQ8Any_rms)[kind];
+    const Q8Table &t = vec ? tables[op][p.xdt][kind] : (a.is_ln ? kQ8Any_ln : kQ8Any_rms)[kind];
     const int i = find_rows(t, N);
     if (i >= 0) {
-        const int slot = (vec ? ((p.xdt * 2 + a.is_ln) * kQ8FwdKinds + kind) * kQ8MaxVariants
+        const int slot = (vec ? ((p.xdt * 3 + op) * kQ8FwdKinds + kind) * kQ8MaxVariants
                               : kAnySlots + (a.is_ln * (kQ8FwdKinds + 1) + kind) * kQ8MaxVariants) + i;
         int64_t units;
         t_last[0] = t.v[i].name;

@@ -86,6 +86,8 @@ constexpr int kQ8MaxVariants = 24;  // entries per table
 constexpr int kQ8FwdKinds = 5;
 extern const Q8Table kQ8Fwd_rms_f32[kQ8FwdKinds], kQ8Fwd_rms_f16[kQ8FwdKinds], kQ8Fwd_rms_bf16[kQ8FwdKinds];
 extern const Q8Table kQ8Fwd_ln_f32[kQ8FwdKinds], kQ8Fwd_ln_f16[kQ8FwdKinds], kQ8Fwd_ln_bf16[kQ8FwdKinds];
+// LayerNorm with 16-bit gamma and beta of the rows' type, kept so in shared memory.
+extern const Q8Table kQ8Fwd_ln_f16_raw[kQ8FwdKinds], kQ8Fwd_ln_bf16_raw[kQ8FwdKinds];
 
 // Backward: dy, dres and dx all fp32, fp16, bf16; any combination.
 extern const Q8Table kQ8Bwd_rms[4], kQ8Bwd_ln[4];

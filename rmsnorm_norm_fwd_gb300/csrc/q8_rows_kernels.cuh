@@ -207,22 +207,31 @@ __device__ __forceinline__ void group_sum_max(float &s, float &m, RowReduce<TPR,
     }
 }
 
-// Mean and sum of squared deviations of a row from its threads' own, of `cnt`
-// elements each (the update of Chan, Golub and LeVeque in its group form: over
-// a warp's lanes, the warps, the CTAs).  EQUAL: every thread has cnt, known at
-// compile time.  cta_cnt: elements of this CTA's part of the row; inv_n: 1 / N.
-template <int TPR, int CL, bool EQUAL>
-__device__ __forceinline__ void group_meanvar(float &mean, float &m2, float cnt, float cta_cnt, float inv_n,
-                                              RowReduce<TPR, CL> &rr) {
-    float s = EQUAL ? mean : mean * cnt, c = cnt;
+// Elements that a thread, its warp and its CTA hold of a row: the same for every
+// row, so taken once.
+struct RowCounts {
+    float thread, inv_thread, warp, inv_warp, cta, inv_cta;
+};
+__device__ __forceinline__ float inv_or_0(float c) { return c > 0.f ? 1.f / c : 0.f; }
+__device__ __forceinline__ RowCounts row_counts(int thread, float cta) {
+    float w = (float)thread;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        if constexpr (!EQUAL) c += __shfl_xor_sync(0xffffffffu, c, o);
-    }
-    const float mw = EQUAL ? s * (1.f / 32) : c > 0.f ? s / c : 0.f;
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    return RowCounts{(float)thread, inv_or_0((float)thread), w, inv_or_0(w), cta, inv_or_0(cta)};
+}
+
+// Mean and sum of squared deviations of a row from its threads' own (the
+// update of Chan, Golub and LeVeque in its group form: over a warp's lanes, the
+// warps, the CTAs).  inv_n: 1 / N.
+template <int TPR, int CL>
+__device__ __forceinline__ void group_meanvar(float &mean, float &m2, const RowCounts &cnt, float inv_n,
+                                              RowReduce<TPR, CL> &rr) {
+    float s = mean * cnt.thread;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float mw = s * cnt.inv_warp;
     const float d = mean - mw;
-    float q = EQUAL || cnt > 0.f ? m2 + cnt * (d * d) : 0.f;
+    float q = cnt.thread > 0.f ? m2 + cnt.thread * (d * d) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
     mean = mw;
@@ -241,9 +250,8 @@ __device__ __forceinline__ void group_meanvar(float &mean, float &m2, float cnt,
             if (o < L) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
     };
     if constexpr (TPR > 32)
-        join(rr.warps(make_float4(mean, m2, EQUAL ? cnt * 32.f : c, 0.f)), pow2_at_least(TPR / 32),
-             CL == 1 ? inv_n : cta_cnt > 0.f ? 1.f / cta_cnt : 0.f);
-    if constexpr (CL > 1) join(rr.ctas(make_float4(mean, m2, cta_cnt, 0.f)), CL, inv_n);
+        join(rr.warps(make_float4(mean, m2, cnt.warp, 0.f)), pow2_at_least(TPR / 32), CL == 1 ? inv_n : cnt.inv_cta);
+    if constexpr (CL > 1) join(rr.ctas(make_float4(mean, m2, cnt.cta, 0.f)), CL, inv_n);
 }
 
 // h = x + r rounded once to the storage type.
@@ -355,8 +363,11 @@ __device__ __forceinline__ void range_of_own(const Raw8<XT> (&h)[VPT], Has &&has
 
 constexpr int kOutY = 0, kOutRow = 1, kOutGroup = 2;  // y in ydt; 8-bit rows with a scale per row; per group
 
-// Bytes of shared memory for the threads' own parameters.
-__host__ __device__ constexpr int q8_fwd_smem(bool ln, int vpt, int nt) { return nt * vpt * 32 * (ln ? 2 : 1); }
+// Bytes of shared memory for the threads' own parameters: as fp32, or (PRAW)
+// in the rows' own 16-bit type.
+__host__ __device__ constexpr int q8_fwd_smem(bool ln, bool praw, int vpt, int nt) {
+    return nt * vpt * (praw ? 16 : 32) * (ln ? 2 : 1);
+}
 
 // Chunks of a row of nc that each of CL CTAs holds: a multiple of a warp's
 // lanes, so that groups stay inside a warp.
@@ -366,7 +377,7 @@ template <int CL> __device__ __forceinline__ int cta_slice(int nc) {
 
 // FULL: every thread holds VPT chunks.  CL > 1: a row is split over the CTAs
 // of a cluster.
-template <bool LN, int XT, int TPR, int VPT, int NT, int CL, int OUT, bool CK, bool FULL>
+template <bool LN, int XT, bool PRAW, int TPR, int VPT, int NT, int CL, int OUT, bool CK, bool FULL>
 __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, float4 *scratch_all) {
     constexpr int RPC = NT / TPR;
     static_assert(CL == 1 || RPC == 1, "a cluster shares one row");
@@ -382,12 +393,34 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
     const int qlg = p.qg - 3, clg = p.cg - 3;  // log2 of the lanes of a group
     const int own = own_chunk<VPT>(lane);
     auto has = [&](int k) { return FULL || k * TPR + t < nc; };
-    float4 *gp = par + threadIdx.x, *bp = par + 2 * VPT * NT + threadIdx.x;
+    constexpr int PW = PRAW ? 1 : 2;  // 16-byte words of a parameter chunk
+    float4 *gp = par + threadIdx.x, *bp = par + PW * VPT * NT + threadIdx.x;
     auto param = [&](const float4 *q, int k, float2 (&f)[4]) {
-        const float4 a = q[2 * k * NT], b = q[(2 * k + 1) * NT];
-        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
-        f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+        if constexpr (PRAW) {
+            Raw8<XT> r;
+            r.v[0] = *reinterpret_cast<const uint4 *>(q + k * NT);
+            unpack8<XT>(r, f);
+        } else {
+            const float4 a = q[2 * k * NT], b = q[(2 * k + 1) * NT];
+            f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+            f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+        }
     };
+    auto keep = [&](float4 *q, int k, const float2 (&f)[4]) {
+        if constexpr (PRAW) {
+            *reinterpret_cast<uint4 *>(q + k * NT) = pack8<XT>(f).v[0];
+        } else {
+            q[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+            q[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        }
+    };
+    RowCounts cnt;
+    if constexpr (LN) {
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) mine += has(k) ? 8 : 0;
+        cnt = row_counts(mine, (float)(8 * nc));
+    }
     bool first = true;
     const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
     for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
@@ -429,12 +462,10 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             for (int k = 0; k < VPT; ++k) {
                 float2 f[4];
                 par8g(has(k) ? p.gamma : nullptr, c0 + k * TPR + t, p.pdt, 1.f, f);
-                gp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-                gp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+                keep(gp, k, f);
                 if constexpr (LN) {
                     par8g(has(k) ? p.beta : nullptr, c0 + k * TPR + t, p.pdt, 0.f, f);
-                    bp[2 * k * NT] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-                    bp[(2 * k + 1) * NT] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+                    keep(bp, k, f);
                 }
             }
         }
@@ -489,12 +520,9 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             const float ref = o[0][0].x;
             const float2 nr = f2s(-ref);
             float2 s2 = f2s(0.f), q2 = f2s(0.f);
-            float cnt = (float)(VPT * 8);
-            if constexpr (!FULL) cnt = 0.f;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 if (!has(k)) continue;
-                if constexpr (!FULL) cnt += 8.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 d = f2add(o[k][i], nr);
@@ -502,11 +530,10 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
                     q2 = f2fma(d, d, q2);
                 }
             }
-            const float s = s2.x + s2.y;
-            const float dm = FULL ? s * (1.f / (VPT * 8)) : cnt > 0.f ? s / cnt : 0.f;
+            const float s = s2.x + s2.y, dm = s * cnt.inv_thread;
             mean = ref + dm;
             acc = fmax_nan(q2.x + q2.y - s * dm, 0.f);
-            group_meanvar<TPR, CL, FULL>(mean, acc, cnt, (float)(8 * nc), inv_n, rr);
+            group_meanvar<TPR, CL>(mean, acc, cnt, inv_n, rr);
         } else {
             float2 a2 = f2s(0.f);
 #pragma unroll
@@ -532,18 +559,22 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
         }
 
         // ---------------------------------------------------------------- output
-        const float2 nm = f2s(-mean), rs = f2s(rstd);
+        // (h - mean) rstd as one multiply-add: mean is itself rounded to fp32, and
+        // the rounding of mean * rstd is of that size
+        const float2 nm = f2s(-mean * rstd), rs = f2s(rstd);
         if constexpr (!RQ) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {  // y; zeros past the row's end
-                float2 g8[4];
+                float2 g8[4], b8[4];
                 param(gp, k, g8);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[k][i] = f2mul(f2mul(LN ? f2add(o[k][i], nm) : o[k][i], rs), g8[i]);
                 if constexpr (LN) {
-                    param(bp, k, g8);
+                    param(bp, k, b8);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[k][i] = has(k) ? f2add(o[k][i], g8[i]) : f2s(0.f);
+                    for (int i = 0; i < 4; ++i)
+                        o[k][i] = has(k) ? f2fma(f2fma(o[k][i], rs, nm), g8[i], b8[i]) : f2s(0.f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[k][i] = f2mul(f2mul(o[k][i], rs), g8[i]);
                 }
                 if constexpr (OUT == kOutY) {
                     if (has(k)) st8p(row_ptr(p.y, row, p.ldy, p.ydt), 8 * (int64_t)(c0 + k * TPR + t), p.ydt, o[k]);
@@ -567,7 +598,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
     }
 }
 
-template <bool LN, int XT, int TPR, int VPT, int NT, int MINB, int CL, int OUT, bool CK>
+template <bool LN, int XT, bool PRAW, int TPR, int VPT, int NT, int MINB, int CL, int OUT, bool CK>
 __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
     static_assert(NT % TPR == 0 && TPR % 32 == 0 && VPT <= 4, "row groups");
     static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
@@ -575,9 +606,9 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_rows(const Q8FwdParams p) {
     __shared__ float4 scratch[NT / TPR * RowReduce<TPR, CL>::SCRATCH];
     if constexpr (CL > 1) cluster_sync_all();  // every CTA runs before another writes to its shared memory
     if (p.N == (int64_t)CL * TPR * VPT * 8)
-        q8_fwd_body<LN, XT, TPR, VPT, NT, CL, OUT, CK, true>(p, q8_par, scratch);
+        q8_fwd_body<LN, XT, PRAW, TPR, VPT, NT, CL, OUT, CK, true>(p, q8_par, scratch);
     else
-        q8_fwd_body<LN, XT, TPR, VPT, NT, CL, OUT, CK, false>(p, q8_par, scratch);
+        q8_fwd_body<LN, XT, PRAW, TPR, VPT, NT, CL, OUT, CK, false>(p, q8_par, scratch);
 }
 
 }  // namespace gbn
