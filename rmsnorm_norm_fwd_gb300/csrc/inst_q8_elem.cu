@@ -4,5 +4,4 @@
 namespace gbn {
 const void *const kQ8FwdElem[2] = {(const void *)&q8_fwd_elem<false>, (const void *)&q8_fwd_elem<true>};
 const void *const kQ8BwdElem[2] = {(const void *)&q8_bwd_elem<false>, (const void *)&q8_bwd_elem<true>};
-const void *const kQ8ReadElem = (const void *)&q8_read_elem;
 }  // namespace gbn

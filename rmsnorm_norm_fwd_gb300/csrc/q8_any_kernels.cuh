@@ -37,15 +37,47 @@ template <typename F> __device__ __forceinline__ void each(const Block &b, F &&f
             if (b.has(i)) f(i);
     }
 }
-// The block's elements of a row, zero past its end.
-__device__ __forceinline__ void ld_block(const void *row, const Block &b, int dt, float (&v)[8]) {
+// The block's elements of a row as stored, zero past its end: loads alone, so
+// that several blocks' are in flight before the first is waited for.
+struct RawBlock {
+    uint32_t w[8];
+};
+__device__ __forceinline__ void ld_raw_block(const void *row, const Block &b, int dt, RawBlock &r) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    auto all = [&](auto *p) { each(b, [&](int i) { v[i] = to_f(p[b.at + 32 * i]); }); };
-    if (dt == kF32) all(static_cast<const float *>(row));
-    else if (dt == kBF16) all(static_cast<const __nv_bfloat16 *>(row));
-    else all(static_cast<const __half *>(row));
+    for (int i = 0; i < 8; ++i) r.w[i] = 0;
+    if (dt == kF32) {
+        const uint32_t *p = static_cast<const uint32_t *>(row) + b.at;
+        each(b, [&](int i) { r.w[i] = p[32 * i]; });
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(row) + b.at;
+        each(b, [&](int i) { r.w[i] = p[32 * i]; });
+    }
 }
+__device__ __forceinline__ void widen_block(const RawBlock &r, int dt, float (&v)[8]) {
+    if (dt == kF32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+    } else if (dt == kBF16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __half2float(__ushort_as_half((unsigned short)r.w[i]));
+    }
+}
+__device__ __forceinline__ void ld_block(const void *row, const Block &b, int dt, float (&v)[8]) {
+    RawBlock r;
+    ld_raw_block(row, b, dt, r);
+    widen_block(r, dt, v);
+}
+// Copies what was read for the first of a group's 2^lg neighbouring elements
+// of a lane to the others.
+template <typename T> __device__ __forceinline__ void spread_groups(T (&v)[8], int lg) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        if (lg >= 3 || (i & ((1 << lg) - 1))) v[i] = v[i - 1];
+}
+__device__ __forceinline__ bool leads_group(int i, int lg) { return lg >= 3 ? i == 0 : (i & ((1 << lg) - 1)) == 0; }
 __device__ __forceinline__ void st_block(void *row, const Block &b, int dt, const float (&v)[8]) {
     auto all = [&](auto *p) {
         using T = typename std::remove_pointer<decltype(p)>::type;
@@ -57,6 +89,22 @@ __device__ __forceinline__ void st_block(void *row, const Block &b, int dt, cons
 }
 __device__ __forceinline__ void st_bytes(uint8_t *row, const Block &b, const uint32_t (&v)[8]) {
     each(b, [&](int i) { row[b.at + 32 * i] = (uint8_t)v[i]; });
+}
+
+// A thread's own parameters of a block in shared memory (as fp32; `absent` past
+// the row's end and for a null row).
+template <int NT> __device__ __forceinline__ void keep_block(float4 *own, const void *row, const Block &b, int dt, float absent) {
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = absent;
+    if (row) ld_block(row, b, dt, g);
+    own[0] = make_float4(g[0], g[1], g[2], g[3]);
+    own[NT] = make_float4(g[4], g[5], g[6], g[7]);
+}
+template <int NT> __device__ __forceinline__ void own_block(const float4 *own, float (&g)[8]) {
+    const float4 a = own[0], b = own[NT];
+    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+    g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
 }
 
 // Maxima over the groups of a block: m[i] joined with its 2^lg - 1 neighbours
@@ -94,9 +142,11 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
     static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
     constexpr int RPC = NT / TPR, WPR = TPR / 32;
     constexpr bool RQ = !LN && OUT != kOutY;  // codes of h * gamma
+    extern __shared__ __align__(16) float4 q8_par[];  // own gamma, then own beta
     __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
     if constexpr (CL > 1) cluster_sync_all();
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = t >> 5;
+    float4 *gp = q8_par + threadIdx.x, *bp = gp + 2 * VB * NT;
     RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
     // this CTA's part of a row: elements [j0, n)
     const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
@@ -118,24 +168,32 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
             for (int i = 0; i < 8; ++i) mine += has(k, i) ? 1 : 0;
         cnt = row_counts(mine, n > j0 ? (float)(n - j0) : 0.f);
     }
+    bool first = true;
     const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
     for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
         float v[VB][8];  // h, then what is stored of it: h * gamma or y
         const void *xr = row_ptr(p.x, row, p.ldx, p.xdt);
+        RawBlock xw[VB], rw[VB];
 #pragma unroll
-        for (int k = 0; k < VB; ++k) ld_block(xr, blk[k], p.xdt, v[k]);
+        for (int k = 0; k < VB; ++k) ld_raw_block(xr, blk[k], p.xdt, xw[k]);
+        if (p.res) {
+            const void *rrow = row_ptr(p.res, row, p.ldr, p.xdt);
+#pragma unroll
+            for (int k = 0; k < VB; ++k) ld_raw_block(rrow, blk[k], p.xdt, rw[k]);
+        }
         if (t == 0 && n > j0) {
             const int64_t next = row + stride;
             if (next < p.M)
                 prefetch_l2_inner(static_cast<const unsigned char *>(row_ptr(p.x, next, p.ldx, p.xdt)) + j0 * esize(p.xdt),
                                   (int)(n - j0) * esize(p.xdt));
         }
+#pragma unroll
+        for (int k = 0; k < VB; ++k) widen_block(xw[k], p.xdt, v[k]);
         if (p.res) {
-            const void *rrow = row_ptr(p.res, row, p.ldr, p.xdt);
 #pragma unroll
             for (int k = 0; k < VB; ++k) {
                 float r[8];
-                ld_block(rrow, blk[k], p.xdt, r);
+                widen_block(rw[k], p.xdt, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] = round_to(v[k][i] + r[i], p.xdt);
             }
@@ -143,6 +201,14 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
                 void *hr = row_ptr(p.h, row, p.ldh, p.xdt);
 #pragma unroll
                 for (int k = 0; k < VB; ++k) st_block(hr, blk[k], p.xdt, v[k]);
+            }
+        }
+        if (first) {  // behind the first row's loads
+            first = false;
+#pragma unroll
+            for (int k = 0; k < VB; ++k) {
+                keep_block<NT>(gp + 2 * k * NT, p.gamma, blk[k], p.pdt, 1.f);
+                if constexpr (LN) keep_block<NT>(bp + 2 * k * NT, p.beta, blk[k], p.pdt, 0.f);
             }
         }
         if constexpr (CK) {
@@ -215,14 +281,13 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc = fmaf(v[k][i], v[k][i], acc);
                 if constexpr (RQ) {
-                    if (p.gamma) {
-                        float g[8];
-                        ld_block(p.gamma, blk[k], p.pdt, g);
+                    float g[8];
+                    own_block<NT>(gp + 2 * k * NT, g);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[k][i] *= g[i];
+                    for (int i = 0; i < 8; ++i) {
+                        v[k][i] *= g[i];
+                        m = fmax_nan(m, fabsf(v[k][i]));
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(v[k][i]));
                 }
             }
             if constexpr (OUT == kOutGroup) put_groups();
@@ -239,15 +304,11 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
 #pragma unroll
             for (int k = 0; k < VB; ++k) {  // y; zeros past the row's end
                 float g[8];
+                own_block<NT>(gp + 2 * k * NT, g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[k][i] = has(k, i) ? (v[k][i] - mean) * rstd : 0.f;
-                if (p.gamma) {
-                    ld_block(p.gamma, blk[k], p.pdt, g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[k][i] *= g[i];
-                }
-                if (LN && p.beta) {
-                    ld_block(p.beta, blk[k], p.pdt, g);
+                for (int i = 0; i < 8; ++i) v[k][i] = has(k, i) ? (v[k][i] - mean) * rstd * g[i] : 0.f;
+                if constexpr (LN) {
+                    own_block<NT>(bp + 2 * k * NT, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[k][i] += g[i];
                 }
@@ -283,11 +344,12 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
     static_assert(TPR == 32 || NT / TPR < 16, "named barriers");
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
     constexpr int RPC = NT / TPR, WPR = TPR / 32;
-    extern __shared__ __align__(16) float q8_sums[];  // RPC > 1: the row groups' column sums, [VB][8][NT]
+    extern __shared__ __align__(16) float4 q8_par[];  // own gamma, then the row groups' column sums, [VB][8][NT]
     __shared__ float4 scratch_all[RPC * RowReduce<TPR, CL>::SCRATCH];
     if constexpr (CL > 1) cluster_sync_all();
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, warp = t >> 5;
     RowReduce<TPR, CL> rr{scratch_all + grp * RowReduce<TPR, CL>::SCRATCH, 0, 1 + grp};
+    float4 *gp = q8_par + threadIdx.x;
     const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
     const int64_t n = CL == 1 ? p.N : (j0 + cols < p.N ? j0 + cols : p.N);
     const float inv_n = 1.f / (float)p.N;
@@ -302,6 +364,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
             accg[k][i] = 0.f;
             if constexpr (LN) accb[k][i] = 0.f;
         }
+    bool first = true;
     const int64_t stride = (int64_t)(gridDim.x / CL) * RPC;
     for (int64_t row = (int64_t)(blockIdx.x / CL) * RPC + grp; row < p.M; row += stride) {
         const void *dyr = row_ptr(p.dy, row, p.lddy, p.ydt);
@@ -309,24 +372,19 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
         const float *cs = p.cs + row * p.ldcs;
         const float rstd = __ldg(p.rstd + row);
         const float mean = LN ? __ldg(p.mean + row) : 0.f;
-        float d[VB][8], xh[VB][8];
+        RawBlock dw[VB];
+        uint8_t code[VB][8];
+        float2 sm[VB][8];  // (scale, mid)
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
-            ld_block(dyr, blk[k], p.ydt, d[k]);
-            int code[8];
-            float2 sm[8];  // (scale, mid)
+            ld_raw_block(dyr, blk[k], p.ydt, dw[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                code[i] = 0;
-                sm[i] = make_float2(0.f, mean);
-            }
+            for (int i = 0; i < 8; ++i) code[k][i] = 0, sm[k][i] = make_float2(0.f, mean);
+            each(blk[k], [&](int i) { code[k][i] = cr[blk[k].at + 32 * i]; });
             each(blk[k], [&](int i) {
-                const int64_t j = blk[k].at + 32 * i;
-                code[i] = (int8_t)cr[j];
-                sm[i] = __ldg(reinterpret_cast<const float2 *>(cs) + (j >> p.cg));
+                if (leads_group(i, p.cg - 5))
+                    sm[k][i] = __ldg(reinterpret_cast<const float2 *>(cs) + ((blk[k].at + 32 * i) >> p.cg));
             });
-#pragma unroll
-            for (int i = 0; i < 8; ++i) xh[k][i] = fmaf((float)code[i], sm[i].x * rstd, (sm[i].y - mean) * rstd);
         }
         if (t == 0 && n > j0) {
             const int64_t next = row + stride;
@@ -336,14 +394,28 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
                 prefetch_l2_inner(p.c + next * p.ldc + j0, (int)(n - j0));
             }
         }
+        if (first) {  // behind the first row's loads
+            first = false;
+#pragma unroll
+            for (int k = 0; k < VB; ++k) keep_block<NT>(gp + 2 * k * NT, p.gamma, blk[k], p.pdt, 1.f);
+        }
+        float d[VB][8], xh[VB][8];
+#pragma unroll
+        for (int k = 0; k < VB; ++k) {
+            widen_block(dw[k], p.ydt, d[k]);
+            spread_groups(sm[k], p.cg - 5);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                xh[k][i] = blk[k].has(i) ? fmaf((float)(int8_t)code[k][i], sm[k][i].x * rstd, (sm[k][i].y - mean) * rstd) : 0.f;
+        }
         float sum[LN ? 2 : 1] = {};
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
             float g[8];
-            if (p.gamma) ld_block(p.gamma, blk[k], p.pdt, g);
+            own_block<NT>(gp + 2 * k * NT, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
+                const float dg = d[k][i] * g[i];
                 sum[0] = fmaf(dg, xh[k][i], sum[0]);
                 if constexpr (LN) sum[LN ? 1 : 0] += dg;
             }
@@ -355,10 +427,10 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
 #pragma unroll
         for (int k = 0; k < VB; ++k) {
             float g[8], o[8];
-            if (p.gamma) ld_block(p.gamma, blk[k], p.pdt, g);
+            own_block<NT>(gp + 2 * k * NT, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float dg = p.gamma ? d[k][i] * g[i] : d[k][i];
+                const float dg = d[k][i] * g[i];
                 o[i] = fmaf(nrc2, xh[k][i], fmaf(rstd, dg, nrc1));
                 accg[k][i] = fmaf(d[k][i], xh[k][i], accg[k][i]);
                 if constexpr (LN) accb[k][i] += d[k][i];
@@ -375,6 +447,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
     // this CTA's (cluster's) partial row; several row groups are added in group order
     auto store = [&](float (&acc)[VB][8], float *ws) {
         if constexpr (RPC > 1) {
+            float *q8_sums = reinterpret_cast<float *>(q8_par);
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < VB; ++k)
@@ -398,6 +471,65 @@ __global__ void __launch_bounds__(NT, MINB) q8_bwd_any(const Q8BwdParams p) {
     const int64_t P = gridDim.x / CL, part = blockIdx.x / CL;
     store(accg, p.ws + part * p.N);
     if constexpr (LN) store(accb, p.ws + (P + part) * p.N);
+}
+
+// 8-bit rows read back: a warp keeps one block of columns, with gamma and beta
+// of it in registers, and walks down the rows.  blockDim.x = 32 wx ry threads:
+// wx blocks of the columns (blockIdx.x), ry rows side by side.
+template <bool NORM>
+__global__ void __launch_bounds__(kElemCTA) q8_read_any(const Q8ReadParams p, int wx) {
+    constexpr int U = 2;  // rows in flight
+    const int warp = threadIdx.x >> 5, ry = blockDim.x / (32 * wx);
+    const Block b = block_at(256 * ((int64_t)blockIdx.x * wx + warp % wx), p.N);
+    if (b.at - (threadIdx.x & 31) >= p.N) return;
+    float g[8], be[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.f, be[i] = 0.f;
+    if constexpr (NORM) {
+        if (p.gamma) ld_block(p.gamma, b, p.pdt, g);
+        if (p.beta) ld_block(p.beta, b, p.pdt, be);
+    }
+    const int glg = p.qg < 0 ? 3 : p.qg - 5;  // log2 of a lane's elements of a group
+    const int64_t step = (int64_t)gridDim.y * ry;
+    for (int64_t row0 = (int64_t)blockIdx.y * ry + warp / wx; row0 < p.M; row0 += U * step) {
+        uint8_t code[U][8];
+        float a[U][8], m[U][8], mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step;
+            mean[u] = 0.f, rstd[u] = 1.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) code[u][i] = 0, a[u][i] = m[u][i] = 0.f;
+            if (row >= p.M) continue;
+            const uint8_t *q = p.q + row * p.ldq + b.at;
+            each(b, [&](int i) { code[u][i] = q[32 * i]; });
+            each(b, [&](int i) {
+                if (leads_group(i, glg)) {
+                    const int64_t at = row * p.s_row + (p.qg < 0 ? 0 : (b.at + 32 * i) >> p.qg) * p.s_grp;
+                    a[u][i] = __ldg(p.scale + at);
+                    if (p.mid) m[u][i] = __ldg(p.mid + at);
+                }
+            });
+            if constexpr (NORM) {
+                if (p.mean) mean[u] = __ldg(p.mean + row);
+                if (p.rstd) rstd[u] = __ldg(p.rstd + row);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * step;
+            if (row >= p.M) break;
+            spread_groups(a[u], glg);
+            spread_groups(m[u], glg);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = fmaf(a[u][i], q8_value(code[u][i], p.qfmt), m[u][i]);
+                if constexpr (NORM) v[i] = fmaf((v[i] - mean[u]) * rstd[u], g[i], be[i]);
+            }
+            st_block(row_ptr(p.y, row, p.ldy, p.ydt), b, p.ydt, v);
+        }
+    }
 }
 
 }  // namespace gbn

@@ -387,26 +387,24 @@ int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int 
     if (M == 0) return GBNORM_OK;
     Q8ReadParams p{static_cast<const uint8_t *>(q), scale, mid, mean, rstd, gamma, beta, y, ldq, s_row, s_group, ldy,
                    M, N, param_dtype, y_dtype, q_format, qg};
-    if (N % 8 == 0 && aligned(q, 8) && ldq % 8 == 0 && vec_rows(y, ldy, elem_size(y_dtype)) && aligned(gamma, 16) &&
-        aligned(beta, 16)) {
-        // column blocks of equal width, as many rows side by side as fit
-        const int64_t nc = N / 8, gx = (nc + kQ8ReadCTA - 1) / kQ8ReadCTA;
-        int tx = (int)((nc + gx - 1) / gx);
-        const int64_t ry = kQ8ReadCTA / tx;
-        const int64_t units = (M + ry * kQ8ReadRows - 1) / (ry * kQ8ReadRows);
-        int64_t gy = grid_of(units * gx, 8, d) / gx;
-        gy = gy < 1 ? 1 : gy > 65535 ? 65535 : gy;
-        const bool norm = mean || rstd || gamma || beta;
-        const bool pair = mid == scale + 1 && s_row % 2 == 0 && s_group % 2 == 0 && aligned(scale, 8);
-        void *args[2] = {&p, &tx};
-        t_last[2] = "vec";
-        if (cudaLaunchKernel(kQ8Read[q_format][norm][pair][y_dtype], dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)(tx * ry)),
-                             args, 0, stream) != cudaSuccess)
-            return GBNORM_ERR_CUDA;
-        return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
-    }
-    t_last[2] = "elem";
-    return launch(kQ8ReadElem, grid_of(M, 8, d), kElemCTA, 0, &p, stream);
+    const bool norm = mean || rstd || gamma || beta;
+    const bool vec = N % 8 == 0 && aligned(q, 8) && ldq % 8 == 0 && vec_rows(y, ldy, elem_size(y_dtype)) &&
+                     aligned(gamma, 16) && aligned(beta, 16);
+    // column blocks of equal width, as many rows side by side as fit
+    const int64_t nc = vec ? N / 8 : (N + 255) / 256, most = vec ? kQ8ReadCTA : kElemCTA / 32;
+    const int64_t gx = (nc + most - 1) / most;
+    int wide = (int)((nc + gx - 1) / gx);
+    const int64_t ry = most / wide, rows = ry * (vec ? kQ8ReadRows : 1);
+    int64_t gy = grid_of((M + rows - 1) / rows * gx, 8, d) / gx;
+    gy = gy < 1 ? 1 : gy > 65535 ? 65535 : gy;
+    const bool pair = mid == scale + 1 && s_row % 2 == 0 && s_group % 2 == 0 && aligned(scale, 8);
+    const void *kernel = vec ? kQ8Read[q_format][norm][pair][y_dtype] : kQ8ReadAny[norm];
+    void *args[2] = {&p, &wide};
+    t_last[2] = vec ? "vec" : "any";
+    if (cudaLaunchKernel(kernel, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)(wide * ry * (vec ? 1 : 32))), args, 0,
+                         stream) != cudaSuccess)
+        return GBNORM_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
 }
 
 int gbnorm_q8_last_variant(int what, char *buf, size_t len) {

@@ -1,7 +1,7 @@
-// q8_elem_kernels.cuh -- the 8-bit operators one element at a time: one CTA
-// per row, any row length, stride, alignment and combination of types.  They
-// read a row two to four times (from L2 after the first), so they serve what
-// the vector kernels cannot.
+// q8_elem_kernels.cuh -- forward and backward of the 8-bit operators one element
+// at a time: one CTA per row, any row length, stride, alignment and combination
+// of types.  They read a row two to four times (from L2 after the first) and
+// serve rows longer than a cluster holds.
 #pragma once
 
 #include "q8_common.cuh"
@@ -169,22 +169,6 @@ __global__ void __launch_bounds__(kElemCTA) q8_bwd_elem(const Q8BwdParams p) {
             st1(dxr, j, p.xdt, o);
             wsg[j] += dyv * xh;
             if constexpr (LN) wsb[j] += dyv;
-        }
-    }
-}
-
-__global__ void __launch_bounds__(kElemCTA) q8_read_elem(const Q8ReadParams p) {
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-        const uint8_t *qr = p.q + row * p.ldq;
-        void *yr = row_ptr(p.y, row, p.ldy, p.ydt);
-        const float mean = p.mean ? __ldg(p.mean + row) : 0.f;
-        const float rstd = p.rstd ? __ldg(p.rstd + row) : 1.f;
-        for (int64_t j = threadIdx.x; j < p.N; j += kElemCTA) {
-            const int64_t at = row * p.s_row + (p.qg >= 0 ? j >> p.qg : 0) * p.s_grp;
-            float v = fmaf(__ldg(p.scale + at), q8_value(qr[j], p.qfmt), p.mid ? __ldg(p.mid + at) : 0.f);
-            v = ((v - mean) * rstd) * (p.gamma ? ld1(p.gamma, j, p.pdt) : 1.f);
-            if (p.beta) v += ld1(p.beta, j, p.pdt);
-            st1(yr, j, p.ydt, v);
         }
     }
 }

@@ -99,10 +99,12 @@ constexpr int kQ8BwdPerSm = 4;
 // argument (int) is the chunks of a row side by side in a CTA.
 extern const void *const kQ8Read[2][2][2][3];
 extern const int kQ8ReadCTA, kQ8ReadRows;
+// Without vectors: [with the norm on top]; a second argument, the blocks of 256
+// columns side by side in a CTA.
+extern const void *const kQ8ReadAny[2];
 
 // Element-wise kernels, [is_ln].
 extern const void *const kQ8FwdElem[2];
 extern const void *const kQ8BwdElem[2];
-extern const void *const kQ8ReadElem;
 
 }  // namespace gbn
