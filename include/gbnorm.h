@@ -279,8 +279,9 @@ int norm_bwd_ex(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t 
  * statistics overlap nothing, and q8_read's y overlaps no input.  With
  * 16-byte-aligned rows of x, residual, h, y, dy, dres, dx and parameters
  * (base and stride), 8-byte-aligned 8-bit rows and N a multiple of 8, rows
- * move as vectors; anything else takes a correct element-wise path.  Status
- * codes, ownership, streams and threading as above.
+ * move as vectors; anything else takes a correct element-wise path.  A pointer
+ * that is not aligned to its elements is rejected.  Status codes, ownership,
+ * streams and threading as above.
  */
 typedef enum {
     GBNORM_E4M3 = 0, /* 4 exponent bits, 3 mantissa bits, largest value 448 */

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -50,6 +51,17 @@ Span rows(const void *p, int64_t M, int64_t N, int64_t ld, int es, bool inplace)
     return {p, p && M > 0 ? ((size_t)(M - 1) * (size_t)ld + (size_t)N) * (size_t)es : 0, ld, es, inplace};
 }
 Span flat(const void *p, int64_t n, int es) { return {p, p ? (size_t)n * (size_t)es : 0, 0, es, false}; }
+
+// Every pointer of these is aligned to its elements (NULL is).
+struct Typed {
+    const void *p;
+    int es;
+};
+bool elements_aligned(std::initializer_list<Typed> l) {
+    for (const Typed &t : l)
+        if (!aligned(t.p, (unsigned)t.es)) return false;
+    return true;
+}
 
 // 16-byte vectors for a row tensor: aligned base and row stride.
 bool vec_rows(const void *p, int64_t ld, int es) { return !p || (aligned(p, 16) && (ld * es) % 16 == 0); }
@@ -149,21 +161,24 @@ int resident(const Q8Variant &v, int slot, const HostDevice &d, int *out) {
     return GBNORM_OK;
 }
 
-// Launches variant v over M rows; *units: its CTAs (clusters).
-int launch_rows(const Q8Variant &v, int slot, int64_t M, int64_t most, const HostDevice &d, void *params,
-                cudaStream_t s, int64_t *units) {
+// CTAs (clusters) of variant v over M rows.
+int row_units(const Q8Variant &v, int slot, int64_t M, const HostDevice &d, int64_t *units) {
     int o;
     const int st = resident(v, slot, d, &o);
     if (st != GBNORM_OK) return st;
     const int64_t rpc = v.cta / v.tpr, want = (M + rpc - 1) / rpc;
-    int64_t cap = o < most ? o : most;
-    const int64_t limit = host_grid_limit() / v.cl;
-    if (host_grid_limit() > 0 && limit < cap) cap = limit > 0 ? limit : 1;
+    int64_t cap = o;
+    const int64_t limit = host_grid_limit();
+    if (limit > 0 && limit / v.cl < cap) cap = limit / v.cl > 0 ? limit / v.cl : 1;
     *units = want < cap ? want : cap;
-    if (v.cl == 1) return launch(v.kernel, *units, v.cta, (size_t)v.smem, params, s);
+    return GBNORM_OK;
+}
+
+int launch_rows(const Q8Variant &v, int64_t units, void *params, cudaStream_t s) {
+    if (v.cl == 1) return launch(v.kernel, units, v.cta, (size_t)v.smem, params, s);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
-    return cluster_launch(v, *units, params, s, &cfg, &attr);
+    return cluster_launch(v, units, params, s, &cfg, &attr);
 }
 
 // The first variant of the table that holds N elements, -1 if none does.
@@ -200,6 +215,9 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
     if (!p.q) p.ldq = N;
     if (!p.c) p.ldc = N;
     const int xs = elem_size(p.xdt), ps = elem_size(p.pdt);
+    if (!elements_aligned({{p.x, xs}, {p.res, xs}, {p.h, xs}, {p.y, elem_size(p.ydt)}, {p.gamma, ps}, {p.beta, ps},
+                           {p.mean, 4}, {p.rstd, 4}}))
+        return GBNORM_ERR_INVALID_ARG;
     int64_t qspan = 0, cspan = 0;
     for (int64_t ld : {p.ldx, p.ldr, p.ldh, p.ldy, p.ldq, p.ldc})
         if (M > 0 && !valid_ld(ld, N, M)) return GBNORM_ERR_INVALID_ARG;
@@ -242,19 +260,49 @@ int do_fwd(FwdArgs &a, cudaStream_t stream) {
         const int slot = (vec ? ((p.xdt * 3 + op) * kQ8FwdKinds + kind) * kQ8MaxVariants
                               : kAnySlots + (a.is_ln * (kQ8FwdKinds + 1) + kind) * kQ8MaxVariants) + i;
         int64_t units;
-        t_last[0] = t.v[i].name;
-        return launch_rows(t.v[i], slot, M, INT64_MAX, d, &p, stream, &units);
+        const int st = row_units(t.v[i], slot, M, d, &units);
+        if (st == GBNORM_OK) {
+            t_last[0] = t.v[i].name;
+            return launch_rows(t.v[i], units, &p, stream);
+        }
+        if (st != GBNORM_ERR_UNSUPPORTED) return st;  // else this device holds no such CTA or cluster
     }
     t_last[0] = "elem";
     return launch(kQ8FwdElem[a.is_ln], grid_of(M, 8, d), kElemCTA, 0, &p, stream);
 }
 
-// Partial rows of the backward: an upper bound over its kernels, so that the
-// workspace depends on the shape alone.
-size_t bwd_ws_bytes(int is_ln, int64_t M, int64_t N, const HostDevice &d) {
-    const int64_t P = grid_of(M, kQ8BwdPerSm, d);
-    const size_t need = (size_t)P * (size_t)N * 4u * (is_ln ? 2u : 1u);
-    return (need + 255u) & ~(size_t)255u;
+// The backward's kernel for rows of these storage types (x_dtype == y_dtype: that
+// type, else 3; without vectors 4) and its partial rows; v NULL: element by
+// element, one CTA per SM.
+struct BwdPlan {
+    const Q8Variant *v;
+    int64_t P;
+};
+int bwd_plan(int is_ln, int types, int64_t M, int64_t N, const HostDevice &d, BwdPlan *pl) {
+    const Q8Table &t = types < 4 ? (is_ln ? kQ8Bwd_ln : kQ8Bwd_rms)[types] : (is_ln ? kQ8Any_ln : kQ8Any_rms)[kQ8FwdKinds];
+    const int i = find_rows(t, N);
+    if (i >= 0) {
+        const int slot = (types < 4 ? kBwdSlots + (is_ln * 4 + types) * kQ8MaxVariants
+                                    : kAnySlots + (is_ln * (kQ8FwdKinds + 1) + kQ8FwdKinds) * kQ8MaxVariants) + i;
+        const int st = row_units(t.v[i], slot, M, d, &pl->P);
+        pl->v = &t.v[i];
+        if (st != GBNORM_ERR_UNSUPPORTED) return st;
+    }
+    *pl = BwdPlan{nullptr, grid_of(M, 1, d)};
+    return GBNORM_OK;
+}
+// Workspace: the most partial rows that any types and alignment need for this
+// shape, so that it depends on the shape alone.
+int bwd_ws_bytes(int is_ln, int64_t M, int64_t N, const HostDevice &d, size_t *bytes) {
+    int64_t P = 0;
+    for (int types = N % 8 == 0 ? 0 : 4; types <= 4 && M > 0; ++types) {
+        BwdPlan pl;
+        const int st = bwd_plan(is_ln, types, M, N, d, &pl);
+        if (st != GBNORM_OK) return st;
+        if (pl.P > P) P = pl.P;
+    }
+    *bytes = ((size_t)P * (size_t)N * 4u * (is_ln ? 2u : 1u) + 255u) & ~(size_t)255u;
+    return GBNORM_OK;
 }
 
 }  // namespace
@@ -292,8 +340,8 @@ int norm_fwd_ck8(int is_layernorm, int64_t M, int64_t N, float eps, const void *
 size_t norm_bwd_ck8_workspace_size(int is_layernorm, int64_t M, int64_t N) {
     if ((is_layernorm != 0 && is_layernorm != 1) || !valid_shape(M, N)) return 0;
     HostDevice d;
-    if (host_device(&d) != GBNORM_OK) return 0;
-    const size_t need = bwd_ws_bytes(is_layernorm, M, N, d);
+    size_t need = 0;
+    if (host_device(&d) != GBNORM_OK || bwd_ws_bytes(is_layernorm, M, N, d, &need) != GBNORM_OK) return 0;
     return need > 0 ? need : 256;  // M = 0: nothing is used; 0 means an error
 }
 
@@ -319,9 +367,13 @@ int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t
         if (!valid_ld(ldcs, pairs, M) || ldcs % 2 != 0 || !aligned(c_scale, 8)) return GBNORM_ERR_INVALID_ARG;
     }
     const int xs = elem_size(x_dtype);
+    if (!elements_aligned({{dy, elem_size(y_dtype)}, {dres, xs}, {dx, xs}, {gamma, elem_size(param_dtype)}, {mean, 4},
+                           {rstd, 4}, {dgamma, 4}, {dbeta, 4}}))
+        return GBNORM_ERR_INVALID_ARG;
     HostDevice d;
-    const int s = host_device(&d);
-    const size_t need = s == GBNORM_OK ? bwd_ws_bytes(is_layernorm, M, N, d) : 0;
+    int s = host_device(&d);
+    size_t need = 0;
+    if (s == GBNORM_OK) s = bwd_ws_bytes(is_layernorm, M, N, d, &need);
     const Span outs[4] = {rows(dx, M, N, lddx, xs, true), flat(dgamma, N, 4), flat(dbeta, N, 4),
                           flat(M > 0 ? workspace : nullptr, (int64_t)need, 1)};
     const Span ins[7] = {rows(dy, M, N, lddy, elem_size(y_dtype), true), rows(dres, M, N, lddres, xs, true),
@@ -339,22 +391,13 @@ int norm_bwd_ck8(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t
         const int ys = elem_size(y_dtype);
         const bool vec = N % 8 == 0 && vec_rows(dy, lddy, ys) && vec_rows(dres, lddres, xs) && vec_rows(dx, lddx, xs) &&
                          aligned(gamma, 16) && aligned(codes, 8) && ldc % 8 == 0;
-        const int types = x_dtype == y_dtype ? x_dtype : 3;
-        const Q8Table &t = vec ? (is_layernorm ? kQ8Bwd_ln : kQ8Bwd_rms)[types]
-                               : (is_layernorm ? kQ8Any_ln : kQ8Any_rms)[kQ8FwdKinds];
-        const int i = find_rows(t, N);
-        int st;
-        if (i >= 0) {
-            const int slot = (vec ? kBwdSlots + (is_layernorm * 4 + types) * kQ8MaxVariants
-                                  : kAnySlots + (is_layernorm * (kQ8FwdKinds + 1) + kQ8FwdKinds) * kQ8MaxVariants) + i;
-            t_last[1] = t.v[i].name;
-            st = launch_rows(t.v[i], slot, M, kQ8BwdPerSm * d.sms, d,
-                             &p, stream, &P);
-        } else {
-            P = grid_of(M, 1, d);
-            t_last[1] = "elem";
-            st = launch(kQ8BwdElem[is_layernorm], P, kElemCTA, 0, &p, stream);
-        }
+        BwdPlan pl;
+        int st = bwd_plan(is_layernorm, !vec ? 4 : x_dtype == y_dtype ? x_dtype : 3, M, N, d, &pl);
+        if (st != GBNORM_OK) return st;
+        P = pl.P;
+        t_last[1] = pl.v ? pl.v->name : "elem";
+        st = pl.v ? launch_rows(*pl.v, P, &p, stream)
+                  : launch(kQ8BwdElem[is_layernorm], P, kElemCTA, 0, &p, stream);
         if (st != GBNORM_OK) return st;
     }
     return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, M > 0, stream);
@@ -376,6 +419,8 @@ int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int 
         if (sspan == 0) return GBNORM_ERR_INVALID_ARG;
     }
     const int ps = elem_size(param_dtype);
+    if (!elements_aligned({{y, elem_size(y_dtype)}, {gamma, ps}, {beta, ps}, {mean, 4}, {rstd, 4}}))
+        return GBNORM_ERR_INVALID_ARG;
     const Span outs[1] = {rows(y, M, N, ldy, elem_size(y_dtype), false)};
     const Span ins[7] = {rows(q, M, N, ldq, 1, false), flat(scale, sspan, 4), flat(mid, sspan, 4), flat(mean, M, 4),
                          flat(rstd, M, 4), flat(gamma, N, ps), flat(beta, N, ps)};

@@ -93,8 +93,6 @@ extern const Q8Table kQ8Fwd_ln_f16_raw[kQ8FwdKinds], kQ8Fwd_ln_bf16_raw[kQ8FwdKi
 extern const Q8Table kQ8Bwd_rms[4], kQ8Bwd_ln[4];
 // Rows without 16-byte vectors, any types: the forward's kinds, then the backward.
 extern const Q8Table kQ8Any_rms[kQ8FwdKinds + 1], kQ8Any_ln[kQ8FwdKinds + 1];
-// Partial rows of the backward are at most this many CTAs per SM.
-constexpr int kQ8BwdPerSm = 4;
 // Reading back: [format][with the norm on top][scale and mid as pairs][type of y]; a second kernel
 // argument (int) is the chunks of a row side by side in a CTA.
 extern const void *const kQ8Read[2][2][2][3];

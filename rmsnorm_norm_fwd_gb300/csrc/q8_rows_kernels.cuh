@@ -559,9 +559,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
         }
 
         // ---------------------------------------------------------------- output
-        // (h - mean) rstd as one multiply-add: mean is itself rounded to fp32, and
-        // the rounding of mean * rstd is of that size
-        const float2 nm = f2s(-mean * rstd), rs = f2s(rstd);
+        const float2 nm = f2s(-mean), rs = f2s(rstd);
         if constexpr (!RQ) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {  // y; zeros past the row's end
@@ -571,7 +569,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
                     param(bp, k, b8);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        o[k][i] = has(k) ? f2fma(f2fma(o[k][i], rs, nm), g8[i], b8[i]) : f2s(0.f);
+                        o[k][i] = has(k) ? f2fma(f2mul(f2add(o[k][i], nm), rs), g8[i], b8[i]) : f2s(0.f);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[k][i] = f2mul(f2mul(o[k][i], rs), g8[i]);

@@ -536,6 +536,105 @@ def test_streams_and_graph():
         assert all(same_bits(a, b) for a, b in zip(out, step(*new)))
 
 
+def test_captured_before_any_eager_call():
+    """A shape and types that nothing ran before, captured at once and replayed; two graphs side by side."""
+    g = lib()
+    M, N = 21, 2824
+    x, dy = ref.rows(M, N, torch.float16, 1).cuda(), ref.rows(M, N, torch.float16, 2).cuda()
+    gamma, beta = (cuda(t) for t in params(N, True, torch.float32))
+
+    def step(x):
+        y, _, ck, mean, rstd = g.norm_fwd_ck8(True, x, gamma, beta, 1e-5, group=32)
+        return [y, *ck[:2], *g.norm_bwd_ck8(True, dy, ck, gamma, mean, rstd), g.read_ck8(ck, y_dtype=torch.float16)]
+    x2 = (x * 0.5).contiguous()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for graph, t in zip(graphs, (x, x2)):
+        with torch.cuda.graph(graph):
+            outs.append(step(t))
+    for graph in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    for t, out in zip((x, x2), outs):
+        assert all(same_bits(a, b) for a, b in zip(out, step(t)))
+
+
+def test_host_threads():
+    """Calls from several host threads, each on its stream, give the bits of the calls one after another."""
+    import threading
+    g = lib()
+    xs = [ref.rows(65, N, torch.bfloat16, k).cuda() for k, N in enumerate((1024, 4096, 1003, 32768))]
+    gammas = [params(x.shape[1], False, torch.bfloat16)[0].cuda() for x in xs]
+
+    def step(k):
+        q, s, *_ , rstd = g.norm_fwd_q8(False, xs[k], gammas[k], None, 1e-6, group=64)
+        y, _, ck, _, r2 = g.norm_fwd_ck8(False, xs[k], gammas[k], None, 1e-6)
+        return [q, s, rstd, y, *ck[:2], *g.norm_bwd_ck8(False, xs[k], ck, gammas[k], None, r2)[:2]]
+    want = [step(k) for k in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got[k] = step(k)
+        stream.synchronize()
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(same_bits(a, b) for w, o in zip(want, got) for a, b in zip(w, o))
+
+
+@pytest.mark.parametrize("N", [256, 1000, 8192, 40000])
+@pytest.mark.parametrize("fmt", [E4M3, I8])
+def test_unaligned_rows_give_the_same_codes(N, fmt):
+    """Rows one element off a 16-byte boundary: the codes and checkpoint bits of the aligned call (they are defined by
+    the rows alone), read back to the same values."""
+    g = lib()
+    M = 19
+    x, r = ref.rows(M, N, torch.bfloat16, 1).cuda(), ref.rows(M, N, torch.bfloat16, 2).cuda()
+    gamma = params(N, False, torch.bfloat16)[0].cuda()
+
+    def off(t, dtype=None):
+        buf = torch.zeros(M, N + 9, device="cuda", dtype=dtype or t.dtype)
+        if t is not None:
+            buf[:, 1:N + 1].copy_(t)
+        return buf[:, 1:N + 1]
+    for group in (0, 32, 256):
+        a = g.checkpoint8_empty(M, N, 64)
+        q, s, h, _, _ = g.norm_fwd_q8(False, x, gamma, None, 1e-6, residual=r, group=group, fmt=fmt, checkpoint=a)
+        b = g.Checkpoint8(off(None, torch.int8), torch.empty_like(a.scales), 64)
+        q2, s2, h2, _, _ = g.norm_fwd_q8(False, off(x), gamma, None, 1e-6, residual=off(r), group=group, checkpoint=b,
+                                         q=off(None, torch.uint8).view(fmt), h=off(None, x.dtype))
+        assert "any" in g.q8_last_variant(0) and same_bits(q, q2) and same_bits(h, h2)
+        assert same_bits(a.codes, b.codes) and same_bits(a.scales, b.scales)
+        assert ((s - s2).abs() <= 1e-5 * s).all()
+        assert same_bits(g.read_q8(q, s, group, y=off(None, torch.bfloat16)), g.read_q8(q, s, group))
+        assert g.q8_last_variant(2) == "vec"
+        assert same_bits(g.read_ck8(b), g.read_ck8(a))
+
+
+def test_workspace_follows_the_partial_rows():
+    """One partial row per row group that runs at once: tens of MB for wide rows, and a workspace one byte short refused."""
+    g = lib()
+    for N in (1003, 4096, 16384, 131072, 200000):
+        for ln in (False, True):
+            need = g.norm_bwd_ck8_workspace_size(ln, 1 << 20, N)
+            assert 4 * N * (2 if ln else 1) <= need <= 1024 * 4 * min(N, 16384) * (2 if ln else 1) * (10 if N > 16384 else 1)
+    x = ref.rows(64, 4096, torch.bfloat16, 1).cuda()
+    _, _, ck, _, rstd = g.norm_fwd_ck8(False, x, None, None, 1e-6)
+    need = g.norm_bwd_ck8_workspace_size(False, 64, 4096)
+    ws = torch.empty(need, device="cuda", dtype=torch.uint8)
+    a = g.norm_bwd_ck8(False, x, ck, None, None, rstd, workspace=ws)
+    b = g.norm_bwd_ck8(False, x, ck, None, None, rstd)
+    assert same_bits(a[0], b[0]) and same_bits(a[1], b[1])
+    with pytest.raises(g.GbnormError):
+        g.norm_bwd_ck8(False, x, ck, None, None, rstd, workspace=ws[:need - 1])
+
+
 def test_no_rows():
     g = lib()
     x = torch.empty(0, 512, device="cuda", dtype=torch.bfloat16)

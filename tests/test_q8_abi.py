@@ -43,7 +43,8 @@ def off(p, by):
 FORWARD = [dict(ln=2), dict(M=-1), dict(N=0), dict(N=(1 << 24) + 1), dict(M=1 << 60), dict(eps=-1.0), dict(eps=float("inf")),
            dict(x=None), dict(ldx=N - 1), dict(xdt=3), dict(pdt=-1), dict(res=None), dict(ldr=N - 1), dict(ldh=0),
            dict(rstd=at(2)), dict(h=off(at(1), 2)), dict(h=at(0), ldh=N + 8), dict(cg=0), dict(cg=96), dict(cs=None),
-           dict(cs=off(at(7), 4)), dict(ldcs=6), dict(ldcs=9), dict(c=at(0)), dict(c=at(2)), dict(cs=at(8))]
+           dict(cs=off(at(7), 4)), dict(ldcs=6), dict(ldcs=9), dict(c=at(0)), dict(c=at(2)), dict(cs=at(8)),
+           dict(x=off(at(0), 1)), dict(gamma=off(at(3), 1)), dict(rstd=off(at(8), 2))]
 
 
 @pytest.mark.parametrize("change", FORWARD + [dict(q=None), dict(fmt=2), dict(qg=100), dict(qg=512), dict(qs=None),
@@ -66,7 +67,8 @@ def test_norm_fwd_ck8_refuses(lib, change):
                                     dict(ldcs=6), dict(cs=off(at(7), 4)), dict(xdt=5), dict(ydt=5), dict(pdt=5),
                                     dict(dx=at(6)), dict(dx=off(at(0), 2)), dict(dx=at(0), lddx=N + 8),
                                     dict(dx=at(0), ydt=0), dict(dgamma=at(2)), dict(dgamma=at(8)),
-                                    dict(ln=1, mean=at(11), dbeta=at(9))])
+                                    dict(ln=1, mean=at(11), dbeta=at(9)), dict(dy=off(at(0), 1)), dict(dx=off(at(2), 1)),
+                                    dict(rstd=off(at(8), 2)), dict(dgamma=off(at(9), 2)), dict(dres=off(at(1), 1))])
 def test_norm_bwd_ck8_refuses(lib, change):
     assert lib.norm_bwd_ck8(*{**BWD, **change}.values()) == BAD
 
@@ -74,7 +76,7 @@ def test_norm_bwd_ck8_refuses(lib, change):
 @pytest.mark.parametrize("change", [dict(M=-1), dict(N=0), dict(q=None), dict(scale=None), dict(y=None), dict(ldq=N - 1),
                                     dict(ldy=N - 1), dict(fmt=2), dict(qg=1), dict(pdt=4), dict(ydt=4), dict(sr=2),
                                     dict(sg=0), dict(y=at(0)), dict(y=at(1)), dict(y=at(4)), dict(mid=off(at(9), 1)),
-                                    dict(y=off(at(0), 64))])
+                                    dict(y=off(at(0), 64)), dict(y=off(at(6), 1)), dict(rstd=off(at(3), 1))])
 def test_q8_read_refuses(lib, change):
     assert lib.q8_read(*{**READ, **change}.values()) == BAD
 
