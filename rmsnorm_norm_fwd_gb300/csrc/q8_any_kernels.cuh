@@ -6,7 +6,9 @@
 // apart, so that every access of a warp is 32 consecutive elements whatever
 // their alignment, and a group of 32..256 columns is 1..8 of a lane's elements
 // across the warp.  Apart from that the steps are those of the vector kernels.
-// What bounds it: the load and store instructions, one an element.
+// What bounds it: the load and store instructions, one an element (8192 x 4001
+// bf16 RMSNorm 33 us, 44% of the copy rate's time, 23 instructions an element;
+// 8191 x 1003 fp32 LayerNorm 19 us, 32%; backward 8192 x 4001 71 us, 34%).
 #pragma once
 
 #include "q8_bwd_kernels.cuh"

@@ -5,6 +5,9 @@
 // enough loads are in flight.  With the statistics folded into the group's
 // (scale, mid) a value is one multiply-add of its code, a second one with the
 // norm on top.  What bounds it: DRAM, 1 byte in and 2 (4) out an element.
+// Measured: 65536 x 2048 with the norm 65 us (93% of the copy rate's time); with
+// the statistics folded in as they were loaded the loads waited for one another
+// (92 us).
 #pragma once
 
 #include "q8_bwd_kernels.cuh"

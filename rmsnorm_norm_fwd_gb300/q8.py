@@ -191,7 +191,8 @@ def norm_fwd_ck8(is_layernorm: bool, x, gamma, beta, eps: float, residual=None, 
                  rstd=None, stream=None):
     """norm_fwd_ex that also leaves an 8-bit checkpoint of the normalised rows
     for norm_bwd_ck8 (int8 codes about the middle of each group of ``group``
-    columns).  Returns (y, h, checkpoint, mean, rstd)."""
+    columns; a checkpoint that is given keeps its own group).  Returns (y, h,
+    checkpoint, mean, rstd)."""
     c = _Call("x", x)
     if checkpoint is None:
         checkpoint = checkpoint8_empty(c.M, c.N, group, x.device)
