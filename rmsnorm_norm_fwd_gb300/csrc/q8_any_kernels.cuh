@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
                     }
             const float dm = s * cnt.inv_thread;
             mean = ref + dm;
-            acc = fmax_nan(q - s * dm, 0.f);
+            acc = m2_about_first(q, s, dm);
             group_meanvar<TPR, CL>(mean, acc, cnt, inv_n, rr);
         } else {
 #pragma unroll

@@ -224,6 +224,13 @@ __device__ __forceinline__ RowCounts row_counts(int thread, float cta) {
     return RowCounts{(float)thread, inv_or_0((float)thread), w, inv_or_0(w), cta, inv_or_0(cta)};
 }
 
+// Sum of squared deviations from their mean of values with sum s and sum of
+// squares q about one of them, dm the mean of those differences.  Squares
+// beyond fp32 stay infinite, as in a two-pass sum (rstd is then 0).
+__device__ __forceinline__ float m2_about_first(float q, float s, float dm) {
+    return q == INFINITY ? q : fmax_nan(q - s * dm, 0.f);
+}
+
 // Mean and sum of squared deviations of a row from its threads' own (the
 // update of Chan, Golub and LeVeque in its group form: over a warp's lanes, the
 // warps, the CTAs).  inv_n: 1 / N.
@@ -536,7 +543,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             }
             const float s = s2.x + s2.y, dm = s * cnt.inv_thread;
             mean = ref + dm;
-            acc = fmax_nan(q2.x + q2.y - s * dm, 0.f);
+            acc = m2_about_first(q2.x + q2.y, s, dm);
             group_meanvar<TPR, CL>(mean, acc, cnt, inv_n, rr);
         } else {
             float2 a2 = f2s(0.f);

@@ -318,6 +318,26 @@ def test_every_kernel_is_reached():
             assert have >= set(want) - ({"rows256x4c1"} if ln and what else set()), (what, ln, have)
 
 
+@pytest.mark.parametrize("ln", [False, True])
+@pytest.mark.parametrize("N", [256, 1003, 5128, 40000, 140000])
+def test_squares_beyond_fp32(N, ln):
+    """Finite rows whose squares are not: rstd is 0 and the rows are zeros (scale 0), as the general form's are; the
+    rows beside them keep their values."""
+    g = lib()
+    x = torch.randn(3, N, generator=torch.Generator().manual_seed(1))
+    x[1] *= 1e25
+    gamma, _ = params(N, ln, torch.float32)
+    for group in (0, 128):
+        q, s, _, _, rstd = g.norm_fwd_q8(ln, x.cuda(), gamma.cuda(), None, 1e-6, group=group)
+        assert rstd[1] == 0 and (s[1] == 0).all()
+        _, _, y, tol = ref.norm(ln, x, gamma, None, 1e-6)
+        for i in (0, 2):
+            ref.check_q8(ln, x[i:i + 1], gamma, q[i:i + 1], s[i:i + 1], group, y[i:i + 1], tol[i:i + 1])
+    y, _, _, _, rstd = g.norm_fwd_ck8(ln, x.cuda(), gamma.cuda(), None, 1e-6)
+    want, _, _, r = g.norm_fwd_ex(ln, x.cuda(), gamma.cuda(), None, 1e-6)
+    assert rstd[1] == 0 and r[1] == 0 and (y[1] == 0).all() and (want[1] == 0).all()
+
+
 # ------------------------------------------------------------------ checkpointed forward
 @pytest.mark.parametrize("N", LENGTHS + [16392, 40000])
 @pytest.mark.parametrize("ln", [False, True])
