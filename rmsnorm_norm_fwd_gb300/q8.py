@@ -3,11 +3,13 @@ q8_read of include/gbnorm.h).
 
 Argument marshalling only, as in ``binding``: tensors are checked, outputs that
 the caller does not pass are allocated with torch's caching allocator, and the
-call goes to the C ABI on torch's current stream of the tensors' device.
+call goes to the C ABI on torch's current stream of the tensors' device, or on
+the one given as the keyword ``stream``, which every operator takes.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -136,9 +138,22 @@ class _Call:
         with torch.cuda.device(self.dev):
             return fn(*args)
 
-    def go(self, name, fn, args, stream):
-        """fn(*args, stream) with the tensors' device current."""
-        _check(name, self.on_device(fn, *args, _raw_stream(self.dev) if stream is None else stream.cuda_stream))
+    def go(self, name, fn, args):
+        """fn(*args, stream) with the tensors' device current, on its current stream."""
+        _check(name, self.on_device(fn, *args, _raw_stream(self.dev)))
+
+
+def _on_stream(f):
+    """Adds the argument ``stream``: the call, and with it the allocation of its
+    outputs and workspace, under that stream (a workspace of another stream's
+    could be handed out again while the kernels still write to it)."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
 def _float_code(name, dtype):
@@ -157,9 +172,10 @@ def _sum_rows(c, x, residual, store_h, h):
     return h, (px, ldx, _float_code("x", x.dtype), pr, ldr, ph, ldh)
 
 
+@_on_stream
 def norm_fwd_q8(is_layernorm: bool, x, gamma, beta, eps: float, residual=None, store_h: bool = True,
                 fmt=torch.float8_e4m3fn, group: int = 0, checkpoint: Checkpoint8 | None = None, q=None, scale=None,
-                h=None, mean=None, rstd=None, save_stats: bool = True, stream=None):
+                h=None, mean=None, rstd=None, save_stats: bool = True):
     """RMSNorm / LayerNorm of x (+ residual) with the output in 8 bits: codes q
     of dtype ``fmt`` (torch.float8_e4m3fn or torch.int8; q's own if q is given)
     and float32 scales [M, ceil(N / group)], one per ``group`` columns (32, 64,
@@ -182,13 +198,14 @@ def norm_fwd_q8(is_layernorm: bool, x, gamma, beta, eps: float, residual=None, s
     mean, rstd, pm, ps = c.stats(is_layernorm, mean, rstd, save_stats)
     c.go("norm_fwd_q8", lib.norm_fwd_q8,
          (int(bool(is_layernorm)), c.M, c.N, eps, *sums, *par, *c.rows("q", q), Q8_CODE[q.dtype], group,
-          *c.scales("scale", scale, group), *c.checkpoint(checkpoint), pm, ps), stream)
+          *c.scales("scale", scale, group), *c.checkpoint(checkpoint), pm, ps))
     return q, scale, h, mean, rstd
 
 
+@_on_stream
 def norm_fwd_ck8(is_layernorm: bool, x, gamma, beta, eps: float, residual=None, store_h: bool = True,
                  group: int = 128, checkpoint: Checkpoint8 | None = None, y_dtype=None, y=None, h=None, mean=None,
-                 rstd=None, stream=None):
+                 rstd=None):
     """norm_fwd_ex that also leaves an 8-bit checkpoint of the normalised rows
     for norm_bwd_ck8 (int8 codes about the middle of each group of ``group``
     columns; a checkpoint that is given keeps its own group).  Returns (y, h,
@@ -203,7 +220,7 @@ def norm_fwd_ck8(is_layernorm: bool, x, gamma, beta, eps: float, residual=None, 
     mean, rstd, pm, ps = c.stats(is_layernorm, mean, rstd, True)
     c.go("norm_fwd_ck8", lib.norm_fwd_ck8,
          (int(bool(is_layernorm)), c.M, c.N, eps, *sums, *par, *c.rows("y", y), _float_code("y", y.dtype),
-          *c.checkpoint(checkpoint), pm, ps), stream)
+          *c.checkpoint(checkpoint), pm, ps))
     return y, h, checkpoint, mean, rstd
 
 
@@ -211,9 +228,9 @@ def norm_bwd_ck8_workspace_size(is_layernorm: bool, M: int, N: int) -> int:
     return int(lib.norm_bwd_ck8_workspace_size(int(bool(is_layernorm)), M, N))
 
 
+@_on_stream
 def norm_bwd_ck8(is_layernorm: bool, dy, checkpoint: Checkpoint8, gamma, mean, rstd, dres=None, dx=None, dx_dtype=None,
-                 dgamma=None, dbeta=None, workspace=None, need_dgamma: bool = True, need_dbeta: bool = True,
-                 stream=None):
+                 dgamma=None, dbeta=None, workspace=None, need_dgamma: bool = True, need_dbeta: bool = True):
     """Backward of the norm from its 8-bit checkpoint and saved statistics; dres
     (dx's dtype) is added into dx.  Returns (dx, dgamma, dbeta): dx of dx_dtype
     (default dres's, else dy's), dgamma and dbeta in float32 (None where not
@@ -245,22 +262,22 @@ def norm_bwd_ck8(is_layernorm: bool, dy, checkpoint: Checkpoint8, gamma, mean, r
           *c.checkpoint(checkpoint), pdr, lddr, pg, pdt, c.vec("mean", mean, c.M, torch.float32),
           c.vec("rstd", rstd, c.M, torch.float32), pdx, lddx, _float_code("dx", dx.dtype),
           c.vec("dgamma", dgamma, c.N, torch.float32), c.vec("dbeta", dbeta, c.N, torch.float32),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size()), stream)
+          workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return dx, dgamma, dbeta
 
 
-def _read(c, pq, ldq, code, group, scale, mid, mean, rstd, gamma, beta, y_dtype, y, like, stream):
+def _read(c, pq, ldq, code, group, scale, mid, mean, rstd, gamma, beta, y_dtype, y, like):
     if y is None:
         y = torch.empty(c.M, c.N, device=like.device, dtype=y_dtype)
     pg, pb, pdt = c.params(gamma, beta, torch.float32)
     c.go("q8_read", lib.q8_read,
          (c.M, c.N, pq, ldq, code, group, scale[0], mid, scale[1], scale[2], c.vec("mean", mean, c.M, torch.float32),
-          c.vec("rstd", rstd, c.M, torch.float32), pg, pb, pdt, *c.rows("y", y), _float_code("y", y.dtype)), stream)
+          c.vec("rstd", rstd, c.M, torch.float32), pg, pb, pdt, *c.rows("y", y), _float_code("y", y.dtype)))
     return y
 
 
-def read_q8(q, scale, group: int = 0, mean=None, rstd=None, gamma=None, beta=None, y_dtype=torch.bfloat16, y=None,
-            stream=None):
+@_on_stream
+def read_q8(q, scale, group: int = 0, mean=None, rstd=None, gamma=None, beta=None, y_dtype=torch.bfloat16, y=None):
     """8-bit rows read back: ((q * scale - mean) * rstd) * gamma + beta in
     y_dtype, with what is None left out."""
     c = _Call("q", q)
@@ -269,17 +286,17 @@ def read_q8(q, scale, group: int = 0, mean=None, rstd=None, gamma=None, beta=Non
     if group != 0 and group not in GROUPS:
         raise ValueError(f"group must be 0 (a scale per row) or one of {GROUPS}")
     return _read(c, *c.rows("q", q), Q8_CODE[q.dtype], group, c.scales("scale", scale, group), None, mean, rstd, gamma,
-                 beta, y_dtype, y, q, stream)
+                 beta, y_dtype, y, q)
 
 
-def read_ck8(checkpoint: Checkpoint8, mean=None, rstd=None, gamma=None, beta=None, y_dtype=torch.bfloat16, y=None,
-             stream=None):
+@_on_stream
+def read_ck8(checkpoint: Checkpoint8, mean=None, rstd=None, gamma=None, beta=None, y_dtype=torch.bfloat16, y=None):
     """A checkpoint read back: the rows it stands for, or, given the saved
     statistics (and gamma, beta), the norm's output computed again from them."""
     c = _Call("checkpoint codes", checkpoint.codes)
     pc, ldc, group, ps, lds = c.checkpoint(checkpoint)
     return _read(c, pc, ldc, Q8_CODE[torch.int8], group, (ps, lds, 2), ps + 4 if ps else None, mean, rstd, gamma, beta,
-                 y_dtype, y, checkpoint.codes, stream)
+                 y_dtype, y, checkpoint.codes)
 
 
 def q8_last_variant(what: int) -> str:

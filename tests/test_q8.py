@@ -543,6 +543,14 @@ def test_streams_and_graph():
         got = step(x, r, dy)
     torch.cuda.current_stream().wait_stream(side)
     assert all(same_bits(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(torch.cuda.Stream()):  # the argument counts, not the current stream
+        y, h, ck, _, rstd = g.norm_fwd_ck8(False, x, gamma, None, 1e-6, residual=r, stream=side)
+        dx, dg, _ = g.norm_bwd_ck8(False, dy, ck, gamma, None, rstd, dres=h, stream=side)
+        v = g.read_ck8(ck, stream=side)
+        q, s, *_ = g.norm_fwd_q8(False, x, gamma, None, 1e-6, residual=r, group=128, stream=side)
+        u = g.read_q8(q, s, 128, stream=side)
+    side.synchronize()
+    assert all(same_bits(a, b) for a, b in zip((q, s, h, rstd, dx, dg, v), want)) and same_bits(u, g.read_q8(q, s, 128))
     xs, rs, ds = (torch.empty_like(t) for t in (x, r, dy))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -653,6 +661,34 @@ def test_workspace_follows_the_partial_rows():
     assert same_bits(a[0], b[0]) and same_bits(a[1], b[1])
     with pytest.raises(g.GbnormError):
         g.norm_bwd_ck8(False, x, ck, None, None, rstd, workspace=ws[:need - 1])
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose strides put the last one past 2^31 elements: the bits of contiguous rows."""
+    g = lib()
+    M, ld = 3, (1 << 30) + 8
+    for N in (4096, 1003):
+        x, r, dy = (ref.rows(M, N, torch.bfloat16, k, special=False).cuda() for k in (1, 2, 3))
+        gamma = params(N, False, torch.bfloat16)[0].cuda()
+
+        def far(t, dtype=torch.bfloat16):
+            buf = torch.empty((M - 1) * ld + N, device="cuda", dtype=torch.uint8 if dtype == E4M3 else dtype)
+            v = (buf.view(E4M3) if dtype == E4M3 else buf).as_strided((M, N), (ld, 1))
+            if t is not None:
+                v.copy_(t)
+            return v
+        xf, rf, hf = far(x), far(r), far(None)
+        want = g.norm_fwd_q8(False, x, gamma, None, 1e-6, residual=r, group=64)
+        got = g.norm_fwd_q8(False, xf, gamma, None, 1e-6, residual=rf, group=64, q=far(None, E4M3), h=hf)
+        assert all(same_bits(a, b) for a, b in zip(got[:3], want[:3]))
+        assert same_bits(g.read_q8(got[0], got[1], 64, y=rf), g.read_q8(want[0], want[1], 64))
+        ck = g.Checkpoint8(far(None, torch.int8), torch.empty(M, -(-N // 64), 2, device="cuda"), 64)
+        y, _, _, _, rstd = g.norm_fwd_ck8(False, xf, gamma, None, 1e-6, checkpoint=ck, y=hf)
+        y2, _, ck2, _, rstd2 = g.norm_fwd_ck8(False, x, gamma, None, 1e-6, group=64)
+        assert same_bits(y, y2) and same_bits(ck.codes, ck2.codes) and same_bits(ck.scales, ck2.scales)
+        a = g.norm_bwd_ck8(False, far(dy), ck, gamma, None, rstd, dx=xf)
+        b = g.norm_bwd_ck8(False, dy, ck2, gamma, None, rstd2)
+        assert same_bits(a[0], b[0]) and same_bits(a[1], b[1])
 
 
 def test_no_rows():
