@@ -49,7 +49,7 @@ __device__ __forceinline__ float2 e4m3_to_f2(uint32_t two) {
 }
 // rint(u) for |u| <= 127 as a byte: adding 1.5 * 2^23 rounds to nearest even
 // and leaves the two's complement integer in the low byte.
-__device__ __forceinline__ uint32_t i8_code(float u) { return __float_as_uint(u + 12582912.f) & 0xffu; }
+__device__ __forceinline__ uint32_t i8_code(float u) { return __float_as_uint(__fadd_rn(u, 12582912.f)) & 0xffu; }
 
 __device__ __forceinline__ uint8_t q8_code(float u, int fmt) {
     return fmt == kI8 ? (uint8_t)i8_code(u) : (uint8_t)e4m3_pair(u, 0.f);
