@@ -229,10 +229,10 @@ int norm_bwd_ex(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t 
  * (q_group 0), with Q = 448 (GBNORM_E4M3) or 127 (GBNORM_INT8):
  *       scale = max |y_j| / Q,    code_j = y_j / scale rounded to nearest even
  * (saturating; int8 codes lie in [-127, 127]).  A group whose values all lie
- * below 2^-100 (for RMSNorm: whose |h_j gamma_j| do) has scale 0 and codes 0,
- * so code * scale is the value in every case.  A NaN in a row makes every
- * scale of the row NaN.  For RMSNorm the codes are taken of h_j gamma_j, rstd
- * cancelling in y_j / max |y_j|.
+ * below 2^-100 (for RMSNorm: whose |h_j gamma_j| do) has scale 0 and codes 0.
+ * A NaN in a row makes every scale of the row NaN, that of a group of zeros
+ * too.  For RMSNorm the codes are taken of h_j gamma_j, rstd cancelling in
+ * y_j / max |y_j|.
  *
  * 8-bit checkpoint of h: int8 codes about the middle of each group's range,
  * with a pair (scale, mid) for every group of c_group columns (32, 64, 128 or

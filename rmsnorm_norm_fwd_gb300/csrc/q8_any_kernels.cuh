@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
                 const int64_t first = base(k) + 32 * lane;
                 if (lane < 8 && (lane & ((1 << qlg) - 1)) == 0 && first < n)
                     qs[(first >> p.qg) * p.qs_grp] =
-                        gmax[k] < kQ8Tiny ? 0.f : RQ ? gmax[k] * rstd * inv_qmax : gmax[k] * inv_qmax;
+                        gmax[k] < kQ8Tiny ? (RQ ? q8_zero_scale(rstd) : 0.f) : RQ ? gmax[k] * rstd * inv_qmax : gmax[k] * inv_qmax;
             }
         } else if constexpr (OUT == kOutRow) {
             if constexpr (!RQ) group_sum_max<TPR, CL, true>(unused, m, rr);

@@ -30,9 +30,12 @@ __device__ __forceinline__ float fmin_nan(float a, float b) {
 __device__ __forceinline__ float q8_inv(float amax, float qmax) {
     return amax < kQ8Tiny ? 0.f : __fdiv_rn(qmax, amax);
 }
-// amax * mul / Q, 0 for a group of zeros.
+// The scale of a group of zeros: 0, also beside an infinite mul (rstd of a row of
+// zeros with eps 0), but NaN with a NaN one (a NaN elsewhere in the row).
+__device__ __forceinline__ float q8_zero_scale(float mul) { return mul != mul ? mul : 0.f; }
+// amax * mul / Q.
 __device__ __forceinline__ float q8_scale(float amax, float mul, float qmax) {
-    return amax < kQ8Tiny ? 0.f : __fdiv_rn(amax * mul, qmax);
+    return amax < kQ8Tiny ? q8_zero_scale(mul) : __fdiv_rn(amax * mul, qmax);
 }
 
 // Two e4m3 codes (low byte: a), saturating at +-448, nearest even.

@@ -596,7 +596,9 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             if constexpr (!RQ) put_groups();
             const int at = own * TPR + (t & ~((1 << qlg) - 1));
             if ((lane & ((1 << qlg) - 1)) < VPT && (FULL || at < nc))
-                qs[((c0 + at) >> qlg) * p.qs_grp] = gscale < kQ8Tiny ? 0.f : RQ ? gscale * rstd * inv_qmax : gscale * inv_qmax;
+                qs[((c0 + at) >> qlg) * p.qs_grp] = gscale < kQ8Tiny ? (RQ ? q8_zero_scale(rstd) : 0.f)
+                                                    : RQ         ? gscale * rstd * inv_qmax
+                                                                 : gscale * inv_qmax;
         } else if constexpr (OUT == kOutRow) {
             if constexpr (!RQ) group_sum_max<TPR, CL, true>(unused, m, rr);
             const float inv = q8_inv(m, qmax);

@@ -1,0 +1,36 @@
+"""Scales of the 8-bit output: NaN in rows with groups of zeros (GPU)."""
+import pytest
+import torch
+
+import q8_ref as ref
+from test_q8 import E4M3, I8, lib, params
+
+pytestmark = pytest.mark.gpu
+# one row group, without vectors, over a cluster, that without vectors, element by element
+KERNELS = [(512, "rows"), (1003, "any"), (40000, "rows"), (40001, "any"), (140000, "elem")]
+
+
+@pytest.mark.parametrize("N,kernel", KERNELS)
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("fmt", [E4M3, I8])
+def test_nan_reaches_groups_of_zeros(N, kernel, group, fmt):
+    """RMSNorm of a row with a NaN: y is NaN everywhere, so is every scale, where the row or gamma is zero too.  Groups
+    of zeros in rows without one keep scale 0, beside an infinity (rstd 0) and in a row of zeros with eps 0 (rstd
+    infinite) as well."""
+    g = lib()
+    x = ref.rows(5, N, torch.bfloat16, 1, special=False)
+    gamma = params(N, False, torch.bfloat16)[0]
+    x[:, :group] = 0.0
+    gamma[2 * group:3 * group] = 0.0
+    x[3, N - 1] = float("nan")
+    x[4, N - 1] = float("inf")
+    q, s, _, _, rstd = g.norm_fwd_q8(False, x.cuda(), gamma.cuda(), None, 1e-6, group=group, fmt=fmt)
+    assert kernel in g.q8_last_variant(0)
+    assert torch.isnan(rstd[3]) and torch.isnan(s[3]).all()
+    assert torch.isnan(g.read_q8(q, s, group)[3]).all()
+    for i in (0, 1, 2, 4):
+        assert s[i, 0] == 0 and s[i, 2] == 0
+        assert (q[i, :group].float() == 0).all() and (q[i, 2 * group:3 * group].float() == 0).all()
+    assert torch.isfinite(s[:3]).all() and (s[:3, 1] > 0).all()
+    q, s, _, _, rstd = g.norm_fwd_q8(False, torch.zeros_like(x).cuda(), gamma.cuda(), None, 0.0, group=group, fmt=fmt)
+    assert torch.isinf(rstd).all() and (s == 0).all() and (q.float() == 0).all()
