@@ -261,21 +261,20 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
             }
         };
         if constexpr (LN) {
-            // one pass about the thread's first element, as the vector kernels
-            const float ref = v[0][0];
-            float s = 0.f, q = 0.f;
+            // the thread's mean, then the deviations from it, as the vector kernels
+#pragma unroll
+            for (int k = 0; k < VB; ++k)  // zeros past the row's end
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mean += v[k][i];
+            mean *= cnt.inv_thread;
 #pragma unroll
             for (int k = 0; k < VB; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (has(k, i)) {
-                        const float d = v[k][i] - ref;
-                        s += d;
-                        q = fmaf(d, d, q);
+                        const float d = v[k][i] - mean;
+                        acc = fmaf(d, d, acc);
                     }
-            const float dm = s * cnt.inv_thread;
-            mean = ref + dm;
-            acc = m2_about_first(q, s, dm);
             group_meanvar<TPR, CL>(mean, acc, cnt, inv_n, rr);
         } else {
 #pragma unroll

@@ -224,13 +224,6 @@ __device__ __forceinline__ RowCounts row_counts(int thread, float cta) {
     return RowCounts{(float)thread, inv_or_0((float)thread), w, inv_or_0(w), cta, inv_or_0(cta)};
 }
 
-// Sum of squared deviations from their mean of values with sum s and sum of
-// squares q about one of them, dm the mean of those differences.  Squares
-// beyond fp32 stay infinite, as in a two-pass sum (rstd is then 0).
-__device__ __forceinline__ float m2_about_first(float q, float s, float dm) {
-    return q == INFINITY ? q : fmax_nan(q - s * dm, 0.f);
-}
-
 // Mean and sum of squared deviations of a row from its threads' own (the
 // update of Chan, Golub and LeVeque in its group form: over a warp's lanes, the
 // warps, the CTAs).  inv_n: 1 / N.
@@ -525,25 +518,29 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             for (int k = 0; k < VPT; ++k) put(k, o[k], fetch<VPT>(inv, lane, k));
         };
         if constexpr (LN) {
-            // One pass: deviations from the thread's first element.  With it
-            // among the n elements, sum d^2 <= (n + 1) M2, so what the
-            // subtraction below cancels is bounded by n + 1 roundings.
-            const float ref = o[0][0].x;
-            const float2 nr = f2s(-ref);
+            // The thread's mean, then the deviations from it: nothing
+            // cancels.  (Sum and squares about the thread's first element in
+            // one pass are as many operations and level in time, but cancel
+            // where that element is an outlier: 8191 x 1003 rows of N(0.5, 1)
+            // with single values of 60, rstd off by up to 35 * 2^-24 against
+            // 3 * 2^-24 this way.)
             float2 s2 = f2s(0.f), q2 = f2s(0.f);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)  // zeros past the row's end
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = f2add(s2, o[k][i]);
+            mean = (s2.x + s2.y) * cnt.inv_thread;
+            const float2 nt = f2s(-mean);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 if (!has(k)) continue;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 d = f2add(o[k][i], nr);
-                    s2 = f2add(s2, d);
+                    const float2 d = f2add(o[k][i], nt);
                     q2 = f2fma(d, d, q2);
                 }
             }
-            const float s = s2.x + s2.y, dm = s * cnt.inv_thread;
-            mean = ref + dm;
-            acc = m2_about_first(q2.x + q2.y, s, dm);
+            acc = q2.x + q2.y;
             group_meanvar<TPR, CL>(mean, acc, cnt, inv_n, rr);
         } else {
             float2 a2 = f2s(0.f);
