@@ -30,12 +30,18 @@ __device__ __forceinline__ float fmin_nan(float a, float b) {
 __device__ __forceinline__ float q8_inv(float amax, float qmax) {
     return amax < kQ8Tiny ? 0.f : __fdiv_rn(qmax, amax);
 }
-// The scale of a group of zeros: 0, also beside an infinite mul (rstd of a row of
-// zeros with eps 0), but NaN with a NaN one (a NaN elsewhere in the row).
-__device__ __forceinline__ float q8_zero_scale(float mul) { return mul != mul ? mul : 0.f; }
-// amax * mul / Q.
-__device__ __forceinline__ float q8_scale(float amax, float mul, float qmax) {
-    return amax < kQ8Tiny ? q8_zero_scale(mul) : __fdiv_rn(amax * mul, qmax);
+// amax * mul / Q rounded as the division rounds it, so that every kernel writes
+// the bits of the definition: the product with the rounded reciprocal, corrected
+// by its exact remainder (Markstein 1990).  Tried for every fp32 dividend and both
+// Q: only subnormal quotients by 448 may differ, in their last place.  1024 x
+// 65536 with group scales 48.7 us, 48.4 us without the correction, 49.4 us with
+// the division and its branch.  An infinite amax gives NaN.  A group of zeros: 0,
+// also beside an infinite mul (rstd of a row of zeros with eps 0), but NaN with a
+// NaN one (a NaN elsewhere in the row).
+__device__ __forceinline__ float q8_scale(float amax, float mul, int fmt) {
+    const float a = amax * mul, inv = fmt == kI8 ? 1.f / 127.f : 1.f / 448.f;
+    const float q = a * inv;
+    return amax < kQ8Tiny ? (mul != mul ? mul : 0.f) : __fmaf_rn(__fmaf_rn(-q, q8_max(fmt), a), inv, q);
 }
 
 // Two e4m3 codes (low byte: a), saturating at +-448, nearest even.

@@ -1,9 +1,9 @@
-"""Scales of the 8-bit output: NaN in rows with groups of zeros (GPU)."""
+"""Scales of the 8-bit output: the division that defines them, NaN in rows with groups of zeros (GPU)."""
 import pytest
 import torch
 
 import q8_ref as ref
-from test_q8 import E4M3, I8, lib, params
+from test_q8 import E4M3, I8, lib, params, same_bits
 
 pytestmark = pytest.mark.gpu
 # one row group, without vectors, over a cluster, that without vectors, element by element
@@ -34,3 +34,23 @@ def test_nan_reaches_groups_of_zeros(N, kernel, group, fmt):
     assert torch.isfinite(s[:3]).all() and (s[:3, 1] > 0).all()
     q, s, _, _, rstd = g.norm_fwd_q8(False, torch.zeros_like(x).cuda(), gamma.cuda(), None, 0.0, group=group, fmt=fmt)
     assert torch.isinf(rstd).all() and (s == 0).all() and (q.float() == 0).all()
+
+
+@pytest.mark.parametrize("N,kernel", KERNELS)
+@pytest.mark.parametrize("group", [0, 32, 256])
+@pytest.mark.parametrize("fmt", [E4M3, I8])
+def test_scales_are_the_division(N, kernel, group, fmt):
+    """scale = max|y| / Q in fp32, the same bits from every kernel: RMSNorm's from max|h gamma| and the saved rstd,
+    LayerNorm's where y is exact (rows of zeros: y is beta)."""
+    g = lib()
+    x = ref.rows(7, N, torch.bfloat16, 3)
+    gamma, beta = params(N, True, torch.bfloat16)
+    _, s, _, _, rstd = g.norm_fwd_q8(False, x.cuda(), gamma.cuda(), None, 1e-6, group=group, fmt=fmt)
+    assert kernel in g.q8_last_variant(0)
+    t = x.float() * gamma.float()
+    amax = torch.stack([b.abs().amax(1) for b in ref.blocks(t, group)], 1)
+    Q = torch.full_like(amax, ref.QMAX[fmt])
+    assert same_bits(s, (amax * rstd.cpu()[:, None]) / Q)
+    _, s, *_ = g.norm_fwd_q8(True, torch.zeros_like(x).cuda(), gamma.cuda(), beta.cuda(), 1e-6, group=group, fmt=fmt)
+    amax = torch.stack([b.abs().amax(1) for b in ref.blocks(beta.float()[None].expand(7, N), group)], 1)
+    assert same_bits(s, amax / Q)
