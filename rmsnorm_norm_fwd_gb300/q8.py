@@ -146,11 +146,17 @@ class _Call:
 def _on_stream(f):
     """Adds the argument ``stream``: the call, and with it the allocation of its
     outputs and workspace, under that stream (a workspace of another stream's
-    could be handed out again while the kernels still write to it)."""
+    could be handed out again while the kernels still write to it).  A stream of
+    another device than the tensors' is refused: the launch would go to that
+    device's current stream instead."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
+        for t in (*args, *kw.values()):
+            t = t.codes if isinstance(t, Checkpoint8) else t
+            if isinstance(t, torch.Tensor) and t.get_device() != stream.device.index:
+                raise ValueError(f"stream is one of {stream.device}, the tensors are on device {t.get_device()}")
         with torch.cuda.stream(stream):
             return f(*args, **kw)
     return call
