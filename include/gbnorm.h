@@ -232,7 +232,12 @@ int norm_bwd_ex(int is_layernorm, int64_t M, int64_t N, const void *dy, int64_t 
  * below 2^-100 (for RMSNorm: whose |h_j gamma_j| do) has scale 0 and codes 0.
  * A NaN in a row makes every scale of the row NaN, that of a group of zeros
  * too.  For RMSNorm the codes are taken of h_j gamma_j, rstd cancelling in
- * y_j / max |y_j|.
+ * y_j / max |y_j|; the quotient is an fp32 product with Q / max |h_j gamma_j|,
+ * so that one within 2^-22 of a tie may go to either side.
+ * Range: rows whose squares pass fp32 have rstd 0 and are zeros, as in the
+ * forms above, while h_j gamma_j (RMSNorm) or the sum of the |h_j| (LayerNorm)
+ * stays inside fp32.  Where the former does not, the scale is not finite; where
+ * the latter does not, statistics and scales may not be.
  *
  * 8-bit checkpoint of h: int8 codes about the middle of each group's range,
  * with a pair (scale, mid) for every group of c_group columns (32, 64, 128 or

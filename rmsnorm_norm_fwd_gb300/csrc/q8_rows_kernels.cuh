@@ -226,7 +226,9 @@ __device__ __forceinline__ RowCounts row_counts(int thread, float cta) {
 
 // Mean and sum of squared deviations of a row from its threads' own (the
 // update of Chan, Golub and LeVeque in its group form: over a warp's lanes, the
-// warps, the CTAs).  inv_n: 1 / N.
+// warps, the CTAs).  inv_n: 1 / N.  Squares beyond fp32 leave m2 infinite (rstd 0)
+// and the mean finite, as long as the sum of the row's magnitudes is inside fp32;
+// past that means become infinite and m2 NaN.
 template <int TPR, int CL>
 __device__ __forceinline__ void group_meanvar(float &mean, float &m2, const RowCounts &cnt, float inv_n,
                                               RowReduce<TPR, CL> &rr) {

@@ -1,4 +1,5 @@
-"""Scales of the 8-bit output: the division that defines them, NaN in rows with groups of zeros (GPU)."""
+"""Scales of the 8-bit output: the division that defines them, NaN in rows with groups of zeros, products h * gamma
+beyond fp32 (GPU)."""
 import pytest
 import torch
 
@@ -54,3 +55,16 @@ def test_scales_are_the_division(N, kernel, group, fmt):
     _, s, *_ = g.norm_fwd_q8(True, torch.zeros_like(x).cuda(), gamma.cuda(), beta.cuda(), 1e-6, group=group, fmt=fmt)
     amax = torch.stack([b.abs().amax(1) for b in ref.blocks(beta.float()[None].expand(7, N), group)], 1)
     assert same_bits(s, amax / Q)
+
+
+@pytest.mark.parametrize("N,kernel", KERNELS)
+@pytest.mark.parametrize("group", [0, 64])
+def test_products_beyond_fp32(N, kernel, group):
+    """RMSNorm where h gamma passes fp32 although y does not: a scale that is not finite, not a wrong value."""
+    g = lib()
+    x = torch.full((2, N), 1e10)
+    x[1] = 1.0
+    q, s, *_ = g.norm_fwd_q8(False, x.cuda(), torch.full((N,), 1e30).cuda(), None, 1e-6, group=group)
+    assert kernel in g.q8_last_variant(0)
+    assert not torch.isfinite(s[0]).any()
+    assert torch.isfinite(s[1]).all() and (q[1].float() == 448).all()

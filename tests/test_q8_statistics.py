@@ -96,3 +96,17 @@ def test_variance_of_rows_with_an_outlier_in_every_thread(vec, big):
         assert g.q8_last_variant(0) == ("rows256x4c1" if vec else "any512x2c1")
         assert (m.cpu().double() == pat.mean()).all()
         assert ((r.cpu().double() - rstd).abs() <= 4 * U * rstd).all()
+
+
+@pytest.mark.parametrize("N", [256, 1003, 5128, 40000, 40001, 140000])
+def test_squares_beyond_fp32_near_the_end_of_the_range(N):
+    """LayerNorm rows whose squares pass fp32 and whose sums of magnitudes do not: rstd 0, zeros, a finite mean."""
+    g = lib()
+    x = torch.randn(3, N, generator=torch.Generator().manual_seed(1))
+    x[1] = torch.where(torch.arange(N) % 2 == 0, 1.0, -1.0) * (2.0 ** 127 / N)
+    mean = x[1].double().mean().item()
+    for group in (0, 128):
+        q, s, _, m, rstd = g.norm_fwd_q8(True, x.cuda(), None, None, 1e-6, group=group)
+        assert rstd[1] == 0 and (s[1] == 0).all() and (q[1].float() == 0).all()
+        assert abs(m[1].item() - mean) <= U * (N / 256 + 64) * 2.0 ** 127 / N
+        assert torch.isfinite(s).all() and (rstd[0] > 0) and (rstd[2] > 0)
