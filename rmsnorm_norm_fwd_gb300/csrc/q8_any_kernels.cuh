@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
     const int64_t cols = cta_columns<CL>(p.N), j0 = CL == 1 ? 0 : (int64_t)cluster_ctarank() * cols;
     const int64_t n = CL == 1 ? p.N : (j0 + cols < p.N ? j0 + cols : p.N);
     const float inv_n = 1.f / (float)p.N;
-    const float qmax = q8_max(p.qfmt);
+    const float qmax = q8_max(p.qfmt), inv_qmax = q8_inv_max(p.qfmt);
     const int qlg = p.qg - 5, clg = p.cg - 5;  // log2 of a lane's elements of a group in a block
     Block blk[VB];
 #pragma unroll
@@ -323,18 +323,22 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
         }
         if constexpr (OUT == kOutGroup) {
             if constexpr (!RQ) put_groups();
+            // lanes 8 k to 8 k + 7 write block k's (block_max leaves i's maximum on every lane l mod 8 = i)
+            static_assert(VB <= 4, "eight lanes a block");
+            float top = gmax[0];
+            int64_t first = base(0);
 #pragma unroll
-            for (int k = 0; k < VB; ++k) {
-                const int64_t first = base(k) + 32 * lane;
-                if (lane < 8 && (lane & ((1 << qlg) - 1)) == 0 && first < n)
-                    qs[(first >> p.qg) * p.qs_grp] = q8_scale(gmax[k], RQ ? rstd : 1.f, p.qfmt);
-            }
+            for (int k = 1; k < VB; ++k)
+                if (lane >> 3 == k) top = gmax[k], first = base(k);
+            first += 32 * (lane & 7);
+            if (lane < 8 * VB && (lane & 7 & ((1 << qlg) - 1)) == 0 && first < n)
+                qs[(first >> p.qg) * p.qs_grp] = q8_scale(top, RQ ? rstd : 1.f, qmax, inv_qmax);
         } else if constexpr (OUT == kOutRow) {
             if constexpr (!RQ) group_sum_max<TPR, CL, true>(unused, m, rr);
             const float inv = q8_inv(m, qmax);
 #pragma unroll
             for (int k = 0; k < VB; ++k) put(k, [&](int) { return inv; });
-            if (t == 0 && j0 == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, p.qfmt);
+            if (t == 0 && j0 == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax, inv_qmax);
         }
     }
 }

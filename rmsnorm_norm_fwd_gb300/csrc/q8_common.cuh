@@ -12,6 +12,7 @@ namespace gbn {
 constexpr float kQ8Tiny = 7.888609052210118e-31f;  // 2^-100
 
 __device__ __forceinline__ float q8_max(int fmt) { return fmt == kI8 ? 127.f : 448.f; }
+__device__ __forceinline__ float q8_inv_max(int fmt) { return fmt == kI8 ? 1.f / 127.f : 1.f / 448.f; }
 
 // Maximum / minimum that return NaN if either operand is NaN, so that a NaN
 // anywhere in a group reaches the group's scale.
@@ -38,10 +39,9 @@ __device__ __forceinline__ float q8_inv(float amax, float qmax) {
 // the division and its branch.  An infinite amax gives NaN.  A group of zeros: 0,
 // also beside an infinite mul (rstd of a row of zeros with eps 0), but NaN with a
 // NaN one (a NaN elsewhere in the row).
-__device__ __forceinline__ float q8_scale(float amax, float mul, int fmt) {
-    const float a = amax * mul, inv = fmt == kI8 ? 1.f / 127.f : 1.f / 448.f;
-    const float q = a * inv;
-    return amax < kQ8Tiny ? (mul != mul ? mul : 0.f) : __fmaf_rn(__fmaf_rn(-q, q8_max(fmt), a), inv, q);
+__device__ __forceinline__ float q8_scale(float amax, float mul, float qmax, float inv_qmax) {
+    const float a = amax * mul, q = a * inv_qmax;
+    return amax < kQ8Tiny ? fmin_nan(mul, 0.f) : __fmaf_rn(__fmaf_rn(-q, qmax, a), inv_qmax, q);
 }
 
 // Two e4m3 codes (low byte: a), saturating at +-448, nearest even.

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kElemCTA) q8_fwd_elem(const Q8FwdParams p) {
                 amax = warp_max_nan(amax);
                 const float inv = q8_inv(amax, qmax);
                 for (int64_t j = j0 + lane; j < j1; j += 32) qr[j] = q8_code(out(j) * inv, p.qfmt);
-                if (lane == 0) p.qs[row * p.qs_row + g * p.qs_grp] = q8_scale(amax, mul, p.qfmt);
+                if (lane == 0) p.qs[row * p.qs_row + g * p.qs_grp] = q8_scale(amax, mul, qmax, q8_inv_max(p.qfmt));
             }
         } else {
             float amax = 0.f;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kElemCTA) q8_fwd_elem(const Q8FwdParams p) {
             for (int w = 0; w < W; ++w) amax = fmax_nan(amax, red_max[w]);
             const float inv = q8_inv(amax, qmax);
             for (int64_t j = threadIdx.x; j < p.N; j += kElemCTA) qr[j] = q8_code(out(j) * inv, p.qfmt);
-            if (threadIdx.x == 0) p.qs[row * p.qs_row] = q8_scale(amax, mul, p.qfmt);
+            if (threadIdx.x == 0) p.qs[row * p.qs_row] = q8_scale(amax, mul, qmax, q8_inv_max(p.qfmt));
         }
     }
 }

@@ -395,7 +395,7 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
     const int slice = cta_slice<CL>((int)(p.N / 8)), c0 = CL == 1 ? 0 : (int)cluster_ctarank() * slice;
     const int nc = CL == 1 ? slice : max(0, min(slice, (int)(p.N / 8) - c0));
     const float inv_n = 1.f / (float)p.N;
-    const float qmax = q8_max(p.qfmt);
+    const float qmax = q8_max(p.qfmt), inv_qmax = q8_inv_max(p.qfmt);
     const int qlg = p.qg - 3, clg = p.cg - 3;  // log2 of the lanes of a group
     const int own = own_chunk<VPT>(lane);
     auto has = [&](int k) { return FULL || k * TPR + t < nc; };
@@ -595,13 +595,13 @@ __device__ __forceinline__ void q8_fwd_body(const Q8FwdParams &p, float4 *par, f
             if constexpr (!RQ) put_groups();
             const int at = own * TPR + (t & ~((1 << qlg) - 1));
             if ((lane & ((1 << qlg) - 1)) < VPT && (FULL || at < nc))
-                qs[((c0 + at) >> qlg) * p.qs_grp] = q8_scale(gscale, RQ ? rstd : 1.f, p.qfmt);
+                qs[((c0 + at) >> qlg) * p.qs_grp] = q8_scale(gscale, RQ ? rstd : 1.f, qmax, inv_qmax);
         } else if constexpr (OUT == kOutRow) {
             if constexpr (!RQ) group_sum_max<TPR, CL, true>(unused, m, rr);
             const float inv = q8_inv(m, qmax);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) put(k, o[k], inv);
-            if (t == 0 && c0 == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, p.qfmt);
+            if (t == 0 && c0 == 0) qs[0] = q8_scale(m, RQ ? rstd : 1.f, qmax, inv_qmax);
         }
     }
 }
