@@ -5,7 +5,7 @@
 namespace gbn {
 
 // (TPR, VB, NT, MINB, CL) by row capacity TPR * VB * CL * 8.  Four CTAs an SM
-// against three: 8192 x 4001 bf16 RMSNorm 31 us against 42 us; four blocks a
+// against three: 8192 x 4001 bf16 RMSNorm 32 us against 34 us; four blocks a
 // thread on fewer threads 49 us.
 #define GBN_Q8A_GEOMS(X)   \
     X(32, 1, 256, 4, 1)    \

@@ -7,7 +7,7 @@ namespace gbn {
 
 // (TPR, VPT, R, NT, MINB, CL) by row capacity TPR * VPT * CL * 8.  LayerNorm
 // holds two column sums per element: fewer elements a thread, but two rows at a
-// time (bf16 16384 x 8192: 143 us against 173 us one at a time).  RMSNorm with
+// time (bf16 16384 x 8192: 145 us against 173 us one at a time).  RMSNorm with
 // its one sum is faster with twice the elements and one row (163 us against 177
 // us with a residual's gradient).  Wide rows go to clusters of 256-thread CTAs,
 // two an SM, as far as they hold them (RMSNorm 2048 x 65536: 154 us against 162

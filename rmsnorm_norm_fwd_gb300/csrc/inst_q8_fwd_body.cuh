@@ -8,8 +8,8 @@ namespace gbn {
 // (TPR, VPT, NT, MINB, CL) by row capacity TPR * VPT * CL * 8; MINB CTAs per SM
 // of the launch bound (as many as registers and the parameters in shared memory
 // allow).  Measured for bf16 LayerNorm with group scales, 16384 x 8192: 256 x 4
-// at four CTAs 80 us, three 88 us, two 98 us; 512 x 2 at two 109 us.  160 x 4
-// fills rows of 5120 (16384 x 5120: 60 us against 78 us on 256 x 3); RMSNorm is
+// at four CTAs 82 us, three 88 us, two 99 us; 512 x 2 at two 112 us.  160 x 4
+// fills rows of 5120 (16384 x 5120: 62 us against 75 us on 256 x 3); RMSNorm is
 // faster there with more CTAs' rows in flight (46 us on 256 x 3, 49 us).  Wide
 // LayerNorm rows: clusters of 256-thread CTAs (2048 x 32768: 59 us against 61
 // us with 512 threads, 93 us with 1024); RMSNorm is level, on half the CTAs.

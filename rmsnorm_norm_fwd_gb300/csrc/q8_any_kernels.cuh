@@ -7,8 +7,9 @@
 // their alignment, and a group of 32..256 columns is 1..8 of a lane's elements
 // across the warp.  Apart from that the steps are those of the vector kernels.
 // What bounds it: the load and store instructions, one an element (8192 x 4001
-// bf16 RMSNorm 33 us, 44% of the copy rate's time, 23 instructions an element;
-// 8191 x 1003 fp32 LayerNorm 19 us, 32%; backward 8192 x 4001 71 us, 34%).
+// bf16 RMSNorm 32 us, 45% of the copy rate's time, 23 instructions an element,
+// with group scales 43 us, 34%; 8191 x 1003 fp32 LayerNorm 18 us, 33%; backward
+// 8192 x 4001 72 us, 34%).
 #pragma once
 
 #include "q8_bwd_kernels.cuh"
@@ -93,8 +94,8 @@ __device__ __forceinline__ void st_bytes(uint8_t *row, const Block &b, const uin
     each(b, [&](int i) { row[b.at + 32 * i] = (uint8_t)v[i]; });
 }
 
-// A thread's own parameters of a block in shared memory (as fp32; `absent` past
-// the row's end and for a null row).
+// A thread's own parameters of a block in shared memory, as fp32: `absent` for a
+// null row, else zero past the row's end (what they multiply is zero there too).
 template <int NT> __device__ __forceinline__ void keep_block(float4 *own, const void *row, const Block &b, int dt, float absent) {
     float g[8];
 #pragma unroll
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(NT, MINB) q8_fwd_any(const Q8FwdParams p) {
         uint8_t *qr = p.q + row * p.ldq;
         float *qs = p.qs + row * p.qs_row;
         float acc = 0.f, mean = 0.f, m = 0.f, unused = 0.f;
-        float gmax[VB];  // lane i < 8: the maximum of i's group
+        float gmax[VB];  // lane l: the maximum of the group of i = l mod 8
         auto put = [&](int k, auto &&inv) {
             uint32_t code[8];
 #pragma unroll

@@ -13,10 +13,11 @@
 // What bounds it: DRAM, 5 bytes an element (bf16 dy and dx, 1.06 bytes of
 // checkpoint), 7 with a residual's gradient.  The next row is prefetched to L2
 // while one is worked on (copying it to shared memory asynchronously instead
-// measured 251 us against 163 us).  Measured, bf16: RMSNorm 16384 x 8192 115 us,
+// measured 251 us against 163 us).  Measured, bf16: RMSNorm 16384 x 8192 117 us,
 // 163 us with a residual's gradient (86% of the copy rate's time); LayerNorm
-// 16384 x 8192 143 us (70%), 16384 x 4096 76 us (66%): 19 instructions an element
-// at 16 warps an SM, which is what two column sums in registers leave.
+// 16384 x 8192 145 us (69%), 16384 x 4096 77 us (65%): 19 instructions an element
+// at 16 warps an SM, which is what two column sums in registers leave; issue at
+// 47%, so latency more than instructions.
 #pragma once
 
 #include "q8_rows_kernels.cuh"

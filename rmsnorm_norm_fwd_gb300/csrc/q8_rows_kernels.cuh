@@ -5,10 +5,12 @@
 // What bounds it: DRAM.  A row is read once and written once (bf16: 2 + 1
 // bytes an element, 7 with a residual sum); per element the arithmetic is a
 // few operations on fp32 pairs.  Measured, bf16, share of the copy rate's time:
-// RMSNorm 16384 x 8192 with a residual 150 us (92%), without 65 us (92%), group
-// scales 16384 x 4096 36 us (83%); LayerNorm 16384 x 8192 with group scales 82
-// us (73%), 15 instructions an element against 10; clusters, 1024 x 65536, 48
-// us (63%).
+// RMSNorm 16384 x 8192 with a residual 150 us (92%), without 65 us (91%), group
+// scales 16384 x 4096 36 us (84%); fp32 rows of 8192 102 us (97%).  LayerNorm
+// 16384 x 8192 with group scales 82 us (73%): 15.6 instructions an element
+// against 10.4, issue at 61% and DRAM at 39%, so latency too: a row group waits
+// for its own loads and two exchanges with nothing of its next row in flight but
+// the prefetch.  The same for clusters: 1024 x 65536 49 us (61%), issue at 44%.
 //
 //   - A chunk is 16 bytes of a 16-bit type in and 8 codes out, so a group of
 //     32..256 columns is 4..32 consecutive lanes of a warp: its maxima are a
@@ -19,12 +21,14 @@
 //   - The checkpoint's codes need h alone and are written before the
 //     statistics too.
 //   - A thread holds 8 to 32 elements, so that four 256-thread CTAs share an SM
-//     (LayerNorm three) and their phases overlap.
+//     (three where LayerNorm keeps gamma and beta as fp32) and their phases overlap.
 //   - Rows longer than one CTA holds are split over a cluster of 2 to 8 CTAs,
 //     which exchange the row's sums through distributed shared memory.
-//   - Every thread keeps gamma (beta) of its own columns as fp32 in its own
-//     slots of shared memory: no conversion, no branch on the parameter type
-//     and no barrier in the loop.
+//   - Every thread keeps gamma (beta) of its own columns in its own slots of
+//     shared memory, as fp32: no conversion, no branch on the parameter type and
+//     no barrier in the loop.  LayerNorm with 16-bit gamma and beta of the rows'
+//     type keeps them so and widens them at each use: that leaves room for the
+//     fourth CTA (16384 x 8192: 82 us against 90 us with fp32 ones).
 #pragma once
 
 #include <type_traits>
