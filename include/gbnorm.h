@@ -319,6 +319,112 @@ int q8_read(int64_t M, int64_t N, const void *q, int64_t ldq, int q_format, int 
 int gbnorm_q8_last_variant(int what, char *buf, size_t len);
 
 /*
+ * Heads: the norm of queries and keys with the position rotation.
+ *
+ * Attention normalises its queries and keys head by head (each head of D
+ * elements by itself, gamma and beta of D elements shared by all heads of
+ * the queries, others by those of the keys) and then rotates pairs of elements
+ * by angles that grow with the token's position.  qk_norm_rope_fwd does both
+ * in one pass over the queries and the keys; rope_fwd rotates alone.
+ *
+ *   n        the RMSNorm or LayerNorm forward above of the D elements of a head
+ *   angle_j  position[axis of pair j] * inv_freq[j] in radians, j < rot / 2;
+ *            product and reduction by whole turns are exact to 2^-65 turns
+ *            times the position
+ *   y        pair j is (a, b) = (j, j + rot / 2), or (2 j, 2 j + 1) where
+ *            `interleaved`:
+ *                y_a = n_a cos_j - n_b sin_j,    y_b = n_b cos_j + n_a sin_j;
+ *            elements rot to D - 1 keep n.  fp32 throughout, rounded once.
+ *
+ * With several axes (time, height and width of an image's or a video's tokens)
+ * every pair follows one of them.  The backward turns the gradient back and
+ * goes on with the norm's backward at the top of this file:
+ *
+ *   t        dy_a cos_j + dy_b sin_j, dy_b cos_j - dy_a sin_j (dy beyond rot)
+ *   dx       of the norm with g = t gamma
+ *   dgamma   sum over tokens and heads of t xhat,  dbeta of t
+ *
+ * rope_bwd turns a gradient back (the rotation's transpose, its inverse).
+ *
+ * Arguments:
+ *   is_layernorm, eps   as above; mean and beta are LayerNorm's alone.
+ *   r        what is the same for all tensors of a call (see below).
+ *   x, y, dy, dx   arrays of two: the queries' heads and the keys'.
+ *            heads[1] = 0: no keys, the second is not read.  x and dx have
+ *            x_dtype, y and dy y_dtype.  Strides are free (queries and keys
+ *            inside a packed projection, heads outside tokens), 0 among the
+ *            inputs' too (the same values for several tokens or heads); no two
+ *            elements of an output may share a place.
+ *   gamma, beta   arrays of two pointers to [D] param_dtype; NULL, or NULL
+ *            in one of the places: 1 and 0.
+ *   mean, rstd    [batches * tokens, heads[0] + heads[1]] float32, a token's
+ *            queries before its keys; written by the forward unless NULL,
+ *            read by the backward.
+ *   dgamma, dbeta [2][D] float32 (queries, keys; [1][D] without keys),
+ *            written; may be NULL.  Zeros without tokens.
+ *   workspace     at least qk_norm_rope_bwd_workspace_size(is_layernorm,
+ *            batches * tokens, heads[0], heads[1], dim) bytes (never 0 for
+ *            valid arguments on a usable device), 16-byte aligned, not shared
+ *            with a concurrent call.
+ *
+ * Aliasing: y may be exactly x and dx exactly dy (tensor by tensor: same
+ * address, strides and element size); any other overlap of an output is
+ * rejected.  Two tensors whose address ranges cross do not overlap if they
+ * are parts of one larger tensor that repeats with one of their strides (for
+ * instance queries and keys of a packed projection).  Pointers not aligned
+ * to their elements are rejected.
+ * Frequencies that are infinite, NaN or 2^87 and more make their pairs NaN.
+ * Status codes, ownership, streams and threading as above.
+ */
+#define GBNORM_MAX_HEADS 65536
+#define GBNORM_MAX_HEAD_DIM 1024
+#define GBNORM_MAX_AXES 4
+
+typedef enum {
+    GBNORM_I32 = 0,
+    GBNORM_I64 = 1
+} gbnorm_index_t;
+
+/* Element i of head h of token s of batch b: p + (b batch + s token + h head + i) elements. */
+typedef struct {
+    void *p;
+    int64_t batch, token, head;
+} gbnorm_heads_t;
+
+typedef struct {
+    int64_t batches, tokens; /* batches of tokens each; 0 of either: nothing is done */
+    int64_t heads[2];        /* of the queries (at least 1) and of the keys (0: no keys) */
+    int64_t dim;             /* D, 1 to GBNORM_MAX_HEAD_DIM */
+    int32_t x_dtype, y_dtype, param_dtype; /* gbnorm_dtype_t */
+    int32_t interleaved;     /* pairs (2 j, 2 j + 1), else (j, j + rot / 2) */
+    int32_t rot;             /* rotated elements, even, at most D; 0 (with the norm): no rotation, nothing below is read */
+    int32_t axes;            /* position axes, 1 to GBNORM_MAX_AXES */
+    int32_t pos_dtype;       /* gbnorm_index_t */
+    int32_t reserved;        /* not read */
+    const void *positions;   /* device: of axis a, batch b, token s at a pos_axis + b pos_batch + s pos_token elements */
+    int64_t pos_axis, pos_batch, pos_token; /* 0: the same for all */
+    const float *inv_freq;   /* device [rot / 2]: radians a position */
+    const uint8_t *pair_axis; /* HOST [rot / 2]: the axis of each pair, read during the call; NULL with one axis */
+} gbnorm_rope_t;
+
+int qk_norm_rope_fwd(int is_layernorm, float eps, const gbnorm_rope_t *r, const gbnorm_heads_t *x,
+                     const gbnorm_heads_t *y, const void *const *gamma, const void *const *beta, float *mean,
+                     float *rstd, gbnorm_stream_t stream);
+size_t qk_norm_rope_bwd_workspace_size(int is_layernorm, int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim);
+int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_heads_t *dy, const gbnorm_heads_t *x,
+                     const gbnorm_heads_t *dx, const void *const *gamma, const float *mean, const float *rstd,
+                     float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, gbnorm_stream_t stream);
+int rope_fwd(const gbnorm_rope_t *r, const gbnorm_heads_t *x, const gbnorm_heads_t *y, gbnorm_stream_t stream);
+int rope_bwd(const gbnorm_rope_t *r, const gbnorm_heads_t *dy, const gbnorm_heads_t *dx, gbnorm_stream_t stream);
+
+/*
+ * The kernel that the calling thread's last qk_norm_rope_fwd (what 0),
+ * qk_norm_rope_bwd (1) or rope_fwd / rope_bwd (2) launched, as
+ * gbnorm_ex_last_variant.  For tests.
+ */
+int gbnorm_rope_last_variant(int what, char *buf, size_t len);
+
+/*
  * RMSNorm backward without a caller-provided workspace.
  *
  * No counterpart on the pages: this entry point exists for callers that cannot

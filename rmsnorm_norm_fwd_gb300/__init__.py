@@ -17,7 +17,12 @@ _OPS = ("rmsnorm_fwd", "layernorm_fwd", "rmsnorm_bwd", "layernorm_bwd", "norm_bw
 _Q8_OPS = ("norm_fwd_q8", "norm_fwd_ck8", "norm_bwd_ck8", "norm_bwd_ck8_workspace_size", "read_q8", "read_ck8",
            "Checkpoint8", "checkpoint8_empty", "q8_last_variant")
 
-__all__ = list(_OPS) + list(_Q8_OPS)
+# Attention heads: norms of queries and keys with the position rotation, the
+# rotation alone.
+_ROPE_OPS = ("qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "rope_fwd", "rope_bwd",
+             "rotary", "Rotary", "rope_last_variant")
+
+__all__ = list(_OPS) + list(_Q8_OPS) + list(_ROPE_OPS)
 
 
 def __getattr__(name):
@@ -27,5 +32,9 @@ def __getattr__(name):
     if name in _Q8_OPS:
         from . import q8
         globals()[name] = f = getattr(q8, name)  # later uses find it without this call
+        return f
+    if name in _ROPE_OPS:
+        from . import rope
+        globals()[name] = f = getattr(rope, name)
         return f
     raise AttributeError(name)

@@ -1,0 +1,401 @@
+// rope_api.cu -- the C ABI of the head operators (include/gbnorm.h): argument
+// checks, the choice of a kernel, launches.  As in api.cu nothing here
+// allocates device memory or synchronises.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "../../include/gbnorm.h"
+#include "host_shared.h"
+#include "rope_params.h"
+
+namespace gbn {
+namespace {
+
+int elem_size(int dtype) { return dtype == GBNORM_F32 ? 4 : 2; }
+bool valid_dtype(int d) { return d == GBNORM_F32 || d == GBNORM_F16 || d == GBNORM_BF16; }
+bool aligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// CTAs an SM of the persistent grids.  The backward's also bounds its partial
+// rows, so that the workspace depends on the shape alone.
+constexpr int64_t kFwdPerSm = 8, kBwdPerSm = 2;
+
+// A tensor of heads as the aliasing check sees it, in bytes: runs of `run`
+// bytes at p + i0 st[0] + i1 st[1] + i2 st[2], i < n; extents of one element
+// have stride 0.
+struct Box {
+    uintptr_t p;
+    int64_t run, n[3], st[3];
+    int es;
+    int64_t span() const {
+        int64_t s = run;
+        for (int i = 0; i < 3; ++i) s += (n[i] - 1) * st[i];
+        return s;
+    }
+};
+
+constexpr int64_t kMostBytes = INT64_MAX / 16;
+
+// False if a stride is negative or the tensor's bytes do not fit.
+bool make_box(const gbnorm_heads_t &h, int64_t B, int64_t S, int64_t H, int64_t D, int dtype, Box *out) {
+    const int es = elem_size(dtype);
+    *out = Box{reinterpret_cast<uintptr_t>(h.p), D * es, {B, S, H}, {h.batch, h.token, h.head}, es};
+    int64_t left = kMostBytes - out->run;
+    for (int i = 0; i < 3; ++i) {
+        if (out->n[i] <= 1) {
+            out->st[i] = 0;
+            continue;
+        }
+        if (out->st[i] < 0 || out->st[i] > left / es / (out->n[i] - 1)) return false;
+        out->st[i] *= es;
+        left -= (out->n[i] - 1) * out->st[i];
+    }
+    return true;
+}
+
+bool same(const Box &a, const Box &b) {
+    return a.p == b.p && a.es == b.es && a.run == b.run && !std::memcmp(a.st, b.st, sizeof a.st) &&
+           !std::memcmp(a.n, b.n, sizeof a.n);
+}
+
+// No two elements in one place: each stride passes all that the smaller ones span.
+bool injective(const Box &a) {
+    int o[3] = {0, 1, 2};
+    std::sort(o, o + 3, [&](int i, int j) { return a.st[i] < a.st[j]; });
+    int64_t inner = a.run;
+    for (int i : o) {
+        if (a.n[i] <= 1) continue;
+        if (a.st[i] < inner) return false;
+        inner += (a.n[i] - 1) * a.st[i];
+    }
+    return true;
+}
+
+// The bytes a box covers in each period of `per` bytes, 0 if it does not repeat with that period.
+int64_t window(const Box &a, int64_t per) {
+    int64_t w = a.run;
+    for (int i = 0; i < 3; ++i)
+        if (a.n[i] > 1 && a.st[i] % per != 0) w += (a.n[i] - 1) * a.st[i];
+    return w <= per ? w : 0;
+}
+
+// May the two share a byte?  Spans apart: no.  Else both may be parts of one
+// larger tensor (queries and keys within a packed projection): if they repeat
+// with a common period and cover different parts of it, no.
+bool may_overlap(const Box &a, const Box &b) {
+    if (!a.p || !b.p) return false;
+    if (a.p + (uintptr_t)a.span() <= b.p || b.p + (uintptr_t)b.span() <= a.p) return false;
+    for (const Box *x : {&a, &b})
+        for (int i = 0; i < 3; ++i) {
+            const int64_t per = x->st[i];
+            if (x->n[i] <= 1 || per <= 0) continue;
+            const int64_t wa = window(a, per), wb = window(b, per);
+            if (!wa || !wb) continue;
+            const int64_t d = (int64_t)((b.p % (uintptr_t)per + (uintptr_t)per - a.p % (uintptr_t)per) % (uintptr_t)per);
+            if (d >= wa && per - d >= wb) return false;
+        }
+    return true;
+}
+
+Box flat(const void *p, int64_t bytes) {
+    return Box{bytes > 0 ? reinterpret_cast<uintptr_t>(p) : 0, bytes, {1, 1, 1}, {0, 0, 0}, 1};
+}
+
+struct Shape {
+    int64_t B, S, H[2], D;
+    int64_t tokens() const { return B * S; }
+    int tensors() const { return H[1] > 0 ? 2 : 1; }
+};
+
+bool valid_shape(const Shape &s) {
+    if (s.B < 0 || s.S < 0 || s.H[0] < 1 || s.H[1] < 0 || s.H[0] > GBNORM_MAX_HEADS || s.H[1] > GBNORM_MAX_HEADS ||
+        s.D < 1 || s.D > kRopeMaxDim)
+        return false;
+    const int64_t most = (int64_t)1 << 40;
+    return s.B <= most && s.S <= most && (s.B == 0 || s.S <= most / s.B);
+}
+
+// Checks what every call has and fills the parameters that do not depend on the direction.
+int common(const gbnorm_rope_t *r, bool need_rotation, Shape *s, RopeParams *p) {
+    if (!r) return GBNORM_ERR_INVALID_ARG;
+    *s = Shape{r->batches, r->tokens, {r->heads[0], r->heads[1]}, r->dim};
+    if (!valid_shape(*s) || !valid_dtype(r->x_dtype) || !valid_dtype(r->y_dtype) || !valid_dtype(r->param_dtype))
+        return GBNORM_ERR_INVALID_ARG;
+    if (r->rot < (need_rotation ? 2 : 0) || r->rot > s->D || r->rot % 2 != 0 ||
+        (r->interleaved != 0 && r->interleaved != 1))
+        return GBNORM_ERR_INVALID_ARG;
+    std::memset(p, 0, sizeof *p);
+    p->B = s->B;
+    p->S = s->S;
+    p->heads[0] = (int)s->H[0];
+    p->heads[1] = (int)s->H[1];
+    p->D = (int)s->D;
+    p->rot = r->rot;
+    p->inter = r->interleaved;
+    p->xdt = r->x_dtype;
+    p->ydt = r->y_dtype;
+    p->pdt = r->param_dtype;
+    p->sign = 1.f;
+    if (r->rot == 0) return GBNORM_OK;
+    if (r->axes < 1 || r->axes > kRopeMaxAxes || (r->pos_dtype != GBNORM_I32 && r->pos_dtype != GBNORM_I64) ||
+        (r->axes > 1 && !r->pair_axis) || !r->inv_freq || !aligned(r->inv_freq, 4))
+        return GBNORM_ERR_INVALID_ARG;
+    const int ps = r->pos_dtype == GBNORM_I64 ? 8 : 4;
+    if (s->tokens() > 0 && (!r->positions || !aligned(r->positions, ps))) return GBNORM_ERR_INVALID_ARG;
+    const int64_t n[3] = {r->axes, s->B, s->S}, st[3] = {r->pos_axis, r->pos_batch, r->pos_token};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] < 0 || st[i] > kMostBytes / 64 / n[i])) return GBNORM_ERR_INVALID_ARG;
+    p->pos = r->positions;
+    p->pos64 = ps == 8;
+    p->pos_axis = r->axes > 1 ? r->pos_axis : 0;
+    p->pos_batch = s->B > 1 ? r->pos_batch : 0;
+    p->pos_token = s->S > 1 ? r->pos_token : 0;
+    p->inv_freq = r->inv_freq;
+    if (r->pair_axis)
+        for (int j = 0; j < r->rot / 2; ++j) {
+            if (r->pair_axis[j] >= r->axes) return GBNORM_ERR_INVALID_ARG;
+            p->axis[j / 16] |= (uint32_t)r->pair_axis[j] << (2 * (j % 16));
+        }
+    return GBNORM_OK;
+}
+
+// The rows of heads of one side of a call (x, y or dy): checked and stored.
+int take(const gbnorm_heads_t *h, const Shape &s, int dtype, bool out, RopeHeads *to, Box *box) {
+    for (int i = 0; i < 2; ++i) {
+        box[i] = flat(nullptr, 0);
+        to[i] = RopeHeads{nullptr, 0, 0, 0};
+        if (i >= s.tensors() || s.tokens() == 0) continue;
+        if (!h || !h[i].p || !aligned(h[i].p, (unsigned)elem_size(dtype)) ||
+            !make_box(h[i], s.B, s.S, s.H[i], s.D, dtype, &box[i]) || (out && !injective(box[i])))
+            return GBNORM_ERR_INVALID_ARG;
+        const int es = elem_size(dtype);
+        to[i] = RopeHeads{h[i].p, box[i].st[0] / es, box[i].st[1] / es, box[i].st[2] / es};
+    }
+    return GBNORM_OK;
+}
+
+// The plain arrays of a call, all read: parameters, statistics, positions, frequencies.
+int64_t pos_bytes(const RopeParams &p) {
+    if (!p.pos || p.B * p.S == 0) return 0;
+    int axes = 1;
+    for (int j = 0; j < p.rot / 2; ++j) axes = std::max(axes, 1 + (int)((p.axis[j / 16] >> (2 * (j % 16))) & 3u));
+    return ((axes - 1) * p.pos_axis + (p.B - 1) * p.pos_batch + (p.S - 1) * p.pos_token + 1) * (p.pos64 ? 8 : 4);
+}
+
+// outs may overlap nothing, except that outs[i] may be exactly ins[i] for i < same_n.
+bool bad_aliasing(const Box *outs, int no, const Box *ins, int ni, int same_n) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < ni; ++j) {
+            if (i == j && i < same_n && same(outs[i], ins[j])) continue;
+            if (may_overlap(outs[i], ins[j])) return true;
+        }
+        for (int j = i + 1; j < no; ++j)
+            if (may_overlap(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+thread_local const char *t_last[3] = {"", "", ""};
+
+// Passes of `at_once` heads, shared out over a grid of at most per_sm CTAs an
+// SM: warps for queries and for keys in proportion to their passes, one pass a
+// warp where that is few enough.  Returns the CTAs.
+int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, const HostDevice &d) {
+    int64_t cap = per_sm * d.sms;
+    const int64_t limit = host_grid_limit();
+    if (limit > 0 && limit < cap) cap = limit;
+    const int64_t most = cap * kRopeWarps;
+    int64_t total = 0;
+    for (int i = 0; i < 2; ++i) {
+        p->units[i] = s.tokens() * ((s.H[i] + at_once - 1) / at_once);
+        total += p->units[i];
+    }
+    if (total <= most) {
+        p->warps[0] = p->units[0];
+        p->warps[1] = p->units[1];
+    } else {
+        // both in one tensor only if there is no second; else at least one warp each
+        const double part = (double)p->units[0] / (double)total * (double)most;
+        p->warps[0] = s.tensors() == 1 ? most : std::min(most - 1, std::max<int64_t>(1, (int64_t)(part + 0.5)));
+        p->warps[1] = most - p->warps[0];
+    }
+    return (p->warps[0] + p->warps[1] + kRopeWarps - 1) / kRopeWarps;
+}
+
+int launch(const void *kernel, int64_t grid, size_t dyn, RopeParams *p, cudaStream_t st) {
+    void *args[1] = {p};
+    if (cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(kRopeCTA), args, dyn, st) != cudaSuccess)
+        return GBNORM_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
+}
+
+int any_size(int64_t D, int rot) {  // log2 of the pairs a lane holds
+    const int64_t pairs = rot / 2 + (D - rot + 1) / 2;
+    int lg = 0;
+    while (((int64_t)32 << lg) < pairs) ++lg;
+    return lg;
+}
+
+// Forward kernels: the norm with the rotation (mode kRopeRms, kRopeLn), the rotation alone.
+int run_fwd(int mode, RopeParams *p, const Shape &s, cudaStream_t st) {
+    const int what = mode == kRopeOnly ? 2 : 0;
+    HostDevice d;
+    const int e = host_device(&d);
+    if (e != GBNORM_OK) return e;
+    t_last[what] = "";
+    if (s.tokens() == 0) return GBNORM_OK;
+    t_last[what] = "any";
+    const int64_t grid = share(p, s, 1, kFwdPerSm, d);
+    return launch(kRopeFwdAny[mode][any_size(s.D, p->rot)], grid, 0, p, st);
+}
+
+int64_t bwd_rows(const Shape &s, const HostDevice &d) {  // most partial rows of any kernel
+    const int64_t units = s.tokens() * (s.H[0] + s.H[1]), cap = kBwdPerSm * d.sms;
+    return std::min(cap, (units + kRopeWarps - 1) / kRopeWarps);
+}
+size_t bwd_ws(int is_ln, const Shape &s, const HostDevice &d) {
+    const size_t b = (size_t)bwd_rows(s, d) * (size_t)s.D * (size_t)s.tensors() * 4u * (is_ln ? 2u : 1u);
+    return (b + 255u) & ~(size_t)255u;
+}
+
+int rotate(const gbnorm_rope_t *r, const gbnorm_heads_t *x, const gbnorm_heads_t *y, bool back, cudaStream_t stream) {
+    Shape s;
+    RopeParams p;
+    int e = common(r, true, &s, &p);
+    if (e != GBNORM_OK) return e;
+    if (back) {
+        std::swap(p.xdt, p.ydt);
+        p.sign = -1.f;
+    }
+    Box in[4], out[2];
+    if ((e = take(x, s, p.xdt, false, p.x, in)) != GBNORM_OK) return e;
+    if ((e = take(y, s, p.ydt, true, p.y, out)) != GBNORM_OK) return e;
+    in[2] = flat(p.pos, pos_bytes(p));
+    in[3] = flat(p.inv_freq, 2 * p.rot);
+    if (bad_aliasing(out, 2, in, 4, 2)) return GBNORM_ERR_INVALID_ARG;
+    return run_fwd(kRopeOnly, &p, s, stream);
+}
+
+}  // namespace
+}  // namespace gbn
+
+using namespace gbn;
+
+extern "C" {
+
+int qk_norm_rope_fwd(int is_layernorm, float eps, const gbnorm_rope_t *r, const gbnorm_heads_t *x,
+                     const gbnorm_heads_t *y, const void *const *gamma, const void *const *beta, float *mean,
+                     float *rstd, gbnorm_stream_t stream) {
+    Shape s;
+    RopeParams p;
+    if ((is_layernorm != 0 && is_layernorm != 1) || !std::isfinite(eps) || eps < 0.f) return GBNORM_ERR_INVALID_ARG;
+    int e = common(r, false, &s, &p);
+    if (e != GBNORM_OK) return e;
+    if (!is_layernorm) {
+        beta = nullptr;
+        mean = nullptr;
+    }
+    Box in[8], out[4];
+    if ((e = take(x, s, p.xdt, false, p.x, in)) != GBNORM_OK) return e;
+    if ((e = take(y, s, p.ydt, true, p.y, out)) != GBNORM_OK) return e;
+    const int ps = elem_size(p.pdt);
+    for (int i = 0; i < 2; ++i) {
+        p.gamma[i] = gamma && i < s.tensors() ? gamma[i] : nullptr;
+        p.beta[i] = beta && i < s.tensors() ? beta[i] : nullptr;
+        if (!aligned(p.gamma[i], (unsigned)ps) || !aligned(p.beta[i], (unsigned)ps)) return GBNORM_ERR_INVALID_ARG;
+        in[4 + i] = flat(p.gamma[i], s.D * ps);
+        in[6 + i] = flat(p.beta[i], s.D * ps);
+    }
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return GBNORM_ERR_INVALID_ARG;
+    in[2] = flat(p.pos, pos_bytes(p));
+    in[3] = flat(p.inv_freq, 2 * p.rot);
+    const int64_t stats = s.tokens() * (s.H[0] + s.H[1]) * 4;
+    out[2] = flat(mean, stats);
+    out[3] = flat(rstd, stats);
+    if (bad_aliasing(out, 4, in, 8, 2)) return GBNORM_ERR_INVALID_ARG;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.eps = eps;
+    return run_fwd(is_layernorm ? kRopeLn : kRopeRms, &p, s, stream);
+}
+
+size_t qk_norm_rope_bwd_workspace_size(int is_layernorm, int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim) {
+    const Shape s{1, tokens, {heads_q, heads_k}, dim};
+    HostDevice d;
+    if ((is_layernorm != 0 && is_layernorm != 1) || !valid_shape(s) || host_device(&d) != GBNORM_OK) return 0;
+    const size_t need = bwd_ws(is_layernorm, s, d);
+    return need > 0 ? need : 256;  // no tokens: nothing is used; 0 means an error
+}
+
+int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_heads_t *dy, const gbnorm_heads_t *x,
+                     const gbnorm_heads_t *dx, const void *const *gamma, const float *mean, const float *rstd,
+                     float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, gbnorm_stream_t stream) {
+    Shape s;
+    RopeParams p;
+    if (is_layernorm != 0 && is_layernorm != 1) return GBNORM_ERR_INVALID_ARG;
+    int e = common(r, false, &s, &p);
+    if (e != GBNORM_OK) return e;
+    if (!is_layernorm) {
+        dbeta = nullptr;
+        mean = nullptr;
+    }
+    Box in[10], out[5];
+    if ((e = take(dy, s, p.ydt, false, p.g, in)) != GBNORM_OK) return e;
+    if ((e = take(x, s, p.xdt, false, p.x, in + 2)) != GBNORM_OK) return e;
+    if ((e = take(dx, s, p.xdt, true, p.y, out)) != GBNORM_OK) return e;
+    if (s.tokens() > 0 && (!rstd || (is_layernorm && !mean))) return GBNORM_ERR_INVALID_ARG;
+    const int ps = elem_size(p.pdt);
+    for (int i = 0; i < 2; ++i) {
+        p.gamma[i] = gamma && i < s.tensors() ? gamma[i] : nullptr;
+        if (!aligned(p.gamma[i], (unsigned)ps)) return GBNORM_ERR_INVALID_ARG;
+        in[4 + i] = flat(p.gamma[i], s.D * ps);
+    }
+    for (const void *v : {(const void *)mean, (const void *)rstd, (const void *)dgamma, (const void *)dbeta})
+        if (!aligned(v, 4)) return GBNORM_ERR_INVALID_ARG;
+    const int64_t stats = s.tokens() * (s.H[0] + s.H[1]) * 4, N = s.D * s.tensors();
+    in[6] = flat(mean, stats);
+    in[7] = flat(rstd, stats);
+    in[8] = flat(p.pos, pos_bytes(p));
+    in[9] = flat(p.inv_freq, 2 * p.rot);
+    HostDevice d;
+    e = host_device(&d);
+    const size_t need = e == GBNORM_OK ? bwd_ws(is_layernorm, s, d) : 0;
+    out[2] = flat(dgamma, N * 4);
+    out[3] = flat(dbeta, N * 4);
+    out[4] = flat(workspace, (int64_t)need);
+    if (bad_aliasing(out, 5, in, 10, 2)) return GBNORM_ERR_INVALID_ARG;
+    if (e != GBNORM_OK) return e;
+    t_last[1] = "";
+    int64_t P = 0;
+    if (s.tokens() > 0) {
+        if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return GBNORM_ERR_WORKSPACE;
+        p.mean = const_cast<float *>(mean);
+        p.rstd = const_cast<float *>(rstd);
+        p.ws = static_cast<float *>(workspace);
+        p.sign = -1.f;
+        t_last[1] = "any";
+        P = share(&p, s, 1, kBwdPerSm, d);
+        e = launch(kRopeBwdAny[is_layernorm][any_size(s.D, p.rot)], P, (size_t)kRopeWarps * s.D * 4, &p, stream);
+        if (e != GBNORM_OK) return e;
+    }
+    return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, P > 0, stream);
+}
+
+int rope_fwd(const gbnorm_rope_t *r, const gbnorm_heads_t *x, const gbnorm_heads_t *y, gbnorm_stream_t stream) {
+    return rotate(r, x, y, false, stream);
+}
+
+int rope_bwd(const gbnorm_rope_t *r, const gbnorm_heads_t *dy, const gbnorm_heads_t *dx, gbnorm_stream_t stream) {
+    return rotate(r, dy, dx, true, stream);
+}
+
+int gbnorm_rope_last_variant(int what, char *buf, size_t len) {
+    if (what < 0 || what > 2 || !buf || len == 0) return GBNORM_ERR_INVALID_ARG;
+    std::snprintf(buf, len, "%s", t_last[what]);
+    return GBNORM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,140 @@
+// rope_common.cuh -- what the kernels of the head operators share: angles, the
+// share of the work that a warp takes, the backward's partial rows.
+#pragma once
+
+#include "ex_kernels.cuh"
+#include "rope_params.h"
+
+namespace gbn {
+
+// Angles.  Position times frequency is taken modulo one turn without rounding
+// either the product or the reduction: a frequency becomes F = f / (2 pi) in
+// units of 2^-64 turns, modulo one turn, and p F in 64-bit integers wraps
+// exactly where the angle does.  F is within half a unit, so the angle of
+// position p is within |p| 2^-65 turns of the product's (a product of fp32
+// values would be off by up to 2^-24 of the whole angle, 0.06 radians at position
+// 10^6).  1 / (2 pi) enters with 128 bits; the bits below them would matter from
+// frequencies of 2^87 on, which, like infinities and NaN, give NaN.
+constexpr uint64_t kTurnHi = 0x28be60db9391054aull, kTurnLo = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
+
+__device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
+    const uint32_t bits = __float_as_uint(f), ex = (bits >> 23) & 0xffu;
+    const uint64_t m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    *bad = ex >= 127 + 87;
+    // m 2^128 / (2 pi) as three words; |f| / (2 pi) turns = that * 2^(e - 128), F = that >> (64 - e)
+    const uint64_t lo = m * kTurnLo, c = __umul64hi(m, kTurnLo), mid = m * kTurnHi + c,
+                   hi = __umul64hi(m, kTurnHi) + (mid < c ? 1u : 0u);
+    const int sh = 64 - ((ex ? (int)ex : 1) - 150);  // 1 .. 213 for frequencies below 2^87
+    uint64_t r = 0;
+    auto from = [&](int s) -> uint64_t {  // bits s .. s + 63 of (hi, mid, lo), s >= 0
+        const uint64_t w[4] = {lo, mid, hi, 0};
+        uint64_t a = 0, b = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (s >> 6 == i) {
+                a = w[i];
+                b = w[i + 1];
+            }
+        const int k = s & 63;
+        return k ? (a >> k) | (b << (64 - k)) : a;
+    };
+    r = from(sh) + (from(sh - 1) & 1u);  // to nearest
+    return (bits >> 31) ? 0 - r : r;
+}
+
+// The pairs whose angles a lane computes: lane, lane + 32, ... (N of them).
+template <int N> struct RopeAngles {
+    uint64_t f[N];
+    uint32_t axis, bad;  // two bits and one bit a pair
+    __device__ __forceinline__ void init(const RopeParams &p, int lane) {
+        axis = bad = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int j = lane + 32 * i;
+            f[i] = 0;
+            if (2 * j >= p.rot) continue;
+            bool b;
+            f[i] = rope_turns(__ldg(p.inv_freq + j), &b);
+            axis |= ((p.axis[j >> 4] >> (2 * (j & 15))) & 3u) << (2 * i);
+            bad |= (uint32_t)b << i;
+        }
+    }
+    // cos and sin of pair lane + 32 i at the token whose axis-0 position has index `at`.
+    __device__ __forceinline__ void get(const RopeParams &p, int64_t at, int i, float *c, float *s) const {
+        const int64_t q = at + (int64_t)((axis >> (2 * i)) & 3u) * p.pos_axis;
+        const int64_t pos = p.pos64 ? __ldg(static_cast<const long long *>(p.pos) + q)
+                                    : (int64_t)__ldg(static_cast<const int *>(p.pos) + q);
+        turn((uint64_t)pos * f[i], i, p.sign, c, s);
+    }
+    // sincospif takes half turns: a multiple of 2^-63 of one, exact down to angles that do not matter in fp32.
+    __device__ __forceinline__ void turn(uint64_t u, int i, float sign, float *c, float *s) const {
+        sincospif(__ll2float_rn((long long)u) * 1.0842021724855044e-19f, s, c);  // 2^-63
+        *s *= sign;
+        if ((bad >> i) & 1u) *s = *c = __int_as_float(0x7fffffff);
+    }
+};
+
+// A warp's share of the passes over one of the two tensors: contiguous, so
+// that the angles of a token serve all its heads.
+struct RopeWalk {
+    int64_t u, end;  // passes left: [u, end)
+    int64_t t, b, s; // token
+    int blk, np;     // pass within the token, passes a token
+    int r;           // 0 queries, 1 keys
+    __device__ __forceinline__ RopeWalk(const RopeParams &p) {
+        int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+        r = w >= p.warps[0];
+        if (r) w -= p.warps[0];
+        const int64_t W = p.warps[r], U = p.units[r];
+        if (w >= W) {
+            u = end = t = b = s = 0;
+            blk = 0;
+            np = 1;
+            return;
+        }
+        const int64_t each = U / W, more = U % W;
+        u = each * w + (w < more ? w : more);
+        end = u + each + (w < more ? 1 : 0);
+        np = (int)(U / (p.B * p.S));
+        t = u / np;
+        blk = (int)(u - t * np);
+        b = t / p.S;
+        s = t - b * p.S;
+    }
+    __device__ __forceinline__ bool more() const { return u < end; }
+    // To the next pass; true if it belongs to another token.
+    __device__ __forceinline__ bool next(const RopeParams &p) {
+        ++u;
+        if (++blk < np) return false;
+        blk = 0;
+        ++t;
+        if (++s == p.S) {
+            s = 0;
+            ++b;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int64_t at(const RopeHeads &h) const { return b * h.batch + s * h.token; }
+};
+
+// The backward's column sums of a CTA: acc[warp][D] in shared memory, each
+// warp's own row filled, added in the order of the warps into the CTA's
+// partial row [2][D] (or [1][D] without keys) of block `which`.
+__device__ __forceinline__ void rope_partial(const RopeParams &p, const float *acc, int which) {
+    const int n = p.D * (p.heads[1] ? 2 : 1);
+    float *row = p.ws + ((int64_t)which * gridDim.x + blockIdx.x) * n;
+    const int64_t first = (int64_t)blockIdx.x * kRopeWarps;
+    // warps below `mid` hold sums of queries, those below `top` of keys
+    const int64_t q = p.warps[0] - first, k = p.warps[0] + p.warps[1] - first;
+    const int mid = q < 0 ? 0 : q > kRopeWarps ? kRopeWarps : (int)q, top = k > kRopeWarps ? kRopeWarps : (int)k;
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += kRopeCTA) {
+        const bool keys = c >= p.D;
+        float v = 0.f;
+        for (int w = keys ? mid : 0; w < (keys ? top : mid); ++w) v += acc[w * p.D + (keys ? c - p.D : c)];
+        row[c] = v;
+    }
+    __syncthreads();  // acc may be filled again
+}
+
+}  // namespace gbn

@@ -1,0 +1,54 @@
+// rope_params.h -- argument block and launch limits of the head operators:
+// norms of queries and keys for each head with the position rotation, their
+// backward, the rotation alone (include/gbnorm.h).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gbn {
+
+constexpr int kRopeMaxDim = 1024;  // largest head (GBNORM_MAX_HEAD_DIM)
+constexpr int kRopeMaxAxes = 4;    // GBNORM_MAX_AXES (two bits a pair in RopeParams::axis)
+constexpr int kRopeCTA = 256;      // threads of a CTA
+constexpr int kRopeWarps = kRopeCTA / 32;
+
+// Heads of one tensor: element i of head h of token (b, s) at
+// p + (b * batch + s * token + h * head + i) elements.
+struct RopeHeads {
+    void *p;
+    int64_t batch, token, head;
+};
+
+// Index 0: queries, 1: keys.
+struct RopeParams {
+    RopeHeads x[2];        // forward: input; backward: the input of the forward
+    RopeHeads y[2];        // forward: output; backward: dx
+    RopeHeads g[2];        // backward: gradient of the forward's output
+    const void *gamma[2];  // [D] pdt, or null (1)
+    const void *beta[2];   // [D] pdt, or null (0; LayerNorm only)
+    float *mean, *rstd;    // [B * S, H0 + H1] or null; the backward reads them
+    float *ws;             // backward: [2][P][2 D] partial rows (second block: dbeta)
+    const void *pos;       // positions, strides in elements
+    const float *inv_freq; // [rot / 2]
+    int64_t pos_axis, pos_batch, pos_token;
+    int64_t B, S;
+    int64_t units[2];      // passes over all tokens (a pass: the heads one warp works on at once)
+    int64_t warps[2];      // warps of the grid that take them
+    int heads[2];
+    int D, rot;
+    int inter;             // pairs (2j, 2j + 1), else (j, j + rot / 2)
+    int pos64;
+    int xdt, ydt, pdt;
+    float eps, sign;       // sign -1: the rotation's transpose
+    uint32_t axis[kRopeMaxDim / 2 / 16];  // the axis of pair j: bits 2 (j mod 16) of word j / 16
+};
+
+enum RopeMode : int { kRopeOnly = 0, kRopeRms = 1, kRopeLn = 2 };
+
+// Element by element, any alignment, stride, type and size: [mode][log2 of pairs a lane].
+constexpr int kRopeAnySizes = 5;
+extern const void *const kRopeFwdAny[3][kRopeAnySizes];
+extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
+
+}  // namespace gbn

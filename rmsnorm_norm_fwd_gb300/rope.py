@@ -1,0 +1,292 @@
+"""Binding of the head operators (qk_norm_rope_fwd, qk_norm_rope_bwd, rope_fwd
+and rope_bwd of include/gbnorm.h).
+
+Argument marshalling only, as in ``binding``: tensors are checked, outputs that
+the caller does not pass are allocated with torch's caching allocator, and the
+call goes to the C ABI on torch's current stream of the tensors' device, or on
+the one given as the keyword ``stream``, which every operator takes.
+
+Queries and keys are [tokens, heads, D] or [batches, tokens, heads, D] with any
+strides but the last, which is 1: parts of a packed projection, or tensors with
+heads outside tokens (transposed).  Positions are int32 or int64, one for each
+token ([tokens], or [batches, tokens] or [tokens] with batches); with several
+axes these come first ([axes, tokens], [axes, batches, tokens]).
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from .binding import DTYPE_CODE, GbnormError, _check, _f, _int, _i64, _sz, _vp, lib
+from .q8 import _on_stream, _raw_stream
+
+lib.qk_norm_rope_fwd.argtypes = [_int, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.qk_norm_rope_bwd_workspace_size.argtypes = [_int, _i64, _i64, _i64, _i64]
+lib.qk_norm_rope_bwd_workspace_size.restype = _sz
+lib.qk_norm_rope_bwd.argtypes = [_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.rope_fwd.argtypes = lib.rope_bwd.argtypes = [_vp, _vp, _vp, _vp]
+lib.gbnorm_rope_last_variant.argtypes = [_int, ctypes.c_char_p, _sz]
+for _fn in ("qk_norm_rope_fwd", "qk_norm_rope_bwd", "rope_fwd", "rope_bwd", "gbnorm_rope_last_variant"):
+    getattr(lib, _fn).restype = _int
+
+MAX_AXES = 4
+_HEADS = struct.Struct("8q").pack    # two gbnorm_heads_t
+_ROPE = struct.Struct("5q8i6q").pack  # gbnorm_rope_t
+_TWO = struct.Struct("2q").pack
+_POS_CODE = {torch.int32: 0, torch.int64: 1}
+
+
+class Rotary:
+    """The rotation of a model's heads, made once (see ``rotary``): float32
+    frequencies on the device, the pairing, and the axis of each pair."""
+
+    __slots__ = ("inv_freq", "interleaved", "axes", "rot", "dev", "pair_axis", "_axis_at")
+
+    def __init__(self, inv_freq, interleaved, axes, pair_axis):
+        self.inv_freq, self.interleaved, self.axes = inv_freq, bool(interleaved), axes
+        self.rot, self.dev = 2 * inv_freq.numel(), inv_freq.get_device()
+        self.pair_axis = pair_axis
+        self._axis_at = ctypes.addressof(pair_axis) if pair_axis is not None else 0
+
+
+def rotary(inv_freq, interleaved: bool = False, sections=None, pair_axis=None) -> Rotary:
+    """A rotation of 2 len(inv_freq) elements of each head: pair j turns by
+    position * inv_freq[j] radians (float32, on the GPU; kept, not copied).
+    Pairs are (j, j + len(inv_freq)), or (2 j, 2 j + 1) where interleaved.  With
+    several position axes, sections gives the number of consecutive pairs that
+    follow each axis, or pair_axis the axis of every pair."""
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda and inv_freq.dim() == 1 and inv_freq.numel() > 0
+            and inv_freq.dtype == torch.float32 and inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous 1-D float32 CUDA tensor with at least one element")
+    n = inv_freq.numel()
+    if sections is not None and pair_axis is not None:
+        raise ValueError("give sections or pair_axis, not both")
+    if sections is not None:
+        sections = [int(w) for w in sections]
+        if not sections or min(sections) < 0 or sum(sections) != n:
+            raise ValueError(f"sections must be numbers of pairs that sum to {n}")
+        pair_axis, axes = [a for a, w in enumerate(sections) for _ in range(w)], len(sections)
+    elif pair_axis is not None:
+        pair_axis = [int(a) for a in pair_axis]
+        if len(pair_axis) != n or min(pair_axis) < 0:
+            raise ValueError(f"pair_axis must be an axis for each of the {n} pairs")
+        axes = max(pair_axis) + 1
+    else:
+        axes = 1
+    if axes > MAX_AXES:
+        raise ValueError(f"at most {MAX_AXES} axes")
+    return Rotary(inv_freq, interleaved, axes, (ctypes.c_uint8 * n)(*pair_axis) if axes > 1 else None)
+
+
+class _Call:
+    """Checks of one call's tensors against its first one (the queries), and its launch on that one's device."""
+
+    __slots__ = ("dev", "q", "k", "B", "S", "D", "hq", "hk")
+
+    def __init__(self, name, q, k):
+        self.dev = q.get_device()
+        if not q.is_cuda or self.dev < 0 or q.dim() not in (3, 4):
+            raise ValueError(f"{name}q must be a CUDA tensor [tokens, heads, D] or [batches, tokens, heads, D]")
+        self.q = q.shape
+        *b, self.S, self.hq, self.D = q.shape
+        self.B = b[0] if b else 1
+        self.k, self.hk = None, 0
+        if k is not None:
+            self.k, self.hk = k.shape, k.shape[-2] if k.dim() >= 2 else 0
+            if k.shape != (*b, self.S, self.hk, self.D):
+                raise ValueError(f"{name}k must have the batches, tokens and head size of {name}q")
+            if self.hk == 0:
+                raise ValueError("keys without heads are given as None")
+
+    def heads(self, name, q, k, dtype=None):
+        """Two gbnorm_heads_t."""
+        return _HEADS(*self._one(name + "q", q, self.q, dtype),
+                      *(self._one(name + "k", k, self.k, dtype or q.dtype) if self.k is not None else (0, 0, 0, 0)))
+
+    def _one(self, name, t, shape, dtype):
+        if t is None or t.shape != shape or t.get_device() != self.dev:
+            raise ValueError(f"{name} must be a {list(shape)} CUDA tensor on device {self.dev}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must have dtype {dtype}")
+        st = t.stride()
+        if st[-1] != 1 and self.D > 1:
+            raise ValueError(f"{name} must have unit stride in its last dimension")
+        return t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2]
+
+    def out(self, given, shape, dtype):
+        return given if given is not None or shape is None else torch.empty(shape, device=self.dev, dtype=dtype)
+
+    def pair(self, name, q, k, n, dtype):
+        """Two pointers to [n] parameters."""
+        for w, t in (("q", q), ("k", k)):
+            if t is not None and (t.shape != (n,) or t.get_device() != self.dev or t.dtype != dtype
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name}_{w} must be a contiguous 1-D CUDA {dtype} tensor of {n} elements on device "
+                                 f"{self.dev}")
+        return _TWO(q.data_ptr() if q is not None else 0, k.data_ptr() if k is not None and self.hk else 0)
+
+    def flat(self, name, t, shape):
+        if t is None:
+            return None
+        if t.shape != shape or t.get_device() != self.dev or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {list(shape)} float32 CUDA tensor on device {self.dev}")
+        return t.data_ptr()
+
+    def stats_shape(self):
+        return (*self.q[:-2], self.hq + self.hk)
+
+    def rope(self, positions, rotary, xdt, ydt, pdt):
+        """gbnorm_rope_t."""
+        head = (self.B, self.S, self.hq, self.hk, self.D, _code(xdt), _code(ydt), _code(pdt))
+        if rotary is None:
+            if positions is not None:
+                raise ValueError("positions without a rotation")
+            return _ROPE(*head, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0)
+        if rotary.rot > self.D:
+            raise ValueError(f"{rotary.rot} rotated elements in heads of {self.D}")
+        if positions is None or not positions.is_cuda or positions.get_device() != self.dev or rotary.dev != self.dev:
+            raise ValueError(f"positions and frequencies must be on device {self.dev}")
+        code = _POS_CODE.get(positions.dtype)
+        if code is None:
+            raise ValueError("positions must be int32 or int64")
+        shape, st, axis = tuple(positions.shape), positions.stride(), 0
+        if rotary.axes > 1:
+            if not shape or shape[0] != rotary.axes:
+                raise ValueError(f"positions must have {rotary.axes} axes first")
+            shape, axis, st = shape[1:], st[0], st[1:]
+        if shape == (self.S,):
+            batch, token = 0, st[0]
+        elif len(self.q) == 4 and shape == (self.B, self.S):
+            batch, token = st
+        else:
+            raise ValueError(f"positions must have one value for each of the tokens {list(self.q[:-2])}")
+        return _ROPE(*head, rotary.interleaved, rotary.rot, rotary.axes, code, 0, positions.data_ptr(), axis, batch,
+                     token, rotary.inv_freq.data_ptr(), rotary._axis_at)
+
+    def on_device(self, fn, *args):
+        """fn(*args) with the tensors' device current."""
+        if self.dev == torch.cuda.current_device():
+            return fn(*args)
+        with torch.cuda.device(self.dev):
+            return fn(*args)
+
+    def go(self, name, fn, *args):
+        """fn(*args, stream) with the tensors' device current, on its current stream."""
+        _check(name, self.on_device(fn, *args, _raw_stream(self.dev)))
+
+
+def _code(dtype):
+    code = DTYPE_CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"tensors must be float32, float16 or bfloat16, not {dtype}")
+    return code
+
+
+def _param_dtype(default, *params):
+    return next((t.dtype for t in params if t is not None), default)
+
+
+@_on_stream
+def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, positions=None,
+                     rotary: Rotary | None = None, beta_q=None, beta_k=None, y_dtype=None, yq=None, yk=None, mean=None,
+                     rstd=None, save_stats: bool = True):
+    """Each head of the queries q and keys k (None: queries alone) normalised
+    by itself (gamma, beta of D elements, None: 1, 0; all of one dtype), then
+    rotated by its token's position (rotary None: the norm alone).  Returns
+    (yq, yk, mean, rstd): outputs of y_dtype (default q's) with q's and k's
+    shapes; mean and rstd float32 [..., heads of q and of k], mean None for
+    RMSNorm, both None without save_stats unless given.  yq may be q itself
+    and yk k itself."""
+    c = _Call("", q, k)
+    dt = yq.dtype if yq is not None else y_dtype or q.dtype
+    yq, yk = c.out(yq, c.q, dt), c.out(yk, c.k, dt)
+    if save_stats:
+        if rstd is None:
+            rstd = torch.empty(c.stats_shape(), device=c.dev, dtype=torch.float32)
+        if is_layernorm and mean is None:
+            mean = torch.empty(c.stats_shape(), device=c.dev, dtype=torch.float32)
+    if not is_layernorm:
+        mean = beta_q = beta_k = None
+    pdt = _param_dtype(q.dtype, gamma_q, gamma_k, beta_q, beta_k)
+    c.go("qk_norm_rope_fwd", lib.qk_norm_rope_fwd, int(bool(is_layernorm)), eps,
+         c.rope(positions, rotary, q.dtype, dt, pdt), c.heads("", q, k), c.heads("y", yq, yk),
+         c.pair("gamma", gamma_q, gamma_k, c.D, pdt), c.pair("beta", beta_q, beta_k, c.D, pdt),
+         c.flat("mean", mean, c.stats_shape()), c.flat("rstd", rstd, c.stats_shape()))
+    return yq, yk, mean, rstd
+
+
+def qk_norm_rope_bwd_workspace_size(is_layernorm: bool, tokens: int, heads_q: int, heads_k: int, dim: int) -> int:
+    return int(lib.qk_norm_rope_bwd_workspace_size(int(bool(is_layernorm)), tokens, heads_q, heads_k, dim))
+
+
+@_on_stream
+def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean, rstd, positions=None,
+                     rotary: Rotary | None = None, dq=None, dk=None, dgamma=None, dbeta=None, workspace=None,
+                     need_dgamma: bool = True, need_dbeta: bool = True):
+    """Backward of qk_norm_rope_fwd from its inputs q and k and its saved
+    statistics.  Returns (dq, dk, dgamma, dbeta): dq and dk of q's dtype, dgamma
+    and dbeta float32 [2, D] (queries, keys; [1, D] without keys), None where not
+    needed, dbeta LayerNorm only.  dq may be dyq itself and dk dyk itself."""
+    c = _Call("", q, k)
+    dq, dk = c.out(dq, c.q, q.dtype), c.out(dk, c.k, q.dtype)
+    sums = (2 if c.hk else 1, c.D)
+    if dgamma is None and need_dgamma:
+        dgamma = torch.empty(sums, device=c.dev, dtype=torch.float32)
+    if not is_layernorm:
+        dbeta = mean = None
+    elif dbeta is None and need_dbeta:
+        dbeta = torch.empty(sums, device=c.dev, dtype=torch.float32)
+    if rstd is None or (is_layernorm and mean is None):
+        raise ValueError("rstd (and mean for LayerNorm) of the forward are needed")
+    if workspace is None:
+        need = c.on_device(lib.qk_norm_rope_bwd_workspace_size, int(bool(is_layernorm)), c.B * c.S, c.hq, c.hk, c.D)
+        if need == 0:
+            raise GbnormError("qk_norm_rope_bwd_workspace_size", 2)
+        workspace = torch.empty(need, device=c.dev, dtype=torch.uint8)
+    elif not workspace.is_contiguous() or workspace.get_device() != c.dev:
+        raise ValueError(f"workspace must be contiguous on device {c.dev}")
+    pdt = _param_dtype(q.dtype, gamma_q, gamma_k)
+    c.go("qk_norm_rope_bwd", lib.qk_norm_rope_bwd, int(bool(is_layernorm)),
+         c.rope(positions, rotary, q.dtype, dyq.dtype, pdt), c.heads("dy", dyq, dyk), c.heads("", q, k),
+         c.heads("d", dq, dk, q.dtype), c.pair("gamma", gamma_q, gamma_k, c.D, pdt),
+         c.flat("mean", mean, c.stats_shape()), c.flat("rstd", rstd, c.stats_shape()), c.flat("dgamma", dgamma, sums),
+         c.flat("dbeta", dbeta, sums), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dq, dk, dgamma, dbeta
+
+
+@_on_stream
+def rope_fwd(q, k, positions, rotary: Rotary, y_dtype=None, yq=None, yk=None):
+    """The heads of q and k (None: of q alone) rotated by their tokens'
+    positions.  Returns (yq, yk) of y_dtype (default q's); yq may be q itself
+    and yk k itself."""
+    c = _Call("", q, k)
+    dt = yq.dtype if yq is not None else y_dtype or q.dtype
+    yq, yk = c.out(yq, c.q, dt), c.out(yk, c.k, dt)
+    if rotary is None:
+        raise ValueError("rotary is needed")
+    c.go("rope_fwd", lib.rope_fwd, c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k),
+         c.heads("y", yq, yk))
+    return yq, yk
+
+
+@_on_stream
+def rope_bwd(dyq, dyk, positions, rotary: Rotary, dx_dtype=None, dq=None, dk=None):
+    """Backward of rope_fwd: gradients turned back.  Returns (dq, dk) of
+    dx_dtype (default dyq's); dq may be dyq itself and dk dyk itself."""
+    c = _Call("dy", dyq, dyk)
+    dt = dq.dtype if dq is not None else dx_dtype or dyq.dtype
+    dq, dk = c.out(dq, c.q, dt), c.out(dk, c.k, dt)
+    if rotary is None:
+        raise ValueError("rotary is needed")
+    c.go("rope_bwd", lib.rope_bwd, c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype), c.heads("dy", dyq, dyk),
+         c.heads("d", dq, dk))
+    return dq, dk
+
+
+def rope_last_variant(what: int) -> str:
+    """The kernel this thread's last qk_norm_rope_fwd (0), qk_norm_rope_bwd (1) or rotation (2) launched ("" for none)."""
+    buf = ctypes.create_string_buffer(64)
+    _check("gbnorm_rope_last_variant", lib.gbnorm_rope_last_variant(what, buf, 64))
+    return buf.value.decode()
