@@ -60,7 +60,7 @@ template <int MODE, int N>
 __global__ void __launch_bounds__(kRopeCTA) rope_fwd_any(const RopeParams p) {
     const int lane = threadIdx.x & 31;
     RopeWalk w(p);
-    if (!w.more()) return;
+    if (!w.left) return;
     const RopeSlots<N> sl(p, lane);
     RopeAngles<N> ang;
     ang.init(p, lane);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kRopeCTA) rope_fwd_any(const RopeParams p) {
         if (p.beta[w.r]) rope_any_load(sl, p.beta[w.r], 0, p.pdt, ba, bb);
     const float inv = 1.f / (float)p.D;
     const RopeHeads x = p.x[w.r], y = p.y[w.r];
-    for (bool fresh = true; w.more(); fresh = w.next(p)) {
+    for (bool fresh = true; w.left; fresh = w.next(p)) {
         if (fresh)
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kRopeCTA) rope_fwd_any(const RopeParams p) {
             group_sum<32, 1>(sq);
             const float rstd = rsqrtf(sq[0] * inv + p.eps);
             if (lane == 0) {
-                const int64_t at = w.t * (p.heads[0] + p.heads[1]) + (w.r ? p.heads[0] : 0) + w.blk;
+                const int64_t at = w.stat(p) + w.blk;
                 if (p.rstd) p.rstd[at] = rstd;
                 if (MODE == kRopeLn && p.mean) p.mean[at] = sum[0];
             }
@@ -122,13 +122,13 @@ __global__ void __launch_bounds__(kRopeCTA) rope_fwd_any(const RopeParams p) {
 template <bool LN, int N>
 __global__ void __launch_bounds__(kRopeCTA) rope_bwd_any(const RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
-    extern __shared__ float rope_acc[];  // [kRopeWarps][D]
+    extern __shared__ __align__(16) float rope_acc[];  // [kRopeWarps][D]
     const int lane = threadIdx.x & 31;
     RopeWalk w(p);
     const RopeSlots<N> sl(p, lane);
     float ga[N], gb[N], c[N], s[N], da[N], db[N], ea[N], eb[N];
     RopeAngles<N> ang;
-    if (w.more()) {
+    if (w.left) {
         ang.init(p, lane);
         rope_any_load(sl, p.gamma[w.r], 0, p.pdt, ga, gb);
     }
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kRopeCTA) rope_bwd_any(const RopeParams p) {
     for (int i = 0; i < N; ++i) da[i] = db[i] = ea[i] = eb[i] = 0.f;
     const float inv = 1.f / (float)p.D;
     const RopeHeads x = p.x[w.r], g = p.g[w.r], y = p.y[w.r];
-    for (bool fresh = true; w.more(); fresh = w.next(p)) {
+    for (bool fresh = true; w.left; fresh = w.next(p)) {
         if (fresh)
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kRopeCTA) rope_bwd_any(const RopeParams p) {
         float a[N], b[N], u[N], v[N];
         rope_any_load(sl, x.p, w.at(x) + w.blk * x.head, p.xdt, a, b);
         rope_any_load(sl, g.p, w.at(g) + w.blk * g.head, p.ydt, u, v);
-        const int64_t at = w.t * (p.heads[0] + p.heads[1]) + (w.r ? p.heads[0] : 0) + w.blk;
+        const int64_t at = w.stat(p) + w.blk;
         const float rstd = p.rstd[at], mean = LN ? p.mean[at] : 0.f;
         float sum[2] = {0.f, 0.f};
 #pragma unroll

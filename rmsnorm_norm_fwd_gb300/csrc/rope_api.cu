@@ -21,7 +21,7 @@ bool aligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p
 
 // CTAs an SM of the persistent grids.  The backward's also bounds its partial
 // rows, so that the workspace depends on the shape alone.
-constexpr int64_t kFwdPerSm = 8, kBwdPerSm = 2;
+constexpr int64_t kFwdPerSm = 2, kBwdPerSm = 2;
 
 // A tensor of heads as the aliasing check sees it, in bytes: runs of `run`
 // bytes at p + i0 st[0] + i1 st[1] + i2 st[2], i < n; extents of one element
@@ -114,8 +114,7 @@ bool valid_shape(const Shape &s) {
     if (s.B < 0 || s.S < 0 || s.H[0] < 1 || s.H[1] < 0 || s.H[0] > GBNORM_MAX_HEADS || s.H[1] > GBNORM_MAX_HEADS ||
         s.D < 1 || s.D > kRopeMaxDim)
         return false;
-    const int64_t most = (int64_t)1 << 40;
-    return s.B <= most && s.S <= most && (s.B == 0 || s.S <= most / s.B);
+    return s.B <= INT32_MAX && s.S <= INT32_MAX && s.tokens() <= (int64_t)1 << 40;
 }
 
 // Checks what every call has and fills the parameters that do not depend on the direction.
@@ -202,7 +201,8 @@ thread_local const char *t_last[3] = {"", "", ""};
 
 // Passes of `at_once` heads, shared out over a grid of at most per_sm CTAs an
 // SM: warps for queries and for keys in proportion to their passes, one pass a
-// warp where that is few enough.  Returns the CTAs.
+// warp where that is few enough.  Returns the CTAs, -1 if a warp's passes do
+// not fit its counter.
 int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, const HostDevice &d) {
     int64_t cap = per_sm * d.sms;
     const int64_t limit = host_grid_limit();
@@ -210,7 +210,8 @@ int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, co
     const int64_t most = cap * kRopeWarps;
     int64_t total = 0;
     for (int i = 0; i < 2; ++i) {
-        p->units[i] = s.tokens() * ((s.H[i] + at_once - 1) / at_once);
+        p->passes[i] = (int)((s.H[i] + at_once - 1) / at_once);
+        p->units[i] = s.tokens() * p->passes[i];
         total += p->units[i];
     }
     if (total <= most) {
@@ -222,6 +223,8 @@ int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, co
         p->warps[0] = s.tensors() == 1 ? most : std::min(most - 1, std::max<int64_t>(1, (int64_t)(part + 0.5)));
         p->warps[1] = most - p->warps[0];
     }
+    for (int i = 0; i < 2; ++i)
+        if (p->warps[i] > 0 && p->units[i] / p->warps[i] >= INT32_MAX) return -1;
     return (p->warps[0] + p->warps[1] + kRopeWarps - 1) / kRopeWarps;
 }
 
@@ -232,11 +235,54 @@ int launch(const void *kernel, int64_t grid, size_t dyn, RopeParams *p, cudaStre
     return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
 }
 
+// A kernel of a call: rows of lanes (or, element by element, warps) a head.
+struct Kernel {
+    const void *f;
+    const char *name;
+    int heads;  // of a pass
+};
+
 int any_size(int64_t D, int rot) {  // log2 of the pairs a lane holds
     const int64_t pairs = rot / 2 + (D - rot + 1) / 2;
     int lg = 0;
     while (((int64_t)32 << lg) < pairs) ++lg;
     return lg;
+}
+
+// Elements of the vectors that all tensors of a call move as: every head and
+// chunk starts on a vector, the rotated part holds whole ones.  0: none.
+int vector_of(const RopeParams &p, bool back) {
+    if (p.xdt != p.ydt) return 0;
+    const int es = elem_size(p.xdt);
+    for (int v = 16 / es; v >= 4; v /= 2) {
+        bool ok = p.D % v == 0 && (p.inter ? p.rot % v : p.rot / 2 % v) == 0;
+        for (const RopeHeads *t : {p.x, p.y, back ? p.g : p.x})
+            for (int i = 0; i < 2; ++i)
+                ok = ok && aligned(t[i].p, (unsigned)(v * es)) && (t[i].batch | t[i].token | t[i].head) % v == 0;
+        for (int i = 0; i < 2; ++i)  // parameters are read 16 bytes (fp32) or 8 at a time
+            for (const void *q : {p.gamma[i], p.beta[i]}) ok = ok && aligned(q, p.pdt == GBNORM_F32 ? 16 : 8);
+        if (ok) return v;
+    }
+    return 0;
+}
+
+// mode: a RopeMode, or -1 - is_layernorm for the backward.
+Kernel pick(int mode, const RopeParams &p) {
+#define GBN_T(M) {kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, kRopeVec_##M##_bf16v4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8}
+    static const void *const *const tables[5][5] = {GBN_T(rot), GBN_T(rms), GBN_T(ln), GBN_T(brms), GBN_T(bln)};
+#undef GBN_T
+    static const char *const names[2][kRopeVecLanes] = {{"vec4x4", "vec4x8", "vec4x16", "vec4x32"},
+                                                        {"vec8x4", "vec8x8", "vec8x16", "vec8x32"}};
+    const int v = vector_of(p, mode < 0);
+    if (v) {
+        const int chunks = p.D / v, rot = p.rot / v;
+        const int slots = p.inter ? (chunks + 1) / 2 : rot / 2 + (chunks - rot + 1) / 2;
+        for (int l = 0; l < kRopeVecLanes; ++l)
+            if (slots <= 4 << l)
+                return {tables[mode < 0 ? 2 - mode : mode][p.xdt + (v == 8 ? 2 : 0)][l], names[v == 8][l], 8 >> l};
+    }
+    const int n = any_size(p.D, p.rot);
+    return {mode < 0 ? kRopeBwdAny[-1 - mode][n] : kRopeFwdAny[mode][n], "any", 1};
 }
 
 // Forward kernels: the norm with the rotation (mode kRopeRms, kRopeLn), the rotation alone.
@@ -247,9 +293,11 @@ int run_fwd(int mode, RopeParams *p, const Shape &s, cudaStream_t st) {
     if (e != GBNORM_OK) return e;
     t_last[what] = "";
     if (s.tokens() == 0) return GBNORM_OK;
-    t_last[what] = "any";
-    const int64_t grid = share(p, s, 1, kFwdPerSm, d);
-    return launch(kRopeFwdAny[mode][any_size(s.D, p->rot)], grid, 0, p, st);
+    const Kernel k = pick(mode, *p);
+    const int64_t grid = share(p, s, k.heads, kFwdPerSm, d);
+    if (grid < 0) return GBNORM_ERR_UNSUPPORTED;
+    t_last[what] = k.name;
+    return launch(k.f, grid, 0, p, st);
 }
 
 int64_t bwd_rows(const Shape &s, const HostDevice &d) {  // most partial rows of any kernel
@@ -376,9 +424,11 @@ int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_head
         p.rstd = const_cast<float *>(rstd);
         p.ws = static_cast<float *>(workspace);
         p.sign = -1.f;
-        t_last[1] = "any";
-        P = share(&p, s, 1, kBwdPerSm, d);
-        e = launch(kRopeBwdAny[is_layernorm][any_size(s.D, p.rot)], P, (size_t)kRopeWarps * s.D * 4, &p, stream);
+        const Kernel k = pick(-1 - is_layernorm, p);
+        P = share(&p, s, k.heads, kBwdPerSm, d);
+        if (P < 0) return GBNORM_ERR_UNSUPPORTED;
+        t_last[1] = k.name;
+        e = launch(k.f, P, (size_t)kRopeWarps * s.D * 4, &p, stream);
         if (e != GBNORM_OK) return e;
     }
     return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, P > 0, stream);

@@ -77,44 +77,40 @@ template <int N> struct RopeAngles {
 // A warp's share of the passes over one of the two tensors: contiguous, so
 // that the angles of a token serve all its heads.
 struct RopeWalk {
-    int64_t u, end;  // passes left: [u, end)
-    int64_t t, b, s; // token
-    int blk, np;     // pass within the token, passes a token
-    int r;           // 0 queries, 1 keys
+    int left;   // passes to go, this one included
+    int b, s;   // token
+    int blk;    // pass within the token
+    int r;      // 0 queries, 1 keys
     __device__ __forceinline__ RopeWalk(const RopeParams &p) {
         int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
         r = w >= p.warps[0];
         if (r) w -= p.warps[0];
         const int64_t W = p.warps[r], U = p.units[r];
-        if (w >= W) {
-            u = end = t = b = s = 0;
-            blk = 0;
-            np = 1;
-            return;
-        }
-        const int64_t each = U / W, more = U % W;
-        u = each * w + (w < more ? w : more);
-        end = u + each + (w < more ? 1 : 0);
-        np = (int)(U / (p.B * p.S));
-        t = u / np;
-        blk = (int)(u - t * np);
-        b = t / p.S;
-        s = t - b * p.S;
+        left = b = s = blk = 0;
+        if (w >= W) return;
+        const int64_t each = U / W, more = U % W, u = each * w + (w < more ? w : more);
+        left = (int)(each + (w < more ? 1 : 0));
+        const int64_t t = u / p.passes[r];
+        blk = (int)(u - t * p.passes[r]);
+        b = (int)(t / p.S);
+        s = (int)(t - b * p.S);
     }
-    __device__ __forceinline__ bool more() const { return u < end; }
     // To the next pass; true if it belongs to another token.
     __device__ __forceinline__ bool next(const RopeParams &p) {
-        ++u;
-        if (++blk < np) return false;
+        --left;
+        if (++blk < p.passes[r]) return false;
         blk = 0;
-        ++t;
-        if (++s == p.S) {
+        if (++s == (int)p.S) {
             s = 0;
             ++b;
         }
         return true;
     }
     __device__ __forceinline__ int64_t at(const RopeHeads &h) const { return b * h.batch + s * h.token; }
+    // Index of the token's first statistic of this tensor.
+    __device__ __forceinline__ int64_t stat(const RopeParams &p) const {
+        return (b * p.S + s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0);
+    }
 };
 
 // The backward's column sums of a CTA: acc[warp][D] in shared memory, each

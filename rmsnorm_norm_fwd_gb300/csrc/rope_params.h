@@ -35,6 +35,7 @@ struct RopeParams {
     int64_t B, S;
     int64_t units[2];      // passes over all tokens (a pass: the heads one warp works on at once)
     int64_t warps[2];      // warps of the grid that take them
+    int passes[2];         // of a token
     int heads[2];
     int D, rot;
     int inter;             // pairs (2j, 2j + 1), else (j, j + rot / 2)
@@ -50,5 +51,19 @@ enum RopeMode : int { kRopeOnly = 0, kRopeRms = 1, kRopeLn = 2 };
 constexpr int kRopeAnySizes = 5;
 extern const void *const kRopeFwdAny[3][kRopeAnySizes];
 extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
+
+// On vectors: [lanes a head: 4, 8, 16, 32], for each direction and norm (rot: the rotation alone; b: backward) and type
+// and elements a vector.
+constexpr int kRopeVecLanes = 4;
+#define GBN_ROPE_VEC(M) \
+    extern const void *const kRopeVec_##M##_bf16v8[kRopeVecLanes], *const kRopeVec_##M##_f16v8[kRopeVecLanes], \
+        *const kRopeVec_##M##_bf16v4[kRopeVecLanes], *const kRopeVec_##M##_f16v4[kRopeVecLanes], \
+        *const kRopeVec_##M##_f32v4[kRopeVecLanes]
+GBN_ROPE_VEC(rot);
+GBN_ROPE_VEC(rms);
+GBN_ROPE_VEC(ln);
+GBN_ROPE_VEC(brms);
+GBN_ROPE_VEC(bln);
+#undef GBN_ROPE_VEC
 
 }  // namespace gbn

@@ -1,0 +1,523 @@
+// rope_vec_kernels.cuh -- the head operators on vectors.
+//
+// A group of L lanes holds one head, 32 / L heads a warp and pass; a lane holds
+// two chunks of V consecutive elements, one 8- or 16-byte vector each.  Where
+// pair j is (j, j + rot / 2) the two chunks are partners (j..j+V-1 and the same
+// behind rot / 2), where pairs are neighbours every chunk holds whole pairs; so
+// the rotation needs no exchange, and a row sum is log2 L shuffles.
+//
+// The lanes of a warp share out the pairs of a token, put their cosines and
+// sines into the warp's part of shared memory, and each lane takes those of its
+// chunks: once a token, for all its heads.  gamma is folded into them,
+//     y_a = n_a (gamma_a cos) - n_b (gamma_b sin),   y_b = n_b (gamma_b cos) + n_a (gamma_a sin),
+// with n the values before gamma, so that an element costs a product with rstd
+// and two with coefficients.
+#pragma once
+
+#include "rope_common.cuh"
+
+namespace gbn {
+
+// V elements as stored.
+template <int XT, int V> struct RopeRaw;
+template <> struct RopeRaw<kF32, 4> { uint4 v; };
+template <> struct RopeRaw<kF16, 8> { uint4 v; };
+template <> struct RopeRaw<kBF16, 8> { uint4 v; };
+template <> struct RopeRaw<kF16, 4> { uint2 v; };
+template <> struct RopeRaw<kBF16, 4> { uint2 v; };
+
+__device__ __forceinline__ void rope_ld(const void *p, uint4 &v) { v = *static_cast<const uint4 *>(p); }
+__device__ __forceinline__ void rope_ld(const void *p, uint2 &v) { v = *static_cast<const uint2 *>(p); }
+__device__ __forceinline__ void rope_st(void *p, const uint4 &v) { *static_cast<uint4 *>(p) = v; }
+__device__ __forceinline__ void rope_st(void *p, const uint2 &v) { *static_cast<uint2 *>(p) = v; }
+
+template <int XT> __device__ __forceinline__ float2 rope_pair(uint32_t w) {
+    if constexpr (XT == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <int XT> __device__ __forceinline__ uint32_t rope_word(float2 f) {
+    if constexpr (XT == kBF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <int XT, int V> __device__ __forceinline__ void rope_unpack(const RopeRaw<XT, V> &r, float2 (&f)[V / 2]) {
+    if constexpr (XT == kF32) {
+        f[0] = make_float2(__uint_as_float(r.v.x), __uint_as_float(r.v.y));
+        f[1] = make_float2(__uint_as_float(r.v.z), __uint_as_float(r.v.w));
+    } else {
+        f[0] = rope_pair<XT>(r.v.x);
+        f[1] = rope_pair<XT>(r.v.y);
+        if constexpr (V == 8) {
+            f[2] = rope_pair<XT>(r.v.z);
+            f[3] = rope_pair<XT>(r.v.w);
+        }
+    }
+}
+template <int XT, int V> __device__ __forceinline__ RopeRaw<XT, V> rope_pack(const float2 (&f)[V / 2]) {
+    RopeRaw<XT, V> r;
+    if constexpr (XT == kF32) {
+        r.v = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                         __float_as_uint(f[1].y));
+    } else {
+        r.v.x = rope_word<XT>(f[0]);
+        r.v.y = rope_word<XT>(f[1]);
+        if constexpr (V == 8) {
+            r.v.z = rope_word<XT>(f[2]);
+            r.v.w = rope_word<XT>(f[3]);
+        }
+    }
+    return r;
+}
+
+// V parameters from element c of a row of dt, or V times `none` for a null row.
+template <int V>
+__device__ __forceinline__ void rope_param(const void *row, int c, int dt, float none, float2 (&f)[V / 2]) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = f2s(none);
+    if (!row) return;
+    if (dt == kF32) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + c) + i);
+            f[2 * i] = make_float2(v.x, v.y);
+            f[2 * i + 1] = make_float2(v.z, v.w);
+        }
+    } else {
+        uint32_t w[V / 2];
+        const uint2 *q = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + c);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const uint2 v = __ldg(q + i);
+            w[2 * i] = v.x;
+            w[2 * i + 1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) f[i] = dt == kBF16 ? rope_pair<kBF16>(w[i]) : rope_pair<kF16>(w[i]);
+    }
+}
+
+// The two chunks of a lane: first elements, whether they are there, whether they are rotated, and their first pair.
+template <int V> struct RopeChunks {
+    int a, b, pa, pb;
+    bool oka, okb, ra, rb;
+    __device__ __forceinline__ RopeChunks(const RopeParams &p, int sl) {
+        const int n = p.D / V, nr = p.rot / V;
+        int ca, cb;
+        if (p.inter) {
+            const int ns = (n + 1) / 2;
+            ca = sl;
+            cb = ns + sl;
+            oka = sl < ns;
+            okb = oka && cb < n;
+            pa = ca * (V / 2);
+            pb = cb * (V / 2);
+        } else {
+            const int half = nr / 2;
+            ca = sl < half ? sl : nr + 2 * (sl - half);
+            cb = sl < half ? sl + half : ca + 1;
+            oka = ca < n;
+            okb = cb < n;
+            pa = pb = sl * V;
+        }
+        a = ca * V;
+        b = cb * V;
+        ra = oka && ca < nr;
+        rb = okb && cb < nr;
+    }
+};
+
+// A warp's cosines and sines: written by the lane that computed the pair, read by those whose chunks hold it.
+template <int V, int L> struct RopeTable {
+    static constexpr int N = V * L, PER = N / 32 > 0 ? N / 32 : 1;
+    float c[N], s[N];
+    __device__ __forceinline__ void put(const RopeAngles<PER> &ang, const RopeParams &p, const uint64_t (&pos)[PER],
+                                        int lane) {
+        __syncwarp();  // the last token's have been read
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int j = lane + 32 * i;
+            if (2 * j < p.rot) ang.turn(pos[i] * ang.f[i], i, p.sign, c + j, s + j);
+        }
+        __syncwarp();
+    }
+};
+
+// The positions a lane needs for its pairs of the token at the walk.
+template <int N>
+__device__ __forceinline__ void rope_fetch(const RopeParams &p, const RopeAngles<N> &ang, const RopeWalk &w, int lane,
+                                           uint64_t (&pos)[N]) {
+    const int64_t at = w.b * p.pos_batch + w.s * p.pos_token;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        pos[i] = 0;
+        if (2 * (lane + 32 * i) >= p.rot) continue;
+        const int64_t q = at + (int64_t)((ang.axis >> (2 * i)) & 3u) * p.pos_axis;
+        pos[i] = p.pos64 ? (uint64_t)__ldg(static_cast<const long long *>(p.pos) + q)
+                         : (uint64_t)(int64_t)__ldg(static_cast<const int *>(p.pos) + q);
+    }
+}
+
+__device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x); }
+
+template <int MODE, int XT, int V, int L, int MINB>
+__global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_constant__ RopeParams p) {
+    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2;
+    using Table = RopeTable<V, L>;
+    __shared__ Table tables[kRopeWarps];
+    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L;
+    Table &tab = tables[threadIdx.x >> 5];
+    RopeWalk w(p);  // the pass to load
+    if (!w.left) return;
+    const RopeChunks<V> ch(p, sl);
+    const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
+    auto address = [&](const RopeHeads &t) {
+        return static_cast<char *>(t.p) + (w.at(t) + (int64_t)(w.blk * G + grp) * t.head + ch.a) * ES;
+    };
+    const char *x = address(p.x[r]);
+    char *y = address(p.y[r]);
+    int64_t stat = w.stat(p) + w.blk * G + grp;
+    int left = heads - w.blk * G - grp;  // heads from this lane's on
+    auto load = [&](RopeRaw<XT, V> &a, RopeRaw<XT, V> &b, bool in) {
+        a = b = {};
+        if (in && ch.oka) rope_ld(x, a.v);
+        if (in && ch.okb) rope_ld(x + off, b.v);
+    };
+    RopeRaw<XT, V> a0, b0, a1, b1;
+    load(a0, b0, left > 0);
+    RopeAngles<Table::PER> ang;
+    ang.init(p, lane);
+    uint64_t pos[Table::PER];
+    rope_fetch(p, ang, w, lane, pos);
+    const float inv = 1.f / (float)p.D;
+    const bool all = p.rot == p.D;
+    float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
+    bool fresh = true;
+    while (true) {
+        const bool nf = w.next(p);
+        if (nf) x = address(p.x[r]);
+        else x += p.x[r].head * (G * ES);
+        if (w.left) load(a1, b1, nf ? grp < heads : left > G);
+        if (fresh) {
+            tab.put(ang, p, pos, lane);
+            float2 ga[H], gb[H];
+            if constexpr (MODE != kRopeOnly) {
+                rope_param<V>(ch.oka ? p.gamma[r] : nullptr, ch.a, p.pdt, 1.f, ga);
+                rope_param<V>(ch.okb ? p.gamma[r] : nullptr, ch.b, p.pdt, 1.f, gb);
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) ga[i] = gb[i] = f2s(1.f);
+            }
+            if constexpr (MODE == kRopeLn) {
+                rope_param<V>(ch.oka ? p.beta[r] : nullptr, ch.a, p.pdt, 0.f, ba);
+                rope_param<V>(ch.okb ? p.beta[r] : nullptr, ch.b, p.pdt, 0.f, bb);
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                ca[i] = ga[i];
+                cb[i] = gb[i];
+                sa[i] = sb[i] = f2s(0.f);
+            }
+            if (p.inter) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    if (ch.ra) {
+                        const float c = tab.c[ch.pa + i], s = tab.s[ch.pa + i];
+                        ca[i] = make_float2(ga[i].x * c, ga[i].y * c);
+                        sa[i] = make_float2(-ga[i].y * s, ga[i].x * s);
+                        if constexpr (MODE == kRopeLn)
+                            ba[i] = make_float2(ba[i].x * c - ba[i].y * s, ba[i].y * c + ba[i].x * s);
+                    }
+                    if (ch.rb) {
+                        const float c = tab.c[ch.pb + i], s = tab.s[ch.pb + i];
+                        cb[i] = make_float2(gb[i].x * c, gb[i].y * c);
+                        sb[i] = make_float2(-gb[i].y * s, gb[i].x * s);
+                        if constexpr (MODE == kRopeLn)
+                            bb[i] = make_float2(bb[i].x * c - bb[i].y * s, bb[i].y * c + bb[i].x * s);
+                    }
+                }
+            } else if (ch.ra) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const float2 c = *reinterpret_cast<const float2 *>(tab.c + ch.pa + 2 * i),
+                                 s = *reinterpret_cast<const float2 *>(tab.s + ch.pa + 2 * i);
+                    ca[i] = f2mul(ga[i], c);
+                    sa[i] = f2mul(gb[i], make_float2(-s.x, -s.y));
+                    cb[i] = f2mul(gb[i], c);
+                    sb[i] = f2mul(ga[i], s);
+                    if constexpr (MODE == kRopeLn) {
+                        const float2 v = ba[i];
+                        ba[i] = make_float2(v.x * c.x - bb[i].x * s.x, v.y * c.y - bb[i].y * s.y);
+                        bb[i] = make_float2(bb[i].x * c.x + v.x * s.x, bb[i].y * c.y + v.y * s.y);
+                    }
+                }
+            }
+        }
+        if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
+        float2 va[H], vb[H];
+        rope_unpack<XT, V>(a0, va);
+        rope_unpack<XT, V>(b0, vb);
+        if constexpr (MODE != kRopeOnly) {
+            float mean = 0.f;
+            if constexpr (MODE == kRopeLn) {
+                float2 t = f2s(0.f);
+#pragma unroll
+                for (int i = 0; i < H; ++i) t = f2add(t, f2add(va[i], vb[i]));
+                float sum[1] = {t.x + t.y};
+                group_sum<L, 1>(sum);
+                mean = sum[0] * inv;
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    va[i] = ch.oka ? f2add(va[i], f2s(-mean)) : f2s(0.f);
+                    vb[i] = ch.okb ? f2add(vb[i], f2s(-mean)) : f2s(0.f);
+                }
+            }
+            float2 t = f2s(0.f);
+#pragma unroll
+            for (int i = 0; i < H; ++i) t = f2fma(va[i], va[i], f2fma(vb[i], vb[i], t));
+            float sq[1] = {t.x + t.y};
+            group_sum<L, 1>(sq);
+            const float rstd = rsqrtf(sq[0] * inv + p.eps);
+            if (sl == 0 && left > 0) {
+                if (p.rstd) p.rstd[stat] = rstd;
+                if (MODE == kRopeLn && p.mean) p.mean[stat] = mean;
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                va[i] = f2mul(va[i], f2s(rstd));
+                vb[i] = f2mul(vb[i], f2s(rstd));
+            }
+        }
+        RopeRaw<XT, V> oa, ob;
+        float2 ua[H], ub[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            float2 ta = p.inter ? f2swap(va[i]) : vb[i], tb = p.inter ? f2swap(vb[i]) : va[i];
+            if (!all) {  // an element that is not rotated takes nothing from another, not even a NaN
+                ta = ch.ra ? ta : f2s(0.f);
+                tb = ch.rb ? tb : f2s(0.f);
+            }
+            ua[i] = f2fma(va[i], ca[i], f2mul(ta, sa[i]));
+            ub[i] = f2fma(vb[i], cb[i], f2mul(tb, sb[i]));
+            if constexpr (MODE == kRopeLn) {
+                ua[i] = f2add(ua[i], ba[i]);
+                ub[i] = f2add(ub[i], bb[i]);
+            }
+        }
+        oa = rope_pack<XT, V>(ua);
+        ob = rope_pack<XT, V>(ub);
+        if (left > 0 && ch.oka) rope_st(y, oa.v);
+        if (left > 0 && ch.okb) rope_st(y + off, ob.v);
+        if (!w.left) break;
+        if (nf) {
+            y = address(p.y[r]);
+            stat = w.stat(p) + grp;
+            left = heads - grp;
+        } else {
+            y += p.y[r].head * (G * ES);
+            stat += G;
+            left -= G;
+        }
+        fresh = nf;
+        a0 = a1;
+        b0 = b1;
+    }
+}
+
+template <bool LN, int XT, int V, int L, int MINB>
+__global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
+    pdl_launch_dependents();  // the column reduce waits for this grid's completion
+    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2;
+    using Table = RopeTable<V, L>;
+    extern __shared__ __align__(16) float rope_acc[];  // [kRopeWarps][D]
+    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
+    __shared__ Table tables[kRopeWarps];
+    Table &tab = tables[warp];
+    RopeWalk w(p);  // the pass to load
+    const RopeChunks<V> ch(p, sl);
+    const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
+    auto address = [&](const RopeHeads &t) {
+        return static_cast<char *>(t.p) + (w.at(t) + (int64_t)(w.blk * G + grp) * t.head + ch.a) * ES;
+    };
+    struct Raw {
+        RopeRaw<XT, V> xa, xb, ga, gb;
+        float mean, rstd;
+    } r0, r1;
+    const char *x = nullptr, *g = nullptr;
+    int64_t stat = 0;
+    auto load = [&](Raw &v, bool in) {
+        v = {};
+        if (!in) return;
+        if (ch.oka) {
+            rope_ld(x, v.xa.v);
+            rope_ld(g, v.ga.v);
+        }
+        if (ch.okb) {
+            rope_ld(x + off, v.xb.v);
+            rope_ld(g + off, v.gb.v);
+        }
+        v.rstd = __ldg(p.rstd + stat);
+        if constexpr (LN) v.mean = __ldg(p.mean + stat);
+    };
+    float2 da[H], db[H], ea[H], eb[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
+    if (w.left) {
+        x = address(p.x[r]);
+        g = address(p.g[r]);
+        char *y = address(p.y[r]);
+        stat = w.stat(p) + w.blk * G + grp;
+        int left = heads - w.blk * G - grp;  // heads from this lane's on
+        load(r0, left > 0);
+        RopeAngles<Table::PER> ang;
+        ang.init(p, lane);
+        uint64_t pos[Table::PER];
+        rope_fetch(p, ang, w, lane, pos);
+        float2 wa[H], wb[H], c[V / 2], s[V / 2];  // c, s: of the pairs of the chunks (neighbours: first a's, then b's)
+        rope_param<V>(ch.oka ? p.gamma[r] : nullptr, ch.a, p.pdt, 1.f, wa);
+        rope_param<V>(ch.okb ? p.gamma[r] : nullptr, ch.b, p.pdt, 1.f, wb);
+        const float inv = 1.f / (float)p.D;
+        const bool all = p.rot == p.D;
+        bool fresh = true;
+        while (true) {
+            const bool nf = w.next(p);
+            if (nf) {
+                x = address(p.x[r]);
+                g = address(p.g[r]);
+                stat = w.stat(p) + grp;
+            } else {
+                x += p.x[r].head * (G * ES);
+                g += p.g[r].head * (G * ES);
+                stat += G;
+            }
+            if (w.left) load(r1, nf ? grp < heads : left > G);
+            if (fresh) {
+                tab.put(ang, p, pos, lane);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    c[i] = f2s(1.f);
+                    s[i] = f2s(0.f);
+                    const int at = p.inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
+                    if (p.inter ? (2 * i < H ? ch.ra : ch.rb) : ch.ra) {
+                        c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
+                        s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
+                    }
+                }
+            }
+            if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
+            // the gradient turned back (the sign of s is the transpose's)
+            float2 ta[H], tb[H];
+            {
+                float2 ga[H], gb[H];
+                rope_unpack<XT, V>(r0.ga, ga);
+                rope_unpack<XT, V>(r0.gb, gb);
+                if (p.inter) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
+                        const float cj = i & 1 ? c[H / 2 + i / 2].y : c[H / 2 + i / 2].x,
+                                    sj = i & 1 ? s[H / 2 + i / 2].y : s[H / 2 + i / 2].x;
+                        float2 u = f2swap(ga[i]), v = f2swap(gb[i]);
+                        if (!all) {
+                            u = ch.ra ? u : f2s(0.f);
+                            v = ch.rb ? v : f2s(0.f);
+                        }
+                        ta[i] = make_float2(ga[i].x * ci - u.x * si, ga[i].y * ci + u.y * si);
+                        tb[i] = make_float2(gb[i].x * cj - v.x * sj, gb[i].y * cj + v.y * sj);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        float2 u = gb[i], v = ga[i];
+                        if (!all) {
+                            u = ch.ra ? u : f2s(0.f);
+                            v = ch.ra ? v : f2s(0.f);
+                        }
+                        ta[i] = f2fma(ga[i], c[i], f2mul(make_float2(-u.x, -u.y), s[i]));
+                        tb[i] = f2fma(gb[i], c[i], f2mul(v, s[i]));
+                    }
+                }
+            }
+            float2 xa[H], xb[H];
+            rope_unpack<XT, V>(r0.xa, xa);
+            rope_unpack<XT, V>(r0.xb, xb);
+            const float rstd = r0.rstd, mean = r0.mean;
+            float2 dot = f2s(0.f), sum = f2s(0.f);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                if constexpr (LN) {
+                    xa[i] = f2add(xa[i], f2s(-mean));
+                    xb[i] = f2add(xb[i], f2s(-mean));
+                    ea[i] = f2add(ea[i], ta[i]);
+                    eb[i] = f2add(eb[i], tb[i]);
+                }
+                xa[i] = f2mul(xa[i], f2s(rstd));
+                xb[i] = f2mul(xb[i], f2s(rstd));
+                da[i] = f2fma(ta[i], xa[i], da[i]);
+                db[i] = f2fma(tb[i], xb[i], db[i]);
+                ta[i] = f2mul(ta[i], wa[i]);
+                tb[i] = f2mul(tb[i], wb[i]);
+                dot = f2fma(ta[i], xa[i], f2fma(tb[i], xb[i], dot));
+                if constexpr (LN) sum = f2add(sum, f2add(ta[i], tb[i]));
+            }
+            float v[LN ? 2 : 1];
+            v[0] = dot.x + dot.y;
+            if constexpr (LN) v[1] = sum.x + sum.y;
+            group_sum<L, LN ? 2 : 1>(v);
+            const float2 c2 = f2s(-v[0] * inv), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv : 0.f);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                if constexpr (LN) {
+                    ta[i] = f2add(ta[i], c1);
+                    tb[i] = f2add(tb[i], c1);
+                }
+                ta[i] = f2mul(f2fma(xa[i], c2, ta[i]), f2s(rstd));
+                tb[i] = f2mul(f2fma(xb[i], c2, tb[i]), f2s(rstd));
+            }
+            const RopeRaw<XT, V> oa = rope_pack<XT, V>(ta), ob = rope_pack<XT, V>(tb);
+            if (left > 0 && ch.oka) rope_st(y, oa.v);
+            if (left > 0 && ch.okb) rope_st(y + off, ob.v);
+            if (!w.left) break;
+            if (nf) {
+                y = address(p.y[r]);
+                left = heads - grp;
+            } else {
+                y += p.y[r].head * (G * ES);
+                left -= G;
+            }
+            fresh = nf;
+            r0 = r1;
+        }
+    }
+    // the sums of the groups of lanes (the same columns) of a warp, then of the CTA's warps
+    float *mine = rope_acc + warp * p.D;
+    auto columns = [&](float2 (&u)[H], float2 (&v)[H]) {
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                u[i].x += __shfl_xor_sync(0xffffffffu, u[i].x, o);
+                u[i].y += __shfl_xor_sync(0xffffffffu, u[i].y, o);
+                v[i].x += __shfl_xor_sync(0xffffffffu, v[i].x, o);
+                v[i].y += __shfl_xor_sync(0xffffffffu, v[i].y, o);
+            }
+        if (grp == 0) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                if (ch.oka) *reinterpret_cast<float2 *>(mine + ch.a + 2 * i) = u[i];
+                if (ch.okb) *reinterpret_cast<float2 *>(mine + ch.b + 2 * i) = v[i];
+            }
+        }
+    };
+    columns(da, db);
+    rope_partial(p, rope_acc, 0);
+    if constexpr (LN) {
+        columns(ea, eb);
+        rope_partial(p, rope_acc, 1);
+    }
+}
+
+}  // namespace gbn
