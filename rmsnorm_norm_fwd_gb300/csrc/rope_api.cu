@@ -2,6 +2,7 @@
 // checks, the choice of a kernel, launches.  As in api.cu nothing here
 // allocates device memory or synchronises.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -19,9 +20,9 @@ int elem_size(int dtype) { return dtype == GBNORM_F32 ? 4 : 2; }
 bool valid_dtype(int d) { return d == GBNORM_F32 || d == GBNORM_F16 || d == GBNORM_BF16; }
 bool aligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-// CTAs an SM of the persistent grids.  The backward's also bounds its partial
-// rows, so that the workspace depends on the shape alone.
-constexpr int64_t kFwdPerSm = 2, kBwdPerSm = 2;
+// Most CTAs an SM of the backward: bounds its partial rows, so that the
+// workspace depends on the shape alone.
+constexpr int64_t kBwdPerSm = 2;
 
 // A tensor of heads as the aliasing check sees it, in bytes: runs of `run`
 // bytes at p + i0 st[0] + i1 st[1] + i2 st[2], i < n; extents of one element
@@ -235,11 +236,13 @@ int launch(const void *kernel, int64_t grid, size_t dyn, RopeParams *p, cudaStre
     return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
 }
 
-// A kernel of a call: rows of lanes (or, element by element, warps) a head.
+// A kernel of a call.
 struct Kernel {
     const void *f;
     const char *name;
     int heads;  // of a pass
+    int smem;
+    int slot;   // its place in the cache of what a device holds
 };
 
 int any_size(int64_t D, int rot) {  // log2 of the pairs a lane holds
@@ -269,20 +272,41 @@ int vector_of(const RopeParams &p, bool back) {
 // mode: a RopeMode, or -1 - is_layernorm for the backward.
 Kernel pick(int mode, const RopeParams &p) {
 #define GBN_T(M) {kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, kRopeVec_##M##_bf16v4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8}
-    static const void *const *const tables[5][5] = {GBN_T(rot), GBN_T(rms), GBN_T(ln), GBN_T(brms), GBN_T(bln)};
+    static const RopeVariant(*const tables[5][5])[kRopeVecLanes] = {GBN_T(rot), GBN_T(rms), GBN_T(ln), GBN_T(brms),
+                                                                     GBN_T(bln)};
 #undef GBN_T
-    static const char *const names[2][kRopeVecLanes] = {{"vec4x4", "vec4x8", "vec4x16", "vec4x32"},
-                                                        {"vec8x4", "vec8x8", "vec8x16", "vec8x32"}};
-    const int v = vector_of(p, mode < 0);
+    const int v = vector_of(p, mode < 0), m = mode < 0 ? 2 - mode : mode;
     if (v) {
         const int chunks = p.D / v, rot = p.rot / v;
         const int slots = p.inter ? (chunks + 1) / 2 : rot / 2 + (chunks - rot + 1) / 2;
+        const int kind = p.rot < p.D ? kRopeVecKinds - 1 : p.inter;
         for (int l = 0; l < kRopeVecLanes; ++l)
-            if (slots <= 4 << l)
-                return {tables[mode < 0 ? 2 - mode : mode][p.xdt + (v == 8 ? 2 : 0)][l], names[v == 8][l], 8 >> l};
+            if (slots <= 4 << l) {
+                const int t = p.xdt + (v == 8 ? 2 : 0);
+                const RopeVariant &k = tables[m][t][kind][l];
+                return {k.f, k.name, 8 >> l, k.smem, ((m * 5 + t) * kRopeVecKinds + kind) * kRopeVecLanes + l};
+            }
     }
-    const int n = any_size(p.D, p.rot);
-    return {mode < 0 ? kRopeBwdAny[-1 - mode][n] : kRopeFwdAny[mode][n], "any", 1};
+    const int n = any_size(p.D, p.rot), slot = 5 * 5 * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
+    return mode < 0 ? Kernel{kRopeBwdAny[-1 - mode][n], "any", 1, kRopeWarps * p.D * 4, slot}
+                    : Kernel{kRopeFwdAny[mode][n], "any", 1, 0, slot};
+}
+constexpr int kSlots = 5 * 5 * kRopeVecKinds * kRopeVecLanes + 5 * kRopeAnySizes;
+std::atomic<int> g_resident[kHostMaxDev][kSlots];
+
+// CTAs of a kernel that an SM holds, measured once per device.
+int resident(const Kernel &k, const HostDevice &d, int *out) {
+    std::atomic<int> &c = g_resident[d.dev][k.slot];
+    int o = c.load(std::memory_order_relaxed);
+    if (o == 0) {
+        if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, std::max(k.smem, 48 * 1024)) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k.f, kRopeCTA, (size_t)k.smem) != cudaSuccess)
+            return GBNORM_ERR_CUDA;
+        if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
+        c.store(o, std::memory_order_relaxed);
+    }
+    *out = o;
+    return GBNORM_OK;
 }
 
 // Forward kernels: the norm with the rotation (mode kRopeRms, kRopeLn), the rotation alone.
@@ -294,10 +318,13 @@ int run_fwd(int mode, RopeParams *p, const Shape &s, cudaStream_t st) {
     t_last[what] = "";
     if (s.tokens() == 0) return GBNORM_OK;
     const Kernel k = pick(mode, *p);
-    const int64_t grid = share(p, s, k.heads, kFwdPerSm, d);
+    int per_sm;
+    const int o = resident(k, d, &per_sm);
+    if (o != GBNORM_OK) return o;
+    const int64_t grid = share(p, s, k.heads, per_sm, d);
     if (grid < 0) return GBNORM_ERR_UNSUPPORTED;
     t_last[what] = k.name;
-    return launch(k.f, grid, 0, p, st);
+    return launch(k.f, grid, (size_t)k.smem, p, st);
 }
 
 int64_t bwd_rows(const Shape &s, const HostDevice &d) {  // most partial rows of any kernel
@@ -425,10 +452,12 @@ int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_head
         p.ws = static_cast<float *>(workspace);
         p.sign = -1.f;
         const Kernel k = pick(-1 - is_layernorm, p);
-        P = share(&p, s, k.heads, kBwdPerSm, d);
+        int per_sm;
+        if ((e = resident(k, d, &per_sm)) != GBNORM_OK) return e;
+        P = share(&p, s, k.heads, std::min<int64_t>(per_sm, kBwdPerSm), d);
         if (P < 0) return GBNORM_ERR_UNSUPPORTED;
         t_last[1] = k.name;
-        e = launch(k.f, P, (size_t)kRopeWarps * s.D * 4, &p, stream);
+        e = launch(k.f, P, (size_t)k.smem, &p, stream);
         if (e != GBNORM_OK) return e;
     }
     return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, P > 0, stream);

@@ -52,13 +52,27 @@ constexpr int kRopeAnySizes = 5;
 extern const void *const kRopeFwdAny[3][kRopeAnySizes];
 extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 
-// On vectors: [lanes a head: 4, 8, 16, 32], for each direction and norm (rot: the rotation alone; b: backward) and type
-// and elements a vector.
-constexpr int kRopeVecLanes = 4;
+// On vectors of v elements of es bytes, l lanes a head: passes in flight a
+// warp, and dynamic shared memory (rings and tables of cosines and sines; the
+// backward's column sums take the place of the rings).
+constexpr int kRopeFwdDepth = 3, kRopeBwdDepth = 3;
+constexpr int rope_fwd_smem(int v, int es, int l) { return kRopeWarps * (kRopeFwdDepth * 64 * v * es + 8 * v * l); }
+constexpr int rope_bwd_smem(int v, int es, int l) {
+    return kRopeWarps * (kRopeBwdDepth * (128 * v * es + 256) + 8 * v * l);
+}
+
+struct RopeVariant {
+    const void *f;
+    const char *name;
+    int smem;
+};
+constexpr int kRopeVecLanes = 4;  // lanes a head: 4, 8, 16, 32
+constexpr int kRopeVecKinds = 3;  // RopeKind
+// For each direction and norm (rot: the rotation alone; b: backward) and vector.
 #define GBN_ROPE_VEC(M) \
-    extern const void *const kRopeVec_##M##_bf16v8[kRopeVecLanes], *const kRopeVec_##M##_f16v8[kRopeVecLanes], \
-        *const kRopeVec_##M##_bf16v4[kRopeVecLanes], *const kRopeVec_##M##_f16v4[kRopeVecLanes], \
-        *const kRopeVec_##M##_f32v4[kRopeVecLanes]
+    extern const RopeVariant kRopeVec_##M##_bf16v8[kRopeVecKinds][kRopeVecLanes], \
+        kRopeVec_##M##_f16v8[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_bf16v4[kRopeVecKinds][kRopeVecLanes], \
+        kRopeVec_##M##_f16v4[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_f32v4[kRopeVecKinds][kRopeVecLanes]
 GBN_ROPE_VEC(rot);
 GBN_ROPE_VEC(rms);
 GBN_ROPE_VEC(ln);

@@ -73,6 +73,21 @@ template <int XT, int V> __device__ __forceinline__ RopeRaw<XT, V> rope_pack(con
     return r;
 }
 
+// Asynchronous copies into the lane's own places of the ring: no other thread
+// reads them, so that waiting for the lane's own groups is enough.  Lanes
+// without an element fill with zeros (`from` is then any valid address).
+__device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, const uint4 &) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, const uint2 &) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, float) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void rope_cp_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void rope_cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // V parameters from element c of a row of dt, or V times `none` for a null row.
 template <int V>
 __device__ __forceinline__ void rope_param(const void *row, int c, int dt, float none, float2 (&f)[V / 2]) {
@@ -100,14 +115,18 @@ __device__ __forceinline__ void rope_param(const void *row, int c, int dt, float
     }
 }
 
+// What is rotated, fixed at compile time where it is common: the whole head, as
+// halves or as neighbours, or anything (read from the call, through selects).
+enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopeSome = 2 };
+
 // The two chunks of a lane: first elements, whether they are there, whether they are rotated, and their first pair.
-template <int V> struct RopeChunks {
+template <int V, int KIND> struct RopeChunks {
     int a, b, pa, pb;
     bool oka, okb, ra, rb;
     __device__ __forceinline__ RopeChunks(const RopeParams &p, int sl) {
         const int n = p.D / V, nr = p.rot / V;
         int ca, cb;
-        if (p.inter) {
+        if (KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter)) {
             const int ns = (n + 1) / 2;
             ca = sl;
             cb = ns + sl;
@@ -163,44 +182,47 @@ __device__ __forceinline__ void rope_fetch(const RopeParams &p, const RopeAngles
 
 __device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x); }
 
-template <int MODE, int XT, int V, int L, int MINB>
+template <int MODE, int XT, int V, int L, int KIND, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_constant__ RopeParams p) {
-    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2;
+    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2, DEPTH = kRopeFwdDepth;
     using Table = RopeTable<V, L>;
-    __shared__ Table tables[kRopeWarps];
-    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L;
-    Table &tab = tables[threadIdx.x >> 5];
-    RopeWalk w(p);  // the pass to load
+    using Raw = RopeRaw<XT, V>;
+    extern __shared__ __align__(16) unsigned char rope_smem[];  // rings, then tables
+    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
+    Raw(*ring)[2][32] = reinterpret_cast<Raw(*)[2][32]>(rope_smem) + warp * DEPTH;
+    Table &tab = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * DEPTH * kRopeWarps)[warp];
+    RopeWalk w(p), ahead = w;  // the pass worked on, the pass to load
     if (!w.left) return;
-    const RopeChunks<V> ch(p, sl);
+    const RopeChunks<V, KIND> ch(p, sl);
     const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
-    auto address = [&](const RopeHeads &t) {
-        return static_cast<char *>(t.p) + (w.at(t) + (int64_t)(w.blk * G + grp) * t.head + ch.a) * ES;
+    auto address = [&](const RopeHeads &t, const RopeWalk &at) {
+        return static_cast<char *>(t.p) + (at.at(t) + (int64_t)(at.blk * G + grp) * t.head + ch.a) * ES;
     };
-    const char *x = address(p.x[r]);
-    char *y = address(p.y[r]);
+    const char *x = address(p.x[r], ahead);
+    auto load = [&](int slot) {
+        if (ahead.left) {
+            const bool in = ahead.blk * G + grp < heads, a = in && ch.oka, b = in && ch.okb;
+            rope_cp(&ring[slot][0][lane], a ? x : p.x[r].p, a, Raw{}.v);
+            rope_cp(&ring[slot][1][lane], b ? x + off : p.x[r].p, b, Raw{}.v);
+            if (ahead.next(p)) x = address(p.x[r], ahead);
+            else x += p.x[r].head * (G * ES);
+        }
+        rope_cp_end();
+    };
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) load(i);
+    char *y = address(p.y[r], w);
     int64_t stat = w.stat(p) + w.blk * G + grp;
-    int left = heads - w.blk * G - grp;  // heads from this lane's on
-    auto load = [&](RopeRaw<XT, V> &a, RopeRaw<XT, V> &b, bool in) {
-        a = b = {};
-        if (in && ch.oka) rope_ld(x, a.v);
-        if (in && ch.okb) rope_ld(x + off, b.v);
-    };
-    RopeRaw<XT, V> a0, b0, a1, b1;
-    load(a0, b0, left > 0);
     RopeAngles<Table::PER> ang;
     ang.init(p, lane);
     uint64_t pos[Table::PER];
     rope_fetch(p, ang, w, lane, pos);
     const float inv = 1.f / (float)p.D;
-    const bool all = p.rot == p.D;
+    const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
     bool fresh = true;
-    while (true) {
-        const bool nf = w.next(p);
-        if (nf) x = address(p.x[r]);
-        else x += p.x[r].head * (G * ES);
-        if (w.left) load(a1, b1, nf ? grp < heads : left > G);
+    for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
+        const bool in = w.blk * G + grp < heads, nf = w.next(p);
         if (fresh) {
             tab.put(ang, p, pos, lane);
             float2 ga[H], gb[H];
@@ -221,7 +243,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 cb[i] = gb[i];
                 sa[i] = sb[i] = f2s(0.f);
             }
-            if (p.inter) {
+            if (inter) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     if (ch.ra) {
@@ -257,9 +279,11 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
             }
         }
         if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
+        rope_cp_wait<DEPTH - 1>();
         float2 va[H], vb[H];
-        rope_unpack<XT, V>(a0, va);
-        rope_unpack<XT, V>(b0, vb);
+        rope_unpack<XT, V>(ring[slot][0][lane], va);
+        rope_unpack<XT, V>(ring[slot][1][lane], vb);
+        load(slot);
         if constexpr (MODE != kRopeOnly) {
             float mean = 0.f;
             if constexpr (MODE == kRopeLn) {
@@ -281,7 +305,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
             float sq[1] = {t.x + t.y};
             group_sum<L, 1>(sq);
             const float rstd = rsqrtf(sq[0] * inv + p.eps);
-            if (sl == 0 && left > 0) {
+            if (sl == 0 && in) {
                 if (p.rstd) p.rstd[stat] = rstd;
                 if (MODE == kRopeLn && p.mean) p.mean[stat] = mean;
             }
@@ -295,8 +319,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         float2 ua[H], ub[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            float2 ta = p.inter ? f2swap(va[i]) : vb[i], tb = p.inter ? f2swap(vb[i]) : va[i];
-            if (!all) {  // an element that is not rotated takes nothing from another, not even a NaN
+            float2 ta = inter ? f2swap(va[i]) : vb[i], tb = inter ? f2swap(vb[i]) : va[i];
+            if constexpr (KIND == kRopeSome) {  // an element that is not rotated takes nothing from another, not even a NaN
                 ta = ch.ra ? ta : f2s(0.f);
                 tb = ch.rb ? tb : f2s(0.f);
             }
@@ -309,69 +333,74 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         }
         oa = rope_pack<XT, V>(ua);
         ob = rope_pack<XT, V>(ub);
-        if (left > 0 && ch.oka) rope_st(y, oa.v);
-        if (left > 0 && ch.okb) rope_st(y + off, ob.v);
+        if (in && ch.oka) rope_st(y, oa.v);
+        if (in && ch.okb) rope_st(y + off, ob.v);
         if (!w.left) break;
         if (nf) {
-            y = address(p.y[r]);
+            y = address(p.y[r], w);
             stat = w.stat(p) + grp;
-            left = heads - grp;
         } else {
             y += p.y[r].head * (G * ES);
             stat += G;
-            left -= G;
         }
         fresh = nf;
-        a0 = a1;
-        b0 = b1;
     }
 }
 
-template <bool LN, int XT, int V, int L, int MINB>
+template <bool LN, int XT, int V, int L, int KIND, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
     constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2;
     using Table = RopeTable<V, L>;
-    extern __shared__ __align__(16) float rope_acc[];  // [kRopeWarps][D]
-    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
-    __shared__ Table tables[kRopeWarps];
-    Table &tab = tables[warp];
-    RopeWalk w(p);  // the pass to load
-    const RopeChunks<V> ch(p, sl);
-    const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
-    auto address = [&](const RopeHeads &t) {
-        return static_cast<char *>(t.p) + (w.at(t) + (int64_t)(w.blk * G + grp) * t.head + ch.a) * ES;
+    // rings of passes, then tables; at the end the column sums [kRopeWarps][D] in their place
+    extern __shared__ __align__(16) unsigned char rope_smem[];
+    constexpr int DEPTH = kRopeBwdDepth;
+    using Raw = RopeRaw<XT, V>;
+    struct Slot {
+        Raw x[2][32], g[2][32];
+        float mean[32], rstd[32];
     };
-    struct Raw {
-        RopeRaw<XT, V> xa, xb, ga, gb;
-        float mean, rstd;
-    } r0, r1;
-    const char *x = nullptr, *g = nullptr;
-    int64_t stat = 0;
-    auto load = [&](Raw &v, bool in) {
-        v = {};
-        if (!in) return;
-        if (ch.oka) {
-            rope_ld(x, v.xa.v);
-            rope_ld(g, v.ga.v);
-        }
-        if (ch.okb) {
-            rope_ld(x + off, v.xb.v);
-            rope_ld(g + off, v.gb.v);
-        }
-        v.rstd = __ldg(p.rstd + stat);
-        if constexpr (LN) v.mean = __ldg(p.mean + stat);
+    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
+    Slot *ring = reinterpret_cast<Slot *>(rope_smem) + warp * DEPTH;
+    Table &tab = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps)[warp];
+    float *rope_acc = reinterpret_cast<float *>(rope_smem);
+    RopeWalk w(p), ahead = w;  // the pass worked on, the pass to load
+    const RopeChunks<V, KIND> ch(p, sl);
+    const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
+    auto address = [&](const RopeHeads &t, const RopeWalk &at) {
+        return static_cast<char *>(t.p) + (at.at(t) + (int64_t)(at.blk * G + grp) * t.head + ch.a) * ES;
     };
     float2 da[H], db[H], ea[H], eb[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
     if (w.left) {
-        x = address(p.x[r]);
-        g = address(p.g[r]);
-        char *y = address(p.y[r]);
-        stat = w.stat(p) + w.blk * G + grp;
-        int left = heads - w.blk * G - grp;  // heads from this lane's on
-        load(r0, left > 0);
+        const char *x = address(p.x[r], ahead), *g = address(p.g[r], ahead);
+        int64_t stat = w.stat(p) + w.blk * G + grp;
+        auto load = [&](int i) {
+            if (ahead.left) {
+                const bool in = ahead.blk * G + grp < heads, a = in && ch.oka, b = in && ch.okb;
+                Slot &to = ring[i];
+                rope_cp(&to.x[0][lane], a ? x : p.x[r].p, a, Raw{}.v);
+                rope_cp(&to.g[0][lane], a ? g : p.g[r].p, a, Raw{}.v);
+                rope_cp(&to.x[1][lane], b ? x + off : p.x[r].p, b, Raw{}.v);
+                rope_cp(&to.g[1][lane], b ? g + off : p.g[r].p, b, Raw{}.v);
+                rope_cp(&to.rstd[lane], p.rstd + (in ? stat : 0), in, 0.f);
+                if constexpr (LN) rope_cp(&to.mean[lane], p.mean + (in ? stat : 0), in, 0.f);
+                if (ahead.next(p)) {
+                    x = address(p.x[r], ahead);
+                    g = address(p.g[r], ahead);
+                    stat = ahead.stat(p) + grp;
+                } else {
+                    x += p.x[r].head * (G * ES);
+                    g += p.g[r].head * (G * ES);
+                    stat += G;
+                }
+            }
+            rope_cp_end();
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) load(i);
+        char *y = address(p.y[r], w);
         RopeAngles<Table::PER> ang;
         ang.init(p, lane);
         uint64_t pos[Table::PER];
@@ -380,48 +409,39 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
         rope_param<V>(ch.oka ? p.gamma[r] : nullptr, ch.a, p.pdt, 1.f, wa);
         rope_param<V>(ch.okb ? p.gamma[r] : nullptr, ch.b, p.pdt, 1.f, wb);
         const float inv = 1.f / (float)p.D;
-        const bool all = p.rot == p.D;
+        const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
         bool fresh = true;
-        while (true) {
-            const bool nf = w.next(p);
-            if (nf) {
-                x = address(p.x[r]);
-                g = address(p.g[r]);
-                stat = w.stat(p) + grp;
-            } else {
-                x += p.x[r].head * (G * ES);
-                g += p.g[r].head * (G * ES);
-                stat += G;
-            }
-            if (w.left) load(r1, nf ? grp < heads : left > G);
+        for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
+            const bool in = w.blk * G + grp < heads, nf = w.next(p);
             if (fresh) {
                 tab.put(ang, p, pos, lane);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     c[i] = f2s(1.f);
                     s[i] = f2s(0.f);
-                    const int at = p.inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
-                    if (p.inter ? (2 * i < H ? ch.ra : ch.rb) : ch.ra) {
+                    const int at = inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
+                    if (inter ? (2 * i < H ? ch.ra : ch.rb) : ch.ra) {
                         c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
                         s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
                     }
                 }
             }
             if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
+            rope_cp_wait<DEPTH - 1>();
             // the gradient turned back (the sign of s is the transpose's)
             float2 ta[H], tb[H];
             {
                 float2 ga[H], gb[H];
-                rope_unpack<XT, V>(r0.ga, ga);
-                rope_unpack<XT, V>(r0.gb, gb);
-                if (p.inter) {
+                rope_unpack<XT, V>(ring[slot].g[0][lane], ga);
+                rope_unpack<XT, V>(ring[slot].g[1][lane], gb);
+                if (inter) {
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
                         const float cj = i & 1 ? c[H / 2 + i / 2].y : c[H / 2 + i / 2].x,
                                     sj = i & 1 ? s[H / 2 + i / 2].y : s[H / 2 + i / 2].x;
                         float2 u = f2swap(ga[i]), v = f2swap(gb[i]);
-                        if (!all) {
+                        if constexpr (KIND == kRopeSome) {
                             u = ch.ra ? u : f2s(0.f);
                             v = ch.rb ? v : f2s(0.f);
                         }
@@ -432,7 +452,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         float2 u = gb[i], v = ga[i];
-                        if (!all) {
+                        if constexpr (KIND == kRopeSome) {
                             u = ch.ra ? u : f2s(0.f);
                             v = ch.ra ? v : f2s(0.f);
                         }
@@ -442,9 +462,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 }
             }
             float2 xa[H], xb[H];
-            rope_unpack<XT, V>(r0.xa, xa);
-            rope_unpack<XT, V>(r0.xb, xb);
-            const float rstd = r0.rstd, mean = r0.mean;
+            rope_unpack<XT, V>(ring[slot].x[0][lane], xa);
+            rope_unpack<XT, V>(ring[slot].x[1][lane], xb);
+            const float rstd = ring[slot].rstd[lane], mean = LN ? ring[slot].mean[lane] : 0.f;
+            load(slot);
             float2 dot = f2s(0.f), sum = f2s(0.f);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
@@ -478,20 +499,15 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 tb[i] = f2mul(f2fma(xb[i], c2, tb[i]), f2s(rstd));
             }
             const RopeRaw<XT, V> oa = rope_pack<XT, V>(ta), ob = rope_pack<XT, V>(tb);
-            if (left > 0 && ch.oka) rope_st(y, oa.v);
-            if (left > 0 && ch.okb) rope_st(y + off, ob.v);
+            if (in && ch.oka) rope_st(y, oa.v);
+            if (in && ch.okb) rope_st(y + off, ob.v);
             if (!w.left) break;
-            if (nf) {
-                y = address(p.y[r]);
-                left = heads - grp;
-            } else {
-                y += p.y[r].head * (G * ES);
-                left -= G;
-            }
+            if (nf) y = address(p.y[r], w);
+            else y += p.y[r].head * (G * ES);
             fresh = nf;
-            r0 = r1;
         }
     }
+    __syncthreads();  // the rings of all warps have been read
     // the sums of the groups of lanes (the same columns) of a warp, then of the CTA's warps
     float *mine = rope_acc + warp * p.D;
     auto columns = [&](float2 (&u)[H], float2 (&v)[H]) {
