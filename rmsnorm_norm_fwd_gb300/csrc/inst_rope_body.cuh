@@ -12,13 +12,15 @@
 #endif
 #if GBN_MODE >= 0
 #define GBN_K(L, KIND, S) \
-    {(const void *)&rope_fwd_vec<GBN_MODE, GBN_XT, GBN_V, L, KIND, 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_fwd_smem(GBN_V, GBN_XT == kF32 ? 4 : 2, L)}
+    {(const void *)&rope_fwd_vec<GBN_MODE, GBN_XT, GBN_V, L, KIND, GBN_FU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
+     rope_fwd_smem(GBN_V, GBN_XT == kF32 ? 4 : 2, L, GBN_FU(KIND)), GBN_FU(KIND)}
 #else
 #define GBN_K(L, KIND, S) \
-    {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, L, KIND, 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_bwd_smem(GBN_V, GBN_XT == kF32 ? 4 : 2, L)}
+    {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, L, KIND, GBN_BU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
+     rope_bwd_smem(GBN_V, GBN_XT == kF32 ? 4 : 2, L, GBN_BU(KIND)), GBN_BU(KIND)}
 #endif
+#define GBN_FU(KIND) (GBN_MODE == 0 && KIND != kRopeSome ? 2 : 1)
+#define GBN_BU(KIND) 1
 #define GBN_ANY {GBN_K(4, kRopeSome, ""), GBN_K(8, kRopeSome, ""), GBN_K(16, kRopeSome, ""), GBN_K(32, kRopeSome, "")}
 
 namespace gbn {
@@ -33,6 +35,8 @@ const RopeVariant GBN_CAT(kRopeVec_, GBN_NAME)[kRopeVecKinds][kRopeVecLanes] = {
     GBN_ANY};
 }  // namespace gbn
 #undef GBN_K
+#undef GBN_FU
+#undef GBN_BU
 #undef GBN_ANY
 #undef GBN_MODE
 #undef GBN_XT

@@ -201,10 +201,10 @@ bool bad_aliasing(const Box *outs, int no, const Box *ins, int ni, int same_n) {
 thread_local const char *t_last[3] = {"", "", ""};
 
 // Passes of `at_once` heads, shared out over a grid of at most per_sm CTAs an
-// SM: warps for queries and for keys in proportion to their passes, one pass a
-// warp where that is few enough.  Returns the CTAs, -1 if a warp's passes do
+// SM: warps for queries and for keys in proportion to their work (or, with
+// `tokens`, for both together), one pass a warp where that is few enough.  Returns the CTAs, -1 if a warp's passes do
 // not fit its counter.
-int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, const HostDevice &d) {
+int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, bool tokens, const HostDevice &d) {
     int64_t cap = per_sm * d.sms;
     const int64_t limit = host_grid_limit();
     if (limit > 0 && limit < cap) cap = limit;
@@ -215,12 +215,18 @@ int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, co
         p->units[i] = s.tokens() * p->passes[i];
         total += p->units[i];
     }
-    if (total <= most) {
+    if (tokens) {
+        p->units[0] = total;
+        p->warps[0] = std::min(total, most);
+        p->units[1] = p->warps[1] = 0;
+    } else if (total <= most) {
         p->warps[0] = p->units[0];
         p->warps[1] = p->units[1];
     } else {
         // both in one tensor only if there is no second; else at least one warp each
-        const double part = (double)p->units[0] / (double)total * (double)most;
+        // a token's angles cost about as much as one and a half passes
+        const double q = (double)s.tokens() * (p->passes[0] + 1.5), k = (double)s.tokens() * (p->passes[1] + 1.5);
+        const double part = q / (q + k) * (double)most;
         p->warps[0] = s.tensors() == 1 ? most : std::min(most - 1, std::max<int64_t>(1, (int64_t)(part + 0.5)));
         p->warps[1] = most - p->warps[0];
     }
@@ -243,6 +249,7 @@ struct Kernel {
     int heads;  // of a pass
     int smem;
     int slot;   // its place in the cache of what a device holds
+    bool tokens;  // a warp takes queries and keys of its tokens (RopeTokens), else of one tensor (RopeWalk)
 };
 
 int any_size(int64_t D, int rot) {  // log2 of the pairs a lane holds
@@ -284,12 +291,14 @@ Kernel pick(int mode, const RopeParams &p) {
             if (slots <= 4 << l) {
                 const int t = p.xdt + (v == 8 ? 2 : 0);
                 const RopeVariant &k = tables[m][t][kind][l];
-                return {k.f, k.name, 8 >> l, k.smem, ((m * 5 + t) * kRopeVecKinds + kind) * kRopeVecLanes + l};
+                // gamma (and beta) of both tensors as fp32 behind the rings
+                const int par = mode == kRopeOnly ? 0 : mode == kRopeLn ? 16 * p.D : 8 * p.D;
+                return {k.f, k.name, (8 >> l) * k.u, k.smem + par, ((m * 5 + t) * kRopeVecKinds + kind) * kRopeVecLanes + l, mode >= 0};
             }
     }
     const int n = any_size(p.D, p.rot), slot = 5 * 5 * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
-    return mode < 0 ? Kernel{kRopeBwdAny[-1 - mode][n], "any", 1, kRopeWarps * p.D * 4, slot}
-                    : Kernel{kRopeFwdAny[mode][n], "any", 1, 0, slot};
+    return mode < 0 ? Kernel{kRopeBwdAny[-1 - mode][n], "any", 1, kRopeWarps * p.D * 4, slot, false}
+                    : Kernel{kRopeFwdAny[mode][n], "any", 1, 0, slot, false};
 }
 constexpr int kSlots = 5 * 5 * kRopeVecKinds * kRopeVecLanes + 5 * kRopeAnySizes;
 std::atomic<int> g_resident[kHostMaxDev][kSlots];
@@ -299,7 +308,9 @@ int resident(const Kernel &k, const HostDevice &d, int *out) {
     std::atomic<int> &c = g_resident[d.dev][k.slot];
     int o = c.load(std::memory_order_relaxed);
     if (o == 0) {
-        if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, std::max(k.smem, 48 * 1024)) != cudaSuccess ||
+        // heads of up to 512 elements share a slot: allow for the parameters of any
+        if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 std::max(k.smem + 8192, 48 * 1024)) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k.f, kRopeCTA, (size_t)k.smem) != cudaSuccess)
             return GBNORM_ERR_CUDA;
         if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
@@ -321,7 +332,7 @@ int run_fwd(int mode, RopeParams *p, const Shape &s, cudaStream_t st) {
     int per_sm;
     const int o = resident(k, d, &per_sm);
     if (o != GBNORM_OK) return o;
-    const int64_t grid = share(p, s, k.heads, per_sm, d);
+    const int64_t grid = share(p, s, k.heads, per_sm, k.tokens, d);
     if (grid < 0) return GBNORM_ERR_UNSUPPORTED;
     t_last[what] = k.name;
     return launch(k.f, grid, (size_t)k.smem, p, st);
@@ -454,7 +465,7 @@ int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_head
         const Kernel k = pick(-1 - is_layernorm, p);
         int per_sm;
         if ((e = resident(k, d, &per_sm)) != GBNORM_OK) return e;
-        P = share(&p, s, k.heads, std::min<int64_t>(per_sm, kBwdPerSm), d);
+        P = share(&p, s, k.heads, std::min<int64_t>(per_sm, kBwdPerSm), k.tokens, d);
         if (P < 0) return GBNORM_ERR_UNSUPPORTED;
         t_last[1] = k.name;
         e = launch(k.f, P, (size_t)k.smem, &p, stream);

@@ -113,6 +113,38 @@ struct RopeWalk {
     }
 };
 
+// The forward's share: contiguous passes over the tokens, each with its
+// queries' heads and then its keys', so that both take the token's angles.
+struct RopeTokens {
+    int left;  // passes to go, this one included
+    int b, s;  // token
+    int blk;   // pass within the token
+    __device__ __forceinline__ RopeTokens(const RopeParams &p) {
+        const int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), W = p.warps[0], U = p.units[0];
+        left = b = s = blk = 0;
+        if (w >= W) return;
+        const int64_t each = U / W, more = U % W, u = each * w + (w < more ? w : more);
+        const int np = p.passes[0] + p.passes[1];
+        left = (int)(each + (w < more ? 1 : 0));
+        const int64_t t = u / np;
+        blk = (int)(u - t * np);
+        b = (int)(t / p.S);
+        s = (int)(t - b * p.S);
+    }
+    // To the next pass; true if it belongs to another token.
+    __device__ __forceinline__ bool next(const RopeParams &p) {
+        --left;
+        if (++blk < p.passes[0] + p.passes[1]) return false;
+        blk = 0;
+        if (++s == (int)p.S) {
+            s = 0;
+            ++b;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int64_t at(const RopeHeads &h) const { return b * h.batch + s * h.token; }
+};
+
 // The backward's column sums of a CTA: acc[warp][D] in shared memory, each
 // warp's own row filled, added in the order of the warps into the CTA's
 // partial row [2][D] (or [1][D] without keys) of block `which`.

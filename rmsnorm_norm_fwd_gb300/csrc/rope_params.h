@@ -52,19 +52,23 @@ constexpr int kRopeAnySizes = 5;
 extern const void *const kRopeFwdAny[3][kRopeAnySizes];
 extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 
-// On vectors of v elements of es bytes, l lanes a head: passes in flight a
-// warp, and dynamic shared memory (rings and tables of cosines and sines; the
-// backward's column sums take the place of the rings).
+// On vectors of v elements of es bytes, l lanes a head, u heads a lane and
+// pass: passes in flight a warp, and dynamic shared memory without the
+// parameters (rings and tables of cosines and sines; the backward's column sums
+// take the place of the rings).
 constexpr int kRopeFwdDepth = 3, kRopeBwdDepth = 3;
-constexpr int rope_fwd_smem(int v, int es, int l) { return kRopeWarps * (kRopeFwdDepth * 64 * v * es + 8 * v * l); }
-constexpr int rope_bwd_smem(int v, int es, int l) {
-    return kRopeWarps * (kRopeBwdDepth * (128 * v * es + 256) + 8 * v * l);
+constexpr int rope_fwd_smem(int v, int es, int l, int u) {
+    return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * l);
+}
+constexpr int rope_bwd_smem(int v, int es, int l, int u) {
+    return kRopeWarps * (kRopeBwdDepth * u * (128 * v * es + 256) + 8 * v * l);
 }
 
 struct RopeVariant {
     const void *f;
     const char *name;
-    int smem;
+    int smem;  // without parameters
+    int u;     // heads a lane and pass
 };
 constexpr int kRopeVecLanes = 4;  // lanes a head: 4, 8, 16, 32
 constexpr int kRopeVecKinds = 3;  // RopeKind

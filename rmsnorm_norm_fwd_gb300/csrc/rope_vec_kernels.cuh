@@ -88,30 +88,17 @@ __device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, flo
 __device__ __forceinline__ void rope_cp_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void rope_cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// V parameters from element c of a row of dt, or V times `none` for a null row.
-template <int V>
-__device__ __forceinline__ void rope_param(const void *row, int c, int dt, float none, float2 (&f)[V / 2]) {
+// Row `row` of D parameters widened to fp32 into shared memory, a null row as `none`; every thread takes its share.
+__device__ __forceinline__ void rope_param(float *to, const void *row, int D, int dt, float none) {
+    for (int c = threadIdx.x; c < D; c += kRopeCTA) to[c] = row ? ld1(row, c, dt) : none;
+}
+// V values from shared memory.
+template <int V> __device__ __forceinline__ void rope_get(const float *from, float2 (&f)[V / 2]) {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) f[i] = f2s(none);
-    if (!row) return;
-    if (dt == kF32) {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + c) + i);
-            f[2 * i] = make_float2(v.x, v.y);
-            f[2 * i + 1] = make_float2(v.z, v.w);
-        }
-    } else {
-        uint32_t w[V / 2];
-        const uint2 *q = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + c);
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const uint2 v = __ldg(q + i);
-            w[2 * i] = v.x;
-            w[2 * i + 1] = v.y;
-        }
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) f[i] = dt == kBF16 ? rope_pair<kBF16>(w[i]) : rope_pair<kF16>(w[i]);
+    for (int i = 0; i < V / 4; ++i) {
+        const float4 v = reinterpret_cast<const float4 *>(from)[i];
+        f[2 * i] = make_float2(v.x, v.y);
+        f[2 * i + 1] = make_float2(v.z, v.w);
     }
 }
 
@@ -146,6 +133,8 @@ template <int V, int KIND> struct RopeChunks {
         b = cb * V;
         ra = oka && ca < nr;
         rb = okb && cb < nr;
+        if (!oka) a = pa = 0;  // lanes without a chunk stay inside the head
+        if (!okb) b = pb = 0;
     }
 };
 
@@ -166,8 +155,8 @@ template <int V, int L> struct RopeTable {
 };
 
 // The positions a lane needs for its pairs of the token at the walk.
-template <int N>
-__device__ __forceinline__ void rope_fetch(const RopeParams &p, const RopeAngles<N> &ang, const RopeWalk &w, int lane,
+template <int N, typename W>
+__device__ __forceinline__ void rope_fetch(const RopeParams &p, const RopeAngles<N> &ang, const W &w, int lane,
                                            uint64_t (&pos)[N]) {
     const int64_t at = w.b * p.pos_batch + w.s * p.pos_token;
 #pragma unroll
@@ -182,37 +171,51 @@ __device__ __forceinline__ void rope_fetch(const RopeParams &p, const RopeAngles
 
 __device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x); }
 
-template <int MODE, int XT, int V, int L, int KIND, int MINB>
+template <int MODE, int XT, int V, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_constant__ RopeParams p) {
     constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2, DEPTH = kRopeFwdDepth;
     using Table = RopeTable<V, L>;
     using Raw = RopeRaw<XT, V>;
-    extern __shared__ __align__(16) unsigned char rope_smem[];  // rings, then tables
+    // rings, tables, then gamma (and beta) of the queries and of the keys
+    extern __shared__ __align__(16) unsigned char rope_smem[];
     const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
-    Raw(*ring)[2][32] = reinterpret_cast<Raw(*)[2][32]>(rope_smem) + warp * DEPTH;
-    Table &tab = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * DEPTH * kRopeWarps)[warp];
-    RopeWalk w(p), ahead = w;  // the pass worked on, the pass to load
-    if (!w.left) return;
+    Raw(*ring)[U][2][32] = reinterpret_cast<Raw(*)[U][2][32]>(rope_smem) + warp * DEPTH;
+    Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * U * DEPTH * kRopeWarps);
+    float *par = reinterpret_cast<float *>(tables + kRopeWarps);
+    Table &tab = tables[warp];
+    RopeTokens w(p), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, KIND> ch(p, sl);
-    const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
-    auto address = [&](const RopeHeads &t, const RopeWalk &at) {
-        return static_cast<char *>(t.p) + (at.at(t) + (int64_t)(at.blk * G + grp) * t.head + ch.a) * ES;
-    };
-    const char *x = address(p.x[r], ahead);
+    const int nq = p.passes[0];
+    const bool fill_a = ch.oka, fill_b = ch.okb;
+    // head of this lane's in a pass; past the last one it repeats that, unstored
+    auto head = [&](int blk, int r, int u) { return (blk - (r ? nq : 0)) * (G * U) + u * G + grp; };
     auto load = [&](int slot) {
         if (ahead.left) {
-            const bool in = ahead.blk * G + grp < heads, a = in && ch.oka, b = in && ch.okb;
-            rope_cp(&ring[slot][0][lane], a ? x : p.x[r].p, a, Raw{}.v);
-            rope_cp(&ring[slot][1][lane], b ? x + off : p.x[r].p, b, Raw{}.v);
-            if (ahead.next(p)) x = address(p.x[r], ahead);
-            else x += p.x[r].head * (G * ES);
+            const int r = ahead.blk >= nq, last = p.heads[r] - 1;
+            const char *x = static_cast<const char *>(p.x[r].p) + ahead.at(p.x[r]) * ES;
+            const int64_t step = p.x[r].head * ES;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = head(ahead.blk, r, u);
+                const char *q = x + (h < last ? h : last) * step;
+                rope_cp(&ring[slot][u][0][lane], q + ch.a * ES, fill_a, Raw{}.v);
+                rope_cp(&ring[slot][u][1][lane], q + ch.b * ES, fill_b, Raw{}.v);
+            }
+            ahead.next(p);
         }
         rope_cp_end();
     };
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) load(i);
-    char *y = address(p.y[r], w);
-    int64_t stat = w.stat(p) + w.blk * G + grp;
+    if constexpr (MODE != kRopeOnly) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            rope_param(par + r * p.D, p.gamma[r], p.D, p.pdt, 1.f);
+            if constexpr (MODE == kRopeLn) rope_param(par + (2 + r) * p.D, p.beta[r], p.D, p.pdt, 0.f);
+        }
+        __syncthreads();
+    }
+    if (!w.left) return;
     RopeAngles<Table::PER> ang;
     ang.init(p, lane);
     uint64_t pos[Table::PER];
@@ -220,22 +223,25 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     const float inv = 1.f / (float)p.D;
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
-    bool fresh = true;
+    bool fresh = true, turn = true;  // another token's angles, another tensor's coefficients
     for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
-        const bool in = w.blk * G + grp < heads, nf = w.next(p);
-        if (fresh) {
-            tab.put(ang, p, pos, lane);
+        const int r = w.blk >= nq, h0 = head(w.blk, r, 0), heads = p.heads[r];
+        char *y = static_cast<char *>(p.y[r].p) + w.at(p.y[r]) * ES;
+        const int64_t stat = (w.b * p.S + w.s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0);
+        const bool nf = w.next(p);
+        if (fresh) tab.put(ang, p, pos, lane);
+        if (turn) {
             float2 ga[H], gb[H];
             if constexpr (MODE != kRopeOnly) {
-                rope_param<V>(ch.oka ? p.gamma[r] : nullptr, ch.a, p.pdt, 1.f, ga);
-                rope_param<V>(ch.okb ? p.gamma[r] : nullptr, ch.b, p.pdt, 1.f, gb);
+                rope_get<V>(par + r * p.D + ch.a, ga);
+                rope_get<V>(par + r * p.D + ch.b, gb);
             } else {
 #pragma unroll
                 for (int i = 0; i < H; ++i) ga[i] = gb[i] = f2s(1.f);
             }
             if constexpr (MODE == kRopeLn) {
-                rope_param<V>(ch.oka ? p.beta[r] : nullptr, ch.a, p.pdt, 0.f, ba);
-                rope_param<V>(ch.okb ? p.beta[r] : nullptr, ch.b, p.pdt, 0.f, bb);
+                rope_get<V>(par + (2 + r) * p.D + ch.a, ba);
+                rope_get<V>(par + (2 + r) * p.D + ch.b, bb);
             }
 #pragma unroll
             for (int i = 0; i < H; ++i) {
@@ -246,14 +252,14 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
             if (inter) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    if (ch.ra) {
+                    if (KIND != kRopeSome || ch.ra) {
                         const float c = tab.c[ch.pa + i], s = tab.s[ch.pa + i];
                         ca[i] = make_float2(ga[i].x * c, ga[i].y * c);
                         sa[i] = make_float2(-ga[i].y * s, ga[i].x * s);
                         if constexpr (MODE == kRopeLn)
                             ba[i] = make_float2(ba[i].x * c - ba[i].y * s, ba[i].y * c + ba[i].x * s);
                     }
-                    if (ch.rb) {
+                    if (KIND != kRopeSome || ch.rb) {
                         const float c = tab.c[ch.pb + i], s = tab.s[ch.pb + i];
                         cb[i] = make_float2(gb[i].x * c, gb[i].y * c);
                         sb[i] = make_float2(-gb[i].y * s, gb[i].x * s);
@@ -261,158 +267,158 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                             bb[i] = make_float2(bb[i].x * c - bb[i].y * s, bb[i].y * c + bb[i].x * s);
                     }
                 }
-            } else if (ch.ra) {
+            } else if (KIND != kRopeSome || ch.ra) {
+                float2 c[H], s[H];
+                rope_get<V>(tab.c + ch.pa, c);
+                rope_get<V>(tab.s + ch.pa, s);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    const float2 c = *reinterpret_cast<const float2 *>(tab.c + ch.pa + 2 * i),
-                                 s = *reinterpret_cast<const float2 *>(tab.s + ch.pa + 2 * i);
-                    ca[i] = f2mul(ga[i], c);
-                    sa[i] = f2mul(gb[i], make_float2(-s.x, -s.y));
-                    cb[i] = f2mul(gb[i], c);
-                    sb[i] = f2mul(ga[i], s);
+                    ca[i] = f2mul(ga[i], c[i]);
+                    sa[i] = f2mul(gb[i], make_float2(-s[i].x, -s[i].y));
+                    cb[i] = f2mul(gb[i], c[i]);
+                    sb[i] = f2mul(ga[i], s[i]);
                     if constexpr (MODE == kRopeLn) {
                         const float2 v = ba[i];
-                        ba[i] = make_float2(v.x * c.x - bb[i].x * s.x, v.y * c.y - bb[i].y * s.y);
-                        bb[i] = make_float2(bb[i].x * c.x + v.x * s.x, bb[i].y * c.y + v.y * s.y);
+                        ba[i] = make_float2(v.x * c[i].x - bb[i].x * s[i].x, v.y * c[i].y - bb[i].y * s[i].y);
+                        bb[i] = make_float2(bb[i].x * c[i].x + v.x * s[i].x, bb[i].y * c[i].y + v.y * s[i].y);
                     }
                 }
             }
         }
         if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
         rope_cp_wait<DEPTH - 1>();
-        float2 va[H], vb[H];
-        rope_unpack<XT, V>(ring[slot][0][lane], va);
-        rope_unpack<XT, V>(ring[slot][1][lane], vb);
+        Raw ra[U], rb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ra[u] = ring[slot][u][0][lane];
+            rb[u] = ring[slot][u][1][lane];
+        }
         load(slot);
-        if constexpr (MODE != kRopeOnly) {
-            float mean = 0.f;
-            if constexpr (MODE == kRopeLn) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * G;
+            float2 va[H], vb[H];
+            rope_unpack<XT, V>(ra[u], va);
+            rope_unpack<XT, V>(rb[u], vb);
+            if constexpr (MODE != kRopeOnly) {
+                float mean = 0.f;
+                if constexpr (MODE == kRopeLn) {
+                    float2 t = f2s(0.f);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) t = f2add(t, f2add(va[i], vb[i]));
+                    float sum[1] = {t.x + t.y};
+                    group_sum<L, 1>(sum);
+                    mean = sum[0] * inv;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        va[i] = ch.oka ? f2add(va[i], f2s(-mean)) : f2s(0.f);
+                        vb[i] = ch.okb ? f2add(vb[i], f2s(-mean)) : f2s(0.f);
+                    }
+                }
                 float2 t = f2s(0.f);
 #pragma unroll
-                for (int i = 0; i < H; ++i) t = f2add(t, f2add(va[i], vb[i]));
-                float sum[1] = {t.x + t.y};
-                group_sum<L, 1>(sum);
-                mean = sum[0] * inv;
+                for (int i = 0; i < H; ++i) t = f2fma(va[i], va[i], f2fma(vb[i], vb[i], t));
+                float sq[1] = {t.x + t.y};
+                group_sum<L, 1>(sq);
+                const float rstd = rsqrtf(sq[0] * inv + p.eps);
+                if (p.rstd && sl == 0 && h < heads) p.rstd[stat + h] = rstd;
+                if (MODE == kRopeLn && p.mean && sl == 0 && h < heads) p.mean[stat + h] = mean;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    va[i] = ch.oka ? f2add(va[i], f2s(-mean)) : f2s(0.f);
-                    vb[i] = ch.okb ? f2add(vb[i], f2s(-mean)) : f2s(0.f);
+                    va[i] = f2mul(va[i], f2s(rstd));
+                    vb[i] = f2mul(vb[i], f2s(rstd));
                 }
             }
-            float2 t = f2s(0.f);
-#pragma unroll
-            for (int i = 0; i < H; ++i) t = f2fma(va[i], va[i], f2fma(vb[i], vb[i], t));
-            float sq[1] = {t.x + t.y};
-            group_sum<L, 1>(sq);
-            const float rstd = rsqrtf(sq[0] * inv + p.eps);
-            if (sl == 0 && in) {
-                if (p.rstd) p.rstd[stat] = rstd;
-                if (MODE == kRopeLn && p.mean) p.mean[stat] = mean;
-            }
+            float2 ua[H], ub[H];
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                va[i] = f2mul(va[i], f2s(rstd));
-                vb[i] = f2mul(vb[i], f2s(rstd));
+                float2 ta = inter ? f2swap(va[i]) : vb[i], tb = inter ? f2swap(vb[i]) : va[i];
+                if constexpr (KIND == kRopeSome) {  // an element that is not rotated takes nothing from another, not even a NaN
+                    ta = ch.ra ? ta : f2s(0.f);
+                    tb = ch.rb ? tb : f2s(0.f);
+                }
+                ua[i] = f2fma(va[i], ca[i], f2mul(ta, sa[i]));
+                ub[i] = f2fma(vb[i], cb[i], f2mul(tb, sb[i]));
+                if constexpr (MODE == kRopeLn) {
+                    ua[i] = f2add(ua[i], ba[i]);
+                    ub[i] = f2add(ub[i], bb[i]);
+                }
             }
+            char *q = y + h * (p.y[r].head * ES);
+            if (h < heads && ch.oka) rope_st(q + ch.a * ES, rope_pack<XT, V>(ua).v);
+            if (h < heads && ch.okb) rope_st(q + ch.b * ES, rope_pack<XT, V>(ub).v);
         }
-        RopeRaw<XT, V> oa, ob;
-        float2 ua[H], ub[H];
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            float2 ta = inter ? f2swap(va[i]) : vb[i], tb = inter ? f2swap(vb[i]) : va[i];
-            if constexpr (KIND == kRopeSome) {  // an element that is not rotated takes nothing from another, not even a NaN
-                ta = ch.ra ? ta : f2s(0.f);
-                tb = ch.rb ? tb : f2s(0.f);
-            }
-            ua[i] = f2fma(va[i], ca[i], f2mul(ta, sa[i]));
-            ub[i] = f2fma(vb[i], cb[i], f2mul(tb, sb[i]));
-            if constexpr (MODE == kRopeLn) {
-                ua[i] = f2add(ua[i], ba[i]);
-                ub[i] = f2add(ub[i], bb[i]);
-            }
-        }
-        oa = rope_pack<XT, V>(ua);
-        ob = rope_pack<XT, V>(ub);
-        if (in && ch.oka) rope_st(y, oa.v);
-        if (in && ch.okb) rope_st(y + off, ob.v);
-        if (!w.left) break;
-        if (nf) {
-            y = address(p.y[r], w);
-            stat = w.stat(p) + grp;
-        } else {
-            y += p.y[r].head * (G * ES);
-            stat += G;
-        }
+        if (!w.left) return;
         fresh = nf;
+        turn = nf || w.blk == nq;
     }
 }
 
-template <bool LN, int XT, int V, int L, int KIND, int MINB>
+template <bool LN, int XT, int V, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
-    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2;
+    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2, DEPTH = kRopeBwdDepth;
     using Table = RopeTable<V, L>;
-    // rings of passes, then tables; at the end the column sums [kRopeWarps][D] in their place
-    extern __shared__ __align__(16) unsigned char rope_smem[];
-    constexpr int DEPTH = kRopeBwdDepth;
     using Raw = RopeRaw<XT, V>;
     struct Slot {
-        Raw x[2][32], g[2][32];
-        float mean[32], rstd[32];
+        Raw x[U][2][32], g[U][2][32];
+        float mean[U][32], rstd[U][32];
     };
+    // rings, tables, gamma of the queries and of the keys; at the end the column sums [kRopeWarps][D] over the rings
+    extern __shared__ __align__(16) unsigned char rope_smem[];
     const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
     Slot *ring = reinterpret_cast<Slot *>(rope_smem) + warp * DEPTH;
-    Table &tab = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps)[warp];
-    float *rope_acc = reinterpret_cast<float *>(rope_smem);
+    Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps);
+    float *par = reinterpret_cast<float *>(tables + kRopeWarps), *rope_acc = reinterpret_cast<float *>(rope_smem);
+    Table &tab = tables[warp];
     RopeWalk w(p), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, KIND> ch(p, sl);
-    const int r = w.r, heads = p.heads[r], off = (ch.b - ch.a) * ES;
-    auto address = [&](const RopeHeads &t, const RopeWalk &at) {
-        return static_cast<char *>(t.p) + (at.at(t) + (int64_t)(at.blk * G + grp) * t.head + ch.a) * ES;
+    const int r = w.r, heads = p.heads[r];
+    auto load = [&](int slot) {
+        if (ahead.left) {
+            const char *x = static_cast<const char *>(p.x[r].p) + ahead.at(p.x[r]) * ES,
+                       *g = static_cast<const char *>(p.g[r].p) + ahead.at(p.g[r]) * ES;
+            const int64_t stat = ahead.stat(p), xs = p.x[r].head * ES, gs = p.g[r].head * ES;
+            Slot &to = ring[slot];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // past the last head a lane repeats that with a gradient of zeros, unstored
+                const int h0 = ahead.blk * (G * U) + u * G + grp, h = h0 < heads ? h0 : heads - 1;
+                const bool in = h0 < heads;
+                rope_cp(&to.x[u][0][lane], x + h * xs + ch.a * ES, ch.oka, Raw{}.v);
+                rope_cp(&to.x[u][1][lane], x + h * xs + ch.b * ES, ch.okb, Raw{}.v);
+                rope_cp(&to.g[u][0][lane], g + h * gs + ch.a * ES, in && ch.oka, Raw{}.v);
+                rope_cp(&to.g[u][1][lane], g + h * gs + ch.b * ES, in && ch.okb, Raw{}.v);
+                rope_cp(&to.rstd[u][lane], p.rstd + stat + h, true, 0.f);
+                if constexpr (LN) rope_cp(&to.mean[u][lane], p.mean + stat + h, true, 0.f);
+            }
+            ahead.next(p);
+        }
+        rope_cp_end();
     };
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) load(i);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rope_param(par + i * p.D, p.gamma[i], p.D, p.pdt, 1.f);
+    __syncthreads();
     float2 da[H], db[H], ea[H], eb[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
     if (w.left) {
-        const char *x = address(p.x[r], ahead), *g = address(p.g[r], ahead);
-        int64_t stat = w.stat(p) + w.blk * G + grp;
-        auto load = [&](int i) {
-            if (ahead.left) {
-                const bool in = ahead.blk * G + grp < heads, a = in && ch.oka, b = in && ch.okb;
-                Slot &to = ring[i];
-                rope_cp(&to.x[0][lane], a ? x : p.x[r].p, a, Raw{}.v);
-                rope_cp(&to.g[0][lane], a ? g : p.g[r].p, a, Raw{}.v);
-                rope_cp(&to.x[1][lane], b ? x + off : p.x[r].p, b, Raw{}.v);
-                rope_cp(&to.g[1][lane], b ? g + off : p.g[r].p, b, Raw{}.v);
-                rope_cp(&to.rstd[lane], p.rstd + (in ? stat : 0), in, 0.f);
-                if constexpr (LN) rope_cp(&to.mean[lane], p.mean + (in ? stat : 0), in, 0.f);
-                if (ahead.next(p)) {
-                    x = address(p.x[r], ahead);
-                    g = address(p.g[r], ahead);
-                    stat = ahead.stat(p) + grp;
-                } else {
-                    x += p.x[r].head * (G * ES);
-                    g += p.g[r].head * (G * ES);
-                    stat += G;
-                }
-            }
-            rope_cp_end();
-        };
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) load(i);
-        char *y = address(p.y[r], w);
         RopeAngles<Table::PER> ang;
         ang.init(p, lane);
         uint64_t pos[Table::PER];
         rope_fetch(p, ang, w, lane, pos);
-        float2 wa[H], wb[H], c[V / 2], s[V / 2];  // c, s: of the pairs of the chunks (neighbours: first a's, then b's)
-        rope_param<V>(ch.oka ? p.gamma[r] : nullptr, ch.a, p.pdt, 1.f, wa);
-        rope_param<V>(ch.okb ? p.gamma[r] : nullptr, ch.b, p.pdt, 1.f, wb);
+        float2 wa[H], wb[H], c[H], s[H];  // c, s: of the pairs of the chunks (neighbours: first a's, then b's)
+        rope_get<V>(par + r * p.D + ch.a, wa);
+        rope_get<V>(par + r * p.D + ch.b, wb);
         const float inv = 1.f / (float)p.D;
         const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
         bool fresh = true;
         for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
-            const bool in = w.blk * G + grp < heads, nf = w.next(p);
+            char *y = static_cast<char *>(p.y[r].p) + w.at(p.y[r]) * ES;
+            const int h0 = w.blk * (G * U) + grp;
+            const bool nf = w.next(p);
             if (fresh) {
                 tab.put(ang, p, pos, lane);
 #pragma unroll
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                     c[i] = f2s(1.f);
                     s[i] = f2s(0.f);
                     const int at = inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
-                    if (inter ? (2 * i < H ? ch.ra : ch.rb) : ch.ra) {
+                    if (KIND != kRopeSome || (inter ? (2 * i < H ? ch.ra : ch.rb) : ch.ra)) {
                         c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
                         s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
                     }
@@ -428,82 +434,84 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
             }
             if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
             rope_cp_wait<DEPTH - 1>();
-            // the gradient turned back (the sign of s is the transpose's)
-            float2 ta[H], tb[H];
-            {
-                float2 ga[H], gb[H];
-                rope_unpack<XT, V>(ring[slot].g[0][lane], ga);
-                rope_unpack<XT, V>(ring[slot].g[1][lane], gb);
-                if (inter) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
-                        const float cj = i & 1 ? c[H / 2 + i / 2].y : c[H / 2 + i / 2].x,
-                                    sj = i & 1 ? s[H / 2 + i / 2].y : s[H / 2 + i / 2].x;
-                        float2 u = f2swap(ga[i]), v = f2swap(gb[i]);
-                        if constexpr (KIND == kRopeSome) {
-                            u = ch.ra ? u : f2s(0.f);
-                            v = ch.rb ? v : f2s(0.f);
+            for (int u = 0; u < U; ++u) {
+                // the gradient turned back (the sign of s is the transpose's)
+                float2 ta[H], tb[H];
+                {
+                    float2 ga[H], gb[H];
+                    rope_unpack<XT, V>(ring[slot].g[u][0][lane], ga);
+                    rope_unpack<XT, V>(ring[slot].g[u][1][lane], gb);
+                    if (inter) {
+#pragma unroll
+                        for (int i = 0; i < H; ++i) {
+                            const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
+                            const float cj = i & 1 ? c[H / 2 + i / 2].y : c[H / 2 + i / 2].x,
+                                        sj = i & 1 ? s[H / 2 + i / 2].y : s[H / 2 + i / 2].x;
+                            float2 m = f2swap(ga[i]), n = f2swap(gb[i]);
+                            if constexpr (KIND == kRopeSome) {
+                                m = ch.ra ? m : f2s(0.f);
+                                n = ch.rb ? n : f2s(0.f);
+                            }
+                            ta[i] = make_float2(ga[i].x * ci - m.x * si, ga[i].y * ci + m.y * si);
+                            tb[i] = make_float2(gb[i].x * cj - n.x * sj, gb[i].y * cj + n.y * sj);
                         }
-                        ta[i] = make_float2(ga[i].x * ci - u.x * si, ga[i].y * ci + u.y * si);
-                        tb[i] = make_float2(gb[i].x * cj - v.x * sj, gb[i].y * cj + v.y * sj);
-                    }
-                } else {
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        float2 u = gb[i], v = ga[i];
-                        if constexpr (KIND == kRopeSome) {
-                            u = ch.ra ? u : f2s(0.f);
-                            v = ch.ra ? v : f2s(0.f);
+                        for (int i = 0; i < H; ++i) {
+                            float2 m = gb[i], n = ga[i];
+                            if constexpr (KIND == kRopeSome) {
+                                m = ch.ra ? m : f2s(0.f);
+                                n = ch.ra ? n : f2s(0.f);
+                            }
+                            ta[i] = f2fma(ga[i], c[i], f2mul(make_float2(-m.x, -m.y), s[i]));
+                            tb[i] = f2fma(gb[i], c[i], f2mul(n, s[i]));
                         }
-                        ta[i] = f2fma(ga[i], c[i], f2mul(make_float2(-u.x, -u.y), s[i]));
-                        tb[i] = f2fma(gb[i], c[i], f2mul(v, s[i]));
                     }
                 }
-            }
-            float2 xa[H], xb[H];
-            rope_unpack<XT, V>(ring[slot].x[0][lane], xa);
-            rope_unpack<XT, V>(ring[slot].x[1][lane], xb);
-            const float rstd = ring[slot].rstd[lane], mean = LN ? ring[slot].mean[lane] : 0.f;
-            load(slot);
-            float2 dot = f2s(0.f), sum = f2s(0.f);
+                float2 xa[H], xb[H];
+                rope_unpack<XT, V>(ring[slot].x[u][0][lane], xa);
+                rope_unpack<XT, V>(ring[slot].x[u][1][lane], xb);
+                const float rstd = ring[slot].rstd[u][lane], mean = LN ? ring[slot].mean[u][lane] : 0.f;
+                if (u == U - 1) load(slot);
+                float2 dot = f2s(0.f), sum = f2s(0.f);
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if constexpr (LN) {
-                    xa[i] = f2add(xa[i], f2s(-mean));
-                    xb[i] = f2add(xb[i], f2s(-mean));
-                    ea[i] = f2add(ea[i], ta[i]);
-                    eb[i] = f2add(eb[i], tb[i]);
+                for (int i = 0; i < H; ++i) {
+                    if constexpr (LN) {
+                        xa[i] = f2add(xa[i], f2s(-mean));
+                        xb[i] = f2add(xb[i], f2s(-mean));
+                        ea[i] = f2add(ea[i], ta[i]);
+                        eb[i] = f2add(eb[i], tb[i]);
+                    }
+                    xa[i] = f2mul(xa[i], f2s(rstd));
+                    xb[i] = f2mul(xb[i], f2s(rstd));
+                    da[i] = f2fma(ta[i], xa[i], da[i]);
+                    db[i] = f2fma(tb[i], xb[i], db[i]);
+                    ta[i] = f2mul(ta[i], wa[i]);
+                    tb[i] = f2mul(tb[i], wb[i]);
+                    dot = f2fma(ta[i], xa[i], f2fma(tb[i], xb[i], dot));
+                    if constexpr (LN) sum = f2add(sum, f2add(ta[i], tb[i]));
                 }
-                xa[i] = f2mul(xa[i], f2s(rstd));
-                xb[i] = f2mul(xb[i], f2s(rstd));
-                da[i] = f2fma(ta[i], xa[i], da[i]);
-                db[i] = f2fma(tb[i], xb[i], db[i]);
-                ta[i] = f2mul(ta[i], wa[i]);
-                tb[i] = f2mul(tb[i], wb[i]);
-                dot = f2fma(ta[i], xa[i], f2fma(tb[i], xb[i], dot));
-                if constexpr (LN) sum = f2add(sum, f2add(ta[i], tb[i]));
-            }
-            float v[LN ? 2 : 1];
-            v[0] = dot.x + dot.y;
-            if constexpr (LN) v[1] = sum.x + sum.y;
-            group_sum<L, LN ? 2 : 1>(v);
-            const float2 c2 = f2s(-v[0] * inv), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv : 0.f);
+                float v[LN ? 2 : 1];
+                v[0] = dot.x + dot.y;
+                if constexpr (LN) v[1] = sum.x + sum.y;
+                group_sum<L, LN ? 2 : 1>(v);
+                const float2 c2 = f2s(-v[0] * inv), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv : 0.f);
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if constexpr (LN) {
-                    ta[i] = f2add(ta[i], c1);
-                    tb[i] = f2add(tb[i], c1);
+                for (int i = 0; i < H; ++i) {
+                    if constexpr (LN) {
+                        ta[i] = f2add(ta[i], c1);
+                        tb[i] = f2add(tb[i], c1);
+                    }
+                    ta[i] = f2mul(f2fma(xa[i], c2, ta[i]), f2s(rstd));
+                    tb[i] = f2mul(f2fma(xb[i], c2, tb[i]), f2s(rstd));
                 }
-                ta[i] = f2mul(f2fma(xa[i], c2, ta[i]), f2s(rstd));
-                tb[i] = f2mul(f2fma(xb[i], c2, tb[i]), f2s(rstd));
+                const int h = h0 + u * G;
+                char *q = y + h * (p.y[r].head * ES);
+                if (h < heads && ch.oka) rope_st(q + ch.a * ES, rope_pack<XT, V>(ta).v);
+                if (h < heads && ch.okb) rope_st(q + ch.b * ES, rope_pack<XT, V>(tb).v);
             }
-            const RopeRaw<XT, V> oa = rope_pack<XT, V>(ta), ob = rope_pack<XT, V>(tb);
-            if (in && ch.oka) rope_st(y, oa.v);
-            if (in && ch.okb) rope_st(y + off, ob.v);
             if (!w.left) break;
-            if (nf) y = address(p.y[r], w);
-            else y += p.y[r].head * (G * ES);
             fresh = nf;
         }
     }
