@@ -150,6 +150,7 @@ int common(const gbnorm_rope_t *r, bool need_rotation, Shape *s, RopeParams *p) 
         if (n[i] > 1 && (st[i] < 0 || st[i] > kMostBytes / 64 / n[i])) return GBNORM_ERR_INVALID_ARG;
     p->pos = r->positions;
     p->pos64 = ps == 8;
+    p->axes = r->axes;
     p->pos_axis = r->axes > 1 ? r->pos_axis : 0;
     p->pos_batch = s->B > 1 ? r->pos_batch : 0;
     p->pos_token = s->S > 1 ? r->pos_token : 0;
@@ -180,9 +181,7 @@ int take(const gbnorm_heads_t *h, const Shape &s, int dtype, bool out, RopeHeads
 // The plain arrays of a call, all read: parameters, statistics, positions, frequencies.
 int64_t pos_bytes(const RopeParams &p) {
     if (!p.pos || p.B * p.S == 0) return 0;
-    int axes = 1;
-    for (int j = 0; j < p.rot / 2; ++j) axes = std::max(axes, 1 + (int)((p.axis[j / 16] >> (2 * (j % 16))) & 3u));
-    return ((axes - 1) * p.pos_axis + (p.B - 1) * p.pos_batch + (p.S - 1) * p.pos_token + 1) * (p.pos64 ? 8 : 4);
+    return ((p.axes - 1) * p.pos_axis + (p.B - 1) * p.pos_batch + (p.S - 1) * p.pos_token + 1) * (p.pos64 ? 8 : 4);
 }
 
 // outs may overlap nothing, except that outs[i] may be exactly ins[i] for i < same_n.

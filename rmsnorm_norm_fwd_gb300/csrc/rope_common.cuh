@@ -42,6 +42,18 @@ __device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
     return (bits >> 31) ? 0 - r : r;
 }
 
+__device__ __forceinline__ uint32_t rope_axis(const RopeParams &p, int j) {
+    return (p.axis[j >> 4] >> (2 * (j & 15))) & 3u;
+}
+// cos and sign * sin of u 2^-64 turns.  sincospif takes half turns: the top bits of u as a multiple of 2^-63, in fp32,
+// exact down to angles that do not matter.
+__device__ __forceinline__ void rope_sincos(uint64_t u, float sign, float *c, float *s) {
+    float sn, cs;
+    sincospif(__ll2float_rn((long long)u) * 1.0842021724855044e-19f, &sn, &cs);
+    *c = cs;
+    *s = sn * sign;
+}
+
 // The pairs whose angles a lane computes: lane, lane + 32, ... (N of them).
 template <int N> struct RopeAngles {
     uint64_t f[N];
@@ -55,7 +67,7 @@ template <int N> struct RopeAngles {
             if (2 * j >= p.rot) continue;
             bool b;
             f[i] = rope_turns(__ldg(p.inv_freq + j), &b);
-            axis |= ((p.axis[j >> 4] >> (2 * (j & 15))) & 3u) << (2 * i);
+            axis |= rope_axis(p, j) << (2 * i);
             bad |= (uint32_t)b << i;
         }
     }
@@ -64,12 +76,7 @@ template <int N> struct RopeAngles {
         const int64_t q = at + (int64_t)((axis >> (2 * i)) & 3u) * p.pos_axis;
         const int64_t pos = p.pos64 ? __ldg(static_cast<const long long *>(p.pos) + q)
                                     : (int64_t)__ldg(static_cast<const int *>(p.pos) + q);
-        turn((uint64_t)pos * f[i], i, p.sign, c, s);
-    }
-    // sincospif takes half turns: a multiple of 2^-63 of one, exact down to angles that do not matter in fp32.
-    __device__ __forceinline__ void turn(uint64_t u, int i, float sign, float *c, float *s) const {
-        sincospif(__ll2float_rn((long long)u) * 1.0842021724855044e-19f, s, c);  // 2^-63
-        *s *= sign;
+        rope_sincos((uint64_t)pos * f[i], p.sign, c, s);
         if ((bad >> i) & 1u) *s = *c = __int_as_float(0x7fffffff);
     }
 };

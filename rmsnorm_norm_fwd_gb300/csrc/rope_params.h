@@ -39,7 +39,7 @@ struct RopeParams {
     int heads[2];
     int D, rot;
     int inter;             // pairs (2j, 2j + 1), else (j, j + rot / 2)
-    int pos64;
+    int pos64, axes;
     int xdt, ydt, pdt;
     float eps, sign;       // sign -1: the rotation's transpose
     uint32_t axis[kRopeMaxDim / 2 / 16];  // the axis of pair j: bits 2 (j mod 16) of word j / 16
@@ -54,14 +54,14 @@ extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 
 // On vectors of v elements of es bytes, l lanes a head, u heads a lane and
 // pass: passes in flight a warp, and dynamic shared memory without the
-// parameters (rings and tables of cosines and sines; the backward's column sums
+// parameters (rings, tables of cosines and sines, frequencies; the backward's column sums
 // take the place of the rings).
 constexpr int kRopeFwdDepth = 3, kRopeBwdDepth = 3;
 constexpr int rope_fwd_smem(int v, int es, int l, int u) {
-    return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * l);
+    return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * (l + 1)) + 12 * v * l;
 }
 constexpr int rope_bwd_smem(int v, int es, int l, int u) {
-    return kRopeWarps * (kRopeBwdDepth * u * (128 * v * es + 256) + 8 * v * l);
+    return kRopeWarps * (kRopeBwdDepth * u * (128 * v * es + 256) + 8 * v * (l + 1)) + 12 * v * l;
 }
 
 struct RopeVariant {

@@ -107,7 +107,7 @@ template <int V> __device__ __forceinline__ void rope_get(const float *from, flo
 enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopeSome = 2 };
 
 // The two chunks of a lane: first elements, whether they are there, whether they are rotated, and their first pair.
-template <int V, int KIND> struct RopeChunks {
+template <int V, int L, int KIND> struct RopeChunks {
     int a, b, pa, pb;
     bool oka, okb, ra, rb;
     __device__ __forceinline__ RopeChunks(const RopeParams &p, int sl) {
@@ -133,40 +133,68 @@ template <int V, int KIND> struct RopeChunks {
         b = cb * V;
         ra = oka && ca < nr;
         rb = okb && cb < nr;
-        if (!oka) a = pa = 0;  // lanes without a chunk stay inside the head
-        if (!okb) b = pb = 0;
+        if (!oka) a = 0;  // lanes without a chunk stay inside the head
+        if (!okb) b = 0;
+        if (!ra) pa = V * L;
+        if (!rb) pb = V * L;
     }
 };
 
+// The frequencies of a call in turns, once a CTA.
+template <int V, int L> struct RopeTurns {
+    static constexpr int N = V * L;
+    static_assert(N <= kRopeCTA, "a pair a thread");
+    uint64_t f[N];
+    float bad[N];  // 0, or NaN where the frequency is not a number of turns
+    __device__ __forceinline__ void fill(const RopeParams &p) {
+        const int j = threadIdx.x;
+        if (2 * j >= p.rot) return;
+        bool b;
+        f[j] = rope_turns(__ldg(p.inv_freq + j), &b);
+        bad[j] = b ? __int_as_float(0x7fffffff) : 0.f;
+    }
+};
 // A warp's cosines and sines: written by the lane that computed the pair, read by those whose chunks hold it.
 template <int V, int L> struct RopeTable {
     static constexpr int N = V * L, PER = N / 32 > 0 ? N / 32 : 1;
-    float c[N], s[N];
-    __device__ __forceinline__ void put(const RopeAngles<PER> &ang, const RopeParams &p, const uint64_t (&pos)[PER],
+    float c[N + V], s[N + V];  // the last V: what is not rotated
+    __device__ __forceinline__ void ones(int lane) {
+        if (lane < V) {
+            c[N + lane] = 1.f;
+            s[N + lane] = 0.f;
+        }
+    }
+    // pos: lane a holds the position on axis a; axis: two bits for each of the lane's pairs lane, lane + 32, ...
+    __device__ __forceinline__ void put(const RopeTurns<V, L> &turns, const RopeParams &p, int64_t pos, uint32_t axis,
                                         int lane) {
         __syncwarp();  // the last token's have been read
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int j = lane + 32 * i;
-            if (2 * j < p.rot) ang.turn(pos[i] * ang.f[i], i, p.sign, c + j, s + j);
+            const int64_t at = __shfl_sync(0xffffffffu, (long long)pos, (axis >> (2 * i)) & 3u);
+            if (2 * j < p.rot) {
+                float cs, sn;
+                rope_sincos((uint64_t)at * turns.f[j], p.sign, &cs, &sn);
+                c[j] = cs + turns.bad[j];
+                s[j] = sn + turns.bad[j];
+            }
         }
         __syncwarp();
     }
-};
-
-// The positions a lane needs for its pairs of the token at the walk.
-template <int N, typename W>
-__device__ __forceinline__ void rope_fetch(const RopeParams &p, const RopeAngles<N> &ang, const W &w, int lane,
-                                           uint64_t (&pos)[N]) {
-    const int64_t at = w.b * p.pos_batch + w.s * p.pos_token;
+    static __device__ __forceinline__ uint32_t axes(const RopeParams &p, int lane) {
+        uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        pos[i] = 0;
-        if (2 * (lane + 32 * i) >= p.rot) continue;
-        const int64_t q = at + (int64_t)((ang.axis >> (2 * i)) & 3u) * p.pos_axis;
-        pos[i] = p.pos64 ? (uint64_t)__ldg(static_cast<const long long *>(p.pos) + q)
-                         : (uint64_t)(int64_t)__ldg(static_cast<const int *>(p.pos) + q);
+        for (int i = 0; i < PER; ++i)
+            if (2 * (lane + 32 * i) < p.rot) a |= rope_axis(p, lane + 32 * i) << (2 * i);
+        return a;
     }
+};
+// Lane a's position of the token at the walk, on axis a.
+template <typename W> __device__ __forceinline__ int64_t rope_position(const RopeParams &p, const W &w, int lane) {
+    if (lane >= p.axes) return 0;
+    const int64_t q = w.b * p.pos_batch + w.s * p.pos_token + lane * p.pos_axis;
+    return p.pos64 ? (int64_t)__ldg(static_cast<const long long *>(p.pos) + q)
+                   : (int64_t)__ldg(static_cast<const int *>(p.pos) + q);
 }
 
 __device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x); }
@@ -176,15 +204,16 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2, DEPTH = kRopeFwdDepth;
     using Table = RopeTable<V, L>;
     using Raw = RopeRaw<XT, V>;
-    // rings, tables, then gamma (and beta) of the queries and of the keys
+    // rings, tables, frequencies, then gamma (and beta) of the queries and of the keys
     extern __shared__ __align__(16) unsigned char rope_smem[];
     const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
     Raw(*ring)[U][2][32] = reinterpret_cast<Raw(*)[U][2][32]>(rope_smem) + warp * DEPTH;
     Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * U * DEPTH * kRopeWarps);
-    float *par = reinterpret_cast<float *>(tables + kRopeWarps);
+    RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
+    float *par = reinterpret_cast<float *>(&turns + 1);
     Table &tab = tables[warp];
     RopeTokens w(p), ahead = w;  // the pass worked on, the pass to load
-    const RopeChunks<V, KIND> ch(p, sl);
+    const RopeChunks<V, L, KIND> ch(p, sl);
     const int nq = p.passes[0];
     const bool fill_a = ch.oka, fill_b = ch.okb;
     // head of this lane's in a pass; past the last one it repeats that, unstored
@@ -207,19 +236,19 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     };
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) load(i);
+    int64_t pos = w.left ? rope_position(p, w, lane) : 0;
+    const uint32_t axis = Table::axes(p, lane);
+    turns.fill(p);
+    tab.ones(lane);
     if constexpr (MODE != kRopeOnly) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             rope_param(par + r * p.D, p.gamma[r], p.D, p.pdt, 1.f);
             if constexpr (MODE == kRopeLn) rope_param(par + (2 + r) * p.D, p.beta[r], p.D, p.pdt, 0.f);
         }
-        __syncthreads();
     }
+    __syncthreads();
     if (!w.left) return;
-    RopeAngles<Table::PER> ang;
-    ang.init(p, lane);
-    uint64_t pos[Table::PER];
-    rope_fetch(p, ang, w, lane, pos);
     const float inv = 1.f / (float)p.D;
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
@@ -229,7 +258,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         char *y = static_cast<char *>(p.y[r].p) + w.at(p.y[r]) * ES;
         const int64_t stat = (w.b * p.S + w.s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0);
         const bool nf = w.next(p);
-        if (fresh) tab.put(ang, p, pos, lane);
+        if (fresh) tab.put(turns, p, pos, axis, lane);
         if (turn) {
             float2 ga[H], gb[H];
             if constexpr (MODE != kRopeOnly) {
@@ -243,23 +272,17 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 rope_get<V>(par + (2 + r) * p.D + ch.a, ba);
                 rope_get<V>(par + (2 + r) * p.D + ch.b, bb);
             }
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                ca[i] = ga[i];
-                cb[i] = gb[i];
-                sa[i] = sb[i] = f2s(0.f);
-            }
             if (inter) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    if (KIND != kRopeSome || ch.ra) {
+                    {
                         const float c = tab.c[ch.pa + i], s = tab.s[ch.pa + i];
                         ca[i] = make_float2(ga[i].x * c, ga[i].y * c);
                         sa[i] = make_float2(-ga[i].y * s, ga[i].x * s);
                         if constexpr (MODE == kRopeLn)
                             ba[i] = make_float2(ba[i].x * c - ba[i].y * s, ba[i].y * c + ba[i].x * s);
                     }
-                    if (KIND != kRopeSome || ch.rb) {
+                    {
                         const float c = tab.c[ch.pb + i], s = tab.s[ch.pb + i];
                         cb[i] = make_float2(gb[i].x * c, gb[i].y * c);
                         sb[i] = make_float2(-gb[i].y * s, gb[i].x * s);
@@ -267,7 +290,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                             bb[i] = make_float2(bb[i].x * c - bb[i].y * s, bb[i].y * c + bb[i].x * s);
                     }
                 }
-            } else if (KIND != kRopeSome || ch.ra) {
+            } else {
                 float2 c[H], s[H];
                 rope_get<V>(tab.c + ch.pa, c);
                 rope_get<V>(tab.s + ch.pa, s);
@@ -284,8 +307,15 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     }
                 }
             }
+            if constexpr (KIND == kRopeSome) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    sa[i] = ch.ra ? sa[i] : f2s(0.f);
+                    sb[i] = ch.rb ? sb[i] : f2s(0.f);
+                }
+            }
         }
-        if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
+        if (w.left && nf) pos = rope_position(p, w, lane);
         rope_cp_wait<DEPTH - 1>();
         Raw ra[U], rb[U];
 #pragma unroll
@@ -364,15 +394,16 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
         Raw x[U][2][32], g[U][2][32];
         float mean[U][32], rstd[U][32];
     };
-    // rings, tables, gamma of the queries and of the keys; at the end the column sums [kRopeWarps][D] over the rings
+    // rings, tables, frequencies, gamma of the queries and of the keys; at the end the column sums [kRopeWarps][D] over the rings
     extern __shared__ __align__(16) unsigned char rope_smem[];
     const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
     Slot *ring = reinterpret_cast<Slot *>(rope_smem) + warp * DEPTH;
     Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps);
-    float *par = reinterpret_cast<float *>(tables + kRopeWarps), *rope_acc = reinterpret_cast<float *>(rope_smem);
+    RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
+    float *par = reinterpret_cast<float *>(&turns + 1), *rope_acc = reinterpret_cast<float *>(rope_smem);
     Table &tab = tables[warp];
     RopeWalk w(p), ahead = w;  // the pass worked on, the pass to load
-    const RopeChunks<V, KIND> ch(p, sl);
+    const RopeChunks<V, L, KIND> ch(p, sl);
     const int r = w.r, heads = p.heads[r];
     auto load = [&](int slot) {
         if (ahead.left) {
@@ -398,6 +429,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     };
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) load(i);
+    int64_t pos = w.left ? rope_position(p, w, lane) : 0;
+    const uint32_t axis = Table::axes(p, lane);
+    turns.fill(p);
+    tab.ones(lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) rope_param(par + i * p.D, p.gamma[i], p.D, p.pdt, 1.f);
     __syncthreads();
@@ -405,13 +440,6 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
 #pragma unroll
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
     if (w.left) {
-        RopeAngles<Table::PER> ang;
-        ang.init(p, lane);
-        uint64_t pos[Table::PER];
-        rope_fetch(p, ang, w, lane, pos);
-        float2 wa[H], wb[H], c[H], s[H];  // c, s: of the pairs of the chunks (neighbours: first a's, then b's)
-        rope_get<V>(par + r * p.D + ch.a, wa);
-        rope_get<V>(par + r * p.D + ch.b, wb);
         const float inv = 1.f / (float)p.D;
         const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
         bool fresh = true;
@@ -419,27 +447,21 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
             char *y = static_cast<char *>(p.y[r].p) + w.at(p.y[r]) * ES;
             const int h0 = w.blk * (G * U) + grp;
             const bool nf = w.next(p);
-            if (fresh) {
-                tab.put(ang, p, pos, lane);
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    c[i] = f2s(1.f);
-                    s[i] = f2s(0.f);
-                    const int at = inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
-                    if (KIND != kRopeSome || (inter ? (2 * i < H ? ch.ra : ch.rb) : ch.ra)) {
-                        c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
-                        s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
-                    }
-                }
-            }
-            if (w.left && nf) rope_fetch(p, ang, w, lane, pos);
+            if (fresh) tab.put(turns, p, pos, axis, lane);
+            if (w.left && nf) pos = rope_position(p, w, lane);
             rope_cp_wait<DEPTH - 1>();
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 // the gradient turned back (the sign of s is the transpose's)
                 float2 ta[H], tb[H];
                 {
-                    float2 ga[H], gb[H];
+                    float2 c[H], s[H], ga[H], gb[H];  // c, s: of the chunks' pairs (neighbours: first a's, then b's)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const int at = inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
+                        c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
+                        s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
+                    }
                     rope_unpack<XT, V>(ring[slot].g[u][0][lane], ga);
                     rope_unpack<XT, V>(ring[slot].g[u][1][lane], gb);
                     if (inter) {
@@ -475,6 +497,9 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 const float rstd = ring[slot].rstd[u][lane], mean = LN ? ring[slot].mean[u][lane] : 0.f;
                 if (u == U - 1) load(slot);
                 float2 dot = f2s(0.f), sum = f2s(0.f);
+                float2 wa[H], wb[H];
+                rope_get<V>(par + r * p.D + ch.a, wa);
+                rope_get<V>(par + r * p.D + ch.b, wb);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     if constexpr (LN) {

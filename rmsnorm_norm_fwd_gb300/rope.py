@@ -86,46 +86,64 @@ class _Call:
     __slots__ = ("dev", "q", "k", "B", "S", "D", "hq", "hk")
 
     def __init__(self, name, q, k):
+        self.q = shape = q.shape
+        n = len(shape)
         self.dev = q.get_device()
-        if not q.is_cuda or self.dev < 0 or q.dim() not in (3, 4):
+        if n == 3:
+            self.B = 1
+            self.S, self.hq, self.D = shape
+        elif n == 4:
+            self.B, self.S, self.hq, self.D = shape
+        if not q.is_cuda or self.dev < 0 or n not in (3, 4):
             raise ValueError(f"{name}q must be a CUDA tensor [tokens, heads, D] or [batches, tokens, heads, D]")
-        self.q = q.shape
-        *b, self.S, self.hq, self.D = q.shape
-        self.B = b[0] if b else 1
         self.k, self.hk = None, 0
         if k is not None:
-            self.k, self.hk = k.shape, k.shape[-2] if k.dim() >= 2 else 0
-            if k.shape != (*b, self.S, self.hk, self.D):
+            self.k = kshape = k.shape
+            if len(kshape) != n or kshape[-1] != self.D or kshape[:-2] != shape[:-2]:
                 raise ValueError(f"{name}k must have the batches, tokens and head size of {name}q")
+            self.hk = kshape[-2]
             if self.hk == 0:
                 raise ValueError("keys without heads are given as None")
 
-    def heads(self, name, q, k, dtype=None):
+    def heads(self, name, q, k, dtype):
         """Two gbnorm_heads_t."""
-        return _HEADS(*self._one(name + "q", q, self.q, dtype),
-                      *(self._one(name + "k", k, self.k, dtype or q.dtype) if self.k is not None else (0, 0, 0, 0)))
+        if self.k is None:
+            return _HEADS(*self._one(name + "q", q, self.q, dtype), 0, 0, 0, 0)
+        return _HEADS(*self._one(name + "q", q, self.q, dtype), *self._one(name + "k", k, self.k, dtype))
 
     def _one(self, name, t, shape, dtype):
         if t is None or t.shape != shape or t.get_device() != self.dev:
             raise ValueError(f"{name} must be a {list(shape)} CUDA tensor on device {self.dev}")
-        if dtype is not None and t.dtype != dtype:
+        if t.dtype != dtype:
             raise ValueError(f"{name} must have dtype {dtype}")
         st = t.stride()
-        if st[-1] != 1 and self.D > 1:
+        if len(st) == 3:
+            token, head, one = st
+            batch = 0
+        else:
+            batch, token, head, one = st
+        if one != 1 and self.D > 1:
             raise ValueError(f"{name} must have unit stride in its last dimension")
-        return t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2]
+        return t.data_ptr(), batch, token, head
 
-    def out(self, given, shape, dtype):
-        return given if given is not None or shape is None else torch.empty(shape, device=self.dev, dtype=dtype)
+    def out(self, yq, yk, dtype):
+        """The two outputs, allocated where they are not given."""
+        if yq is None:
+            yq = torch.empty(self.q, dtype=dtype, device=self.dev)
+        if yk is None and self.k is not None:
+            yk = torch.empty(self.k, dtype=dtype, device=self.dev)
+        return yq, yk
 
-    def pair(self, name, q, k, n, dtype):
-        """Two pointers to [n] parameters."""
+    def pair(self, name, q, k, dtype):
+        """Two pointers to [D] parameters."""
+        if q is None and k is None:
+            return None
         for w, t in (("q", q), ("k", k)):
-            if t is not None and (t.shape != (n,) or t.get_device() != self.dev or t.dtype != dtype
+            if t is not None and (t.shape != (self.D,) or t.get_device() != self.dev or t.dtype != dtype
                                   or not t.is_contiguous()):
-                raise ValueError(f"{name}_{w} must be a contiguous 1-D CUDA {dtype} tensor of {n} elements on device "
-                                 f"{self.dev}")
-        return _TWO(q.data_ptr() if q is not None else 0, k.data_ptr() if k is not None and self.hk else 0)
+                raise ValueError(f"{name}_{w} must be a contiguous 1-D CUDA {dtype} tensor of {self.D} elements on "
+                                 f"device {self.dev}")
+        return _TWO(0 if q is None else q.data_ptr(), 0 if k is None else k.data_ptr())
 
     def flat(self, name, t, shape):
         if t is None:
@@ -139,31 +157,35 @@ class _Call:
 
     def rope(self, positions, rotary, xdt, ydt, pdt):
         """gbnorm_rope_t."""
-        head = (self.B, self.S, self.hq, self.hk, self.D, _code(xdt), _code(ydt), _code(pdt))
+        try:
+            xdt, ydt, pdt = DTYPE_CODE[xdt], DTYPE_CODE[ydt], DTYPE_CODE[pdt]
+        except KeyError:
+            raise ValueError(f"tensors must be float32, float16 or bfloat16, not {xdt}, {ydt}, {pdt}") from None
         if rotary is None:
             if positions is not None:
                 raise ValueError("positions without a rotation")
-            return _ROPE(*head, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0)
+            return _ROPE(self.B, self.S, self.hq, self.hk, self.D, xdt, ydt, pdt, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0)
         if rotary.rot > self.D:
             raise ValueError(f"{rotary.rot} rotated elements in heads of {self.D}")
-        if positions is None or not positions.is_cuda or positions.get_device() != self.dev or rotary.dev != self.dev:
+        if positions is None or positions.get_device() != self.dev or rotary.dev != self.dev:
             raise ValueError(f"positions and frequencies must be on device {self.dev}")
         code = _POS_CODE.get(positions.dtype)
         if code is None:
             raise ValueError("positions must be int32 or int64")
-        shape, st, axis = tuple(positions.shape), positions.stride(), 0
+        shape, st, axis = positions.shape, positions.stride(), 0
         if rotary.axes > 1:
             if not shape or shape[0] != rotary.axes:
                 raise ValueError(f"positions must have {rotary.axes} axes first")
             shape, axis, st = shape[1:], st[0], st[1:]
-        if shape == (self.S,):
+        if len(shape) == 1 and shape[0] == self.S:
             batch, token = 0, st[0]
-        elif len(self.q) == 4 and shape == (self.B, self.S):
+        elif len(self.q) == 4 and len(shape) == 2 and shape[0] == self.B and shape[1] == self.S:
             batch, token = st
         else:
             raise ValueError(f"positions must have one value for each of the tokens {list(self.q[:-2])}")
-        return _ROPE(*head, rotary.interleaved, rotary.rot, rotary.axes, code, 0, positions.data_ptr(), axis, batch,
-                     token, rotary.inv_freq.data_ptr(), rotary._axis_at)
+        return _ROPE(self.B, self.S, self.hq, self.hk, self.D, xdt, ydt, pdt, rotary.interleaved, rotary.rot,
+                     rotary.axes, code, 0, positions.data_ptr(), axis, batch, token, rotary.inv_freq.data_ptr(),
+                     rotary._axis_at)
 
     def on_device(self, fn, *args):
         """fn(*args) with the tensors' device current."""
@@ -174,18 +196,16 @@ class _Call:
 
     def go(self, name, fn, *args):
         """fn(*args, stream) with the tensors' device current, on its current stream."""
-        _check(name, self.on_device(fn, *args, _raw_stream(self.dev)))
-
-
-def _code(dtype):
-    code = DTYPE_CODE.get(dtype)
-    if code is None:
-        raise ValueError(f"tensors must be float32, float16 or bfloat16, not {dtype}")
-    return code
+        status = self.on_device(fn, *args, _raw_stream(self.dev))
+        if status:
+            _check(name, status)
 
 
 def _param_dtype(default, *params):
-    return next((t.dtype for t in params if t is not None), default)
+    for t in params:
+        if t is not None:
+            return t.dtype
+    return default
 
 
 @_on_stream
@@ -201,19 +221,20 @@ def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, pos
     and yk k itself."""
     c = _Call("", q, k)
     dt = yq.dtype if yq is not None else y_dtype or q.dtype
-    yq, yk = c.out(yq, c.q, dt), c.out(yk, c.k, dt)
+    yq, yk = c.out(yq, yk, dt)
+    stats = c.stats_shape()
     if save_stats:
         if rstd is None:
-            rstd = torch.empty(c.stats_shape(), device=c.dev, dtype=torch.float32)
+            rstd = torch.empty(stats, dtype=torch.float32, device=c.dev)
         if is_layernorm and mean is None:
-            mean = torch.empty(c.stats_shape(), device=c.dev, dtype=torch.float32)
+            mean = torch.empty(stats, dtype=torch.float32, device=c.dev)
     if not is_layernorm:
         mean = beta_q = beta_k = None
     pdt = _param_dtype(q.dtype, gamma_q, gamma_k, beta_q, beta_k)
     c.go("qk_norm_rope_fwd", lib.qk_norm_rope_fwd, int(bool(is_layernorm)), eps,
-         c.rope(positions, rotary, q.dtype, dt, pdt), c.heads("", q, k), c.heads("y", yq, yk),
-         c.pair("gamma", gamma_q, gamma_k, c.D, pdt), c.pair("beta", beta_q, beta_k, c.D, pdt),
-         c.flat("mean", mean, c.stats_shape()), c.flat("rstd", rstd, c.stats_shape()))
+         c.rope(positions, rotary, q.dtype, dt, pdt), c.heads("", q, k, q.dtype), c.heads("y", yq, yk, dt),
+         c.pair("gamma", gamma_q, gamma_k, pdt), c.pair("beta", beta_q, beta_k, pdt), c.flat("mean", mean, stats),
+         c.flat("rstd", rstd, stats))
     return yq, yk, mean, rstd
 
 
@@ -230,29 +251,30 @@ def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean,
     and dbeta float32 [2, D] (queries, keys; [1, D] without keys), None where not
     needed, dbeta LayerNorm only.  dq may be dyq itself and dk dyk itself."""
     c = _Call("", q, k)
-    dq, dk = c.out(dq, c.q, q.dtype), c.out(dk, c.k, q.dtype)
-    sums = (2 if c.hk else 1, c.D)
+    dt = q.dtype
+    dq, dk = c.out(dq, dk, dt)
+    sums, stats = (2 if c.hk else 1, c.D), c.stats_shape()
     if dgamma is None and need_dgamma:
-        dgamma = torch.empty(sums, device=c.dev, dtype=torch.float32)
+        dgamma = torch.empty(sums, dtype=torch.float32, device=c.dev)
     if not is_layernorm:
         dbeta = mean = None
     elif dbeta is None and need_dbeta:
-        dbeta = torch.empty(sums, device=c.dev, dtype=torch.float32)
+        dbeta = torch.empty(sums, dtype=torch.float32, device=c.dev)
     if rstd is None or (is_layernorm and mean is None):
         raise ValueError("rstd (and mean for LayerNorm) of the forward are needed")
     if workspace is None:
         need = c.on_device(lib.qk_norm_rope_bwd_workspace_size, int(bool(is_layernorm)), c.B * c.S, c.hq, c.hk, c.D)
         if need == 0:
             raise GbnormError("qk_norm_rope_bwd_workspace_size", 2)
-        workspace = torch.empty(need, device=c.dev, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=c.dev)
     elif not workspace.is_contiguous() or workspace.get_device() != c.dev:
         raise ValueError(f"workspace must be contiguous on device {c.dev}")
-    pdt = _param_dtype(q.dtype, gamma_q, gamma_k)
+    pdt = _param_dtype(dt, gamma_q, gamma_k)
     c.go("qk_norm_rope_bwd", lib.qk_norm_rope_bwd, int(bool(is_layernorm)),
-         c.rope(positions, rotary, q.dtype, dyq.dtype, pdt), c.heads("dy", dyq, dyk), c.heads("", q, k),
-         c.heads("d", dq, dk, q.dtype), c.pair("gamma", gamma_q, gamma_k, c.D, pdt),
-         c.flat("mean", mean, c.stats_shape()), c.flat("rstd", rstd, c.stats_shape()), c.flat("dgamma", dgamma, sums),
-         c.flat("dbeta", dbeta, sums), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+         c.rope(positions, rotary, dt, dyq.dtype, pdt), c.heads("dy", dyq, dyk, dyq.dtype), c.heads("", q, k, dt),
+         c.heads("d", dq, dk, dt), c.pair("gamma", gamma_q, gamma_k, pdt), c.flat("mean", mean, stats),
+         c.flat("rstd", rstd, stats), c.flat("dgamma", dgamma, sums), c.flat("dbeta", dbeta, sums),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dgamma, dbeta
 
 
@@ -263,11 +285,11 @@ def rope_fwd(q, k, positions, rotary: Rotary, y_dtype=None, yq=None, yk=None):
     and yk k itself."""
     c = _Call("", q, k)
     dt = yq.dtype if yq is not None else y_dtype or q.dtype
-    yq, yk = c.out(yq, c.q, dt), c.out(yk, c.k, dt)
     if rotary is None:
         raise ValueError("rotary is needed")
-    c.go("rope_fwd", lib.rope_fwd, c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k),
-         c.heads("y", yq, yk))
+    yq, yk = c.out(yq, yk, dt)
+    c.go("rope_fwd", lib.rope_fwd, c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k, q.dtype),
+         c.heads("y", yq, yk, dt))
     return yq, yk
 
 
@@ -277,11 +299,11 @@ def rope_bwd(dyq, dyk, positions, rotary: Rotary, dx_dtype=None, dq=None, dk=Non
     dx_dtype (default dyq's); dq may be dyq itself and dk dyk itself."""
     c = _Call("dy", dyq, dyk)
     dt = dq.dtype if dq is not None else dx_dtype or dyq.dtype
-    dq, dk = c.out(dq, c.q, dt), c.out(dk, c.k, dt)
     if rotary is None:
         raise ValueError("rotary is needed")
-    c.go("rope_bwd", lib.rope_bwd, c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype), c.heads("dy", dyq, dyk),
-         c.heads("d", dq, dk))
+    dq, dk = c.out(dq, dk, dt)
+    c.go("rope_bwd", lib.rope_bwd, c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype),
+         c.heads("dy", dyq, dyk, dyq.dtype), c.heads("d", dq, dk, dt))
     return dq, dk
 
 
