@@ -81,6 +81,11 @@ template <int N> struct RopeAngles {
     }
 };
 
+// a / n of numbers that mostly fit 32 bits (a division in 64 is some hundred instructions).
+__device__ __forceinline__ int64_t rope_div(int64_t a, int64_t n) {
+    return ((a | n) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)n) : a / n;
+}
+
 // A warp's share of the passes over one of the two tensors: contiguous, so
 // that the angles of a token serve all its heads.
 struct RopeWalk {
@@ -95,11 +100,11 @@ struct RopeWalk {
         const int64_t W = p.warps[r], U = p.units[r];
         left = b = s = blk = 0;
         if (w >= W) return;
-        const int64_t each = U / W, more = U % W, u = each * w + (w < more ? w : more);
+        const int64_t each = rope_div(U, W), more = U - each * W, u = each * w + (w < more ? w : more);
         left = (int)(each + (w < more ? 1 : 0));
-        const int64_t t = u / p.passes[r];
+        const int64_t t = rope_div(u, p.passes[r]);
         blk = (int)(u - t * p.passes[r]);
-        b = (int)(t / p.S);
+        b = (int)rope_div(t, p.S);
         s = (int)(t - b * p.S);
     }
     // To the next pass; true if it belongs to another token.
@@ -120,36 +125,97 @@ struct RopeWalk {
     }
 };
 
-// The forward's share: contiguous passes over the tokens, each with its
-// queries' heads and then its keys', so that both take the token's angles.
-struct RopeTokens {
-    int left;  // passes to go, this one included
-    int b, s;  // token
-    int blk;   // pass within the token
-    __device__ __forceinline__ RopeTokens(const RopeParams &p) {
-        const int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), W = p.warps[0], U = p.units[0];
-        left = b = s = blk = 0;
+// The same for kernels on vectors, whose passes take GU heads, lane group `grp`
+// one of them (and every 32 / L-th).  BOTH: over the tokens, each with its
+// queries' heads and then its keys', so that both take the token's angles (units
+// and warps of index 0 count both); else over one tensor.  Passes over one
+// tensor of a token are a segment: within one a step is an addition.
+//
+// A warp takes every W-th token as long as all W warps have one, so that the
+// grid moves through memory as a front, and then its share of the passes over
+// the tokens that are left.
+template <int GU, bool BOTH> struct RopeCursor {
+    int left;    // passes to go, this one included
+    int cnt;     // of the segment
+    int hl;      // heads of the segment from this lane's on
+    int b, s;    // token
+    int r;       // 0 queries, 1 keys
+    int rounds;  // whole tokens to go
+    __device__ __forceinline__ RopeCursor(const RopeParams &p, int grp) {
+        int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+        r = !BOTH && w >= p.warps[0];
+        if (r) w -= p.warps[0];
+        const int64_t W = p.warps[r];
+        left = cnt = hl = b = s = rounds = 0;
         if (w >= W) return;
-        const int64_t each = U / W, more = U % W, u = each * w + (w < more ? w : more);
-        const int np = p.passes[0] + p.passes[1];
-        left = (int)(each + (w < more ? 1 : 0));
-        const int64_t t = u / np;
-        blk = (int)(u - t * np);
-        b = (int)(t / p.S);
+        const int np = passes(p);
+        int64_t first, count;
+        rest(p, w, W, np, &first, &count);
+        rounds = p.rounds[r];
+        left = rounds * np + (int)count;
+        if (rounds > 0) start(p, grp, w * np, np);
+        else start(p, grp, first, np);
+    }
+    __device__ __forceinline__ int passes(const RopeParams &p) const {
+        return BOTH ? p.passes[0] + p.passes[1] : p.passes[r];
+    }
+    // The share of warp w in the passes over the tokens behind the whole rounds.
+    __device__ __forceinline__ void rest(const RopeParams &p, int64_t w, int64_t W, int np, int64_t *first,
+                                         int64_t *count) const {
+        const int64_t done = p.rounds[r] * W * np, U = p.units[r] - done, each = rope_div(U, W), more = U - each * W;
+        *first = done + each * w + (w < more ? w : more);
+        *count = each + (w < more ? 1 : 0);
+    }
+    __device__ __forceinline__ void start(const RopeParams &p, int grp, int64_t u, int np) {
+        const int64_t t = rope_div(u, np);
+        int blk = (int)(u - t * np);
+        if (BOTH) {
+            r = blk >= p.passes[0];
+            if (r) blk -= p.passes[0];
+        }
+        cnt = p.passes[r] - blk;
+        hl = p.heads[r] - blk * GU - grp;
+        b = (int)rope_div(t, p.S);
         s = (int)(t - b * p.S);
     }
-    // To the next pass; true if it belongs to another token.
-    __device__ __forceinline__ bool next(const RopeParams &p) {
+    // To the next pass: 0 of the same segment, 1 of the keys of the token, 2 of another token.
+    __device__ __forceinline__ int next(const RopeParams &p, int grp) {
         --left;
-        if (++blk < p.passes[0] + p.passes[1]) return false;
-        blk = 0;
-        if (++s == (int)p.S) {
-            s = 0;
+        if (--cnt) {
+            hl -= GU;
+            return 0;
+        }
+        const bool keys = BOTH && r == 0 && p.passes[1] > 0;
+        if (BOTH) r = keys;
+        cnt = p.passes[r];
+        hl = p.heads[r] - grp;
+        if (keys) return 1;
+        --rounds;
+        const bool far = rounds > 0;
+        b += far ? p.step_b[r] : 0;
+        s += far ? p.step_s[r] : 1;
+        if (s >= (int)p.S) {
+            s -= (int)p.S;
             ++b;
         }
-        return true;
+        if (rounds == 0) {
+            int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), first, count;
+            if (r) w -= p.warps[0];
+            const int np = passes(p);
+            rest(p, w, p.warps[r], np, &first, &count);
+            start(p, grp, first, np);
+        }
+        return 2;
     }
-    __device__ __forceinline__ int64_t at(const RopeHeads &h) const { return b * h.batch + s * h.token; }
+    // This lane's head of the pass, the last one if it has none.
+    __device__ __forceinline__ int head(const RopeParams &p) const { return p.heads[r] - (hl > 0 ? hl : 1); }
+    // Byte address of that head in t.
+    __device__ __forceinline__ char *at(const RopeParams &p, const RopeHeads &t, int es) const {
+        return static_cast<char *>(t.p) + (b * t.batch + s * t.token + head(p) * t.head) * es;
+    }
+    __device__ __forceinline__ int64_t stat(const RopeParams &p) const {
+        return (b * p.S + s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0) + head(p);
+    }
 };
 
 // The backward's column sums of a CTA: acc[warp][D] in shared memory, each

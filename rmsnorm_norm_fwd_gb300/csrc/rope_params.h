@@ -36,6 +36,8 @@ struct RopeParams {
     int64_t units[2];      // passes over all tokens (a pass: the heads one warp works on at once)
     int64_t warps[2];      // warps of the grid that take them
     int passes[2];         // of a token
+    int rounds[2];         // whole tokens a warp (vectors)
+    int step_b[2], step_s[2];  // warps[i] tokens on, in batches and tokens
     int heads[2];
     int D, rot;
     int inter;             // pairs (2j, 2j + 1), else (j, j + rot / 2)
@@ -56,7 +58,7 @@ extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 // pass: passes in flight a warp, and dynamic shared memory without the
 // parameters (rings, tables of cosines and sines, frequencies; the backward's column sums
 // take the place of the rings).
-constexpr int kRopeFwdDepth = 3, kRopeBwdDepth = 3;
+constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
 constexpr int rope_fwd_smem(int v, int es, int l, int u) {
     return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * (l + 1)) + 12 * v * l;
 }

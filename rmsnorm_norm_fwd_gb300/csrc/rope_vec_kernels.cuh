@@ -88,15 +88,21 @@ __device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, flo
 __device__ __forceinline__ void rope_cp_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void rope_cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Row `row` of D parameters widened to fp32 into shared memory, a null row as `none`; every thread takes its share.
-__device__ __forceinline__ void rope_param(float *to, const void *row, int D, int dt, float none) {
-    for (int c = threadIdx.x; c < D; c += kRopeCTA) to[c] = row ? ld1(row, c, dt) : none;
+// Values that a lane reads V at a time lie in shared memory as planes of four
+// (element 8 c + 4 h + i at h n / 2 + 4 c + i of n), so that the lanes' 16-byte
+// reads are side by side; with V = 4 they are so as they are.
+template <int V> __device__ __forceinline__ int rope_place(int e, int n) {
+    return V == 8 ? ((e >> 2) & 1) * (n / 2) + (e >> 3) * 4 + (e & 3) : e;
 }
-// V values from shared memory.
-template <int V> __device__ __forceinline__ void rope_get(const float *from, float2 (&f)[V / 2]) {
+// Row `row` of D parameters widened to fp32 into shared memory, a null row as `none`; every thread takes its share.
+template <int V> __device__ __forceinline__ void rope_param(float *to, const void *row, int D, int dt, float none) {
+    for (int c = threadIdx.x; c < D; c += kRopeCTA) to[rope_place<V>(c, D)] = row ? ld1(row, c, dt) : none;
+}
+// The V values from e (a multiple of V) on, of n.
+template <int V> __device__ __forceinline__ void rope_get(const float *from, int e, int n, float2 (&f)[V / 2]) {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
-        const float4 v = reinterpret_cast<const float4 *>(from)[i];
+        const float4 v = *reinterpret_cast<const float4 *>(from + e / (V / 4) + i * (n / 2));
         f[2 * i] = make_float2(v.x, v.y);
         f[2 * i + 1] = make_float2(v.z, v.w);
     }
@@ -155,18 +161,20 @@ template <int V, int L> struct RopeTurns {
     }
 };
 // A warp's cosines and sines: written by the lane that computed the pair, read by those whose chunks hold it.
+// As halves, a chunk's V pairs are read at once, and lie as rope_place says.
 template <int V, int L> struct RopeTable {
-    static constexpr int N = V * L, PER = N / 32 > 0 ? N / 32 : 1;
-    float c[N + V], s[N + V];  // the last V: what is not rotated
-    __device__ __forceinline__ void ones(int lane) {
+    static constexpr int N = V * L, M = N + V, PER = N / 32 > 0 ? N / 32 : 1;
+    float c[M], s[M];  // pairs from N on: what is not rotated
+    __device__ __forceinline__ void ones(int lane, bool inter) {
         if (lane < V) {
-            c[N + lane] = 1.f;
-            s[N + lane] = 0.f;
+            const int at = inter ? N + lane : rope_place<V>(N + lane, M);
+            c[at] = 1.f;
+            s[at] = 0.f;
         }
     }
     // pos: lane a holds the position on axis a; axis: two bits for each of the lane's pairs lane, lane + 32, ...
     __device__ __forceinline__ void put(const RopeTurns<V, L> &turns, const RopeParams &p, int64_t pos, uint32_t axis,
-                                        int lane) {
+                                        int lane, bool inter) {
         __syncwarp();  // the last token's have been read
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -175,8 +183,9 @@ template <int V, int L> struct RopeTable {
             if (2 * j < p.rot) {
                 float cs, sn;
                 rope_sincos((uint64_t)at * turns.f[j], p.sign, &cs, &sn);
-                c[j] = cs + turns.bad[j];
-                s[j] = sn + turns.bad[j];
+                const int to = inter ? j : rope_place<V>(j, M);
+                c[to] = cs + turns.bad[j];
+                s[to] = sn + turns.bad[j];
             }
         }
         __syncwarp();
@@ -212,25 +221,27 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1);
     Table &tab = tables[warp];
-    RopeTokens w(p), ahead = w;  // the pass worked on, the pass to load
+    RopeCursor<G * U, true> w(p, grp), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, L, KIND> ch(p, sl);
-    const int nq = p.passes[0];
-    const bool fill_a = ch.oka, fill_b = ch.okb;
-    // head of this lane's in a pass; past the last one it repeats that, unstored
-    auto head = [&](int blk, int r, int u) { return (blk - (r ? nq : 0)) * (G * U) + u * G + grp; };
+    const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
+    const int fa = ch.a * ES, fb = ch.b * ES;
+    const char *x = ahead.at(p, p.x[ahead.r], ES);
+    int64_t xs = p.x[ahead.r].head * (G * ES);
     auto load = [&](int slot) {
         if (ahead.left) {
-            const int r = ahead.blk >= nq, last = p.heads[r] - 1;
-            const char *x = static_cast<const char *>(p.x[r].p) + ahead.at(p.x[r]) * ES;
-            const int64_t step = p.x[r].head * ES;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = head(ahead.blk, r, u);
-                const char *q = x + (h < last ? h : last) * step;
-                rope_cp(&ring[slot][u][0][lane], q + ch.a * ES, fill_a, Raw{}.v);
-                rope_cp(&ring[slot][u][1][lane], q + ch.b * ES, fill_b, Raw{}.v);
+                // a lane without a head in the pass reads another, and stores nothing
+                const char *q = u == 0 ? x : x + (ahead.hl > u * G ? u * xs : 0);
+                rope_cp(&ring[slot][u][0][lane], q + fa, ch.oka, Raw{}.v);
+                rope_cp(&ring[slot][u][1][lane], q + fb, ch.okb, Raw{}.v);
             }
-            ahead.next(p);
+            if (ahead.next(p, grp)) {
+                x = ahead.at(p, p.x[ahead.r], ES);
+                xs = p.x[ahead.r].head * (G * ES);
+            } else if (ahead.hl > 0) {
+                x += U * xs;
+            }
         }
         rope_cp_end();
     };
@@ -239,38 +250,36 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
     const uint32_t axis = Table::axes(p, lane);
     turns.fill(p);
-    tab.ones(lane);
+    tab.ones(lane, inter);
     if constexpr (MODE != kRopeOnly) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            rope_param(par + r * p.D, p.gamma[r], p.D, p.pdt, 1.f);
-            if constexpr (MODE == kRopeLn) rope_param(par + (2 + r) * p.D, p.beta[r], p.D, p.pdt, 0.f);
+            rope_param<V>(par + r * p.D, p.gamma[r], p.D, p.pdt, 1.f);
+            if constexpr (MODE == kRopeLn) rope_param<V>(par + (2 + r) * p.D, p.beta[r], p.D, p.pdt, 0.f);
         }
     }
     __syncthreads();
     if (!w.left) return;
     const float inv = 1.f / (float)p.D;
-    const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
+    char *y = w.at(p, p.y[w.r], ES);
+    int64_t ys = p.y[w.r].head * (G * ES), stat = w.stat(p);
     float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
-    bool fresh = true, turn = true;  // another token's angles, another tensor's coefficients
+    int turn = 2;  // 2: another token's angles, 1: another tensor's coefficients
     for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
-        const int r = w.blk >= nq, h0 = head(w.blk, r, 0), heads = p.heads[r];
-        char *y = static_cast<char *>(p.y[r].p) + w.at(p.y[r]) * ES;
-        const int64_t stat = (w.b * p.S + w.s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0);
-        const bool nf = w.next(p);
-        if (fresh) tab.put(turns, p, pos, axis, lane);
+        const int r = w.r, hl = w.hl;
+        if (turn == 2) tab.put(turns, p, pos, axis, lane, inter);
         if (turn) {
             float2 ga[H], gb[H];
             if constexpr (MODE != kRopeOnly) {
-                rope_get<V>(par + r * p.D + ch.a, ga);
-                rope_get<V>(par + r * p.D + ch.b, gb);
+                rope_get<V>(par + r * p.D, ch.a, p.D, ga);
+                rope_get<V>(par + r * p.D, ch.b, p.D, gb);
             } else {
 #pragma unroll
                 for (int i = 0; i < H; ++i) ga[i] = gb[i] = f2s(1.f);
             }
             if constexpr (MODE == kRopeLn) {
-                rope_get<V>(par + (2 + r) * p.D + ch.a, ba);
-                rope_get<V>(par + (2 + r) * p.D + ch.b, bb);
+                rope_get<V>(par + (2 + r) * p.D, ch.a, p.D, ba);
+                rope_get<V>(par + (2 + r) * p.D, ch.b, p.D, bb);
             }
             if (inter) {
 #pragma unroll
@@ -292,8 +301,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 }
             } else {
                 float2 c[H], s[H];
-                rope_get<V>(tab.c + ch.pa, c);
-                rope_get<V>(tab.s + ch.pa, s);
+                rope_get<V>(tab.c, ch.pa, Table::M, c);
+                rope_get<V>(tab.s, ch.pa, Table::M, s);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     ca[i] = f2mul(ga[i], c[i]);
@@ -315,7 +324,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 }
             }
         }
-        if (w.left && nf) pos = rope_position(p, w, lane);
+        turn = w.next(p, grp);
+        if (w.left && turn == 2) pos = rope_position(p, w, lane);
         rope_cp_wait<DEPTH - 1>();
         Raw ra[U], rb[U];
 #pragma unroll
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         load(slot);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * G;
+            const bool in = hl > u * G;
             float2 va[H], vb[H];
             rope_unpack<XT, V>(ra[u], va);
             rope_unpack<XT, V>(rb[u], vb);
@@ -341,18 +351,23 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     mean = sum[0] * inv;
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
-                        va[i] = ch.oka ? f2add(va[i], f2s(-mean)) : f2s(0.f);
-                        vb[i] = ch.okb ? f2add(vb[i], f2s(-mean)) : f2s(0.f);
+                        va[i] = f2add(va[i], f2s(-mean));
+                        vb[i] = f2add(vb[i], f2s(-mean));
                     }
                 }
-                float2 t = f2s(0.f);
+                float2 ta = f2s(0.f), tb = f2s(0.f);
 #pragma unroll
-                for (int i = 0; i < H; ++i) t = f2fma(va[i], va[i], f2fma(vb[i], vb[i], t));
-                float sq[1] = {t.x + t.y};
+                for (int i = 0; i < H; ++i) {
+                    ta = f2fma(va[i], va[i], ta);
+                    tb = f2fma(vb[i], vb[i], tb);
+                }
+                // a chunk that is not there holds zeros, with the mean off it no longer
+                const bool ka = MODE != kRopeLn || ch.oka, kb = MODE != kRopeLn || ch.okb;
+                float sq[1] = {(ka ? ta.x + ta.y : 0.f) + (kb ? tb.x + tb.y : 0.f)};
                 group_sum<L, 1>(sq);
                 const float rstd = rsqrtf(sq[0] * inv + p.eps);
-                if (p.rstd && sl == 0 && h < heads) p.rstd[stat + h] = rstd;
-                if (MODE == kRopeLn && p.mean && sl == 0 && h < heads) p.mean[stat + h] = mean;
+                if (p.rstd && sl == 0 && in) p.rstd[stat + u * G] = rstd;
+                if (MODE == kRopeLn && p.mean && sl == 0 && in) p.mean[stat + u * G] = mean;
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     va[i] = f2mul(va[i], f2s(rstd));
@@ -367,20 +382,22 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     ta = ch.ra ? ta : f2s(0.f);
                     tb = ch.rb ? tb : f2s(0.f);
                 }
-                ua[i] = f2fma(va[i], ca[i], f2mul(ta, sa[i]));
-                ub[i] = f2fma(vb[i], cb[i], f2mul(tb, sb[i]));
-                if constexpr (MODE == kRopeLn) {
-                    ua[i] = f2add(ua[i], ba[i]);
-                    ub[i] = f2add(ub[i], bb[i]);
-                }
+                ua[i] = f2fma(va[i], ca[i], MODE == kRopeLn ? f2fma(ta, sa[i], ba[i]) : f2mul(ta, sa[i]));
+                ub[i] = f2fma(vb[i], cb[i], MODE == kRopeLn ? f2fma(tb, sb[i], bb[i]) : f2mul(tb, sb[i]));
             }
-            char *q = y + h * (p.y[r].head * ES);
-            if (h < heads && ch.oka) rope_st(q + ch.a * ES, rope_pack<XT, V>(ua).v);
-            if (h < heads && ch.okb) rope_st(q + ch.b * ES, rope_pack<XT, V>(ub).v);
+            char *q = u == 0 ? y : y + u * ys;
+            if (in && ch.oka) rope_st(q + fa, rope_pack<XT, V>(ua).v);
+            if (in && ch.okb) rope_st(q + fb, rope_pack<XT, V>(ub).v);
         }
         if (!w.left) return;
-        fresh = nf;
-        turn = nf || w.blk == nq;
+        if (turn) {
+            y = w.at(p, p.y[w.r], ES);
+            ys = p.y[w.r].head * (G * ES);
+            stat = w.stat(p);
+        } else {
+            y += U * ys;
+            stat += U * G;
+        }
     }
 }
 
@@ -402,28 +419,37 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1), *rope_acc = reinterpret_cast<float *>(rope_smem);
     Table &tab = tables[warp];
-    RopeWalk w(p), ahead = w;  // the pass worked on, the pass to load
+    RopeCursor<G * U, false> w(p, grp), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, L, KIND> ch(p, sl);
-    const int r = w.r, heads = p.heads[r];
+    const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
+    const int r = w.r, fa = ch.a * ES, fb = ch.b * ES;
+    const char *x = ahead.at(p, p.x[r], ES), *g = ahead.at(p, p.g[r], ES);
+    const int64_t xs = p.x[r].head * (G * ES), gs = p.g[r].head * (G * ES);
+    int64_t stat = ahead.stat(p);
     auto load = [&](int slot) {
         if (ahead.left) {
-            const char *x = static_cast<const char *>(p.x[r].p) + ahead.at(p.x[r]) * ES,
-                       *g = static_cast<const char *>(p.g[r].p) + ahead.at(p.g[r]) * ES;
-            const int64_t stat = ahead.stat(p), xs = p.x[r].head * ES, gs = p.g[r].head * ES;
             Slot &to = ring[slot];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                // past the last head a lane repeats that with a gradient of zeros, unstored
-                const int h0 = ahead.blk * (G * U) + u * G + grp, h = h0 < heads ? h0 : heads - 1;
-                const bool in = h0 < heads;
-                rope_cp(&to.x[u][0][lane], x + h * xs + ch.a * ES, ch.oka, Raw{}.v);
-                rope_cp(&to.x[u][1][lane], x + h * xs + ch.b * ES, ch.okb, Raw{}.v);
-                rope_cp(&to.g[u][0][lane], g + h * gs + ch.a * ES, in && ch.oka, Raw{}.v);
-                rope_cp(&to.g[u][1][lane], g + h * gs + ch.b * ES, in && ch.okb, Raw{}.v);
-                rope_cp(&to.rstd[u][lane], p.rstd + stat + h, true, 0.f);
-                if constexpr (LN) rope_cp(&to.mean[u][lane], p.mean + stat + h, true, 0.f);
+                // a lane without a head in the pass reads another with a gradient of zeros, and stores nothing
+                const bool in = ahead.hl > u * G;
+                const char *q = u == 0 ? x : x + (in ? u * xs : 0), *d = u == 0 ? g : g + (in ? u * gs : 0);
+                rope_cp(&to.x[u][0][lane], q + fa, ch.oka, Raw{}.v);
+                rope_cp(&to.x[u][1][lane], q + fb, ch.okb, Raw{}.v);
+                rope_cp(&to.g[u][0][lane], d + fa, in && ch.oka, Raw{}.v);
+                rope_cp(&to.g[u][1][lane], d + fb, in && ch.okb, Raw{}.v);
+                rope_cp(&to.rstd[u][lane], p.rstd + stat + (in ? u * G : 0), true, 0.f);
+                if constexpr (LN) rope_cp(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true, 0.f);
             }
-            ahead.next(p);
+            if (ahead.next(p, grp)) {
+                x = ahead.at(p, p.x[r], ES);
+                g = ahead.at(p, p.g[r], ES);
+                stat = ahead.stat(p);
+            } else if (ahead.hl > 0) {
+                x += U * xs;
+                g += U * gs;
+                stat += U * G;
+            }
         }
         rope_cp_end();
     };
@@ -432,23 +458,23 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
     const uint32_t axis = Table::axes(p, lane);
     turns.fill(p);
-    tab.ones(lane);
+    tab.ones(lane, inter);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) rope_param(par + i * p.D, p.gamma[i], p.D, p.pdt, 1.f);
+    for (int i = 0; i < 2; ++i) rope_param<V>(par + i * p.D, p.gamma[i], p.D, p.pdt, 1.f);
     __syncthreads();
     float2 da[H], db[H], ea[H], eb[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
     if (w.left) {
         const float inv = 1.f / (float)p.D;
-        const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
-        bool fresh = true;
+        char *y = w.at(p, p.y[r], ES);
+        const int64_t ys = p.y[r].head * (G * ES);
+        int turn = 2;
         for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
-            char *y = static_cast<char *>(p.y[r].p) + w.at(p.y[r]) * ES;
-            const int h0 = w.blk * (G * U) + grp;
-            const bool nf = w.next(p);
-            if (fresh) tab.put(turns, p, pos, axis, lane);
-            if (w.left && nf) pos = rope_position(p, w, lane);
+            const int hl = w.hl;
+            if (turn) tab.put(turns, p, pos, axis, lane, inter);
+            turn = w.next(p, grp);
+            if (w.left && turn) pos = rope_position(p, w, lane);
             rope_cp_wait<DEPTH - 1>();
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -456,11 +482,16 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 float2 ta[H], tb[H];
                 {
                     float2 c[H], s[H], ga[H], gb[H];  // c, s: of the chunks' pairs (neighbours: first a's, then b's)
+                    if (inter) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const int at = inter ? (2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H) : ch.pa + 2 * i;
-                        c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
-                        s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
+                        for (int i = 0; i < H; ++i) {
+                            const int at = 2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H;
+                            c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
+                            s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
+                        }
+                    } else {
+                        rope_get<V>(tab.c, ch.pa, Table::M, c);
+                        rope_get<V>(tab.s, ch.pa, Table::M, s);
                     }
                     rope_unpack<XT, V>(ring[slot].g[u][0][lane], ga);
                     rope_unpack<XT, V>(ring[slot].g[u][1][lane], gb);
@@ -498,8 +529,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 if (u == U - 1) load(slot);
                 float2 dot = f2s(0.f), sum = f2s(0.f);
                 float2 wa[H], wb[H];
-                rope_get<V>(par + r * p.D + ch.a, wa);
-                rope_get<V>(par + r * p.D + ch.b, wb);
+                rope_get<V>(par + r * p.D, ch.a, p.D, wa);
+                rope_get<V>(par + r * p.D, ch.b, p.D, wb);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     if constexpr (LN) {
@@ -521,23 +552,21 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 v[0] = dot.x + dot.y;
                 if constexpr (LN) v[1] = sum.x + sum.y;
                 group_sum<L, LN ? 2 : 1>(v);
-                const float2 c2 = f2s(-v[0] * inv), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv : 0.f);
+                // dx = rstd g - rstd c1 - xhat (rstd c2)
+                const float2 c2 = f2s(-v[0] * inv * rstd), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv * rstd : 0.f);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    if constexpr (LN) {
-                        ta[i] = f2add(ta[i], c1);
-                        tb[i] = f2add(tb[i], c1);
-                    }
-                    ta[i] = f2mul(f2fma(xa[i], c2, ta[i]), f2s(rstd));
-                    tb[i] = f2mul(f2fma(xb[i], c2, tb[i]), f2s(rstd));
+                    ta[i] = f2fma(xa[i], c2, LN ? f2fma(ta[i], f2s(rstd), c1) : f2mul(ta[i], f2s(rstd)));
+                    tb[i] = f2fma(xb[i], c2, LN ? f2fma(tb[i], f2s(rstd), c1) : f2mul(tb[i], f2s(rstd)));
                 }
-                const int h = h0 + u * G;
-                char *q = y + h * (p.y[r].head * ES);
-                if (h < heads && ch.oka) rope_st(q + ch.a * ES, rope_pack<XT, V>(ta).v);
-                if (h < heads && ch.okb) rope_st(q + ch.b * ES, rope_pack<XT, V>(tb).v);
+                const bool in = hl > u * G;
+                char *q = u == 0 ? y : y + u * ys;
+                if (in && ch.oka) rope_st(q + fa, rope_pack<XT, V>(ta).v);
+                if (in && ch.okb) rope_st(q + fb, rope_pack<XT, V>(tb).v);
             }
             if (!w.left) break;
-            fresh = nf;
+            if (turn) y = w.at(p, p.y[r], ES);
+            else y += U * ys;
         }
     }
     __syncthreads();  // the rings of all warps have been read
