@@ -275,7 +275,8 @@ int vector_of(const RopeParams &p, bool back) {
         bool ok = p.D % v == 0 && (p.inter ? p.rot % v : p.rot / 2 % v) == 0;
         for (const RopeHeads *t : {p.x, p.y, back ? p.g : p.x})
             for (int i = 0; i < 2; ++i)
-                ok = ok && aligned(t[i].p, (unsigned)(v * es)) && (t[i].batch | t[i].token | t[i].head) % v == 0;
+                ok = ok && aligned(t[i].p, (unsigned)(v * es)) && (t[i].batch | t[i].token | t[i].head) % v == 0 &&
+                     ((t[i].batch | t[i].token | t[i].head) / v) >> 32 == 0;
         for (int i = 0; i < 2; ++i)  // parameters are read 16 bytes (fp32) or 8 at a time
             for (const void *q : {p.gamma[i], p.beta[i]}) ok = ok && aligned(q, p.pdt == GBNORM_F32 ? 16 : 8);
         if (ok) return v;
@@ -283,8 +284,8 @@ int vector_of(const RopeParams &p, bool back) {
     return 0;
 }
 
-// mode: a RopeMode, or -1 - is_layernorm for the backward.
-Kernel pick(int mode, const RopeParams &p) {
+// mode: a RopeMode, or -1 - is_layernorm for the backward.  Strides become those of the kernel's kind.
+Kernel pick(int mode, RopeParams &p) {
 #define GBN_T(M) {kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, kRopeVec_##M##_bf16v4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8}
     static const RopeVariant(*const tables[5][5])[kRopeVecLanes] = {GBN_T(rot), GBN_T(rms), GBN_T(ln), GBN_T(brms),
                                                                      GBN_T(bln)};
@@ -298,6 +299,12 @@ Kernel pick(int mode, const RopeParams &p) {
             if (slots <= 4 << l) {
                 const int t = p.xdt + (v == 8 ? 2 : 0);
                 const RopeVariant &k = tables[m][t][kind][l];
+                for (RopeHeads *h : {p.x, p.y, p.g})
+                    for (int i = 0; i < 2; ++i) {
+                        h[i].batch /= v;
+                        h[i].token /= v;
+                        h[i].head /= v;
+                    }
                 // gamma (and beta) of both tensors as fp32 behind the rings
                 const int par = mode == kRopeOnly ? 0 : mode == kRopeLn ? 16 * p.D : 8 * p.D;
                 return {k.f, k.name, (8 >> l) * k.u, k.smem + par, ((m * 5 + t) * kRopeVecKinds + kind) * kRopeVecLanes + l, mode >= 0};

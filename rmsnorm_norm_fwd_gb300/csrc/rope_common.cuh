@@ -209,9 +209,10 @@ template <int GU, bool BOTH> struct RopeCursor {
     }
     // This lane's head of the pass, the last one if it has none.
     __device__ __forceinline__ int head(const RopeParams &p) const { return p.heads[r] - (hl > 0 ? hl : 1); }
-    // Byte address of that head in t.
-    __device__ __forceinline__ char *at(const RopeParams &p, const RopeHeads &t, int es) const {
-        return static_cast<char *>(t.p) + (b * t.batch + s * t.token + head(p) * t.head) * es;
+    // Address of that head in t, whose strides are in vectors of `size` bytes and below 2^32.
+    __device__ __forceinline__ char *at(const RopeParams &p, const RopeHeads &t, int size) const {
+        auto times = [](int i, int64_t stride) { return (uint64_t)(uint32_t)i * (uint32_t)stride; };
+        return static_cast<char *>(t.p) + (times(b, t.batch) + times(s, t.token) + times(head(p), t.head)) * size;
     }
     __device__ __forceinline__ int64_t stat(const RopeParams &p) const {
         return (b * p.S + s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0) + head(p);

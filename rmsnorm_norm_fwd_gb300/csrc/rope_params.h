@@ -14,7 +14,8 @@ constexpr int kRopeCTA = 256;      // threads of a CTA
 constexpr int kRopeWarps = kRopeCTA / 32;
 
 // Heads of one tensor: element i of head h of token (b, s) at
-// p + (b * batch + s * token + h * head + i) elements.
+// p + (b * batch + s * token + h * head + i) elements (for the kernels on
+// vectors the strides are in vectors).
 struct RopeHeads {
     void *p;
     int64_t batch, token, head;
@@ -60,10 +61,10 @@ extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 // take the place of the rings).
 constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
 constexpr int rope_fwd_smem(int v, int es, int l, int u) {
-    return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * (l + 1)) + 12 * v * l;
+    return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * l) + 12 * v * l;
 }
 constexpr int rope_bwd_smem(int v, int es, int l, int u) {
-    return kRopeWarps * (kRopeBwdDepth * u * (128 * v * es + 256) + 8 * v * (l + 1)) + 12 * v * l;
+    return kRopeWarps * (kRopeBwdDepth * u * (128 * v * es + 256) + 8 * v * l) + 12 * v * l;
 }
 
 struct RopeVariant {

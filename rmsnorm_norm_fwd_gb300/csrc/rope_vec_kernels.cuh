@@ -129,10 +129,11 @@ template <int V, int L, int KIND> struct RopeChunks {
             pb = cb * (V / 2);
         } else {
             const int half = nr / 2;
-            ca = sl < half ? sl : nr + 2 * (sl - half);
-            cb = sl < half ? sl + half : ca + 1;
-            oka = ca < n;
-            okb = cb < n;
+            const int rest = (n - nr + 1) / 2;
+            ca = sl < half ? sl : nr + (sl - half);
+            cb = sl < half ? sl + half : ca + rest;
+            oka = sl < half + rest;
+            okb = oka && cb < n;
             pa = pb = sl * V;
         }
         a = ca * V;
@@ -141,8 +142,6 @@ template <int V, int L, int KIND> struct RopeChunks {
         rb = okb && cb < nr;
         if (!oka) a = 0;  // lanes without a chunk stay inside the head
         if (!okb) b = 0;
-        if (!ra) pa = V * L;
-        if (!rb) pb = V * L;
     }
 };
 
@@ -163,11 +162,12 @@ template <int V, int L> struct RopeTurns {
 // A warp's cosines and sines: written by the lane that computed the pair, read by those whose chunks hold it.
 // As halves, a chunk's V pairs are read at once, and lie as rope_place says.
 template <int V, int L> struct RopeTable {
-    static constexpr int N = V * L, M = N + V, PER = N / 32 > 0 ? N / 32 : 1;
-    float c[M], s[M];  // pairs from N on: what is not rotated
-    __device__ __forceinline__ void ones(int lane, bool inter) {
-        if (lane < V) {
-            const int at = inter ? N + lane : rope_place<V>(N + lane, M);
+    static constexpr int N = V * L, PER = N / 32 > 0 ? N / 32 : 1;
+    float c[N], s[N];
+    // Behind the rotated pairs: cosine 1 and sine 0, for the chunks that are not.
+    __device__ __forceinline__ void ones(int lane, int rot, bool inter) {
+        for (int j = rot / 2 + lane; j < N; j += 32) {
+            const int at = inter ? j : rope_place<V>(j, N);
             c[at] = 1.f;
             s[at] = 0.f;
         }
@@ -183,7 +183,7 @@ template <int V, int L> struct RopeTable {
             if (2 * j < p.rot) {
                 float cs, sn;
                 rope_sincos((uint64_t)at * turns.f[j], p.sign, &cs, &sn);
-                const int to = inter ? j : rope_place<V>(j, M);
+                const int to = inter ? j : rope_place<V>(j, N);
                 c[to] = cs + turns.bad[j];
                 s[to] = sn + turns.bad[j];
             }
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     const RopeChunks<V, L, KIND> ch(p, sl);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     const int fa = ch.a * ES, fb = ch.b * ES;
-    const char *x = ahead.at(p, p.x[ahead.r], ES);
-    int64_t xs = p.x[ahead.r].head * (G * ES);
+    const char *x = ahead.at(p, p.x[ahead.r], V * ES);
+    int64_t xs = p.x[ahead.r].head * (G * V * ES);
     auto load = [&](int slot) {
         if (ahead.left) {
 #pragma unroll
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 rope_cp(&ring[slot][u][1][lane], q + fb, ch.okb, Raw{}.v);
             }
             if (ahead.next(p, grp)) {
-                x = ahead.at(p, p.x[ahead.r], ES);
-                xs = p.x[ahead.r].head * (G * ES);
+                x = ahead.at(p, p.x[ahead.r], V * ES);
+                xs = p.x[ahead.r].head * (G * V * ES);
             } else if (ahead.hl > 0) {
                 x += U * xs;
             }
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
     const uint32_t axis = Table::axes(p, lane);
     turns.fill(p);
-    tab.ones(lane, inter);
+    tab.ones(lane, p.rot, inter);
     if constexpr (MODE != kRopeOnly) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     __syncthreads();
     if (!w.left) return;
     const float inv = 1.f / (float)p.D;
-    char *y = w.at(p, p.y[w.r], ES);
-    int64_t ys = p.y[w.r].head * (G * ES), stat = w.stat(p);
+    char *y = w.at(p, p.y[w.r], V * ES);
+    int64_t ys = p.y[w.r].head * (G * V * ES), stat = w.stat(p);
     float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
     int turn = 2;  // 2: another token's angles, 1: another tensor's coefficients
     for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 }
             } else {
                 float2 c[H], s[H];
-                rope_get<V>(tab.c, ch.pa, Table::M, c);
-                rope_get<V>(tab.s, ch.pa, Table::M, s);
+                rope_get<V>(tab.c, ch.pa, Table::N, c);
+                rope_get<V>(tab.s, ch.pa, Table::N, s);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     ca[i] = f2mul(ga[i], c[i]);
@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         }
         if (!w.left) return;
         if (turn) {
-            y = w.at(p, p.y[w.r], ES);
-            ys = p.y[w.r].head * (G * ES);
+            y = w.at(p, p.y[w.r], V * ES);
+            ys = p.y[w.r].head * (G * V * ES);
             stat = w.stat(p);
         } else {
             y += U * ys;
@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     const RopeChunks<V, L, KIND> ch(p, sl);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     const int r = w.r, fa = ch.a * ES, fb = ch.b * ES;
-    const char *x = ahead.at(p, p.x[r], ES), *g = ahead.at(p, p.g[r], ES);
-    const int64_t xs = p.x[r].head * (G * ES), gs = p.g[r].head * (G * ES);
+    const char *x = ahead.at(p, p.x[r], V * ES), *g = ahead.at(p, p.g[r], V * ES);
+    const int64_t xs = p.x[r].head * (G * V * ES), gs = p.g[r].head * (G * V * ES);
     int64_t stat = ahead.stat(p);
     auto load = [&](int slot) {
         if (ahead.left) {
@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 if constexpr (LN) rope_cp(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true, 0.f);
             }
             if (ahead.next(p, grp)) {
-                x = ahead.at(p, p.x[r], ES);
-                g = ahead.at(p, p.g[r], ES);
+                x = ahead.at(p, p.x[r], V * ES);
+                g = ahead.at(p, p.g[r], V * ES);
                 stat = ahead.stat(p);
             } else if (ahead.hl > 0) {
                 x += U * xs;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
     const uint32_t axis = Table::axes(p, lane);
     turns.fill(p);
-    tab.ones(lane, inter);
+    tab.ones(lane, p.rot, inter);
 #pragma unroll
     for (int i = 0; i < 2; ++i) rope_param<V>(par + i * p.D, p.gamma[i], p.D, p.pdt, 1.f);
     __syncthreads();
@@ -467,8 +467,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
     if (w.left) {
         const float inv = 1.f / (float)p.D;
-        char *y = w.at(p, p.y[r], ES);
-        const int64_t ys = p.y[r].head * (G * ES);
+        char *y = w.at(p, p.y[r], V * ES);
+        const int64_t ys = p.y[r].head * (G * V * ES);
         int turn = 2;
         for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
             const int hl = w.hl;
@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                             s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
                         }
                     } else {
-                        rope_get<V>(tab.c, ch.pa, Table::M, c);
-                        rope_get<V>(tab.s, ch.pa, Table::M, s);
+                        rope_get<V>(tab.c, ch.pa, Table::N, c);
+                        rope_get<V>(tab.s, ch.pa, Table::N, s);
                     }
                     rope_unpack<XT, V>(ring[slot].g[u][0][lane], ga);
                     rope_unpack<XT, V>(ring[slot].g[u][1][lane], gb);
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 if (in && ch.okb) rope_st(q + fb, rope_pack<XT, V>(tb).v);
             }
             if (!w.left) break;
-            if (turn) y = w.at(p, p.y[r], ES);
+            if (turn) y = w.at(p, p.y[r], V * ES);
             else y += U * ys;
         }
     }
