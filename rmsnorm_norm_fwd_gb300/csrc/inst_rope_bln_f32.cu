@@ -1,7 +1,7 @@
-// Head operators on vectors: one direction, norm and type.
+// Head operators on vectors: one direction and norm, these types.
 #define GBN_MODE -2
 #define GBN_XT kF32
 #define GBN_V 4
-#define GBN_WHOLE 1
+#define GBN_WHOLE 2
 #define GBN_NAME bln_f32v4
 #include "inst_rope_body.cuh"

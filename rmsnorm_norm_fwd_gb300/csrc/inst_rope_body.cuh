@@ -1,7 +1,7 @@
 // Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V, the
-// type and elements of a vector.  Defines kRopeVec_<GBN_NAME>[kind][lanes a head].  Whole heads rotated as halves or as
-// neighbours have kernels of their own on 16-byte vectors up to 16 lanes, where they measured faster; the rest runs
-// on the kernels for any rotation.
+// type and elements of a vector.  Defines kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE 2 (16-byte vectors): whole
+// heads rotated as halves or as neighbours have kernels of their own up to 16 lanes, where they measured faster; 1, 0:
+// all run on the kernels for any rotation, and on fewer numbers of lanes.
 #include "rope_vec_kernels.cuh"
 
 #ifndef GBN_CAT
@@ -13,27 +13,37 @@
 #if GBN_MODE >= 0
 #define GBN_K(L, KIND, S) \
     {(const void *)&rope_fwd_vec<GBN_MODE, GBN_XT, GBN_V, L, KIND, GBN_FU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_fwd_smem(GBN_V, GBN_XT == kF32 ? 4 : 2, L, GBN_FU(KIND)), GBN_FU(KIND)}
+     rope_fwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_V, L, GBN_FU(KIND)), GBN_FU(KIND), L}
 #else
 #define GBN_K(L, KIND, S) \
     {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, L, KIND, GBN_BU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_bwd_smem(GBN_V, GBN_XT == kF32 ? 4 : 2, L, GBN_BU(KIND)), GBN_BU(KIND)}
+     rope_bwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_V, L, GBN_BU(KIND)), GBN_BU(KIND), L}
 #endif
 #define GBN_FU(KIND) (GBN_MODE == 0 && KIND != kRopeSome ? 2 : 1)
 #define GBN_BU(KIND) 1
-#define GBN_ANY {GBN_K(4, kRopeSome, ""), GBN_K(8, kRopeSome, ""), GBN_K(16, kRopeSome, ""), GBN_K(32, kRopeSome, "")}
+#define GBN_ANY(L) GBN_K(L, kRopeSome, "")
+#if GBN_WHOLE == 2
+#define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(6), GBN_ANY(8), GBN_ANY(9), GBN_ANY(10), GBN_ANY(16), GBN_ANY(32)}
+#elif GBN_WHOLE == 1
+#define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(8), GBN_ANY(8), GBN_ANY(9), GBN_ANY(16), GBN_ANY(16), GBN_ANY(32)}
+#else
+#define GBN_SOME {GBN_ANY(4), GBN_ANY(8), GBN_ANY(8), GBN_ANY(8), GBN_ANY(16), GBN_ANY(16), GBN_ANY(16), GBN_ANY(32)}
+#endif
 
 namespace gbn {
 const RopeVariant GBN_CAT(kRopeVec_, GBN_NAME)[kRopeVecKinds][kRopeVecLanes] = {
-#if GBN_WHOLE
-    {GBN_K(4, kRopeHalves, "h"), GBN_K(8, kRopeHalves, "h"), GBN_K(16, kRopeHalves, "h"), GBN_K(32, kRopeSome, "")},
-    {GBN_K(4, kRopeNeighbours, "n"), GBN_K(8, kRopeNeighbours, "n"), GBN_K(16, kRopeNeighbours, "n"),
-     GBN_K(32, kRopeSome, "")},
+#if GBN_WHOLE == 2
+    {GBN_K(4, kRopeHalves, "h"), GBN_K(5, kRopeHalves, "h"), GBN_K(6, kRopeHalves, "h"), GBN_K(8, kRopeHalves, "h"),
+     GBN_K(9, kRopeHalves, "h"), GBN_K(10, kRopeHalves, "h"), GBN_K(16, kRopeHalves, "h"), GBN_ANY(32)},
+    {GBN_K(4, kRopeNeighbours, "n"), GBN_K(5, kRopeNeighbours, "n"), GBN_K(6, kRopeNeighbours, "n"),
+     GBN_K(8, kRopeNeighbours, "n"), GBN_K(9, kRopeNeighbours, "n"), GBN_K(10, kRopeNeighbours, "n"),
+     GBN_K(16, kRopeNeighbours, "n"), GBN_ANY(32)},
 #else
-    GBN_ANY, GBN_ANY,
+    GBN_SOME, GBN_SOME,
 #endif
-    GBN_ANY};
+    GBN_SOME};
 }  // namespace gbn
+#undef GBN_SOME
 #undef GBN_K
 #undef GBN_FU
 #undef GBN_BU

@@ -1,0 +1,7 @@
+// Head operators on vectors: one direction and norm, these types.
+#define GBN_MODE -1
+#define GBN_XT kF16
+#define GBN_V 4
+#define GBN_WHOLE 1
+#define GBN_NAME brms_f16v4
+#include "inst_rope_body.cuh"

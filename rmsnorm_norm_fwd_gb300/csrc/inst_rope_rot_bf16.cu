@@ -1,13 +1,7 @@
-// Head operators on vectors: one direction, norm and type.
+// Head operators on vectors: one direction and norm, these types.
 #define GBN_MODE 0
 #define GBN_XT kBF16
 #define GBN_V 8
-#define GBN_WHOLE 1
+#define GBN_WHOLE 2
 #define GBN_NAME rot_bf16v8
-#include "inst_rope_body.cuh"
-#define GBN_MODE 0
-#define GBN_XT kBF16
-#define GBN_V 4
-#define GBN_WHOLE 0
-#define GBN_NAME rot_bf16v4
 #include "inst_rope_body.cuh"

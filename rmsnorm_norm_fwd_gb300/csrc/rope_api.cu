@@ -222,12 +222,11 @@ int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, bo
         p->warps[0] = p->units[0];
         p->warps[1] = p->units[1];
     } else {
-        // both in one tensor only if there is no second; else at least one warp each
         // a token's angles cost about as much as one and a half passes
-        const double q = (double)s.tokens() * (p->passes[0] + 1.5), k = (double)s.tokens() * (p->passes[1] + 1.5);
-        const double part = q / (q + k) * (double)most;
-        p->warps[0] = s.tensors() == 1 ? most : std::min(most - 1, std::max<int64_t>(1, (int64_t)(part + 0.5)));
-        p->warps[1] = most - p->warps[0];
+        const double q = p->passes[0] + 1.5, k = s.tensors() == 1 ? 0.0 : p->passes[1] + 1.5;
+        const int64_t part = std::max<int64_t>(1, (int64_t)(q / (q + k) * (double)most + 0.5));
+        p->warps[0] = std::min(p->units[0], s.tensors() == 1 ? most : std::min(most - 1, part));
+        p->warps[1] = std::min(p->units[1], most - p->warps[0]);
     }
     for (int i = 0; i < 2; ++i) {
         if (p->warps[i] == 0) continue;
@@ -266,19 +265,24 @@ int any_size(int64_t D, int rot) {  // log2 of the pairs a lane holds
     return lg;
 }
 
+constexpr int kVecTypes = 6;  // fp32, fp16, bf16 by four, fp16, bf16 by eight, differing types
+
 // Elements of the vectors that all tensors of a call move as: every head and
 // chunk starts on a vector, the rotated part holds whole ones.  0: none.
 int vector_of(const RopeParams &p, bool back) {
-    if (p.xdt != p.ydt) return 0;
-    const int es = elem_size(p.xdt);
-    for (int v = 16 / es; v >= 4; v /= 2) {
+    const int xs = elem_size(p.xdt), ys = elem_size(p.ydt);
+    const struct {
+        const RopeHeads *t;
+        int es;
+    } all[3] = {{p.x, xs}, {p.y, back ? xs : ys}, {back ? p.g : p.x, back ? ys : xs}};
+    for (int v = p.xdt == p.ydt && xs == 2 ? 8 : 4; v >= 4; v /= 2) {
         bool ok = p.D % v == 0 && (p.inter ? p.rot % v : p.rot / 2 % v) == 0;
-        for (const RopeHeads *t : {p.x, p.y, back ? p.g : p.x})
-            for (int i = 0; i < 2; ++i)
-                ok = ok && aligned(t[i].p, (unsigned)(v * es)) && (t[i].batch | t[i].token | t[i].head) % v == 0 &&
-                     ((t[i].batch | t[i].token | t[i].head) / v) >> 32 == 0;
-        for (int i = 0; i < 2; ++i)  // parameters are read 16 bytes (fp32) or 8 at a time
-            for (const void *q : {p.gamma[i], p.beta[i]}) ok = ok && aligned(q, p.pdt == GBNORM_F32 ? 16 : 8);
+        for (const auto &a : all)
+            for (int i = 0; i < 2; ++i) {
+                const RopeHeads &t = a.t[i];
+                ok = ok && aligned(t.p, (unsigned)(v * a.es)) && (t.batch | t.token | t.head) % v == 0 &&
+                     ((t.batch | t.token | t.head) / v) >> 32 == 0;
+            }
         if (ok) return v;
     }
     return 0;
@@ -286,9 +290,11 @@ int vector_of(const RopeParams &p, bool back) {
 
 // mode: a RopeMode, or -1 - is_layernorm for the backward.  Strides become those of the kernel's kind.
 Kernel pick(int mode, RopeParams &p) {
-#define GBN_T(M) {kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, kRopeVec_##M##_bf16v4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8}
-    static const RopeVariant(*const tables[5][5])[kRopeVecLanes] = {GBN_T(rot), GBN_T(rms), GBN_T(ln), GBN_T(brms),
-                                                                     GBN_T(bln)};
+#define GBN_T(M) \
+    {kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, kRopeVec_##M##_bf16v4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8, \
+     kRopeVec_##M##_mixv4}
+    static const RopeVariant(*const tables[5][kVecTypes])[kRopeVecLanes] = {GBN_T(rot), GBN_T(rms), GBN_T(ln),
+                                                                            GBN_T(brms), GBN_T(bln)};
 #undef GBN_T
     const int v = vector_of(p, mode < 0), m = mode < 0 ? 2 - mode : mode;
     if (v) {
@@ -296,8 +302,8 @@ Kernel pick(int mode, RopeParams &p) {
         const int slots = p.inter ? (chunks + 1) / 2 : rot / 2 + (chunks - rot + 1) / 2;
         const int kind = p.rot < p.D ? kRopeVecKinds - 1 : p.inter;
         for (int l = 0; l < kRopeVecLanes; ++l)
-            if (slots <= 4 << l) {
-                const int t = p.xdt + (v == 8 ? 2 : 0);
+            if (slots <= kRopeLaneCounts[l]) {
+                const int t = p.xdt != p.ydt ? kVecTypes - 1 : p.xdt + (v == 8 ? 2 : 0);
                 const RopeVariant &k = tables[m][t][kind][l];
                 for (RopeHeads *h : {p.x, p.y, p.g})
                     for (int i = 0; i < 2; ++i) {
@@ -307,14 +313,14 @@ Kernel pick(int mode, RopeParams &p) {
                     }
                 // gamma (and beta) of both tensors as fp32 behind the rings
                 const int par = mode == kRopeOnly ? 0 : mode == kRopeLn ? 16 * p.D : 8 * p.D;
-                return {k.f, k.name, (8 >> l) * k.u, k.smem + par, ((m * 5 + t) * kRopeVecKinds + kind) * kRopeVecLanes + l, mode >= 0};
+                return {k.f, k.name, 32 / k.lanes * k.u, k.smem + par, ((m * kVecTypes + t) * kRopeVecKinds + kind) * kRopeVecLanes + l, mode >= 0};
             }
     }
-    const int n = any_size(p.D, p.rot), slot = 5 * 5 * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
+    const int n = any_size(p.D, p.rot), slot = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
     return mode < 0 ? Kernel{kRopeBwdAny[-1 - mode][n], "any", 1, kRopeWarps * p.D * 4, slot, false}
                     : Kernel{kRopeFwdAny[mode][n], "any", 1, 0, slot, false};
 }
-constexpr int kSlots = 5 * 5 * kRopeVecKinds * kRopeVecLanes + 5 * kRopeAnySizes;
+constexpr int kSlots = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + 5 * kRopeAnySizes;
 std::atomic<int> g_resident[kHostMaxDev][kSlots];
 
 // CTAs of a kernel that an SM holds, measured once per device.

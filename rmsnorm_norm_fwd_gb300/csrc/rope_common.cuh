@@ -193,11 +193,9 @@ template <int GU, bool BOTH> struct RopeCursor {
         --rounds;
         const bool far = rounds > 0;
         b += far ? p.step_b[r] : 0;
-        s += far ? p.step_s[r] : 1;
-        if (s >= (int)p.S) {
-            s -= (int)p.S;
-            ++b;
-        }
+        const uint32_t to = (uint32_t)s + (far ? p.step_s[r] : 1), S = (uint32_t)p.S;  // below 2^32
+        s = (int)(to >= S ? to - S : to);
+        b += to >= S;
         if (rounds == 0) {
             int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), first, count;
             if (r) w -= p.warps[0];

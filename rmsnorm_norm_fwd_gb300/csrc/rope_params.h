@@ -55,16 +55,16 @@ constexpr int kRopeAnySizes = 5;
 extern const void *const kRopeFwdAny[3][kRopeAnySizes];
 extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 
-// On vectors of v elements of es bytes, l lanes a head, u heads a lane and
+// On vectors of v elements and `vector` bytes, l lanes a head, u heads a lane and
 // pass: passes in flight a warp, and dynamic shared memory without the
 // parameters (rings, tables of cosines and sines, frequencies; the backward's column sums
 // take the place of the rings).
 constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
-constexpr int rope_fwd_smem(int v, int es, int l, int u) {
-    return kRopeWarps * (kRopeFwdDepth * u * 64 * v * es + 8 * v * l) + 12 * v * l;
+constexpr int rope_fwd_smem(int vector, int v, int l, int u) {
+    return kRopeWarps * (kRopeFwdDepth * u * 64 * vector + 8 * v * l) + 12 * v * l;
 }
-constexpr int rope_bwd_smem(int v, int es, int l, int u) {
-    return kRopeWarps * (kRopeBwdDepth * u * (128 * v * es + 256) + 8 * v * l) + 12 * v * l;
+constexpr int rope_bwd_smem(int vector, int v, int l, int u) {
+    return kRopeWarps * (kRopeBwdDepth * u * (128 * vector + 256) + 8 * v * l) + 12 * v * l;
 }
 
 struct RopeVariant {
@@ -72,14 +72,17 @@ struct RopeVariant {
     const char *name;
     int smem;  // without parameters
     int u;     // heads a lane and pass
+    int lanes; // a head
 };
-constexpr int kRopeVecLanes = 4;  // lanes a head: 4, 8, 16, 32
+constexpr int kRopeVecLanes = 8;
+constexpr int kRopeLaneCounts[kRopeVecLanes] = {4, 5, 6, 8, 9, 10, 16, 32};  // lanes a head
 constexpr int kRopeVecKinds = 3;  // RopeKind
 // For each direction and norm (rot: the rotation alone; b: backward) and vector.
 #define GBN_ROPE_VEC(M) \
     extern const RopeVariant kRopeVec_##M##_bf16v8[kRopeVecKinds][kRopeVecLanes], \
         kRopeVec_##M##_f16v8[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_bf16v4[kRopeVecKinds][kRopeVecLanes], \
-        kRopeVec_##M##_f16v4[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_f32v4[kRopeVecKinds][kRopeVecLanes]
+        kRopeVec_##M##_f16v4[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_f32v4[kRopeVecKinds][kRopeVecLanes], \
+        kRopeVec_##M##_mixv4[kRopeVecKinds][kRopeVecLanes]
 GBN_ROPE_VEC(rot);
 GBN_ROPE_VEC(rms);
 GBN_ROPE_VEC(ln);

@@ -25,11 +25,10 @@ template <> struct RopeRaw<kF16, 8> { uint4 v; };
 template <> struct RopeRaw<kBF16, 8> { uint4 v; };
 template <> struct RopeRaw<kF16, 4> { uint2 v; };
 template <> struct RopeRaw<kBF16, 4> { uint2 v; };
-
-__device__ __forceinline__ void rope_ld(const void *p, uint4 &v) { v = *static_cast<const uint4 *>(p); }
-__device__ __forceinline__ void rope_ld(const void *p, uint2 &v) { v = *static_cast<const uint2 *>(p); }
-__device__ __forceinline__ void rope_st(void *p, const uint4 &v) { *static_cast<uint4 *>(p) = v; }
-__device__ __forceinline__ void rope_st(void *p, const uint2 &v) { *static_cast<uint2 *>(p) = v; }
+// Types that differ within a call, read from it: 16 bytes hold four elements of any.
+constexpr int kMixed = 3;
+template <> struct RopeRaw<kMixed, 4> { uint4 v; };
+template <int XT> __device__ __forceinline__ int rope_esize(int dt) { return XT == kMixed ? esize(dt) : XT == kF32 ? 4 : 2; }
 
 template <int XT> __device__ __forceinline__ float2 rope_pair(uint32_t w) {
     if constexpr (XT == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -44,8 +43,20 @@ template <int XT> __device__ __forceinline__ uint32_t rope_word(float2 f) {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
-template <int XT, int V> __device__ __forceinline__ void rope_unpack(const RopeRaw<XT, V> &r, float2 (&f)[V / 2]) {
-    if constexpr (XT == kF32) {
+template <int XT, int V>
+__device__ __forceinline__ void rope_unpack(const RopeRaw<XT, V> &r, int dt, float2 (&f)[V / 2]) {
+    if constexpr (XT == kMixed) {
+        if (dt == kF32) {
+            f[0] = make_float2(__uint_as_float(r.v.x), __uint_as_float(r.v.y));
+            f[1] = make_float2(__uint_as_float(r.v.z), __uint_as_float(r.v.w));
+        } else if (dt == kBF16) {
+            f[0] = rope_pair<kBF16>(r.v.x);
+            f[1] = rope_pair<kBF16>(r.v.y);
+        } else {
+            f[0] = rope_pair<kF16>(r.v.x);
+            f[1] = rope_pair<kF16>(r.v.y);
+        }
+    } else if constexpr (XT == kF32) {
         f[0] = make_float2(__uint_as_float(r.v.x), __uint_as_float(r.v.y));
         f[1] = make_float2(__uint_as_float(r.v.z), __uint_as_float(r.v.w));
     } else {
@@ -57,33 +68,33 @@ template <int XT, int V> __device__ __forceinline__ void rope_unpack(const RopeR
         }
     }
 }
-template <int XT, int V> __device__ __forceinline__ RopeRaw<XT, V> rope_pack(const float2 (&f)[V / 2]) {
-    RopeRaw<XT, V> r;
-    if constexpr (XT == kF32) {
-        r.v = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
-                         __float_as_uint(f[1].y));
+// V elements rounded to their type and stored.
+template <int XT, int V> __device__ __forceinline__ void rope_store(char *p, int dt, const float2 (&f)[V / 2]) {
+    if (XT == kF32 || (XT == kMixed && dt == kF32)) {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    } else if constexpr (V == 8) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(rope_word<XT>(f[0]), rope_word<XT>(f[1]), rope_word<XT>(f[2]), rope_word<XT>(f[3]));
+    } else if (XT == kBF16 || (XT == kMixed && dt == kBF16)) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(rope_word<kBF16>(f[0]), rope_word<kBF16>(f[1]));
     } else {
-        r.v.x = rope_word<XT>(f[0]);
-        r.v.y = rope_word<XT>(f[1]);
-        if constexpr (V == 8) {
-            r.v.z = rope_word<XT>(f[2]);
-            r.v.w = rope_word<XT>(f[3]);
-        }
+        *reinterpret_cast<uint2 *>(p) = make_uint2(rope_word<kF16>(f[0]), rope_word<kF16>(f[1]));
     }
-    return r;
 }
 
 // Asynchronous copies into the lane's own places of the ring: no other thread
 // reads them, so that waiting for the lane's own groups is enough.  Lanes
 // without an element fill with zeros (`from` is then any valid address).
-__device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, const uint4 &) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
+template <int BYTES> __device__ __forceinline__ void rope_cp_bytes(void *to, const void *from, bool in) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? BYTES : 0), "n"(BYTES)
+                     : "memory");
 }
-__device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, const uint2 &) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void rope_cp(void *to, const void *from, bool in, float) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
+template <int XT, int V> __device__ __forceinline__ void rope_cp(RopeRaw<XT, V> *to, const char *from, bool in, int dt) {
+    if (XT == kF32 || V == 8 || (XT == kMixed && dt == kF32)) rope_cp_bytes<16>(to, from, in);
+    else rope_cp_bytes<8>(to, from, in);
 }
 __device__ __forceinline__ void rope_cp_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void rope_cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -116,7 +127,7 @@ enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopeSome = 2 };
 template <int V, int L, int KIND> struct RopeChunks {
     int a, b, pa, pb;
     bool oka, okb, ra, rb;
-    __device__ __forceinline__ RopeChunks(const RopeParams &p, int sl) {
+    __device__ __forceinline__ RopeChunks(const RopeParams &p, int sl, bool used) {
         const int n = p.D / V, nr = p.rot / V;
         int ca, cb;
         if (KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter)) {
@@ -138,10 +149,50 @@ template <int V, int L, int KIND> struct RopeChunks {
         }
         a = ca * V;
         b = cb * V;
+        oka = oka && used;
+        okb = okb && used;
         ra = oka && ca < nr;
         rb = okb && cb < nr;
         if (!oka) a = 0;  // lanes without a chunk stay inside the head
         if (!okb) b = 0;
+    }
+};
+
+// Sums over the L lanes of a head.  Powers of two by a butterfly.  Else by
+// rotations within the group, whose order of additions differs between lanes:
+// sums over 3 lanes are two rotations more, over 5 a chain (2, 4, 5).
+template <int L> struct RopeLanes {
+    static constexpr bool POW2 = (L & (L - 1)) == 0;
+    int sl, base;
+    __device__ __forceinline__ RopeLanes(int lane) : sl(lane % L), base(lane - lane % L) {}
+    __device__ __forceinline__ float from(float v, int by) const {
+        const int at = sl + by;
+        return __shfl_sync(0xffffffffu, v, base + (at >= L ? at - L : at));
+    }
+    template <int R> __device__ __forceinline__ void sum(float (&v)[R]) const {
+        if constexpr (POW2) {
+            group_sum<L, R>(v);
+        } else {
+            static_assert(L == 5 || L == 6 || L == 9 || L == 10, "lanes a head");
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float t = v[i];
+                if constexpr (L == 6) t += from(t, 3);
+                if constexpr (L == 10) t += from(t, 5);
+                if constexpr (L == 9) {
+                    const float a = from(t, 3), b = from(t, 6);
+                    t += a + b;
+                }
+                if constexpr (L == 6 || L == 9) {
+                    const float a = from(t, 1), b = from(t, 2);
+                    v[i] = t + (a + b);
+                } else {
+                    float u = t + from(t, 1);
+                    u += from(u, 2);
+                    v[i] = u + from(t, 4);
+                }
+            }
+        }
     }
 };
 
@@ -162,7 +213,7 @@ template <int V, int L> struct RopeTurns {
 // A warp's cosines and sines: written by the lane that computed the pair, read by those whose chunks hold it.
 // As halves, a chunk's V pairs are read at once, and lie as rope_place says.
 template <int V, int L> struct RopeTable {
-    static constexpr int N = V * L, PER = N / 32 > 0 ? N / 32 : 1;
+    static constexpr int N = V * L, PER = (N + 31) / 32;
     float c[N], s[N];
     // Behind the rotated pairs: cosine 1 and sine 0, for the chunks that are not.
     __device__ __forceinline__ void ones(int lane, int rot, bool inter) {
@@ -206,39 +257,43 @@ template <typename W> __device__ __forceinline__ int64_t rope_position(const Rop
                    : (int64_t)__ldg(static_cast<const int *>(p.pos) + q);
 }
 
+constexpr int kRopeNoHead = 1 << 20;  // the group of lanes beyond the last whole one: never has a head
+
 __device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x); }
 
 template <int MODE, int XT, int V, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_constant__ RopeParams p) {
-    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2, DEPTH = kRopeFwdDepth;
+    constexpr int G = 32 / L, H = V / 2, DEPTH = kRopeFwdDepth;
     using Table = RopeTable<V, L>;
     using Raw = RopeRaw<XT, V>;
     // rings, tables, frequencies, then gamma (and beta) of the queries and of the keys
     extern __shared__ __align__(16) unsigned char rope_smem[];
-    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const RopeLanes<L> lanes(lane);
+    const int sl = lanes.sl, grp = lane < G * L ? lane / L : kRopeNoHead;
     Raw(*ring)[U][2][32] = reinterpret_cast<Raw(*)[U][2][32]>(rope_smem) + warp * DEPTH;
     Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * U * DEPTH * kRopeWarps);
     RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1);
     Table &tab = tables[warp];
     RopeCursor<G * U, true> w(p, grp), ahead = w;  // the pass worked on, the pass to load
-    const RopeChunks<V, L, KIND> ch(p, sl);
+    const RopeChunks<V, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
-    const int fa = ch.a * ES, fb = ch.b * ES;
-    const char *x = ahead.at(p, p.x[ahead.r], V * ES);
-    int64_t xs = p.x[ahead.r].head * (G * V * ES);
+    const int xes = rope_esize<XT>(p.xdt), yes = rope_esize<XT>(p.ydt);
+    const char *x = ahead.at(p, p.x[ahead.r], V * xes);
+    int64_t xs = p.x[ahead.r].head * (G * V * xes);
     auto load = [&](int slot) {
         if (ahead.left) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 // a lane without a head in the pass reads another, and stores nothing
                 const char *q = u == 0 ? x : x + (ahead.hl > u * G ? u * xs : 0);
-                rope_cp(&ring[slot][u][0][lane], q + fa, ch.oka, Raw{}.v);
-                rope_cp(&ring[slot][u][1][lane], q + fb, ch.okb, Raw{}.v);
+                rope_cp(&ring[slot][u][0][lane], q + ch.a * xes, ch.oka, p.xdt);
+                rope_cp(&ring[slot][u][1][lane], q + ch.b * xes, ch.okb, p.xdt);
             }
             if (ahead.next(p, grp)) {
-                x = ahead.at(p, p.x[ahead.r], V * ES);
-                xs = p.x[ahead.r].head * (G * V * ES);
+                x = ahead.at(p, p.x[ahead.r], V * xes);
+                xs = p.x[ahead.r].head * (G * V * xes);
             } else if (ahead.hl > 0) {
                 x += U * xs;
             }
@@ -261,8 +316,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     __syncthreads();
     if (!w.left) return;
     const float inv = 1.f / (float)p.D;
-    char *y = w.at(p, p.y[w.r], V * ES);
-    int64_t ys = p.y[w.r].head * (G * V * ES), stat = w.stat(p);
+    char *y = w.at(p, p.y[w.r], V * yes);
+    int64_t ys = p.y[w.r].head * (G * V * yes), stat = w.stat(p);
     float2 ca[H], sa[H], cb[H], sb[H], ba[H], bb[H];
     int turn = 2;  // 2: another token's angles, 1: another tensor's coefficients
     for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
@@ -338,8 +393,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         for (int u = 0; u < U; ++u) {
             const bool in = hl > u * G;
             float2 va[H], vb[H];
-            rope_unpack<XT, V>(ra[u], va);
-            rope_unpack<XT, V>(rb[u], vb);
+            rope_unpack<XT, V>(ra[u], p.xdt, va);
+            rope_unpack<XT, V>(rb[u], p.xdt, vb);
             if constexpr (MODE != kRopeOnly) {
                 float mean = 0.f;
                 if constexpr (MODE == kRopeLn) {
@@ -347,7 +402,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < H; ++i) t = f2add(t, f2add(va[i], vb[i]));
                     float sum[1] = {t.x + t.y};
-                    group_sum<L, 1>(sum);
+                    lanes.sum(sum);
                     mean = sum[0] * inv;
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
@@ -364,7 +419,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 // a chunk that is not there holds zeros, with the mean off it no longer
                 const bool ka = MODE != kRopeLn || ch.oka, kb = MODE != kRopeLn || ch.okb;
                 float sq[1] = {(ka ? ta.x + ta.y : 0.f) + (kb ? tb.x + tb.y : 0.f)};
-                group_sum<L, 1>(sq);
+                lanes.sum(sq);
                 const float rstd = rsqrtf(sq[0] * inv + p.eps);
                 if (p.rstd && sl == 0 && in) p.rstd[stat + u * G] = rstd;
                 if (MODE == kRopeLn && p.mean && sl == 0 && in) p.mean[stat + u * G] = mean;
@@ -386,13 +441,13 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 ub[i] = f2fma(vb[i], cb[i], MODE == kRopeLn ? f2fma(tb, sb[i], bb[i]) : f2mul(tb, sb[i]));
             }
             char *q = u == 0 ? y : y + u * ys;
-            if (in && ch.oka) rope_st(q + fa, rope_pack<XT, V>(ua).v);
-            if (in && ch.okb) rope_st(q + fb, rope_pack<XT, V>(ub).v);
+            if (in && ch.oka) rope_store<XT, V>(q + ch.a * yes, p.ydt, ua);
+            if (in && ch.okb) rope_store<XT, V>(q + ch.b * yes, p.ydt, ub);
         }
         if (!w.left) return;
         if (turn) {
-            y = w.at(p, p.y[w.r], V * ES);
-            ys = p.y[w.r].head * (G * V * ES);
+            y = w.at(p, p.y[w.r], V * yes);
+            ys = p.y[w.r].head * (G * V * yes);
             stat = w.stat(p);
         } else {
             y += U * ys;
@@ -404,7 +459,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
 template <bool LN, int XT, int V, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
-    constexpr int G = 32 / L, H = V / 2, ES = XT == kF32 ? 4 : 2, DEPTH = kRopeBwdDepth;
+    constexpr int G = 32 / L, H = V / 2, DEPTH = kRopeBwdDepth;
     using Table = RopeTable<V, L>;
     using Raw = RopeRaw<XT, V>;
     struct Slot {
@@ -413,18 +468,20 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     };
     // rings, tables, frequencies, gamma of the queries and of the keys; at the end the column sums [kRopeWarps][D] over the rings
     extern __shared__ __align__(16) unsigned char rope_smem[];
-    const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const RopeLanes<L> lanes(lane);
+    const int sl = lanes.sl, grp = lane < G * L ? lane / L : kRopeNoHead;
     Slot *ring = reinterpret_cast<Slot *>(rope_smem) + warp * DEPTH;
     Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps);
     RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1), *rope_acc = reinterpret_cast<float *>(rope_smem);
     Table &tab = tables[warp];
     RopeCursor<G * U, false> w(p, grp), ahead = w;  // the pass worked on, the pass to load
-    const RopeChunks<V, L, KIND> ch(p, sl);
+    const RopeChunks<V, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
-    const int r = w.r, fa = ch.a * ES, fb = ch.b * ES;
-    const char *x = ahead.at(p, p.x[r], V * ES), *g = ahead.at(p, p.g[r], V * ES);
-    const int64_t xs = p.x[r].head * (G * V * ES), gs = p.g[r].head * (G * V * ES);
+    const int r = w.r, xes = rope_esize<XT>(p.xdt), ges = rope_esize<XT>(p.ydt);
+    const char *x = ahead.at(p, p.x[r], V * xes), *g = ahead.at(p, p.g[r], V * ges);
+    const int64_t xs = p.x[r].head * (G * V * xes), gs = p.g[r].head * (G * V * ges);
     int64_t stat = ahead.stat(p);
     auto load = [&](int slot) {
         if (ahead.left) {
@@ -434,16 +491,16 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 // a lane without a head in the pass reads another with a gradient of zeros, and stores nothing
                 const bool in = ahead.hl > u * G;
                 const char *q = u == 0 ? x : x + (in ? u * xs : 0), *d = u == 0 ? g : g + (in ? u * gs : 0);
-                rope_cp(&to.x[u][0][lane], q + fa, ch.oka, Raw{}.v);
-                rope_cp(&to.x[u][1][lane], q + fb, ch.okb, Raw{}.v);
-                rope_cp(&to.g[u][0][lane], d + fa, in && ch.oka, Raw{}.v);
-                rope_cp(&to.g[u][1][lane], d + fb, in && ch.okb, Raw{}.v);
-                rope_cp(&to.rstd[u][lane], p.rstd + stat + (in ? u * G : 0), true, 0.f);
-                if constexpr (LN) rope_cp(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true, 0.f);
+                rope_cp(&to.x[u][0][lane], q + ch.a * xes, ch.oka, p.xdt);
+                rope_cp(&to.x[u][1][lane], q + ch.b * xes, ch.okb, p.xdt);
+                rope_cp(&to.g[u][0][lane], d + ch.a * ges, in && ch.oka, p.ydt);
+                rope_cp(&to.g[u][1][lane], d + ch.b * ges, in && ch.okb, p.ydt);
+                rope_cp_bytes<4>(&to.rstd[u][lane], p.rstd + stat + (in ? u * G : 0), true);
+                if constexpr (LN) rope_cp_bytes<4>(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true);
             }
             if (ahead.next(p, grp)) {
-                x = ahead.at(p, p.x[r], V * ES);
-                g = ahead.at(p, p.g[r], V * ES);
+                x = ahead.at(p, p.x[r], V * xes);
+                g = ahead.at(p, p.g[r], V * ges);
                 stat = ahead.stat(p);
             } else if (ahead.hl > 0) {
                 x += U * xs;
@@ -467,8 +524,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
     if (w.left) {
         const float inv = 1.f / (float)p.D;
-        char *y = w.at(p, p.y[r], V * ES);
-        const int64_t ys = p.y[r].head * (G * V * ES);
+        char *y = w.at(p, p.y[r], V * xes);
+        const int64_t ys = p.y[r].head * (G * V * xes);
         int turn = 2;
         for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
             const int hl = w.hl;
@@ -493,8 +550,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                         rope_get<V>(tab.c, ch.pa, Table::N, c);
                         rope_get<V>(tab.s, ch.pa, Table::N, s);
                     }
-                    rope_unpack<XT, V>(ring[slot].g[u][0][lane], ga);
-                    rope_unpack<XT, V>(ring[slot].g[u][1][lane], gb);
+                    rope_unpack<XT, V>(ring[slot].g[u][0][lane], p.ydt, ga);
+                    rope_unpack<XT, V>(ring[slot].g[u][1][lane], p.ydt, gb);
                     if (inter) {
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
@@ -523,8 +580,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                     }
                 }
                 float2 xa[H], xb[H];
-                rope_unpack<XT, V>(ring[slot].x[u][0][lane], xa);
-                rope_unpack<XT, V>(ring[slot].x[u][1][lane], xb);
+                rope_unpack<XT, V>(ring[slot].x[u][0][lane], p.xdt, xa);
+                rope_unpack<XT, V>(ring[slot].x[u][1][lane], p.xdt, xb);
                 const float rstd = ring[slot].rstd[u][lane], mean = LN ? ring[slot].mean[u][lane] : 0.f;
                 if (u == U - 1) load(slot);
                 float2 dot = f2s(0.f), sum = f2s(0.f);
@@ -551,7 +608,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 float v[LN ? 2 : 1];
                 v[0] = dot.x + dot.y;
                 if constexpr (LN) v[1] = sum.x + sum.y;
-                group_sum<L, LN ? 2 : 1>(v);
+                lanes.sum(v);
                 // dx = rstd g - rstd c1 - xhat (rstd c2)
                 const float2 c2 = f2s(-v[0] * inv * rstd), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv * rstd : 0.f);
 #pragma unroll
@@ -561,11 +618,11 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 }
                 const bool in = hl > u * G;
                 char *q = u == 0 ? y : y + u * ys;
-                if (in && ch.oka) rope_st(q + fa, rope_pack<XT, V>(ta).v);
-                if (in && ch.okb) rope_st(q + fb, rope_pack<XT, V>(tb).v);
+                if (in && ch.oka) rope_store<XT, V>(q + ch.a * xes, p.xdt, ta);
+                if (in && ch.okb) rope_store<XT, V>(q + ch.b * xes, p.xdt, tb);
             }
             if (!w.left) break;
-            if (turn) y = w.at(p, p.y[r], V * ES);
+            if (turn) y = w.at(p, p.y[r], V * xes);
             else y += U * ys;
         }
     }
@@ -573,15 +630,29 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     // the sums of the groups of lanes (the same columns) of a warp, then of the CTA's warps
     float *mine = rope_acc + warp * p.D;
     auto columns = [&](float2 (&u)[H], float2 (&v)[H]) {
+        if constexpr (RopeLanes<L>::POW2) {
 #pragma unroll
-        for (int o = L; o < 32; o <<= 1)
+            for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    u[i].x += __shfl_xor_sync(0xffffffffu, u[i].x, o);
+                    u[i].y += __shfl_xor_sync(0xffffffffu, u[i].y, o);
+                    v[i].x += __shfl_xor_sync(0xffffffffu, v[i].x, o);
+                    v[i].y += __shfl_xor_sync(0xffffffffu, v[i].y, o);
+                }
+        } else {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                u[i].x += __shfl_xor_sync(0xffffffffu, u[i].x, o);
-                u[i].y += __shfl_xor_sync(0xffffffffu, u[i].y, o);
-                v[i].x += __shfl_xor_sync(0xffffffffu, v[i].x, o);
-                v[i].y += __shfl_xor_sync(0xffffffffu, v[i].y, o);
+                const float2 a = u[i], b = v[i];
+#pragma unroll
+                for (int o = L; o < G * L; o += L) {
+                    u[i].x += __shfl_down_sync(0xffffffffu, a.x, o);
+                    u[i].y += __shfl_down_sync(0xffffffffu, a.y, o);
+                    v[i].x += __shfl_down_sync(0xffffffffu, b.x, o);
+                    v[i].y += __shfl_down_sync(0xffffffffu, b.y, o);
+                }
             }
+        }
         if (grp == 0) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
