@@ -15,6 +15,7 @@ axes these come first ([axes, tokens], [axes, batches, tokens]).
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -35,6 +36,7 @@ MAX_AXES = 4
 _HEADS = struct.Struct("8q").pack    # two gbnorm_heads_t
 _ROPE = struct.Struct("5q8i6q").pack  # gbnorm_rope_t
 _TWO = struct.Struct("2q").pack
+_CONTIGUOUS = torch.contiguous_format
 _POS_CODE = {torch.int32: 0, torch.int64: 1}
 
 
@@ -126,12 +128,12 @@ class _Call:
             raise ValueError(f"{name} must have unit stride in its last dimension")
         return t.data_ptr(), batch, token, head
 
-    def out(self, yq, yk, dtype):
+    def out(self, yq, yk, q, k, dtype):
         """The two outputs, allocated where they are not given."""
         if yq is None:
-            yq = torch.empty(self.q, dtype=dtype, device=self.dev)
-        if yk is None and self.k is not None:
-            yk = torch.empty(self.k, dtype=dtype, device=self.dev)
+            yq = torch.empty_like(q, dtype=dtype, memory_format=_CONTIGUOUS)
+        if yk is None and k is not None:
+            yk = torch.empty_like(k, dtype=dtype, memory_format=_CONTIGUOUS)
         return yq, yk
 
     def pair(self, name, q, k, dtype):
@@ -187,16 +189,13 @@ class _Call:
                      rotary.axes, code, 0, positions.data_ptr(), axis, batch, token, rotary.inv_freq.data_ptr(),
                      rotary._axis_at)
 
-    def on_device(self, fn, *args):
-        """fn(*args) with the tensors' device current."""
-        if self.dev == torch.cuda.current_device():
-            return fn(*args)
-        with torch.cuda.device(self.dev):
-            return fn(*args)
-
     def go(self, name, fn, *args):
         """fn(*args, stream) with the tensors' device current, on its current stream."""
-        status = self.on_device(fn, *args, _raw_stream(self.dev))
+        if self.dev == torch.cuda.current_device():
+            status = fn(*args, _raw_stream(self.dev))
+        else:
+            with torch.cuda.device(self.dev):
+                status = fn(*args, _raw_stream(self.dev))
         if status:
             _check(name, status)
 
@@ -208,10 +207,9 @@ def _param_dtype(default, *params):
     return default
 
 
-@_on_stream
 def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, positions=None,
                      rotary: Rotary | None = None, beta_q=None, beta_k=None, y_dtype=None, yq=None, yk=None, mean=None,
-                     rstd=None, save_stats: bool = True):
+                     rstd=None, save_stats: bool = True, stream=None):
     """Each head of the queries q and keys k (None: queries alone) normalised
     by itself (gamma, beta of D elements, None: 1, 0; all of one dtype), then
     rotated by its token's position (rotary None: the norm alone).  Returns
@@ -219,9 +217,12 @@ def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, pos
     shapes; mean and rstd float32 [..., heads of q and of k], mean None for
     RMSNorm, both None without save_stats unless given.  yq may be q itself
     and yk k itself."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope_fwd)(is_layernorm, q, k, gamma_q, gamma_k, eps, positions, rotary, beta_q,
+                                            beta_k, y_dtype, yq, yk, mean, rstd, save_stats, stream=stream)
     c = _Call("", q, k)
     dt = yq.dtype if yq is not None else y_dtype or q.dtype
-    yq, yk = c.out(yq, yk, dt)
+    yq, yk = c.out(yq, yk, q, k, dt)
     stats = c.stats_shape()
     if save_stats:
         if rstd is None:
@@ -242,17 +243,30 @@ def qk_norm_rope_bwd_workspace_size(is_layernorm: bool, tokens: int, heads_q: in
     return int(lib.qk_norm_rope_bwd_workspace_size(int(bool(is_layernorm)), tokens, heads_q, heads_k, dim))
 
 
-@_on_stream
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(ln, tokens, heads_q, heads_k, dim, dev):
+    """A function of the shape and the device alone."""
+    with torch.cuda.device(dev):
+        need = lib.qk_norm_rope_bwd_workspace_size(ln, tokens, heads_q, heads_k, dim)
+    if need == 0:
+        raise GbnormError("qk_norm_rope_bwd_workspace_size", 2)
+    return need
+
+
 def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean, rstd, positions=None,
                      rotary: Rotary | None = None, dq=None, dk=None, dgamma=None, dbeta=None, workspace=None,
-                     need_dgamma: bool = True, need_dbeta: bool = True):
+                     need_dgamma: bool = True, need_dbeta: bool = True, stream=None):
     """Backward of qk_norm_rope_fwd from its inputs q and k and its saved
     statistics.  Returns (dq, dk, dgamma, dbeta): dq and dk of q's dtype, dgamma
     and dbeta float32 [2, D] (queries, keys; [1, D] without keys), None where not
     needed, dbeta LayerNorm only.  dq may be dyq itself and dk dyk itself."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope_bwd)(is_layernorm, dyq, dyk, q, k, gamma_q, gamma_k, mean, rstd, positions,
+                                            rotary, dq, dk, dgamma, dbeta, workspace, need_dgamma, need_dbeta,
+                                            stream=stream)
     c = _Call("", q, k)
     dt = q.dtype
-    dq, dk = c.out(dq, dk, dt)
+    dq, dk = c.out(dq, dk, q, k, dt)
     sums, stats = (2 if c.hk else 1, c.D), c.stats_shape()
     if dgamma is None and need_dgamma:
         dgamma = torch.empty(sums, dtype=torch.float32, device=c.dev)
@@ -263,10 +277,8 @@ def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean,
     if rstd is None or (is_layernorm and mean is None):
         raise ValueError("rstd (and mean for LayerNorm) of the forward are needed")
     if workspace is None:
-        need = c.on_device(lib.qk_norm_rope_bwd_workspace_size, int(bool(is_layernorm)), c.B * c.S, c.hq, c.hk, c.D)
-        if need == 0:
-            raise GbnormError("qk_norm_rope_bwd_workspace_size", 2)
-        workspace = torch.empty(need, dtype=torch.uint8, device=c.dev)
+        workspace = torch.empty(_workspace_bytes(int(bool(is_layernorm)), c.B * c.S, c.hq, c.hk, c.D, c.dev),
+                                dtype=torch.uint8, device=c.dev)
     elif not workspace.is_contiguous() or workspace.get_device() != c.dev:
         raise ValueError(f"workspace must be contiguous on device {c.dev}")
     pdt = _param_dtype(dt, gamma_q, gamma_k)
@@ -278,30 +290,32 @@ def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean,
     return dq, dk, dgamma, dbeta
 
 
-@_on_stream
-def rope_fwd(q, k, positions, rotary: Rotary, y_dtype=None, yq=None, yk=None):
+def rope_fwd(q, k, positions, rotary: Rotary, y_dtype=None, yq=None, yk=None, stream=None):
     """The heads of q and k (None: of q alone) rotated by their tokens'
     positions.  Returns (yq, yk) of y_dtype (default q's); yq may be q itself
     and yk k itself."""
+    if stream is not None:
+        return _on_stream(rope_fwd)(q, k, positions, rotary, y_dtype, yq, yk, stream=stream)
     c = _Call("", q, k)
     dt = yq.dtype if yq is not None else y_dtype or q.dtype
     if rotary is None:
         raise ValueError("rotary is needed")
-    yq, yk = c.out(yq, yk, dt)
+    yq, yk = c.out(yq, yk, q, k, dt)
     c.go("rope_fwd", lib.rope_fwd, c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k, q.dtype),
          c.heads("y", yq, yk, dt))
     return yq, yk
 
 
-@_on_stream
-def rope_bwd(dyq, dyk, positions, rotary: Rotary, dx_dtype=None, dq=None, dk=None):
+def rope_bwd(dyq, dyk, positions, rotary: Rotary, dx_dtype=None, dq=None, dk=None, stream=None):
     """Backward of rope_fwd: gradients turned back.  Returns (dq, dk) of
     dx_dtype (default dyq's); dq may be dyq itself and dk dyk itself."""
+    if stream is not None:
+        return _on_stream(rope_bwd)(dyq, dyk, positions, rotary, dx_dtype, dq, dk, stream=stream)
     c = _Call("dy", dyq, dyk)
     dt = dq.dtype if dq is not None else dx_dtype or dyq.dtype
     if rotary is None:
         raise ValueError("rotary is needed")
-    dq, dk = c.out(dq, dk, dt)
+    dq, dk = c.out(dq, dk, dyq, dyk, dt)
     c.go("rope_bwd", lib.rope_bwd, c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype),
          c.heads("dy", dyq, dyk, dyq.dtype), c.heads("d", dq, dk, dt))
     return dq, dk
