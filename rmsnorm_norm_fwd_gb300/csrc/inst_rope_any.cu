@@ -2,12 +2,9 @@
 #include "rope_any_kernels.cuh"
 
 namespace gbn {
-#define GBN_FWD(MODE) \
-    {(const void *)&rope_fwd_any<MODE, 1>, (const void *)&rope_fwd_any<MODE, 2>, (const void *)&rope_fwd_any<MODE, 4>, \
-     (const void *)&rope_fwd_any<MODE, 8>, (const void *)&rope_fwd_any<MODE, 16>}
-#define GBN_BWD(LN) \
-    {(const void *)&rope_bwd_any<LN, 1>, (const void *)&rope_bwd_any<LN, 2>, (const void *)&rope_bwd_any<LN, 4>, \
-     (const void *)&rope_bwd_any<LN, 8>, (const void *)&rope_bwd_any<LN, 16>}
-const void *const kRopeFwdAny[3][kRopeAnySizes] = {GBN_FWD(kRopeOnly), GBN_FWD(kRopeRms), GBN_FWD(kRopeLn)};
-const void *const kRopeBwdAny[2][kRopeAnySizes] = {GBN_BWD(false), GBN_BWD(true)};
+#define GBN_K(F, M, L, C, B) {(const void *)&F<M, L, C, B>, "any" #L "x" #C, (int)sizeof(RopeAnySmem<L, C>), 1, L}
+#define GBN_SIZES(F, M) {GBN_K(F, M, 4, 8, 2), GBN_K(F, M, 8, 8, 2), GBN_K(F, M, 16, 8, 2), GBN_K(F, M, 32, 8, 2), GBN_K(F, M, 32, 16, 1)}
+const RopeVariant kRopeFwdAny[3][kRopeAnySizes] = {GBN_SIZES(rope_fwd_any, kRopeOnly), GBN_SIZES(rope_fwd_any, kRopeRms),
+                                                   GBN_SIZES(rope_fwd_any, kRopeLn)};
+const RopeVariant kRopeBwdAny[2][kRopeAnySizes] = {GBN_SIZES(rope_bwd_any, false), GBN_SIZES(rope_bwd_any, true)};
 }  // namespace gbn

@@ -258,10 +258,10 @@ struct Kernel {
     bool tokens;  // a warp takes queries and keys of its tokens (RopeTokens), else of one tensor (RopeWalk)
 };
 
-int any_size(int64_t D, int rot) {  // log2 of the pairs a lane holds
-    const int64_t pairs = rot / 2 + (D - rot + 1) / 2;
+int any_size(int D, int rot) {  // 32 << that pairs hold a head
+    const int pairs = rot / 2 + (D - rot + 1) / 2;
     int lg = 0;
-    while (((int64_t)32 << lg) < pairs) ++lg;
+    while (32 << lg < pairs) ++lg;
     return lg;
 }
 
@@ -317,8 +317,8 @@ Kernel pick(int mode, RopeParams &p) {
             }
     }
     const int n = any_size(p.D, p.rot), slot = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
-    return mode < 0 ? Kernel{kRopeBwdAny[-1 - mode][n], "any", 1, kRopeWarps * p.D * 4, slot, false}
-                    : Kernel{kRopeFwdAny[mode][n], "any", 1, 0, slot, false};
+    const RopeVariant &k = mode < 0 ? kRopeBwdAny[-1 - mode][n] : kRopeFwdAny[mode][n];
+    return {k.f, k.name, 32 / k.lanes, k.smem + (mode < 0 ? kRopeWarps * p.D * 4 : 0), slot, mode >= 0};
 }
 constexpr int kSlots = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + 5 * kRopeAnySizes;
 std::atomic<int> g_resident[kHostMaxDev][kSlots];
@@ -328,9 +328,9 @@ int resident(const Kernel &k, const HostDevice &d, int *out) {
     std::atomic<int> &c = g_resident[d.dev][k.slot];
     int o = c.load(std::memory_order_relaxed);
     if (o == 0) {
-        // heads of up to 512 elements share a slot: allow for the parameters of any
+        // heads of several sizes share a kernel: allow for the parameters (8 KB) or column sums (32 KB) of any
         if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 std::max(k.smem + 8192, 48 * 1024)) != cudaSuccess ||
+                                 std::max(k.smem, 16 * 1024) + 32 * 1024) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k.f, kRopeCTA, (size_t)k.smem) != cudaSuccess)
             return GBNORM_ERR_CUDA;
         if (o <= 0) return GBNORM_ERR_UNSUPPORTED;

@@ -54,82 +54,17 @@ __device__ __forceinline__ void rope_sincos(uint64_t u, float sign, float *c, fl
     *s = sn * sign;
 }
 
-// The pairs whose angles a lane computes: lane, lane + 32, ... (N of them).
-template <int N> struct RopeAngles {
-    uint64_t f[N];
-    uint32_t axis, bad;  // two bits and one bit a pair
-    __device__ __forceinline__ void init(const RopeParams &p, int lane) {
-        axis = bad = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int j = lane + 32 * i;
-            f[i] = 0;
-            if (2 * j >= p.rot) continue;
-            bool b;
-            f[i] = rope_turns(__ldg(p.inv_freq + j), &b);
-            axis |= rope_axis(p, j) << (2 * i);
-            bad |= (uint32_t)b << i;
-        }
-    }
-    // cos and sin of pair lane + 32 i at the token whose axis-0 position has index `at`.
-    __device__ __forceinline__ void get(const RopeParams &p, int64_t at, int i, float *c, float *s) const {
-        const int64_t q = at + (int64_t)((axis >> (2 * i)) & 3u) * p.pos_axis;
-        const int64_t pos = p.pos64 ? __ldg(static_cast<const long long *>(p.pos) + q)
-                                    : (int64_t)__ldg(static_cast<const int *>(p.pos) + q);
-        rope_sincos((uint64_t)pos * f[i], p.sign, c, s);
-        if ((bad >> i) & 1u) *s = *c = __int_as_float(0x7fffffff);
-    }
-};
-
 // a / n of numbers that mostly fit 32 bits (a division in 64 is some hundred instructions).
 __device__ __forceinline__ int64_t rope_div(int64_t a, int64_t n) {
     return ((a | n) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)n) : a / n;
 }
 
-// A warp's share of the passes over one of the two tensors: contiguous, so
-// that the angles of a token serve all its heads.
-struct RopeWalk {
-    int left;   // passes to go, this one included
-    int b, s;   // token
-    int blk;    // pass within the token
-    int r;      // 0 queries, 1 keys
-    __device__ __forceinline__ RopeWalk(const RopeParams &p) {
-        int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-        r = w >= p.warps[0];
-        if (r) w -= p.warps[0];
-        const int64_t W = p.warps[r], U = p.units[r];
-        left = b = s = blk = 0;
-        if (w >= W) return;
-        const int64_t each = rope_div(U, W), more = U - each * W, u = each * w + (w < more ? w : more);
-        left = (int)(each + (w < more ? 1 : 0));
-        const int64_t t = rope_div(u, p.passes[r]);
-        blk = (int)(u - t * p.passes[r]);
-        b = (int)rope_div(t, p.S);
-        s = (int)(t - b * p.S);
-    }
-    // To the next pass; true if it belongs to another token.
-    __device__ __forceinline__ bool next(const RopeParams &p) {
-        --left;
-        if (++blk < p.passes[r]) return false;
-        blk = 0;
-        if (++s == (int)p.S) {
-            s = 0;
-            ++b;
-        }
-        return true;
-    }
-    __device__ __forceinline__ int64_t at(const RopeHeads &h) const { return b * h.batch + s * h.token; }
-    // Index of the token's first statistic of this tensor.
-    __device__ __forceinline__ int64_t stat(const RopeParams &p) const {
-        return (b * p.S + s) * (p.heads[0] + p.heads[1]) + (r ? p.heads[0] : 0);
-    }
-};
-
-// The same for kernels on vectors, whose passes take GU heads, lane group `grp`
-// one of them (and every 32 / L-th).  BOTH: over the tokens, each with its
-// queries' heads and then its keys', so that both take the token's angles (units
-// and warps of index 0 count both); else over one tensor.  Passes over one
-// tensor of a token are a segment: within one a step is an addition.
+// A warp's share of the passes.  A pass takes GU heads, lane group `grp` one of
+// them (and every 32 / L-th).  BOTH: over the tokens, each with its queries'
+// heads and then its keys', so that both take the token's angles (units and warps
+// of index 0 count both); else over one tensor, which the backward's column sums
+// belong to.  Passes over one tensor of a token are a segment: within one a step
+// is an addition.
 //
 // A warp takes every W-th token as long as all W warps have one, so that the
 // grid moves through memory as a front, and then its share of the passes over

@@ -50,10 +50,18 @@ struct RopeParams {
 
 enum RopeMode : int { kRopeOnly = 0, kRopeRms = 1, kRopeLn = 2 };
 
-// Element by element, any alignment, stride, type and size: [mode][log2 of pairs a lane].
+struct RopeVariant {
+    const void *f;
+    const char *name;
+    int smem;  // without parameters (vectors) or column sums (element by element)
+    int u;     // heads a lane and pass
+    int lanes; // a head
+};
+
+// Element by element, any alignment, strides, types and size: [mode][by pairs a head: 32, 64, 128, 256, 512].
 constexpr int kRopeAnySizes = 5;
-extern const void *const kRopeFwdAny[3][kRopeAnySizes];
-extern const void *const kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
+extern const RopeVariant kRopeFwdAny[3][kRopeAnySizes];
+extern const RopeVariant kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 
 // On vectors of v elements and `vector` bytes, l lanes a head, u heads a lane and
 // pass: passes in flight a warp, and dynamic shared memory without the
@@ -67,13 +75,6 @@ constexpr int rope_bwd_smem(int vector, int v, int l, int u) {
     return kRopeWarps * (kRopeBwdDepth * u * (128 * vector + 256) + 8 * v * l) + 12 * v * l;
 }
 
-struct RopeVariant {
-    const void *f;
-    const char *name;
-    int smem;  // without parameters
-    int u;     // heads a lane and pass
-    int lanes; // a head
-};
 constexpr int kRopeVecLanes = 8;
 constexpr int kRopeLaneCounts[kRopeVecLanes] = {4, 5, 6, 8, 9, 10, 16, 32};  // lanes a head
 constexpr int kRopeVecKinds = 3;  // RopeKind
