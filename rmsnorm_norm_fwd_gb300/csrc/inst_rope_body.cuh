@@ -1,5 +1,5 @@
-// Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V, the
-// type and elements of a vector.  Defines kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE 2 (16-byte vectors): whole
+// Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V, GBN_C, the
+// type and elements of a vector and the vectors of half a lane's elements.  Defines kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE 2 (16-byte vectors): whole
 // heads rotated as halves or as neighbours have kernels of their own up to 16 lanes, where they measured faster; 1, 0:
 // all run on the kernels for any rotation, and on fewer numbers of lanes.
 #include "rope_vec_kernels.cuh"
@@ -12,12 +12,12 @@
 #endif
 #if GBN_MODE >= 0
 #define GBN_K(L, KIND, S) \
-    {(const void *)&rope_fwd_vec<GBN_MODE, GBN_XT, GBN_V, L, KIND, GBN_FU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_fwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_V, L, GBN_FU(KIND)), GBN_FU(KIND), L}
+    {(const void *)&rope_fwd_vec<GBN_MODE, GBN_XT, GBN_V, GBN_C, L, KIND, GBN_FU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
+     rope_fwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_C, GBN_C * GBN_V, L, GBN_FU(KIND)), GBN_FU(KIND), L}
 #else
 #define GBN_K(L, KIND, S) \
-    {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, L, KIND, GBN_BU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_bwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_V, L, GBN_BU(KIND)), GBN_BU(KIND), L}
+    {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, GBN_C, L, KIND, GBN_BU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
+     rope_bwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_C, GBN_C * GBN_V, L, GBN_BU(KIND)), GBN_BU(KIND), L}
 #endif
 #define GBN_FU(KIND) (GBN_MODE == 0 && KIND != kRopeSome ? 2 : 1)
 #define GBN_BU(KIND) 1
@@ -25,7 +25,7 @@
 #if GBN_WHOLE == 2
 #define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(6), GBN_ANY(8), GBN_ANY(9), GBN_ANY(10), GBN_ANY(16), GBN_ANY(32)}
 #elif GBN_WHOLE == 1
-#define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(8), GBN_ANY(8), GBN_ANY(9), GBN_ANY(16), GBN_ANY(16), GBN_ANY(32)}
+#define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(6), GBN_ANY(8), GBN_ANY(10), GBN_ANY(10), GBN_ANY(16), GBN_ANY(32)}
 #else
 #define GBN_SOME {GBN_ANY(4), GBN_ANY(8), GBN_ANY(8), GBN_ANY(8), GBN_ANY(16), GBN_ANY(16), GBN_ANY(16), GBN_ANY(32)}
 #endif
@@ -51,5 +51,6 @@ const RopeVariant GBN_CAT(kRopeVec_, GBN_NAME)[kRopeVecKinds][kRopeVecLanes] = {
 #undef GBN_MODE
 #undef GBN_XT
 #undef GBN_V
+#undef GBN_C
 #undef GBN_WHOLE
 #undef GBN_NAME

@@ -265,7 +265,7 @@ int any_size(int D, int rot) {  // 32 << that pairs hold a head
     return lg;
 }
 
-constexpr int kVecTypes = 6;  // fp32, fp16, bf16 by four, fp16, bf16 by eight, differing types
+constexpr int kVecTypes = 9;  // fp32, fp16, bf16 by two, by four, differing types by four, fp16, bf16 by eight
 
 // Elements of the vectors that all tensors of a call move as: every head and
 // chunk starts on a vector, the rotated part holds whole ones.  0: none.
@@ -275,7 +275,7 @@ int vector_of(const RopeParams &p, bool back) {
         const RopeHeads *t;
         int es;
     } all[3] = {{p.x, xs}, {p.y, back ? xs : ys}, {back ? p.g : p.x, back ? ys : xs}};
-    for (int v = p.xdt == p.ydt && xs == 2 ? 8 : 4; v >= 4; v /= 2) {
+    for (int v = p.xdt == p.ydt && xs == 2 ? 8 : 4; v >= (p.xdt == p.ydt ? 2 : 4); v /= 2) {
         bool ok = p.D % v == 0 && (p.inter ? p.rot % v : p.rot / 2 % v) == 0;
         for (const auto &a : all)
             for (int i = 0; i < 2; ++i) {
@@ -291,8 +291,8 @@ int vector_of(const RopeParams &p, bool back) {
 // mode: a RopeMode, or -1 - is_layernorm for the backward.  Strides become those of the kernel's kind.
 Kernel pick(int mode, RopeParams &p) {
 #define GBN_T(M) \
-    {kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, kRopeVec_##M##_bf16v4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8, \
-     kRopeVec_##M##_mixv4}
+    {kRopeVec_##M##_f32v2, kRopeVec_##M##_f16v2, kRopeVec_##M##_bf16v2, kRopeVec_##M##_f32v4, kRopeVec_##M##_f16v4, \
+     kRopeVec_##M##_bf16v4, kRopeVec_##M##_mixv4, kRopeVec_##M##_f16v8, kRopeVec_##M##_bf16v8}
     static const RopeVariant(*const tables[5][kVecTypes])[kRopeVecLanes] = {GBN_T(rot), GBN_T(rms), GBN_T(ln),
                                                                             GBN_T(brms), GBN_T(bln)};
 #undef GBN_T
@@ -301,9 +301,10 @@ Kernel pick(int mode, RopeParams &p) {
         const int chunks = p.D / v, rot = p.rot / v;
         const int slots = p.inter ? (chunks + 1) / 2 : rot / 2 + (chunks - rot + 1) / 2;
         const int kind = p.rot < p.D ? kRopeVecKinds - 1 : p.inter;
+        const int t = p.xdt != p.ydt ? 6 : p.xdt + (v == 2 ? 0 : v == 4 ? 3 : 6);
+        const int c = p.xdt == p.ydt && p.xdt == GBNORM_F32 ? 4 / v : 8 / v;  // slots a lane
         for (int l = 0; l < kRopeVecLanes; ++l)
-            if (slots <= kRopeLaneCounts[l]) {
-                const int t = p.xdt != p.ydt ? kVecTypes - 1 : p.xdt + (v == 8 ? 2 : 0);
+            if (slots <= kRopeLaneCounts[l] * c) {
                 const RopeVariant &k = tables[m][t][kind][l];
                 for (RopeHeads *h : {p.x, p.y, p.g})
                     for (int i = 0; i < 2; ++i) {

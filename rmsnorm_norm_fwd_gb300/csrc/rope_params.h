@@ -63,16 +63,16 @@ constexpr int kRopeAnySizes = 5;
 extern const RopeVariant kRopeFwdAny[3][kRopeAnySizes];
 extern const RopeVariant kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 
-// On vectors of v elements and `vector` bytes, l lanes a head, u heads a lane and
-// pass: passes in flight a warp, and dynamic shared memory without the
-// parameters (rings, tables of cosines and sines, frequencies; the backward's column sums
-// take the place of the rings).
+// On vectors of `vector` bytes, c of them for each half of a lane's 2 * half
+// elements, l lanes a head, u heads a lane and pass: passes in flight a warp, and
+// dynamic shared memory without the parameters (rings, tables of cosines and
+// sines, frequencies; the backward's column sums take the place of the rings).
 constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
-constexpr int rope_fwd_smem(int vector, int v, int l, int u) {
-    return kRopeWarps * (kRopeFwdDepth * u * 64 * vector + 8 * v * l) + 12 * v * l;
+constexpr int rope_fwd_smem(int vector, int c, int half, int l, int u) {
+    return kRopeWarps * (kRopeFwdDepth * u * 64 * c * vector + 8 * half * l) + 12 * half * l;
 }
-constexpr int rope_bwd_smem(int vector, int v, int l, int u) {
-    return kRopeWarps * (kRopeBwdDepth * u * (128 * vector + 256) + 8 * v * l) + 12 * v * l;
+constexpr int rope_bwd_smem(int vector, int c, int half, int l, int u) {
+    return kRopeWarps * (kRopeBwdDepth * u * (128 * c * vector + 256) + 8 * half * l) + 12 * half * l;
 }
 
 constexpr int kRopeVecLanes = 8;
@@ -82,8 +82,9 @@ constexpr int kRopeVecKinds = 3;  // RopeKind
 #define GBN_ROPE_VEC(M) \
     extern const RopeVariant kRopeVec_##M##_bf16v8[kRopeVecKinds][kRopeVecLanes], \
         kRopeVec_##M##_f16v8[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_bf16v4[kRopeVecKinds][kRopeVecLanes], \
-        kRopeVec_##M##_f16v4[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_f32v4[kRopeVecKinds][kRopeVecLanes], \
-        kRopeVec_##M##_mixv4[kRopeVecKinds][kRopeVecLanes]
+        kRopeVec_##M##_f16v4[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_bf16v2[kRopeVecKinds][kRopeVecLanes], \
+        kRopeVec_##M##_f16v2[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_f32v4[kRopeVecKinds][kRopeVecLanes], \
+        kRopeVec_##M##_f32v2[kRopeVecKinds][kRopeVecLanes], kRopeVec_##M##_mixv4[kRopeVecKinds][kRopeVecLanes]
 GBN_ROPE_VEC(rot);
 GBN_ROPE_VEC(rms);
 GBN_ROPE_VEC(ln);

@@ -1,7 +1,8 @@
 // rope_vec_kernels.cuh -- the head operators on vectors.
 //
-// A group of L lanes holds one head, 32 / L heads a warp and pass; a lane holds
-// two chunks of V consecutive elements, one 8- or 16-byte vector each.  Where
+// A group of L lanes holds one head, 32 / L heads a warp and pass; a lane holds C
+// times two chunks of V consecutive elements, each moved as one vector of 4, 8 or
+// 16 bytes (C V = 8 for 16-bit types, so that a lane has 16 elements).  Where
 // pair j is (j, j + rot / 2) the two chunks are partners (j..j+V-1 and the same
 // behind rot / 2), where pairs are neighbours every chunk holds whole pairs; so
 // the rotation needs no exchange, and a row sum is log2 L shuffles.
@@ -25,6 +26,9 @@ template <> struct RopeRaw<kF16, 8> { uint4 v; };
 template <> struct RopeRaw<kBF16, 8> { uint4 v; };
 template <> struct RopeRaw<kF16, 4> { uint2 v; };
 template <> struct RopeRaw<kBF16, 4> { uint2 v; };
+template <> struct RopeRaw<kF32, 2> { uint2 v; };
+template <> struct RopeRaw<kF16, 2> { uint32_t v; };
+template <> struct RopeRaw<kBF16, 2> { uint32_t v; };
 // Types that differ within a call, read from it: 16 bytes hold four elements of any.
 constexpr int kMixed = 3;
 template <> struct RopeRaw<kMixed, 4> { uint4 v; };
@@ -44,8 +48,11 @@ template <int XT> __device__ __forceinline__ uint32_t rope_word(float2 f) {
     }
 }
 template <int XT, int V>
-__device__ __forceinline__ void rope_unpack(const RopeRaw<XT, V> &r, int dt, float2 (&f)[V / 2]) {
-    if constexpr (XT == kMixed) {
+__device__ __forceinline__ void rope_unpack(const RopeRaw<XT, V> &r, int dt, float2 *f) {
+    if constexpr (V == 2) {
+        if constexpr (XT == kF32) f[0] = make_float2(__uint_as_float(r.v.x), __uint_as_float(r.v.y));
+        else f[0] = rope_pair<XT>(r.v);
+    } else if constexpr (XT == kMixed) {
         if (dt == kF32) {
             f[0] = make_float2(__uint_as_float(r.v.x), __uint_as_float(r.v.y));
             f[1] = make_float2(__uint_as_float(r.v.z), __uint_as_float(r.v.w));
@@ -69,8 +76,11 @@ __device__ __forceinline__ void rope_unpack(const RopeRaw<XT, V> &r, int dt, flo
     }
 }
 // V elements rounded to their type and stored.
-template <int XT, int V> __device__ __forceinline__ void rope_store(char *p, int dt, const float2 (&f)[V / 2]) {
-    if (XT == kF32 || (XT == kMixed && dt == kF32)) {
+template <int XT, int V> __device__ __forceinline__ void rope_store(char *p, int dt, const float2 *f) {
+    if constexpr (V == 2) {
+        if constexpr (XT == kF32) *reinterpret_cast<float2 *>(p) = f[0];
+        else *reinterpret_cast<uint32_t *>(p) = rope_word<XT>(f[0]);
+    } else if (XT == kF32 || (XT == kMixed && dt == kF32)) {
         *reinterpret_cast<float4 *>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
     } else if constexpr (V == 8) {
         *reinterpret_cast<uint4 *>(p) =
@@ -93,8 +103,12 @@ template <int BYTES> __device__ __forceinline__ void rope_cp_bytes(void *to, con
                      : "memory");
 }
 template <int XT, int V> __device__ __forceinline__ void rope_cp(RopeRaw<XT, V> *to, const char *from, bool in, int dt) {
-    if (XT == kF32 || V == 8 || (XT == kMixed && dt == kF32)) rope_cp_bytes<16>(to, from, in);
-    else rope_cp_bytes<8>(to, from, in);
+    if constexpr (XT == kMixed) {
+        if (dt == kF32) rope_cp_bytes<16>(to, from, in);
+        else rope_cp_bytes<8>(to, from, in);
+    } else {
+        rope_cp_bytes<(int)sizeof(RopeRaw<XT, V>)>(to, from, in);
+    }
 }
 __device__ __forceinline__ void rope_cp_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void rope_cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -110,12 +124,16 @@ template <int V> __device__ __forceinline__ void rope_param(float *to, const voi
     for (int c = threadIdx.x; c < D; c += kRopeCTA) to[rope_place<V>(c, D)] = row ? ld1(row, c, dt) : none;
 }
 // The V values from e (a multiple of V) on, of n.
-template <int V> __device__ __forceinline__ void rope_get(const float *from, int e, int n, float2 (&f)[V / 2]) {
+template <int V> __device__ __forceinline__ void rope_get(const float *from, int e, int n, float2 *f) {
+    if constexpr (V == 2) {
+        f[0] = *reinterpret_cast<const float2 *>(from + e);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4 *>(from + e / (V / 4) + i * (n / 2));
-        f[2 * i] = make_float2(v.x, v.y);
-        f[2 * i + 1] = make_float2(v.z, v.w);
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(from + e / (V / 4) + i * (n / 2));
+            f[2 * i] = make_float2(v.x, v.y);
+            f[2 * i + 1] = make_float2(v.z, v.w);
+        }
     }
 }
 
@@ -123,38 +141,35 @@ template <int V> __device__ __forceinline__ void rope_get(const float *from, int
 // halves or as neighbours, or anything (read from the call, through selects).
 enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopeSome = 2 };
 
-// The two chunks of a lane: first elements, whether they are there, whether they are rotated, and their first pair.
-template <int V, int L, int KIND> struct RopeChunks {
-    int a, b, pa, pb;
-    bool oka, okb, ra, rb;
+// The chunks of a lane: first elements, whether they are there, whether they are rotated.  Slot i of lane sl is number
+// i L + sl of the head.
+template <int V, int C, int L, int KIND> struct RopeChunks {
+    int a[C], b[C];
+    bool oka[C], okb[C], ra[C], rb[C];
     __device__ __forceinline__ RopeChunks(const RopeParams &p, int sl, bool used) {
         const int n = p.D / V, nr = p.rot / V;
-        int ca, cb;
-        if (KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter)) {
-            const int ns = (n + 1) / 2;
-            ca = sl;
-            cb = ns + sl;
-            oka = sl < ns;
-            okb = oka && cb < n;
-            pa = ca * (V / 2);
-            pb = cb * (V / 2);
-        } else {
-            const int half = nr / 2;
-            const int rest = (n - nr + 1) / 2;
-            ca = sl < half ? sl : nr + (sl - half);
-            cb = sl < half ? sl + half : ca + rest;
-            oka = sl < half + rest;
-            okb = oka && cb < n;
-            pa = pb = sl * V;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int j = i * L + sl;
+            int ca, cb;
+            if (KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter)) {
+                const int ns = (n + 1) / 2;
+                ca = j;
+                cb = ns + j;
+                oka[i] = j < ns;
+            } else {
+                const int half = nr / 2, rest = (n - nr + 1) / 2;
+                ca = j < half ? j : nr + (j - half);
+                cb = j < half ? j + half : ca + rest;
+                oka[i] = j < half + rest;
+            }
+            oka[i] = oka[i] && used;
+            okb[i] = oka[i] && cb < n;
+            ra[i] = oka[i] && ca < nr;
+            rb[i] = okb[i] && cb < nr;
+            a[i] = oka[i] ? ca * V : 0;  // lanes without a chunk stay inside the head
+            b[i] = okb[i] ? cb * V : 0;
         }
-        a = ca * V;
-        b = cb * V;
-        oka = oka && used;
-        okb = okb && used;
-        ra = oka && ca < nr;
-        rb = okb && cb < nr;
-        if (!oka) a = 0;  // lanes without a chunk stay inside the head
-        if (!okb) b = 0;
     }
 };
 
@@ -197,8 +212,7 @@ template <int L> struct RopeLanes {
 };
 
 // The frequencies of a call in turns, once a CTA.
-template <int V, int L> struct RopeTurns {
-    static constexpr int N = V * L;
+template <int N> struct RopeTurns {
     static_assert(N <= kRopeCTA, "a pair a thread");
     uint64_t f[N];
     float bad[N];  // 0, or NaN where the frequency is not a number of turns
@@ -212,8 +226,8 @@ template <int V, int L> struct RopeTurns {
 };
 // A warp's cosines and sines: written by the lane that computed the pair, read by those whose chunks hold it.
 // As halves, a chunk's V pairs are read at once, and lie as rope_place says.
-template <int V, int L> struct RopeTable {
-    static constexpr int N = V * L, PER = (N + 31) / 32;
+template <int V, int N> struct RopeTable {
+    static constexpr int PER = (N + 31) / 32;
     float c[N], s[N];
     // Behind the rotated pairs: cosine 1 and sine 0, for the chunks that are not.
     __device__ __forceinline__ void ones(int lane, int rot, bool inter) {
@@ -224,7 +238,7 @@ template <int V, int L> struct RopeTable {
         }
     }
     // pos: lane a holds the position on axis a; axis: two bits for each of the lane's pairs lane, lane + 32, ...
-    __device__ __forceinline__ void put(const RopeTurns<V, L> &turns, const RopeParams &p, int64_t pos, uint32_t axis,
+    __device__ __forceinline__ void put(const RopeTurns<N> &turns, const RopeParams &p, int64_t pos, uint32_t axis,
                                         int lane, bool inter) {
         __syncwarp();  // the last token's have been read
 #pragma unroll
@@ -261,23 +275,23 @@ constexpr int kRopeNoHead = 1 << 20;  // the group of lanes beyond the last whol
 
 __device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x); }
 
-template <int MODE, int XT, int V, int L, int KIND, int U, int MINB>
+template <int MODE, int XT, int V, int C, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_constant__ RopeParams p) {
-    constexpr int G = 32 / L, H = V / 2, DEPTH = kRopeFwdDepth;
-    using Table = RopeTable<V, L>;
+    constexpr int G = 32 / L, HV = V / 2, H = C * HV, N = C * V * L, DEPTH = kRopeFwdDepth;
+    using Table = RopeTable<V, N>;
     using Raw = RopeRaw<XT, V>;
     // rings, tables, frequencies, then gamma (and beta) of the queries and of the keys
     extern __shared__ __align__(16) unsigned char rope_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const RopeLanes<L> lanes(lane);
     const int sl = lanes.sl, grp = lane < G * L ? lane / L : kRopeNoHead;
-    Raw(*ring)[U][2][32] = reinterpret_cast<Raw(*)[U][2][32]>(rope_smem) + warp * DEPTH;
-    Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * U * DEPTH * kRopeWarps);
-    RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
+    Raw(*ring)[U][2 * C][32] = reinterpret_cast<Raw(*)[U][2 * C][32]>(rope_smem) + warp * DEPTH;
+    Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Raw) * 64 * C * U * DEPTH * kRopeWarps);
+    RopeTurns<N> &turns = *reinterpret_cast<RopeTurns<N> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1);
     Table &tab = tables[warp];
     RopeCursor<G * U, true> w(p, grp), ahead = w;  // the pass worked on, the pass to load
-    const RopeChunks<V, L, KIND> ch(p, sl, lane < G * L);
+    const RopeChunks<V, C, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     const int xes = rope_esize<XT>(p.xdt), yes = rope_esize<XT>(p.ydt);
     const char *x = ahead.at(p, p.x[ahead.r], V * xes);
@@ -288,8 +302,11 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
             for (int u = 0; u < U; ++u) {
                 // a lane without a head in the pass reads another, and stores nothing
                 const char *q = u == 0 ? x : x + (ahead.hl > u * G ? u * xs : 0);
-                rope_cp(&ring[slot][u][0][lane], q + ch.a * xes, ch.oka, p.xdt);
-                rope_cp(&ring[slot][u][1][lane], q + ch.b * xes, ch.okb, p.xdt);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    rope_cp(&ring[slot][u][2 * i][lane], q + ch.a[i] * xes, ch.oka[i], p.xdt);
+                    rope_cp(&ring[slot][u][2 * i + 1][lane], q + ch.b[i] * xes, ch.okb[i], p.xdt);
+                }
             }
             if (ahead.next(p, grp)) {
                 x = ahead.at(p, p.x[ahead.r], V * xes);
@@ -325,39 +342,39 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
         if (turn == 2) tab.put(turns, p, pos, axis, lane, inter);
         if (turn) {
             float2 ga[H], gb[H];
-            if constexpr (MODE != kRopeOnly) {
-                rope_get<V>(par + r * p.D, ch.a, p.D, ga);
-                rope_get<V>(par + r * p.D, ch.b, p.D, gb);
-            } else {
 #pragma unroll
-                for (int i = 0; i < H; ++i) ga[i] = gb[i] = f2s(1.f);
+            for (int i = 0; i < C; ++i) {
+                if constexpr (MODE != kRopeOnly) {
+                    rope_get<V>(par + r * p.D, ch.a[i], p.D, ga + i * HV);
+                    rope_get<V>(par + r * p.D, ch.b[i], p.D, gb + i * HV);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < HV; ++k) ga[i * HV + k] = gb[i * HV + k] = f2s(1.f);
+                }
+                if constexpr (MODE == kRopeLn) {
+                    rope_get<V>(par + (2 + r) * p.D, ch.a[i], p.D, ba + i * HV);
+                    rope_get<V>(par + (2 + r) * p.D, ch.b[i], p.D, bb + i * HV);
+                }
             }
-            if constexpr (MODE == kRopeLn) {
-                rope_get<V>(par + (2 + r) * p.D, ch.a, p.D, ba);
-                rope_get<V>(par + (2 + r) * p.D, ch.b, p.D, bb);
-            }
-            if (inter) {
+            if (inter) {  // pairs of a chunk from element e on: from e / 2 on
+                auto fold = [&](const float2 &g, int at, float2 &cc, float2 &ss, float2 &bias) {
+                    const float c = tab.c[at], s = tab.s[at];
+                    cc = make_float2(g.x * c, g.y * c);
+                    ss = make_float2(-g.y * s, g.x * s);
+                    if constexpr (MODE == kRopeLn) bias = make_float2(bias.x * c - bias.y * s, bias.y * c + bias.x * s);
+                };
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    {
-                        const float c = tab.c[ch.pa + i], s = tab.s[ch.pa + i];
-                        ca[i] = make_float2(ga[i].x * c, ga[i].y * c);
-                        sa[i] = make_float2(-ga[i].y * s, ga[i].x * s);
-                        if constexpr (MODE == kRopeLn)
-                            ba[i] = make_float2(ba[i].x * c - ba[i].y * s, ba[i].y * c + ba[i].x * s);
-                    }
-                    {
-                        const float c = tab.c[ch.pb + i], s = tab.s[ch.pb + i];
-                        cb[i] = make_float2(gb[i].x * c, gb[i].y * c);
-                        sb[i] = make_float2(-gb[i].y * s, gb[i].x * s);
-                        if constexpr (MODE == kRopeLn)
-                            bb[i] = make_float2(bb[i].x * c - bb[i].y * s, bb[i].y * c + bb[i].x * s);
-                    }
+                    fold(ga[i], ch.a[i / HV] / 2 + i % HV, ca[i], sa[i], ba[i]);
+                    fold(gb[i], ch.b[i / HV] / 2 + i % HV, cb[i], sb[i], bb[i]);
                 }
             } else {
                 float2 c[H], s[H];
-                rope_get<V>(tab.c, ch.pa, Table::N, c);
-                rope_get<V>(tab.s, ch.pa, Table::N, s);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    rope_get<V>(tab.c, (i * L + sl) * V, N, c + i * HV);
+                    rope_get<V>(tab.s, (i * L + sl) * V, N, s + i * HV);
+                }
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     ca[i] = f2mul(ga[i], c[i]);
@@ -374,27 +391,27 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
             if constexpr (KIND == kRopeSome) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    sa[i] = ch.ra ? sa[i] : f2s(0.f);
-                    sb[i] = ch.rb ? sb[i] : f2s(0.f);
+                    sa[i] = ch.ra[i / HV] ? sa[i] : f2s(0.f);
+                    sb[i] = ch.rb[i / HV] ? sb[i] : f2s(0.f);
                 }
             }
         }
         turn = w.next(p, grp);
         if (w.left && turn == 2) pos = rope_position(p, w, lane);
         rope_cp_wait<DEPTH - 1>();
-        Raw ra[U], rb[U];
+        Raw raw[U][2 * C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            ra[u] = ring[slot][u][0][lane];
-            rb[u] = ring[slot][u][1][lane];
-        }
+        for (int i = 0; i < U * 2 * C; ++i) raw[i / (2 * C)][i % (2 * C)] = ring[slot][i / (2 * C)][i % (2 * C)][lane];
         load(slot);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool in = hl > u * G;
             float2 va[H], vb[H];
-            rope_unpack<XT, V>(ra[u], p.xdt, va);
-            rope_unpack<XT, V>(rb[u], p.xdt, vb);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                rope_unpack<XT, V>(raw[u][2 * i], p.xdt, va + i * HV);
+                rope_unpack<XT, V>(raw[u][2 * i + 1], p.xdt, vb + i * HV);
+            }
             if constexpr (MODE != kRopeOnly) {
                 float mean = 0.f;
                 if constexpr (MODE == kRopeLn) {
@@ -410,15 +427,19 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                         vb[i] = f2add(vb[i], f2s(-mean));
                     }
                 }
-                float2 ta = f2s(0.f), tb = f2s(0.f);
+                float sq[1] = {0.f};
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    ta = f2fma(va[i], va[i], ta);
-                    tb = f2fma(vb[i], vb[i], tb);
+                for (int i = 0; i < C; ++i) {
+                    float2 ta = f2s(0.f), tb = f2s(0.f);
+#pragma unroll
+                    for (int k = i * HV; k < (i + 1) * HV; ++k) {
+                        ta = f2fma(va[k], va[k], ta);
+                        tb = f2fma(vb[k], vb[k], tb);
+                    }
+                    // a chunk that is not there holds zeros, with the mean off it no longer
+                    const bool ka = MODE != kRopeLn || ch.oka[i], kb = MODE != kRopeLn || ch.okb[i];
+                    sq[0] += (ka ? ta.x + ta.y : 0.f) + (kb ? tb.x + tb.y : 0.f);
                 }
-                // a chunk that is not there holds zeros, with the mean off it no longer
-                const bool ka = MODE != kRopeLn || ch.oka, kb = MODE != kRopeLn || ch.okb;
-                float sq[1] = {(ka ? ta.x + ta.y : 0.f) + (kb ? tb.x + tb.y : 0.f)};
                 lanes.sum(sq);
                 const float rstd = rsqrtf(sq[0] * inv + p.eps);
                 if (p.rstd && sl == 0 && in) p.rstd[stat + u * G] = rstd;
@@ -434,15 +455,18 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
             for (int i = 0; i < H; ++i) {
                 float2 ta = inter ? f2swap(va[i]) : vb[i], tb = inter ? f2swap(vb[i]) : va[i];
                 if constexpr (KIND == kRopeSome) {  // an element that is not rotated takes nothing from another, not even a NaN
-                    ta = ch.ra ? ta : f2s(0.f);
-                    tb = ch.rb ? tb : f2s(0.f);
+                    ta = ch.ra[i / HV] ? ta : f2s(0.f);
+                    tb = ch.rb[i / HV] ? tb : f2s(0.f);
                 }
                 ua[i] = f2fma(va[i], ca[i], MODE == kRopeLn ? f2fma(ta, sa[i], ba[i]) : f2mul(ta, sa[i]));
                 ub[i] = f2fma(vb[i], cb[i], MODE == kRopeLn ? f2fma(tb, sb[i], bb[i]) : f2mul(tb, sb[i]));
             }
             char *q = u == 0 ? y : y + u * ys;
-            if (in && ch.oka) rope_store<XT, V>(q + ch.a * yes, p.ydt, ua);
-            if (in && ch.okb) rope_store<XT, V>(q + ch.b * yes, p.ydt, ub);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (in && ch.oka[i]) rope_store<XT, V>(q + ch.a[i] * yes, p.ydt, ua + i * HV);
+                if (in && ch.okb[i]) rope_store<XT, V>(q + ch.b[i] * yes, p.ydt, ub + i * HV);
+            }
         }
         if (!w.left) return;
         if (turn) {
@@ -456,14 +480,14 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     }
 }
 
-template <bool LN, int XT, int V, int L, int KIND, int U, int MINB>
+template <bool LN, int XT, int V, int C, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
-    constexpr int G = 32 / L, H = V / 2, DEPTH = kRopeBwdDepth;
-    using Table = RopeTable<V, L>;
+    constexpr int G = 32 / L, HV = V / 2, H = C * HV, N = C * V * L, DEPTH = kRopeBwdDepth;
+    using Table = RopeTable<V, N>;
     using Raw = RopeRaw<XT, V>;
     struct Slot {
-        Raw x[U][2][32], g[U][2][32];
+        Raw x[U][2 * C][32], g[U][2 * C][32];
         float mean[U][32], rstd[U][32];
     };
     // rings, tables, frequencies, gamma of the queries and of the keys; at the end the column sums [kRopeWarps][D] over the rings
@@ -473,11 +497,11 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     const int sl = lanes.sl, grp = lane < G * L ? lane / L : kRopeNoHead;
     Slot *ring = reinterpret_cast<Slot *>(rope_smem) + warp * DEPTH;
     Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps);
-    RopeTurns<V, L> &turns = *reinterpret_cast<RopeTurns<V, L> *>(tables + kRopeWarps);
+    RopeTurns<N> &turns = *reinterpret_cast<RopeTurns<N> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1), *rope_acc = reinterpret_cast<float *>(rope_smem);
     Table &tab = tables[warp];
     RopeCursor<G * U, false> w(p, grp), ahead = w;  // the pass worked on, the pass to load
-    const RopeChunks<V, L, KIND> ch(p, sl, lane < G * L);
+    const RopeChunks<V, C, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     const int r = w.r, xes = rope_esize<XT>(p.xdt), ges = rope_esize<XT>(p.ydt);
     const char *x = ahead.at(p, p.x[r], V * xes), *g = ahead.at(p, p.g[r], V * ges);
@@ -491,10 +515,13 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 // a lane without a head in the pass reads another with a gradient of zeros, and stores nothing
                 const bool in = ahead.hl > u * G;
                 const char *q = u == 0 ? x : x + (in ? u * xs : 0), *d = u == 0 ? g : g + (in ? u * gs : 0);
-                rope_cp(&to.x[u][0][lane], q + ch.a * xes, ch.oka, p.xdt);
-                rope_cp(&to.x[u][1][lane], q + ch.b * xes, ch.okb, p.xdt);
-                rope_cp(&to.g[u][0][lane], d + ch.a * ges, in && ch.oka, p.ydt);
-                rope_cp(&to.g[u][1][lane], d + ch.b * ges, in && ch.okb, p.ydt);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    rope_cp(&to.x[u][2 * i][lane], q + ch.a[i] * xes, ch.oka[i], p.xdt);
+                    rope_cp(&to.x[u][2 * i + 1][lane], q + ch.b[i] * xes, ch.okb[i], p.xdt);
+                    rope_cp(&to.g[u][2 * i][lane], d + ch.a[i] * ges, in && ch.oka[i], p.ydt);
+                    rope_cp(&to.g[u][2 * i + 1][lane], d + ch.b[i] * ges, in && ch.okb[i], p.ydt);
+                }
                 rope_cp_bytes<4>(&to.rstd[u][lane], p.rstd + stat + (in ? u * G : 0), true);
                 if constexpr (LN) rope_cp_bytes<4>(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true);
             }
@@ -538,41 +565,37 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 // the gradient turned back (the sign of s is the transpose's)
                 float2 ta[H], tb[H];
                 {
-                    float2 c[H], s[H], ga[H], gb[H];  // c, s: of the chunks' pairs (neighbours: first a's, then b's)
-                    if (inter) {
+                    float2 ga[H], gb[H];
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            const int at = 2 * i < H ? ch.pa + 2 * i : ch.pb + 2 * i - H;
-                            c[i] = *reinterpret_cast<const float2 *>(tab.c + at);
-                            s[i] = *reinterpret_cast<const float2 *>(tab.s + at);
-                        }
-                    } else {
-                        rope_get<V>(tab.c, ch.pa, Table::N, c);
-                        rope_get<V>(tab.s, ch.pa, Table::N, s);
+                    for (int i = 0; i < C; ++i) {
+                        rope_unpack<XT, V>(ring[slot].g[u][2 * i][lane], p.ydt, ga + i * HV);
+                        rope_unpack<XT, V>(ring[slot].g[u][2 * i + 1][lane], p.ydt, gb + i * HV);
                     }
-                    rope_unpack<XT, V>(ring[slot].g[u][0][lane], p.ydt, ga);
-                    rope_unpack<XT, V>(ring[slot].g[u][1][lane], p.ydt, gb);
                     if (inter) {
+                        auto turned = [&](float2 d, int at, bool rotated) {
+                            const float c = tab.c[at], s = tab.s[at];
+                            float2 m = f2swap(d);
+                            if constexpr (KIND == kRopeSome) m = rotated ? m : f2s(0.f);
+                            return make_float2(d.x * c - m.x * s, d.y * c + m.y * s);
+                        };
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
-                            const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
-                            const float cj = i & 1 ? c[H / 2 + i / 2].y : c[H / 2 + i / 2].x,
-                                        sj = i & 1 ? s[H / 2 + i / 2].y : s[H / 2 + i / 2].x;
-                            float2 m = f2swap(ga[i]), n = f2swap(gb[i]);
-                            if constexpr (KIND == kRopeSome) {
-                                m = ch.ra ? m : f2s(0.f);
-                                n = ch.rb ? n : f2s(0.f);
-                            }
-                            ta[i] = make_float2(ga[i].x * ci - m.x * si, ga[i].y * ci + m.y * si);
-                            tb[i] = make_float2(gb[i].x * cj - n.x * sj, gb[i].y * cj + n.y * sj);
+                            ta[i] = turned(ga[i], ch.a[i / HV] / 2 + i % HV, ch.ra[i / HV]);
+                            tb[i] = turned(gb[i], ch.b[i / HV] / 2 + i % HV, ch.rb[i / HV]);
                         }
                     } else {
+                        float2 c[H], s[H];
+#pragma unroll
+                        for (int i = 0; i < C; ++i) {
+                            rope_get<V>(tab.c, (i * L + sl) * V, N, c + i * HV);
+                            rope_get<V>(tab.s, (i * L + sl) * V, N, s + i * HV);
+                        }
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
                             float2 m = gb[i], n = ga[i];
                             if constexpr (KIND == kRopeSome) {
-                                m = ch.ra ? m : f2s(0.f);
-                                n = ch.ra ? n : f2s(0.f);
+                                m = ch.ra[i / HV] ? m : f2s(0.f);
+                                n = ch.ra[i / HV] ? n : f2s(0.f);
                             }
                             ta[i] = f2fma(ga[i], c[i], f2mul(make_float2(-m.x, -m.y), s[i]));
                             tb[i] = f2fma(gb[i], c[i], f2mul(n, s[i]));
@@ -580,14 +603,20 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                     }
                 }
                 float2 xa[H], xb[H];
-                rope_unpack<XT, V>(ring[slot].x[u][0][lane], p.xdt, xa);
-                rope_unpack<XT, V>(ring[slot].x[u][1][lane], p.xdt, xb);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    rope_unpack<XT, V>(ring[slot].x[u][2 * i][lane], p.xdt, xa + i * HV);
+                    rope_unpack<XT, V>(ring[slot].x[u][2 * i + 1][lane], p.xdt, xb + i * HV);
+                }
                 const float rstd = ring[slot].rstd[u][lane], mean = LN ? ring[slot].mean[u][lane] : 0.f;
                 if (u == U - 1) load(slot);
                 float2 dot = f2s(0.f), sum = f2s(0.f);
                 float2 wa[H], wb[H];
-                rope_get<V>(par + r * p.D, ch.a, p.D, wa);
-                rope_get<V>(par + r * p.D, ch.b, p.D, wb);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    rope_get<V>(par + r * p.D, ch.a[i], p.D, wa + i * HV);
+                    rope_get<V>(par + r * p.D, ch.b[i], p.D, wb + i * HV);
+                }
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     if constexpr (LN) {
@@ -618,8 +647,11 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 }
                 const bool in = hl > u * G;
                 char *q = u == 0 ? y : y + u * ys;
-                if (in && ch.oka) rope_store<XT, V>(q + ch.a * xes, p.xdt, ta);
-                if (in && ch.okb) rope_store<XT, V>(q + ch.b * xes, p.xdt, tb);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    if (in && ch.oka[i]) rope_store<XT, V>(q + ch.a[i] * xes, p.xdt, ta + i * HV);
+                    if (in && ch.okb[i]) rope_store<XT, V>(q + ch.b[i] * xes, p.xdt, tb + i * HV);
+                }
             }
             if (!w.left) break;
             if (turn) y = w.at(p, p.y[r], V * xes);
@@ -656,8 +688,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
         if (grp == 0) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                if (ch.oka) *reinterpret_cast<float2 *>(mine + ch.a + 2 * i) = u[i];
-                if (ch.okb) *reinterpret_cast<float2 *>(mine + ch.b + 2 * i) = v[i];
+                if (ch.oka[i / HV]) *reinterpret_cast<float2 *>(mine + ch.a[i / HV] + 2 * (i % HV)) = u[i];
+                if (ch.okb[i / HV]) *reinterpret_cast<float2 *>(mine + ch.b[i / HV] + 2 * (i % HV)) = v[i];
             }
         }
     };

@@ -34,7 +34,7 @@ def cuda(t):
 
 def place(t, how, fill=float("nan")):
     """t on the GPU as: "dense", "packed" (behind other heads of its token), "major" (heads outside tokens), "odd" (one
-    element off every boundary), the rest of the memory holding `fill`."""
+    element off every boundary), "two" (two off), the rest of the memory holding `fill`."""
     if t is None:
         return None
     B, S, H, D = t.shape
@@ -46,19 +46,20 @@ def place(t, how, fill=float("nan")):
         buf = torch.full((B, S, H + 3, D), fill, device="cuda").to(t.dtype)
         out = buf[:, :, 2:2 + H]
     else:
-        buf = torch.full((B, S, H, D + 3), fill, device="cuda").to(t.dtype)
-        out = buf[..., 1:1 + D]
+        first = 1 if how == "odd" else 2
+        buf = torch.full((B, S, H, D + 2 + first), fill, device="cuda").to(t.dtype)
+        out = buf[..., first:first + D]
     out.copy_(t)
     return out
 
 
 def untouched(t, how, fill):
     """What lies around a tensor that `place` laid out still holds `fill`."""
-    if how not in ("packed", "odd"):
+    if how not in ("packed", "odd", "two"):
         return True
     whole = t._base
     inner = torch.zeros(whole.shape, dtype=torch.bool, device="cuda")
-    (inner[:, :, 2:2 + t.shape[2]] if how == "packed" else inner[..., 1:1 + t.shape[3]]).fill_(True)
+    (inner[:, :, 2:2 + t.shape[2]] if how == "packed" else inner[..., (1 if how == "odd" else 2):][..., :t.shape[3]]).fill_(True)
     return bool((whole[~inner] == fill).all())
 
 

@@ -48,10 +48,11 @@ def test_parts_of_heads(dt, v, L):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
-@pytest.mark.parametrize("D,L", [(8, 4), (24, 4), (40, 5), (56, 8), (72, 9), (104, 16), (200, 32), (256, 32)])
+@pytest.mark.parametrize("D,L", [(8, 4), (24, 4), (40, 4), (56, 4), (72, 5), (88, 6), (104, 8), (136, 10), (200, 16), (256, 16),
+                                 (424, 32)])
 def test_vectors_of_four(dt, D, L):
-    how = "packed" if D < 256 else "dense"
-    rot = D if D < 256 else 200  # half of 200 is no multiple of eight
+    how = "packed" if D < 200 else "dense"
+    rot = D if D != 256 else 200  # half of 200 is no multiple of eight
     for mode in (False, True):
         run_forward(mode, 1, 9, 7, 3, D, rot, dt=dt, how=how)
         run_backward(mode, 1, 9, 7, 3, D, rot, dt=dt, how=how)
@@ -59,7 +60,7 @@ def test_vectors_of_four(dt, D, L):
     assert names() == [f"vec4x{L}"] * 3
 
 
-@pytest.mark.parametrize("D,L", [(32, 4), (64, 8), (80, 16), (128, 16), (256, 32)])
+@pytest.mark.parametrize("D,L", [(32, 4), (64, 4), (80, 8), (128, 8), (256, 16), (512, 32)])
 @pytest.mark.parametrize("xt,yt", [("fp32", "bf16"), ("bf16", "fp32"), ("fp16", "bf16"), ("fp32", "fp16")])
 def test_differing_types(D, L, xt, yt):
     for inter in (False, True):
@@ -68,6 +69,25 @@ def test_differing_types(D, L, xt, yt):
             run_backward(mode, 1, 9, 7, 3, D, dt=xt, ydt=yt, inter=inter, pdt="fp32")
         run_forward(None, 1, 9, 7, 3, D, D // 2, dt=xt, ydt=yt, inter=inter)
         assert names() == [f"vec4x{L}"] * 3
+
+
+# Halves of an even number of pairs, or neighbours, on boundaries of two elements.
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("D,rot,inter,L", [(4, 4, False, 4), (2, 2, True, 4), (44, 44, False, 4), (98, 98, True, 8),
+                                           (100, 44, False, 8), (130, 130, True, 16), (250, 20, True, 16),
+                                           (252, 252, False, 16), (258, 258, True, 32)])
+def test_vectors_of_two(dt, D, rot, inter, L):
+    if dt == "fp32":
+        L = 2 * L if 2 * 2 * L * 2 < D + 8 else L  # eight elements a lane, not sixteen
+        if D >= 258:
+            return
+    for mode in (False, True):
+        run_forward(mode, 1, 9, 7, 3, D, rot, dt=dt, inter=inter, how="two")
+        run_backward(mode, 1, 9, 7, 3, D, rot, dt=dt, inter=inter, how="two")
+    run_forward(None, 1, 9, 7, 3, D, rot, dt=dt, inter=inter, how="two")
+    assert all(n.startswith("vec2x") for n in names()), names()
+    if dt != "fp32":
+        assert names() == [f"vec2x{L}"] * 3
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
