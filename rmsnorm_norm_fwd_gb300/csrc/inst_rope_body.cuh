@@ -1,7 +1,8 @@
 // Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V, GBN_C, the
 // type and elements of a vector and the vectors of half a lane's elements.  Defines kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE 2 (16-byte vectors): whole
-// heads rotated as halves or as neighbours have kernels of their own up to 16 lanes, where they measured faster; 1, 0:
-// all run on the kernels for any rotation, and on fewer numbers of lanes.
+// heads rotated as halves or as neighbours, and parts rotated as halves, have kernels of their own up to 16 lanes (prefill
+// of 16384 tokens of 40 heads of 128 54 us against 60 us, backward of heads of 256 with a quarter rotated 56 us against 57
+// us); 1, 0: all run on the kernels for any rotation, and on fewer numbers of lanes.
 #include "rope_vec_kernels.cuh"
 
 #ifndef GBN_CAT
@@ -17,9 +18,9 @@
 #else
 #define GBN_K(L, KIND, S) \
     {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, GBN_C, L, KIND, GBN_BU(KIND), 2>, "vec" GBN_STR(GBN_V) "x" #L S, \
-     rope_bwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_C, GBN_C * GBN_V, L, GBN_BU(KIND)), GBN_BU(KIND), L}
+     rope_bwd_smem(sizeof(RopeRaw<GBN_XT, GBN_V>), GBN_C, GBN_C * GBN_V, L, GBN_BU(KIND), GBN_MODE == -2), GBN_BU(KIND), L}
 #endif
-#define GBN_FU(KIND) (GBN_MODE == 0 && KIND != kRopeSome ? 2 : 1)
+#define GBN_FU(KIND) (GBN_MODE == 0 && rope_whole(KIND) ? 2 : 1)
 #define GBN_BU(KIND) 1
 #define GBN_ANY(L) GBN_K(L, kRopeSome, "")
 #if GBN_WHOLE == 2
@@ -38,8 +39,10 @@ const RopeVariant GBN_CAT(kRopeVec_, GBN_NAME)[kRopeVecKinds][kRopeVecLanes] = {
     {GBN_K(4, kRopeNeighbours, "n"), GBN_K(5, kRopeNeighbours, "n"), GBN_K(6, kRopeNeighbours, "n"),
      GBN_K(8, kRopeNeighbours, "n"), GBN_K(9, kRopeNeighbours, "n"), GBN_K(10, kRopeNeighbours, "n"),
      GBN_K(16, kRopeNeighbours, "n"), GBN_ANY(32)},
+    {GBN_K(4, kRopePart, "p"), GBN_ANY(5), GBN_ANY(6), GBN_K(8, kRopePart, "p"), GBN_ANY(9), GBN_ANY(10),
+     GBN_K(16, kRopePart, "p"), GBN_ANY(32)},
 #else
-    GBN_SOME, GBN_SOME,
+    GBN_SOME, GBN_SOME, GBN_SOME,
 #endif
     GBN_SOME};
 }  // namespace gbn

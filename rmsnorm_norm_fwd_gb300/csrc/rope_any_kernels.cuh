@@ -169,6 +169,11 @@ template <int L, int C> struct RopeAnySmem {
     }
 };
 
+template <bool LN, int L, int C> struct RopeAnyBwdSmem {
+    RopeAnySmem<L, C> sm;
+    RopeAside<C / 2 * (LN ? 2 : 1)> asides[kRopeWarps];
+};
+
 template <int MODE, int L, int C, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_any(const __grid_constant__ RopeParams p) {
     constexpr int G = 32 / L, H = C / 2, N = L * C;
@@ -177,10 +182,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_any(const __grid_cons
     RopeAnySmem<L, C> &sm = *reinterpret_cast<RopeAnySmem<L, C> *>(rope_smem);
     const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L;
     RopeSlotTable<L, C> &tab = sm.tables[threadIdx.x >> 5];
-    RopeCursor<G, true> w(p, grp);
+    RopeCursor<G> w(p, grp);
     const Slots ch(p, sl);
     const int xes = esize(p.xdt), yes = esize(p.ydt);
-    auto at = [&](const RopeCursor<G, true> &c, const RopeHeads &t, int es) {
+    auto at = [&](const RopeCursor<G> &c, const RopeHeads &t, int es) {
         return static_cast<char *>(t.p) + (c.b * t.batch + c.s * t.token + c.head(p) * t.head) * es;
     };
     uint32_t ra[C], rb[C];
@@ -302,22 +307,25 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
     constexpr int G = 32 / L, H = C / 2, N = L * C;
     using Slots = RopeSlots<L, C>;
-    extern __shared__ __align__(16) unsigned char rope_smem[];  // RopeAnySmem, then the column sums [kRopeWarps][D]
-    RopeAnySmem<L, C> &sm = *reinterpret_cast<RopeAnySmem<L, C> *>(rope_smem);
-    float *acc = reinterpret_cast<float *>(&sm + 1);
+    using Aside = RopeAside<H * (LN ? 2 : 1)>;
+    extern __shared__ __align__(16) unsigned char rope_smem[];  // RopeAnyBwdSmem, then the column sums [kRopeWarps][D]
+    RopeAnyBwdSmem<LN, L, C> &both = *reinterpret_cast<RopeAnyBwdSmem<LN, L, C> *>(rope_smem);
+    RopeAnySmem<L, C> &sm = both.sm;
+    float *acc = reinterpret_cast<float *>(&both + 1);
     const int lane = threadIdx.x & 31, sl = lane % L, grp = lane / L, warp = threadIdx.x >> 5;
     RopeSlotTable<L, C> &tab = sm.tables[warp];
-    RopeCursor<G, false> w(p, grp);
+    Aside &aside = both.asides[warp];
+    RopeCursor<G> w(p, grp);
     const Slots ch(p, sl);
-    const int r = w.r, xes = esize(p.xdt), ges = esize(p.ydt);
+    const int xes = esize(p.xdt), ges = esize(p.ydt);
     auto at = [&](const RopeHeads &t, int es) {
         return static_cast<char *>(t.p) + (w.b * t.batch + w.s * t.token + w.head(p) * t.head) * es;
     };
     uint32_t xa[C], xb[C], ga[C], gb[C];
     float rstd = 0.f, mean = 0.f;
     auto load = [&] {
-        ch.load(at(p.x[r], xes), p.xdt, w.hl > 0, xa, xb);
-        ch.load(at(p.g[r], ges), p.ydt, w.hl > 0, ga, gb);
+        ch.load(at(p.x[w.r], xes), p.xdt, w.hl > 0, xa, xb);
+        ch.load(at(p.g[w.r], ges), p.ydt, w.hl > 0, ga, gb);
         rstd = __ldg(p.rstd + w.stat(p));
         if constexpr (LN) mean = __ldg(p.mean + w.stat(p));
     };
@@ -331,12 +339,23 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
     float2 da[H], db[H], ea[H], eb[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
+    aside.clear(lane);
+    auto swap = [&] {
+        aside.template swap<H / 2>(da, 0, lane);
+        aside.template swap<H / 2>(db, H / 2, lane);
+        if constexpr (LN) {
+            aside.template swap<H / 2>(ea, H, lane);
+            aside.template swap<H / 2>(eb, H + H / 2, lane);
+        }
+    };
     if (w.left) {
-        const float inv = 1.f / (float)p.D, *par = sm.par + r * 4 * N;
+        const float inv = 1.f / (float)p.D;
         int turn = 2;
         while (true) {
             float2 va[H], vb[H], ta[H], tb[H];
-            if (turn) tab.put(sm.turns, sm.bad, p, pos, lane);
+            const int r = w.r;
+            const float *par = sm.par + r * 4 * N;
+            if (turn == 2) tab.put(sm.turns, sm.bad, p, pos, lane);
             Slots::widen(ga, p.ydt, va);
             Slots::widen(gb, p.ydt, vb);
             {  // the gradient turned back (the sign of s is the transpose's)
@@ -366,7 +385,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
             turn = w.next(p, grp);
             if (w.left) {
                 load();
-                if (turn) pos = rope_position(p, w, lane);
+                if (turn == 2) pos = rope_position(p, w, lane);
             }
             float2 dot = f2s(0.f), sum = f2s(0.f), wa[H], wb[H];
             Slots::get(par, sl, wa);
@@ -399,6 +418,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
                 tb[i] = f2fma(vb[i], c2, LN ? f2fma(tb[i], f2s(rs), c1) : f2mul(tb[i], f2s(rs)));
             }
             if (in) ch.store(y, p.xdt, ta, tb);
+            if (w.left ? w.r != r : r) swap();  // at the end the queries' are in the registers
             if (!w.left) break;
         }
     }
@@ -416,11 +436,14 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
             }
         if (grp == 0) ch.store(mine, kF32, u, v);
     };
-    columns(da, db);
-    rope_partial(p, acc, 0);
-    if constexpr (LN) {
-        columns(ea, eb);
-        rope_partial(p, acc, 1);
+    for (int r = 0; r < (p.heads[1] ? 2 : 1); ++r) {
+        if (r) swap();
+        columns(da, db);
+        rope_partial(p, acc, 0, r);
+        if constexpr (LN) {
+            columns(ea, eb);
+            rope_partial(p, acc, 1, r);
+        }
     }
 }
 

@@ -200,45 +200,26 @@ bool bad_aliasing(const Box *outs, int no, const Box *ins, int ni, int same_n) {
 thread_local const char *t_last[3] = {"", "", ""};
 
 // Passes of `at_once` heads, shared out over a grid of at most per_sm CTAs an
-// SM: warps for queries and for keys in proportion to their work (or, with
-// `tokens`, for both together), one pass a warp where that is few enough.  Returns the CTAs, -1 if a warp's passes do
-// not fit its counter.
-int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, bool tokens, const HostDevice &d) {
+// SM: one pass a warp where that is few enough.  Returns the CTAs, -1 if a
+// warp's passes do not fit its counter.
+int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, const HostDevice &d) {
     int64_t cap = per_sm * d.sms;
     const int64_t limit = host_grid_limit();
     if (limit > 0 && limit < cap) cap = limit;
-    const int64_t most = cap * kRopeWarps;
-    int64_t total = 0;
+    p->units = 0;
     for (int i = 0; i < 2; ++i) {
         p->passes[i] = (int)((s.H[i] + at_once - 1) / at_once);
-        p->units[i] = s.tokens() * p->passes[i];
-        total += p->units[i];
+        p->units += s.tokens() * p->passes[i];
     }
-    if (tokens) {
-        p->units[0] = total;
-        p->warps[0] = std::min(total, most);
-        p->units[1] = p->warps[1] = 0;
-    } else if (total <= most) {
-        p->warps[0] = p->units[0];
-        p->warps[1] = p->units[1];
-    } else {
-        // a token's angles cost about as much as one and a half passes
-        const double q = p->passes[0] + 1.5, k = s.tensors() == 1 ? 0.0 : p->passes[1] + 1.5;
-        const int64_t part = std::max<int64_t>(1, (int64_t)(q / (q + k) * (double)most + 0.5));
-        p->warps[0] = std::min(p->units[0], s.tensors() == 1 ? most : std::min(most - 1, part));
-        p->warps[1] = std::min(p->units[1], most - p->warps[0]);
-    }
-    for (int i = 0; i < 2; ++i) {
-        if (p->warps[i] == 0) continue;
-        if (p->units[i] / p->warps[i] >= INT32_MAX) return -1;
-        // whole tokens as a front (prefill of 16384 tokens 62 -> 57 us, backward 97 -> 88 us) where a warp has four or more;
-        // below, the uneven rest costs more than the order gives (8192 tokens rotated: 21.7 us without, 23.0 us with)
-        const int64_t rounds = s.tokens() / p->warps[i];
-        p->rounds[i] = rounds < 4 ? 0 : (int)rounds;
-        p->step_b[i] = (int)(p->warps[i] / s.S);
-        p->step_s[i] = (int)(p->warps[i] % s.S);
-    }
-    return (p->warps[0] + p->warps[1] + kRopeWarps - 1) / kRopeWarps;
+    p->warps = std::min(p->units, cap * kRopeWarps);
+    if (p->units / p->warps >= INT32_MAX) return -1;
+    // whole tokens as a front (prefill of 16384 tokens 62 -> 57 us, backward 97 -> 88 us) where a warp has four or more;
+    // below, the uneven rest costs more than the order gives (8192 tokens rotated: 21.7 us without, 23.0 us with)
+    const int64_t rounds = s.tokens() / p->warps;
+    p->rounds = rounds < 4 ? 0 : (int)rounds;
+    p->step_b = (int)(p->warps / s.S);
+    p->step_s = (int)(p->warps % s.S);
+    return (p->warps + kRopeWarps - 1) / kRopeWarps;
 }
 
 int launch(const void *kernel, int64_t grid, size_t dyn, RopeParams *p, cudaStream_t st) {
@@ -255,7 +236,6 @@ struct Kernel {
     int heads;  // of a pass
     int smem;
     int slot;   // its place in the cache of what a device holds
-    bool tokens;  // a warp takes queries and keys of its tokens (RopeTokens), else of one tensor (RopeWalk)
 };
 
 int any_size(int D, int rot) {  // 32 << that pairs hold a head
@@ -300,7 +280,7 @@ Kernel pick(int mode, RopeParams &p) {
     if (v) {
         const int chunks = p.D / v, rot = p.rot / v;
         const int slots = p.inter ? (chunks + 1) / 2 : rot / 2 + (chunks - rot + 1) / 2;
-        const int kind = p.rot < p.D ? kRopeVecKinds - 1 : p.inter;
+        const int kind = p.rot == p.D ? p.inter : p.inter ? 3 : 2;  // as RopeKind
         const int t = p.xdt != p.ydt ? 6 : p.xdt + (v == 2 ? 0 : v == 4 ? 3 : 6);
         const int c = p.xdt == p.ydt && p.xdt == GBNORM_F32 ? 4 / v : 8 / v;  // slots a lane
         for (int l = 0; l < kRopeVecLanes; ++l)
@@ -314,12 +294,12 @@ Kernel pick(int mode, RopeParams &p) {
                     }
                 // gamma (and beta) of both tensors as fp32 behind the rings
                 const int par = mode == kRopeOnly ? 0 : mode == kRopeLn ? 16 * p.D : 8 * p.D;
-                return {k.f, k.name, 32 / k.lanes * k.u, k.smem + par, ((m * kVecTypes + t) * kRopeVecKinds + kind) * kRopeVecLanes + l, mode >= 0};
+                return {k.f, k.name, 32 / k.lanes * k.u, k.smem + par, ((m * kVecTypes + t) * kRopeVecKinds + kind) * kRopeVecLanes + l};
             }
     }
     const int n = any_size(p.D, p.rot), slot = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
     const RopeVariant &k = mode < 0 ? kRopeBwdAny[-1 - mode][n] : kRopeFwdAny[mode][n];
-    return {k.f, k.name, 32 / k.lanes, k.smem + (mode < 0 ? kRopeWarps * p.D * 4 : 0), slot, mode >= 0};
+    return {k.f, k.name, 32 / k.lanes, k.smem + (mode < 0 ? kRopeWarps * p.D * 4 : 0), slot};
 }
 constexpr int kSlots = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + 5 * kRopeAnySizes;
 std::atomic<int> g_resident[kHostMaxDev][kSlots];
@@ -331,7 +311,7 @@ int resident(const Kernel &k, const HostDevice &d, int *out) {
     if (o == 0) {
         // heads of several sizes share a kernel: allow for the parameters (8 KB) or column sums (32 KB) of any
         if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 std::max(k.smem, 16 * 1024) + 32 * 1024) != cudaSuccess ||
+                                 k.smem + 32 * 1024) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k.f, kRopeCTA, (size_t)k.smem) != cudaSuccess)
             return GBNORM_ERR_CUDA;
         if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
@@ -353,7 +333,7 @@ int run_fwd(int mode, RopeParams *p, const Shape &s, cudaStream_t st) {
     int per_sm;
     const int o = resident(k, d, &per_sm);
     if (o != GBNORM_OK) return o;
-    const int64_t grid = share(p, s, k.heads, per_sm, k.tokens, d);
+    const int64_t grid = share(p, s, k.heads, per_sm, d);
     if (grid < 0) return GBNORM_ERR_UNSUPPORTED;
     t_last[what] = k.name;
     return launch(k.f, grid, (size_t)k.smem, p, st);
@@ -486,7 +466,7 @@ int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_head
         const Kernel k = pick(-1 - is_layernorm, p);
         int per_sm;
         if ((e = resident(k, d, &per_sm)) != GBNORM_OK) return e;
-        P = share(&p, s, k.heads, std::min<int64_t>(per_sm, kBwdPerSm), k.tokens, d);
+        P = share(&p, s, k.heads, std::min<int64_t>(per_sm, kBwdPerSm), d);
         if (P < 0) return GBNORM_ERR_UNSUPPORTED;
         t_last[1] = k.name;
         e = launch(k.f, P, (size_t)k.smem, &p, stream);

@@ -59,17 +59,15 @@ __device__ __forceinline__ int64_t rope_div(int64_t a, int64_t n) {
     return ((a | n) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)n) : a / n;
 }
 
-// A warp's share of the passes.  A pass takes GU heads, lane group `grp` one of
-// them (and every 32 / L-th).  BOTH: over the tokens, each with its queries'
-// heads and then its keys', so that both take the token's angles (units and warps
-// of index 0 count both); else over one tensor, which the backward's column sums
-// belong to.  Passes over one tensor of a token are a segment: within one a step
-// is an addition.
+// A warp's share of the passes over the tokens, each with its queries' heads and
+// then its keys', so that both take the token's angles.  A pass takes GU heads,
+// lane group `grp` one of them (and every 32 / L-th).  Passes over one tensor of
+// a token are a segment: within one a step is an addition.
 //
 // A warp takes every W-th token as long as all W warps have one, so that the
 // grid moves through memory as a front, and then its share of the passes over
 // the tokens that are left.
-template <int GU, bool BOTH> struct RopeCursor {
+template <int GU> struct RopeCursor {
     int left;    // passes to go, this one included
     int cnt;     // of the segment
     int hl;      // heads of the segment from this lane's on
@@ -77,37 +75,30 @@ template <int GU, bool BOTH> struct RopeCursor {
     int r;       // 0 queries, 1 keys
     int rounds;  // whole tokens to go
     __device__ __forceinline__ RopeCursor(const RopeParams &p, int grp) {
-        int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-        r = !BOTH && w >= p.warps[0];
-        if (r) w -= p.warps[0];
-        const int64_t W = p.warps[r];
-        left = cnt = hl = b = s = rounds = 0;
-        if (w >= W) return;
-        const int np = passes(p);
+        const int64_t w = warp();
+        left = cnt = hl = b = s = r = rounds = 0;
+        if (w >= p.warps) return;
+        const int np = p.passes[0] + p.passes[1];
         int64_t first, count;
-        rest(p, w, W, np, &first, &count);
-        rounds = p.rounds[r];
+        rest(p, w, np, &first, &count);
+        rounds = p.rounds;
         left = rounds * np + (int)count;
-        if (rounds > 0) start(p, grp, w * np, np);
-        else start(p, grp, first, np);
+        start(p, grp, rounds > 0 ? w * np : first, np);
     }
-    __device__ __forceinline__ int passes(const RopeParams &p) const {
-        return BOTH ? p.passes[0] + p.passes[1] : p.passes[r];
+    static __device__ __forceinline__ int64_t warp() {
+        return (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     }
     // The share of warp w in the passes over the tokens behind the whole rounds.
-    __device__ __forceinline__ void rest(const RopeParams &p, int64_t w, int64_t W, int np, int64_t *first,
-                                         int64_t *count) const {
-        const int64_t done = p.rounds[r] * W * np, U = p.units[r] - done, each = rope_div(U, W), more = U - each * W;
+    static __device__ __forceinline__ void rest(const RopeParams &p, int64_t w, int np, int64_t *first, int64_t *count) {
+        const int64_t W = p.warps, done = p.rounds * W * np, U = p.units - done, each = rope_div(U, W), more = U - each * W;
         *first = done + each * w + (w < more ? w : more);
         *count = each + (w < more ? 1 : 0);
     }
     __device__ __forceinline__ void start(const RopeParams &p, int grp, int64_t u, int np) {
         const int64_t t = rope_div(u, np);
         int blk = (int)(u - t * np);
-        if (BOTH) {
-            r = blk >= p.passes[0];
-            if (r) blk -= p.passes[0];
-        }
+        r = blk >= p.passes[0];
+        if (r) blk -= p.passes[0];
         cnt = p.passes[r] - blk;
         hl = p.heads[r] - blk * GU - grp;
         b = (int)rope_div(t, p.S);
@@ -120,22 +111,21 @@ template <int GU, bool BOTH> struct RopeCursor {
             hl -= GU;
             return 0;
         }
-        const bool keys = BOTH && r == 0 && p.passes[1] > 0;
-        if (BOTH) r = keys;
+        const bool keys = r == 0 && p.passes[1] > 0;
+        r = keys;
         cnt = p.passes[r];
         hl = p.heads[r] - grp;
         if (keys) return 1;
         --rounds;
         const bool far = rounds > 0;
-        b += far ? p.step_b[r] : 0;
-        const uint32_t to = (uint32_t)s + (far ? p.step_s[r] : 1), S = (uint32_t)p.S;  // below 2^32
+        b += far ? p.step_b : 0;
+        const uint32_t to = (uint32_t)s + (far ? p.step_s : 1), S = (uint32_t)p.S;  // below 2^32
         s = (int)(to >= S ? to - S : to);
         b += to >= S;
         if (rounds == 0) {
-            int64_t w = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), first, count;
-            if (r) w -= p.warps[0];
-            const int np = passes(p);
-            rest(p, w, p.warps[r], np, &first, &count);
+            int64_t first, count;
+            const int np = p.passes[0] + p.passes[1];
+            rest(p, warp(), np, &first, &count);
             start(p, grp, first, np);
         }
         return 2;
@@ -153,23 +143,39 @@ template <int GU, bool BOTH> struct RopeCursor {
 };
 
 // The backward's column sums of a CTA: acc[warp][D] in shared memory, each
-// warp's own row filled, added in the order of the warps into the CTA's
-// partial row [2][D] (or [1][D] without keys) of block `which`.
-__device__ __forceinline__ void rope_partial(const RopeParams &p, const float *acc, int which) {
+// warp's own row filled with its sums of tensor r, added in the order of the
+// warps into the CTA's partial row [2][D] (or [1][D] without keys) of block
+// `which`.
+__device__ __forceinline__ void rope_partial(const RopeParams &p, const float *acc, int which, int r) {
     const int n = p.D * (p.heads[1] ? 2 : 1);
-    float *row = p.ws + ((int64_t)which * gridDim.x + blockIdx.x) * n;
-    const int64_t first = (int64_t)blockIdx.x * kRopeWarps;
-    // warps below `mid` hold sums of queries, those below `top` of keys
-    const int64_t q = p.warps[0] - first, k = p.warps[0] + p.warps[1] - first;
-    const int mid = q < 0 ? 0 : q > kRopeWarps ? kRopeWarps : (int)q, top = k > kRopeWarps ? kRopeWarps : (int)k;
+    float *row = p.ws + ((int64_t)which * gridDim.x + blockIdx.x) * n + r * p.D;
     __syncthreads();
-    for (int c = threadIdx.x; c < n; c += kRopeCTA) {
-        const bool keys = c >= p.D;
+    for (int c = threadIdx.x; c < p.D; c += kRopeCTA) {
         float v = 0.f;
-        for (int w = keys ? mid : 0; w < (keys ? top : mid); ++w) v += acc[w * p.D + (keys ? c - p.D : c)];
+#pragma unroll
+        for (int w = 0; w < kRopeWarps; ++w) v += acc[w * p.D + c];
         row[c] = v;
     }
     __syncthreads();  // acc may be filled again
 }
+
+// The sums of the tensor that a warp is not working on: N float4 a lane.
+template <int N> struct RopeAside {
+    float4 v[N][32];
+    __device__ __forceinline__ void clear(int lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // Changes places with f[0 .. 2 M - 1], kept from entry `at` on.
+    template <int M> __device__ __forceinline__ void swap(float2 (&f)[2 * M], int at, int lane) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float4 t = v[at + i][lane];
+            v[at + i][lane] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+            f[2 * i] = make_float2(t.x, t.y);
+            f[2 * i + 1] = make_float2(t.z, t.w);
+        }
+    }
+};
 
 }  // namespace gbn

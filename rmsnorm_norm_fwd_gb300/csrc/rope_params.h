@@ -34,11 +34,11 @@ struct RopeParams {
     const float *inv_freq; // [rot / 2]
     int64_t pos_axis, pos_batch, pos_token;
     int64_t B, S;
-    int64_t units[2];      // passes over all tokens (a pass: the heads one warp works on at once)
-    int64_t warps[2];      // warps of the grid that take them
+    int64_t units;         // passes over all tokens (a pass: the heads one warp works on at once)
+    int64_t warps;         // warps of the grid that take them
     int passes[2];         // of a token
-    int rounds[2];         // whole tokens a warp (vectors)
-    int step_b[2], step_s[2];  // warps[i] tokens on, in batches and tokens
+    int rounds;            // whole tokens a warp
+    int step_b, step_s;    // warps tokens on, in batches and tokens
     int heads[2];
     int D, rot;
     int inter;             // pairs (2j, 2j + 1), else (j, j + rot / 2)
@@ -66,18 +66,20 @@ extern const RopeVariant kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 // On vectors of `vector` bytes, c of them for each half of a lane's 2 * half
 // elements, l lanes a head, u heads a lane and pass: passes in flight a warp, and
 // dynamic shared memory without the parameters (rings, tables of cosines and
-// sines, frequencies; the backward's column sums take the place of the rings).
+// sines, frequencies, the backward's sums of the other tensor; its column sums
+// take the place of the rings).
 constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
 constexpr int rope_fwd_smem(int vector, int c, int half, int l, int u) {
     return kRopeWarps * (kRopeFwdDepth * u * 64 * c * vector + 8 * half * l) + 12 * half * l;
 }
-constexpr int rope_bwd_smem(int vector, int c, int half, int l, int u) {
-    return kRopeWarps * (kRopeBwdDepth * u * (128 * c * vector + 256) + 8 * half * l) + 12 * half * l;
+constexpr int rope_bwd_smem(int vector, int c, int half, int l, int u, bool ln) {
+    return kRopeWarps * (kRopeBwdDepth * u * (128 * c * vector + 256) + 8 * half * l + half * (ln ? 512 : 256)) +
+           12 * half * l;
 }
 
 constexpr int kRopeVecLanes = 8;
 constexpr int kRopeLaneCounts[kRopeVecLanes] = {4, 5, 6, 8, 9, 10, 16, 32};  // lanes a head
-constexpr int kRopeVecKinds = 3;  // RopeKind
+constexpr int kRopeVecKinds = 4;  // RopeKind
 // For each direction and norm (rot: the rotation alone; b: backward) and vector.
 #define GBN_ROPE_VEC(M) \
     extern const RopeVariant kRopeVec_##M##_bf16v8[kRopeVecKinds][kRopeVecLanes], \

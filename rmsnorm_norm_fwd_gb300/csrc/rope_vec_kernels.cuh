@@ -138,8 +138,10 @@ template <int V> __device__ __forceinline__ void rope_get(const float *from, int
 }
 
 // What is rotated, fixed at compile time where it is common: the whole head, as
-// halves or as neighbours, or anything (read from the call, through selects).
-enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopeSome = 2 };
+// halves or as neighbours, a part of it as halves, or anything (read from the
+// call).
+enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopePart = 2, kRopeSome = 3 };
+constexpr bool rope_whole(int kind) { return kind == kRopeHalves || kind == kRopeNeighbours; }
 
 // The chunks of a lane: first elements, whether they are there, whether they are rotated.  Slot i of lane sl is number
 // i L + sl of the head.
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     RopeTurns<N> &turns = *reinterpret_cast<RopeTurns<N> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1);
     Table &tab = tables[warp];
-    RopeCursor<G * U, true> w(p, grp), ahead = w;  // the pass worked on, the pass to load
+    RopeCursor<G * U> w(p, grp), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, C, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     const int xes = rope_esize<XT>(p.xdt), yes = rope_esize<XT>(p.ydt);
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     }
                 }
             }
-            if constexpr (KIND == kRopeSome) {
+            if constexpr (!rope_whole(KIND)) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     sa[i] = ch.ra[i / HV] ? sa[i] : f2s(0.f);
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 float2 ta = inter ? f2swap(va[i]) : vb[i], tb = inter ? f2swap(vb[i]) : va[i];
-                if constexpr (KIND == kRopeSome) {  // an element that is not rotated takes nothing from another, not even a NaN
+                if constexpr (!rope_whole(KIND)) {  // an element that is not rotated takes nothing from another, not even a NaN
                     ta = ch.ra[i / HV] ? ta : f2s(0.f);
                     tb = ch.rb[i / HV] ? tb : f2s(0.f);
                 }
@@ -490,22 +492,25 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
         Raw x[U][2 * C][32], g[U][2 * C][32];
         float mean[U][32], rstd[U][32];
     };
-    // rings, tables, frequencies, gamma of the queries and of the keys; at the end the column sums [kRopeWarps][D] over the rings
+    // rings, sums aside, tables, frequencies, gamma of the queries and of the keys; at the end the column sums
+    // [kRopeWarps][D] over the rings
+    using Aside = RopeAside<H * (LN ? 2 : 1)>;
     extern __shared__ __align__(16) unsigned char rope_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const RopeLanes<L> lanes(lane);
     const int sl = lanes.sl, grp = lane < G * L ? lane / L : kRopeNoHead;
     Slot *ring = reinterpret_cast<Slot *>(rope_smem) + warp * DEPTH;
-    Table *tables = reinterpret_cast<Table *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps);
+    Aside *asides = reinterpret_cast<Aside *>(rope_smem + sizeof(Slot) * DEPTH * kRopeWarps), &aside = asides[warp];
+    Table *tables = reinterpret_cast<Table *>(asides + kRopeWarps);
     RopeTurns<N> &turns = *reinterpret_cast<RopeTurns<N> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1), *rope_acc = reinterpret_cast<float *>(rope_smem);
     Table &tab = tables[warp];
-    RopeCursor<G * U, false> w(p, grp), ahead = w;  // the pass worked on, the pass to load
+    RopeCursor<G * U> w(p, grp), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, C, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
-    const int r = w.r, xes = rope_esize<XT>(p.xdt), ges = rope_esize<XT>(p.ydt);
-    const char *x = ahead.at(p, p.x[r], V * xes), *g = ahead.at(p, p.g[r], V * ges);
-    const int64_t xs = p.x[r].head * (G * V * xes), gs = p.g[r].head * (G * V * ges);
+    const int xes = rope_esize<XT>(p.xdt), ges = rope_esize<XT>(p.ydt);
+    const char *x = ahead.at(p, p.x[ahead.r], V * xes), *g = ahead.at(p, p.g[ahead.r], V * ges);
+    int64_t xs = p.x[ahead.r].head * (G * V * xes), gs = p.g[ahead.r].head * (G * V * ges);
     int64_t stat = ahead.stat(p);
     auto load = [&](int slot) {
         if (ahead.left) {
@@ -526,8 +531,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 if constexpr (LN) rope_cp_bytes<4>(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true);
             }
             if (ahead.next(p, grp)) {
-                x = ahead.at(p, p.x[r], V * xes);
-                g = ahead.at(p, p.g[r], V * ges);
+                x = ahead.at(p, p.x[ahead.r], V * xes);
+                g = ahead.at(p, p.g[ahead.r], V * ges);
+                xs = p.x[ahead.r].head * (G * V * xes);
+                gs = p.g[ahead.r].head * (G * V * ges);
                 stat = ahead.stat(p);
             } else if (ahead.hl > 0) {
                 x += U * xs;
@@ -549,16 +556,25 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     float2 da[H], db[H], ea[H], eb[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) da[i] = db[i] = ea[i] = eb[i] = f2s(0.f);
+    aside.clear(lane);
+    auto swap = [&] {
+        aside.template swap<H / 2>(da, 0, lane);
+        aside.template swap<H / 2>(db, H / 2, lane);
+        if constexpr (LN) {
+            aside.template swap<H / 2>(ea, H, lane);
+            aside.template swap<H / 2>(eb, H + H / 2, lane);
+        }
+    };
     if (w.left) {
         const float inv = 1.f / (float)p.D;
-        char *y = w.at(p, p.y[r], V * xes);
-        const int64_t ys = p.y[r].head * (G * V * xes);
+        char *y = w.at(p, p.y[w.r], V * xes);
+        int64_t ys = p.y[w.r].head * (G * V * xes);
         int turn = 2;
         for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
-            const int hl = w.hl;
-            if (turn) tab.put(turns, p, pos, axis, lane, inter);
+            const int hl = w.hl, r = w.r;
+            if (turn == 2) tab.put(turns, p, pos, axis, lane, inter);
             turn = w.next(p, grp);
-            if (w.left && turn) pos = rope_position(p, w, lane);
+            if (w.left && turn == 2) pos = rope_position(p, w, lane);
             rope_cp_wait<DEPTH - 1>();
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                         auto turned = [&](float2 d, int at, bool rotated) {
                             const float c = tab.c[at], s = tab.s[at];
                             float2 m = f2swap(d);
-                            if constexpr (KIND == kRopeSome) m = rotated ? m : f2s(0.f);
+                            if constexpr (!rope_whole(KIND)) m = rotated ? m : f2s(0.f);
                             return make_float2(d.x * c - m.x * s, d.y * c + m.y * s);
                         };
 #pragma unroll
@@ -593,7 +609,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
                             float2 m = gb[i], n = ga[i];
-                            if constexpr (KIND == kRopeSome) {
+                            if constexpr (!rope_whole(KIND)) {
                                 m = ch.ra[i / HV] ? m : f2s(0.f);
                                 n = ch.ra[i / HV] ? n : f2s(0.f);
                             }
@@ -653,9 +669,17 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                     if (in && ch.okb[i]) rope_store<XT, V>(q + ch.b[i] * xes, p.xdt, tb + i * HV);
                 }
             }
-            if (!w.left) break;
-            if (turn) y = w.at(p, p.y[r], V * xes);
-            else y += U * ys;
+            if (!w.left) {
+                if (r) swap();
+                break;
+            }
+            if (turn) {
+                y = w.at(p, p.y[w.r], V * xes);
+                ys = p.y[w.r].head * (G * V * xes);
+                if (w.r != r) swap();
+            } else {
+                y += U * ys;
+            }
         }
     }
     __syncthreads();  // the rings of all warps have been read
@@ -693,11 +717,15 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
             }
         }
     };
-    columns(da, db);
-    rope_partial(p, rope_acc, 0);
-    if constexpr (LN) {
-        columns(ea, eb);
-        rope_partial(p, rope_acc, 1);
+    // the queries' sums are in the registers, the keys' aside
+    for (int r = 0; r < (p.heads[1] ? 2 : 1); ++r) {
+        if (r) swap();
+        columns(da, db);
+        rope_partial(p, rope_acc, 0, r);
+        if constexpr (LN) {
+            columns(ea, eb);
+            rope_partial(p, rope_acc, 1, r);
+        }
     }
 }
 

@@ -41,10 +41,11 @@ def test_parts_of_heads(dt, v, L):
         for mode in (False, True):
             run_forward(mode, 1, 5, 7, 3, D, rot, dt=dt, inter=inter)
             run_backward(mode, 1, 5, 7, 3, D, rot, dt=dt, inter=inter)
-        assert names()[:2] == [f"vec{v}x{L}"] * 2
+        name = f"vec{v}x{L}" + ("p" if not inter and L in (4, 8, 16) else "")
+        assert names()[:2] == [name] * 2
         if rot:
             run_forward(None, 1, 5, 7, 3, D, rot, dt=dt, inter=inter)
-            assert names()[2] == f"vec{v}x{L}"
+            assert names()[2] == name
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
