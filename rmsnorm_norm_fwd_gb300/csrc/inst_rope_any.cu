@@ -16,4 +16,5 @@ template <bool LN, int L, int C, int B> constexpr RopeVariant bwd(const char *na
 const RopeVariant kRopeFwdAny[3][kRopeAnySizes] = {GBN_SIZES(fwd, kRopeOnly), GBN_SIZES(fwd, kRopeRms),
                                                    GBN_SIZES(fwd, kRopeLn)};
 const RopeVariant kRopeBwdAny[2][kRopeAnySizes] = {GBN_SIZES(bwd, false), GBN_SIZES(bwd, true)};
+const void *const kRopeColumns = (const void *)&rope_columns;
 }  // namespace gbn

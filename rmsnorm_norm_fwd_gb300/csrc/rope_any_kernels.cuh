@@ -447,4 +447,35 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
     }
 }
 
+// out[c] = sum over the P partial rows of ws [2][P][N] (block blockIdx.y), 32
+// columns a CTA, warp w the rows w, w + 32, ..., then the warps in order.  A head
+// has few columns, so one CTA for all of them (as for long rows) would read the
+// rows one latency after another.
+constexpr int kRopeColumnsCTA = 1024;
+__global__ void __launch_bounds__(kRopeColumnsCTA) rope_columns(const float *ws, int P, int N, float *out0, float *out1) {
+    __shared__ float part[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    float *out = blockIdx.y ? out1 : out0;
+    pdl_wait_primary();  // launched right behind the kernel that writes ws
+    if (!out) return;
+    const float *from = ws + (int64_t)blockIdx.y * P * N + col;
+    float v = 0.f;
+    if (col < N) {
+        constexpr int AT_ONCE = 10;  // 304 rows (two CTAs an SM) are one round
+        for (int p0 = warp; p0 < P; p0 += 32 * AT_ONCE) {
+            float a[AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) a[i] = p0 + 32 * i < P ? __ldg(from + (int64_t)(p0 + 32 * i) * N) : 0.f;
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) v += a[i];
+        }
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp || col >= N) return;
+#pragma unroll
+    for (int i = 1; i < 32; ++i) v += part[i][lane];
+    out[col] = v;
+}
+
 }  // namespace gbn

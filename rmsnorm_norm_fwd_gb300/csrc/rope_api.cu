@@ -238,6 +238,24 @@ struct Kernel {
     int slot;   // its place in the cache of what a device holds
 };
 
+// Column sums of the P partial rows into dgamma and dbeta (0 rows: zeros).  The
+// launch may begin while the rows' kernel drains; it waits for that before it reads.
+int columns(int is_ln, const float *ws, int P, int N, float *dgamma, float *dbeta, cudaStream_t st) {
+    if (!dgamma && !dbeta) return GBNORM_OK;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((N + 31) / 32), is_ln ? 2u : 1u);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = P > 0 ? 1 : 0;
+    void *args[5] = {&ws, &P, &N, &dgamma, &dbeta};
+    if (cudaLaunchKernelExC(&cfg, kRopeColumns, args) != cudaSuccess) return GBNORM_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? GBNORM_OK : GBNORM_ERR_CUDA;
+}
+
 int any_size(int D, int rot) {  // 32 << that pairs hold a head
     const int pairs = rot / 2 + (D - rot + 1) / 2;
     int lg = 0;
@@ -472,7 +490,7 @@ int qk_norm_rope_bwd(int is_layernorm, const gbnorm_rope_t *r, const gbnorm_head
         e = launch(k.f, P, (size_t)k.smem, &p, stream);
         if (e != GBNORM_OK) return e;
     }
-    return host_colreduce(is_layernorm, static_cast<const float *>(workspace), P, N, dgamma, dbeta, P > 0, stream);
+    return columns(is_layernorm, static_cast<const float *>(workspace), (int)P, (int)N, dgamma, dbeta, stream);
 }
 
 int rope_fwd(const gbnorm_rope_t *r, const gbnorm_heads_t *x, const gbnorm_heads_t *y, gbnorm_stream_t stream) {

@@ -62,6 +62,8 @@ struct RopeVariant {
 constexpr int kRopeAnySizes = 5;
 extern const RopeVariant kRopeFwdAny[3][kRopeAnySizes];
 extern const RopeVariant kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
+// The backward's second stage: (ws, int P, int N, dgamma, dbeta), CTAs of 1024 for 32 columns each.
+extern const void *const kRopeColumns;
 
 // On vectors of `vector` bytes, c of them for each half of a lane's 2 * half
 // elements, l lanes a head, u heads a lane and pass: passes in flight a warp, and
