@@ -128,13 +128,29 @@ class _Call:
             raise ValueError(f"{name} must have unit stride in its last dimension")
         return t.data_ptr(), batch, token, head
 
-    def out(self, yq, yk, q, k, dtype):
-        """The two outputs, allocated where they are not given."""
-        if yq is None:
-            yq = torch.empty_like(q, dtype=dtype, memory_format=_CONTIGUOUS)
-        if yk is None and k is not None:
-            yk = torch.empty_like(k, dtype=dtype, memory_format=_CONTIGUOUS)
-        return yq, yk
+    def out(self, name, yq, yk, q, k, dtype):
+        """The two outputs, allocated where they are not given, and their gbnorm_heads_t."""
+        if yq is not None or (yk is not None and k is not None):
+            if yq is None:
+                yq = torch.empty_like(q, dtype=dtype, memory_format=_CONTIGUOUS)
+            if yk is None and k is not None:
+                yk = torch.empty_like(k, dtype=dtype, memory_format=_CONTIGUOUS)
+            return yq, yk, self.heads(name, yq, yk, dtype)
+        D, tq, tk = self.D, self.hq * self.D, self.hk * self.D
+        yq = torch.empty_like(q, dtype=dtype, memory_format=_CONTIGUOUS)
+        if k is None:
+            return yq, None, _HEADS(yq.data_ptr(), self.S * tq, tq, D, 0, 0, 0, 0)
+        yk = torch.empty_like(k, dtype=dtype, memory_format=_CONTIGUOUS)
+        return yq, yk, _HEADS(yq.data_ptr(), self.S * tq, tq, D, yk.data_ptr(), self.S * tk, tk, D)
+
+    def sums(self, name, t, shape, needed):
+        """A float32 output, allocated where it is needed and not given, and its pointer."""
+        if t is not None:
+            return t, self.flat(name, t, shape)
+        if not needed:
+            return None, None
+        t = torch.empty(shape, dtype=torch.float32, device=self.dev)
+        return t, t.data_ptr()
 
     def pair(self, name, q, k, dtype):
         """Two pointers to [D] parameters."""
@@ -222,20 +238,16 @@ def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, pos
                                             beta_k, y_dtype, yq, yk, mean, rstd, save_stats, stream=stream)
     c = _Call("", q, k)
     dt = yq.dtype if yq is not None else y_dtype or q.dtype
-    yq, yk = c.out(yq, yk, q, k, dt)
-    stats = c.stats_shape()
-    if save_stats:
-        if rstd is None:
-            rstd = torch.empty(stats, dtype=torch.float32, device=c.dev)
-        if is_layernorm and mean is None:
-            mean = torch.empty(stats, dtype=torch.float32, device=c.dev)
     if not is_layernorm:
         mean = beta_q = beta_k = None
     pdt = _param_dtype(q.dtype, gamma_q, gamma_k, beta_q, beta_k)
-    c.go("qk_norm_rope_fwd", lib.qk_norm_rope_fwd, int(bool(is_layernorm)), eps,
-         c.rope(positions, rotary, q.dtype, dt, pdt), c.heads("", q, k, q.dtype), c.heads("y", yq, yk, dt),
-         c.pair("gamma", gamma_q, gamma_k, pdt), c.pair("beta", beta_q, beta_k, pdt), c.flat("mean", mean, stats),
-         c.flat("rstd", rstd, stats))
+    r, x = c.rope(positions, rotary, q.dtype, dt, pdt), c.heads("", q, k, q.dtype)
+    yq, yk, y = c.out("y", yq, yk, q, k, dt)
+    stats = c.stats_shape()
+    rstd, ps = c.sums("rstd", rstd, stats, save_stats)
+    mean, pm = c.sums("mean", mean, stats, save_stats and is_layernorm)
+    c.go("qk_norm_rope_fwd", lib.qk_norm_rope_fwd, int(bool(is_layernorm)), eps, r, x, y,
+         c.pair("gamma", gamma_q, gamma_k, pdt), c.pair("beta", beta_q, beta_k, pdt), pm, ps)
     return yq, yk, mean, rstd
 
 
@@ -266,26 +278,23 @@ def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean,
                                             stream=stream)
     c = _Call("", q, k)
     dt = q.dtype
-    dq, dk = c.out(dq, dk, q, k, dt)
-    sums, stats = (2 if c.hk else 1, c.D), c.stats_shape()
-    if dgamma is None and need_dgamma:
-        dgamma = torch.empty(sums, dtype=torch.float32, device=c.dev)
     if not is_layernorm:
-        dbeta = mean = None
-    elif dbeta is None and need_dbeta:
-        dbeta = torch.empty(sums, dtype=torch.float32, device=c.dev)
+        dbeta, mean, need_dbeta = None, None, False
     if rstd is None or (is_layernorm and mean is None):
         raise ValueError("rstd (and mean for LayerNorm) of the forward are needed")
+    pdt = _param_dtype(dt, gamma_q, gamma_k)
+    r, dy, x = c.rope(positions, rotary, dt, dyq.dtype, pdt), c.heads("dy", dyq, dyk, dyq.dtype), c.heads("", q, k, dt)
+    dq, dk, dx = c.out("d", dq, dk, q, k, dt)
+    sums, stats = (2 if c.hk else 1, c.D), c.stats_shape()
+    dgamma, pg = c.sums("dgamma", dgamma, sums, need_dgamma)
+    dbeta, pb = c.sums("dbeta", dbeta, sums, need_dbeta)
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(int(bool(is_layernorm)), c.B * c.S, c.hq, c.hk, c.D, c.dev),
                                 dtype=torch.uint8, device=c.dev)
     elif not workspace.is_contiguous() or workspace.get_device() != c.dev:
         raise ValueError(f"workspace must be contiguous on device {c.dev}")
-    pdt = _param_dtype(dt, gamma_q, gamma_k)
-    c.go("qk_norm_rope_bwd", lib.qk_norm_rope_bwd, int(bool(is_layernorm)),
-         c.rope(positions, rotary, dt, dyq.dtype, pdt), c.heads("dy", dyq, dyk, dyq.dtype), c.heads("", q, k, dt),
-         c.heads("d", dq, dk, dt), c.pair("gamma", gamma_q, gamma_k, pdt), c.flat("mean", mean, stats),
-         c.flat("rstd", rstd, stats), c.flat("dgamma", dgamma, sums), c.flat("dbeta", dbeta, sums),
+    c.go("qk_norm_rope_bwd", lib.qk_norm_rope_bwd, int(bool(is_layernorm)), r, dy, x, dx,
+         c.pair("gamma", gamma_q, gamma_k, pdt), c.flat("mean", mean, stats), c.flat("rstd", rstd, stats), pg, pb,
          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dgamma, dbeta
 
@@ -300,9 +309,9 @@ def rope_fwd(q, k, positions, rotary: Rotary, y_dtype=None, yq=None, yk=None, st
     dt = yq.dtype if yq is not None else y_dtype or q.dtype
     if rotary is None:
         raise ValueError("rotary is needed")
-    yq, yk = c.out(yq, yk, q, k, dt)
-    c.go("rope_fwd", lib.rope_fwd, c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k, q.dtype),
-         c.heads("y", yq, yk, dt))
+    r, x = c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k, q.dtype)
+    yq, yk, y = c.out("y", yq, yk, q, k, dt)
+    c.go("rope_fwd", lib.rope_fwd, r, x, y)
     return yq, yk
 
 
@@ -315,9 +324,9 @@ def rope_bwd(dyq, dyk, positions, rotary: Rotary, dx_dtype=None, dq=None, dk=Non
     dt = dq.dtype if dq is not None else dx_dtype or dyq.dtype
     if rotary is None:
         raise ValueError("rotary is needed")
-    dq, dk = c.out(dq, dk, dyq, dyk, dt)
-    c.go("rope_bwd", lib.rope_bwd, c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype),
-         c.heads("dy", dyq, dyk, dyq.dtype), c.heads("d", dq, dk, dt))
+    r, dy = c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype), c.heads("dy", dyq, dyk, dyq.dtype)
+    dq, dk, dx = c.out("d", dq, dk, dyq, dyk, dt)
+    c.go("rope_bwd", lib.rope_bwd, r, dy, dx)
     return dq, dk
 
 
