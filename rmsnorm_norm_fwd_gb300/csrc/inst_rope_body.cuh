@@ -1,8 +1,9 @@
 // Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V, GBN_C, the
-// type and elements of a vector and the vectors of half a lane's elements.  Defines kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE 2 (16-byte vectors): whole
-// heads rotated as halves or as neighbours, and parts rotated as halves, have kernels of their own up to 16 lanes (prefill
-// of 16384 tokens of 40 heads of 128 54 us against 60 us, backward of heads of 256 with a quarter rotated 56 us against 57
-// us); 1, 0: all run on the kernels for any rotation, and on fewer numbers of lanes.
+// type and elements of a vector and the vectors of half a lane's elements.  Defines kRopeVec_<GBN_NAME>[kind][lanes a
+// head].  GBN_WHOLE 2: whole heads rotated as halves or as neighbours, and parts rotated as halves, have kernels of their
+// own up to 16 lanes (prefill of 16384 tokens of 40 heads of 128 54 us against 60 us; 32 heads of 72, 8-byte vectors, 38
+// us against 45 us, their rotation 33 us against 37 us).  1, 0: all run on the kernels for any rotation, and on fewer
+// numbers of lanes: the backward on 8-byte vectors (64.3 us against 65.8 us) and what is rarer.
 #include "rope_vec_kernels.cuh"
 
 #ifndef GBN_CAT
@@ -22,6 +23,8 @@
 #endif
 #define GBN_FU(KIND) (GBN_MODE == 0 && rope_whole(KIND) ? 2 : 1)
 #define GBN_BU(KIND) 1
+// Heads a lane and pass: two for the rotation alone (26520 tokens of 80 heads 179 us, 194 us with one), one for the norms
+// (prefill of 16384 tokens 57.8 us, 64.7 us with two; backward 98 us, 108 us with two).
 #define GBN_ANY(L) GBN_K(L, kRopeSome, "")
 #if GBN_WHOLE == 2
 #define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(6), GBN_ANY(8), GBN_ANY(9), GBN_ANY(10), GBN_ANY(16), GBN_ANY(32)}

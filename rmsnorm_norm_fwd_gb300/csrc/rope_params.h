@@ -70,6 +70,8 @@ extern const void *const kRopeColumns;
 // dynamic shared memory without the parameters (rings, tables of cosines and
 // sines, frequencies, the backward's sums of the other tensor; its column sums
 // take the place of the rings).
+// Two passes: forward of 16384 tokens of 40 heads of 128 54.5 us, 56.9 us with
+// three, 58.6 us with four; backward 85.0, 88.3 and 89.2 us then.
 constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
 constexpr int rope_fwd_smem(int vector, int c, int half, int l, int u) {
     return kRopeWarps * (kRopeFwdDepth * u * 64 * c * vector + 8 * half * l) + 12 * half * l;
