@@ -373,6 +373,9 @@ int gbnorm_q8_last_variant(int what, char *buf, size_t len);
  * are parts of one larger tensor that repeats with one of their strides (for
  * instance queries and keys of a packed projection).  Pointers not aligned
  * to their elements are rejected.
+ * Heads move as vectors of 16, 8 or 4 bytes where base, strides, dim and rot
+ * (pairs as neighbours) or rot / 2 (as halves) are multiples of them, up to 512
+ * elements (fp32: 256); anything else element by element.
  * Frequencies that are infinite, NaN or 2^87 and more make their pairs NaN.
  * Status codes, ownership, streams and threading as above.
  */

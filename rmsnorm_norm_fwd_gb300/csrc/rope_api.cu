@@ -178,7 +178,7 @@ int take(const gbnorm_heads_t *h, const Shape &s, int dtype, bool out, RopeHeads
     return GBNORM_OK;
 }
 
-// The plain arrays of a call, all read: parameters, statistics, positions, frequencies.
+// Bytes that the positions span.
 int64_t pos_bytes(const RopeParams &p) {
     if (!p.pos || p.B * p.S == 0) return 0;
     return ((p.axes - 1) * p.pos_axis + (p.B - 1) * p.pos_batch + (p.S - 1) * p.pos_token + 1) * (p.pos64 ? 8 : 4);
@@ -312,7 +312,8 @@ Kernel pick(int mode, RopeParams &p) {
                     }
                 // gamma (and beta) of both tensors as fp32 behind the rings
                 const int par = mode == kRopeOnly ? 0 : mode == kRopeLn ? 16 * p.D : 8 * p.D;
-                return {k.f, k.name, 32 / k.lanes * k.u, k.smem + par, ((m * kVecTypes + t) * kRopeVecKinds + kind) * kRopeVecLanes + l};
+                return {k.f, k.name, 32 / k.lanes * k.u, k.smem + par,
+                        ((m * kVecTypes + t) * kRopeVecKinds + kind) * kRopeVecLanes + l};
             }
     }
     const int n = any_size(p.D, p.rot), slot = 5 * kVecTypes * kRopeVecKinds * kRopeVecLanes + m * kRopeAnySizes + n;
@@ -328,8 +329,7 @@ int resident(const Kernel &k, const HostDevice &d, int *out) {
     int o = c.load(std::memory_order_relaxed);
     if (o == 0) {
         // heads of several sizes share a kernel: allow for the parameters (8 KB) or column sums (32 KB) of any
-        if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 k.smem + 32 * 1024) != cudaSuccess ||
+        if (cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem + 32 * 1024) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k.f, kRopeCTA, (size_t)k.smem) != cudaSuccess)
             return GBNORM_ERR_CUDA;
         if (o <= 0) return GBNORM_ERR_UNSUPPORTED;
