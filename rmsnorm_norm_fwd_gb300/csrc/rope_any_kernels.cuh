@@ -82,7 +82,8 @@ template <int L, int C> struct RopeSlots {
     static __device__ __forceinline__ void widen(const uint32_t (&r)[C], int dt, float2 (&f)[C / 2]) {
         if (dt == kF32) {
 #pragma unroll
-            for (int i = 0; i < C / 2; ++i) f[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            for (int i = 0; i < C / 2; ++i)
+                f[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         } else if (dt == kBF16) {
 #pragma unroll
             for (int i = 0; i < C / 2; ++i)
@@ -139,7 +140,8 @@ template <int L, int C> struct RopeSlotTable {
             s[RopeSlots<L, C>::place(j)] = 0.f;
         }
     }
-    __device__ __forceinline__ void put(const uint64_t *turns, const float *bad, const RopeParams &p, int64_t pos, int lane) {
+    __device__ __forceinline__ void put(const uint64_t *turns, const float *bad, const RopeParams &p, int64_t pos,
+                                        int lane) {
         __syncwarp();  // the last token's have been read
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -455,7 +457,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
 // has few columns, so one CTA for all of them (as for long rows) would read the
 // rows one latency after another.
 constexpr int kRopeColumnsCTA = 1024;
-__global__ void __launch_bounds__(kRopeColumnsCTA) rope_columns(const float *ws, int P, int N, float *out0, float *out1) {
+__global__ void __launch_bounds__(kRopeColumnsCTA)
+    rope_columns(const float *ws, int P, int N, float *out0, float *out1) {
     __shared__ float part[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
     float *out = blockIdx.y ? out1 : out0;

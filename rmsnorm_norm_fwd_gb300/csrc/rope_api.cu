@@ -95,7 +95,8 @@ bool may_overlap(const Box &a, const Box &b) {
             if (x->n[i] <= 1 || per <= 0) continue;
             const int64_t wa = window(a, per), wb = window(b, per);
             if (!wa || !wb) continue;
-            const int64_t d = (int64_t)((b.p % (uintptr_t)per + (uintptr_t)per - a.p % (uintptr_t)per) % (uintptr_t)per);
+            const uintptr_t u = (uintptr_t)per;
+            const int64_t d = (int64_t)((b.p % u + u - a.p % u) % u);
             if (d >= wa && per - d >= wb) return false;
         }
     return true;
@@ -213,8 +214,8 @@ int64_t share(RopeParams *p, const Shape &s, int64_t at_once, int64_t per_sm, co
     }
     p->warps = std::min(p->units, cap * kRopeWarps);
     if (p->units / p->warps >= INT32_MAX) return -1;
-    // whole tokens as a front (prefill of 16384 tokens 62 -> 57 us, backward 97 -> 88 us) where a warp has four or more;
-    // below, the uneven rest costs more than the order gives (8192 tokens rotated: 21.7 us without, 23.0 us with)
+    // whole tokens as a front (prefill of 16384 tokens 62 -> 57 us, backward 97 -> 88 us) where a warp has four or
+    // more; below, the uneven rest costs more than the order gives (8192 tokens rotated: 21.7 us without, 23.0 us with)
     const int64_t rounds = s.tokens() / p->warps;
     p->rounds = rounds < 4 ? 0 : (int)rounds;
     p->step_b = (int)(p->warps / s.S);
@@ -298,7 +299,7 @@ Kernel pick(int mode, RopeParams &p) {
     if (v) {
         const int chunks = p.D / v, rot = p.rot / v;
         const int slots = p.inter ? (chunks + 1) / 2 : rot / 2 + (chunks - rot + 1) / 2;
-        const int kind = p.rot == p.D ? p.inter : p.inter ? 3 : 2;  // as RopeKind
+        const int kind = p.rot == p.D ? p.inter : 2;  // as RopeKind
         const int t = p.xdt != p.ydt ? 6 : p.xdt + (v == 2 ? 0 : v == 4 ? 3 : 6);
         const int c = p.xdt == p.ydt && p.xdt == GBNORM_F32 ? 4 / v : 8 / v;  // slots a lane
         for (int l = 0; l < kRopeVecLanes; ++l)
@@ -427,7 +428,8 @@ int qk_norm_rope_fwd(int is_layernorm, float eps, const gbnorm_rope_t *r, const 
     return run_fwd(is_layernorm ? kRopeLn : kRopeRms, &p, s, stream);
 }
 
-size_t qk_norm_rope_bwd_workspace_size(int is_layernorm, int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim) {
+size_t qk_norm_rope_bwd_workspace_size(int is_layernorm, int64_t tokens, int64_t heads_q, int64_t heads_k,
+                                       int64_t dim) {
     const Shape s{1, tokens, {heads_q, heads_k}, dim};
     HostDevice d;
     if ((is_layernorm != 0 && is_layernorm != 1) || !valid_shape(s) || host_device(&d) != GBNORM_OK) return 0;

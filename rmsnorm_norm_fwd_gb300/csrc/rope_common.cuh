@@ -89,8 +89,10 @@ template <int GU> struct RopeCursor {
         return (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     }
     // The share of warp w in the passes over the tokens behind the whole rounds.
-    static __device__ __forceinline__ void rest(const RopeParams &p, int64_t w, int np, int64_t *first, int64_t *count) {
-        const int64_t W = p.warps, done = p.rounds * W * np, U = p.units - done, each = rope_div(U, W), more = U - each * W;
+    static __device__ __forceinline__ void rest(const RopeParams &p, int64_t w, int np, int64_t *first,
+                                                int64_t *count) {
+        const int64_t W = p.warps, done = p.rounds * W * np, U = p.units - done, each = rope_div(U, W);
+        const int64_t more = U - each * W;
         *first = done + each * w + (w < more ? w : more);
         *count = each + (w < more ? 1 : 0);
     }

@@ -66,7 +66,7 @@ extern const RopeVariant kRopeBwdAny[2][kRopeAnySizes];  // RMSNorm, LayerNorm
 extern const void *const kRopeColumns;
 
 // On vectors of `vector` bytes, c of them for each half of a lane's 2 * half
-// elements, l lanes a head, u heads a lane and pass: passes in flight a warp, and
+// elements, l lanes a head, u heads a lane and pass (backward: one): passes in flight a warp, and
 // dynamic shared memory without the parameters (rings, tables of cosines and
 // sines, frequencies, the backward's sums of the other tensor; its column sums
 // take the place of the rings).
@@ -76,14 +76,14 @@ constexpr int kRopeFwdDepth = 2, kRopeBwdDepth = 2;
 constexpr int rope_fwd_smem(int vector, int c, int half, int l, int u) {
     return kRopeWarps * (kRopeFwdDepth * u * 64 * c * vector + 8 * half * l) + 12 * half * l;
 }
-constexpr int rope_bwd_smem(int vector, int c, int half, int l, int u, bool ln) {
-    return kRopeWarps * (kRopeBwdDepth * u * (128 * c * vector + 256) + 8 * half * l + half * (ln ? 512 : 256)) +
+constexpr int rope_bwd_smem(int vector, int c, int half, int l, bool ln) {
+    return kRopeWarps * (kRopeBwdDepth * (128 * c * vector + 256) + 8 * half * l + half * (ln ? 512 : 256)) +
            12 * half * l;
 }
 
-constexpr int kRopeVecLanes = 8;
-constexpr int kRopeLaneCounts[kRopeVecLanes] = {4, 5, 6, 8, 9, 10, 16, 32};  // lanes a head
-constexpr int kRopeVecKinds = 4;  // RopeKind
+constexpr int kRopeVecLanes = 7;
+constexpr int kRopeLaneCounts[kRopeVecLanes] = {4, 5, 6, 8, 10, 16, 32};  // lanes a head
+constexpr int kRopeVecKinds = 3;  // RopeKind
 // For each direction and norm (rot: the rotation alone; b: backward) and vector.
 #define GBN_ROPE_VEC(M) \
     extern const RopeVariant kRopeVec_##M##_bf16v8[kRopeVecKinds][kRopeVecLanes], \

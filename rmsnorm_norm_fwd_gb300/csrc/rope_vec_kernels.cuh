@@ -42,7 +42,9 @@ template <> struct RopeRaw<kBF16, 2> { uint32_t v; };
 // Types that differ within a call, read from it: 16 bytes hold four elements of any.
 constexpr int kMixed = 3;
 template <> struct RopeRaw<kMixed, 4> { uint4 v; };
-template <int XT> __device__ __forceinline__ int rope_esize(int dt) { return XT == kMixed ? esize(dt) : XT == kF32 ? 4 : 2; }
+template <int XT> __device__ __forceinline__ int rope_esize(int dt) {
+    return XT == kMixed ? esize(dt) : XT == kF32 ? 4 : 2;
+}
 
 template <int XT> __device__ __forceinline__ float2 rope_pair(uint32_t w) {
     if constexpr (XT == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -107,12 +109,15 @@ template <int XT, int V> __device__ __forceinline__ void rope_store(char *p, int
 // without an element fill with zeros (`from` is then any valid address).
 template <int BYTES> __device__ __forceinline__ void rope_cp_bytes(void *to, const void *from, bool in) {
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0)
+                     : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? BYTES : 0), "n"(BYTES)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(to)), "l"(from),
+                     "r"(in ? BYTES : 0), "n"(BYTES)
                      : "memory");
 }
-template <int XT, int V> __device__ __forceinline__ void rope_cp(RopeRaw<XT, V> *to, const char *from, bool in, int dt) {
+template <int XT, int V>
+__device__ __forceinline__ void rope_cp(RopeRaw<XT, V> *to, const char *from, bool in, int dt) {
     if constexpr (XT == kMixed) {
         if (dt == kF32) rope_cp_bytes<16>(to, from, in);
         else rope_cp_bytes<8>(to, from, in);
@@ -121,7 +126,9 @@ template <int XT, int V> __device__ __forceinline__ void rope_cp(RopeRaw<XT, V> 
     }
 }
 __device__ __forceinline__ void rope_cp_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void rope_cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ void rope_cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Values that a lane reads V at a time lie in shared memory as planes of four
 // (element 8 c + 4 h + i at h n / 2 + 4 c + i of n), so that the lanes' 16-byte
@@ -148,10 +155,8 @@ template <int V> __device__ __forceinline__ void rope_get(const float *from, int
 }
 
 // What is rotated, fixed at compile time where it is common: the whole head, as
-// halves or as neighbours, a part of it as halves, or anything (read from the
-// call).
-enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopePart = 2, kRopeSome = 3 };
-constexpr bool rope_whole(int kind) { return kind == kRopeHalves || kind == kRopeNeighbours; }
+// halves or as neighbours, or anything (read from the call, through selects).
+enum RopeKind : int { kRopeHalves = 0, kRopeNeighbours = 1, kRopeSome = 2 };
 
 // The chunks of a lane: first elements, whether they are there, whether they are rotated.  Slot i of lane sl is number
 // i L + sl of the head.
@@ -187,7 +192,9 @@ template <int V, int C, int L, int KIND> struct RopeChunks {
 
 // Sums over the L lanes of a head.  Powers of two by a butterfly.  Else by
 // rotations within the group, whose order of additions differs between lanes:
-// sums over 3 lanes are two rotations more, over 5 a chain (2, 4, 5).
+// halves first where L is even, then sums of 3 by two rotations, of 5 by a chain
+// of 2, 4 and 5.  (Heads of 80 on five lanes instead of eight: 16.4 us against 19.0
+// us for 4099 tokens of 32, LayerNorm.)
 template <int L> struct RopeLanes {
     static constexpr bool POW2 = (L & (L - 1)) == 0;
     int sl, base;
@@ -200,17 +207,13 @@ template <int L> struct RopeLanes {
         if constexpr (POW2) {
             group_sum<L, R>(v);
         } else {
-            static_assert(L == 5 || L == 6 || L == 9 || L == 10, "lanes a head");
+            static_assert(L == 5 || L == 6 || L == 10, "lanes a head");
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 float t = v[i];
                 if constexpr (L == 6) t += from(t, 3);
                 if constexpr (L == 10) t += from(t, 5);
-                if constexpr (L == 9) {
-                    const float a = from(t, 3), b = from(t, 6);
-                    t += a + b;
-                }
-                if constexpr (L == 6 || L == 9) {
+                if constexpr (L == 6) {
                     const float a = from(t, 1), b = from(t, 2);
                     v[i] = t + (a + b);
                 } else {
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     }
                 }
             }
-            if constexpr (!rope_whole(KIND)) {
+            if constexpr (KIND == kRopeSome) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     sa[i] = ch.ra[i / HV] ? sa[i] : f2s(0.f);
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 float2 ta = inter ? f2swap(va[i]) : vb[i], tb = inter ? f2swap(vb[i]) : va[i];
-                if constexpr (!rope_whole(KIND)) {  // an element that is not rotated takes nothing from another, not even a NaN
+                if constexpr (KIND == kRopeSome) {  // what is not rotated takes nothing from another, not even a NaN
                     ta = ch.ra[i / HV] ? ta : f2s(0.f);
                     tb = ch.rb[i / HV] ? tb : f2s(0.f);
                 }
@@ -492,15 +495,15 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     }
 }
 
-template <bool LN, int XT, int V, int C, int L, int KIND, int U, int MINB>
+template <bool LN, int XT, int V, int C, int L, int KIND, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
     constexpr int G = 32 / L, HV = V / 2, H = C * HV, N = C * V * L, DEPTH = kRopeBwdDepth;
     using Table = RopeTable<V, N>;
     using Raw = RopeRaw<XT, V>;
     struct Slot {
-        Raw x[U][2 * C][32], g[U][2 * C][32];
-        float mean[U][32], rstd[U][32];
+        Raw x[2 * C][32], g[2 * C][32];
+        float mean[32], rstd[32];
     };
     // rings, sums aside, tables, frequencies, gamma of the queries and of the keys; at the end the column sums
     // [kRopeWarps][D] over the rings
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     RopeTurns<N> &turns = *reinterpret_cast<RopeTurns<N> *>(tables + kRopeWarps);
     float *par = reinterpret_cast<float *>(&turns + 1), *rope_acc = reinterpret_cast<float *>(rope_smem);
     Table &tab = tables[warp];
-    RopeCursor<G * U> w(p, grp), ahead = w;  // the pass worked on, the pass to load
+    RopeCursor<G> w(p, grp), ahead = w;  // the pass worked on, the pass to load
     const RopeChunks<V, C, L, KIND> ch(p, sl, lane < G * L);
     const bool inter = KIND == kRopeNeighbours || (KIND == kRopeSome && p.inter);
     const int xes = rope_esize<XT>(p.xdt), ges = rope_esize<XT>(p.ydt);
@@ -525,21 +528,17 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     auto load = [&](int slot) {
         if (ahead.left) {
             Slot &to = ring[slot];
+            // a lane without a head in the pass reads another with a gradient of zeros, and stores nothing
+            const bool in = ahead.hl > 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // a lane without a head in the pass reads another with a gradient of zeros, and stores nothing
-                const bool in = ahead.hl > u * G;
-                const char *q = u == 0 ? x : x + (in ? u * xs : 0), *d = u == 0 ? g : g + (in ? u * gs : 0);
-#pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    rope_cp(&to.x[u][2 * i][lane], q + ch.a[i] * xes, ch.oka[i], p.xdt);
-                    rope_cp(&to.x[u][2 * i + 1][lane], q + ch.b[i] * xes, ch.okb[i], p.xdt);
-                    rope_cp(&to.g[u][2 * i][lane], d + ch.a[i] * ges, in && ch.oka[i], p.ydt);
-                    rope_cp(&to.g[u][2 * i + 1][lane], d + ch.b[i] * ges, in && ch.okb[i], p.ydt);
-                }
-                rope_cp_bytes<4>(&to.rstd[u][lane], p.rstd + stat + (in ? u * G : 0), true);
-                if constexpr (LN) rope_cp_bytes<4>(&to.mean[u][lane], p.mean + stat + (in ? u * G : 0), true);
+            for (int i = 0; i < C; ++i) {
+                rope_cp(&to.x[2 * i][lane], x + ch.a[i] * xes, ch.oka[i], p.xdt);
+                rope_cp(&to.x[2 * i + 1][lane], x + ch.b[i] * xes, ch.okb[i], p.xdt);
+                rope_cp(&to.g[2 * i][lane], g + ch.a[i] * ges, in && ch.oka[i], p.ydt);
+                rope_cp(&to.g[2 * i + 1][lane], g + ch.b[i] * ges, in && ch.okb[i], p.ydt);
             }
+            rope_cp_bytes<4>(&to.rstd[lane], p.rstd + stat, true);
+            if constexpr (LN) rope_cp_bytes<4>(&to.mean[lane], p.mean + stat, true);
             if (ahead.next(p, grp)) {
                 x = ahead.at(p, p.x[ahead.r], V * xes);
                 g = ahead.at(p, p.g[ahead.r], V * ges);
@@ -547,9 +546,9 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 gs = p.g[ahead.r].head * (G * V * ges);
                 stat = ahead.stat(p);
             } else if (ahead.hl > 0) {
-                x += U * xs;
-                g += U * gs;
-                stat += U * G;
+                x += xs;
+                g += gs;
+                stat += G;
             }
         }
         rope_cp_end();
@@ -581,103 +580,99 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
         int64_t ys = p.y[w.r].head * (G * V * xes);
         int turn = 2;
         for (int slot = 0;; slot = slot == DEPTH - 1 ? 0 : slot + 1) {
-            const int hl = w.hl, r = w.r;
+            const int r = w.r;
+            const bool in = w.hl > 0;
             if (turn == 2) tab.put(turns, p, pos, axis, lane, inter);
             turn = w.next(p, grp);
             if (w.left && turn == 2) pos = rope_position(p, w, lane);
             rope_cp_wait<DEPTH - 1>();
+            // the gradient turned back (the sign of s is the transpose's)
+            float2 ta[H], tb[H];
+            {
+                float2 ga[H], gb[H];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // the gradient turned back (the sign of s is the transpose's)
-                float2 ta[H], tb[H];
-                {
-                    float2 ga[H], gb[H];
+                for (int i = 0; i < C; ++i) {
+                    rope_unpack<XT, V>(ring[slot].g[2 * i][lane], p.ydt, ga + i * HV);
+                    rope_unpack<XT, V>(ring[slot].g[2 * i + 1][lane], p.ydt, gb + i * HV);
+                }
+                if (inter) {
+                    auto turned = [&](float2 d, int at, bool rotated) {
+                        const float c = tab.c[at], s = tab.s[at];
+                        float2 m = f2swap(d);
+                        if constexpr (KIND == kRopeSome) m = rotated ? m : f2s(0.f);
+                        return make_float2(d.x * c - m.x * s, d.y * c + m.y * s);
+                    };
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        ta[i] = turned(ga[i], ch.a[i / HV] / 2 + i % HV, ch.ra[i / HV]);
+                        tb[i] = turned(gb[i], ch.b[i / HV] / 2 + i % HV, ch.rb[i / HV]);
+                    }
+                } else {
+                    float2 c[H], s[H];
 #pragma unroll
                     for (int i = 0; i < C; ++i) {
-                        rope_unpack<XT, V>(ring[slot].g[u][2 * i][lane], p.ydt, ga + i * HV);
-                        rope_unpack<XT, V>(ring[slot].g[u][2 * i + 1][lane], p.ydt, gb + i * HV);
+                        rope_get<V>(tab.c, (i * L + sl) * V, N, c + i * HV);
+                        rope_get<V>(tab.s, (i * L + sl) * V, N, s + i * HV);
                     }
-                    if (inter) {
-                        auto turned = [&](float2 d, int at, bool rotated) {
-                            const float c = tab.c[at], s = tab.s[at];
-                            float2 m = f2swap(d);
-                            if constexpr (!rope_whole(KIND)) m = rotated ? m : f2s(0.f);
-                            return make_float2(d.x * c - m.x * s, d.y * c + m.y * s);
-                        };
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            ta[i] = turned(ga[i], ch.a[i / HV] / 2 + i % HV, ch.ra[i / HV]);
-                            tb[i] = turned(gb[i], ch.b[i / HV] / 2 + i % HV, ch.rb[i / HV]);
+                    for (int i = 0; i < H; ++i) {
+                        float2 m = gb[i], n = ga[i];
+                        if constexpr (KIND == kRopeSome) {
+                            m = ch.ra[i / HV] ? m : f2s(0.f);
+                            n = ch.ra[i / HV] ? n : f2s(0.f);
                         }
-                    } else {
-                        float2 c[H], s[H];
-#pragma unroll
-                        for (int i = 0; i < C; ++i) {
-                            rope_get<V>(tab.c, (i * L + sl) * V, N, c + i * HV);
-                            rope_get<V>(tab.s, (i * L + sl) * V, N, s + i * HV);
-                        }
-#pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            float2 m = gb[i], n = ga[i];
-                            if constexpr (!rope_whole(KIND)) {
-                                m = ch.ra[i / HV] ? m : f2s(0.f);
-                                n = ch.ra[i / HV] ? n : f2s(0.f);
-                            }
-                            ta[i] = f2fma(ga[i], c[i], f2mul(make_float2(-m.x, -m.y), s[i]));
-                            tb[i] = f2fma(gb[i], c[i], f2mul(n, s[i]));
-                        }
+                        ta[i] = f2fma(ga[i], c[i], f2mul(make_float2(-m.x, -m.y), s[i]));
+                        tb[i] = f2fma(gb[i], c[i], f2mul(n, s[i]));
                     }
                 }
-                float2 xa[H], xb[H];
+            }
+            float2 xa[H], xb[H];
 #pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    rope_unpack<XT, V>(ring[slot].x[u][2 * i][lane], p.xdt, xa + i * HV);
-                    rope_unpack<XT, V>(ring[slot].x[u][2 * i + 1][lane], p.xdt, xb + i * HV);
-                }
-                const float rstd = ring[slot].rstd[u][lane], mean = LN ? ring[slot].mean[u][lane] : 0.f;
-                if (u == U - 1) load(slot);
-                float2 dot = f2s(0.f), sum = f2s(0.f);
-                float2 wa[H], wb[H];
+            for (int i = 0; i < C; ++i) {
+                rope_unpack<XT, V>(ring[slot].x[2 * i][lane], p.xdt, xa + i * HV);
+                rope_unpack<XT, V>(ring[slot].x[2 * i + 1][lane], p.xdt, xb + i * HV);
+            }
+            const float rstd = ring[slot].rstd[lane], mean = LN ? ring[slot].mean[lane] : 0.f;
+            load(slot);
+            float2 dot = f2s(0.f), sum = f2s(0.f);
+            float2 wa[H], wb[H];
 #pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    rope_get<V>(par + r * p.D, ch.a[i], p.D, wa + i * HV);
-                    rope_get<V>(par + r * p.D, ch.b[i], p.D, wb + i * HV);
-                }
+            for (int i = 0; i < C; ++i) {
+                rope_get<V>(par + r * p.D, ch.a[i], p.D, wa + i * HV);
+                rope_get<V>(par + r * p.D, ch.b[i], p.D, wb + i * HV);
+            }
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    if constexpr (LN) {
-                        xa[i] = f2add(xa[i], f2s(-mean));
-                        xb[i] = f2add(xb[i], f2s(-mean));
-                        ea[i] = f2add(ea[i], ta[i]);
-                        eb[i] = f2add(eb[i], tb[i]);
-                    }
-                    xa[i] = f2mul(xa[i], f2s(rstd));
-                    xb[i] = f2mul(xb[i], f2s(rstd));
-                    da[i] = f2fma(ta[i], xa[i], da[i]);
-                    db[i] = f2fma(tb[i], xb[i], db[i]);
-                    ta[i] = f2mul(ta[i], wa[i]);
-                    tb[i] = f2mul(tb[i], wb[i]);
-                    dot = f2fma(ta[i], xa[i], f2fma(tb[i], xb[i], dot));
-                    if constexpr (LN) sum = f2add(sum, f2add(ta[i], tb[i]));
+            for (int i = 0; i < H; ++i) {
+                if constexpr (LN) {
+                    xa[i] = f2add(xa[i], f2s(-mean));
+                    xb[i] = f2add(xb[i], f2s(-mean));
+                    ea[i] = f2add(ea[i], ta[i]);
+                    eb[i] = f2add(eb[i], tb[i]);
                 }
-                float v[LN ? 2 : 1];
-                v[0] = dot.x + dot.y;
-                if constexpr (LN) v[1] = sum.x + sum.y;
-                lanes.sum(v);
-                // dx = rstd g - rstd c1 - xhat (rstd c2)
-                const float2 c2 = f2s(-v[0] * inv * rstd), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv * rstd : 0.f);
+                xa[i] = f2mul(xa[i], f2s(rstd));
+                xb[i] = f2mul(xb[i], f2s(rstd));
+                da[i] = f2fma(ta[i], xa[i], da[i]);
+                db[i] = f2fma(tb[i], xb[i], db[i]);
+                ta[i] = f2mul(ta[i], wa[i]);
+                tb[i] = f2mul(tb[i], wb[i]);
+                dot = f2fma(ta[i], xa[i], f2fma(tb[i], xb[i], dot));
+                if constexpr (LN) sum = f2add(sum, f2add(ta[i], tb[i]));
+            }
+            float v[LN ? 2 : 1];
+            v[0] = dot.x + dot.y;
+            if constexpr (LN) v[1] = sum.x + sum.y;
+            lanes.sum(v);
+            // dx = rstd g - rstd c1 - xhat (rstd c2)
+            const float2 c2 = f2s(-v[0] * inv * rstd), c1 = f2s(LN ? -v[LN ? 1 : 0] * inv * rstd : 0.f);
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    ta[i] = f2fma(xa[i], c2, LN ? f2fma(ta[i], f2s(rstd), c1) : f2mul(ta[i], f2s(rstd)));
-                    tb[i] = f2fma(xb[i], c2, LN ? f2fma(tb[i], f2s(rstd), c1) : f2mul(tb[i], f2s(rstd)));
-                }
-                const bool in = hl > u * G;
-                char *q = u == 0 ? y : y + u * ys;
-#pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    if (in && ch.oka[i]) rope_store<XT, V>(q + ch.a[i] * xes, p.xdt, ta + i * HV);
-                    if (in && ch.okb[i]) rope_store<XT, V>(q + ch.b[i] * xes, p.xdt, tb + i * HV);
-                }
+            for (int i = 0; i < H; ++i) {
+                ta[i] = f2fma(xa[i], c2, LN ? f2fma(ta[i], f2s(rstd), c1) : f2mul(ta[i], f2s(rstd)));
+                tb[i] = f2fma(xb[i], c2, LN ? f2fma(tb[i], f2s(rstd), c1) : f2mul(tb[i], f2s(rstd)));
+            }
+                        #pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (in && ch.oka[i]) rope_store<XT, V>(y + ch.a[i] * xes, p.xdt, ta + i * HV);
+                if (in && ch.okb[i]) rope_store<XT, V>(y + ch.b[i] * xes, p.xdt, tb + i * HV);
             }
             if (!w.left) {
                 if (r) swap();
@@ -688,7 +683,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 ys = p.y[w.r].head * (G * V * xes);
                 if (w.r != r) swap();
             } else {
-                y += U * ys;
+                y += ys;
             }
         }
     }
