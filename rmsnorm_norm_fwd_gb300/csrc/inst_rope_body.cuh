@@ -1,9 +1,9 @@
 // Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V,
 // GBN_C, the type and elements of a vector and the vectors of half a lane's elements.  Defines
-// kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE 2: whole heads rotated as halves or as neighbours have kernels of
-// their own up to 16 lanes (prefill of 16384 tokens of 32 heads of 72, 8-byte vectors, 38 us against 45 us, their
-// rotation 33 us against 37 us).  1: all run on the kernels for any rotation, as the backward on 8-byte vectors (64.3 us
-// against 65.8 us); 0: and on powers of two.
+// kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE: whole heads rotated as halves (1) and as neighbours (2) have
+// kernels of their own up to 16 lanes (prefill of 16384 tokens of 32 heads of 72, 8-byte vectors, 38 us against 45 us, their
+// rotation 33 us against 37 us; not the backward on 8-byte vectors, 64.3 us against 65.8 us); what is rarer runs on the
+// kernels for any rotation.  GBN_ODD: heads on 5, 6 and 10 lanes too (heads of 80 16.4 us against 19.0 us).
 #include "rope_vec_kernels.cuh"
 
 #ifndef GBN_CAT
@@ -26,34 +26,39 @@
     {(const void *)&rope_bwd_vec<GBN_MODE == -2, GBN_XT, GBN_V, GBN_C, L, KIND, 2>, GBN_NAMED(L, S), \
      rope_bwd_smem(GBN_VECTOR, L, GBN_MODE == -2), 1, L}
 #endif
-#define GBN_ANY(L) GBN_K(L, kRopeSome, "")
-#if GBN_WHOLE
-#define GBN_SOME {GBN_ANY(4), GBN_ANY(5), GBN_ANY(6), GBN_ANY(8), GBN_ANY(10), GBN_ANY(16), GBN_ANY(32)}
+#if GBN_ODD
+#define GBN_LANES(KIND, S) \
+    {GBN_K(4, KIND, S), GBN_K(5, KIND, S), GBN_K(6, KIND, S), GBN_K(8, KIND, S), GBN_K(10, KIND, S), \
+     GBN_K(16, KIND, S), GBN_K(32, kRopeSome, "")}
 #else
-#define GBN_SOME {GBN_ANY(4), GBN_ANY(8), GBN_ANY(8), GBN_ANY(8), GBN_ANY(16), GBN_ANY(16), GBN_ANY(32)}
+#define GBN_LANES(KIND, S) \
+    {GBN_K(4, KIND, S), GBN_K(8, KIND, S), GBN_K(8, KIND, S), GBN_K(8, KIND, S), GBN_K(16, KIND, S), \
+     GBN_K(16, KIND, S), GBN_K(32, kRopeSome, "")}
 #endif
 
 namespace gbn {
 const RopeVariant GBN_CAT(kRopeVec_, GBN_NAME)[kRopeVecKinds][kRopeVecLanes] = {
-#if GBN_WHOLE == 2
-    {GBN_K(4, kRopeHalves, "h"), GBN_K(5, kRopeHalves, "h"), GBN_K(6, kRopeHalves, "h"), GBN_K(8, kRopeHalves, "h"),
-     GBN_K(10, kRopeHalves, "h"), GBN_K(16, kRopeHalves, "h"), GBN_ANY(32)},
-    {GBN_K(4, kRopeNeighbours, "n"), GBN_K(5, kRopeNeighbours, "n"), GBN_K(6, kRopeNeighbours, "n"),
-     GBN_K(8, kRopeNeighbours, "n"), GBN_K(10, kRopeNeighbours, "n"), GBN_K(16, kRopeNeighbours, "n"), GBN_ANY(32)},
+#if GBN_WHOLE >= 1
+    GBN_LANES(kRopeHalves, "h"),
 #else
-    GBN_SOME, GBN_SOME,
+    GBN_LANES(kRopeSome, ""),
 #endif
-    GBN_SOME};
+#if GBN_WHOLE >= 2
+    GBN_LANES(kRopeNeighbours, "n"),
+#else
+    GBN_LANES(kRopeSome, ""),
+#endif
+    GBN_LANES(kRopeSome, "")};
 }  // namespace gbn
-#undef GBN_SOME
+#undef GBN_LANES
 #undef GBN_K
 #undef GBN_U
 #undef GBN_VECTOR
 #undef GBN_NAMED
-#undef GBN_ANY
 #undef GBN_MODE
 #undef GBN_XT
 #undef GBN_V
 #undef GBN_C
 #undef GBN_WHOLE
+#undef GBN_ODD
 #undef GBN_NAME

@@ -4,5 +4,6 @@
 #define GBN_V 4
 #define GBN_C 1
 #define GBN_WHOLE 2
+#define GBN_ODD 0
 #define GBN_NAME rms_f32v4
 #include "inst_rope_body.cuh"
