@@ -17,7 +17,8 @@ additions one after another: a lane's own elements, then levels):
   dx        r (e_g + e_c1 + |xhat| e_c2 + 4 u (|g| + |c1| + 2 |xhat c2|)) + 2 u |dx|,
             e_g = |gamma| e_t + u |g|, xhat within 3 u, e_c2 = mean(e_g |xhat| + 3 u |g xhat|) + u (K + 2) mean|g xhat|
   dgamma    sum(e_t |xhat| + 4 u |t xhat|) + u N sum|t xhat| with N = heads / 1024 + 64 (a grid of 304 CTAs of
-            8 warps that add their heads one after another, then the warps, then the partial rows)
+            8 warps that add their heads one after another, then the warps, then the partial rows; with the grid
+            capped, at most 1100 heads over the 32 groups of lanes of a CTA)
 """
 import math
 
