@@ -395,7 +395,7 @@ typedef struct {
 } gbnorm_heads_t;
 
 typedef struct {
-    int64_t batches, tokens; /* batches of tokens each; 0 of either: nothing is done */
+    int64_t batches, tokens; /* batches of tokens each, at most 2^31 - 1 of either, 2^40 in all; 0: nothing is done */
     int64_t heads[2];        /* of the queries (at least 1) and of the keys (0: no keys) */
     int64_t dim;             /* D, 1 to GBNORM_MAX_HEAD_DIM */
     int32_t x_dtype, y_dtype, param_dtype; /* gbnorm_dtype_t */

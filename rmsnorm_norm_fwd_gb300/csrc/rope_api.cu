@@ -112,11 +112,15 @@ struct Shape {
     int tensors() const { return H[1] > 0 ? 2 : 1; }
 };
 
+constexpr int64_t kMostTokens = (int64_t)1 << 40;
+
+bool valid_heads(const Shape &s) {
+    return s.H[0] >= 1 && s.H[1] >= 0 && s.H[0] <= GBNORM_MAX_HEADS && s.H[1] <= GBNORM_MAX_HEADS && s.D >= 1 &&
+           s.D <= kRopeMaxDim;
+}
 bool valid_shape(const Shape &s) {
-    if (s.B < 0 || s.S < 0 || s.H[0] < 1 || s.H[1] < 0 || s.H[0] > GBNORM_MAX_HEADS || s.H[1] > GBNORM_MAX_HEADS ||
-        s.D < 1 || s.D > kRopeMaxDim)
-        return false;
-    return s.B <= INT32_MAX && s.S <= INT32_MAX && s.tokens() <= (int64_t)1 << 40;
+    if (!valid_heads(s) || s.B < 0 || s.S < 0) return false;
+    return s.B <= INT32_MAX && s.S <= INT32_MAX && s.tokens() <= kMostTokens;
 }
 
 // Checks what every call has and fills the parameters that do not depend on the direction.
@@ -430,9 +434,11 @@ int qk_norm_rope_fwd(int is_layernorm, float eps, const gbnorm_rope_t *r, const 
 
 size_t qk_norm_rope_bwd_workspace_size(int is_layernorm, int64_t tokens, int64_t heads_q, int64_t heads_k,
                                        int64_t dim) {
-    const Shape s{1, tokens, {heads_q, heads_k}, dim};
+    const Shape s{1, tokens, {heads_q, heads_k}, dim};  // of all batches: more than one may hold
     HostDevice d;
-    if ((is_layernorm != 0 && is_layernorm != 1) || !valid_shape(s) || host_device(&d) != GBNORM_OK) return 0;
+    if ((is_layernorm != 0 && is_layernorm != 1) || !valid_heads(s) || tokens < 0 || tokens > kMostTokens ||
+        host_device(&d) != GBNORM_OK)
+        return 0;
     const size_t need = bwd_ws(is_layernorm, s, d);
     return need > 0 ? need : 256;  // no tokens: nothing is used; 0 means an error
 }
