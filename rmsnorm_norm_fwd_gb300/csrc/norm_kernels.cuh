@@ -587,6 +587,8 @@ __global__ void __launch_bounds__(kColCTA) colreduce(const float *ws, int64_t P,
     if (ok) {
         // Bands of up to kColBatch rows: all loads of a batch are issued before
         // any is added, so a band costs one memory latency, not one per row.
+        // __ldcg: `ws` is written while this grid may already be resident, and
+        // the read-only path (__ldg) is for memory that nobody writes meanwhile.
         constexpr int kColBatch = 16;
         for (int64_t q0 = p0; q0 < p1; q0 += kColBatch) {
             if constexpr (VW == 4) {
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(kColCTA) colreduce(const float *ws, int64_t P,
                 float4 a[kColBatch];
 #pragma unroll
                 for (int i = 0; i < kColBatch; ++i)
-                    a[i] = q0 + i < p1 ? __ldg(s4 + (q0 + i) * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    a[i] = q0 + i < p1 ? __ldcg(s4 + (q0 + i) * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kColBatch; ++i) {
                     acc[0] += a[i].x;
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kColCTA) colreduce(const float *ws, int64_t P,
             } else {
                 float a[kColBatch];
 #pragma unroll
-                for (int i = 0; i < kColBatch; ++i) a[i] = q0 + i < p1 ? __ldg(src + (q0 + i) * N + col) : 0.f;
+                for (int i = 0; i < kColBatch; ++i) a[i] = q0 + i < p1 ? __ldcg(src + (q0 + i) * N + col) : 0.f;
 #pragma unroll
                 for (int i = 0; i < kColBatch; ++i) acc[0] += a[i];
             }

@@ -455,7 +455,9 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
 // out[c] = sum over the P partial rows of ws [2][P][N] (block blockIdx.y), 32
 // columns a CTA, warp w the rows w, w + 32, ..., then the warps in order.  A head
 // has few columns, so one CTA for all of them (as for long rows) would read the
-// rows one latency after another.
+// rows one latency after another.  __ldcg: ws is written while this grid may
+// already be resident, and the read-only path (__ldg) is for memory that nobody
+// writes meanwhile.
 constexpr int kRopeColumnsCTA = 1024;
 __global__ void __launch_bounds__(kRopeColumnsCTA)
     rope_columns(const float *ws, int P, int N, float *out0, float *out1) {
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kRopeColumnsCTA)
         for (int p0 = warp; p0 < P; p0 += 32 * AT_ONCE) {
             float a[AT_ONCE];
 #pragma unroll
-            for (int i = 0; i < AT_ONCE; ++i) a[i] = p0 + 32 * i < P ? __ldg(from + (int64_t)(p0 + 32 * i) * N) : 0.f;
+            for (int i = 0; i < AT_ONCE; ++i) a[i] = p0 + 32 * i < P ? __ldcg(from + (int64_t)(p0 + 32 * i) * N) : 0.f;
 #pragma unroll
             for (int i = 0; i < AT_ONCE; ++i) v += a[i];
         }
