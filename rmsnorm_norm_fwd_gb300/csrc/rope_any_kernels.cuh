@@ -238,9 +238,15 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_any(const __grid_cons
                 sa[i] = f2mul(gb[i], make_float2(-s[i].x, -s[i].y));
                 sb[i] = f2mul(ga[i], s[i]);
                 if constexpr (MODE == kRopeLn) {
-                    const float2 v = ba[i];
-                    ba[i] = make_float2(v.x * c[i].x - bb[i].x * s[i].x, v.y * c[i].y - bb[i].y * s[i].y);
-                    bb[i] = make_float2(bb[i].x * c[i].x + v.x * s[i].x, bb[i].y * c[i].y + v.y * s[i].y);
+                    // beta turned; where there is no partner it takes nothing from another, as x below
+                    const float2 va = ba[i], vb = bb[i];
+                    auto turned = [&](float own, float other, float cc, float ss, int slot) {
+                        return (ch.turned >> slot) & 1u ? own * cc + other * ss : own;
+                    };
+                    ba[i].x = turned(va.x, vb.x, c[i].x, -s[i].x, 2 * i);
+                    ba[i].y = turned(va.y, vb.y, c[i].y, -s[i].y, 2 * i + 1);
+                    bb[i].x = turned(vb.x, va.x, c[i].x, s[i].x, 2 * i);
+                    bb[i].y = turned(vb.y, va.y, c[i].y, s[i].y, 2 * i + 1);
                 }
             }
             Slots::keep(ch.turned, sa);

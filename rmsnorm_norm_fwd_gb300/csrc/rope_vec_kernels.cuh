@@ -372,16 +372,20 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                 }
             }
             if (inter) {  // pairs of a chunk from element e on: from e / 2 on
-                auto fold = [&](const float2 &g, int at, float2 &cc, float2 &ss, float2 &bias) {
+                auto fold = [&](const float2 &g, int at, bool rotated, float2 &cc, float2 &ss, float2 &bias) {
                     const float c = tab.c[at], s = tab.s[at];
                     cc = make_float2(g.x * c, g.y * c);
                     ss = make_float2(-g.y * s, g.x * s);
-                    if constexpr (MODE == kRopeLn) bias = make_float2(bias.x * c - bias.y * s, bias.y * c + bias.x * s);
+                    if constexpr (MODE == kRopeLn) {
+                        float2 v = f2swap(bias);
+                        if constexpr (KIND == kRopeSome) v = rotated ? v : f2s(0.f);
+                        bias = make_float2(bias.x * c - v.x * s, bias.y * c + v.y * s);
+                    }
                 };
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    fold(ga[i], ch.a[i / HV] / 2 + i % HV, ca[i], sa[i], ba[i]);
-                    fold(gb[i], ch.b[i / HV] / 2 + i % HV, cb[i], sb[i], bb[i]);
+                    fold(ga[i], ch.a[i / HV] / 2 + i % HV, ch.ra[i / HV], ca[i], sa[i], ba[i]);
+                    fold(gb[i], ch.b[i / HV] / 2 + i % HV, ch.rb[i / HV], cb[i], sb[i], bb[i]);
                 }
             } else {
                 float2 c[H], s[H];
@@ -397,8 +401,12 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     cb[i] = f2mul(gb[i], c[i]);
                     sb[i] = f2mul(ga[i], s[i]);
                     if constexpr (MODE == kRopeLn) {
-                        const float2 v = ba[i];
-                        ba[i] = make_float2(v.x * c[i].x - bb[i].x * s[i].x, v.y * c[i].y - bb[i].y * s[i].y);
+                        float2 u = bb[i], v = ba[i];
+                        if constexpr (KIND == kRopeSome) {  // as below: no partner, not even a NaN's product with 0
+                            u = ch.ra[i / HV] ? u : f2s(0.f);
+                            v = ch.ra[i / HV] ? v : f2s(0.f);
+                        }
+                        ba[i] = make_float2(ba[i].x * c[i].x - u.x * s[i].x, ba[i].y * c[i].y - u.y * s[i].y);
                         bb[i] = make_float2(bb[i].x * c[i].x + v.x * s[i].x, bb[i].y * c[i].y + v.y * s[i].y);
                     }
                 }
