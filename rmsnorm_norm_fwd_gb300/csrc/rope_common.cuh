@@ -13,17 +13,19 @@ namespace gbn {
 // exactly where the angle does.  F is within half a unit, so the angle of
 // position p is within |p| 2^-65 turns of the product's (a product of fp32
 // values would be off by up to 2^-24 of the whole angle, 0.06 radians at position
-// 10^6).  1 / (2 pi) enters with 128 bits; the bits below them would matter from
-// frequencies of 2^87 on, which, like infinities and NaN, give NaN.
-constexpr uint64_t kTurnHi = 0x28be60db9391054aull, kTurnLo = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
+// 10^6).  1 / (2 pi) enters with 192 bits: what is cut off below them is less than
+// 2^-40 of a unit for every frequency below 2^87 (128 bits would cut off 28 units
+// at 2^70).  Frequencies from there on, like infinities and NaN, give NaN.
+constexpr uint64_t kTurnHi = 0x28be60db9391054aull, kTurnMid = 0x7f09d5f47d4d3770ull,
+                   kTurnLo = 0x36d8a5664f10e410ull;  // 2^192 / (2 pi)
 
 __device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
     const uint32_t bits = __float_as_uint(f), ex = (bits >> 23) & 0xffu;
     const uint64_t m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
     *bad = ex >= 127 + 87;
     // m 2^128 / (2 pi) as three words; |f| / (2 pi) turns = that * 2^(e - 128), F = that >> (64 - e)
-    const uint64_t lo = m * kTurnLo, c = __umul64hi(m, kTurnLo), mid = m * kTurnHi + c,
-                   hi = __umul64hi(m, kTurnHi) + (mid < c ? 1u : 0u);
+    const uint64_t b = __umul64hi(m, kTurnLo), lo = m * kTurnMid + b, c = __umul64hi(m, kTurnMid) + (lo < b ? 1u : 0u),
+                   mid = m * kTurnHi + c, hi = __umul64hi(m, kTurnHi) + (mid < c ? 1u : 0u);
     const int sh = 64 - ((ex ? (int)ex : 1) - 150);  // 1 .. 213 for frequencies below 2^87
     uint64_t r = 0;
     auto from = [&](int s) -> uint64_t {  // bits s .. s + 63 of (hi, mid, lo), s >= 0

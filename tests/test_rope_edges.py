@@ -1,5 +1,5 @@
-"""Head operators at the edges of what their documentation allows: very many tokens, parameters that
-are not finite (GPU)."""
+"""Head operators at the edges of what their documentation allows: very many tokens, parameters that are not finite, large
+frequencies (GPU)."""
 import pytest
 import torch
 
@@ -58,3 +58,23 @@ def test_a_parameter_that_is_not_finite_reaches_its_own_element(D, rot, inter, b
         for ln, gamma, beta in ((False, w, None), (True, w, None), (True, none, w)):
             y = g.qk_norm_rope_fwd(ln, q, None, cuda(gamma), None, EPS, pos, r, beta_q=cuda(beta))[0].cpu()
             assert not torch.isfinite(y[..., hit]).any() and torch.isfinite(y[..., ~hit]).all(), (at, ln, beta is None)
+
+
+def test_large_frequencies_at_far_positions():
+    """Frequencies up to 2^87 with all bits of their mantissas set, at positions where half a unit of 2^-64 turns in
+    the frequency is 2^-25 turns of the angle; against exact turns."""
+    from fractions import Fraction
+    g = lib()
+    pi = Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679,
+                  10 ** 100)
+    big = [2.0 ** e * (2 - 2.0 ** -23) for e in (0, 40, 60, 62, 63, 64, 67, 70, 73, 75, 77, 80, 82, 84, 85, 86)]
+    f = torch.tensor([(-1) ** i * v for i, v in enumerate(big)], dtype=torch.float64).float()
+    D = 2 * len(big)
+    pos = torch.tensor([[1, 2 ** 20 + 1, 2 ** 33 - 7, -2 ** 36 + 5, 2 ** 40, 2 ** 40 - 1]])
+    turns = [[float((int(p) * Fraction(float(w)) / (2 * pi)) % 1) for w in f] for p in pos[0]]
+    angle = 2 * torch.pi * torch.tensor(turns, dtype=torch.float64)[None, :, None]
+    far = pos.double().abs()[..., None, None]
+    q = ref.heads(1, pos.shape[1], 3, D, torch.float32, 1)
+    for inter in (False, True):
+        want, tol = ref.forward(None, q, None, None, 0, angle, far, D, inter)[2]
+        ref.held("yq", g.rope_fwd(q.cuda(), None, pos.cuda(), plan(f, None, inter))[0], want, tol + 1e-14)
