@@ -47,13 +47,18 @@ __device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
 __device__ __forceinline__ uint32_t rope_axis(const RopeParams &p, int j) {
     return (p.axis[j >> 4] >> (2 * (j & 15))) & 3u;
 }
-// cos and sign * sin of u 2^-64 turns.  sincospif takes half turns: the top bits of u as a multiple of 2^-63, in fp32,
-// exact down to angles that do not matter.
+// cos and sign * sin of u 2^-64 turns.  The nearest quarter turn comes off in the
+// integer, so that the one rounding of the angle, of what is left to fp32, is of
+// at most an eighth of a turn: pi 2^-27 radians.  (Of up to half a turn it would
+// be pi 2^-25, more than sincospif's own error.)
 __device__ __forceinline__ void rope_sincos(uint64_t u, float sign, float *c, float *s) {
+    const uint32_t quarter = ((uint32_t)(u >> 32) + (1u << 29)) >> 30;
+    const int64_t left = (int64_t)(u - ((uint64_t)quarter << 62));
     float sn, cs;
-    sincospif(__ll2float_rn((long long)u) * 1.0842021724855044e-19f, &sn, &cs);
-    *c = cs;
-    *s = sn * sign;
+    sincospif(__ll2float_rn(left) * 1.0842021724855044e-19f, &sn, &cs);  // half turns: 2^-63
+    const float a = quarter & 1u ? sn : cs, b = quarter & 1u ? cs : sn;
+    *c = (quarter + 1u) & 2u ? -a : a;
+    *s = (quarter & 2u ? -b : b) * sign;
 }
 
 // a / n of numbers that mostly fit 32 bits (a division in 64 is some hundred instructions).

@@ -1,5 +1,5 @@
 """Head operators at the edges of what their documentation allows: very many tokens, parameters that are not finite, large
-frequencies (GPU)."""
+frequencies; cosines and sines to their last bits (GPU)."""
 import pytest
 import torch
 
@@ -78,3 +78,20 @@ def test_large_frequencies_at_far_positions():
     for inter in (False, True):
         want, tol = ref.forward(None, q, None, None, 0, angle, far, D, inter)[2]
         ref.held("yq", g.rope_fwd(q.cuda(), None, pos.cuda(), plan(f, None, inter))[0], want, tol + 1e-14)
+
+
+@pytest.mark.parametrize("D,inter,how", [(128, False, "dense"), (128, True, "dense"), (98, True, "two"), (98, False, "odd")])
+def test_cosines_and_sines_to_an_fp32_unit(D, inter, how):
+    """Pairs (1, 0) turned are the cosine and the sine themselves: 1 ulp of sinpi and cospi below 1 (2^-24), and the
+    angle's rounding to fp32 when at most an eighth of a turn is left of it (pi 2^-27).  The angles here are below 2^12
+    radians, the reference's own product within 2^-41."""
+    g = lib()
+    S, gen = 4096, torch.Generator().manual_seed(3)
+    f = torch.rand(D // 2, generator=gen)
+    a, b = ref.pairs(D, inter)
+    q = torch.zeros(1, S, 1, D)
+    q[..., a] = 1.0
+    angle, _ = ref.angles(torch.arange(S)[None], f, None, 1, S)
+    y = g.rope_fwd(place(q, how), None, torch.arange(S)[None].cuda(), plan(f, None, inter))[0].cpu().double()
+    tol = 2.0 ** -24 + torch.pi * 2.0 ** -27 + 2.0 ** -40
+    assert (y[..., a] - torch.cos(angle)).abs().max() <= tol and (y[..., b] - torch.sin(angle)).abs().max() <= tol
