@@ -110,6 +110,8 @@ class _Call:
     def heads(self, name, q, k, dtype):
         """Two gbnorm_heads_t."""
         if self.k is None:
+            if k is not None:
+                raise ValueError(f"{name}k is given without k")
             return _HEADS(*self._one(name + "q", q, self.q, dtype), 0, 0, 0, 0)
         return _HEADS(*self._one(name + "q", q, self.q, dtype), *self._one(name + "k", k, self.k, dtype))
 
@@ -130,7 +132,9 @@ class _Call:
 
     def out(self, name, yq, yk, q, k, dtype):
         """The two outputs, allocated where they are not given, and their gbnorm_heads_t."""
-        if yq is not None or (yk is not None and k is not None):
+        if k is None and yk is not None:
+            raise ValueError(f"{name}k is given without k")
+        if yq is not None or yk is not None:
             if yq is None:
                 yq = torch.empty_like(q, dtype=dtype, memory_format=_CONTIGUOUS)
             if yk is None and k is not None:
@@ -232,7 +236,7 @@ def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, pos
     (yq, yk, mean, rstd): outputs of y_dtype (default q's) with q's and k's
     shapes; mean and rstd float32 [..., heads of q and of k], mean None for
     RMSNorm, both None without save_stats unless given.  yq may be q itself
-    and yk k itself."""
+    and yk k itself.  Without k, gamma_k and beta_k (a layer's) are not read, yk is refused."""
     if stream is not None:
         return _on_stream(qk_norm_rope_fwd)(is_layernorm, q, k, gamma_q, gamma_k, eps, positions, rotary, beta_q,
                                             beta_k, y_dtype, yq, yk, mean, rstd, save_stats, stream=stream)
@@ -271,7 +275,8 @@ def qk_norm_rope_bwd(is_layernorm: bool, dyq, dyk, q, k, gamma_q, gamma_k, mean,
     """Backward of qk_norm_rope_fwd from its inputs q and k and its saved
     statistics.  Returns (dq, dk, dgamma, dbeta): dq and dk of q's dtype, dgamma
     and dbeta float32 [2, D] (queries, keys; [1, D] without keys), None where not
-    needed, dbeta LayerNorm only.  dq may be dyq itself and dk dyk itself."""
+    needed, dbeta LayerNorm only.  dq may be dyq itself and dk dyk itself.
+    Without k, gamma_k is not read, dyk and dk are refused."""
     if stream is not None:
         return _on_stream(qk_norm_rope_bwd)(is_layernorm, dyq, dyk, q, k, gamma_q, gamma_k, mean, rstd, positions,
                                             rotary, dq, dk, dgamma, dbeta, workspace, need_dgamma, need_dbeta,
