@@ -220,6 +220,15 @@ class _Call:
             _check(name, status)
 
 
+def _out_dtype(name, out, dtype, default):
+    """The type of an output: its own where it is given, which the argument may not contradict."""
+    if out is None:
+        return dtype or default
+    if dtype is not None and out.dtype != dtype:
+        raise ValueError(f"{name} has dtype {out.dtype}, not the {dtype} asked for")
+    return out.dtype
+
+
 def _param_dtype(default, *params):
     for t in params:
         if t is not None:
@@ -241,7 +250,7 @@ def qk_norm_rope_fwd(is_layernorm: bool, q, k, gamma_q, gamma_k, eps: float, pos
         return _on_stream(qk_norm_rope_fwd)(is_layernorm, q, k, gamma_q, gamma_k, eps, positions, rotary, beta_q,
                                             beta_k, y_dtype, yq, yk, mean, rstd, save_stats, stream=stream)
     c = _Call("", q, k)
-    dt = yq.dtype if yq is not None else y_dtype or q.dtype
+    dt = _out_dtype("yq", yq, y_dtype, q.dtype)
     if not is_layernorm:
         mean = beta_q = beta_k = None
     pdt = _param_dtype(q.dtype, gamma_q, gamma_k, beta_q, beta_k)
@@ -311,7 +320,7 @@ def rope_fwd(q, k, positions, rotary: Rotary, y_dtype=None, yq=None, yk=None, st
     if stream is not None:
         return _on_stream(rope_fwd)(q, k, positions, rotary, y_dtype, yq, yk, stream=stream)
     c = _Call("", q, k)
-    dt = yq.dtype if yq is not None else y_dtype or q.dtype
+    dt = _out_dtype("yq", yq, y_dtype, q.dtype)
     if rotary is None:
         raise ValueError("rotary is needed")
     r, x = c.rope(positions, rotary, q.dtype, dt, q.dtype), c.heads("", q, k, q.dtype)
@@ -326,7 +335,7 @@ def rope_bwd(dyq, dyk, positions, rotary: Rotary, dx_dtype=None, dq=None, dk=Non
     if stream is not None:
         return _on_stream(rope_bwd)(dyq, dyk, positions, rotary, dx_dtype, dq, dk, stream=stream)
     c = _Call("dy", dyq, dyk)
-    dt = dq.dtype if dq is not None else dx_dtype or dyq.dtype
+    dt = _out_dtype("dq", dq, dx_dtype, dyq.dtype)
     if rotary is None:
         raise ValueError("rotary is needed")
     r, dy = c.rope(positions, rotary, dt, dyq.dtype, dyq.dtype), c.heads("dy", dyq, dyk, dyq.dtype)

@@ -41,3 +41,12 @@ def test_keys_outputs_and_gradients_without_keys(rope, where, given):
               lambda: rope.qk_norm_rope_bwd(False, q, zeros(S, H, D), q, None, None, None, None, rstd, *where, dq=out)):
         with pytest.raises(ValueError, match="without k"):
             f()
+
+
+def test_a_dtype_that_the_given_output_contradicts(rope, where):
+    q, y = zeros(S, H, D), zeros(S, H, D, dtype=torch.float16)
+    for f in (lambda: rope.rope_fwd(q, None, *where, y_dtype=torch.float32, yq=y),
+              lambda: rope.qk_norm_rope_fwd(False, q, None, None, None, 1e-6, *where, y_dtype=torch.bfloat16, yq=y),
+              lambda: rope.rope_bwd(q, None, *where, dx_dtype=torch.float32, dq=y)):
+        with pytest.raises(ValueError, match="dtype"):
+            f()
