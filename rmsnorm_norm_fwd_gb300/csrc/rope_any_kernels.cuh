@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
     auto load = [&] {
         ch.load(at(p.x[w.r], xes), p.xdt, w.hl > 0, xa, xb);
         ch.load(at(p.g[w.r], ges), p.ydt, w.hl > 0, ga, gb);
-        rstd = __ldg(p.rstd + w.stat(p));
-        if constexpr (LN) mean = __ldg(p.mean + w.stat(p));
+        rstd = w.hl > 0 ? __ldg(p.rstd + w.stat(p)) : 0.f;  // zeros throughout where there is no head
+        if constexpr (LN) mean = w.hl > 0 ? __ldg(p.mean + w.stat(p)) : 0.f;
     };
     if (w.left) load();
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;

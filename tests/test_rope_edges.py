@@ -1,5 +1,5 @@
 """Head operators at the edges of what their documentation allows: very many tokens, parameters that are not finite, large
-frequencies; cosines and sines to their last bits (GPU)."""
+frequencies; cosines and sines to their last bits, column sums to their additions (GPU)."""
 import pytest
 import torch
 
@@ -95,3 +95,83 @@ def test_cosines_and_sines_to_an_fp32_unit(D, inter, how):
     y = g.rope_fwd(place(q, how), None, torch.arange(S)[None].cuda(), plan(f, None, inter))[0].cpu().double()
     tol = 2.0 ** -24 + torch.pi * 2.0 ** -27 + 2.0 ** -40
     assert (y[..., a] - torch.cos(angle)).abs().max() <= tol and (y[..., b] - torch.sin(angle)).abs().max() <= tol
+
+
+@pytest.mark.parametrize("D,rot,dt,how", [(128, 128, "bf16", "dense"), (128, 64, "fp16", "dense"), (80, 32, "bf16", "dense"),
+                                          (64, 64, "fp32", "two"), (98, 40, "bf16", "odd")])
+@pytest.mark.parametrize("ln", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_not_finite_in_the_backwards_input(D, rot, dt, how, ln, inter, bad):
+    """With the statistics given, a NaN or an infinity in x reaches its head of dx and its column of its tensor's dgamma,
+    an infinity as an infinity; every other output keeps its bits.  The heads do not fill their passes."""
+    g = lib()
+    S, heads, dtype = 5, (11, 3), ref.TYPES[dt]
+    r, pos = plan(rotation(rot)[0], None, inter), positions(1, S, 1).cuda()
+    x = [ref.heads(1, S, h, D, dtype, h) for h in heads]
+    dy = [place(torch.randn(1, S, h, D, generator=torch.Generator().manual_seed(h)).to(dtype), how) for h in heads]
+    rstd, mean = torch.ones(1, S, sum(heads)).cuda(), torch.zeros(1, S, sum(heads)).cuda() if ln else None
+
+    def run():
+        return g.qk_norm_rope_bwd(ln, *dy, *[place(t, how) for t in x], None, None, mean, rstd, pos, r)
+    clean = run()
+    for i in (0, 1):
+        for head in (heads[i] - 1, heads[i] // 2):
+            for at in (0, rot - 1, D - 1):
+                x[i][0, 2, head, at], keep = bad, x[i][0, 2, head, at].clone()
+                got = run()
+                x[i][0, 2, head, at] = keep
+                assert not torch.isfinite(got[i][0, 2, head]).all()
+                got[i][0, 2, head] = clean[i][0, 2, head]
+                value = got[2][i, at].item()
+                assert abs(value) == bad if bad == float("inf") else value != value
+                got[2][i, at] = clean[2][i, at]
+                assert all(torch.equal(a, b) for a, b in zip(got[:3], clean[:3]))
+                assert (got[3] is None) if not ln else torch.equal(got[3], clean[3])
+
+
+@pytest.mark.parametrize("limit", [1, 2])
+@pytest.mark.parametrize("B,S,hq,hk", [(7, 25, 9, 2), (131, 1, 9, 2), (1, 97, 3, 1), (40, 3, 5, 0)])
+@pytest.mark.parametrize("D", [128, 80, 98])
+@pytest.mark.parametrize("ln", [False, True])
+def test_column_sums_of_few_warps(limit, B, S, hq, hk, D, ln):
+    """dgamma and dbeta on a grid of one or two CTAs, held to the additions that its longest chain makes: a lane adds a
+    value a pass of its warp (whole tokens, then a share of the other passes), then come the groups of lanes of a warp,
+    the 8 warps of a CTA, and the partial rows, one after another."""
+    import re
+    g = lib()
+    try:
+        g.set_grid_limit(limit)
+        f, _ = rotation(D)
+        pos = positions(B, S, 1)
+        angle, far = ref.angles(pos, f, None, B, S)
+        r = plan(f, None, False)
+        H = [h for h in (hq, hk) if h]
+        x = [ref.heads(B, S, h, D, torch.bfloat16, h, 0.5 if ln else 0.0) for h in H]
+        dy = [ref.heads(B, S, h, D, torch.bfloat16, h + 20) for h in H]
+        stats = [ref.norm(ln, t, None, None, EPS) for t in x]
+        mean, rstd = (torch.cat([s[i][0].float() for s in stats], 2).contiguous() for i in (0, 1))
+        more = [None] * (2 - len(H))
+        _, _, dgamma, dbeta = g.qk_norm_rope_bwd(ln, *[cuda(t) for t in dy + more + x + more], None, None,
+                                                 cuda(mean) if ln else None, cuda(rstd), cuda(pos), r)
+        groups = 32 // int(re.match(r"(?:vec\d+x|any)(\d+)", g.rope_last_variant(1)).group(1))
+    finally:
+        g.set_grid_limit(0)
+    passes = [-(-h // groups) for h in H]
+    tokens, units = B * S, B * S * sum(passes)
+    warps = min(8 * limit, units)
+    rounds = tokens // warps  # whole tokens of a warp, where there are four or more
+    rest = -(-(tokens - rounds * warps) * sum(passes) // warps)
+    at = 0
+    for i, h in enumerate(H):
+        chain = (rounds * passes[i] + rest if rounds >= 4 else -(-units // warps)) + groups + 8 + limit
+        t = ref.rotate(dy[i].double(), angle, D, False, -1.0)
+        et = ref.rotate_tol(dy[i].double(), torch.zeros_like(t), far, D, False)
+        xh = x[i].double() - (mean[..., at:at + h, None].double() if ln else 0.0)
+        xh = xh * rstd[..., at:at + h, None].double()
+        p, dims = (t * xh).abs(), (0, 1, 2)
+        tol = (et * xh.abs() + 4 * ref.U * p).sum(dims) + chain * ref.U * p.sum(dims)
+        ref.held("dgamma", dgamma[i], (t * xh).sum(dims), tol)
+        if ln:
+            ref.held("dbeta", dbeta[i], t.sum(dims), et.sum(dims) + chain * ref.U * t.abs().sum(dims))
+        at += h
