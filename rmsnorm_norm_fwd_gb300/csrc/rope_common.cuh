@@ -26,21 +26,10 @@ __device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
     // m 2^128 / (2 pi) as three words; |f| / (2 pi) turns = that * 2^(e - 128), F = that >> (64 - e)
     const uint64_t b = __umul64hi(m, kTurnLo), lo = m * kTurnMid + b, c = __umul64hi(m, kTurnMid) + (lo < b ? 1u : 0u),
                    mid = m * kTurnHi + c, hi = __umul64hi(m, kTurnHi) + (mid < c ? 1u : 0u);
-    const int sh = 64 - ((ex ? (int)ex : 1) - 150);  // 1 .. 213 for frequencies below 2^87
-    uint64_t r = 0;
-    auto from = [&](int s) -> uint64_t {  // bits s .. s + 63 of (hi, mid, lo), s >= 0
-        const uint64_t w[4] = {lo, mid, hi, 0};
-        uint64_t a = 0, b = 0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (s >> 6 == i) {
-                a = w[i];
-                b = w[i + 1];
-            }
-        const int k = s & 63;
-        return k ? (a >> k) | (b << (64 - k)) : a;
-    };
-    r = from(sh) + (from(sh - 1) & 1u);  // to nearest
+    // bits at .. at + 63 of (hi, mid, lo) and the next above them: F and, lowest, what it is rounded by
+    const int at = 63 - ((ex ? (int)ex : 1) - 150), k = at & 63;  // 0 .. 212 for frequencies below 2^87
+    const uint64_t x = at < 64 ? lo : at < 128 ? mid : at < 192 ? hi : 0, y = at < 64 ? mid : at < 128 ? hi : 0;
+    const uint64_t t = k ? (x >> k) | (y << (64 - k)) : x, r = (t >> 1) + ((y >> k) << 63) + (t & 1u);
     return (bits >> 31) ? 0 - r : r;
 }
 
@@ -52,13 +41,13 @@ __device__ __forceinline__ uint32_t rope_axis(const RopeParams &p, int j) {
 // at most an eighth of a turn: pi 2^-27 radians.  (Of up to half a turn it would
 // be pi 2^-25, more than sincospif's own error.)
 __device__ __forceinline__ void rope_sincos(uint64_t u, float sign, float *c, float *s) {
-    const uint32_t quarter = ((uint32_t)(u >> 32) + (1u << 29)) >> 30;
-    const int64_t left = (int64_t)(u - ((uint64_t)quarter << 62));
+    const uint32_t h = (uint32_t)(u >> 32) + (1u << 29);  // its top bits: the quarter
+    const uint64_t left = (uint64_t)((h & 0x3fffffffu) - (1u << 29)) << 32 | (uint32_t)u;
     float sn, cs;
-    sincospif(__ll2float_rn(left) * 1.0842021724855044e-19f, &sn, &cs);  // half turns: 2^-63
-    const float a = quarter & 1u ? sn : cs, b = quarter & 1u ? cs : sn;
-    *c = (quarter + 1u) & 2u ? -a : a;
-    *s = (quarter & 2u ? -b : b) * sign;
+    sincospif(__ll2float_rn((long long)left) * 1.0842021724855044e-19f, &sn, &cs);  // half turns: 2^-63
+    const uint32_t a = __float_as_uint(h & 0x40000000u ? sn : cs), b = __float_as_uint(h & 0x40000000u ? cs : sn);
+    *c = __uint_as_float(a ^ ((h + 0x40000000u) & 0x80000000u));
+    *s = __uint_as_float(b ^ (h & 0x80000000u)) * sign;
 }
 
 // a / n of numbers that mostly fit 32 bits (a division in 64 is some hundred instructions).
