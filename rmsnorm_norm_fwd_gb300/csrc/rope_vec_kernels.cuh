@@ -376,11 +376,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     const float c = tab.c[at], s = tab.s[at];
                     cc = make_float2(g.x * c, g.y * c);
                     ss = make_float2(-g.y * s, g.x * s);
-                    if constexpr (MODE == kRopeLn) {
-                        float2 v = f2swap(bias);
-                        if constexpr (KIND == kRopeSome) v = rotated ? v : f2s(0.f);
-                        bias = make_float2(bias.x * c - v.x * s, bias.y * c + v.y * s);
-                    }
+                    if (MODE == kRopeLn && (KIND != kRopeSome || rotated))  // as below: no partner, no NaN from it
+                        bias = make_float2(bias.x * c - bias.y * s, bias.y * c + bias.x * s);
                 };
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
@@ -400,13 +397,9 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     sa[i] = f2mul(gb[i], make_float2(-s[i].x, -s[i].y));
                     cb[i] = f2mul(gb[i], c[i]);
                     sb[i] = f2mul(ga[i], s[i]);
-                    if constexpr (MODE == kRopeLn) {
-                        float2 u = bb[i], v = ba[i];
-                        if constexpr (KIND == kRopeSome) {  // as below: no partner, not even a NaN's product with 0
-                            u = ch.ra[i / HV] ? u : f2s(0.f);
-                            v = ch.ra[i / HV] ? v : f2s(0.f);
-                        }
-                        ba[i] = make_float2(ba[i].x * c[i].x - u.x * s[i].x, ba[i].y * c[i].y - u.y * s[i].y);
+                    if (MODE == kRopeLn && (KIND != kRopeSome || ch.ra[i / HV])) {
+                        const float2 v = ba[i];
+                        ba[i] = make_float2(v.x * c[i].x - bb[i].x * s[i].x, v.y * c[i].y - bb[i].y * s[i].y);
                         bb[i] = make_float2(bb[i].x * c[i].x + v.x * s[i].x, bb[i].y * c[i].y + v.y * s[i].y);
                     }
                 }
