@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
     auto load = [&] {
         ch.load(at(p.x[w.r], xes), p.xdt, w.hl > 0, xa, xb);
         ch.load(at(p.g[w.r], ges), p.ydt, w.hl > 0, ga, gb);
-        rstd = w.hl > 0 ? __ldg(p.rstd + w.stat(p)) : 0.f;  // zeros throughout where there is no head
-        if constexpr (LN) mean = w.hl > 0 ? __ldg(p.mean + w.stat(p)) : 0.f;
+        rstd = __ldg(p.rstd + w.stat(p));
+        if constexpr (LN) mean = __ldg(p.mean + w.stat(p));
     };
     if (w.left) load();
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
@@ -411,8 +411,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_any(const __grid_cons
                 }
                 va[i] = f2mul(va[i], f2s(rs));
                 vb[i] = f2mul(vb[i], f2s(rs));
-                da[i] = f2fma(ta[i], va[i], da[i]);
-                db[i] = f2fma(tb[i], vb[i], db[i]);
+                if (in) {  // zeros times another head's infinite statistics are NaN
+                    da[i] = f2fma(ta[i], va[i], da[i]);
+                    db[i] = f2fma(tb[i], vb[i], db[i]);
+                }
                 ta[i] = f2mul(ta[i], wa[i]);
                 tb[i] = f2mul(tb[i], wb[i]);
                 dot = f2fma(ta[i], va[i], f2fma(tb[i], vb[i], dot));

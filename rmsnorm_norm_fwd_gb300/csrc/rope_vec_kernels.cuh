@@ -529,18 +529,17 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     auto load = [&](int slot) {
         if (ahead.left) {
             Slot &to = ring[slot];
-            // a lane without a head in the pass has zeros throughout (another head's infinity times a gradient of zeros
-            // would be a NaN in the sums), and stores nothing
+            // a lane without a head in the pass reads another with a gradient of zeros, adds and stores nothing
             const bool in = ahead.hl > 0;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                rope_cp(&to.x[2 * i][lane], x + ch.a[i] * xes, in && ch.oka[i], p.xdt);
-                rope_cp(&to.x[2 * i + 1][lane], x + ch.b[i] * xes, in && ch.okb[i], p.xdt);
+                rope_cp(&to.x[2 * i][lane], x + ch.a[i] * xes, ch.oka[i], p.xdt);
+                rope_cp(&to.x[2 * i + 1][lane], x + ch.b[i] * xes, ch.okb[i], p.xdt);
                 rope_cp(&to.g[2 * i][lane], g + ch.a[i] * ges, in && ch.oka[i], p.ydt);
                 rope_cp(&to.g[2 * i + 1][lane], g + ch.b[i] * ges, in && ch.okb[i], p.ydt);
             }
-            rope_cp_bytes<4>(&to.rstd[lane], p.rstd + stat, in);
-            if constexpr (LN) rope_cp_bytes<4>(&to.mean[lane], p.mean + stat, in);
+            rope_cp_bytes<4>(&to.rstd[lane], p.rstd + stat, true);
+            if constexpr (LN) rope_cp_bytes<4>(&to.mean[lane], p.mean + stat, true);
             if (ahead.next(p, grp)) {
                 x = ahead.at(p, p.x[ahead.r], V * xes);
                 g = ahead.at(p, p.g[ahead.r], V * ges);
@@ -653,8 +652,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 }
                 xa[i] = f2mul(xa[i], f2s(rstd));
                 xb[i] = f2mul(xb[i], f2s(rstd));
-                da[i] = f2fma(ta[i], xa[i], da[i]);
-                db[i] = f2fma(tb[i], xb[i], db[i]);
+                if (in) {  // zeros times another head's infinity are NaN
+                    da[i] = f2fma(ta[i], xa[i], da[i]);
+                    db[i] = f2fma(tb[i], xb[i], db[i]);
+                }
                 ta[i] = f2mul(ta[i], wa[i]);
                 tb[i] = f2mul(tb[i], wb[i]);
                 dot = f2fma(ta[i], xa[i], f2fma(tb[i], xb[i], dot));
