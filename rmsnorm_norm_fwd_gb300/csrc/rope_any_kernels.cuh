@@ -142,8 +142,10 @@ template <int L, int C> struct RopeSlotTable {
     }
     __device__ __forceinline__ void put(const uint64_t *turns, const float *bad, const RopeParams &p, int64_t pos,
                                         int lane) {
+        // sixteen at once are more code than the loop bears: backward of heads of 602 160 us, 130 us with two
+        constexpr int AT_ONCE = PER > 8 ? 2 : PER;
         __syncwarp();  // the last token's have been read
-#pragma unroll
+#pragma unroll AT_ONCE
         for (int i = 0; i < PER; ++i) {
             const int j = lane + 32 * i;
             const bool in = 2 * j < p.rot;
@@ -168,7 +170,7 @@ template <int L, int C> struct RopeAnySmem {
     __device__ __forceinline__ void fill(const RopeParams &p) {
         for (int j = threadIdx.x; 2 * j < p.rot; j += kRopeCTA) {
             bool b;
-            turns[j] = rope_turns(__ldg(p.inv_freq + j), &b);
+            turns[j] = rope_turns<false>(__ldg(p.inv_freq + j), &b);
             bad[j] = b ? __int_as_float(0x7fffffff) : 0.f;
         }
     }

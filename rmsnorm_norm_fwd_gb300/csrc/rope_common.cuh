@@ -16,20 +16,48 @@ namespace gbn {
 // 10^6).  1 / (2 pi) enters with 192 bits: what is cut off below them is less than
 // 2^-40 of a unit for every frequency below 2^87 (128 bits would cut off 28 units
 // at 2^70).  Frequencies from there on, like infinities and NaN, give NaN.
+//
+// LOCAL: the words come from an array indexed at run time, in local memory, else
+// by selects, to the same bits.  Selects start a kernel sooner (a single token
+// 3.45 us, 3.65 us from the array); 16-bit vectors of two, whose kernels use every
+// register, run on fewer of them with the array (16384 tokens of 32 + 8 heads of 98
+// as neighbours 72.7 us, 75.5 us with selects).
 constexpr uint64_t kTurnHi = 0x28be60db9391054aull, kTurnMid = 0x7f09d5f47d4d3770ull,
                    kTurnLo = 0x36d8a5664f10e410ull;  // 2^192 / (2 pi)
 
-__device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
+template <bool LOCAL> __device__ __forceinline__ uint64_t rope_turns(float f, bool *bad) {
     const uint32_t bits = __float_as_uint(f), ex = (bits >> 23) & 0xffu;
     const uint64_t m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
     *bad = ex >= 127 + 87;
     // m 2^128 / (2 pi) as three words; |f| / (2 pi) turns = that * 2^(e - 128), F = that >> (64 - e)
     const uint64_t b = __umul64hi(m, kTurnLo), lo = m * kTurnMid + b, c = __umul64hi(m, kTurnMid) + (lo < b ? 1u : 0u),
                    mid = m * kTurnHi + c, hi = __umul64hi(m, kTurnHi) + (mid < c ? 1u : 0u);
-    // bits at .. at + 63 of (hi, mid, lo) and the next above them: F and, lowest, what it is rounded by
-    const int at = 63 - ((ex ? (int)ex : 1) - 150), k = at & 63;  // 0 .. 212 for frequencies below 2^87
-    const uint64_t x = at < 64 ? lo : at < 128 ? mid : at < 192 ? hi : 0, y = at < 64 ? mid : at < 128 ? hi : 0;
-    const uint64_t t = k ? (x >> k) | (y << (64 - k)) : x, r = (t >> 1) + ((y >> k) << 63) + (t & 1u);
+    const int sh = 64 - ((ex ? (int)ex : 1) - 150);  // 1 .. 213 for frequencies below 2^87
+    uint64_t r;
+    if constexpr (LOCAL) {
+        auto from = [&](int at) -> uint64_t {  // bits at .. at + 63 of (hi, mid, lo)
+            const uint64_t w[4] = {lo, mid, hi, 0};
+            uint64_t x = 0, y = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (at >> 6 == i) {
+                    x = w[i];
+                    y = w[i + 1];
+                }
+            const int k = at & 63;
+            return k ? (x >> k) | (y << (64 - k)) : x;
+        };
+        r = from(sh) + (from(sh - 1) & 1u);  // to nearest
+    } else {
+        const int at = sh - 1, k = at & 63;
+        uint64_t x = at < 64 ? lo : mid, y = at < 64 ? mid : hi;
+        if (at >= 128) {
+            x = at < 192 ? hi : 0;
+            y = 0;
+        }
+        const uint64_t t = (x >> k) | (y << 1 << (63 - k));  // one bit more than r, and the one above it in y
+        r = (t >> 1) + ((y >> k) << 63) + (t & 1u);
+    }
     return (bits >> 31) ? 0 - r : r;
 }
 

@@ -231,11 +231,11 @@ template <int N> struct RopeTurns {
     static_assert(N <= kRopeCTA, "a pair a thread");
     uint64_t f[N];
     float bad[N];  // 0, or NaN where the frequency is not a number of turns
-    __device__ __forceinline__ void fill(const RopeParams &p) {
+    template <bool LOCAL> __device__ __forceinline__ void fill(const RopeParams &p) {
         const int j = threadIdx.x;
         if (2 * j >= p.rot) return;
         bool b;
-        f[j] = rope_turns(__ldg(p.inv_freq + j), &b);
+        f[j] = rope_turns<LOCAL>(__ldg(p.inv_freq + j), &b);
         bad[j] = b ? __int_as_float(0x7fffffff) : 0.f;
     }
 };
@@ -293,6 +293,12 @@ __device__ __forceinline__ float2 f2swap(float2 v) { return make_float2(v.y, v.x
 template <int MODE, int XT, int V, int C, int L, int KIND, int U, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_constant__ RopeParams p) {
     constexpr int G = 32 / L, HV = V / 2, H = C * HV, N = C * V * L, DEPTH = kRopeFwdDepth;
+    // Where an element is not rotated, its beta stays as it is and takes nothing from another's, not even a NaN's
+    // product with 0: left out of the fold, or, where that takes registers the kernel does not have, read again.
+    // (LayerNorm of heads of 98 on 16-bit vectors of two: 92.7 us read again, 99.7 us left out, 92.3 us without either;
+    // of 80 on vectors of eight 16.3 us read again, 15.9 us left out; fp32 of 98 56.3 us and 55.3 us.)
+    constexpr bool AGAIN = MODE == kRopeLn && KIND == kRopeSome && C == 4;
+    constexpr bool SELECT = MODE == kRopeLn && KIND == kRopeSome && C != 4;
     using Table = RopeTable<V, N>;
     using Raw = RopeRaw<XT, V>;
     // rings, tables, frequencies, then gamma (and beta) of the queries and of the keys
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
     for (int i = 0; i < DEPTH; ++i) load(i);
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
     const uint32_t axis = Table::axes(p, lane);
-    turns.fill(p);
+    turns.template fill<C == 4>(p);
     tab.ones(lane, p.rot, inter);
     if constexpr (MODE != kRopeOnly) {
 #pragma unroll
@@ -376,8 +382,10 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     const float c = tab.c[at], s = tab.s[at];
                     cc = make_float2(g.x * c, g.y * c);
                     ss = make_float2(-g.y * s, g.x * s);
-                    if (MODE == kRopeLn && (KIND != kRopeSome || rotated))  // as below: no partner, no NaN from it
-                        bias = make_float2(bias.x * c - bias.y * s, bias.y * c + bias.x * s);
+                    if constexpr (MODE == kRopeLn) {
+                        if (!SELECT || rotated)
+                            bias = make_float2(bias.x * c - bias.y * s, bias.y * c + bias.x * s);
+                    }
                 };
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
@@ -397,11 +405,22 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_fwd_vec(const __grid_cons
                     sa[i] = f2mul(gb[i], make_float2(-s[i].x, -s[i].y));
                     cb[i] = f2mul(gb[i], c[i]);
                     sb[i] = f2mul(ga[i], s[i]);
-                    if (MODE == kRopeLn && (KIND != kRopeSome || ch.ra[i / HV])) {
-                        const float2 v = ba[i];
-                        ba[i] = make_float2(v.x * c[i].x - bb[i].x * s[i].x, v.y * c[i].y - bb[i].y * s[i].y);
-                        bb[i] = make_float2(bb[i].x * c[i].x + v.x * s[i].x, bb[i].y * c[i].y + v.y * s[i].y);
+                    if constexpr (MODE == kRopeLn) {
+                        const float2 v = ba[i], u = bb[i];
+                        ba[i] = make_float2(v.x * c[i].x - u.x * s[i].x, v.y * c[i].y - u.y * s[i].y);
+                        bb[i] = make_float2(u.x * c[i].x + v.x * s[i].x, u.y * c[i].y + v.y * s[i].y);
+                        if constexpr (SELECT) {
+                            ba[i] = ch.ra[i / HV] ? ba[i] : v;
+                            bb[i] = ch.ra[i / HV] ? bb[i] : u;
+                        }
                     }
+                }
+            }
+            if constexpr (AGAIN) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    if (!ch.ra[i]) rope_get<V>(par + (2 + r) * p.D, ch.a[i], p.D, ba + i * HV);
+                    if (!ch.rb[i]) rope_get<V>(par + (2 + r) * p.D, ch.b[i], p.D, bb + i * HV);
                 }
             }
             if constexpr (KIND == kRopeSome) {
@@ -500,6 +519,11 @@ template <bool LN, int XT, int V, int C, int L, int KIND, int MINB>
 __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_constant__ RopeParams p) {
     pdl_launch_dependents();  // the column reduce waits for this grid's completion
     constexpr int G = 32 / L, HV = V / 2, H = C * HV, N = C * V * L, DEPTH = kRopeBwdDepth;
+    // A gradient of zeros times another head's infinity is a NaN, so that lanes without a head either have zeros for x
+    // and its statistics too or leave the column sums out.  (Zeros, leaving out: heads of 98 as neighbours 106.7 us,
+    // 110.7 us; vectors of eight, LayerNorm of heads of 256 51.9 us, 50.0 us, of 192 145 us, 142 us; bf16 to fp32 120 us,
+    // 113 us.)
+    constexpr bool ZEROS = V == 2;
     using Table = RopeTable<V, N>;
     using Raw = RopeRaw<XT, V>;
     struct Slot {
@@ -529,17 +553,17 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     auto load = [&](int slot) {
         if (ahead.left) {
             Slot &to = ring[slot];
-            // a lane without a head in the pass reads another with a gradient of zeros, adds and stores nothing
-            const bool in = ahead.hl > 0;
+            // a lane without a head in the pass reads another (or zeros) with a gradient of zeros, and stores nothing
+            const bool in = ahead.hl > 0, at = in || !ZEROS;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                rope_cp(&to.x[2 * i][lane], x + ch.a[i] * xes, ch.oka[i], p.xdt);
-                rope_cp(&to.x[2 * i + 1][lane], x + ch.b[i] * xes, ch.okb[i], p.xdt);
+                rope_cp(&to.x[2 * i][lane], x + ch.a[i] * xes, at && ch.oka[i], p.xdt);
+                rope_cp(&to.x[2 * i + 1][lane], x + ch.b[i] * xes, at && ch.okb[i], p.xdt);
                 rope_cp(&to.g[2 * i][lane], g + ch.a[i] * ges, in && ch.oka[i], p.ydt);
                 rope_cp(&to.g[2 * i + 1][lane], g + ch.b[i] * ges, in && ch.okb[i], p.ydt);
             }
-            rope_cp_bytes<4>(&to.rstd[lane], p.rstd + stat, true);
-            if constexpr (LN) rope_cp_bytes<4>(&to.mean[lane], p.mean + stat, true);
+            rope_cp_bytes<4>(&to.rstd[lane], p.rstd + stat, at);
+            if constexpr (LN) rope_cp_bytes<4>(&to.mean[lane], p.mean + stat, at);
             if (ahead.next(p, grp)) {
                 x = ahead.at(p, p.x[ahead.r], V * xes);
                 g = ahead.at(p, p.g[ahead.r], V * ges);
@@ -558,7 +582,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     for (int i = 0; i < DEPTH; ++i) load(i);
     int64_t pos = w.left ? rope_position(p, w, lane) : 0;
     const uint32_t axis = Table::axes(p, lane);
-    turns.fill(p);
+    turns.template fill<C == 4>(p);
     tab.ones(lane, p.rot, inter);
 #pragma unroll
     for (int i = 0; i < 2; ++i) rope_param<V>(par + i * p.D, p.gamma[i], p.D, p.pdt, 1.f);
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 }
                 xa[i] = f2mul(xa[i], f2s(rstd));
                 xb[i] = f2mul(xb[i], f2s(rstd));
-                if (in) {  // zeros times another head's infinity are NaN
+                if (ZEROS || in) {
                     da[i] = f2fma(ta[i], xa[i], da[i]);
                     db[i] = f2fma(tb[i], xb[i], db[i]);
                 }
