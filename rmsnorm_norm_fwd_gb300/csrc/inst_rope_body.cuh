@@ -1,9 +1,30 @@
 // Vector kernels of the head operators: GBN_MODE, a RopeMode, or -1 - is_layernorm for the backward; GBN_XT, GBN_V,
 // GBN_C, the type and elements of a vector and the vectors of half a lane's elements.  Defines
-// kRopeVec_<GBN_NAME>[kind][lanes a head].  GBN_WHOLE: whole heads rotated as halves (1) and as neighbours (2) have
-// kernels of their own up to 16 lanes (prefill of 16384 tokens of 32 heads of 72, 8-byte vectors, 38 us against 45 us, their
-// rotation 33 us against 37 us; not the backward on 8-byte vectors, 64.3 us against 65.8 us); what is rarer runs on the
-// kernels for any rotation.  GBN_ODD: heads on 5, 6 and 10 lanes too (heads of 80 16.4 us against 19.0 us).
+// kRopeVec_<GBN_NAME>[kind][lanes a head].
+//
+// GBN_WHOLE: whole heads rotated as halves (1) and as neighbours (2) have kernels of their own up to 16 lanes; what is
+// rarer runs on the kernels for any rotation.  With them and without, bf16, 16384 tokens of 32 + 8 heads as halves
+// (heads of 256: 8192), us:
+//     head   RMSNorm, LayerNorm      backward of each        rotation
+//      64    30.9 33.1  35.5 40.7    44.8 45.6  54.2 57.2    28.2 30.4
+//      96    46.9 50.0  53.8 62.0    67.1 69.5  82.3 85.1    41.3 45.8
+//     128    54.3 56.0  58.8 66.8    81.9 80.8  89.1 92.3    57.2 53.6
+//     256    56.3 56.5  58.5 63.4    88.0 83.3  88.1 90.1    57.2 55.2
+// (the rotation of 26520 tokens of 80 heads of 128: 170 us, 179 us).  Neighbours the same within 1% where they have
+// kernels; fp32, at 90% of the copy rate either way, within 1% (rotation of heads of 64: 55.2 us, 53.0 us).  On 8-byte
+// vectors heads of 72 37.8 us against 45 us, their rotation 33 us against 37 us, not the backward: 64.3 us, 65.8 us.
+//
+// GBN_ODD: heads on 5, 6 and 10 lanes too, else on the next power of two.  With them and without, 16384 tokens of
+// 16 + 16 heads as halves, us (80, 96, 160: bf16 on 16-byte vectors; 72, 88, 152: fp16 on 8-byte ones):
+//     head lanes  RMSNorm, LayerNorm      backward of each          rotation
+//      80    5    35.9 41.8  42.5 51.0    54.6  63.6   65.1  79.1   35.1 32.6
+//      96    6    41.3 42.4  49.8 51.4    61.0  63.6   75.6  79.2   34.5 34.0
+//     160   10    60.5 70.2  72.1 88.2    93.7 113.1  115.5 143.2   57.6 54.4
+//      72    5    37.8 43.4  46.8 54.8    65.8  75.7   83.3  90.7   33.8 32.2
+//      88    6    43.3 43.7  54.7 55.1    76.1  76.0   99.2  91.2   35.2 34.8
+//     152   10    62.2 72.0  81.8 98.1   118.4 133.2  158.0 168.6   54.8 58.4
+// Heads of 112 and 192 leave an eighth and a quarter of 8 and 16 lanes without work: 44.1 us and 74.4 us forward (78%
+// and 80% of the copy rate), 65.5 us and 113 us backward.
 #include "rope_vec_kernels.cuh"
 
 #ifndef GBN_CAT

@@ -9,10 +9,14 @@
 // lie in shared memory in the order of the lanes' slots.
 //
 // What bounds it: instructions, 35 an element in the forward (16384 tokens of 40
-// heads of 98 bf16 106 us, 36% of the copy rate's time) and 62 in the backward (194
+// heads of 98 bf16 106 us, 36% of the copy rate's time) and 61 in the backward (161
 // us): a load, a store and a conversion for each element, where the kernels on
-// vectors take one of each for four to eight.  A warp a head, without the next
-// pass ahead, measured 319 and 837 us.
+// vectors take one of each for four to eight, and register spills: 16 elements a
+// lane with coefficients or sums, and three types in one kernel, are more than 128
+// registers (bytes of stores and loads: rotation 36, 72; RMSNorm 72, 144, its
+// backward 104, 144; LayerNorm 148, 360, its backward 372, 620; with 16 slots three
+// of the five spill at 255 registers).  A warp a head, without the next pass ahead,
+// measured 319 and 837 us.
 #pragma once
 
 #include "rope_vec_kernels.cuh"

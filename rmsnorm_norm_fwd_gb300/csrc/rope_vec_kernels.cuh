@@ -15,12 +15,15 @@
 // and two with coefficients.
 //
 // What bounds it: DRAM for the rotation alone (26520 tokens of 80 heads of 128
-// bf16 171 us, 94% of the copy rate's time) and RMSNorm (16384 tokens of 40 heads:
-// forward 54.7 us, 90%, 13 instructions an element; backward 80.6 us, 93%, 19);
+// bf16 170 us, 94% of the copy rate's time) and RMSNorm (16384 tokens of 40 heads:
+// forward 54.6 us, 91%, 13 instructions an element; backward 80.2 us, 93%, 19);
 // with LayerNorm (60 and 90 us, 83%) and heads that leave lanes or vectors unused,
 // instruction issue and latency at 16 warps an SM.  That is what 16 elements of a
 // lane with their coefficients or sums leave (106 to 128 registers): capped at 80
 // registers for 24 warps the kernels spill, forward 81 us and backward 142 us.
+// At 128 registers some of LayerNorm's spill too: the backward on vectors below
+// 16 bytes, for differing types and in fp16 on 10 and 32 lanes by 4 to 108 bytes,
+// the forward on 8-byte vectors and for differing types by 4 to 32.
 // Copies straight into registers, one pass ahead, in place of the rings: forward
 // 98 us, backward 147 us.
 #pragma once
@@ -521,8 +524,8 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
     constexpr int G = 32 / L, HV = V / 2, H = C * HV, N = C * V * L, DEPTH = kRopeBwdDepth;
     // A gradient of zeros times another head's infinity is a NaN, so that lanes without a head either have zeros for x
     // and its statistics too or leave the column sums out.  (Zeros, leaving out: heads of 98 as neighbours 106.7 us,
-    // 110.7 us; vectors of eight, LayerNorm of heads of 256 51.9 us, 50.0 us, of 192 145 us, 142 us; bf16 to fp32 120 us,
-    // 113 us.)
+    // 110.7 us; on vectors of eight LayerNorm of heads of 256 51.9 us, 50.0 us, of 192 145 us, 142 us; bf16 rows with
+    // an fp32 gradient 120 us, 113 us.)
     constexpr bool ZEROS = V == 2;
     using Table = RopeTable<V, N>;
     using Raw = RopeRaw<XT, V>;
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kRopeCTA, MINB) rope_bwd_vec(const __grid_cons
                 ta[i] = f2fma(xa[i], c2, LN ? f2fma(ta[i], f2s(rstd), c1) : f2mul(ta[i], f2s(rstd)));
                 tb[i] = f2fma(xb[i], c2, LN ? f2fma(tb[i], f2s(rstd), c1) : f2mul(tb[i], f2s(rstd)));
             }
-                        #pragma unroll
+#pragma unroll
             for (int i = 0; i < C; ++i) {
                 if (in && ch.oka[i]) rope_store<XT, V>(y + ch.a[i] * xes, p.xdt, ta + i * HV);
                 if (in && ch.okb[i]) rope_store<XT, V>(y + ch.b[i] * xes, p.xdt, tb + i * HV);
